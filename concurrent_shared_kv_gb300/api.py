@@ -23,7 +23,8 @@ HW_DESC_EARLY_LOADS = 2
 STATUS = {0: "HW_OK", -1: "HW_ERR_INVALID", -2: "HW_ERR_UNSUPPORTED", -3: "HW_ERR_WORKSPACE",
           -4: "HW_ERR_CAPACITY", -5: "HW_ERR_OVERLAP", -6: "HW_ERR_CUDA", -7: "HW_ERR_DEVICE"}
 DEV_FLAGS = {1: "HW_DEV_BAD_BLOCK", 2: "HW_DEV_BAD_RANGE", 4: "HW_DEV_BAD_HEADMAP",
-             8: "HW_DEV_TOO_MANY_REFS", 16: "HW_DEV_TIMEOUT", 32: "HW_DEV_BAD_PLAN"}
+             8: "HW_DEV_TOO_MANY_REFS", 16: "HW_DEV_TIMEOUT", 32: "HW_DEV_BAD_PLAN",
+             64: "HW_DEV_BAD_TREE"}
 
 # every symbol the header declares
 EXPORTS = ["hw_attn_decode_workspace_size", "hw_workspace_init", "hw_attn_decode",
@@ -32,11 +33,14 @@ EXPORTS = ["hw_attn_decode_workspace_size", "hw_workspace_init", "hw_attn_decode
            "hw_attn_append_decode_planned", "hw_plan_export", "hw_attn_decode_noalloc",
            "hw_block_commit", "hw_block_commit_many", "hw_workspace_status", "hw_views_combined",
            "hw_views", "hw_views_chunked", "hw_last_cuda_error", "hw_status_string",
-           "hw_test_set_merge_wait_limit", "hw_noalloc_status", "hw_trace_read", "hw_trace_clear"]
+           "hw_test_set_merge_wait_limit", "hw_noalloc_status", "hw_trace_read", "hw_trace_clear",
+           "hw_attn_tree_workspace_size", "hw_attn_plan_tree", "hw_attn_decode_tree",
+           "hw_attn_decode_tree_fp8", "hw_tree_verify", "hw_tree_commit"]
 HW_LAYOUT_COMBINED, HW_LAYOUT_INTERLEAVED, HW_LAYOUT_CONTIGUOUS = 0, 1, 2
 LAYOUTS = {"combined": HW_LAYOUT_COMBINED, "interleaved": HW_LAYOUT_INTERLEAVED,
            "contiguous": HW_LAYOUT_CONTIGUOUS}
 HW_MAX_COMMITS = 64
+HW_MAX_TREE_NODES = 128
 
 
 class HwError(RuntimeError):
@@ -102,6 +106,14 @@ def lib(path: Optional[str] = None):
     L.hw_views_combined.argtypes = [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P]
     L.hw_views.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P]
     L.hw_views_chunked.argtypes = [ctypes.c_int32] * 4 + [_P] * 5
+    tree = [ctypes.POINTER(AttnDesc), ctypes.c_int32]
+    L.hw_attn_tree_workspace_size.argtypes = tree + [ctypes.POINTER(ctypes.c_size_t)]
+    L.hw_attn_plan_tree.argtypes = tree + [_P] * 11 + [ctypes.c_size_t, _P]
+    L.hw_attn_decode_tree.argtypes = tree + [_P] * 8 + [ctypes.c_size_t, _P]
+    L.hw_attn_decode_tree_fp8.argtypes = tree + [_P] * 10 + [ctypes.c_size_t, _P]
+    L.hw_tree_commit.argtypes = tree + [ctypes.c_int32] + [_P] * 5 + [ctypes.c_size_t, _P]
+    L.hw_tree_verify.argtypes = [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_int64, _P, ctypes.c_int64] + [
+        _P] * 6
     L.hw_last_cuda_error.argtypes = []
     L.hw_test_set_merge_wait_limit.argtypes = [ctypes.c_int64]
     L.hw_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int32), _P]
@@ -362,6 +374,70 @@ def views_chunked(layout, block_len, n_problems: int, n_workers: int, chunk: int
                                                       bl.ctypes.data, vb.ctypes.data, vo.ctypes.data,
                                                       vl.ctypes.data, qp.ctypes.data))
     return vb, vo, vl, qp
+
+
+def attn_tree_workspace_size(desc: AttnDesc, max_nodes: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("hw_attn_tree_workspace_size",
+           lib().hw_attn_tree_workspace_size(ctypes.byref(desc), int(max_nodes), ctypes.byref(n)))
+    return int(n.value)
+
+
+def attn_plan_tree(desc: AttnDesc, max_nodes: int, block_start, block_len, view_block, view_offset,
+                   q_pos, tree_block, n_nodes, parent, workspace, workspace_bytes: int,
+                   tree_start=None, q_to_kv=None, stream=None) -> int:
+    """hw_attn_plan_tree: a step whose rows each query a tree of drafted tokens."""
+    st = lib().hw_attn_plan_tree(ctypes.byref(desc), int(max_nodes), _ptr(block_start),
+                                 _ptr(block_len), _ptr(view_block), _ptr(view_offset), _ptr(q_pos),
+                                 _ptr(q_to_kv), _ptr(tree_block), _ptr(tree_start), _ptr(n_nodes),
+                                 _ptr(parent), _ptr(workspace), int(workspace_bytes),
+                                 _stream(stream))
+    _check("hw_attn_plan_tree", st)
+    return st
+
+
+def attn_decode_tree(desc: AttnDesc, max_nodes: int, q, k_new, v_new, k_cache, v_cache, out, lse,
+                     workspace, workspace_bytes: int, stream=None) -> int:
+    """hw_attn_decode_tree: one layer, its drafted tokens written, then attended."""
+    st = lib().hw_attn_decode_tree(ctypes.byref(desc), int(max_nodes), _ptr(q), _ptr(k_new),
+                                   _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse),
+                                   _ptr(workspace), int(workspace_bytes), _stream(stream))
+    _check("hw_attn_decode_tree", st)
+    return st
+
+
+def attn_decode_tree_fp8(desc: AttnDesc, max_nodes: int, q, k_new, v_new, k_cache, v_cache,
+                         k_scale, v_scale, out, lse, workspace, workspace_bytes: int,
+                         stream=None) -> int:
+    """hw_attn_decode_tree_fp8: the same over E4M3 caches with per-kv-head scales."""
+    st = lib().hw_attn_decode_tree_fp8(ctypes.byref(desc), int(max_nodes), _ptr(q), _ptr(k_new),
+                                       _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                       _ptr(v_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                                       int(workspace_bytes), _stream(stream))
+    _check("hw_attn_decode_tree_fp8", st)
+    return st
+
+
+def tree_verify(dtype: int, n_rows: int, max_nodes: int, vocab: int, n_nodes, parent, token, p,
+                p_stride: int, q, q_stride: int, u_accept, u_sample, path, n_path, next_token,
+                stream=None) -> int:
+    """hw_tree_verify: the drafted tokens that stand, and the token after them."""
+    st = lib().hw_tree_verify(int(dtype), int(n_rows), int(max_nodes), int(vocab), _ptr(n_nodes),
+                              _ptr(parent), _ptr(token), _ptr(p), int(p_stride), _ptr(q),
+                              int(q_stride), _ptr(u_accept), _ptr(u_sample), _ptr(path),
+                              _ptr(n_path), _ptr(next_token), _stream(stream))
+    _check("hw_tree_verify", st)
+    return st
+
+
+def tree_commit(desc: AttnDesc, max_nodes: int, n_layers: int, k_cache, v_cache, path, n_path,
+                workspace, workspace_bytes: int, stream=None) -> int:
+    """hw_tree_commit: the accepted nodes appended to their rows' blocks."""
+    st = lib().hw_tree_commit(ctypes.byref(desc), int(max_nodes), int(n_layers), _ptr(k_cache),
+                              _ptr(v_cache), _ptr(path), _ptr(n_path), _ptr(workspace),
+                              int(workspace_bytes), _stream(stream))
+    _check("hw_tree_commit", st)
+    return st
 
 
 def status_string(st: int) -> str:

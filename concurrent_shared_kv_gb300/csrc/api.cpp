@@ -22,7 +22,7 @@ static thread_local int g_last_cuda_error = 0;
 constexpr long long kDefaultMergeWait = 2000000000ll;  // ~1 s at 2 GHz
 static std::atomic<long long> g_merge_wait{kDefaultMergeWait};
 
-static int cuda_fail(cudaError_t e) {
+int cuda_fail(cudaError_t e) {
   g_last_cuda_error = static_cast<int>(e);
   return HW_ERR_CUDA;
 }
@@ -44,18 +44,28 @@ int device_sm_count() {
 // frac(w_i / 2pi) * 2^64 with w_i = theta^(-2i/D), in long double so that the
 // table is exact to well below one unit of its last place for positions up to
 // 2^31.
+// 64 powl calls cost about 100 us where long double is emulated (aarch64), so
+// a thread keeps the table of the last (head_dim, theta) it made.
 void rope_phase_table(int head_dim, double theta, uint64_t *phase) {
-  const long double two_pi = 6.283185307179586476925286766559005768L;
-  for (int i = 0; i < 64; ++i) phase[i] = 0;
-  for (int i = 0; i < head_dim / 2 && i < 64; ++i) {
-    const long double w = powl(static_cast<long double>(theta),
-                               -2.0L * static_cast<long double>(i) / static_cast<long double>(head_dim));
-    long double f = w / two_pi;
-    f -= floorl(f);
-    long double x = ldexpl(f, 64) + 0.5L;
-    if (x >= 18446744073709551616.0L) x -= 18446744073709551616.0L;
-    phase[i] = static_cast<uint64_t>(x);
+  static thread_local int last_dim = 0;
+  static thread_local double last_theta = 0.0;
+  static thread_local uint64_t last[64];
+  if (head_dim != last_dim || theta != last_theta) {
+    const long double two_pi = 6.283185307179586476925286766559005768L;
+    for (int i = 0; i < 64; ++i) last[i] = 0;
+    for (int i = 0; i < head_dim / 2 && i < 64; ++i) {
+      const long double w = powl(static_cast<long double>(theta),
+                                 -2.0L * static_cast<long double>(i) / static_cast<long double>(head_dim));
+      long double f = w / two_pi;
+      f -= floorl(f);
+      long double x = ldexpl(f, 64) + 0.5L;
+      if (x >= 18446744073709551616.0L) x -= 18446744073709551616.0L;
+      last[i] = static_cast<uint64_t>(x);
+    }
+    last_dim = head_dim;
+    last_theta = theta;
   }
+  std::memcpy(phase, last, sizeof last);
 }
 
 // cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
@@ -78,8 +88,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
 // Tokens past the capacity read as zeros.
 // A [Hkv][capacity][128] pool as 128-token tiles of 128 bytes per row,
 // 128-byte swizzled: bf16 in two boxes of 64 elements, E4M3 in one of 128.
-static bool make_pool_map(CUtensorMap *m, const void *pool, int64_t capacity, int n_kv_heads,
-                          bool e4m3 = false) {
+bool make_pool_map(CUtensorMap *m, const void *pool, int64_t capacity, int n_kv_heads,
+                   bool e4m3) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t cap = capacity > 0 ? static_cast<cuuint64_t>(capacity) : 1;
@@ -165,7 +175,7 @@ static MetaCopies meta_copies(const hw_attn_desc &d, const WorkspaceLayout &L, v
   return c;
 }
 
-static int check_desc(const hw_attn_desc *d) {
+int check_desc(const hw_attn_desc *d) {
   if (!d) return HW_ERR_INVALID;
   if (d->n_rows < 0 || d->n_blocks < 0 || d->max_view_blocks < 0 || d->cache_capacity < 0)
     return HW_ERR_INVALID;

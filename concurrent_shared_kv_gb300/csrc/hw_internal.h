@@ -112,6 +112,13 @@ WorkspaceLayout decode_workspace_layout(const hw_attn_desc &d);
 
 int device_sm_count();  // SMs of the current device, cached; <= 0 on failure
 
+// Host checks shared by the entry points (api.cpp).
+int check_desc(const hw_attn_desc *d);  // an hw_status
+int cuda_fail(cudaError_t e);           // records the error; HW_ERR_CUDA
+// TMA map of a head_dim-128 pool in 128-token tiles.
+bool make_pool_map(CUtensorMap *m, const void *pool, int64_t capacity, int n_kv_heads,
+                   bool e4m3 = false);
+
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_decode_simt(const DecodeArgs &a, int dtype, int ctas, cudaStream_t s);
 cudaError_t launch_decode_tc(const DecodeArgs &a, const CUtensorMap &k_map,

@@ -1,0 +1,131 @@
+// hw_tree.h - the draft-tree operators' plan: its layout in a workspace, and
+// the arguments their kernels share.  Not part of the public interface.
+//
+// A step's plan is built once by tree_plan_kernel (tree_plan.cu) and read by
+// every layer's launches:
+//   segment  = the tokens of one block (or of one row's tree) against up to
+//              `cols` query columns.  The columns of a block are its view
+//              references in view-entry order, each with (node, q head of the
+//              kv head's group) of its row; a block with more is cut into
+//              segments of `cols` columns that each read its tokens.  A row's
+//              tree has the row's own columns only.
+//   unit     = one tile of `tile` tokens of a segment for one kv head; units
+//              are ordered by kv head, then segment, then tile, on a weighted
+//              line: a unit weighs its segment's tile_w, the first unit of a
+//              segment seg_w more (a switch costs a record epilogue and new
+//              rotated queries).  CTA c of C takes the units that start in
+//              [c W / C, (c + 1) W / C); C is small enough that every CTA
+//              inside a segment owns a unit of it.
+//   record   = what a CTA leaves for (segment, kv head): per column the
+//              running maximum m and sum l of the softmax (log2 domain) and
+//              the unnormalised output.  The records of one (kv head,
+//              segment) lie behind one another, CTA after CTA.
+// tree_merge_kernel then joins the records of every (row, node, q head).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "hogwild.h"
+
+namespace hw {
+
+constexpr uint32_t kTreeMagic = 0x48577472u;
+constexpr int kMaxNodes = HW_MAX_TREE_NODES;
+
+struct TreeHeader {
+  uint32_t magic;
+  int32_t n_rows, max_nodes, n_q_heads, n_kv_heads, head_dim, n_blocks, n_view, dtype;
+  int32_t n_segs;  // segments per kv head
+  int32_t n_ctas;  // CTAs with units (0: nothing to attend)
+  int32_t pad;
+  int64_t capacity;
+};
+
+struct TreeSeg {
+  int32_t start, len;      // pool tokens
+  int32_t row;             // the row whose tree this is, or -1: a block
+  int32_t ref0, n_ref;     // its block's references
+  int32_t col0, n_cols;    // columns of the block it covers
+  int32_t pad;
+};
+struct TreeRef {
+  int32_t row, col;  // query row; its first column among the block's columns
+  int64_t rel;       // rotation of the row's root: q_pos - view_offset (a tree: the root's position)
+};
+struct TreeCta {
+  int32_t head, seg, tile, n_units;  // first unit and count
+};
+
+// Byte offsets of the plan's arrays in the workspace (the error word is at 0).
+struct TreeLayout {
+  size_t hdr, segs, wbase, refs, entry_seg, entry_col, piece_row, piece_cta, ctas;
+  size_t n_nodes, slot, pos, end, depth, mask, heads, block_start, block_len;
+  size_t ml, o, total;
+  int64_t max_segs, max_refs, max_rows;
+  int32_t cols, tile, ctas_max;
+};
+
+struct TreeArgs {
+  const void *q, *k_new, *v_new;
+  void *k, *v;
+  const float *k_scale, *v_scale;
+  void *out;
+  float *lse;
+  uint8_t *ws;
+  TreeLayout L;
+  int32_t n_rows, max_nodes, n_q_heads, n_kv_heads, head_dim, n_blocks, n_view, dtype;
+  int64_t capacity;
+  float scale_log2;
+  uint64_t phase[64];  // RoPE phase table (hw_internal.h)
+};
+
+// The caller's metadata of a step (device pointers).
+struct TreeMeta {
+  const int32_t *block_start, *block_len, *view_block, *view_offset, *q_pos, *q_to_kv;
+  const int32_t *tree_block, *tree_start, *n_nodes, *parent;
+};
+
+struct TreeCommitArgs {
+  void *k, *v;
+  const int32_t *path, *n_path;
+  int32_t n_layers, elem_bytes;
+};
+
+struct TreeVerifyArgs {
+  const void *p, *q;
+  int64_t p_stride, q_stride;
+  const int32_t *n_nodes, *parent, *token;
+  const float *u_accept, *u_sample;
+  int32_t *path, *n_path, *next_token;
+  int32_t n_rows, max_nodes, vocab, dtype;
+};
+
+TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms);
+// Whether these caches run on the tensor cores.
+inline bool tree_on_tensor_cores(int dtype, int head_dim) { return false; }
+
+cudaError_t launch_tree_plan(const TreeArgs &a, const TreeMeta &m, cudaStream_t s);
+cudaError_t launch_tree_append(const TreeArgs &a, cudaStream_t s);
+cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t s);
+cudaError_t launch_tree_merge(const TreeArgs &a, cudaStream_t s);
+cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaStream_t s);
+cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t s);
+
+#ifdef __CUDACC__
+template <typename T>
+__device__ __forceinline__ T *tree_at(const TreeArgs &a, size_t off) {
+  return reinterpret_cast<T *>(a.ws + off);
+}
+// The plan in the workspace is one of this description.
+__device__ __forceinline__ bool tree_plan_ok(const TreeArgs &a) {
+  const TreeHeader &h = *tree_at<const TreeHeader>(a, a.L.hdr);
+  return h.magic == kTreeMagic && h.n_rows == a.n_rows && h.max_nodes == a.max_nodes &&
+         h.n_q_heads == a.n_q_heads && h.n_kv_heads == a.n_kv_heads && h.head_dim == a.head_dim &&
+         h.n_blocks == a.n_blocks && h.n_view == a.n_view && h.dtype == a.dtype &&
+         h.capacity == a.capacity;
+}
+#endif
+
+}  // namespace hw

@@ -167,6 +167,116 @@ class DecodeSession:
         return api.workspace_status(self.workspace)
 
 
+def _int32(x, device):
+    t = torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32)) if not torch.is_tensor(x) else x
+    return t.to(device, dtype=torch.int32).contiguous()
+
+
+class TreeSession:
+    """Steps whose rows each query a tree of drafted tokens: plan(), one
+    decode() a layer, tree_verify(), commit()."""
+
+    def __init__(self, *, n_rows: int, max_nodes: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                 n_blocks: int, max_view_blocks: int, capacity: int, dtype: torch.dtype,
+                 rope_theta: float, scale: Optional[float] = None, device="cuda",
+                 kv_fp8: bool = False):
+        """max_nodes: nodes of the largest tree (q, out and the new tokens are
+        [rows][max_nodes][heads][D]).  dtype, kv_fp8: as in DecodeSession."""
+        self.device = torch.device(device)
+        self.dtype = dtype
+        self.max_nodes = int(max_nodes)
+        self.desc = api.make_desc(n_rows, n_q_heads, n_kv_heads, head_dim, n_blocks,
+                                  max_view_blocks, capacity,
+                                  api.HW_FP8_E4M3 if kv_fp8 else DTYPES[dtype], rope_theta,
+                                  head_dim ** -0.5 if scale is None else scale)
+        self.ws_bytes = api.attn_tree_workspace_size(self.desc, self.max_nodes)
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        api.workspace_init(self.workspace, self.ws_bytes)
+        self.meta = None
+
+    def set_metadata(self, block_start, block_len, view_block, view_offset, q_pos, q_to_kv=None):
+        """Upload the step's views: those of the rows' tokens before their trees."""
+        self.meta = [_int32(x, self.device) for x in (block_start, block_len, view_block, view_offset, q_pos)]
+        self.q_to_kv = None if q_to_kv is None else _int32(q_to_kv, self.device)
+
+    def plan(self, tree_block, n_nodes, parent, tree_start=None, stream=None):
+        """hw_attn_plan_tree: the step's trees (tree_start None: behind each row's block)."""
+        self.trees = [_int32(x, self.device) for x in (tree_block, n_nodes, parent)]
+        self.tree_start = None if tree_start is None else _int32(tree_start, self.device)
+        api.attn_plan_tree(self.desc, self.max_nodes, *self.meta, *self.trees, self.workspace,
+                           self.ws_bytes, tree_start=self.tree_start, q_to_kv=self.q_to_kv,
+                           stream=stream)
+
+    def _outputs(self, out, lse, want_lse):
+        d = self.desc
+        shape = (d.n_rows, self.max_nodes, d.n_q_heads)
+        if out is None:
+            out = torch.empty(shape + (d.head_dim,), dtype=self.dtype, device=self.device)
+        if lse is None and want_lse:
+            lse = torch.empty(shape, dtype=torch.float32, device=self.device)
+        return out, lse
+
+    def decode(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+               k_cache: torch.Tensor, v_cache: torch.Tensor, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+        """One layer: the trees' tokens written into the cache, then attended.
+        Rows of out and lse behind a tree's nodes keep what they hold."""
+        out, lse = self._outputs(out, lse, want_lse)
+        api.attn_decode_tree(self.desc, self.max_nodes, q, k_new, v_new, k_cache, v_cache, out, lse,
+                             self.workspace, self.ws_bytes, stream=stream)
+        return out, lse
+
+    def decode_fp8(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                   k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                   v_scale: torch.Tensor, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+        """decode() over E4M3 pools with float32 scales [Hkv]; q and the new tokens bf16."""
+        out, lse = self._outputs(out, lse, want_lse)
+        api.attn_decode_tree_fp8(self.desc, self.max_nodes, q, k_new, v_new, k_cache, v_cache,
+                                 k_scale, v_scale, out, lse, self.workspace, self.ws_bytes,
+                                 stream=stream)
+        return out, lse
+
+    def commit(self, k_cache: torch.Tensor, v_cache: torch.Tensor, path: torch.Tensor,
+               n_path: torch.Tensor, stream=None):
+        """The accepted nodes (tree_verify's path and n_path) appended to the
+        rows' blocks in every layer; pools [layers][Hkv][cap][D] or [Hkv][cap][D]."""
+        layers = 1 if k_cache.dim() == 3 else k_cache.shape[0]
+        api.tree_commit(self.desc, self.max_nodes, layers, k_cache, v_cache, path, n_path,
+                        self.workspace, self.ws_bytes, stream=stream)
+
+    def device_flags(self) -> int:
+        return api.workspace_status(self.workspace)
+
+
+def tree_verify(n_nodes: torch.Tensor, parent: torch.Tensor, token: torch.Tensor, p: torch.Tensor,
+                q: Optional[torch.Tensor], u_accept: torch.Tensor, u_sample: torch.Tensor,
+                path: Optional[torch.Tensor] = None, n_path: Optional[torch.Tensor] = None,
+                next_token: Optional[torch.Tensor] = None, stream=None):
+    """hw_tree_verify: (path, n_path, next_token) of drafted trees.  p and q:
+    [rows][max_nodes][vocab], float32 or bfloat16, the last dimension dense and
+    the first two one stride apart; q None: the tokens were chosen, not drawn."""
+    R, T, V = p.shape
+
+    def step(x):
+        if x.shape != p.shape or x.dtype != p.dtype:
+            raise ValueError("p and q differ in shape or type")
+        if (x.stride(2) != 1 and V > 1) or (R > 1 and T > 1 and x.stride(0) != T * x.stride(1)):
+            raise ValueError("p and q need rows one stride apart with dense values")
+        return x.stride(1) if T > 1 else x.stride(0) if R > 1 else V
+
+    if path is None:
+        path = torch.empty((R, T), dtype=torch.int32, device=p.device)
+    if n_path is None:
+        n_path = torch.empty(R, dtype=torch.int32, device=p.device)
+    if next_token is None:
+        next_token = torch.empty(R, dtype=torch.int32, device=p.device)
+    api.tree_verify(DTYPES[p.dtype], R, T, V, n_nodes, parent, token, p, step(p), q,
+                    0 if q is None else step(q), u_accept, u_sample, path, n_path, next_token,
+                    stream=stream)
+    return path, n_path, next_token
+
+
 def block_commit(k_src: torch.Tensor, v_src: torch.Tensor, src_begin: int, n_tokens: int,
                  k_dst: torch.Tensor, v_dst: torch.Tensor, dst_offset: int, pos_delta: int,
                  rope_theta: float, stream=None):

@@ -81,7 +81,8 @@ enum {
                                (it is skipped), or a (row, q head) gathers more partial
                                results than a merge holds */
   HW_DEV_TIMEOUT = 16,      /* a bounded in-kernel wait expired; results are invalid */
-  HW_DEV_BAD_PLAN = 32      /* hw_attn_decode_planned found no plan for this description */
+  HW_DEV_BAD_PLAN = 32,     /* a planned call found no plan for this description */
+  HW_DEV_BAD_TREE = 64      /* a draft tree's node count, parents or path are not a tree's */
 };
 
 /* Limits of this build. */
@@ -95,6 +96,9 @@ enum {
 #define HW_MAX_QHEADS_PER_BLOCK 32
 #define HW_MAX_REFS_PER_BLOCK 255  /* view entries naming one block */
 #define HW_MAX_Q_HEADS 256         /* n_q_heads */
+#define HW_MAX_TREE_NODES 128      /* nodes of a row's draft tree (max_nodes) */
+#define HW_MAX_TREE_QUERIES 65536  /* n_rows * max_nodes of the draft-tree calls */
+#define HW_MAX_VOCAB (1 << 24)     /* hw_tree_verify's vocabulary */
 
 /* Host-side description of one decode call (all scalars, host memory). */
 typedef struct {
@@ -321,6 +325,125 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
                                       const float *k_scale, const float *v_scale, void *out,
                                       float *lse, void *workspace, size_t workspace_bytes,
                                       void *stream);
+
+/*
+ * Trees of drafted tokens.  A step may propose several continuations of each
+ * row (worker) at once, as a tree: its nodes are tokens, parent[i] < i is the
+ * node before node i (-1: none; node 0 is usually the row's pending token),
+ * depth(i) the number of its ancestors.  One pass attends all nodes,
+ * hw_tree_verify decides which of them stand, hw_tree_commit keeps those.
+ *
+ * hw_attn_plan_tree plans a step, once for all its layers, as hw_attn_plan
+ * does; a row's view (view_block, view_offset, q_pos as in hw_attn_decode) is
+ * that of its tokens before the tree, e.g. hw_views on the block lengths, with
+ * q_pos the position of its depth-0 nodes.  Besides (dev, int32):
+ *  tree_block  [n_rows]: the row's own block b; node i's key stands at
+ *              block-local position block_len[b] + depth(i)
+ *  tree_start  [n_rows], the pool token of the row's node 0, node i's is
+ *              tree_start + i; or NULL: the tokens right behind block b
+ *  n_nodes     [n_rows], 0 .. max_nodes (0: the row takes no part)
+ *  parent      [n_rows][max_nodes]
+ * hw_attn_decode_tree then runs one layer: for every row r and node i < n_nodes[r]
+ *   K[h][tree_start + i] = rho(k_new[r][i][h], block_len[b] + depth(i))
+ *   V[h][tree_start + i] = v_new[r][i][h]
+ * (rounded once to the cache's type), and its queries attend every block of
+ * the row's view whole, q rotated by q_pos + depth(i) - view_offset, and of
+ * the tree's tokens node i itself and its ancestors, q rotated by
+ * block_len[b] + depth(i): out and lse as in hw_attn_decode.
+ *  q, out      dev  [n_rows][max_nodes][Hq][D], q 16-byte aligned
+ *  k_new, v_new dev [n_rows][max_nodes][Hkv][D], 16-byte aligned
+ *  lse         dev  float [n_rows][max_nodes][Hq] or NULL
+ * (q, k_new, v_new, out bf16 for HW_FP8_E4M3 caches).  Entries of q, k_new and
+ * v_new at or behind n_nodes[r] are not read, those of out and lse keep what
+ * they hold.  v_new must be finite: as in any masked product, an infinite or
+ * NaN value reaches the nodes that do not attend it too.
+ *
+ * The trees' tokens lie outside every block and one another.  A row whose
+ * tree does not (or leaves the pool) sets HW_DEV_BAD_RANGE, one whose counts
+ * or parents are not a tree's HW_DEV_BAD_TREE, one without a block
+ * HW_DEV_BAD_BLOCK: it takes no part.  View entries and blocks are checked as
+ * in hw_attn_decode (entries of bad blocks are skipped; there is no limit on
+ * the entries that name one block); a q_to_kv without equal groups
+ * (HW_DEV_BAD_HEADMAP) leaves every row out.
+ *
+ * Types: those of hw_attn_decode, and HW_FP8_E4M3 (hw_attn_decode_tree_fp8,
+ * scales as in hw_attn_decode_planned_fp8, new tokens stored as
+ * hw_attn_append_decode_planned_fp8 stores them); no HW_DESC_VIEW_LIMITS.
+ * HW_DESC_EARLY_LOADS is accepted and changes nothing.  The workspace is that
+ * of hw_attn_tree_workspace_size, zeroed once with hw_workspace_init, used by
+ * one stream at a time and by the tree calls of this description and
+ * max_nodes only; hw_workspace_status reads its HW_DEV_* bits.
+ */
+int hw_attn_tree_workspace_size(const hw_attn_desc *d, int32_t max_nodes, size_t *bytes);
+
+int hw_attn_plan_tree(const hw_attn_desc *d, int32_t max_nodes, const int32_t *block_start,
+                      const int32_t *block_len, const int32_t *view_block,
+                      const int32_t *view_offset, const int32_t *q_pos, const int32_t *q_to_kv,
+                      const int32_t *tree_block, const int32_t *tree_start, const int32_t *n_nodes,
+                      const int32_t *parent, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+int hw_attn_decode_tree(const hw_attn_desc *d, int32_t max_nodes, const void *q, const void *k_new,
+                        const void *v_new, void *k_cache, void *v_cache, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+int hw_attn_decode_tree_fp8(const hw_attn_desc *d, int32_t max_nodes, const void *q,
+                            const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                            const float *k_scale, const float *v_scale, void *out, float *lse,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Which drafted tokens stand against the target's probabilities, and the
+ * token after them.  Node 0 is the root, taken as accepted.  At a node the
+ * children are tried in index order, each against the target distribution
+ * p' = p[node] that is left after the children rejected before it:
+ *  q given: every child was drawn from the draft distribution q[node], on its
+ *    own; child x is accepted if u_accept q(x) < p'(x), and a rejection makes
+ *    p' the normalised max(p' - q, 0) (if nothing is left, p' stays);
+ *  q NULL: the children were chosen without chance (say, the draft's best);
+ *    child x is accepted if u_accept < p'(x), and a rejection removes x from
+ *    p' and normalises it.
+ * An accepted child is the next node.  Where none is left, next_token is
+ * drawn from p': the smallest x whose cumulative sum exceeds u_sample times
+ * the whole (-1 if p' is zero everywhere).  The accepted tokens and next_token
+ * are then distributed as the target's own samples.
+ *  dtype       HW_F32 or HW_BF16: type of p and q
+ *  n_nodes     dev int32 [n_rows], parent, token dev int32 [n_rows][max_nodes]
+ *  p, q        dev [n_rows][max_nodes] rows of `vocab` values, p_stride and
+ *              q_stride elements apart: the target's and the draft's
+ *              distribution after each node (element-aligned; q may be NULL).
+ *              Values outside [0, 1] count as the nearer end, NaN as 0; a row
+ *              of p sums to at most 128
+ *  u_accept    dev float [n_rows][max_nodes], in [0, 1): node i's test
+ *  u_sample    dev float [n_rows], in [0, 1)
+ *  path        dev int32 [n_rows][max_nodes]: 0, then the accepted nodes, then -1
+ *  n_path      dev int32 [n_rows]: their number with the root
+ *  next_token  dev int32 [n_rows]
+ * Sums are kept in 64-bit fixed point, so the result does not depend on the
+ * order of anything.  A row with n_nodes 0, or whose counts, parents or tokens
+ * (of nodes 1 ..) are out of range, gets n_path 0 and next_token -1.
+ */
+int hw_tree_verify(int32_t dtype, int32_t n_rows, int32_t max_nodes, int32_t vocab,
+                   const int32_t *n_nodes, const int32_t *parent, const int32_t *token,
+                   const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                   const float *u_accept, const float *u_sample, int32_t *path, int32_t *n_path,
+                   int32_t *next_token, void *stream);
+
+/*
+ * The accepted nodes of every row appended to its block, in all layers, from
+ * hw_tree_verify's path and n_path (dev; the step's plan in the workspace):
+ *   K[l][h][end + j] = K[l][h][tree_start + path[j]],  V alike,  j < n_path[r],
+ * with end = block_start + block_len of the row's tree_block: bit copies, the
+ * keys already stand at their positions.  Pools [n_layers][Hkv][capacity][D].
+ * Block lengths are the caller's to update (block_len += n_path).  A path that
+ * does not ascend through its row's nodes sets HW_DEV_BAD_TREE, a destination
+ * outside the pool, or one that meets another block, tree or destination,
+ * HW_DEV_BAD_RANGE (its own tree may lie right behind the block): that row
+ * moves nothing.
+ */
+int hw_tree_commit(const hw_attn_desc *d, int32_t max_nodes, int32_t n_layers, void *k_cache,
+                   void *v_cache, const int32_t *path, const int32_t *n_path, void *workspace,
+                   size_t workspace_bytes, void *stream);
 
 /*
  * For tests: the work split of the plan in `workspace` (bf16 head_dim-128

@@ -1,0 +1,137 @@
+"""Host checks of the draft-tree calls: refusals before anything is enqueued."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+from concurrent_shared_kv_gb300 import api
+
+P = 1 << 20  # a non-null, aligned pointer that no refused call touches
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
+
+
+@pytest.fixture(scope="module")
+def L():
+    return api.lib()
+
+
+def desc(**kw):
+    a = dict(n_rows=2, n_q_heads=8, n_kv_heads=2, head_dim=128, n_blocks=3, max_view_blocks=3, cache_capacity=1000,
+             dtype=api.HW_BF16, rope_theta=1e4, scale=0.1, flags=0)
+    a.update(kw)
+    return api.make_desc(**a)
+
+
+def size(L, d, nodes):
+    n = ctypes.c_size_t(0)
+    return L.hw_attn_tree_workspace_size(ctypes.byref(d), nodes, ctypes.byref(n))
+
+
+@pytest.mark.parametrize("kw,nodes,status", [
+    ({}, 0, INVALID), ({}, -1, INVALID), ({}, 129, UNSUPPORTED), ({"flags": 1}, 4, UNSUPPORTED),
+    ({"flags": 4}, 4, INVALID), ({"head_dim": 96}, 4, UNSUPPORTED), ({"dtype": 3}, 4, INVALID),
+    ({"dtype": api.HW_FP8_E4M3, "head_dim": 64}, 4, UNSUPPORTED), ({"n_q_heads": 7}, 4, INVALID),
+    ({"n_rows": 4097, "max_view_blocks": 0}, 1, UNSUPPORTED), ({"n_rows": 1024, "max_view_blocks": 1}, 65, UNSUPPORTED),
+    ({"n_rows": -1}, 4, INVALID), ({"rope_theta": 1.0}, 4, INVALID)])
+def test_descriptions(L, kw, nodes, status):
+    assert size(L, desc(**kw), nodes) == status
+    d = desc(**kw)
+    assert L.hw_attn_plan_tree(ctypes.byref(d), nodes, *[P] * 11, 1 << 40, None) == status
+    assert L.hw_tree_commit(ctypes.byref(d), nodes, 1, *[P] * 5, 1 << 40, None) == status
+    if d.dtype != api.HW_FP8_E4M3:
+        assert L.hw_attn_decode_tree(ctypes.byref(d), nodes, *[P] * 8, 1 << 40, None) == status
+
+
+def test_no_rows_is_no_work(L):
+    d = desc(n_rows=0)
+    assert L.hw_attn_plan_tree(ctypes.byref(d), 4, *[None] * 11, 0, None) == OK
+    assert L.hw_attn_decode_tree(ctypes.byref(d), 4, *[None] * 8, 0, None) == OK
+    assert L.hw_tree_commit(ctypes.byref(d), 4, 3, *[None] * 5, 0, None) == OK
+    assert L.hw_tree_commit(ctypes.byref(desc()), 4, 0, *[None] * 5, 0, None) == OK
+    assert L.hw_tree_verify(0, 0, 4, 10, None, None, None, None, 10, None, 0, *[None] * 6) == OK
+
+
+@pytest.mark.parametrize("missing", range(11))
+def test_plan_arguments(L, missing):
+    # block_start, block_len, view_block, view_offset, q_pos, q_to_kv, tree_block, tree_start, n_nodes, parent, workspace
+    a = [P] * 11
+    a[missing] = None
+    want = WORKSPACE if missing in (5, 7, 10) else INVALID  # q_to_kv and tree_start may be NULL
+    a[10] = None if missing in (5, 7) else a[10]            # (then the workspace is what is missing)
+    assert L.hw_attn_plan_tree(ctypes.byref(desc()), 4, *a, 1 << 40, None) == want
+
+
+@pytest.mark.parametrize("missing", range(8))
+def test_decode_arguments(L, missing):
+    # q, k_new, v_new, k_cache, v_cache, out, lse, workspace
+    a = [P] * 8
+    a[missing] = None
+    a[7] = None if missing == 6 else a[7]
+    want = WORKSPACE if missing >= 6 else INVALID  # lse may be NULL
+    assert L.hw_attn_decode_tree(ctypes.byref(desc()), 4, *a, 1 << 40, None) == want
+
+
+@pytest.mark.parametrize("odd", range(5))
+def test_decode_alignment(L, odd):
+    a = [P] * 8
+    a[odd] = P + 8
+    assert L.hw_attn_decode_tree(ctypes.byref(desc()), 4, *a, 1 << 40, None) == INVALID
+    a = [P] * 8
+    a[7] = P + 128  # the workspace at 256 bytes
+    assert L.hw_attn_decode_tree(ctypes.byref(desc()), 4, *a, 1 << 40, None) == WORKSPACE
+
+
+def test_types_have_their_calls(L):
+    f8 = desc(dtype=api.HW_FP8_E4M3)
+    assert L.hw_attn_decode_tree(ctypes.byref(f8), 4, *[P] * 8, 1 << 40, None) == UNSUPPORTED
+    assert L.hw_attn_decode_tree_fp8(ctypes.byref(desc()), 4, *[P] * 10, 1 << 40, None) == INVALID
+    for missing in (5, 6):  # the scales
+        a = [P] * 10
+        a[missing] = None
+        assert L.hw_attn_decode_tree_fp8(ctypes.byref(f8), 4, *a, 1 << 40, None) == INVALID
+
+
+@pytest.mark.parametrize("missing", range(5))
+def test_commit_arguments(L, missing):
+    a = [P] * 5  # k_cache, v_cache, path, n_path, workspace
+    a[missing] = None
+    assert L.hw_tree_commit(ctypes.byref(desc()), 4, 1, *a, 1 << 40, None) == (WORKSPACE if missing == 4 else INVALID)
+    assert L.hw_tree_commit(ctypes.byref(desc()), 4, -1, *[P] * 5, 1 << 40, None) == INVALID
+    a = [P + 8, P, P, P, P]
+    assert L.hw_tree_commit(ctypes.byref(desc()), 4, 1, *a, 1 << 40, None) == INVALID
+
+
+def verify(L, **kw):
+    a = dict(dtype=0, n_rows=2, max_nodes=4, vocab=10, n_nodes=P, parent=P, token=P, p=P, p_stride=10, q=P, q_stride=10,
+             u_accept=P, u_sample=P, path=P, n_path=P, next_token=P, stream=None)
+    a.update(kw)
+    return L.hw_tree_verify(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"dtype": 2}, INVALID), ({"dtype": 7}, INVALID), ({"n_rows": -1}, INVALID), ({"max_nodes": 0}, INVALID),
+    ({"max_nodes": 129}, UNSUPPORTED), ({"vocab": 0}, INVALID), ({"p_stride": 9}, INVALID), ({"q_stride": 9}, INVALID),
+    ({"vocab": (1 << 24) + 1, "p_stride": 1 << 25, "q_stride": 1 << 25}, UNSUPPORTED),
+    ({"n_rows": 20000}, UNSUPPORTED), ({"p": P + 2}, INVALID), ({"q": P + 1, "dtype": 1}, INVALID),
+    ({"n_nodes": None}, INVALID), ({"parent": None}, INVALID), ({"token": None}, INVALID), ({"p": None}, INVALID),
+    ({"u_accept": None}, INVALID), ({"u_sample": None}, INVALID), ({"path": None}, INVALID),
+    ({"n_path": None}, INVALID), ({"next_token": None}, INVALID)])
+def test_verify_arguments(L, kw, status):
+    assert verify(L, **kw) == status
+
+
+def test_verify_tensor_layouts():
+    torch = pytest.importorskip("torch")
+    from concurrent_shared_kv_gb300 import engine
+    i = torch.zeros(2, 3, dtype=torch.int32)
+    u = torch.zeros(2, 3)
+    p = torch.zeros(2, 3, 8)
+    with pytest.raises(ValueError):
+        engine.tree_verify(i[:, 0], i, i, p, p[..., :7], u, u[:, 0])
+    with pytest.raises(ValueError):
+        engine.tree_verify(i[:, 0], i, i, p, p.bfloat16(), u, u[:, 0])
+    with pytest.raises(ValueError):
+        engine.tree_verify(i[:, 0], i, i, p[..., ::2], None, u, u[:, 0])
+    with pytest.raises(ValueError):
+        engine.tree_verify(i[:, 0], i, i, torch.zeros(4, 3, 8)[::2], None, u, u[:, 0])
