@@ -23,7 +23,7 @@ BUILD_TRACE = os.path.join(PKG, "_build_trace")
 LIB_TRACE = os.path.join(BUILD_TRACE, "libhogwild_trace.so")
 
 SOURCES = ["api.cpp", "attn_decode_simt.cu", "attn_decode_tc.cu", "block_commit.cu",
-           "attn_decode_noalloc.cu", "tree_api.cpp", "tree_plan.cu", "tree_simt.cu", "tree_verify.cu"]
+           "attn_decode_noalloc.cu", "tree_api.cpp", "tree_plan.cu", "tree_simt.cu", "tree_tc.cu", "tree_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

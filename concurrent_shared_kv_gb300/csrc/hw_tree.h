@@ -19,7 +19,10 @@
 //   record   = what a CTA leaves for (segment, kv head): per column the
 //              running maximum m and sum l of the softmax (log2 domain) and
 //              the unnormalised output.  The records of one (kv head,
-//              segment) lie behind one another, CTA after CTA.
+//              segment) lie behind one another, CTA after CTA.  Within a
+//              record 8 output elements (32 bytes, a sector) of every column
+//              lie side by side, then the next 8: a thread that owns a column
+//              and a warp that owns a row both move whole sectors.
 // tree_merge_kernel then joins the records of every (row, node, q head).
 #pragma once
 
@@ -48,11 +51,15 @@ struct TreeSeg {
   int32_t row;             // the row whose tree this is, or -1: a block
   int32_t ref0, n_ref;     // its block's references
   int32_t col0, n_cols;    // columns of the block it covers
-  int32_t pad;
+  int32_t table;           // its first entry in the column table
 };
 struct TreeRef {
   int32_t row, col;  // query row; its first column among the block's columns
   int64_t rel;       // rotation of the row's root: q_pos - view_offset (a tree: the root's position)
+};
+struct TreeColumn {
+  int32_t node, head;  // row * max_nodes + node; q head within its kv head's
+  int64_t rel;         // the query's rotation
 };
 struct TreeCta {
   int32_t head, seg, tile, n_units;  // first unit and count
@@ -60,10 +67,10 @@ struct TreeCta {
 
 // Byte offsets of the plan's arrays in the workspace (the error word is at 0).
 struct TreeLayout {
-  size_t hdr, segs, wbase, refs, entry_seg, entry_col, piece_row, piece_cta, ctas;
+  size_t hdr, segs, wbase, refs, columns, entry_seg, entry_col, piece_row, piece_cta, ctas;
   size_t n_nodes, slot, pos, end, depth, mask, heads, block_start, block_len;
   size_t ml, o, total;
-  int64_t max_segs, max_refs, max_rows;
+  int64_t max_segs, max_refs, max_cols, max_rows;
   int32_t cols, tile, ctas_max;
 };
 
@@ -104,16 +111,23 @@ struct TreeVerifyArgs {
 
 TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms);
 // Whether these caches run on the tensor cores.
-inline bool tree_on_tensor_cores(int dtype, int head_dim) { return false; }
+inline bool tree_on_tensor_cores(int dtype, int head_dim) {
+  return dtype == HW_BF16 && head_dim == 128;
+}
 
 cudaError_t launch_tree_plan(const TreeArgs &a, const TreeMeta &m, cudaStream_t s);
 cudaError_t launch_tree_append(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t s);
+cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);
 cudaError_t launch_tree_merge(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaStream_t s);
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
+// Element d of column col in a record of n_cols columns that starts at row rec.
+__device__ __forceinline__ int64_t record_at(int64_t rec, int n_cols, int col, int d, int D) {
+  return rec * D + static_cast<int64_t>(d >> 3) * n_cols * 8 + col * 8 + (d & 7);
+}
 template <typename T>
 __device__ __forceinline__ T *tree_at(const TreeArgs &a, size_t off) {
   return reinterpret_cast<T *>(a.ws + off);

@@ -74,7 +74,15 @@ static int decode_tree(const hw_attn_desc *d, int32_t max_nodes, const void *q, 
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_tree_append(a, s);
-  if (e == cudaSuccess) e = launch_tree_simt(a, s);
+  if (e == cudaSuccess && tree_on_tensor_cores(d->dtype, d->head_dim)) {
+    CUtensorMap km, vm;
+    if (!make_pool_map(&km, k_cache, d->cache_capacity, d->n_kv_heads) ||
+        !make_pool_map(&vm, v_cache, d->cache_capacity, d->n_kv_heads))
+      return cuda_fail(cudaErrorInvalidValue);
+    e = launch_tree_tc(a, km, vm, s);
+  } else if (e == cudaSuccess) {
+    e = launch_tree_simt(a, s);
+  }
   if (e == cudaSuccess) e = launch_tree_merge(a, s);
   return e == cudaSuccess ? HW_OK : cuda_fail(e);
 }

@@ -308,6 +308,15 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
+  // the segments' places in the column table
+  for (int s0 = 0; s0 < n_segs; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    const int64_t at = block_scan(S, s < n_segs ? segs[s].n_cols : 0);
+    if (s < n_segs) segs[s].table = static_cast<int32_t>(at);
+  }
+  __syncthreads();
+  if (tid == 0) S.carry = 0;
+  __syncthreads();
   int64_t *ubase = wbase + a.L.max_segs;
   for (int s0 = 0; s0 < n_segs; s0 += kPlanThreads) {
     const int s = s0 + tid;
@@ -376,6 +385,30 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
                      n_segs, C, 0, a.capacity};
 }
 
+// The columns' queries and rotations, a CTA a segment.
+__global__ void __launch_bounds__(256) tree_columns_kernel(const __grid_constant__ TreeArgs a) {
+  if (!tree_plan_ok(a)) return;
+  const int n_segs = tree_at<TreeHeader>(a, a.L.hdr)->n_segs;
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const TreeRef *refs = tree_at<TreeRef>(a, a.L.refs);
+  for (int s = blockIdx.x; s < n_segs; s += gridDim.x) {
+    const TreeSeg sg = tree_at<TreeSeg>(a, a.L.segs)[s];
+    for (int x = threadIdx.x; x < sg.n_cols; x += 256) {
+      const int col = sg.col0 + x;
+      int lo = 0, hi = sg.n_ref;  // the reference that holds the column
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (refs[sg.ref0 + mid].col <= col) lo = mid; else hi = mid;
+      }
+      const TreeRef ref = refs[sg.ref0 + lo];
+      const int local = col - ref.col;
+      const int node = ref.row * a.max_nodes + local / G;
+      tree_at<TreeColumn>(a, a.L.columns)[sg.table + x] =
+          TreeColumn{node, local % G, ref.rel + tree_at<int32_t>(a, a.L.depth)[node]};
+    }
+  }
+}
+
 // ---------------------------------------------------------------- append
 
 // cos and sin of a position's angle for one pair, for keys that stay in the
@@ -398,6 +431,10 @@ __device__ __forceinline__ void rope_cos_sin_exact(int64_t rel, uint64_t phase, 
 // head's scale first, saturating at 448).
 template <typename T, bool kFp8>
 __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant__ TreeArgs a) {
+  // Dependents start only once everything before this launch is complete:
+  // the attention kernel counts on it.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!tree_plan_ok(a)) return;  // the attention launch records it
   const int lane = threadIdx.x & 31, half = a.head_dim / 2, D = a.head_dim;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -443,7 +480,7 @@ constexpr int kMergeList = 256;  // records a warp lists at a time
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int EPL = D / 32;
-  __shared__ int32_t list_s[kMergeWarps][kMergeList];
+  __shared__ int2 list_s[kMergeWarps][kMergeList];  // record's first row; its columns, the item's column
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (!tree_plan_ok(a)) return;
   const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
@@ -452,13 +489,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   const int x = static_cast<int>(item % a.n_q_heads);  // place in the head list: kv head, then its q heads
   const int64_t node = item / a.n_q_heads;
   const int r = static_cast<int>(node / a.max_nodes), i = static_cast<int>(node % a.max_nodes);
-  if (r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) return;
+  if (r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever follows this grid follows that one
+    return;
+  }
   const int h = x / G, hq = tree_at<int32_t>(a, a.L.heads)[x];
   const int local = i * G + x % G;
-  int32_t *list = list_s[warp];
+  int2 *list = list_s[warp];
+  bool waited = false;
   const int32_t *entry_seg = tree_at<int32_t>(a, a.L.entry_seg), *entry_col = tree_at<int32_t>(a, a.L.entry_col);
   const float2 *ml = tree_at<float2>(a, a.L.ml);
-  const float *o = tree_at<float>(a, a.L.o) + lane * EPL;
+  const float *o = tree_at<float>(a, a.L.o);
   float M = -INFINITY, L = 0.f, acc[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
@@ -468,17 +509,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
     int n = 0;
     for (int v0 = 0; v0 <= a.n_view; v0 += 32) {
       const int v = v0 + lane;
-      int cnt = 0, row0 = 0, step = 0;
+      int cnt = 0, row0 = 0, step = 0, col = 0;
       if (v <= a.n_view) {
         const int e = v < a.n_view ? r * a.n_view + v : a.n_rows * a.n_view + r;
         const int s0 = entry_seg[e];
         if (s0 >= 0) {
-          const int col = entry_col[e] + local;
+          col = entry_col[e] + local;
           const int s = s0 + col / a.L.cols;
+          col %= a.L.cols;
           const int64_t k = static_cast<int64_t>(h) * hdr.n_segs + s;
           cnt = tree_at<int2>(a, a.L.piece_cta)[k].y;
           step = tree_at<TreeSeg>(a, a.L.segs)[s].n_cols;
-          row0 = tree_at<int32_t>(a, a.L.piece_row)[k] + col % a.L.cols;
+          row0 = tree_at<int32_t>(a, a.L.piece_row)[k];
         }
       }
       int incl = cnt;
@@ -488,14 +530,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
         if (lane >= d) incl += y;
       }
       const int at = n + incl - cnt - first;
-      for (int j = max(0, -at); j < cnt && at + j < kMergeList; ++j) list[at + j] = row0 + j * step;
+      for (int j = max(0, -at); j < cnt && at + j < kMergeList; ++j)
+        list[at + j] = make_int2(row0 + j * step, step << 16 | col);
       n += __shfl_sync(0xffffffffu, incl, 31);
     }
     __syncwarp();
     total = n;
     n = min(n - first, kMergeList);
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the records
+    waited = true;
     float top = M;
-    for (int j = lane; j < n; j += 32) top = fmaxf(top, ml[list[j]].x);
+    for (int j = lane; j < n; j += 32) top = fmaxf(top, ml[list[j].x + (list[j].y & 0xffff)].x);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     const float old = M == -INFINITY ? 0.f : ex2(M - top);
@@ -505,16 +550,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
     for (int e = 0; e < EPL; ++e) acc[e] *= old;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) {
-      const int row = list[j];
-      const float2 x2 = ml[row];
+      const int2 at = list[j];
+      const int col = at.y & 0xffff;
+      const float2 x2 = ml[at.x + col];
       const float w = M == -INFINITY ? 0.f : ex2(x2.x - M);
       L += x2.y * w;
+      const float *src = o + record_at(at.x, at.y >> 16, col, lane * EPL, D);
       float val[EPL];
       if constexpr (EPL == 4) {
-        const float4 y = *reinterpret_cast<const float4 *>(o + static_cast<int64_t>(row) * D);
+        const float4 y = *reinterpret_cast<const float4 *>(src);
         val[0] = y.x; val[1] = y.y; val[2] = y.z; val[3] = y.w;
       } else {
-        const float2 y = *reinterpret_cast<const float2 *>(o + static_cast<int64_t>(row) * D);
+        const float2 y = *reinterpret_cast<const float2 *>(src);
         val[0] = y.x; val[1] = y.y;
       }
 #pragma unroll
@@ -603,36 +650,48 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
 
 }  // namespace
 
+// A launch that may start while the one before it on the stream ends; the
+// kernel waits for that one itself (griddepcontrol.wait).
+template <typename... P, typename... A>
+static cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_tree_plan(const TreeArgs &a, const TreeMeta &m, cudaStream_t s) {
   static_assert(sizeof(TreePlanSmem) <= 48 * 1024, "the plan's shared memory needs no opt-in");
   tree_plan_kernel<<<1, kPlanThreads, sizeof(TreePlanSmem), s>>>(a, m);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t most = 4ll * a.L.ctas_max;
+  tree_columns_kernel<<<static_cast<unsigned>(a.L.max_segs < most ? a.L.max_segs : most), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_tree_append(const TreeArgs &a, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(a.n_rows) * a.max_nodes * a.n_kv_heads;
   const unsigned grid = static_cast<unsigned>((items + 7) / 8);
-  if (a.dtype == HW_F32)
-    tree_append_kernel<float, false><<<grid, 256, 0, s>>>(a);
-  else if (a.dtype == HW_FP8_E4M3)
-    tree_append_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(a);
-  else
-    tree_append_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.dtype == HW_F32) return launch_dependent(tree_append_kernel<float, false>, grid, 256, s, a);
+  if (a.dtype == HW_FP8_E4M3) return launch_dependent(tree_append_kernel<__nv_bfloat16, true>, grid, 256, s, a);
+  return launch_dependent(tree_append_kernel<__nv_bfloat16, false>, grid, 256, s, a);
 }
 
 cudaError_t launch_tree_merge(const TreeArgs &a, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(a.n_rows) * a.max_nodes * a.n_q_heads;
   const unsigned grid = static_cast<unsigned>((items + kMergeWarps - 1) / kMergeWarps);
   const bool d64 = a.head_dim == 64;
-  if (a.dtype == HW_F32) {
-    if (d64) tree_merge_kernel<float, 64><<<grid, kMergeWarps * 32, 0, s>>>(a);
-    else tree_merge_kernel<float, 128><<<grid, kMergeWarps * 32, 0, s>>>(a);
-  } else {
-    if (d64) tree_merge_kernel<__nv_bfloat16, 64><<<grid, kMergeWarps * 32, 0, s>>>(a);
-    else tree_merge_kernel<__nv_bfloat16, 128><<<grid, kMergeWarps * 32, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.dtype == HW_F32)
+    return launch_dependent(d64 ? tree_merge_kernel<float, 64> : tree_merge_kernel<float, 128>, grid, kMergeWarps * 32, s, a);
+  return launch_dependent(d64 ? tree_merge_kernel<__nv_bfloat16, 64> : tree_merge_kernel<__nv_bfloat16, 128>, grid,
+                          kMergeWarps * 32, s, a);
 }
 
 cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaStream_t s) {
@@ -659,6 +718,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.max_refs = E + R;
   // sum of ceil(cols / L.cols) over the referenced blocks and the trees
   L.max_segs = d.n_blocks + block_cols / L.cols + R + tree_cols / L.cols + 1;
+  L.max_cols = block_cols + tree_cols;
   L.max_rows = d.n_kv_heads * (block_cols + tree_cols) + static_cast<int64_t>(L.ctas_max) * L.cols;
   size_t at = 256;
   auto put = [&](size_t bytes) {
@@ -670,6 +730,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.segs = put(sizeof(TreeSeg) * L.max_segs);
   L.wbase = put(2 * sizeof(int64_t) * L.max_segs);  // weights, then units before each segment
   L.refs = put(sizeof(TreeRef) * L.max_refs);
+  L.columns = put(sizeof(TreeColumn) * L.max_cols);
   L.entry_seg = put(4 * L.max_refs);
   L.entry_col = put(4 * L.max_refs);
   L.piece_row = put(4 * L.max_segs * d.n_kv_heads);

@@ -78,8 +78,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
   if (c >= hdr.n_ctas) return;
   TreeCta at = tree_at<TreeCta>(a, a.L.ctas)[c];
   const TreeSeg *segs = tree_at<TreeSeg>(a, a.L.segs);
-  const TreeRef *refs = tree_at<TreeRef>(a, a.L.refs);
-  const int32_t *depth = tree_at<int32_t>(a, a.L.depth);
+  const TreeColumn *columns = tree_at<TreeColumn>(a, a.L.columns);
   const int G = a.n_q_heads / a.n_kv_heads;
   constexpr int EPV = 16 / sizeof(KV), CPR = D / EPV;
   constexpr int QSTEP = kThreads / D;   // columns side by side in P.V
@@ -90,20 +89,11 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     const TreeSeg sg = segs[at.seg];
     const int h = at.head, nq = sg.n_cols;
     const float ks = a.k_scale ? a.k_scale[h] : 1.f, vs = a.v_scale ? a.v_scale[h] : 1.f;
-    // the columns' nodes
     if (tid < nq) {
-      const int col = sg.col0 + tid;
-      int lo = 0, hi = sg.n_ref;  // the reference that holds the column
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (refs[sg.ref0 + mid].col <= col) lo = mid; else hi = mid;
-      }
-      const TreeRef ref = refs[sg.ref0 + lo];
-      const int local = col - ref.col;
-      const int node = ref.row * a.max_nodes + local / G;
-      S.node[tid] = node;
-      S.qrow[tid] = node * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[h * G + local % G];
-      S.rel[tid] = ref.rel + depth[node];
+      const TreeColumn tc = columns[sg.table + tid];
+      S.node[tid] = tc.node;
+      S.qrow[tid] = tc.node * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[h * G + tc.head];
+      S.rel[tid] = tc.rel;
       S.m[tid] = -INFINITY;
       S.l[tid] = 0.f;
     }
@@ -209,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     for (int k2 = 0; k2 < QPT; ++k2) {
       const int qi = qfirst + k2 * QSTEP;
       if (qi < nq) {
-        tree_at<float>(a, a.L.o)[(rec + qi) * D + dcol] = acc[k2];
+        tree_at<float>(a, a.L.o)[record_at(rec, nq, qi, dcol, D)] = acc[k2];
         if (dcol == 0) tree_at<float2>(a, a.L.ml)[rec + qi] = make_float2(S.m[qi], S.l[qi]);
       }
     }

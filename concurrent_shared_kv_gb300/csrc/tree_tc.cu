@@ -1,0 +1,515 @@
+// tree_tc.cu - attention for trees of drafted tokens on the sm_100 tensor
+// cores (tcgen05 + TMEM): bf16 caches with head_dim 128.
+//
+// A segment (hw_tree.h) puts up to 256 query columns (nodes x q heads of a kv
+// head x rows that see the block) against its tokens, as two query tiles of
+// 128 rows that share every K/V tile:
+//   S [128 queries x 128 tokens] = Q~ . K^T     (A, B in shared memory)
+//   O [128 queries x 128 d]     += P . V        (A = P in TMEM)
+// With a query per TMEM lane, a softmax thread owns its row: no exchange for
+// maxima and sums, and P goes back to the columns that S came from.
+//
+// Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 the TMA producer, 9 the MMA
+// issuer.  The issuer alternates the tiles - PV0(i-1), QK0(i), PV1(i-1),
+// QK1(i) - so that one tile's products run under the other's softmax.
+// Rotated queries carry scale * log2(e), so scores leave the MMA in log2
+// units; they are rounded to bf16 once, as P is: both leave an error of half a
+// bf16 step, that of the output itself.
+#include <cuda.h>
+
+#include "hw_device.cuh"
+#include "hw_sm100.cuh"
+#include "hw_tree.h"
+
+namespace hw {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kT = 128;                      // tokens per tile
+constexpr uint32_t kBox = 128 * 128;         // 128 rows of 128 bytes, 128-byte swizzled
+constexpr uint32_t kQTile = 2 * kBox;        // a query tile: d 0-63, d 64-127
+constexpr uint32_t kStage = 2 * kBox;        // a K or a V tile
+constexpr int kStages = 5;
+constexpr float kLazy = 8.f;                 // O is rescaled only when a maximum grows by over 2^8
+constexpr uint32_t kTmemCols = 512;          // S0/P0, S1/P1, O0, O1: 128 columns each
+
+struct TcSmem {
+  alignas(1024) uint8_t q[2][kQTile];
+  alignas(1024) uint8_t kv[kStages][kStage];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_empty[2], mma_done;
+  uint32_t tmem;
+  int32_t abort_flag;
+};
+static_assert(sizeof(TcSmem) + 1024 <= 232448, "shared memory of one CTA per SM");
+
+__device__ __forceinline__ bool aborted(TcSmem &S) {
+  return *reinterpret_cast<volatile int32_t *>(&S.abort_flag) != 0;
+}
+// Wait with a bound; false once the CTA winds down.
+__device__ __forceinline__ bool wait_or_abort(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
+  if (mbar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (aborted(S)) return false;
+    if (clock64() - t0 > kWaitLimit) {
+      *reinterpret_cast<volatile int32_t *>(&S.abort_flag) = 1;
+      flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulator.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// The CTA's units, segment by segment.
+struct Walk {
+  int head, seg, tile, left;  // kv head, segment, first tile of it, units still to come
+  int n_segs;
+  TreeSeg sg;
+  int tiles;  // of this segment that are the CTA's
+  __device__ __forceinline__ void load(const TreeSeg *segs) {
+    sg = segs[seg];
+    tiles = min((sg.len + kT - 1) / kT - tile, left);
+  }
+  __device__ __forceinline__ bool next(const TreeSeg *segs) {
+    left -= tiles;
+    if (left <= 0) return false;
+    tile = 0;
+    if (++seg == n_segs) {
+      seg = 0;
+      ++head;
+    }
+    load(segs);
+    return true;
+  }
+};
+
+__device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, const CUtensorMap *tv, Walk w,
+                         const TreeSeg *segs) {
+  const uint64_t pol = policy_evict_first();
+  int n = 0;  // ring entries issued: K(0), V(0), K(1), V(1), ...
+  bool waited = false, go = true;
+  do {
+    if (w.sg.row >= 0 && !waited) {  // a tree: its tokens come from the launch before
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      asm volatile("fence.proxy.async;" ::: "memory");
+      waited = true;
+    }
+    for (int t = w.tile; go && t < w.tile + w.tiles; ++t) {
+      const int row = w.sg.start + t * kT;
+      for (int kv = 0; kv < 2; ++kv, ++n) {
+        const int s = n % kStages;
+        if (n >= kStages && !wait_or_abort(S, a, &S.kv_empty[s], ((n / kStages) & 1) ^ 1)) {
+          go = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&S.kv_full[s], kStage);
+        tma_load_3d(S.kv[s], kv ? tv : tk, &S.kv_full[s], 0, row, w.head, pol);
+        tma_load_3d(S.kv[s] + kBox, kv ? tv : tk, &S.kv_full[s], 64, row, w.head, pol);
+      }
+    }
+  } while (go && w.next(segs));
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // no copy may still be landing when the CTA retires
+  for (int j = n > kStages ? n - kStages : 0; j < n; ++j) mbar_wait(&S.kv_full[j % kStages], (j / kStages) & 1);
+}
+
+__device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, const TreeSeg *segs) {
+  constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0), idesc_pv = idesc_bf16(128, 128, 0, 1);
+  const uint32_t q0 = smem_u32(S.q[0]), kv0 = smem_u32(S.kv[0]);
+  const uint64_t a_qk = smem_desc(q0, 16, 1024, kSw128), b_qk = smem_desc(kv0, 16, 1024, kSw128);
+  const uint64_t b_pv = smem_desc(kv0, kBox, 1024, kSw128);
+  int i = 0;                         // tiles whose QK is issued
+  // per query tile: PVs issued, segments whose PVs and whose QKs have begun
+  int np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0};
+  auto qk = [&](int qt, int s) {
+    const uint64_t as = a_qk + ((qt * kQTile) >> 4), bs = b_qk + ((s * kStage) >> 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
+      const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+      mma_bf16(tmem + qt * 128, as + o, bs + o, idesc_qk, k > 0);
+    }
+    mma_commit(&S.s_full[qt]);
+  };
+  // PV of query tile qt against the V in ring entry n
+  auto pv = [&](int qt, int n, int ksteps, bool first) -> bool {
+    if (!wait_or_abort(S, a, &S.p_full[qt], np[qt] & 1)) return false;
+    if (!wait_or_abort(S, a, &S.kv_full[n % kStages], (n / kStages) & 1)) return false;
+    if (first) {
+      if (!wait_or_abort(S, a, &S.o_empty[qt], (no[qt] & 1) ^ 1)) return false;
+      ++no[qt];
+    }
+    tc_fence_after();
+    const uint64_t bs = b_pv + (((n % kStages) * kStage) >> 4);
+    for (int k = 0; k < ksteps; ++k)  // steps of 16 tokens
+      mma_bf16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + k * 8, bs + ((k * 2048) >> 4), idesc_pv,
+                  !(first && k == 0));
+    mma_commit(&S.pv_done[qt]);
+    ++np[qt];
+    return true;
+  };
+  bool pend = false, pend_two = false, pend_first = false;  // the tile whose PVs are to come
+  int pend_steps = 0;
+  bool go = true;
+  do {
+    const bool two = w.sg.n_cols > 128;
+    for (int t = 0; go && t < w.tiles; ++t, ++i) {
+      const bool first = t == 0;
+      const int nk = 2 * i, nv = 2 * i - 1;
+      if (pend && !(go = pv(0, nv, pend_steps, pend_first))) break;
+      if (!first) {
+        if (!(go = wait_or_abort(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
+        tc_fence_after();
+        qk(0, nk % kStages);
+      }
+      if (pend && pend_two && !(go = pv(1, nv, pend_steps, pend_first))) break;
+      if (pend) mma_commit(&S.kv_empty[nv % kStages]);
+      if (first) {
+        if (!(go = wait_or_abort(S, a, &S.q_full[0], nq[0]++ & 1))) break;
+        if (two && !(go = wait_or_abort(S, a, &S.q_full[1], nq[1]++ & 1))) break;
+        if (!(go = wait_or_abort(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
+        tc_fence_after();
+        qk(0, nk % kStages);
+      }
+      if (two) qk(1, nk % kStages);
+      mma_commit(&S.kv_empty[nk % kStages]);
+      pend = true;
+      pend_two = two;
+      pend_first = first;
+      pend_steps = (min(kT, w.sg.len - (w.tile + t) * kT) + 15) / 16;
+    }
+  } while (go && w.next(segs));
+  if (go && pend) {
+    if (pv(0, 2 * i - 1, pend_steps, pend_first) && pend_two) pv(1, 2 * i - 1, pend_steps, pend_first);
+  }
+  mma_commit(&S.mma_done);
+  mbar_wait(&S.mma_done, 0);
+}
+
+// One row's record: (m, l) and O, 32 bytes of every 8 d side by side for the
+// segment's columns, so that a warp's stores fill whole sectors.
+__device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem, int64_t rec, int n_cols, int col,
+                                             float m, float l) {
+  float *dst = tree_at<float>(a, a.L.o) + rec * 128 + col * 8;
+  const bool on = col < n_cols;
+  if (on) tree_at<float2>(a, a.L.ml)[rec + col] = make_float2(m, l);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    tmem_ld32(o_tmem + 32 * c, r);
+    tmem_wait_ld();
+    if (on) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float4 v = make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
+                                     __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
+        *reinterpret_cast<float4 *>(dst + static_cast<int64_t>(4 * c + x / 2) * n_cols * 8 + (x & 1) * 4) = v;
+      }
+    }
+  }
+}
+
+// wait_or_abort by a whole warp, with one answer for all its lanes: what
+// follows are warp-wide TMEM accesses.
+__device__ __forceinline__ bool warp_wait(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_or_abort(S, a, bar, parity));
+}
+
+__device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, const TreeSeg *segs, int qt) {
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
+  const int col = qt * 128 + row;  // the thread's column of a segment
+  const uint32_t s_tmem = tmem + qt * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+  const uint32_t o_tmem = s_tmem + 256;
+  const TreeColumn *columns = tree_at<TreeColumn>(a, a.L.columns);
+  const int32_t *heads = tree_at<int32_t>(a, a.L.heads);
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const uint32_t qrow = smem_u32(S.q[qt]) + row * 128;
+  int ns = 0;          // tiles of this query tile so far
+  int i = 0;           // tiles of the CTA so far
+  float m = 0.f, l = 0.f;
+  // the record to come: that of the segment before
+  bool have = false;
+  int64_t rec = 0;
+  int rec_cols = 0;
+  do {
+    const bool mine = col < w.sg.n_cols;                      // a query in this row
+    const bool active = qt == 0 || w.sg.n_cols > 128;         // a query in this tile
+    const bool warp_on = qt * 128 + quarter * 32 < w.sg.n_cols;
+    TreeColumn tc = {};
+    const uint4 *src = nullptr;
+    if (mine) {
+      tc = columns[w.sg.table + col];
+      const int64_t at = (static_cast<int64_t>(tc.node) * a.n_q_heads + heads[w.head * G + tc.head]) * 128;
+      src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at);
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(src + 8));
+    }
+    // the segment before is done with Q~ and with O
+    if (have && !warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
+    if (mine) {
+#pragma unroll 2
+      for (int c = 0; c < 8; ++c) {  // elements 8c .. 8c+7 and their partners, 64 further
+        const uint4 u = __ldg(src + c), v = __ldg(src + c + 8);
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+        uint32_t p[4], r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo[2], hi[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x0 = __uint_as_float(e ? (x[j] & 0xffff0000u) : (x[j] << 16));
+            const float x1 = __uint_as_float(e ? (y[j] & 0xffff0000u) : (y[j] << 16));
+            float cs, sn;
+            rope_cos_sin_fast(tc.rel, a.phase[8 * c + 2 * j + e], &cs, &sn);
+            lo[e] = (x0 * cs - x1 * sn) * a.scale_log2;
+            hi[e] = (x1 * cs + x0 * sn) * a.scale_log2;
+          }
+          p[j] = pack_bf16(lo[0], lo[1]);
+          r[j] = pack_bf16(hi[0], hi[1]);
+        }
+        const uint32_t o = (c ^ (row & 7)) << 4;
+        st_shared_v4(qrow + o, p[0], p[1], p[2], p[3]);
+        st_shared_v4(qrow + kBox + o, r[0], r[1], r[2], r[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (active && lane == 0) mbar_arrive(&S.q_full[qt]);
+    if (have) {
+      tc_fence_after();
+      store_record(a, o_tmem, rec, rec_cols, col, m, l);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.o_empty[qt]);
+    }
+    have = active;
+    if (!active) {
+      i += w.tiles;
+      continue;
+    }
+    {
+      const int64_t k = static_cast<int64_t>(w.head) * w.n_segs + w.seg;
+      rec = tree_at<int32_t>(a, a.L.piece_row)[k] +
+            static_cast<int64_t>(blockIdx.x - tree_at<int2>(a, a.L.piece_cta)[k].x) * w.sg.n_cols;
+      rec_cols = w.sg.n_cols;
+    }
+    uint4 tree = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (w.sg.row >= 0 && mine) tree = tree_at<uint4>(a, a.L.mask)[tc.node];
+    for (int t = 0; t < w.tiles; ++t, ++i, ++ns) {
+      const int valid = min(kT, w.sg.len - (w.tile + t) * kT);
+      if (!warp_wait(S, a, &S.s_full[qt], ns & 1)) return;
+      if (qt == 0 && (valid & 15)) {
+        // V rows past the segment may hold anything, and 0 * NaN would poison
+        // the sum: the rows of the last step of 16 tokens are cleared
+        const int nv = 2 * i + 1;
+        if (!warp_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1)) return;
+        const int rows = 16 - (valid & 15);
+        for (int z = row; z < rows * 16; z += 128)
+          st_shared_v4(smem_u32(S.kv[nv % kStages]) + ((z >> 3) & 1) * kBox + (valid + (z >> 4)) * 128 + (z & 7) * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      if (warp_on) {
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
+        tmem_wait_ld();
+        if (valid < kT || w.sg.row >= 0) {
+          const uint32_t tm[4] = {tree.x, tree.y, tree.z, tree.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int in = min(32, max(0, valid - 32 * c));
+            const uint32_t bits = tm[c] & (in == 32 ? ~0u : (1u << in) - 1u);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((bits >> j) & 1u)) s[c][j] = 0xff800000u;  // -inf
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+          for (int j = 2; j < 32; j += 2)
+            mx[c] = max3(mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+        }
+        float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        if (top == -INFINITY) top = -1e30f;  // (only where nothing is finite)
+        if (t == 0) {
+          m = top;
+          l = 0.f;
+        } else if (__any_sync(0xffffffffu, mine && top > m + kLazy)) {
+          // (rows without a query hold anything: they must not count)
+          const float to = top > m + kLazy ? top : m, al = ex2(m - to);
+          m = to;
+          l *= al;
+          if (!warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 16; ++c) {  // (rare: few registers beside S matter more than speed)
+            uint32_t r[8];
+            tmem_ld8(o_tmem + 8 * c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al);
+            tmem_st8(o_tmem + 8 * c, r);
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float p0 = ex2(__uint_as_float(s[2 * c + j / 16][2 * j % 32]) - m);
+            const float p1 = ex2(__uint_as_float(s[2 * c + j / 16][2 * j % 32 + 1]) - m);
+            sum[2 * (j & 1)] += p0;
+            sum[2 * (j & 1) + 1] += p1;
+            p[j] = pack_bf16(p0, p1);
+          }
+          tmem_st32(s_tmem + 32 * c, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[qt]);
+    }
+  } while (w.next(segs));
+  if (have) {
+    if (!warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
+    tc_fence_after();
+    store_record(a, o_tmem, rec, rec_cols, col, m, l);
+  }
+}
+
+// A programmatic dependent of the append launch, which itself starts its
+// dependents only once everything before it is complete: the plan, q and the
+// records' memory may be used at once, and only the trees' tiles wait for the
+// launch before (the producer).  Every CTA waits for it before it ends, so
+// that whoever follows this grid follows the append too.
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv) {
+  extern __shared__ uint8_t smem_raw[];
+  TcSmem &S = *reinterpret_cast<TcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!tree_plan_ok(a)) {
+    if (tid == 0) flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_BAD_PLAN);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
+  if (static_cast<int>(blockIdx.x) >= hdr.n_ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const TreeSeg *segs = tree_at<TreeSeg>(a, a.L.segs);
+  const TreeCta c = tree_at<TreeCta>(a, a.L.ctas)[blockIdx.x];
+  Walk w = {c.head, c.seg, c.tile, c.n_units, hdr.n_segs, {}, 0};
+  w.load(segs);
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&S.kv_full[s], 1);
+      mbar_init(&S.kv_empty[s], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&S.q_full[q], 4);
+      mbar_init(&S.s_full[q], 1);
+      mbar_init(&S.p_full[q], 4);
+      mbar_init(&S.pv_done[q], 1);
+      mbar_init(&S.o_empty[q], 4);
+    }
+    mbar_init(&S.mma_done, 1);
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&S.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  if (warp == kWarpTma) {
+    if ((tid & 31) == 0) producer(a, S, &tk, &tv, w, segs);
+  } else if (warp == kWarpMma) {
+    if ((tid & 31) == 0) mma_issuer(a, S, tmem, w, segs);
+  } else if (warp < 8) {
+    softmax(a, S, tmem, w, segs, warp >> 2);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
+  const size_t smem = sizeof(TcSmem) + 1024;
+  static bool configured = false;
+  if (!configured) {
+    const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    configured = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.L.ctas_max);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_tc_kernel, a, tk, tv);
+}
+
+}  // namespace hw
