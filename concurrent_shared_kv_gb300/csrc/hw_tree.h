@@ -23,6 +23,8 @@
 //              record 8 output elements (32 bytes, a sector) of every column
 //              lie side by side, then the next 8: a thread that owns a column
 //              and a warp that owns a row both move whole sectors.
+// The rotation of a (reference, node) is the same for every layer and q head:
+// the plan holds its cos and sin, fp32, one row of head_dim / 2 pairs each.
 // tree_merge_kernel then joins the records of every (row, node, q head).
 #pragma once
 
@@ -52,6 +54,8 @@ struct TreeSeg {
   int32_t ref0, n_ref;     // its block's references
   int32_t col0, n_cols;    // columns of the block it covers
   int32_t table;           // its first entry in the column table
+  int32_t rot0;            // its block's first row in the rotation table
+  int32_t pad[3];
 };
 struct TreeRef {
   int32_t row, col;  // query row; its first column among the block's columns
@@ -59,7 +63,8 @@ struct TreeRef {
 };
 struct TreeColumn {
   int32_t node, head;  // row * max_nodes + node; q head within its kv head's
-  int64_t rel;         // the query's rotation
+  int32_t rot;         // the query's rotation: row of the table of (cos, sin) pairs
+  int32_t pad;
 };
 struct TreeCta {
   int32_t head, seg, tile, n_units;  // first unit and count
@@ -67,10 +72,10 @@ struct TreeCta {
 
 // Byte offsets of the plan's arrays in the workspace (the error word is at 0).
 struct TreeLayout {
-  size_t hdr, segs, wbase, refs, columns, entry_seg, entry_col, piece_row, piece_cta, ctas;
+  size_t hdr, segs, wbase, refs, columns, rot, entry_seg, entry_col, piece_row, piece_cta, ctas;
   size_t n_nodes, slot, pos, end, depth, mask, heads, block_start, block_len;
   size_t ml, o, total;
-  int64_t max_segs, max_refs, max_cols, max_rows;
+  int64_t max_segs, max_refs, max_cols, max_rots, max_rows;
   int32_t cols, tile, ctas_max;
 };
 

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       if (pass) {
         const int first = S.refs[b], seg0 = S.seg0[b];
         for (int g = lane; g * CG < ncol; g += 32)
-          segs[seg0 + g] = TreeSeg{S.start[b], S.len[b], -1, first, nref, g * CG, min(CG, ncol - g * CG), 0};
+          segs[seg0 + g] = TreeSeg{S.start[b], S.len[b], -1, first, nref, g * CG, min(CG, ncol - g * CG), 0, 0, {}};
       }
     }
     __syncthreads();
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       refs[E + r] = TreeRef{r, 0, n > 0 ? tree_at<int32_t>(a, a.L.pos)[r] : 0};
       const int at = n > 0 ? tree_at<int32_t>(a, a.L.slot)[r] : 0;
       for (int g = 0; g < ns; ++g)
-        segs[s0 + g] = TreeSeg{at, n, r, E + r, 1, g * CG, min(CG, n * G - g * CG), 0};
+        segs[s0 + g] = TreeSeg{at, n, r, E + r, 1, g * CG, min(CG, n * G - g * CG), 0, 0, {}};
     }
   }
   const int n_segs = static_cast<int>(S.carry);
@@ -312,7 +312,11 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   for (int s0 = 0; s0 < n_segs; s0 += kPlanThreads) {
     const int s = s0 + tid;
     const int64_t at = block_scan(S, s < n_segs ? segs[s].n_cols : 0);
-    if (s < n_segs) segs[s].table = static_cast<int32_t>(at);
+    if (s < n_segs) {
+      segs[s].table = static_cast<int32_t>(at);
+      // (a block's columns are whole groups of G: its first one starts a row)
+      segs[s].rot0 = static_cast<int32_t>((at - segs[s].col0) / G);
+    }
   }
   __syncthreads();
   if (tid == 0) S.carry = 0;
@@ -385,34 +389,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
                      n_segs, C, 0, a.capacity};
 }
 
-// The columns' queries and rotations, a CTA a segment.
-__global__ void __launch_bounds__(256) tree_columns_kernel(const __grid_constant__ TreeArgs a) {
-  if (!tree_plan_ok(a)) return;
-  const int n_segs = tree_at<TreeHeader>(a, a.L.hdr)->n_segs;
-  const int G = a.n_q_heads / a.n_kv_heads;
-  const TreeRef *refs = tree_at<TreeRef>(a, a.L.refs);
-  for (int s = blockIdx.x; s < n_segs; s += gridDim.x) {
-    const TreeSeg sg = tree_at<TreeSeg>(a, a.L.segs)[s];
-    for (int x = threadIdx.x; x < sg.n_cols; x += 256) {
-      const int col = sg.col0 + x;
-      int lo = 0, hi = sg.n_ref;  // the reference that holds the column
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (refs[sg.ref0 + mid].col <= col) lo = mid; else hi = mid;
-      }
-      const TreeRef ref = refs[sg.ref0 + lo];
-      const int local = col - ref.col;
-      const int node = ref.row * a.max_nodes + local / G;
-      tree_at<TreeColumn>(a, a.L.columns)[sg.table + x] =
-          TreeColumn{node, local % G, ref.rel + tree_at<int32_t>(a, a.L.depth)[node]};
-    }
-  }
-}
-
-// ---------------------------------------------------------------- append
-
-// cos and sin of a position's angle for one pair, for keys that stay in the
-// cache: the angle in turns is exact in 64-bit integers (rope_cos_sin); here
+// cos and sin of a position's angle for one pair: the angle in turns is exact in 64-bit integers (rope_cos_sin); here
 // only what is left of the nearest quarter turn, at most an eighth, is
 // rounded to fp32, so both are good to about an ulp.
 __device__ __forceinline__ void rope_cos_sin_exact(int64_t rel, uint64_t phase, float *c, float *s) {
@@ -424,6 +401,43 @@ __device__ __forceinline__ void rope_cos_sin_exact(int64_t rel, uint64_t phase, 
   *c = (quarter & 1) ? ((quarter & 2) ? y : -y) : ((quarter & 2) ? -x : x);
   *s = (quarter & 1) ? ((quarter & 2) ? -x : x) : ((quarter & 2) ? -y : y);
 }
+
+// The columns' queries, a CTA a segment, and their rotations, a warp a row.
+__global__ void __launch_bounds__(256) tree_columns_kernel(const __grid_constant__ TreeArgs a) {
+  if (!tree_plan_ok(a)) return;
+  const int n_segs = tree_at<TreeHeader>(a, a.L.hdr)->n_segs;
+  const int G = a.n_q_heads / a.n_kv_heads, half = a.head_dim / 2;
+  const int lane = threadIdx.x & 31;
+  const TreeRef *refs = tree_at<TreeRef>(a, a.L.refs);
+  for (int s = blockIdx.x; s < n_segs; s += gridDim.x) {
+    const TreeSeg sg = tree_at<TreeSeg>(a, a.L.segs)[s];
+    auto ref_of = [&](int col) {
+      int lo = 0, hi = sg.n_ref;  // the reference that holds the column
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (refs[sg.ref0 + mid].col <= col) lo = mid; else hi = mid;
+      }
+      return refs[sg.ref0 + lo];
+    };
+    for (int x = threadIdx.x; x < sg.n_cols; x += 256) {
+      const int col = sg.col0 + x;
+      const TreeRef ref = ref_of(col);
+      const int local = col - ref.col;
+      tree_at<TreeColumn>(a, a.L.columns)[sg.table + x] =
+          TreeColumn{ref.row * a.max_nodes + local / G, local % G, sg.rot0 + col / G, 0};
+    }
+    // rows whose first column is the segment's
+    const int p0 = (sg.col0 + G - 1) / G, p1 = (sg.col0 + sg.n_cols + G - 1) / G;
+    for (int p = p0 + (threadIdx.x >> 5); p < p1; p += 8) {
+      const TreeRef ref = ref_of(p * G);
+      const int64_t rel = ref.rel + tree_at<int32_t>(a, a.L.depth)[ref.row * a.max_nodes + p - ref.col / G];
+      float2 *to = tree_at<float2>(a, a.L.rot) + static_cast<int64_t>(sg.rot0 + p) * half;
+      for (int j = lane; j < half; j += 32) rope_cos_sin_exact(rel, a.phase[j], &to[j].x, &to[j].y);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- append
 
 // The drafted tokens written into the cache, a warp a (row, node, kv head):
 //   K[h][slot + i] = rho(k_new[r][i][h], pos + depth(i)),  V = v_new
@@ -442,15 +456,16 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
   const int64_t node = item / a.n_kv_heads;
   const int r = static_cast<int>(node / a.max_nodes), i = static_cast<int>(node % a.max_nodes);
   if (r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) return;
-  const int64_t rel = static_cast<int64_t>(tree_at<int32_t>(a, a.L.pos)[r]) + tree_at<int32_t>(a, a.L.depth)[node];
+  // the tree's own segment holds the keys' rotations too
+  const TreeSeg &sg = tree_at<TreeSeg>(a, a.L.segs)[tree_at<int32_t>(a, a.L.entry_seg)[a.n_rows * a.n_view + r]];
+  const float2 *rot = tree_at<float2>(a, a.L.rot) + static_cast<int64_t>(sg.rot0 + i) * half;
   const int64_t slot = static_cast<int64_t>(tree_at<int32_t>(a, a.L.slot)[r]) + i;
   const T *kn = reinterpret_cast<const T *>(a.k_new) + item * D;
   const T *vn = reinterpret_cast<const T *>(a.v_new) + item * D;
   const int64_t to = (h * a.capacity + slot) * D;
   const float ks = kFp8 ? a.k_scale[h] : 1.f, vs = kFp8 ? a.v_scale[h] : 1.f;
   for (int j = lane; j < half; j += 32) {
-    float c, s;
-    rope_cos_sin_exact(rel, a.phase[j], &c, &s);
+    const float c = rot[j].x, s = rot[j].y;
     const float x0 = to_f32<T>(kn[j]), x1 = to_f32<T>(kn[j + half]);
     const float y0 = __fmaf_rn(x0, c, -__fmul_rn(x1, s)), y1 = __fmaf_rn(x1, c, __fmul_rn(x0, s));
     if constexpr (kFp8) {
@@ -719,6 +734,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   // sum of ceil(cols / L.cols) over the referenced blocks and the trees
   L.max_segs = d.n_blocks + block_cols / L.cols + R + tree_cols / L.cols + 1;
   L.max_cols = block_cols + tree_cols;
+  L.max_rots = L.max_cols / G;
   L.max_rows = d.n_kv_heads * (block_cols + tree_cols) + static_cast<int64_t>(L.ctas_max) * L.cols;
   size_t at = 256;
   auto put = [&](size_t bytes) {
@@ -731,6 +747,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.wbase = put(2 * sizeof(int64_t) * L.max_segs);  // weights, then units before each segment
   L.refs = put(sizeof(TreeRef) * L.max_refs);
   L.columns = put(sizeof(TreeColumn) * L.max_cols);
+  L.rot = put(4 * static_cast<size_t>(d.head_dim) * L.max_rots);
   L.entry_seg = put(4 * L.max_refs);
   L.entry_col = put(4 * L.max_refs);
   L.piece_row = put(4 * L.max_segs * d.n_kv_heads);

@@ -28,7 +28,7 @@ struct Smem {
   float m[kCols], l[kCols], alpha[kCols];
   int32_t qrow[kCols];    // query row of the column: node * Hq + q head
   int32_t node[kCols];    // row * max_nodes + node
-  int64_t rel[kCols];
+  int32_t rot[kCols];     // its row of the rotation table
 };
 
 template <typename KV>
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
       const TreeColumn tc = columns[sg.table + tid];
       S.node[tid] = tc.node;
       S.qrow[tid] = tc.node * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[h * G + tc.head];
-      S.rel[tid] = tc.rel;
+      S.rot[tid] = tc.rot;
       S.m[tid] = -INFINITY;
       S.l[tid] = 0.f;
     }
@@ -102,10 +102,9 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
       const int qi = x / (D / 2), i = x % (D / 2);
       const T *qp = reinterpret_cast<const T *>(a.q) + static_cast<int64_t>(S.qrow[qi]) * D;
       const float x0 = to_f32<T>(qp[i]), x1 = to_f32<T>(qp[i + D / 2]);
-      float cs, sn;
-      rope_cos_sin(S.rel[qi], a.phase[i], &cs, &sn);
-      S.q[qi][i] = x0 * cs - x1 * sn;
-      S.q[qi][i + D / 2] = x1 * cs + x0 * sn;
+      const float2 r = tree_at<float2>(a, a.L.rot)[static_cast<int64_t>(S.rot[qi]) * (D / 2) + i];
+      S.q[qi][i] = x0 * r.x - x1 * r.y;
+      S.q[qi][i + D / 2] = x1 * r.x + x0 * r.y;
     }
     float acc[QPT];
 #pragma unroll

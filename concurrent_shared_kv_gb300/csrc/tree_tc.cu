@@ -52,9 +52,9 @@ __device__ __forceinline__ bool aborted(TcSmem &S) {
 }
 // Wait with a bound; false once the CTA winds down.
 __device__ __forceinline__ bool wait_or_abort(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try(bar, parity)) {
+  while (!mbar_test(bar, parity)) {
     if (aborted(S)) return false;
     if (clock64() - t0 > kWaitLimit) {
       *reinterpret_cast<volatile int32_t *>(&S.abort_flag) = 1;
@@ -63,6 +63,12 @@ __device__ __forceinline__ bool wait_or_abort(TcSmem &S, const TreeArgs &a, uint
     }
   }
   return true;
+}
+
+// wait_or_abort by a whole warp, with one answer for all its lanes: what
+// follows are warp-wide TMEM accesses.
+__device__ __forceinline__ bool warp_wait(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_or_abort(S, a, bar, parity));
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulator.
@@ -86,6 +92,17 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -154,39 +171,56 @@ __device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, co
   for (int j = n > kStages ? n - kStages : 0; j < n; ++j) mbar_wait(&S.kv_full[j % kStages], (j / kStages) & 1);
 }
 
+// The whole warp walks and waits; one elected lane issues.  (Descriptors then
+// stay in uniform registers: issued from a branch of one lane, 8 MMAs took
+// 1200 clocks instead of the 512 the tensor cores need for them, and 4 x 64
+// nodes on a 16K history 225 us.)
 __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, const TreeSeg *segs) {
   constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0), idesc_pv = idesc_bf16(128, 128, 0, 1);
   const uint32_t q0 = smem_u32(S.q[0]), kv0 = smem_u32(S.kv[0]);
   const uint64_t a_qk = smem_desc(q0, 16, 1024, kSw128), b_qk = smem_desc(kv0, 16, 1024, kSw128);
   const uint64_t b_pv = smem_desc(kv0, kBox, 1024, kSw128);
-  int i = 0;                         // tiles whose QK is issued
+  int i = 0;  // tiles whose QK is issued
   // per query tile: PVs issued, segments whose PVs and whose QKs have begun
   int np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0};
+  // S of query tile qt from the K in stage s
   auto qk = [&](int qt, int s) {
     const uint64_t as = a_qk + ((qt * kQTile) >> 4), bs = b_qk + ((s * kStage) >> 4);
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
-      const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-      mma_bf16(tmem + qt * 128, as + o, bs + o, idesc_qk, k > 0);
+      for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
+        const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+        mma_bf16(tmem + qt * 128, as + o, bs + o, idesc_qk, k > 0);
+      }
+      mma_commit(&S.s_full[qt]);
     }
-    mma_commit(&S.s_full[qt]);
+    __syncwarp();
   };
-  // PV of query tile qt against the V in ring entry n
+  // O of query tile qt (+)= P . V, V in ring entry n
   auto pv = [&](int qt, int n, int ksteps, bool first) -> bool {
-    if (!wait_or_abort(S, a, &S.p_full[qt], np[qt] & 1)) return false;
-    if (!wait_or_abort(S, a, &S.kv_full[n % kStages], (n / kStages) & 1)) return false;
+    if (!warp_wait(S, a, &S.p_full[qt], np[qt] & 1)) return false;
+    if (!warp_wait(S, a, &S.kv_full[n % kStages], (n / kStages) & 1)) return false;
     if (first) {
-      if (!wait_or_abort(S, a, &S.o_empty[qt], (no[qt] & 1) ^ 1)) return false;
+      if (!warp_wait(S, a, &S.o_empty[qt], (no[qt] & 1) ^ 1)) return false;
       ++no[qt];
     }
     tc_fence_after();
     const uint64_t bs = b_pv + (((n % kStages) * kStage) >> 4);
-    for (int k = 0; k < ksteps; ++k)  // steps of 16 tokens
-      mma_bf16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + k * 8, bs + ((k * 2048) >> 4), idesc_pv,
-                  !(first && k == 0));
-    mma_commit(&S.pv_done[qt]);
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)  // steps of 16 tokens
+        if (k < ksteps)
+          mma_bf16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + k * 8, bs + ((k * 2048) >> 4), idesc_pv,
+                      !(first && k == 0));
+      mma_commit(&S.pv_done[qt]);
+    }
+    __syncwarp();
     ++np[qt];
     return true;
+  };
+  auto release = [&](int s) {
+    if (elect_one()) mma_commit(&S.kv_empty[s]);
+    __syncwarp();
   };
   bool pend = false, pend_two = false, pend_first = false;  // the tile whose PVs are to come
   int pend_steps = 0;
@@ -198,21 +232,21 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
       const int nk = 2 * i, nv = 2 * i - 1;
       if (pend && !(go = pv(0, nv, pend_steps, pend_first))) break;
       if (!first) {
-        if (!(go = wait_or_abort(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
+        if (!(go = warp_wait(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
         tc_fence_after();
         qk(0, nk % kStages);
       }
       if (pend && pend_two && !(go = pv(1, nv, pend_steps, pend_first))) break;
-      if (pend) mma_commit(&S.kv_empty[nv % kStages]);
+      if (pend) release(nv % kStages);
       if (first) {
-        if (!(go = wait_or_abort(S, a, &S.q_full[0], nq[0]++ & 1))) break;
-        if (two && !(go = wait_or_abort(S, a, &S.q_full[1], nq[1]++ & 1))) break;
-        if (!(go = wait_or_abort(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
+        if (!(go = warp_wait(S, a, &S.q_full[0], nq[0]++ & 1))) break;
+        if (two && !(go = warp_wait(S, a, &S.q_full[1], nq[1]++ & 1))) break;
+        if (!(go = warp_wait(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
         tc_fence_after();
         qk(0, nk % kStages);
       }
       if (two) qk(1, nk % kStages);
-      mma_commit(&S.kv_empty[nk % kStages]);
+      release(nk % kStages);
       pend = true;
       pend_two = two;
       pend_first = first;
@@ -222,7 +256,8 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
   if (go && pend) {
     if (pv(0, 2 * i - 1, pend_steps, pend_first) && pend_two) pv(1, 2 * i - 1, pend_steps, pend_first);
   }
-  mma_commit(&S.mma_done);
+  if (elect_one()) mma_commit(&S.mma_done);
+  __syncwarp();
   mbar_wait(&S.mma_done, 0);
 }
 
@@ -249,12 +284,6 @@ __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem,
   }
 }
 
-// wait_or_abort by a whole warp, with one answer for all its lanes: what
-// follows are warp-wide TMEM accesses.
-__device__ __forceinline__ bool warp_wait(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_or_abort(S, a, bar, parity));
-}
-
 __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, const TreeSeg *segs, int qt) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
   const int col = qt * 128 + row;  // the thread's column of a segment
@@ -277,12 +306,16 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, con
     const bool warp_on = qt * 128 + quarter * 32 < w.sg.n_cols;
     TreeColumn tc = {};
     const uint4 *src = nullptr;
+    const float4 *rot = nullptr;
     if (mine) {
       tc = columns[w.sg.table + col];
       const int64_t at = (static_cast<int64_t>(tc.node) * a.n_q_heads + heads[w.head * G + tc.head]) * 128;
       src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at);
       asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
       asm volatile("prefetch.global.L1 [%0];" ::"l"(src + 8));
+      rot = tree_at<float4>(a, a.L.rot) + static_cast<int64_t>(tc.rot) * 32;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) asm volatile("prefetch.global.L1 [%0];" ::"l"(rot + 8 * c));
     }
     // the segment before is done with Q~ and with O
     if (have && !warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
@@ -294,18 +327,11 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, con
         uint32_t p[4], r[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float lo[2], hi[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x0 = __uint_as_float(e ? (x[j] & 0xffff0000u) : (x[j] << 16));
-            const float x1 = __uint_as_float(e ? (y[j] & 0xffff0000u) : (y[j] << 16));
-            float cs, sn;
-            rope_cos_sin_fast(tc.rel, a.phase[8 * c + 2 * j + e], &cs, &sn);
-            lo[e] = (x0 * cs - x1 * sn) * a.scale_log2;
-            hi[e] = (x1 * cs + x0 * sn) * a.scale_log2;
-          }
-          p[j] = pack_bf16(lo[0], lo[1]);
-          r[j] = pack_bf16(hi[0], hi[1]);
+          const float4 cs = __ldg(rot + 4 * c + j);  // (cos, sin) of two elements
+          const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
+          const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
+          p[j] = pack_bf16((x0 * cs.x - y0 * cs.y) * a.scale_log2, (x1 * cs.z - y1 * cs.w) * a.scale_log2);
+          r[j] = pack_bf16((y0 * cs.x + x0 * cs.y) * a.scale_log2, (y1 * cs.z + x1 * cs.w) * a.scale_log2);
         }
         const uint32_t o = (c ^ (row & 7)) << 4;
         st_shared_v4(qrow + o, p[0], p[1], p[2], p[3]);
@@ -434,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tv) {
   extern __shared__ uint8_t smem_raw[];
   TcSmem &S = *reinterpret_cast<TcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!tree_plan_ok(a)) {
     if (tid == 0) flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_BAD_PLAN);
@@ -473,11 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = S.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
   if (warp == kWarpTma) {
     if ((tid & 31) == 0) producer(a, S, &tk, &tv, w, segs);
   } else if (warp == kWarpMma) {
-    if ((tid & 31) == 0) mma_issuer(a, S, tmem, w, segs);
+    mma_issuer(a, S, tmem, w, segs);
   } else if (warp < 8) {
     softmax(a, S, tmem, w, segs, warp >> 2);
   }
