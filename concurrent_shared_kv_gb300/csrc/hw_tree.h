@@ -1,31 +1,33 @@
 // hw_tree.h - the draft-tree operators' plan: its layout in a workspace, and
 // the arguments their kernels share.  Not part of the public interface.
 //
-// A step's plan is built once by tree_plan_kernel (tree_plan.cu) and read by
+// A step's plan is built once by launch_tree_plan (tree_plan.cu) and read by
 // every layer's launches:
-//   segment  = the tokens of one block (or of one row's tree) against up to
-//              `cols` query columns.  The columns of a block are its view
-//              references in view-entry order, each with (node, q head of the
-//              kv head's group) of its row; a block with more is cut into
-//              segments of `cols` columns that each read its tokens.  A row's
-//              tree has the row's own columns only.
-//   unit     = one tile of `tile` tokens of a segment for one kv head; units
-//              are ordered by kv head, then segment, then tile, on a weighted
-//              line: a unit weighs its segment's tile_w, the first unit of a
-//              segment seg_w more (a switch costs a record epilogue and new
-//              rotated queries).  CTA c of C takes the units that start in
-//              [c W / C, (c + 1) W / C); C is small enough that every CTA
-//              inside a segment owns a unit of it.
-//   record   = what a CTA leaves for (segment, kv head): per column the
-//              running maximum m and sum l of the softmax (log2 domain) and
-//              the unnormalised output.  The records of one (kv head,
-//              segment) lie behind one another, CTA after CTA.  Within a
-//              record 8 output elements (32 bytes, a sector) of every column
-//              lie side by side, then the next 8: a thread that owns a column
-//              and a warp that owns a row both move whole sectors.
-// The rotation of a (reference, node) is the same for every layer and q head:
-// the plan holds its cos and sin, fp32, one row of head_dim / 2 pairs each.
-// tree_merge_kernel then joins the records of every (row, node, q head).
+//   column   = one query of a kv head: a row's node and one of the kv head's q
+//              heads.  Columns are numbered row by row, node by node.
+//   group    = up to `cols` neighbouring columns, attended together: every K/V
+//              tile that one of them sees is read once for all of them.
+//              Neighbouring rows join one group as long as they share a block.
+//   span     = the tokens of a block that rows of the group see, or of one
+//              row's tree.  A group's blocks come by number (a block that a
+//              row names twice, twice), then its rows' trees.  From span to
+//              span only the queries' rotation changes; the softmax goes on.
+//   unit     = one tile of `tile` tokens of a span for one kv head; units are
+//              ordered by kv head, group, span and tile, on a weighted line:
+//              a tile weighs tile1 or tile2 (over 128 columns), the first tile
+//              of a span `span` more, that of a group `group` more still.  CTA
+//              c of C takes the units that start in [c W / C, (c + 1) W / C);
+//              C is small enough that every CTA inside a group owns a unit.
+//   record   = what a CTA leaves for (kv head, group): per column the running
+//              maximum m and sum l of the softmax (log2 domain) and the
+//              unnormalised output.  The records of one (kv head, group) lie
+//              behind one another, CTA after CTA.  Within a record 8 output
+//              elements (32 bytes, a sector) of every column lie side by
+//              side, then the next 8: a thread that owns a column and a warp
+//              that owns a row both move whole sectors.
+// The rotation of a (row, view entry, node) is the same for every layer and q
+// head: the plan holds its cos and sin, fp32, head_dim / 2 pairs each.
+// tree_merge_kernel joins the records of every (row, node, q head).
 #pragma once
 
 #include <cuda.h>
@@ -42,40 +44,41 @@ constexpr int kMaxNodes = HW_MAX_TREE_NODES;
 struct TreeHeader {
   uint32_t magic;
   int32_t n_rows, max_nodes, n_q_heads, n_kv_heads, head_dim, n_blocks, n_view, dtype;
-  int32_t n_segs;  // segments per kv head
-  int32_t n_ctas;  // CTAs with units (0: nothing to attend)
+  int32_t n_groups;  // per kv head
+  int32_t n_ctas;    // CTAs with units (0: nothing to attend)
   int32_t pad;
   int64_t capacity;
 };
 
-struct TreeSeg {
-  int32_t start, len;      // pool tokens
-  int32_t row;             // the row whose tree this is, or -1: a block
-  int32_t ref0, n_ref;     // its block's references
-  int32_t col0, n_cols;    // columns of the block it covers
-  int32_t table;           // its first entry in the column table
-  int32_t rot0;            // its block's first row in the rotation table
-  int32_t pad[3];
+struct TreeGroup {
+  int32_t row0, row1;      // first and last row with columns in the group
+  int32_t rank0, n_rows;   // rows with nodes before row0; such rows in the group
+  int32_t col0, n_cols;    // its columns (numbered over all rows)
+  int32_t span0, n_spans;
 };
-struct TreeRef {
-  int32_t row, col;  // query row; its first column among the block's columns
-  int64_t rel;       // rotation of the row's root: q_pos - view_offset (a tree: the root's position)
+struct TreeSpan {
+  int32_t start, len;  // pool tokens
+  int32_t row;         // the row whose tree this is, or -1: a block
+  int32_t map;         // block: in the map, per row of the group its view entry, or -1
+  int32_t tile0;       // tiles of the group before it
+  int32_t partial;     // not every column sees every token of it
+  int64_t w0;          // weight of the group before it
 };
 struct TreeColumn {
-  int32_t node, head;  // row * max_nodes + node; q head within its kv head's
-  int32_t rot;         // the query's rotation: row of the table of (cos, sin) pairs
-  int32_t pad;
+  int32_t node, head;   // row * max_nodes + node; q head within its kv head's
+  int32_t rot;          // table row of the rotation for view entry 0; entry v's lies v * n_nodes further
+  uint16_t n_nodes, row;  // of its row; the row's number among the group's rows
 };
 struct TreeCta {
-  int32_t head, seg, tile, n_units;  // first unit and count
+  int32_t head, group, span, tile, n_units;  // first unit and count
 };
 
 // Byte offsets of the plan's arrays in the workspace (the error word is at 0).
 struct TreeLayout {
-  size_t hdr, segs, wbase, refs, columns, rot, entry_seg, entry_col, piece_row, piece_cta, ctas;
-  size_t n_nodes, slot, pos, end, depth, mask, heads, block_start, block_len;
+  size_t hdr, groups, wbase, spans, map, columns, rot, piece_row, piece_cta, ctas;
+  size_t n_nodes, slot, pos, end, col, run, rot0, rank, depth, mask, heads, block_start, block_len;
   size_t ml, o, total;
-  int64_t max_segs, max_refs, max_cols, max_rots, max_rows;
+  int64_t max_groups, max_spans, max_map, max_cols, max_rots, max_rows;
   int32_t cols, tile, ctas_max;
 };
 

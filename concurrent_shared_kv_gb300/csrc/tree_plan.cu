@@ -17,24 +17,29 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Weights of the unit line.  Tensor cores: a tile against up to 128 columns
 // is bound by its K/V bytes, one against 129..256 by both products and the
-// softmax of two query tiles; a segment costs its queries and its records.
+// softmax of two query tiles; a span costs new rotated queries, a group its
+// records and an empty pipeline.
 struct TreeCost {
-  int32_t tile1, tile2, seg;
+  int32_t tile1, tile2, span, group;
 };
 __host__ __device__ inline TreeCost tree_cost(int cols) {
-  return cols > 128 ? TreeCost{2, 3, 3} : TreeCost{2, 2, 1};
+  return cols > 128 ? TreeCost{2, 3, 1, 4} : TreeCost{4, 4, 1, 1};
 }
 
 struct TreePlanSmem {
   int32_t len[HW_MAX_BLOCKS], start[HW_MAX_BLOCKS];
-  int32_t refs[HW_MAX_BLOCKS + 1], cols[HW_MAX_BLOCKS], seg0[HW_MAX_BLOCKS + 1];
   int64_t scan[kPlanWarps + 1];
   int64_t carry;
   int64_t uidx[1025];
-  int32_t ok;
-  uint8_t parent[kPlanWarps][kMaxNodes];
-  int16_t vb[HW_MAX_VIEW_ENTRIES];    // block of every view entry, -1: none
+  int32_t ok, n_groups, n_spans, n_map, n_live;
+  union {
+    uint8_t parent[kPlanWarps][kMaxNodes];
+    uint8_t count[kPlanWarps][HW_MAX_BLOCKS];  // of a group: the most often a row names the block
+  };
+  int16_t first[kPlanWarps][HW_MAX_BLOCKS];    // of a group: the block's first span
+  int16_t vb[HW_MAX_VIEW_ENTRIES];    // block of every view entry with tokens, -1: none
   uint8_t nodes[HW_MAX_VIEW_ENTRIES];  // nodes of every row (rows <= HW_MAX_VIEW_ENTRIES)
+  uint8_t apart[HW_MAX_VIEW_ENTRIES];  // the row shares no block with the one before it
 };
 
 // Exclusive prefix sum over the CTA; returns this thread's prefix and adds
@@ -137,37 +142,178 @@ __device__ int plan_row(const TreeArgs &a, const TreeMeta &m, TreePlanSmem &S, i
   return n;
 }
 
-// Weight before tile t of a segment (t > 0 includes the segment's own).
-__device__ __forceinline__ int64_t tile_weight(const TreeCost &c, int n_cols, int t) {
-  return t == 0 ? 0 : c.seg + static_cast<int64_t>(t) * (n_cols > 128 ? c.tile2 : c.tile1);
+// Weight of a span before its tile t (t > 0 includes the span's own).
+__device__ __forceinline__ int64_t tile_weight(const TreeCost &c, int n_cols, bool first, int t) {
+  return t == 0 ? 0 : c.span + (first ? c.group : 0) + static_cast<int64_t>(t) * (n_cols > 128 ? c.tile2 : c.tile1);
 }
 // The CTA that owns a unit starting at weight w.
 __device__ __forceinline__ int cta_of_weight(int64_t w, int64_t W, int C) {
   return static_cast<int>(((w + 1) * C - 1) / W);
 }
 
-// The whole plan, by one CTA.
+// How often the row names entry v's block before v, and whether v is the last.
+__device__ __forceinline__ int entry_rank(const TreePlanSmem &S, int e0, int v, int V, bool *last) {
+  const int b = S.vb[e0 + v];
+  int k = 0;
+  *last = true;
+  for (int x = 0; x < V; ++x)
+    if (x != v && S.vb[e0 + x] == b) {
+      if (x < v) ++k; else *last = false;
+    }
+  return k;
+}
+
+// Rows into groups: their columns one behind another, cut where a row shares
+// no block with the one before it and every a.L.cols columns.  One thread.
+__device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
+  const int R = a.n_rows, V = a.n_view, G = a.n_q_heads / a.n_kv_heads, CG = a.L.cols;
+  TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
+  int col = 0, rank = 0, rot = 0, n = 0;
+  int2 run = make_int2(0, 0);  // the run's first group and column
+  TreeGroup g = {};
+  g.n_cols = CG;
+  for (int r = 0; r < R; ++r) {
+    const int nodes = S.nodes[r];
+    tree_at<int32_t>(a, a.L.col)[r] = col;
+    tree_at<int32_t>(a, a.L.rank)[r] = rank;
+    tree_at<int32_t>(a, a.L.rot0)[r] = rot;
+    if (nodes == 0) continue;
+    if (S.apart[r]) {
+      if (n > 0) groups[n - 1] = g;
+      g.n_cols = CG;
+      run = make_int2(n, col);
+    }
+    tree_at<int2>(a, a.L.run)[r] = run;
+    for (int left = nodes * G; left > 0;) {
+      if (g.n_cols == CG) {
+        if (n > 0 && !(S.apart[r] && left == nodes * G)) groups[n - 1] = g;
+        g = TreeGroup{r, r, rank, 0, col, 0, 0, 0};
+        ++n;
+      }
+      const int take = min(left, CG - g.n_cols);
+      g.n_cols += take;
+      g.row1 = r;
+      g.n_rows = rank + 1 - g.rank0;
+      col += take;
+      left -= take;
+    }
+    ++rank;
+    rot += nodes * (V + 1);
+  }
+  if (n > 0) groups[n - 1] = g;
+  S.n_groups = n;
+}
+
+// A group's spans, by one warp; its weight and tiles go to wbase and ubase.
+__device__ void plan_spans(const TreeArgs &a, TreePlanSmem &S, const TreeCost &cost, int gi, int64_t *wbase,
+                           int64_t *ubase, int lane) {
+  const int V = a.n_view, TL = a.L.tile, warp = threadIdx.x >> 5;
+  TreeGroup &g = tree_at<TreeGroup>(a, a.L.groups)[gi];
+  uint8_t *count = S.count[warp];
+  int16_t *first = S.first[warp];
+  for (int b = lane; b < a.n_blocks; b += 32) count[b] = 0;
+  __syncwarp();
+  for (int r = g.row0; r <= g.row1; ++r) {
+    if (S.nodes[r] == 0) continue;
+    for (int v = lane; v < V; v += 32) {
+      const int b = S.vb[r * V + v];
+      bool last;
+      const int k = b < 0 ? 0 : entry_rank(S, r * V, v, V, &last);
+      if (b >= 0 && last && k + 1 > count[b]) count[b] = static_cast<uint8_t>(k + 1);
+    }
+    __syncwarp();
+  }
+  int nb = 0;
+  for (int b0 = 0; b0 < a.n_blocks; b0 += 32) {
+    const int b = b0 + lane, c = b < a.n_blocks ? count[b] : 0;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (b < a.n_blocks) first[b] = static_cast<int16_t>(nb + incl - c);
+    nb += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  const int n = nb + g.n_rows;
+  int span0 = 0, map0 = 0;
+  if (lane == 0) {
+    span0 = atomicAdd(&S.n_spans, n);
+    map0 = atomicAdd(&S.n_map, nb * g.n_rows);
+    g.span0 = span0;
+    g.n_spans = n;
+  }
+  span0 = __shfl_sync(0xffffffffu, span0, 0);
+  map0 = __shfl_sync(0xffffffffu, map0, 0);
+  TreeSpan *spans = tree_at<TreeSpan>(a, a.L.spans) + span0;
+  int16_t *map = tree_at<int16_t>(a, a.L.map) + map0;
+  for (int x = lane; x < nb * g.n_rows; x += 32) map[x] = -1;
+  for (int b = lane; b < a.n_blocks; b += 32)
+    for (int k = 0; k < count[b]; ++k)
+      spans[first[b] + k] = TreeSpan{S.start[b], S.len[b], -1, map0 + (first[b] + k) * g.n_rows, 0, 0, 0};
+  __syncwarp();
+  int j = 0;
+  for (int r = g.row0; r <= g.row1; ++r) {
+    if (S.nodes[r] == 0) continue;
+    for (int v = lane; v < V; v += 32) {
+      const int b = S.vb[r * V + v];
+      bool last;
+      if (b >= 0) map[(first[b] + entry_rank(S, r * V, v, V, &last)) * g.n_rows + j] = static_cast<int16_t>(v);
+    }
+    if (lane == 0) spans[nb + j] = TreeSpan{tree_at<int32_t>(a, a.L.slot)[r], S.nodes[r], r, 0, 0, 1, 0};
+    ++j;
+  }
+  __syncwarp();
+  int64_t w = 0;
+  int tiles = 0;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const int s = s0 + lane;
+    const int t = s < n ? (spans[s].len + TL - 1) / TL : 0;
+    const int64_t ws = s < n ? tile_weight(cost, g.n_cols, s == 0, t) : 0;
+    int ti = t;
+    int64_t wi = ws;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, ti, o);
+      const int64_t z = __shfl_up_sync(0xffffffffu, wi, o);
+      if (lane >= o) {
+        ti += y;
+        wi += z;
+      }
+    }
+    if (s < n) {
+      spans[s].tile0 = tiles + ti - t;
+      spans[s].w0 = w + wi - ws;
+      if (s < nb)
+        for (int x = 0; x < g.n_rows; ++x) spans[s].partial |= map[s * g.n_rows + x] < 0;
+    }
+    tiles += __shfl_sync(0xffffffffu, ti, 31);
+    w += __shfl_sync(0xffffffffu, wi, 31);
+  }
+  if (lane == 0) {
+    wbase[gi] = w;
+    ubase[gi] = tiles;
+  }
+}
+
+// The plan but for its tables, by one CTA.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_constant__ TreeArgs a,
                                                                  const __grid_constant__ TreeMeta m) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   TreePlanSmem &S = *reinterpret_cast<TreePlanSmem *>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = a.n_rows, V = a.n_view, E = R * V, T = a.max_nodes;
-  const int G = a.n_q_heads / a.n_kv_heads, CG = a.L.cols;
-  const TreeCost cost = tree_cost(CG);
+  const int G = a.n_q_heads / a.n_kv_heads, TL = a.L.tile;
+  const TreeCost cost = tree_cost(a.L.cols);
   int32_t *err = reinterpret_cast<int32_t *>(a.ws);
   TreeHeader &hdr = *tree_at<TreeHeader>(a, a.L.hdr);
-  int32_t *n_nodes = tree_at<int32_t>(a, a.L.n_nodes);
-  int32_t *entry_seg = tree_at<int32_t>(a, a.L.entry_seg), *entry_col = tree_at<int32_t>(a, a.L.entry_col);
-  TreeRef *refs = tree_at<TreeRef>(a, a.L.refs);
-  TreeSeg *segs = tree_at<TreeSeg>(a, a.L.segs);
-  int64_t *wbase = tree_at<int64_t>(a, a.L.wbase);
   if (tid == 0) {
     S.ok = 1;
     S.carry = 0;
+    S.n_spans = S.n_map = 0;
     hdr.magic = 0;
   }
-  // blocks: the usable length of each (0: skipped)
+  // blocks: the usable length of each (-1: skipped)
   for (int b = tid; b < a.n_blocks; b += kPlanThreads) {
     const int st = m.block_start[b], ln = m.block_len[b];
     const bool bad = st < 0 || ln < 0 || static_cast<int64_t>(st) + ln > a.capacity;
@@ -176,16 +322,6 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     S.len[b] = bad ? -1 : ln;
     tree_at<int32_t>(a, a.L.block_start)[b] = S.start[b];
     tree_at<int32_t>(a, a.L.block_len)[b] = S.len[b];
-    S.refs[b] = 0;
-    S.cols[b] = 0;
-  }
-  __syncthreads();
-  for (int r = warp; r < R; r += kPlanWarps) {
-    const int n = plan_row(a, m, S, err, r, lane);
-    if (lane == 0) {
-      n_nodes[r] = n;
-      S.nodes[r] = static_cast<uint8_t>(n);
-    }
   }
   // the q heads of every kv head
   for (int h = warp; h < a.n_kv_heads; h += kPlanWarps) {
@@ -203,180 +339,121 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       S.ok = 0;
     }
   }
+  __syncthreads();
+  for (int r = warp; r < R; r += kPlanWarps) {
+    int n = plan_row(a, m, S, err, r, lane);
+    if (!S.ok) n = 0;  // no usable head map: the plan attends and writes nothing
+    if (lane == 0) {
+      tree_at<int32_t>(a, a.L.n_nodes)[r] = n;
+      S.nodes[r] = static_cast<uint8_t>(n);
+    }
+  }
   for (int e = tid; e < E; e += kPlanThreads) {
     const int b = m.view_block[e];
     const bool bad = b < -1 || b >= a.n_blocks;
     if (bad) flag_error(err, HW_DEV_BAD_BLOCK);
-    S.vb[e] = static_cast<int16_t>(bad ? -1 : b);
-    entry_seg[e] = -1;
-    entry_col[e] = 0;
+    S.vb[e] = static_cast<int16_t>(bad || b < 0 || S.len[b] <= 0 ? -1 : b);
   }
   __syncthreads();
-  if (!S.ok) {  // no usable head map: the plan attends and writes nothing
-    for (int r = tid; r < R; r += kPlanThreads) {
-      n_nodes[r] = 0;
-      S.nodes[r] = 0;
-    }
-    __syncthreads();
+  for (int r = warp; r < R; r += kPlanWarps) {
+    int before = r - 1;  // the row before it that takes part
+    while (before >= 0 && S.nodes[before] == 0) --before;
+    bool share = false;
+    for (int v = lane; before >= 0 && v < V; v += 32)
+      for (int x = 0; x < V; ++x) share |= S.vb[r * V + v] >= 0 && S.vb[r * V + v] == S.vb[before * V + x];
+    share = __any_sync(0xffffffffu, share);
+    if (lane == 0) S.apart[r] = !share;
   }
-  // references of every block: first counted, then written in entry order
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int b = warp; b < a.n_blocks; b += kPlanWarps) {
-      int nref = 0, ncol = 0;
-      if (S.len[b] > 0) {
-        for (int e0 = 0; e0 < E; e0 += 32) {
-          const int e = e0 + lane;
-          const int r = e < E ? e / V : 0;
-          const int n = e < E && S.vb[e] == b ? S.nodes[r] : 0;
-          const unsigned hit = __ballot_sync(0xffffffffu, n > 0);
-          if (!hit) continue;
-          int incl = n * G;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          if (pass && n > 0) {
-            TreeRef ref;
-            ref.row = r;
-            ref.col = ncol + incl - n * G;
-            ref.rel = static_cast<int64_t>(m.q_pos[r]) - m.view_offset[e];
-            refs[S.refs[b] + nref + __popc(hit & lanemask_lt(lane))] = ref;
-            entry_seg[e] = S.seg0[b];
-            entry_col[e] = ref.col;
-          }
-          nref += __popc(hit);
-          ncol += __shfl_sync(0xffffffffu, incl, 31);
-        }
-      }
-      if (!pass && lane == 0) {
-        S.refs[b] = nref;
-        S.cols[b] = ncol;
-      }
-      if (pass) {
-        const int first = S.refs[b], seg0 = S.seg0[b];
-        for (int g = lane; g * CG < ncol; g += 32)
-          segs[seg0 + g] = TreeSeg{S.start[b], S.len[b], -1, first, nref, g * CG, min(CG, ncol - g * CG), 0, 0, {}};
-      }
-    }
-    __syncthreads();
-    if (!pass && tid == 0) {
-      int ref0 = 0, seg0 = 0;
-      for (int b = 0; b < a.n_blocks; ++b) {
-        const int nr = S.refs[b];
-        S.refs[b] = ref0;
-        S.seg0[b] = seg0;
-        ref0 += nr;
-        seg0 += (S.cols[b] + CG - 1) / CG;
-      }
-      S.seg0[a.n_blocks] = seg0;
-      S.carry = seg0;
-    }
-    __syncthreads();
-  }
-  // the rows' trees
-  for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
-    const int r = r0 + tid;
-    const int n = r < R ? n_nodes[r] : 0;
-    const int ns = (n * G + CG - 1) / CG;
-    const int s0 = static_cast<int>(block_scan(S, ns));
-    if (r < R) {
-      entry_seg[E + r] = n > 0 ? s0 : -1;
-      entry_col[E + r] = 0;
-      refs[E + r] = TreeRef{r, 0, n > 0 ? tree_at<int32_t>(a, a.L.pos)[r] : 0};
-      const int at = n > 0 ? tree_at<int32_t>(a, a.L.slot)[r] : 0;
-      for (int g = 0; g < ns; ++g)
-        segs[s0 + g] = TreeSeg{at, n, r, E + r, 1, g * CG, min(CG, n * G - g * CG), 0, 0, {}};
-    }
-  }
-  const int n_segs = static_cast<int>(S.carry);
   __syncthreads();
-  if (tid == 0) S.carry = 0;
+  if (tid == 0) plan_groups(a, S);
   __syncthreads();
-  // the weighted line, and (in the high half) the units before each segment
-  const int TL = a.L.tile;
-  for (int s0 = 0; s0 < n_segs; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    int64_t w = 0;
-    if (s < n_segs) w = tile_weight(cost, segs[s].n_cols, (segs[s].len + TL - 1) / TL);
-    const int64_t at = block_scan(S, w);
-    if (s < n_segs) wbase[s] = at;
+  const int n_groups = S.n_groups;
+  int64_t *wbase = tree_at<int64_t>(a, a.L.wbase), *ubase = wbase + a.L.max_groups;
+  for (int g = warp; g < n_groups; g += kPlanWarps) plan_spans(a, S, cost, g, wbase, ubase, lane);
+  __syncthreads();
+  const TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
+  const TreeSpan *spans = tree_at<TreeSpan>(a, a.L.spans);
+  // weights and units before each group
+  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    const int64_t at = block_scan(S, g < n_groups ? wbase[g] : 0);
+    if (g < n_groups) wbase[g] = at;
   }
   const int64_t WH = S.carry, W = WH * a.n_kv_heads;
-  const int64_t most = W / (cost.seg + cost.tile2);
-  const int C = static_cast<int>(most < a.L.ctas_max ? most : a.L.ctas_max);
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
-  // the segments' places in the column table
-  for (int s0 = 0; s0 < n_segs; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    const int64_t at = block_scan(S, s < n_segs ? segs[s].n_cols : 0);
-    if (s < n_segs) {
-      segs[s].table = static_cast<int32_t>(at);
-      // (a block's columns are whole groups of G: its first one starts a row)
-      segs[s].rot0 = static_cast<int32_t>((at - segs[s].col0) / G);
-    }
-  }
-  __syncthreads();
-  if (tid == 0) S.carry = 0;
-  __syncthreads();
-  int64_t *ubase = wbase + a.L.max_segs;
-  for (int s0 = 0; s0 < n_segs; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    const int64_t at = block_scan(S, s < n_segs ? (segs[s].len + TL - 1) / TL : 0);
-    if (s < n_segs) ubase[s] = at;
+  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    const int64_t at = block_scan(S, g < n_groups ? ubase[g] : 0);
+    if (g < n_groups) ubase[g] = at;
   }
   const int64_t UH = S.carry;
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
+  // as many CTAs as leave each at least one unit of every group it is inside
+  const int64_t most = W / (cost.group + cost.span + cost.tile2);
+  const int C = static_cast<int>(most < a.L.ctas_max ? most : a.L.ctas_max);
   // every CTA's first unit
   TreeCta *ctas = tree_at<TreeCta>(a, a.L.ctas);
   for (int c = tid; c <= C && C > 0; c += kPlanThreads) {
     const int64_t lo = c * W / C;
-    int h = static_cast<int>(lo / WH), s = 0, t = 0;
+    int h = static_cast<int>(lo / WH);
     if (h >= a.n_kv_heads) {
       S.uidx[c] = UH * a.n_kv_heads;
       continue;
     }
     const int64_t rem = lo - h * WH;
-    int hi = n_segs;
-    while (hi - s > 1) {  // the last segment that starts at or before rem
-      const int mid = (s + hi) >> 1;
-      if (wbase[mid] <= rem) s = mid; else hi = mid;
+    int g = 0, hi = n_groups;
+    while (hi - g > 1) {  // the last group that starts at or before rem
+      const int mid = (g + hi) >> 1;
+      if (wbase[mid] <= rem) g = mid; else hi = mid;
     }
-    const int64_t in = rem - wbase[s];
-    const int tw = segs[s].n_cols > 128 ? cost.tile2 : cost.tile1;
-    const int tiles = (segs[s].len + TL - 1) / TL;
-    if (in > 0) t = in <= cost.seg + tw ? 1 : static_cast<int>((in - cost.seg + tw - 1) / tw);
-    if (t >= tiles) {
+    const TreeGroup gr = groups[g];
+    const TreeSpan *sp = spans + gr.span0;
+    const int64_t in = rem - wbase[g];
+    int s = 0;
+    hi = gr.n_spans;
+    while (hi - s > 1) {
+      const int mid = (s + hi) >> 1;
+      if (sp[mid].w0 <= in) s = mid; else hi = mid;
+    }
+    const int64_t x = in - sp[s].w0;
+    const int own = cost.span + (s == 0 ? cost.group : 0), tw = gr.n_cols > 128 ? cost.tile2 : cost.tile1;
+    int t = x == 0 ? 0 : x <= own + tw ? 1 : static_cast<int>((x - own + tw - 1) / tw);
+    if (t >= (sp[s].len + TL - 1) / TL) {
       t = 0;
-      if (++s == n_segs) {
+      if (++s == gr.n_spans) {
         s = 0;
-        ++h;
+        if (++g == n_groups) {
+          g = 0;
+          ++h;
+        }
       }
     }
-    S.uidx[c] = h < a.n_kv_heads ? h * UH + ubase[s] + t : UH * a.n_kv_heads;
-    if (c < C) ctas[c] = TreeCta{h, s, t, 0};
+    S.uidx[c] = h < a.n_kv_heads ? h * UH + ubase[g] + spans[groups[g].span0 + s].tile0 + t : UH * a.n_kv_heads;
+    if (c < C) ctas[c] = TreeCta{h, g, s, t, 0};
   }
   __syncthreads();
   for (int c = tid; c < C; c += kPlanThreads) ctas[c].n_units = static_cast<int>(S.uidx[c + 1] - S.uidx[c]);
-  // the records of every (kv head, segment)
+  // the records of every (kv head, group)
   int32_t *piece_row = tree_at<int32_t>(a, a.L.piece_row);
   int2 *piece_cta = tree_at<int2>(a, a.L.piece_cta);
-  const int64_t K = C > 0 ? static_cast<int64_t>(n_segs) * a.n_kv_heads : 0;
+  const int64_t K = C > 0 ? static_cast<int64_t>(n_groups) * a.n_kv_heads : 0;
   for (int64_t k0 = 0; k0 < K; k0 += kPlanThreads) {
     const int64_t k = k0 + tid;
     int64_t rows = 0;
     int2 pc = make_int2(0, 0);
     if (k < K) {
-      const int h = static_cast<int>(k / n_segs), s = static_cast<int>(k % n_segs);
-      const int tiles = (segs[s].len + TL - 1) / TL;
-      const int64_t w = h * WH + wbase[s];
+      const int g = static_cast<int>(k % n_groups);
+      const TreeGroup gr = groups[g];
+      const TreeSpan last = spans[gr.span0 + gr.n_spans - 1];
+      const int64_t w = k / n_groups * WH + wbase[g];
+      const int tiles = (last.len + TL - 1) / TL;
       pc.x = cta_of_weight(w, W, C);
-      pc.y = cta_of_weight(w + tile_weight(cost, segs[s].n_cols, tiles - 1), W, C) - pc.x + 1;
-      rows = static_cast<int64_t>(pc.y) * segs[s].n_cols;
+      pc.y = cta_of_weight(w + last.w0 + tile_weight(cost, gr.n_cols, gr.n_spans == 1, tiles - 1), W, C) - pc.x + 1;
+      rows = static_cast<int64_t>(pc.y) * gr.n_cols;
     }
     const int64_t at = block_scan(S, rows);
     if (k < K) {
@@ -386,7 +463,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   }
   if (tid == 0)
     hdr = TreeHeader{kTreeMagic, R, T, a.n_q_heads, a.n_kv_heads, a.head_dim, a.n_blocks, V, a.dtype,
-                     n_segs, C, 0, a.capacity};
+                     n_groups, C, 0, a.capacity};
 }
 
 // cos and sin of a position's angle for one pair: the angle in turns is exact in 64-bit integers (rope_cos_sin); here
@@ -402,36 +479,38 @@ __device__ __forceinline__ void rope_cos_sin_exact(int64_t rel, uint64_t phase, 
   *s = (quarter & 1) ? ((quarter & 2) ? -x : x) : ((quarter & 2) ? -y : y);
 }
 
-// The columns' queries, a CTA a segment, and their rotations, a warp a row.
-__global__ void __launch_bounds__(256) tree_columns_kernel(const __grid_constant__ TreeArgs a) {
+// The tables: the columns of every group, and every row's rotations.
+__global__ void __launch_bounds__(256) tree_tables_kernel(const __grid_constant__ TreeArgs a,
+                                                          const __grid_constant__ TreeMeta m) {
   if (!tree_plan_ok(a)) return;
-  const int n_segs = tree_at<TreeHeader>(a, a.L.hdr)->n_segs;
-  const int G = a.n_q_heads / a.n_kv_heads, half = a.head_dim / 2;
-  const int lane = threadIdx.x & 31;
-  const TreeRef *refs = tree_at<TreeRef>(a, a.L.refs);
-  for (int s = blockIdx.x; s < n_segs; s += gridDim.x) {
-    const TreeSeg sg = tree_at<TreeSeg>(a, a.L.segs)[s];
-    auto ref_of = [&](int col) {
-      int lo = 0, hi = sg.n_ref;  // the reference that holds the column
+  const int G = a.n_q_heads / a.n_kv_heads, half = a.head_dim / 2, V = a.n_view, T = a.max_nodes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t *n_nodes = tree_at<int32_t>(a, a.L.n_nodes), *first = tree_at<int32_t>(a, a.L.col);
+  const int32_t *rot0 = tree_at<int32_t>(a, a.L.rot0), *rank = tree_at<int32_t>(a, a.L.rank);
+  for (int gi = blockIdx.x; gi < tree_at<TreeHeader>(a, a.L.hdr)->n_groups; gi += gridDim.x) {
+    const TreeGroup g = tree_at<TreeGroup>(a, a.L.groups)[gi];
+    for (int x = threadIdx.x; x < g.n_cols; x += 256) {
+      int lo = g.row0, hi = g.row1 + 1;  // the last row that starts at or before the column
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (refs[sg.ref0 + mid].col <= col) lo = mid; else hi = mid;
+        if (first[mid] <= g.col0 + x) lo = mid; else hi = mid;
       }
-      return refs[sg.ref0 + lo];
-    };
-    for (int x = threadIdx.x; x < sg.n_cols; x += 256) {
-      const int col = sg.col0 + x;
-      const TreeRef ref = ref_of(col);
-      const int local = col - ref.col;
-      tree_at<TreeColumn>(a, a.L.columns)[sg.table + x] =
-          TreeColumn{ref.row * a.max_nodes + local / G, local % G, sg.rot0 + col / G, 0};
+      const int local = g.col0 + x - first[lo], i = local / G;
+      tree_at<TreeColumn>(a, a.L.columns)[g.col0 + x] =
+          TreeColumn{lo * T + i, local % G, rot0[lo] + i, static_cast<uint16_t>(n_nodes[lo]),
+                     static_cast<uint16_t>(rank[lo] - g.rank0)};
     }
-    // rows whose first column is the segment's
-    const int p0 = (sg.col0 + G - 1) / G, p1 = (sg.col0 + sg.n_cols + G - 1) / G;
-    for (int p = p0 + (threadIdx.x >> 5); p < p1; p += 8) {
-      const TreeRef ref = ref_of(p * G);
-      const int64_t rel = ref.rel + tree_at<int32_t>(a, a.L.depth)[ref.row * a.max_nodes + p - ref.col / G];
-      float2 *to = tree_at<float2>(a, a.L.rot) + static_cast<int64_t>(sg.rot0 + p) * half;
+  }
+  // rotations: a warp a (view entry or tree, node), a CTA a share of a row's
+  const int64_t work = static_cast<int64_t>(a.n_rows) * (V + 1);
+  for (int64_t x = blockIdx.x; x < work; x += gridDim.x) {
+    const int r = static_cast<int>(x / (V + 1)), v = static_cast<int>(x % (V + 1)), n = n_nodes[r];
+    if (n == 0 || (v < V && (m.view_block[r * V + v] < 0))) continue;
+    const int64_t root = v < V ? static_cast<int64_t>(m.q_pos[r]) - m.view_offset[r * V + v]
+                               : tree_at<int32_t>(a, a.L.pos)[r];
+    for (int i = warp; i < n; i += 8) {
+      const int64_t rel = root + tree_at<int32_t>(a, a.L.depth)[static_cast<int64_t>(r) * T + i];
+      float2 *to = tree_at<float2>(a, a.L.rot) + (rot0[r] + static_cast<int64_t>(v) * n + i) * half;
       for (int j = lane; j < half; j += 32) rope_cos_sin_exact(rel, a.phase[j], &to[j].x, &to[j].y);
     }
   }
@@ -456,9 +535,10 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
   const int64_t node = item / a.n_kv_heads;
   const int r = static_cast<int>(node / a.max_nodes), i = static_cast<int>(node % a.max_nodes);
   if (r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) return;
-  // the tree's own segment holds the keys' rotations too
-  const TreeSeg &sg = tree_at<TreeSeg>(a, a.L.segs)[tree_at<int32_t>(a, a.L.entry_seg)[a.n_rows * a.n_view + r]];
-  const float2 *rot = tree_at<float2>(a, a.L.rot) + static_cast<int64_t>(sg.rot0 + i) * half;
+  // the keys turn as the queries do against their own tree
+  const int nodes = tree_at<int32_t>(a, a.L.n_nodes)[r];
+  const float2 *rot = tree_at<float2>(a, a.L.rot) +
+                      (tree_at<int32_t>(a, a.L.rot0)[r] + static_cast<int64_t>(a.n_view) * nodes + i) * half;
   const int64_t slot = static_cast<int64_t>(tree_at<int32_t>(a, a.L.slot)[r]) + i;
   const T *kn = reinterpret_cast<const T *>(a.k_new) + item * D;
   const T *vn = reinterpret_cast<const T *>(a.v_new) + item * D;
@@ -487,111 +567,67 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
 // ----------------------------------------------------------------- merge
 
 constexpr int kMergeWarps = 8;
-constexpr int kMergeList = 256;  // records a warp lists at a time
 
 // One (row, node, q head) a warp: its records - one for every CTA that
-// touched a segment holding its column - joined as
+// touched its group - joined as
 //   M = max m,  out = sum o 2^(m - M) / sum l 2^(m - M),  lse = (M + log2 l) ln 2.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int EPL = D / 32;
-  __shared__ int2 list_s[kMergeWarps][kMergeList];  // record's first row; its columns, the item's column
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (!tree_plan_ok(a)) return;
-  const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp;
   const int G = a.n_q_heads / a.n_kv_heads;
   const int x = static_cast<int>(item % a.n_q_heads);  // place in the head list: kv head, then its q heads
   const int64_t node = item / a.n_q_heads;
   const int r = static_cast<int>(node / a.max_nodes), i = static_cast<int>(node % a.max_nodes);
-  if (r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) {
+  if (!tree_plan_ok(a) || r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever follows this grid follows that one
     return;
   }
+  const int n_groups = tree_at<const TreeHeader>(a, a.L.hdr)->n_groups;
   const int h = x / G, hq = tree_at<int32_t>(a, a.L.heads)[x];
-  const int local = i * G + x % G;
-  int2 *list = list_s[warp];
-  bool waited = false;
-  const int32_t *entry_seg = tree_at<int32_t>(a, a.L.entry_seg), *entry_col = tree_at<int32_t>(a, a.L.entry_col);
-  const float2 *ml = tree_at<float2>(a, a.L.ml);
-  const float *o = tree_at<float>(a, a.L.o);
-  float M = -INFINITY, L = 0.f, acc[EPL];
+  const int2 run = tree_at<int2>(a, a.L.run)[r];
+  const int in_run = tree_at<int32_t>(a, a.L.col)[r] + i * G + x % G - run.y;
+  const int g = run.x + in_run / a.L.cols, col = in_run % a.L.cols;
+  const int n_cols = tree_at<TreeGroup>(a, a.L.groups)[g].n_cols;
+  const int64_t k = static_cast<int64_t>(h) * n_groups + g;
+  const int n = tree_at<int2>(a, a.L.piece_cta)[k].y;
+  const int64_t row0 = tree_at<int32_t>(a, a.L.piece_row)[k];
+  const float2 *ml = tree_at<float2>(a, a.L.ml) + row0 + col;
+  const float *o = tree_at<float>(a, a.L.o) + record_at(row0, n_cols, col, lane * EPL, D);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the records
+  float M = -INFINITY;
+  for (int j = lane; j < n; j += 32) M = fmaxf(M, ml[j * n_cols].x);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float L = 0.f, acc[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  // usually one window: a view that names one block many times has more
-  for (int first = 0, total = 1; first < total; first += kMergeList) {
-    // the records' rows, from the row's view entries and its tree
-    int n = 0;
-    for (int v0 = 0; v0 <= a.n_view; v0 += 32) {
-      const int v = v0 + lane;
-      int cnt = 0, row0 = 0, step = 0, col = 0;
-      if (v <= a.n_view) {
-        const int e = v < a.n_view ? r * a.n_view + v : a.n_rows * a.n_view + r;
-        const int s0 = entry_seg[e];
-        if (s0 >= 0) {
-          col = entry_col[e] + local;
-          const int s = s0 + col / a.L.cols;
-          col %= a.L.cols;
-          const int64_t k = static_cast<int64_t>(h) * hdr.n_segs + s;
-          cnt = tree_at<int2>(a, a.L.piece_cta)[k].y;
-          step = tree_at<TreeSeg>(a, a.L.segs)[s].n_cols;
-          row0 = tree_at<int32_t>(a, a.L.piece_row)[k];
-        }
-      }
-      int incl = cnt;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += y;
-      }
-      const int at = n + incl - cnt - first;
-      for (int j = max(0, -at); j < cnt && at + j < kMergeList; ++j)
-        list[at + j] = make_int2(row0 + j * step, step << 16 | col);
-      n += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    __syncwarp();
-    total = n;
-    n = min(n - first, kMergeList);
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the records
-    waited = true;
-    float top = M;
-    for (int j = lane; j < n; j += 32) top = fmaxf(top, ml[list[j].x + (list[j].y & 0xffff)].x);
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float old = M == -INFINITY ? 0.f : ex2(M - top);
-    M = top;
-    L *= old;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] *= old;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const int2 at = list[j];
-      const int col = at.y & 0xffff;
-      const float2 x2 = ml[at.x + col];
-      const float w = M == -INFINITY ? 0.f : ex2(x2.x - M);
-      L += x2.y * w;
-      const float *src = o + record_at(at.x, at.y >> 16, col, lane * EPL, D);
-      float val[EPL];
-      if constexpr (EPL == 4) {
-        const float4 y = *reinterpret_cast<const float4 *>(src);
-        val[0] = y.x; val[1] = y.y; val[2] = y.z; val[3] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2 *>(src);
-        val[0] = y.x; val[1] = y.y;
-      }
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, val[e], acc[e]);
+  for (int j = 0; j < n; ++j) {
+    const float2 x2 = ml[j * n_cols];
+    const float *src = o + static_cast<int64_t>(j) * n_cols * D;
+    const float w = ex2(x2.x - M);
+    L += x2.y * w;
+    float val[EPL];
+    if constexpr (EPL == 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(src);
+      val[0] = y.x; val[1] = y.y; val[2] = y.z; val[3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2 *>(src);
+      val[0] = y.x; val[1] = y.y;
     }
-    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, val[e], acc[e]);
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = 1.f / L;  // (a node attends itself; NaN where its values are)
   T res[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) res[e] = from_f32<T>(acc[e] * inv);
   const int64_t out_row = node * a.n_q_heads + hq;
   store_row_part<T, EPL>(static_cast<T *>(a.out) + out_row * D + lane * EPL, res);
   if (a.lse && lane == 0)
-    a.lse[out_row] = L > 0.f ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
+    a.lse[out_row] = (M + log2f(L)) * 0.693147180559945309f;
 }
 
 // ---------------------------------------------------------------- commit
@@ -682,12 +718,18 @@ static cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int thr
 }
 
 cudaError_t launch_tree_plan(const TreeArgs &a, const TreeMeta &m, cudaStream_t s) {
-  static_assert(sizeof(TreePlanSmem) <= 48 * 1024, "the plan's shared memory needs no opt-in");
+  static bool configured = false;
+  if (!configured) {
+    const cudaError_t e = cudaFuncSetAttribute(tree_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(TreePlanSmem)));
+    if (e != cudaSuccess) return e;
+    configured = true;
+  }
   tree_plan_kernel<<<1, kPlanThreads, sizeof(TreePlanSmem), s>>>(a, m);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t most = 4ll * a.L.ctas_max;
-  tree_columns_kernel<<<static_cast<unsigned>(a.L.max_segs < most ? a.L.max_segs : most), 256, 0, s>>>(a);
+  const int64_t work = static_cast<int64_t>(a.n_rows) * (a.n_view + 1), most = 4ll * a.L.ctas_max;
+  tree_tables_kernel<<<static_cast<unsigned>(work < most ? work : most), 256, 0, s>>>(a, m);
   return cudaGetLastError();
 }
 
@@ -727,15 +769,17 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.tile = tc ? 128 : 64;
   L.ctas_max = tc ? sms : 2 * sms;
   if (L.ctas_max > 1024) L.ctas_max = 1024;
-  const int64_t R = d.n_rows, E = R * d.max_view_blocks, G = d.n_q_heads / d.n_kv_heads;
+  const int64_t R = d.n_rows, V = d.max_view_blocks, G = d.n_q_heads / d.n_kv_heads;
   const int64_t Q = R * max_nodes;  // nodes
-  const int64_t block_cols = Q * d.max_view_blocks * G, tree_cols = Q * G;
-  L.max_refs = E + R;
-  // sum of ceil(cols / L.cols) over the referenced blocks and the trees
-  L.max_segs = d.n_blocks + block_cols / L.cols + R + tree_cols / L.cols + 1;
-  L.max_cols = block_cols + tree_cols;
-  L.max_rots = L.max_cols / G;
-  L.max_rows = d.n_kv_heads * (block_cols + tree_cols) + static_cast<int64_t>(L.ctas_max) * L.cols;
+  L.max_cols = Q * G;
+  // a row ends a group early at most once, and is cut by each full one
+  L.max_groups = R + L.max_cols / L.cols + 1;
+  const int64_t parts = R + L.max_groups;  // (row, group) pairs
+  L.max_spans = parts * (V + 1);
+  // spans of blocks times rows: a group has up to min(R, cols) rows
+  L.max_map = parts * V * (R < L.cols ? R : L.cols);
+  L.max_rots = Q * (V + 1);
+  L.max_rows = d.n_kv_heads * L.max_cols + static_cast<int64_t>(L.ctas_max) * L.cols;
   size_t at = 256;
   auto put = [&](size_t bytes) {
     const size_t o = at;
@@ -743,20 +787,23 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
     return o;
   };
   L.hdr = put(sizeof(TreeHeader));
-  L.segs = put(sizeof(TreeSeg) * L.max_segs);
-  L.wbase = put(2 * sizeof(int64_t) * L.max_segs);  // weights, then units before each segment
-  L.refs = put(sizeof(TreeRef) * L.max_refs);
+  L.groups = put(sizeof(TreeGroup) * L.max_groups);
+  L.wbase = put(2 * sizeof(int64_t) * L.max_groups);  // weights, then units before each group
+  L.spans = put(sizeof(TreeSpan) * L.max_spans);
+  L.map = put(2 * L.max_map);
   L.columns = put(sizeof(TreeColumn) * L.max_cols);
   L.rot = put(4 * static_cast<size_t>(d.head_dim) * L.max_rots);
-  L.entry_seg = put(4 * L.max_refs);
-  L.entry_col = put(4 * L.max_refs);
-  L.piece_row = put(4 * L.max_segs * d.n_kv_heads);
-  L.piece_cta = put(8 * L.max_segs * d.n_kv_heads);
+  L.piece_row = put(4 * L.max_groups * d.n_kv_heads);
+  L.piece_cta = put(8 * L.max_groups * d.n_kv_heads);
   L.ctas = put(sizeof(TreeCta) * L.ctas_max);
   L.n_nodes = put(4 * R);
   L.slot = put(4 * R);
   L.pos = put(4 * R);
   L.end = put(4 * R);
+  L.col = put(4 * R);
+  L.run = put(8 * R);
+  L.rot0 = put(4 * R);
+  L.rank = put(4 * R);
   L.depth = put(4 * Q);
   L.mask = put(16 * Q);
   L.heads = put(4 * d.n_q_heads);

@@ -2,10 +2,10 @@
 // (fp32 FMA, fp32 accumulation): fp32 caches, where tensor-core rounding is
 // too coarse, and head_dim 64.
 //
-// A CTA walks its units (hw_tree.h): per segment up to 32 rotated queries in
-// shared memory, tiles of 64 tokens, an online softmax in the log2 domain,
-// and a record of (m, l, o) per column at the end.  A tree's tile is masked
-// with the ancestor bits of each column's node.
+// A CTA walks its units (hw_tree.h): per group up to 32 queries in shared
+// memory, rotated anew for every span, tiles of 64 tokens, an online softmax
+// in the log2 domain, and a record of (m, l, o) per column at the end.  A
+// tree's tile is masked with the ancestor bits of each column's node.
 #include <cuda_fp8.h>
 
 #include "hw_device.cuh"
@@ -26,9 +26,9 @@ struct Smem {
   alignas(16) float v[kTile][D + 4];
   alignas(16) float p[kCols][kTile + 4];
   float m[kCols], l[kCols], alpha[kCols];
-  int32_t qrow[kCols];    // query row of the column: node * Hq + q head
-  int32_t node[kCols];    // row * max_nodes + node
-  int32_t rot[kCols];     // its row of the rotation table
+  TreeColumn col[kCols];
+  int32_t rot[kCols];     // row of the rotation table for this span, or -1: unseen
+  uint32_t bad[2];        // a partial tile's tokens with a value that is not finite
 };
 
 template <typename KV>
@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
   const int c = blockIdx.x;
   if (c >= hdr.n_ctas) return;
   TreeCta at = tree_at<TreeCta>(a, a.L.ctas)[c];
-  const TreeSeg *segs = tree_at<TreeSeg>(a, a.L.segs);
-  const TreeColumn *columns = tree_at<TreeColumn>(a, a.L.columns);
+  const TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
+  const TreeSpan *spans = tree_at<TreeSpan>(a, a.L.spans);
   const int G = a.n_q_heads / a.n_kv_heads;
   constexpr int EPV = 16 / sizeof(KV), CPR = D / EPV;
   constexpr int QSTEP = kThreads / D;   // columns side by side in P.V
@@ -86,112 +86,134 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
   const int dcol = tid % D, qfirst = tid / D;
 
   while (at.n_units > 0) {
-    const TreeSeg sg = segs[at.seg];
-    const int h = at.head, nq = sg.n_cols;
+    const TreeGroup gr = groups[at.group];
+    const int h = at.head, nq = gr.n_cols;
     const float ks = a.k_scale ? a.k_scale[h] : 1.f, vs = a.v_scale ? a.v_scale[h] : 1.f;
     if (tid < nq) {
-      const TreeColumn tc = columns[sg.table + tid];
-      S.node[tid] = tc.node;
-      S.qrow[tid] = tc.node * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[h * G + tc.head];
-      S.rot[tid] = tc.rot;
+      S.col[tid] = tree_at<TreeColumn>(a, a.L.columns)[gr.col0 + tid];
       S.m[tid] = -INFINITY;
       S.l[tid] = 0.f;
-    }
-    __syncthreads();
-    for (int x = tid; x < nq * (D / 2); x += kThreads) {
-      const int qi = x / (D / 2), i = x % (D / 2);
-      const T *qp = reinterpret_cast<const T *>(a.q) + static_cast<int64_t>(S.qrow[qi]) * D;
-      const float x0 = to_f32<T>(qp[i]), x1 = to_f32<T>(qp[i + D / 2]);
-      const float2 r = tree_at<float2>(a, a.L.rot)[static_cast<int64_t>(S.rot[qi]) * (D / 2) + i];
-      S.q[qi][i] = x0 * r.x - x1 * r.y;
-      S.q[qi][i + D / 2] = x1 * r.x + x0 * r.y;
     }
     float acc[QPT];
 #pragma unroll
     for (int k = 0; k < QPT; ++k) acc[k] = 0.f;
-    const int tiles = (sg.len + kTile - 1) / kTile;
-    const int t1 = min(tiles, at.tile + at.n_units);
-    for (int t = at.tile; t < t1; ++t) {
-      const int valid = min(kTile, sg.len - t * kTile);
-      const int64_t row0 = static_cast<int64_t>(h) * a.capacity + sg.start + t * kTile;
-      const KV *kb = reinterpret_cast<const KV *>(a.k) + row0 * D;
-      const KV *vb = reinterpret_cast<const KV *>(a.v) + row0 * D;
+    for (; at.span < gr.n_spans && at.n_units > 0; ++at.span, at.tile = 0) {
+      const TreeSpan sp = spans[gr.span0 + at.span];
       __syncthreads();
-      for (int x = tid; x < kTile * CPR; x += kThreads) {
-        const int row = x / CPR, col = (x % CPR) * EPV;
-        float kf[EPV], vf[EPV];
-        if (row < valid) {
-          unpack<KV>(*reinterpret_cast<const uint4 *>(kb + static_cast<int64_t>(row) * D + col), kf);
-          unpack<KV>(*reinterpret_cast<const uint4 *>(vb + static_cast<int64_t>(row) * D + col), vf);
-        } else {  // rows past the segment may hold anything
-#pragma unroll
-          for (int i = 0; i < EPV; ++i) kf[i] = vf[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < EPV; ++i) {
-          S.k[row][col + i] = kf[i] * ks;
-          S.v[row][col + i] = vf[i] * vs;
-        }
+      if (tid < nq) {  // the columns that see the span, and their rotations
+        const TreeColumn &cl = S.col[tid];
+        const int v = sp.row < 0 ? tree_at<int16_t>(a, a.L.map)[sp.map + cl.row] : cl.node / a.max_nodes == sp.row ? a.n_view : -1;
+        S.rot[tid] = v < 0 ? -1 : cl.rot + v * cl.n_nodes;
       }
       __syncthreads();
-      for (int qq = warp; qq < nq; qq += kThreads / 32) {
-        float s0 = 0.f, s1 = 0.f;
+      for (int x = tid; x < nq * (D / 2); x += kThreads) {
+        const int qi = x / (D / 2), i = x % (D / 2);
+        if (S.rot[qi] < 0) continue;
+        const int64_t row = static_cast<int64_t>(S.col[qi].node) * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[h * G + S.col[qi].head];
+        const T *qp = reinterpret_cast<const T *>(a.q) + row * D;
+        const float x0 = to_f32<T>(qp[i]), x1 = to_f32<T>(qp[i + D / 2]);
+        const float2 r = tree_at<float2>(a, a.L.rot)[static_cast<int64_t>(S.rot[qi]) * (D / 2) + i];
+        S.q[qi][i] = x0 * r.x - x1 * r.y;
+        S.q[qi][i + D / 2] = x1 * r.x + x0 * r.y;
+      }
+      const int t1 = min((sp.len + kTile - 1) / kTile, at.tile + at.n_units);
+      at.n_units -= t1 - at.tile;
+      for (int t = at.tile; t < t1; ++t) {
+        const int valid = min(kTile, sp.len - t * kTile);
+        const int64_t row0 = static_cast<int64_t>(h) * a.capacity + sp.start + t * kTile;
+        const KV *kb = reinterpret_cast<const KV *>(a.k) + row0 * D;
+        const KV *vb = reinterpret_cast<const KV *>(a.v) + row0 * D;
+        __syncthreads();
+        if (tid < 2) S.bad[tid] = 0;
+        __syncthreads();
+        for (int x = tid; x < kTile * CPR; x += kThreads) {
+          const int row = x / CPR, col = (x % CPR) * EPV;
+          float kf[EPV], vf[EPV];
+          if (row < valid) {
+            unpack<KV>(*reinterpret_cast<const uint4 *>(kb + static_cast<int64_t>(row) * D + col), kf);
+            unpack<KV>(*reinterpret_cast<const uint4 *>(vb + static_cast<int64_t>(row) * D + col), vf);
+          } else {  // rows past the span may hold anything
+#pragma unroll
+            for (int i = 0; i < EPV; ++i) kf[i] = vf[i] = 0.f;
+          }
+          if (sp.partial) {
+            // 0 * NaN must not reach the columns that do not see the token;
+            // those that do get a NaN through their sum
+#pragma unroll
+            for (int i = 0; i < EPV; ++i)
+              if (!(fabsf(vf[i]) < INFINITY)) {
+                vf[i] = 0.f;
+                atomicOr(&S.bad[row >> 5], 1u << (row & 31));
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < EPV; ++i) {
+            S.k[row][col + i] = kf[i] * ks;
+            S.v[row][col + i] = vf[i] * vs;
+          }
+        }
+        __syncthreads();
+        for (int qq = warp; qq < nq; qq += kThreads / 32) {
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll 8
-        for (int d = 0; d < D; d += 4) {
-          const float4 qv = *reinterpret_cast<const float4 *>(&S.q[qq][d]);
-          const float4 k0 = *reinterpret_cast<const float4 *>(&S.k[lane][d]);
-          const float4 k1 = *reinterpret_cast<const float4 *>(&S.k[lane + 32][d]);
-          s0 += qv.x * k0.x + qv.y * k0.y + qv.z * k0.z + qv.w * k0.w;
-          s1 += qv.x * k1.x + qv.y * k1.y + qv.z * k1.z + qv.w * k1.w;
-        }
-        bool in0 = lane < valid, in1 = lane + 32 < valid;
-        if (sg.row >= 0) {  // a tree: the node's ancestors and itself
-          const uint32_t *mask = tree_at<uint32_t>(a, a.L.mask) + static_cast<int64_t>(S.node[qq]) * 4 + 2 * t;
-          in0 = in0 && (mask[0] >> lane) & 1u;
-          in1 = in1 && (mask[1] >> lane) & 1u;
-        }
-        s0 = in0 ? s0 * a.scale_log2 : -INFINITY;
-        s1 = in1 ? s1 * a.scale_log2 : -INFINITY;
-        float mx = fmaxf(s0, s1);
+          for (int d = 0; d < D; d += 4) {
+            const float4 qv = *reinterpret_cast<const float4 *>(&S.q[qq][d]);
+            const float4 k0 = *reinterpret_cast<const float4 *>(&S.k[lane][d]);
+            const float4 k1 = *reinterpret_cast<const float4 *>(&S.k[lane + 32][d]);
+            s0 += qv.x * k0.x + qv.y * k0.y + qv.z * k0.z + qv.w * k0.w;
+            s1 += qv.x * k1.x + qv.y * k1.y + qv.z * k1.z + qv.w * k1.w;
+          }
+          const bool seen = S.rot[qq] >= 0;
+          bool in0 = seen && lane < valid, in1 = seen && lane + 32 < valid;
+          if (sp.row >= 0) {  // a tree: the node's ancestors and itself
+            const uint32_t *mask = tree_at<uint32_t>(a, a.L.mask) + static_cast<int64_t>(S.col[qq].node) * 4 + 2 * t;
+            in0 = in0 && (mask[0] >> lane) & 1u;
+            in1 = in1 && (mask[1] >> lane) & 1u;
+          }
+          s0 = in0 ? s0 * a.scale_log2 : -INFINITY;
+          s1 = in1 ? s1 * a.scale_log2 : -INFINITY;
+          float mx = fmaxf(s0, s1);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_old = S.m[qq];
-        const float m_new = fmaxf(m_old, mx);
-        const float base = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: weights 0, no NaN
-        const float p0 = ex2(s0 - base), p1 = ex2(s1 - base);
-        float sum = p0 + p1;
+          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const float m_old = S.m[qq];
+          const float m_new = fmaxf(m_old, mx);
+          const float base = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: weights 0, no NaN
+          const float p0 = ex2(s0 - base), p1 = ex2(s1 - base);
+          float sum = p0 + p1;
+          if ((in0 && (S.bad[0] >> lane) & 1u) || (in1 && (S.bad[1] >> lane) & 1u)) sum = NAN;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        S.p[qq][lane] = p0;
-        S.p[qq][lane + 32] = p1;
-        if (lane == 0) {
-          const float alpha = ex2(m_old - base);
-          S.alpha[qq] = alpha;
-          S.m[qq] = m_new;
-          S.l[qq] = S.l[qq] * alpha + sum;
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          S.p[qq][lane] = p0;
+          S.p[qq][lane + 32] = p1;
+          if (lane == 0) {
+            const float alpha = ex2(m_old - base);
+            S.alpha[qq] = alpha;
+            S.m[qq] = m_new;
+            S.l[qq] = S.l[qq] * alpha + sum;
+          }
         }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < QPT; ++k) {
-        const int qi = qfirst + k * QSTEP;
-        if (qi < nq) acc[k] *= S.alpha[qi];
-      }
-      for (int tt = 0; tt < valid; tt += 4) {
-        const float v0 = S.v[tt][dcol], v1 = S.v[tt + 1][dcol];
-        const float v2 = S.v[tt + 2][dcol], v3 = S.v[tt + 3][dcol];
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < QPT; ++k) {
           const int qi = qfirst + k * QSTEP;
-          if (qi < nq) {
-            const float4 pp = *reinterpret_cast<const float4 *>(&S.p[qi][tt]);
-            acc[k] += pp.x * v0 + pp.y * v1 + pp.z * v2 + pp.w * v3;
+          if (qi < nq) acc[k] *= S.alpha[qi];
+        }
+        for (int tt = 0; tt < valid; tt += 4) {
+          const float v0 = S.v[tt][dcol], v1 = S.v[tt + 1][dcol];
+          const float v2 = S.v[tt + 2][dcol], v3 = S.v[tt + 3][dcol];
+#pragma unroll
+          for (int k = 0; k < QPT; ++k) {
+            const int qi = qfirst + k * QSTEP;
+            if (qi < nq) {
+              const float4 pp = *reinterpret_cast<const float4 *>(&S.p[qi][tt]);
+              acc[k] += pp.x * v0 + pp.y * v1 + pp.z * v2 + pp.w * v3;
+            }
           }
         }
       }
     }
     // the record
-    const int64_t k = static_cast<int64_t>(h) * hdr.n_segs + at.seg;
+    const int64_t k = static_cast<int64_t>(h) * hdr.n_groups + at.group;
     const int64_t rec = tree_at<int32_t>(a, a.L.piece_row)[k] +
                         static_cast<int64_t>(c - tree_at<int2>(a, a.L.piece_cta)[k].x) * nq;
 #pragma unroll
@@ -203,10 +225,9 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
       }
     }
     __syncthreads();
-    at.n_units -= t1 - at.tile;
-    at.tile = 0;
-    if (++at.seg == hdr.n_segs) {
-      at.seg = 0;
+    at.span = at.tile = 0;
+    if (++at.group == hdr.n_groups) {
+      at.group = 0;
       ++at.head;
     }
   }

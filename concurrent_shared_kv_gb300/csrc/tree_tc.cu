@@ -1,9 +1,9 @@
 // tree_tc.cu - attention for trees of drafted tokens on the sm_100 tensor
 // cores (tcgen05 + TMEM): bf16 caches with head_dim 128.
 //
-// A segment (hw_tree.h) puts up to 256 query columns (nodes x q heads of a kv
-// head x rows that see the block) against its tokens, as two query tiles of
-// 128 rows that share every K/V tile:
+// A group (hw_tree.h) puts up to 256 query columns (nodes x q heads of a kv
+// head x rows that share blocks) against its spans' tokens, as two query tiles
+// of 128 rows that share every K/V tile:
 //   S [128 queries x 128 tokens] = Q~ . K^T     (A, B in shared memory)
 //   O [128 queries x 128 d]     += P . V        (A = P in TMEM)
 // With a query per TMEM lane, a softmax thread owns its row: no exchange for
@@ -42,6 +42,8 @@ struct TcSmem {
   alignas(1024) uint8_t kv[kStages][kStage];
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_empty[2], mma_done;
+  uint64_t scanned[2];   // partial tiles: the tokens with a value that is not finite are known
+  uint32_t bad[2][4];
   uint32_t tmem;
   int32_t abort_flag;
 };
@@ -114,46 +116,58 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&p);
 }
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&x)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// The CTA's units, segment by segment.
+// The CTA's units, span by span.
 struct Walk {
-  int head, seg, tile, left;  // kv head, segment, first tile of it, units still to come
-  int n_segs;
-  TreeSeg sg;
-  int tiles;  // of this segment that are the CTA's
-  __device__ __forceinline__ void load(const TreeSeg *segs) {
-    sg = segs[seg];
-    tiles = min((sg.len + kT - 1) / kT - tile, left);
+  const TreeGroup *groups;
+  const TreeSpan *spans;
+  int n_groups;
+  int head, group, span, tile, left;  // kv head, group, span, its first tile, units still to come
+  TreeGroup g;
+  TreeSpan sp;
+  int tiles;  // of this span that are the CTA's
+  __device__ __forceinline__ void load_span() {
+    sp = spans[g.span0 + span];
+    tiles = min((sp.len + kT - 1) / kT - tile, left);
   }
-  __device__ __forceinline__ bool next(const TreeSeg *segs) {
+  // On to the next span: 0 at the end, 1 in the same group, 2 in another one.
+  __device__ __forceinline__ int next() {
     left -= tiles;
-    if (left <= 0) return false;
+    if (left <= 0) return 0;
     tile = 0;
-    if (++seg == n_segs) {
-      seg = 0;
-      ++head;
+    const bool other = ++span == g.n_spans;
+    if (other) {
+      span = 0;
+      if (++group == n_groups) {
+        group = 0;
+        ++head;
+      }
+      g = groups[group];
     }
-    load(segs);
-    return true;
+    load_span();
+    return other ? 2 : 1;
   }
 };
 
-__device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, const CUtensorMap *tv, Walk w,
-                         const TreeSeg *segs) {
+__device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, const CUtensorMap *tv, Walk w) {
   const uint64_t pol = policy_evict_first();
   int n = 0;  // ring entries issued: K(0), V(0), K(1), V(1), ...
   bool waited = false, go = true;
   do {
-    if (w.sg.row >= 0 && !waited) {  // a tree: its tokens come from the launch before
+    if (w.sp.row >= 0 && !waited) {  // a tree: its tokens come from the launch before
       asm volatile("griddepcontrol.wait;" ::: "memory");
       asm volatile("fence.proxy.async;" ::: "memory");
       waited = true;
     }
     for (int t = w.tile; go && t < w.tile + w.tiles; ++t) {
-      const int row = w.sg.start + t * kT;
+      const int row = w.sp.start + t * kT;
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const int s = n % kStages;
         if (n >= kStages && !wait_or_abort(S, a, &S.kv_empty[s], ((n / kStages) & 1) ^ 1)) {
@@ -165,7 +179,7 @@ __device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, co
         tma_load_3d(S.kv[s] + kBox, kv ? tv : tk, &S.kv_full[s], 64, row, w.head, pol);
       }
     }
-  } while (go && w.next(segs));
+  } while (go && w.next());
   if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
   // no copy may still be landing when the CTA retires
   for (int j = n > kStages ? n - kStages : 0; j < n; ++j) mbar_wait(&S.kv_full[j % kStages], (j / kStages) & 1);
@@ -175,13 +189,13 @@ __device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, co
 // stay in uniform registers: issued from a branch of one lane, 8 MMAs took
 // 1200 clocks instead of the 512 the tensor cores need for them, and 4 x 64
 // nodes on a 16K history 225 us.)
-__device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, const TreeSeg *segs) {
+__device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w) {
   constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0), idesc_pv = idesc_bf16(128, 128, 0, 1);
   const uint32_t q0 = smem_u32(S.q[0]), kv0 = smem_u32(S.kv[0]);
   const uint64_t a_qk = smem_desc(q0, 16, 1024, kSw128), b_qk = smem_desc(kv0, 16, 1024, kSw128);
   const uint64_t b_pv = smem_desc(kv0, kBox, 1024, kSw128);
   int i = 0;  // tiles whose QK is issued
-  // per query tile: PVs issued, segments whose PVs and whose QKs have begun
+  // per query tile: PVs issued, groups whose PVs have begun, rotations used
   int np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0};
   // S of query tile qt from the K in stage s
   auto qk = [&](int qt, int s) {
@@ -223,36 +237,31 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
     __syncwarp();
   };
   bool pend = false, pend_two = false, pend_first = false;  // the tile whose PVs are to come
-  int pend_steps = 0;
+  int pend_steps = 0, step = 2;
   bool go = true;
   do {
-    const bool two = w.sg.n_cols > 128;
+    const bool two = w.g.n_cols > 128;
     for (int t = 0; go && t < w.tiles; ++t, ++i) {
-      const bool first = t == 0;
-      const int nk = 2 * i, nv = 2 * i - 1;
+      const int nk = 2 * i, nv = 2 * i - 1, s = nk % kStages;
       if (pend && !(go = pv(0, nv, pend_steps, pend_first))) break;
-      if (!first) {
-        if (!(go = warp_wait(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
-        tc_fence_after();
-        qk(0, nk % kStages);
-      }
+      if (t == 0 && !(go = warp_wait(S, a, &S.q_full[0], nq[0]++ & 1))) break;
+      if (!(go = warp_wait(S, a, &S.kv_full[s], (nk / kStages) & 1))) break;
+      tc_fence_after();
+      qk(0, s);
       if (pend && pend_two && !(go = pv(1, nv, pend_steps, pend_first))) break;
       if (pend) release(nv % kStages);
-      if (first) {
-        if (!(go = warp_wait(S, a, &S.q_full[0], nq[0]++ & 1))) break;
-        if (two && !(go = warp_wait(S, a, &S.q_full[1], nq[1]++ & 1))) break;
-        if (!(go = warp_wait(S, a, &S.kv_full[nk % kStages], (nk / kStages) & 1))) break;
+      if (two) {
+        if (t == 0 && !(go = warp_wait(S, a, &S.q_full[1], nq[1]++ & 1))) break;
         tc_fence_after();
-        qk(0, nk % kStages);
+        qk(1, s);
       }
-      if (two) qk(1, nk % kStages);
-      release(nk % kStages);
+      release(s);
       pend = true;
       pend_two = two;
-      pend_first = first;
-      pend_steps = (min(kT, w.sg.len - (w.tile + t) * kT) + 15) / 16;
+      pend_first = t == 0 && step == 2;
+      pend_steps = (min(kT, w.sp.len - (w.tile + t) * kT) + 15) / 16;
     }
-  } while (go && w.next(segs));
+  } while (go && (step = w.next()));
   if (go && pend) {
     if (pv(0, 2 * i - 1, pend_steps, pend_first) && pend_two) pv(1, 2 * i - 1, pend_steps, pend_first);
   }
@@ -284,95 +293,129 @@ __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem,
   }
 }
 
-__device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, const TreeSeg *segs, int qt) {
+__device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int qt) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
-  const int col = qt * 128 + row;  // the thread's column of a segment
+  const int col = qt * 128 + row;  // the thread's column of a group
   const uint32_t s_tmem = tmem + qt * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t o_tmem = s_tmem + 256;
-  const TreeColumn *columns = tree_at<TreeColumn>(a, a.L.columns);
-  const int32_t *heads = tree_at<int32_t>(a, a.L.heads);
-  const int G = a.n_q_heads / a.n_kv_heads;
   const uint32_t qrow = smem_u32(S.q[qt]) + row * 128;
   int ns = 0;          // tiles of this query tile so far
   int i = 0;           // tiles of the CTA so far
+  int np = 0;          // partial tiles of the CTA so far
   float m = 0.f, l = 0.f;
-  // the record to come: that of the segment before
+  // the record to come: that of the group before
   bool have = false;
   int64_t rec = 0;
   int rec_cols = 0;
+  TreeColumn tc = {};
+  const uint4 *src = nullptr;
+  int step = 2;
   do {
-    const bool mine = col < w.sg.n_cols;                      // a query in this row
-    const bool active = qt == 0 || w.sg.n_cols > 128;         // a query in this tile
-    const bool warp_on = qt * 128 + quarter * 32 < w.sg.n_cols;
-    TreeColumn tc = {};
-    const uint4 *src = nullptr;
-    const float4 *rot = nullptr;
-    if (mine) {
-      tc = columns[w.sg.table + col];
-      const int64_t at = (static_cast<int64_t>(tc.node) * a.n_q_heads + heads[w.head * G + tc.head]) * 128;
-      src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at);
+    const bool mine = col < w.g.n_cols;                      // a query in this row
+    const bool active = qt == 0 || w.g.n_cols > 128;         // a query in this tile
+    const bool warp_on = qt * 128 + quarter * 32 < w.g.n_cols;
+    if (mine && step == 2) {
+      tc = tree_at<TreeColumn>(a, a.L.columns)[w.g.col0 + col];
+      const int hq = tree_at<int32_t>(a, a.L.heads)[w.head * (a.n_q_heads / a.n_kv_heads) + tc.head];
+      src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                            (static_cast<int64_t>(tc.node) * a.n_q_heads + hq) * 128);
       asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
       asm volatile("prefetch.global.L1 [%0];" ::"l"(src + 8));
-      rot = tree_at<float4>(a, a.L.rot) + static_cast<int64_t>(tc.rot) * 32;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) asm volatile("prefetch.global.L1 [%0];" ::"l"(rot + 8 * c));
     }
-    // the segment before is done with Q~ and with O
-    if (have && !warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
+    // the tokens the column sees: all, a node's ancestors and itself, or none
+    uint4 see = make_uint4(0, 0, 0, 0);
     if (mine) {
+      const int v = w.sp.row < 0 ? tree_at<int16_t>(a, a.L.map)[w.sp.map + tc.row]
+                    : tc.node / a.max_nodes == w.sp.row ? a.n_view : -1;
+      if (v >= 0) {
+        see = w.sp.row < 0 ? make_uint4(~0u, ~0u, ~0u, ~0u) : tree_at<uint4>(a, a.L.mask)[tc.node];
+        const float4 *rot = tree_at<float4>(a, a.L.rot) + (static_cast<int64_t>(tc.rot) + v * tc.n_nodes) * 32;
+        // Q~ of the span before is free: its last scores are there.
 #pragma unroll 2
-      for (int c = 0; c < 8; ++c) {  // elements 8c .. 8c+7 and their partners, 64 further
-        const uint4 u = __ldg(src + c), v = __ldg(src + c + 8);
-        const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
-        uint32_t p[4], r[4];
+        for (int c = 0; c < 8; ++c) {  // elements 8c .. 8c+7 and their partners, 64 further
+          const uint4 u = __ldg(src + c), u2 = __ldg(src + c + 8);
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {u2.x, u2.y, u2.z, u2.w};
+          uint32_t p[4], r[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 cs = __ldg(rot + 4 * c + j);  // (cos, sin) of two elements
-          const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
-          const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
-          p[j] = pack_bf16((x0 * cs.x - y0 * cs.y) * a.scale_log2, (x1 * cs.z - y1 * cs.w) * a.scale_log2);
-          r[j] = pack_bf16((y0 * cs.x + x0 * cs.y) * a.scale_log2, (y1 * cs.z + x1 * cs.w) * a.scale_log2);
+          for (int j = 0; j < 4; ++j) {
+            const float4 cs = __ldg(rot + 4 * c + j);  // (cos, sin) of two elements
+            const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
+            const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
+            p[j] = pack_bf16((x0 * cs.x - y0 * cs.y) * a.scale_log2, (x1 * cs.z - y1 * cs.w) * a.scale_log2);
+            r[j] = pack_bf16((y0 * cs.x + x0 * cs.y) * a.scale_log2, (y1 * cs.z + x1 * cs.w) * a.scale_log2);
+          }
+          const uint32_t o = (c ^ (row & 7)) << 4;
+          st_shared_v4(qrow + o, p[0], p[1], p[2], p[3]);
+          st_shared_v4(qrow + kBox + o, r[0], r[1], r[2], r[3]);
         }
-        const uint32_t o = (c ^ (row & 7)) << 4;
-        st_shared_v4(qrow + o, p[0], p[1], p[2], p[3]);
-        st_shared_v4(qrow + kBox + o, r[0], r[1], r[2], r[3]);
+        fence_proxy_async_smem();
       }
-      fence_proxy_async_smem();
     }
     __syncwarp();
     if (active && lane == 0) mbar_arrive(&S.q_full[qt]);
-    if (have) {
-      tc_fence_after();
-      store_record(a, o_tmem, rec, rec_cols, col, m, l);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.o_empty[qt]);
+    if (step == 2) {
+      if (have) {
+        if (!warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
+        tc_fence_after();
+        store_record(a, o_tmem, rec, rec_cols, col, m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.o_empty[qt]);
+      }
+      have = active;
+      const int64_t k = static_cast<int64_t>(w.head) * w.n_groups + w.group;
+      rec_cols = w.g.n_cols;
+      rec = tree_at<int32_t>(a, a.L.piece_row)[k] +
+            static_cast<int64_t>(blockIdx.x - tree_at<int2>(a, a.L.piece_cta)[k].x) * rec_cols;
     }
-    have = active;
     if (!active) {
       i += w.tiles;
+      np += w.sp.partial ? w.tiles : 0;
       continue;
     }
-    {
-      const int64_t k = static_cast<int64_t>(w.head) * w.n_segs + w.seg;
-      rec = tree_at<int32_t>(a, a.L.piece_row)[k] +
-            static_cast<int64_t>(blockIdx.x - tree_at<int2>(a, a.L.piece_cta)[k].x) * w.sg.n_cols;
-      rec_cols = w.sg.n_cols;
-    }
-    uint4 tree = make_uint4(~0u, ~0u, ~0u, ~0u);
-    if (w.sg.row >= 0 && mine) tree = tree_at<uint4>(a, a.L.mask)[tc.node];
     for (int t = 0; t < w.tiles; ++t, ++i, ++ns) {
-      const int valid = min(kT, w.sg.len - (w.tile + t) * kT);
+      const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
+      const bool first = step == 2 && t == 0;
       if (!warp_wait(S, a, &S.s_full[qt], ns & 1)) return;
-      if (qt == 0 && (valid & 15)) {
-        // V rows past the segment may hold anything, and 0 * NaN would poison
-        // the sum: the rows of the last step of 16 tokens are cleared
+      uint32_t bad = 0;
+      if (w.sp.partial || (qt == 0 && (valid & 15))) {
         const int nv = 2 * i + 1;
-        if (!warp_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1)) return;
-        const int rows = 16 - (valid & 15);
-        for (int z = row; z < rows * 16; z += 128)
-          st_shared_v4(smem_u32(S.kv[nv % kStages]) + ((z >> 3) & 1) * kBox + (valid + (z >> 4)) * 128 + (z & 7) * 16, 0, 0, 0, 0);
-        fence_proxy_async_smem();
+        if (qt == 0) {
+          // 0 * NaN would poison a sum.  V rows past the span, up to the end
+          // of the last step of 16 tokens, may hold anything: cleared.  In a
+          // tile that not every column sees, so are tokens with a value that
+          // is not finite: the columns that see them get a NaN through l.
+          if (!warp_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1)) return;
+          const uint32_t at = smem_u32(S.kv[nv % kStages]) + row * 128;
+          bool clear = row >= valid && row < ((valid + 15) & ~15);
+          bool odd = false;
+          if (w.sp.partial && row < valid)
+            for (int c = 0; c < 16; ++c) {
+              uint32_t x[4];
+              ld_shared_v4(at + (c >> 3) * kBox + ((c + row) & 7) * 16, x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                odd |= (x[j] & 0x7f80u) == 0x7f80u || (x[j] & 0x7f800000u) == 0x7f800000u;
+            }
+          if (clear || odd) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) st_shared_v4(at + (c >> 3) * kBox + (c & 7) * 16, 0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          if (w.sp.partial) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, odd);
+            if (lane == 0) {
+              S.bad[np & 1][quarter] = bits;
+              mbar_arrive(&S.scanned[np & 1]);
+            }
+          }
+        }
+        if (w.sp.partial) {
+          if (!warp_wait(S, a, &S.scanned[np & 1], (np >> 1) & 1)) return;
+          const uint32_t *b = S.bad[np & 1];
+          bad = (b[0] & see.x) | (b[1] & see.y) | (b[2] & see.z) | (b[3] & see.w);
+          ++np;
+        }
       }
       if (warp_on) {
         tc_fence_after();
@@ -380,8 +423,8 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, con
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
         tmem_wait_ld();
-        if (valid < kT || w.sg.row >= 0) {
-          const uint32_t tm[4] = {tree.x, tree.y, tree.z, tree.w};
+        if (valid < kT || w.sp.partial) {
+          const uint32_t tm[4] = {see.x, see.y, see.z, see.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int in = min(32, max(0, valid - 32 * c));
@@ -399,10 +442,9 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, con
           for (int j = 2; j < 32; j += 2)
             mx[c] = max3(mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
         }
-        float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-        if (top == -INFINITY) top = -1e30f;  // (only where nothing is finite)
-        if (t == 0) {
-          m = top;
+        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        if (first) {
+          m = fmaxf(top, -1e30f);  // (nothing seen yet: weights 0, no NaN)
           l = 0.f;
         } else if (__any_sync(0xffffffffu, mine && top > m + kLazy)) {
           // (rows without a query hold anything: they must not count)
@@ -421,7 +463,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, con
             tmem_st8(o_tmem + 8 * c, r);
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float sum[4] = {bad ? NAN : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t p[32];
@@ -442,7 +484,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, con
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[qt]);
     }
-  } while (w.next(segs));
+  } while ((step = w.next()));
   if (have) {
     if (!warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
     tc_fence_after();
@@ -472,10 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  const TreeSeg *segs = tree_at<TreeSeg>(a, a.L.segs);
   const TreeCta c = tree_at<TreeCta>(a, a.L.ctas)[blockIdx.x];
-  Walk w = {c.head, c.seg, c.tile, c.n_units, hdr.n_segs, {}, 0};
-  w.load(segs);
+  Walk w = {tree_at<TreeGroup>(a, a.L.groups), tree_at<TreeSpan>(a, a.L.spans), hdr.n_groups,
+            c.head, c.group, c.span, c.tile, c.n_units, {}, {}, 0};
+  w.g = w.groups[w.group];
+  w.load_span();
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&S.kv_full[s], 1);
@@ -487,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.p_full[q], 4);
       mbar_init(&S.pv_done[q], 1);
       mbar_init(&S.o_empty[q], 4);
+      mbar_init(&S.scanned[q], 4);
     }
     mbar_init(&S.mma_done, 1);
     S.abort_flag = 0;
@@ -501,11 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
   if (warp == kWarpTma) {
-    if ((tid & 31) == 0) producer(a, S, &tk, &tv, w, segs);
+    if ((tid & 31) == 0) producer(a, S, &tk, &tv, w);
   } else if (warp == kWarpMma) {
-    mma_issuer(a, S, tmem, w, segs);
+    mma_issuer(a, S, tmem, w);
   } else if (warp < 8) {
-    softmax(a, S, tmem, w, segs, warp >> 2);
+    softmax(a, S, tmem, w, warp >> 2);
   }
   __syncwarp();
   tc_fence_before();
