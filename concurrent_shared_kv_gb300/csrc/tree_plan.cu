@@ -23,7 +23,7 @@ struct TreeCost {
   int32_t tile1, tile2, span, group;
 };
 __host__ __device__ inline TreeCost tree_cost(int cols) {
-  return cols > 128 ? TreeCost{2, 3, 1, 4} : TreeCost{4, 4, 1, 1};
+  return cols > 128 ? TreeCost{2, 3, 3, 3} : TreeCost{4, 4, 1, 1};
 }
 
 struct TreePlanSmem {
@@ -453,6 +453,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       const int tiles = (last.len + TL - 1) / TL;
       pc.x = cta_of_weight(w, W, C);
       pc.y = cta_of_weight(w + last.w0 + tile_weight(cost, gr.n_cols, gr.n_spans == 1, tiles - 1), W, C) - pc.x + 1;
+      // tensor cores: up to 128 columns leave two records a CTA (tree_tc.cu)
+      if (a.L.cols > 128 && gr.n_cols <= 128) pc.y *= 2;
       rows = static_cast<int64_t>(pc.y) * gr.n_cols;
     }
     const int64_t at = block_scan(S, rows);
@@ -607,14 +609,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   for (int j = 0; j < n; ++j) {
     const float2 x2 = ml[j * n_cols];
     const float *src = o + static_cast<int64_t>(j) * n_cols * D;
-    const float w = ex2(x2.x - M);
+    const bool none = x2.x == -INFINITY;  // a record without tiles: no output either
+    const float w = none ? 0.f : ex2(x2.x - M);
     L += x2.y * w;
     float val[EPL];
     if constexpr (EPL == 4) {
-      const float4 y = *reinterpret_cast<const float4 *>(src);
+      const float4 y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(src);
       val[0] = y.x; val[1] = y.y; val[2] = y.z; val[3] = y.w;
     } else {
-      const float2 y = *reinterpret_cast<const float2 *>(src);
+      const float2 y = none ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(src);
       val[0] = y.x; val[1] = y.y;
     }
 #pragma unroll
@@ -779,7 +782,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   // spans of blocks times rows: a group has up to min(R, cols) rows
   L.max_map = parts * V * (R < L.cols ? R : L.cols);
   L.max_rots = Q * (V + 1);
-  L.max_rows = d.n_kv_heads * L.max_cols + static_cast<int64_t>(L.ctas_max) * L.cols;
+  L.max_rows = (d.n_kv_heads * L.max_cols + static_cast<int64_t>(L.ctas_max) * L.cols) * (tc ? 2 : 1);
   size_t at = 256;
   auto put = [&](size_t bytes) {
     const size_t o = at;

@@ -9,9 +9,14 @@
 // With a query per TMEM lane, a softmax thread owns its row: no exchange for
 // maxima and sums, and P goes back to the columns that S came from.
 //
-// Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 the TMA producer, 9 the MMA
-// issuer.  The issuer alternates the tiles - PV0(i-1), QK0(i), PV1(i-1),
-// QK1(i) - so that one tile's products run under the other's softmax.
+// The CTA runs two streams, each with its own S/P, O and four softmax warps:
+// with over 128 columns stream q is query tile q and both take every K/V
+// tile; with up to 128 there is one query tile and stream q takes every other
+// K/V tile (two records, like two CTAs).  The issuer alternates them - a
+// stream's PV of its tile before, then its next QK - so that one stream's
+// products run under the other's softmax.
+// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 the TMA producer, 9 the
+// MMA issuer.
 // Rotated queries carry scale * log2(e), so scores leave the MMA in log2
 // units; they are rounded to bf16 once, as P is: both leave an error of half a
 // bf16 step, that of the output itself.
@@ -41,9 +46,10 @@ struct TcSmem {
   alignas(1024) uint8_t q[2][kQTile];
   alignas(1024) uint8_t kv[kStages][kStage];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_empty[2], mma_done;
-  uint64_t scanned[2];   // partial tiles: the tokens with a value that is not finite are known
-  uint32_t bad[2][4];
+  uint64_t q_full[2], q_free, s_full[2], p_half[2], p_full[2], pv_done[2], o_empty[2], mma_done;
+  // partial tiles, by who scans them, alternating: the tokens with a value that is not finite are known
+  uint64_t scanned[2][2];
+  uint32_t bad[2][2][4];
   uint32_t tmem;
   int32_t abort_flag;
 };
@@ -135,6 +141,7 @@ struct Walk {
   int tiles;  // of this span that are the CTA's
   __device__ __forceinline__ void load_span() {
     sp = spans[g.span0 + span];
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(spans + g.span0 + span + 1));
     tiles = min((sp.len + kT - 1) / kT - tile, left);
   }
   // On to the next span: 0 at the end, 1 in the same group, 2 in another one.
@@ -194,89 +201,136 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w) 
   const uint32_t q0 = smem_u32(S.q[0]), kv0 = smem_u32(S.kv[0]);
   const uint64_t a_qk = smem_desc(q0, 16, 1024, kSw128), b_qk = smem_desc(kv0, 16, 1024, kSw128);
   const uint64_t b_pv = smem_desc(kv0, kBox, 1024, kSw128);
-  int i = 0;  // tiles whose QK is issued
-  // per query tile: PVs issued, groups whose PVs have begun, rotations used
-  int np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0};
-  // S of query tile qt from the K in stage s
-  auto qk = [&](int qt, int s) {
-    const uint64_t as = a_qk + ((qt * kQTile) >> 4), bs = b_qk + ((s * kStage) >> 4);
-    if (elect_one()) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
-        const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-        mma_bf16(tmem + qt * 128, as + o, bs + o, idesc_qk, k > 0);
-      }
-      mma_commit(&S.s_full[qt]);
-    }
-    __syncwarp();
-  };
-  // O of query tile qt (+)= P . V, V in ring entry n
-  auto pv = [&](int qt, int n, int ksteps, bool first) -> bool {
-    if (!warp_wait(S, a, &S.p_full[qt], np[qt] & 1)) return false;
-    if (!warp_wait(S, a, &S.kv_full[n % kStages], (n / kStages) & 1)) return false;
-    if (first) {
-      if (!warp_wait(S, a, &S.o_empty[qt], (no[qt] & 1) ^ 1)) return false;
-      ++no[qt];
-    }
+  // per stream: PVs issued, groups whose PVs have begun; rotations used
+  int np[2] = {0, 0}, no[2] = {0, 0}, nq = 0;
+  // per stream, the tile whose PV is to come: its V's ring entry (-1: none),
+  // its steps of 16 tokens, whether it is the stream's first of a group and
+  // the last use of the V
+  int pend[2] = {-1, -1}, pend_steps[2] = {0, 0};
+  bool pend_first[2] = {false, false}, pend_last[2] = {false, false}, first[2] = {true, true};
+  // O of stream q (+)= P . V.  Everything but P is waited for first: P is
+  // what the products wait for.
+  auto pv = [&](int q) -> bool {
+    const int n = pend[q], s = n % kStages, steps = pend_steps[q];
+    const bool begin = pend_first[q];
+    if (!warp_wait(S, a, &S.kv_full[s], (n / kStages) & 1)) return false;
+    if (begin && !warp_wait(S, a, &S.o_empty[q], (no[q]++ & 1) ^ 1)) return false;
+    const uint64_t bs = b_pv + ((s * kStage) >> 4);
+    const uint32_t d = tmem + 256 + q * 128, p = tmem + q * 128;
+    if (!warp_wait(S, a, &S.p_half[q], np[q] & 1)) return false;
     tc_fence_after();
-    const uint64_t bs = b_pv + (((n % kStages) * kStage) >> 4);
     if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)  // steps of 16 tokens
-        if (k < ksteps)
-          mma_bf16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + k * 8, bs + ((k * 2048) >> 4), idesc_pv,
-                      !(first && k == 0));
-      mma_commit(&S.pv_done[qt]);
+      for (int k = 0; k < 4; ++k)
+        if (k < steps) mma_bf16_ts(d, p + k * 8, bs + ((k * 2048) >> 4), idesc_pv, !(begin && k == 0));
     }
     __syncwarp();
-    ++np[qt];
+    if (!warp_wait(S, a, &S.p_full[q], np[q] & 1)) return false;
+    tc_fence_after();
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 4; k < 8; ++k)
+        if (k < steps) mma_bf16_ts(d, p + k * 8, bs + ((k * 2048) >> 4), idesc_pv, true);
+      mma_commit(&S.pv_done[q]);
+      if (pend_last[q]) mma_commit(&S.kv_empty[s]);
+    }
+    __syncwarp();
+    ++np[q];
+    pend[q] = -1;
     return true;
   };
-  auto release = [&](int s) {
-    if (elect_one()) mma_commit(&S.kv_empty[s]);
-    __syncwarp();
-  };
-  bool pend = false, pend_two = false, pend_first = false;  // the tile whose PVs are to come
-  int pend_steps = 0, step = 2;
+  int i = 0, step = 2;  // tiles so far; 2: a group starts
+  int turn = 0;         // the next tile's stream, where streams take turns
   bool go = true;
   do {
     const bool two = w.g.n_cols > 128;
+    if (step == 2) {  // the softmax warps wait for a group's last products
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (go && pend[q] >= 0) go = pv(q);
+      turn = 0;
+      first[0] = first[1] = true;
+    }
     for (int t = 0; go && t < w.tiles; ++t, ++i) {
-      const int nk = 2 * i, nv = 2 * i - 1, s = nk % kStages;
-      if (pend && !(go = pv(0, nv, pend_steps, pend_first))) break;
-      if (t == 0 && !(go = warp_wait(S, a, &S.q_full[0], nq[0]++ & 1))) break;
+      const int nk = 2 * i, s = nk % kStages, last = two ? 1 : turn;
       if (!(go = warp_wait(S, a, &S.kv_full[s], (nk / kStages) & 1))) break;
-      tc_fence_after();
-      qk(0, s);
-      if (pend && pend_two && !(go = pv(1, nv, pend_steps, pend_first))) break;
-      if (pend) release(nv % kStages);
-      if (two) {
-        if (t == 0 && !(go = warp_wait(S, a, &S.q_full[1], nq[1]++ & 1))) break;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (!go || (!two && turn != q)) continue;
+        if (pend[q] >= 0 && !(go = pv(q))) continue;
+        if (t == 0 && (!two || q == 0)) {  // both halves of the softmax warps write queries
+          if (!(go = warp_wait(S, a, &S.q_full[0], nq & 1) && warp_wait(S, a, &S.q_full[1], nq & 1))) continue;
+          ++nq;
+        }
         tc_fence_after();
-        qk(1, s);
+        const uint64_t as = a_qk + ((two ? q * kQTile : 0) >> 4), bs = b_qk + ((s * kStage) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
+            const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+            mma_bf16(tmem + q * 128, as + o, bs + o, idesc_qk, k > 0);
+          }
+          mma_commit(&S.s_full[q]);
+          if (q == last) {
+            mma_commit(&S.kv_empty[s]);
+            if (t == w.tiles - 1) mma_commit(&S.q_free);
+          }
+        }
+        __syncwarp();
+        pend[q] = nk + 1;
+        pend_steps[q] = (min(kT, w.sp.len - (w.tile + t) * kT) + 15) / 16;
+        pend_first[q] = first[q];
+        pend_last[q] = q == last;
+        first[q] = false;
       }
-      release(s);
-      pend = true;
-      pend_two = two;
-      pend_first = t == 0 && step == 2;
-      pend_steps = (min(kT, w.sp.len - (w.tile + t) * kT) + 15) / 16;
+      turn ^= 1;
     }
   } while (go && (step = w.next()));
-  if (go && pend) {
-    if (pv(0, 2 * i - 1, pend_steps, pend_first) && pend_two) pv(1, 2 * i - 1, pend_steps, pend_first);
-  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (go && pend[q] >= 0) go = pv(q);
   if (elect_one()) mma_commit(&S.mma_done);
   __syncwarp();
   mbar_wait(&S.mma_done, 0);
 }
 
+// Four of a query's eight 16-byte pieces (and their partners, 64 elements
+// further), rotated, scaled and rounded into the query tile.
+__device__ __forceinline__ void write_query(const uint4 *src, const float4 *rot, uint32_t to, int row, float scale,
+                                            int c0) {
+  uint4 u[4], v[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    u[c] = __ldg(src + c0 + c);
+    v[c] = __ldg(src + c0 + c + 8);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w}, y[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+    uint32_t p[4], r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 cs = __ldg(rot + 4 * (c0 + c) + j);  // (cos, sin) of two elements
+      const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
+      const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
+      p[j] = pack_bf16((x0 * cs.x - y0 * cs.y) * scale, (x1 * cs.z - y1 * cs.w) * scale);
+      r[j] = pack_bf16((y0 * cs.x + x0 * cs.y) * scale, (y1 * cs.z + x1 * cs.w) * scale);
+    }
+    const uint32_t o = ((c0 + c) ^ (row & 7)) << 4;
+    st_shared_v4(to + o, p[0], p[1], p[2], p[3]);
+    st_shared_v4(to + kBox + o, r[0], r[1], r[2], r[3]);
+  }
+}
+
 // One row's record: (m, l) and O, 32 bytes of every 8 d side by side for the
-// segment's columns, so that a warp's stores fill whole sectors.
+// group's columns, so that a warp's stores fill whole sectors.  A stream
+// without a tile leaves m = -inf and no O.
 __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem, int64_t rec, int n_cols, int col,
-                                             float m, float l) {
+                                             float m, float l, bool some) {
   float *dst = tree_at<float>(a, a.L.o) + rec * 128 + col * 8;
   const bool on = col < n_cols;
-  if (on) tree_at<float2>(a, a.L.ml)[rec + col] = make_float2(m, l);
+  if (on) tree_at<float2>(a, a.L.ml)[rec + col] = make_float2(some ? m : -INFINITY, some ? l : 0.f);
+  if (!some || col - static_cast<int>(threadIdx.x & 31) >= n_cols) return;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
@@ -293,101 +347,106 @@ __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem,
   }
 }
 
-__device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int qt) {
+// Packed fp32: two numbers an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int q) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
-  const int col = qt * 128 + row;  // the thread's column of a group
-  const uint32_t s_tmem = tmem + qt * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+  const uint32_t s_tmem = tmem + q * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t o_tmem = s_tmem + 256;
-  const uint32_t qrow = smem_u32(S.q[qt]) + row * 128;
-  int ns = 0;          // tiles of this query tile so far
-  int i = 0;           // tiles of the CTA so far
-  int np = 0;          // partial tiles of the CTA so far
+  int ns = 0;              // tiles of this stream so far
+  int i = 0;               // tiles of the CTA so far
+  int nspan = 0;           // spans of the CTA so far
+  int np0 = 0, np1 = 0;    // partial tiles scanned by each half of the warps so far
   float m = 0.f, l = 0.f;
-  // the record to come: that of the group before
-  bool have = false;
+  // the record to come: that of the group before (0 columns: none)
   int64_t rec = 0;
-  int rec_cols = 0;
+  int rec_cols = 0, rec_col = 0;
+  bool some = false;       // the stream had a tile of it
   TreeColumn tc = {};
   const uint4 *src = nullptr;
-  int step = 2;
+  int step = 2, turn = 0;
   do {
+    const bool two = w.g.n_cols > 128;
+    const int col = two ? q * 128 + row : row;               // the thread's column of the group
     const bool mine = col < w.g.n_cols;                      // a query in this row
-    const bool active = qt == 0 || w.g.n_cols > 128;         // a query in this tile
-    const bool warp_on = qt * 128 + quarter * 32 < w.g.n_cols;
+    const bool warp_on = col - lane < w.g.n_cols;
     if (mine && step == 2) {
       tc = tree_at<TreeColumn>(a, a.L.columns)[w.g.col0 + col];
       const int hq = tree_at<int32_t>(a, a.L.heads)[w.head * (a.n_q_heads / a.n_kv_heads) + tc.head];
       src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                             (static_cast<int64_t>(tc.node) * a.n_q_heads + hq) * 128);
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(src + 8));
     }
     // the tokens the column sees: all, a node's ancestors and itself, or none
     uint4 see = make_uint4(0, 0, 0, 0);
+    int v = -1;
     if (mine) {
-      const int v = w.sp.row < 0 ? tree_at<int16_t>(a, a.L.map)[w.sp.map + tc.row]
-                    : tc.node / a.max_nodes == w.sp.row ? a.n_view : -1;
-      if (v >= 0) {
-        see = w.sp.row < 0 ? make_uint4(~0u, ~0u, ~0u, ~0u) : tree_at<uint4>(a, a.L.mask)[tc.node];
-        const float4 *rot = tree_at<float4>(a, a.L.rot) + (static_cast<int64_t>(tc.rot) + v * tc.n_nodes) * 32;
-        // Q~ of the span before is free: its last scores are there.
-#pragma unroll 2
-        for (int c = 0; c < 8; ++c) {  // elements 8c .. 8c+7 and their partners, 64 further
-          const uint4 u = __ldg(src + c), u2 = __ldg(src + c + 8);
-          const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {u2.x, u2.y, u2.z, u2.w};
-          uint32_t p[4], r[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 cs = __ldg(rot + 4 * c + j);  // (cos, sin) of two elements
-            const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
-            const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
-            p[j] = pack_bf16((x0 * cs.x - y0 * cs.y) * a.scale_log2, (x1 * cs.z - y1 * cs.w) * a.scale_log2);
-            r[j] = pack_bf16((y0 * cs.x + x0 * cs.y) * a.scale_log2, (y1 * cs.z + x1 * cs.w) * a.scale_log2);
-          }
-          const uint32_t o = (c ^ (row & 7)) << 4;
-          st_shared_v4(qrow + o, p[0], p[1], p[2], p[3]);
-          st_shared_v4(qrow + kBox + o, r[0], r[1], r[2], r[3]);
-        }
-        fence_proxy_async_smem();
-      }
+      v = w.sp.row < 0 ? tree_at<int16_t>(a, a.L.map)[w.sp.map + tc.row]
+          : static_cast<uint32_t>(tc.node - w.sp.row * a.max_nodes) < static_cast<uint32_t>(a.max_nodes) ? a.n_view : -1;
+      if (v >= 0) see = w.sp.row < 0 ? make_uint4(~0u, ~0u, ~0u, ~0u) : tree_at<uint4>(a, a.L.mask)[tc.node];
+    }
+    // Q~ of the span before is free once its last scores are there
+    if (nspan > 0 && !warp_wait(S, a, &S.q_free, (nspan - 1) & 1)) return;
+    if (v >= 0) {
+      const float4 *rot = tree_at<float4>(a, a.L.rot) + (static_cast<int64_t>(tc.rot) + v * tc.n_nodes) * 32;
+      // two query tiles: each half of the warps its own; one: half of d each
+      const uint32_t to = smem_u32(S.q[two ? q : 0]) + row * 128;
+      write_query(src, rot, to, row, a.scale_log2, 4 * q);
+      if (two) write_query(src, rot, to, row, a.scale_log2, 4 - 4 * q);
+      fence_proxy_async_smem();
     }
     __syncwarp();
-    if (active && lane == 0) mbar_arrive(&S.q_full[qt]);
+    if (lane == 0) mbar_arrive(&S.q_full[q]);
     if (step == 2) {
-      if (have) {
-        if (!warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
+      if (rec_cols > 0) {
+        if (some && !warp_wait(S, a, &S.pv_done[q], (ns - 1) & 1)) return;
         tc_fence_after();
-        store_record(a, o_tmem, rec, rec_cols, col, m, l);
+        store_record(a, o_tmem, rec, rec_cols, rec_col, m, l, some);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.o_empty[qt]);
+        if (some && lane == 0) mbar_arrive(&S.o_empty[q]);
       }
-      have = active;
       const int64_t k = static_cast<int64_t>(w.head) * w.n_groups + w.group;
       rec_cols = w.g.n_cols;
-      rec = tree_at<int32_t>(a, a.L.piece_row)[k] +
-            static_cast<int64_t>(blockIdx.x - tree_at<int2>(a, a.L.piece_cta)[k].x) * rec_cols;
+      rec_col = col;
+      // one record a CTA, or one a stream
+      const int nth = static_cast<int>(blockIdx.x) - tree_at<int2>(a, a.L.piece_cta)[k].x;
+      rec = tree_at<int32_t>(a, a.L.piece_row)[k] + static_cast<int64_t>(two ? nth : 2 * nth + q) * rec_cols;
+      some = false;
+      turn = 0;
     }
-    if (!active) {
-      i += w.tiles;
-      np += w.sp.partial ? w.tiles : 0;
-      continue;
-    }
-    for (int t = 0; t < w.tiles; ++t, ++i, ++ns) {
+    ++nspan;
+    for (int t = 0; t < w.tiles; ++t, ++i, turn ^= 1) {
+      const int owner = two ? 0 : turn;  // who looks after the V tile
+      if (!two && turn != q) {
+        if (w.sp.partial) ++(owner ? np1 : np0);
+        continue;
+      }
       const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
-      const bool first = step == 2 && t == 0;
-      if (!warp_wait(S, a, &S.s_full[qt], ns & 1)) return;
+      if (!warp_wait(S, a, &S.s_full[q], ns & 1)) return;
       uint32_t bad = 0;
-      if (w.sp.partial || (qt == 0 && (valid & 15))) {
-        const int nv = 2 * i + 1;
-        if (qt == 0) {
+      if (w.sp.partial || (q == owner && (valid & 15))) {
+        const int nv = 2 * i + 1, np = owner ? np1 : np0, par = np & 1;
+        if (q == owner) {
           // 0 * NaN would poison a sum.  V rows past the span, up to the end
           // of the last step of 16 tokens, may hold anything: cleared.  In a
           // tile that not every column sees, so are tokens with a value that
           // is not finite: the columns that see them get a NaN through l.
           if (!warp_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1)) return;
           const uint32_t at = smem_u32(S.kv[nv % kStages]) + row * 128;
-          bool clear = row >= valid && row < ((valid + 15) & ~15);
+          const bool clear = row >= valid && row < ((valid + 15) & ~15);
           bool odd = false;
           if (w.sp.partial && row < valid)
             for (int c = 0; c < 16; ++c) {
@@ -405,16 +464,16 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
           if (w.sp.partial) {
             const uint32_t bits = __ballot_sync(0xffffffffu, odd);
             if (lane == 0) {
-              S.bad[np & 1][quarter] = bits;
-              mbar_arrive(&S.scanned[np & 1]);
+              S.bad[owner][par][quarter] = bits;
+              mbar_arrive(&S.scanned[owner][par]);
             }
           }
         }
         if (w.sp.partial) {
-          if (!warp_wait(S, a, &S.scanned[np & 1], (np >> 1) & 1)) return;
-          const uint32_t *b = S.bad[np & 1];
+          if (!warp_wait(S, a, &S.scanned[owner][par], (np >> 1) & 1)) return;
+          const uint32_t *b = S.bad[owner][par];
           bad = (b[0] & see.x) | (b[1] & see.y) | (b[2] & see.z) | (b[3] & see.w);
-          ++np;
+          ++(owner ? np1 : np0);
         }
       }
       if (warp_on) {
@@ -443,7 +502,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
             mx[c] = max3(mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
         }
         const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-        if (first) {
+        if (!some) {
           m = fmaxf(top, -1e30f);  // (nothing seen yet: weights 0, no NaN)
           l = 0.f;
         } else if (__any_sync(0xffffffffu, mine && top > m + kLazy)) {
@@ -451,7 +510,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
           const float to = top > m + kLazy ? top : m, al = ex2(m - to);
           m = to;
           l *= al;
-          if (!warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
+          if (!warp_wait(S, a, &S.pv_done[q], (ns - 1) & 1)) return;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 16; ++c) {  // (rare: few registers beside S matter more than speed)
@@ -463,33 +522,45 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
             tmem_st8(o_tmem + 8 * c, r);
           }
         }
-        float sum[4] = {bad ? NAN : 0.f, 0.f, 0.f, 0.f};
+        const uint64_t neg = pack2(-m, -m);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 2; ++c) {  // P in two halves: PV starts on the first
           uint32_t p[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float p0 = ex2(__uint_as_float(s[2 * c + j / 16][2 * j % 32]) - m);
-            const float p1 = ex2(__uint_as_float(s[2 * c + j / 16][2 * j % 32 + 1]) - m);
-            sum[2 * (j & 1)] += p0;
-            sum[2 * (j & 1) + 1] += p1;
+            float p0, p1;
+            unpack2(add2(pack2(__uint_as_float(s[2 * c + j / 16][2 * j % 32]),
+                               __uint_as_float(s[2 * c + j / 16][2 * j % 32 + 1])), neg), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
             p[j] = pack_bf16(p0, p1);
           }
           tmem_st32(s_tmem + 32 * c, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c == 0 ? &S.p_half[q] : &S.p_full[q]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
+        float x[4];
+        unpack2(sum[0], x[0], x[1]);
+        unpack2(sum[1], x[2], x[3]);
+        l += ((x[0] + x[1]) + (x[2] + x[3])) + (bad ? NAN : 0.f);
+      } else {
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.p_half[q]);
+          mbar_arrive(&S.p_full[q]);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full[qt]);
+      some = true;
+      ++ns;
     }
   } while ((step = w.next()));
-  if (have) {
-    if (!warp_wait(S, a, &S.pv_done[qt], (ns - 1) & 1)) return;
-    tc_fence_after();
-    store_record(a, o_tmem, rec, rec_cols, col, m, l);
-  }
+  if (some && !warp_wait(S, a, &S.pv_done[q], (ns - 1) & 1)) return;
+  tc_fence_after();
+  store_record(a, o_tmem, rec, rec_cols, rec_col, m, l, some);
 }
 
 // A programmatic dependent of the append launch, which itself starts its
@@ -526,12 +597,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&S.q_full[q], 4);
+      mbar_init(&S.p_half[q], 4);
       mbar_init(&S.s_full[q], 1);
       mbar_init(&S.p_full[q], 4);
       mbar_init(&S.pv_done[q], 1);
       mbar_init(&S.o_empty[q], 4);
-      mbar_init(&S.scanned[q], 4);
+      mbar_init(&S.scanned[q][0], 4);
+      mbar_init(&S.scanned[q][1], 4);
     }
+    mbar_init(&S.q_free, 1);
     mbar_init(&S.mma_done, 1);
     S.abort_flag = 0;
     fence_mbar_init();
