@@ -26,7 +26,8 @@
 //              side, then the next 8: a thread that owns a column and a warp
 //              that owns a row both move whole sectors.
 // The rotation of a (row, view entry, node) is the same for every layer and q
-// head: the plan holds its cos and sin, fp32, head_dim / 2 pairs each.
+// head: the plan holds its cos and sin, fp32, head_dim / 2 pairs each (in the
+// order of rot_at).
 // tree_merge_kernel joins the records of every (row, node, q head).
 #pragma once
 
@@ -132,6 +133,12 @@ cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaS
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
+// Where a table row keeps element e's (cos, sin), e < half = head_dim / 2:
+// elements 8c + 2j and 8c + 2j + 1 side by side, c running before j, so that
+// the lanes that each turn 8 neighbouring elements read neighbouring memory.
+__host__ __device__ __forceinline__ int rot_at(int e, int half) {
+  return ((((e & 7) >> 1) * (half >> 3) + (e >> 3)) << 1) | (e & 1);
+}
 // Element d of column col in a record of n_cols columns that starts at row rec.
 __device__ __forceinline__ int64_t record_at(int64_t rec, int n_cols, int col, int d, int D) {
   return rec * D + static_cast<int64_t>(d >> 3) * n_cols * 8 + col * 8 + (d & 7);

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   // as many CTAs as leave each at least one unit of every group it is inside
   const int64_t most = W / (cost.group + cost.span + cost.tile2);
-  const int C = static_cast<int>(most < a.L.ctas_max ? most : a.L.ctas_max);
+  const int C = W == 0 ? 0 : static_cast<int>(most < 1 ? 1 : most < a.L.ctas_max ? most : a.L.ctas_max);
   // every CTA's first unit
   TreeCta *ctas = tree_at<TreeCta>(a, a.L.ctas);
   for (int c = tid; c <= C && C > 0; c += kPlanThreads) {
@@ -513,7 +513,10 @@ __global__ void __launch_bounds__(256) tree_tables_kernel(const __grid_constant_
     for (int i = warp; i < n; i += 8) {
       const int64_t rel = root + tree_at<int32_t>(a, a.L.depth)[static_cast<int64_t>(r) * T + i];
       float2 *to = tree_at<float2>(a, a.L.rot) + (rot0[r] + static_cast<int64_t>(v) * n + i) * half;
-      for (int j = lane; j < half; j += 32) rope_cos_sin_exact(rel, a.phase[j], &to[j].x, &to[j].y);
+      for (int j = lane; j < half; j += 32) {
+        float2 &x = to[rot_at(j, half)];
+        rope_cos_sin_exact(rel, a.phase[j], &x.x, &x.y);
+      }
     }
   }
 }
@@ -547,7 +550,8 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
   const int64_t to = (h * a.capacity + slot) * D;
   const float ks = kFp8 ? a.k_scale[h] : 1.f, vs = kFp8 ? a.v_scale[h] : 1.f;
   for (int j = lane; j < half; j += 32) {
-    const float c = rot[j].x, s = rot[j].y;
+    const float2 cs = rot[rot_at(j, half)];
+    const float c = cs.x, s = cs.y;
     const float x0 = to_f32<T>(kn[j]), x1 = to_f32<T>(kn[j + half]);
     const float y0 = __fmaf_rn(x0, c, -__fmul_rn(x1, s)), y1 = __fmaf_rn(x1, c, __fmul_rn(x0, s));
     if constexpr (kFp8) {

@@ -9,14 +9,16 @@
 // With a query per TMEM lane, a softmax thread owns its row: no exchange for
 // maxima and sums, and P goes back to the columns that S came from.
 //
-// The CTA runs two streams, each with its own S/P, O and four softmax warps:
-// with over 128 columns stream q is query tile q and both take every K/V
-// tile; with up to 128 there is one query tile and stream q takes every other
-// K/V tile (two records, like two CTAs).  The issuer alternates them - a
-// stream's PV of its tile before, then its next QK - so that one stream's
-// products run under the other's softmax.
-// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 the TMA producer, 9 the
-// MMA issuer.
+// The CTA runs two streams, each with its own S/P, O, issuing warp and eight
+// softmax warps: with over 128 columns stream q is query tile q and both take
+// every K/V tile; with up to 128 there is one query tile and stream q takes
+// every other K/V tile (two records, like two CTAs).  One stream's products
+// run under the other's softmax; within a stream QK, softmax and PV follow one
+// another (S and P share their columns: TMEM holds no third score tile), so
+// what counts is the length of that chain.  Two threads share a row, 64 tokens
+// each, and exchange their maxima.
+// Warps: 0-7 softmax of stream 0 (0-3 tokens 0-63, 4-7 the others), 8-15 of
+// stream 1, 16 the TMA producer, 17 and 18 the issuers.
 // Rotated queries carry scale * log2(e), so scores leave the MMA in log2
 // units; they are rounded to bf16 once, as P is: both leave an error of half a
 // bf16 step, that of the output itself.
@@ -32,8 +34,8 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kThreads = 608;
+constexpr int kWarpTma = 16, kWarpMma = 17;  // and 18: an issuer a stream
 constexpr int kT = 128;                      // tokens per tile
 constexpr uint32_t kBox = 128 * 128;         // 128 rows of 128 bytes, 128-byte swizzled
 constexpr uint32_t kQTile = 2 * kBox;        // a query tile: d 0-63, d 64-127
@@ -46,14 +48,15 @@ struct TcSmem {
   alignas(1024) uint8_t q[2][kQTile];
   alignas(1024) uint8_t kv[kStages][kStage];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full[2], q_free, s_full[2], p_half[2], p_full[2], pv_done[2], o_empty[2], mma_done;
-  // partial tiles, by who scans them, alternating: the tokens with a value that is not finite are known
+  uint64_t q_full[2], q_free, s_full[2], p_full[2], pv_done[2], o_empty[2], order, mma_done;
+  // tidied V tiles, by the stream that does it, alternating; the tokens with a value that is not finite
   uint64_t scanned[2][2];
-  uint32_t bad[2][2][4];
+  uint32_t bad[2][2][2][4];
+  float red[2][2][128];  // per stream: the maxima of a row's halves (at a record: sums)
   uint32_t tmem;
   int32_t abort_flag;
 };
-static_assert(sizeof(TcSmem) + 1024 <= 232448, "shared memory of one CTA per SM");
+static_assert(sizeof(TcSmem) <= 232448, "shared memory of one CTA per SM");
 
 __device__ __forceinline__ bool aborted(TcSmem &S) {
   return *reinterpret_cast<volatile int32_t *>(&S.abort_flag) != 0;
@@ -77,6 +80,22 @@ __device__ __forceinline__ bool wait_or_abort(TcSmem &S, const TreeArgs &a, uint
 // follows are warp-wide TMEM accesses.
 __device__ __forceinline__ bool warp_wait(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_or_abort(S, a, bar, parity));
+}
+// The same for the softmax warps: suspended while they wait.  (Sixteen warps
+// that poll take the issue slots of those that compute.)
+__device__ __forceinline__ void idle_wait(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
+  if (!mbar_try(bar, parity)) {
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+      if (aborted(S)) break;
+      if (clock64() - t0 > kWaitLimit) {
+        *reinterpret_cast<volatile int32_t *>(&S.abort_flag) = 1;
+        flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_TIMEOUT);
+        break;
+      }
+    }
+  }
+  __syncwarp();
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulator.
@@ -192,149 +211,181 @@ __device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, co
   for (int j = n > kStages ? n - kStages : 0; j < n; ++j) mbar_wait(&S.kv_full[j % kStages], (j / kStages) & 1);
 }
 
-// The whole warp walks and waits; one elected lane issues.  (Descriptors then
-// stay in uniform registers: issued from a branch of one lane, 8 MMAs took
-// 1200 clocks instead of the 512 the tensor cores need for them, and 4 x 64
-// nodes on a 16K history 225 us.)
-__device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w) {
+// One stream's products.  The whole warp walks and waits; one elected lane
+// issues.  (Descriptors then stay in uniform registers: issued from a branch
+// of one lane, 8 MMAs took 1200 clocks instead of the 512 the tensor cores
+// need for them.  Even so a tile's waits and 16 MMAs keep a warp busy for
+// 1700 clocks, which is why each stream has its own.)
+__device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int q) {
   constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0), idesc_pv = idesc_bf16(128, 128, 0, 1);
   const uint32_t q0 = smem_u32(S.q[0]), kv0 = smem_u32(S.kv[0]);
   const uint64_t a_qk = smem_desc(q0, 16, 1024, kSw128), b_qk = smem_desc(kv0, 16, 1024, kSw128);
   const uint64_t b_pv = smem_desc(kv0, kBox, 1024, kSw128);
-  // per stream: PVs issued, groups whose PVs have begun; rotations used
-  int np[2] = {0, 0}, no[2] = {0, 0}, nq = 0;
-  // per stream, the tile whose PV is to come: its V's ring entry (-1: none),
-  // its steps of 16 tokens, whether it is the stream's first of a group and
-  // the last use of the V
-  int pend[2] = {-1, -1}, pend_steps[2] = {0, 0};
-  bool pend_first[2] = {false, false}, pend_last[2] = {false, false}, first[2] = {true, true};
-  // O of stream q (+)= P . V.  Everything but P is waited for first: P is
-  // what the products wait for.
-  auto pv = [&](int q) -> bool {
-    const int n = pend[q], s = n % kStages, steps = pend_steps[q];
-    const bool begin = pend_first[q];
-    if (!warp_wait(S, a, &S.kv_full[s], (n / kStages) & 1)) return false;
-    if (begin && !warp_wait(S, a, &S.o_empty[q], (no[q]++ & 1) ^ 1)) return false;
+  const uint32_t s_tmem = tmem + q * 128, o_tmem = s_tmem + 256;
+  int np = 0, no = 0, nspan = 0;  // PVs issued, groups whose PVs have begun, spans
+  // the tile whose PV is to come: its V's ring entry (-1: none), its steps of
+  // 16 tokens, whether it is the stream's first of a group
+  int pend = -1, pend_steps = 0;
+  bool pend_first = false, pend_two = false, first = true;
+  // Everything but P is waited for first: P is what the products wait for.
+  auto pv_ready = [&]() -> bool {
+    const int s = pend % kStages;
+    return warp_wait(S, a, &S.kv_full[s], (pend / kStages) & 1) &&
+           (!pend_first || warp_wait(S, a, &S.o_empty[q], (no++ & 1) ^ 1)) &&
+           warp_wait(S, a, &S.p_full[q], np & 1);
+  };
+  auto pv = [&]() {  // by the elected lane
+    const int s = pend % kStages;
     const uint64_t bs = b_pv + ((s * kStage) >> 4);
-    const uint32_t d = tmem + 256 + q * 128, p = tmem + q * 128;
-    if (!warp_wait(S, a, &S.p_half[q], np[q] & 1)) return false;
-    tc_fence_after();
-    if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < steps) mma_bf16_ts(d, p + k * 8, bs + ((k * 2048) >> 4), idesc_pv, !(begin && k == 0));
-    }
-    __syncwarp();
-    if (!warp_wait(S, a, &S.p_full[q], np[q] & 1)) return false;
+    for (int k = 0; k < 8; ++k)
+      if (k < pend_steps)
+        mma_bf16_ts(o_tmem, s_tmem + k * 8, bs + ((k * 2048) >> 4), idesc_pv, !(pend_first && k == 0));
+    mma_commit(&S.pv_done[q]);
+    mma_commit(&S.kv_empty[s]);
+    if (!pend_two) mma_commit(&S.kv_empty[s]);  // (for the other stream, which does not use it)
+  };
+  // The products that end a group, outside the order of the others.
+  auto flush = [&]() -> bool {
+    if (!pv_ready()) return false;
     tc_fence_after();
-    if (elect_one()) {
-#pragma unroll
-      for (int k = 4; k < 8; ++k)
-        if (k < steps) mma_bf16_ts(d, p + k * 8, bs + ((k * 2048) >> 4), idesc_pv, true);
-      mma_commit(&S.pv_done[q]);
-      if (pend_last[q]) mma_commit(&S.kv_empty[s]);
-    }
+    if (elect_one()) pv();
     __syncwarp();
-    ++np[q];
-    pend[q] = -1;
+    ++np;
+    pend = -1;
     return true;
+  };
+  // The span's queries; one query tile is written by all softmax warps.
+  auto queries = [&](bool two) -> bool {
+    return ((two && q == 1) || warp_wait(S, a, &S.q_full[0], nspan & 1)) &&
+           ((two && q == 0) || warp_wait(S, a, &S.q_full[1], nspan & 1));
   };
   int i = 0, step = 2;  // tiles so far; 2: a group starts
   int turn = 0;         // the next tile's stream, where streams take turns
+  int turns = 0;        // turns at the tensor cores so far, of both streams
   bool go = true;
   do {
     const bool two = w.g.n_cols > 128;
     if (step == 2) {  // the softmax warps wait for a group's last products
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        if (go && pend[q] >= 0) go = pv(q);
+      if (pend >= 0 && !(go = flush())) break;
       turn = 0;
-      first[0] = first[1] = true;
+      first = true;
     }
-    for (int t = 0; go && t < w.tiles; ++t, ++i) {
-      const int nk = 2 * i, s = nk % kStages, last = two ? 1 : turn;
+    bool turned = false;  // this span's queries are there
+    for (int t = 0; t < w.tiles; ++t, ++i, turn ^= 1, turns += two ? 2 : 1) {
+      if (!two && turn != q) continue;
+      const int nk = 2 * i, s = nk % kStages, mine = turns + (two ? q : 0);
       if (!(go = warp_wait(S, a, &S.kv_full[s], (nk / kStages) & 1))) break;
+      // (a new span's queries come after the last P, so their wait is last)
+      // One stream's PV and QK go out together, the streams in turn: mixed,
+      // both would wait for both, and their softmaxes would run at the same
+      // time, the tensor cores idle.
+      if (mine > 0 && !(go = warp_wait(S, a, &S.order, (mine - 1) & 1))) break;
+      if (pend >= 0 && !(go = pv_ready())) break;
+      if (!turned && !(go = queries(two))) break;
+      turned = true;
+      tc_fence_after();
+      const uint64_t as = a_qk + ((two ? q * kQTile : 0) >> 4), bs = b_qk + ((s * kStage) >> 4);
+      if (elect_one()) {
+        if (pend >= 0) pv();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (!go || (!two && turn != q)) continue;
-        if (pend[q] >= 0 && !(go = pv(q))) continue;
-        if (t == 0 && (!two || q == 0)) {  // both halves of the softmax warps write queries
-          if (!(go = warp_wait(S, a, &S.q_full[0], nq & 1) && warp_wait(S, a, &S.q_full[1], nq & 1))) continue;
-          ++nq;
+        for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
+          const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+          mma_bf16(s_tmem, as + o, bs + o, idesc_qk, k > 0);
+          if (k == 5) mbar_arrive(&S.order);  // (the next turn's first MMA is two MMAs away)
         }
-        tc_fence_after();
-        const uint64_t as = a_qk + ((two ? q * kQTile : 0) >> 4), bs = b_qk + ((s * kStage) >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
-            const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-            mma_bf16(tmem + q * 128, as + o, bs + o, idesc_qk, k > 0);
-          }
-          mma_commit(&S.s_full[q]);
-          if (q == last) {
-            mma_commit(&S.kv_empty[s]);
-            if (t == w.tiles - 1) mma_commit(&S.q_free);
-          }
-        }
-        __syncwarp();
-        pend[q] = nk + 1;
-        pend_steps[q] = (min(kT, w.sp.len - (w.tile + t) * kT) + 15) / 16;
-        pend_first[q] = first[q];
-        pend_last[q] = q == last;
-        first[q] = false;
+        mma_commit(&S.s_full[q]);
+        mma_commit(&S.kv_empty[s]);
+        if (!two) mma_commit(&S.kv_empty[s]);
       }
-      turn ^= 1;
+      __syncwarp();
+      if (pend >= 0) ++np;
+      pend = nk + 1;
+      pend_steps = (min(kT, w.sp.len - (w.tile + t) * kT) + 15) / 16;
+      pend_first = first;
+      pend_two = two;
+      first = false;
     }
-  } while (go && (step = w.next()));
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    if (go && pend[q] >= 0) go = pv(q);
+    // (also without a tile: the issuer must not run ahead of the queries)
+    if (!go || (!turned && !(go = queries(two)))) break;
+    if (elect_one()) mma_commit(&S.q_free);
+    __syncwarp();
+    ++nspan;
+  } while ((step = w.next()));
+  if (go && pend >= 0) flush();
   if (elect_one()) mma_commit(&S.mma_done);
   __syncwarp();
   mbar_wait(&S.mma_done, 0);
 }
 
-// Four of a query's eight 16-byte pieces (and their partners, 64 elements
-// further), rotated, scaled and rounded into the query tile.
-__device__ __forceinline__ void write_query(const uint4 *src, const float4 *rot, uint32_t to, int row, float scale,
-                                            int c0) {
-  uint4 u[4], v[4];
+// N queries of a warp's 32 (a row each, from `first`), rotated, scaled and
+// rounded into the query tile at `to`.  Eight lanes take a query, each 8
+// elements and their partners 64 further: every load of a query or of a
+// rotation is then one line of memory.  (A thread a query touched 32 lines a
+// load and took 8000 clocks for 256 queries.)  src, rot: the query and the
+// rotation's table row of this lane's own query, rot < 0: it does not see the
+// span, and its row of the tile may hold anything.
+template <int N>
+__device__ __forceinline__ void write_queries(const __nv_bfloat16 *q, const float4 *table, int src, int rot, uint32_t to,
+                                              float scale, int first, int lane) {
+  const int c = lane & 7;
+  // (rows that see nothing read row 0: loads without branches are all under
+  // way before the first is needed, and one trip to L2 costs a thousand
+  // clocks or more)
+  uint4 u[N / 4], v[N / 4];
+  int turn[N / 4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    u[c] = __ldg(src + c0 + c);
-    v[c] = __ldg(src + c0 + c + 8);
+  for (int i = 0; i < N / 4; ++i) {
+    const int at = first + 4 * i + (lane >> 3);
+    const int row = __shfl_sync(0xffffffffu, src, at);
+    turn[i] = max(0, __shfl_sync(0xffffffffu, rot, at));
+    const uint4 *x = reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(row) * 128);
+    u[i] = __ldg(x + c);
+    v[i] = __ldg(x + c + 8);
   }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w}, y[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-    uint32_t p[4], r[4];
+  for (int i0 = 0; i0 < N / 4; i0 += 2) {
+    float4 cs[2][4];  // (cos, sin) of elements 8c + 2j and 8c + 2j + 1
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 cs = __ldg(rot + 4 * (c0 + c) + j);  // (cos, sin) of two elements
-      const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
-      const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
-      p[j] = pack_bf16((x0 * cs.x - y0 * cs.y) * scale, (x1 * cs.z - y1 * cs.w) * scale);
-      r[j] = pack_bf16((y0 * cs.x + x0 * cs.y) * scale, (y1 * cs.z + x1 * cs.w) * scale);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cs[i][j] = __ldg(table + static_cast<int64_t>(turn[i0 + i]) * 32 + 8 * j + c);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 a = u[i0 + i], b = v[i0 + i];
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+      uint32_t p[4], r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 w = cs[i][j];
+        const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
+        const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
+        p[j] = pack_bf16((x0 * w.x - y0 * w.y) * scale, (x1 * w.z - y1 * w.w) * scale);
+        r[j] = pack_bf16((y0 * w.x + x0 * w.y) * scale, (y1 * w.z + x1 * w.w) * scale);
+      }
+      const int at = first + 4 * (i0 + i) + (lane >> 3);
+      const uint32_t o = to + at * 128 + ((c ^ (at & 7)) << 4);
+      st_shared_v4(o, p[0], p[1], p[2], p[3]);
+      st_shared_v4(o + kBox, r[0], r[1], r[2], r[3]);
     }
-    const uint32_t o = ((c0 + c) ^ (row & 7)) << 4;
-    st_shared_v4(to + o, p[0], p[1], p[2], p[3]);
-    st_shared_v4(to + kBox + o, r[0], r[1], r[2], r[3]);
   }
 }
 
-// One row's record: (m, l) and O, 32 bytes of every 8 d side by side for the
-// group's columns, so that a warp's stores fill whole sectors.  A stream
-// without a tile leaves m = -inf and no O.
+// The two warps that share rows (barriers 1 .. 8).
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+// Half of one row's record: 64 of O's columns, 32 bytes of every 8 d side by
+// side for the group's columns, so that a warp's stores fill whole sectors.
 __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem, int64_t rec, int n_cols, int col,
-                                             float m, float l, bool some) {
-  float *dst = tree_at<float>(a, a.L.o) + rec * 128 + col * 8;
+                                             int half) {
+  float *dst = tree_at<float>(a, a.L.o) + rec * 128 + col * 8 + static_cast<int64_t>(half) * 8 * n_cols * 8;
   const bool on = col < n_cols;
-  if (on) tree_at<float2>(a, a.L.ml)[rec + col] = make_float2(some ? m : -INFINITY, some ? l : 0.f);
-  if (!some || col - static_cast<int>(threadIdx.x & 31) >= n_cols) return;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 2; ++c) {
     uint32_t r[32];
-    tmem_ld32(o_tmem + 32 * c, r);
+    tmem_ld32(o_tmem + 64 * half + 32 * c, r);
     tmem_wait_ld();
     if (on) {
 #pragma unroll
@@ -362,21 +413,42 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The softmax of a stream.  Its waits give up together (abort_flag), and the
+// code then runs on to its end without waiting, on whatever the tiles hold:
+// the named barriers in it stay matched.
 __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int q) {
-  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = (threadIdx.x >> 7) & 1;
+  const int row = quarter * 32 + lane, pair = 1 + q * 4 + quarter;
   const uint32_t s_tmem = tmem + q * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t o_tmem = s_tmem + 256;
   int ns = 0;              // tiles of this stream so far
   int i = 0;               // tiles of the CTA so far
   int nspan = 0;           // spans of the CTA so far
-  int np0 = 0, np1 = 0;    // partial tiles scanned by each half of the warps so far
-  float m = 0.f, l = 0.f;
+  int np0 = 0, np1 = 0;    // tiles tidied by each stream so far
+  float m = 0.f, l = 0.f;  // the row's maximum; this half's sum
   // the record to come: that of the group before (0 columns: none)
   int64_t rec = 0;
   int rec_cols = 0, rec_col = 0;
   bool some = false;       // the stream had a tile of it
   TreeColumn tc = {};
-  const uint4 *src = nullptr;
+  int src = 0;             // the row's query (row 0 where there is none)
+  auto record = [&]() {
+    const bool on = rec_col - lane < rec_cols;  // (the same for the pair's warps)
+    if (some) idle_wait(S, a, &S.pv_done[q], (ns - 1) & 1);
+    if (on) {
+      S.red[q][half][row] = l;
+      pair_sync(pair);
+      if (half == 0 && rec_col < rec_cols)  // a stream without a tile leaves m = -inf and no O
+        tree_at<float2>(a, a.L.ml)[rec + rec_col] =
+            some ? make_float2(m, l + S.red[q][1][row]) : make_float2(-INFINITY, 0.f);
+      pair_sync(pair);
+      tc_fence_after();
+      if (some) store_record(a, o_tmem, rec, rec_cols, rec_col, half);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (some && lane == 0) mbar_arrive(&S.o_empty[q]);
+  };
   int step = 2, turn = 0;
   do {
     const bool two = w.g.n_cols > 128;
@@ -385,39 +457,34 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
     const bool warp_on = col - lane < w.g.n_cols;
     if (mine && step == 2) {
       tc = tree_at<TreeColumn>(a, a.L.columns)[w.g.col0 + col];
-      const int hq = tree_at<int32_t>(a, a.L.heads)[w.head * (a.n_q_heads / a.n_kv_heads) + tc.head];
-      src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                            (static_cast<int64_t>(tc.node) * a.n_q_heads + hq) * 128);
+      src = tc.node * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[w.head * (a.n_q_heads / a.n_kv_heads) + tc.head];
     }
     // the tokens the column sees: all, a node's ancestors and itself, or none
-    uint4 see = make_uint4(0, 0, 0, 0);
+    uint2 see = make_uint2(0, 0);
     int v = -1;
     if (mine) {
       v = w.sp.row < 0 ? tree_at<int16_t>(a, a.L.map)[w.sp.map + tc.row]
           : static_cast<uint32_t>(tc.node - w.sp.row * a.max_nodes) < static_cast<uint32_t>(a.max_nodes) ? a.n_view : -1;
-      if (v >= 0) see = w.sp.row < 0 ? make_uint4(~0u, ~0u, ~0u, ~0u) : tree_at<uint4>(a, a.L.mask)[tc.node];
+      if (v >= 0) see = w.sp.row < 0 ? make_uint2(~0u, ~0u) : tree_at<uint2>(a, a.L.mask)[2 * static_cast<int64_t>(tc.node) + half];
     }
     // Q~ of the span before is free once its last scores are there
-    if (nspan > 0 && !warp_wait(S, a, &S.q_free, (nspan - 1) & 1)) return;
-    if (v >= 0) {
-      const float4 *rot = tree_at<float4>(a, a.L.rot) + (static_cast<int64_t>(tc.rot) + v * tc.n_nodes) * 32;
-      // two query tiles: each half of the warps its own; one: half of d each
-      const uint32_t to = smem_u32(S.q[two ? q : 0]) + row * 128;
-      write_query(src, rot, to, row, a.scale_log2, 4 * q);
-      if (two) write_query(src, rot, to, row, a.scale_log2, 4 - 4 * q);
+    if (nspan > 0) idle_wait(S, a, &S.q_free, (nspan - 1) & 1);
+    if (warp_on) {
+      const __nv_bfloat16 *qs = static_cast<const __nv_bfloat16 *>(a.q);
+      const float4 *table = tree_at<float4>(a, a.L.rot);
+      const int rot = v < 0 ? -1 : tc.rot + v * tc.n_nodes;
+      // two query tiles: a tile a stream, half of a warp's rows a half; one: a quarter each
+      const uint32_t to = smem_u32(S.q[two ? q : 0]) + quarter * 32 * 128;
+      if (two)
+        write_queries<16>(qs, table, src, rot, to, a.scale_log2, 16 * half, lane);
+      else
+        write_queries<8>(qs, table, src, rot, to, a.scale_log2, 8 * (2 * q + half), lane);
       fence_proxy_async_smem();
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.q_full[q]);
     if (step == 2) {
-      if (rec_cols > 0) {
-        if (some && !warp_wait(S, a, &S.pv_done[q], (ns - 1) & 1)) return;
-        tc_fence_after();
-        store_record(a, o_tmem, rec, rec_cols, rec_col, m, l, some);
-        tc_fence_before();
-        __syncwarp();
-        if (some && lane == 0) mbar_arrive(&S.o_empty[q]);
-      }
+      if (rec_cols > 0) record();
       const int64_t k = static_cast<int64_t>(w.head) * w.n_groups + w.group;
       rec_cols = w.g.n_cols;
       rec_col = col;
@@ -429,79 +496,80 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
     }
     ++nspan;
     for (int t = 0; t < w.tiles; ++t, ++i, turn ^= 1) {
-      const int owner = two ? 0 : turn;  // who looks after the V tile
+      const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
+      const int owner = two ? 0 : turn;  // who tidies the V tile, where that is needed
+      const bool tidy = w.sp.partial || (valid & 15);
       if (!two && turn != q) {
-        if (w.sp.partial) ++(owner ? np1 : np0);
+        if (tidy) ++(owner ? np1 : np0);
         continue;
       }
-      const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
-      if (!warp_wait(S, a, &S.s_full[q], ns & 1)) return;
-      uint32_t bad = 0;
-      if (w.sp.partial || (q == owner && (valid & 15))) {
+      idle_wait(S, a, &S.s_full[q], ns & 1);
+      bool bad = false;
+      if (tidy) {
         const int nv = 2 * i + 1, np = owner ? np1 : np0, par = np & 1;
         if (q == owner) {
           // 0 * NaN would poison a sum.  V rows past the span, up to the end
           // of the last step of 16 tokens, may hold anything: cleared.  In a
-          // tile that not every column sees, so are tokens with a value that
-          // is not finite: the columns that see them get a NaN through l.
-          if (!warp_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1)) return;
-          const uint32_t at = smem_u32(S.kv[nv % kStages]) + row * 128;
+          // tile that not every column sees, so are values that are not
+          // finite: the columns that see their token get a NaN through l.
+          idle_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1);
+          const uint32_t at = smem_u32(S.kv[nv % kStages]) + half * kBox + row * 128;
           const bool clear = row >= valid && row < ((valid + 15) & ~15);
           bool odd = false;
           if (w.sp.partial && row < valid)
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
               uint32_t x[4];
-              ld_shared_v4(at + (c >> 3) * kBox + ((c + row) & 7) * 16, x);
+              ld_shared_v4(at + ((c + row) & 7) * 16, x);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 odd |= (x[j] & 0x7f80u) == 0x7f80u || (x[j] & 0x7f800000u) == 0x7f800000u;
             }
           if (clear || odd) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) st_shared_v4(at + (c >> 3) * kBox + (c & 7) * 16, 0, 0, 0, 0);
+            for (int c = 0; c < 8; ++c) st_shared_v4(at + c * 16, 0, 0, 0, 0);
             fence_proxy_async_smem();
           }
-          if (w.sp.partial) {
-            const uint32_t bits = __ballot_sync(0xffffffffu, odd);
-            if (lane == 0) {
-              S.bad[owner][par][quarter] = bits;
-              mbar_arrive(&S.scanned[owner][par]);
-            }
+          const uint32_t bits = __ballot_sync(0xffffffffu, odd);
+          if (lane == 0) {
+            S.bad[owner][par][half][quarter] = bits;
+            mbar_arrive(&S.scanned[owner][par]);
           }
         }
-        if (w.sp.partial) {
-          if (!warp_wait(S, a, &S.scanned[owner][par], (np >> 1) & 1)) return;
-          const uint32_t *b = S.bad[owner][par];
-          bad = (b[0] & see.x) | (b[1] & see.y) | (b[2] & see.z) | (b[3] & see.w);
-          ++(owner ? np1 : np0);
-        }
+        idle_wait(S, a, &S.scanned[owner][par], (np >> 1) & 1);
+        const uint32_t(*b)[4] = S.bad[owner][par];
+        bad = ((b[0][2 * half] | b[1][2 * half]) & see.x) || ((b[0][2 * half + 1] | b[1][2 * half + 1]) & see.y);
+        ++(owner ? np1 : np0);
       }
       if (warp_on) {
         tc_fence_after();
-        uint32_t s[4][32];
+        uint32_t s[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld32(s_tmem + 64 * half + 32 * c, s[c]);
         tmem_wait_ld();
         if (valid < kT || w.sp.partial) {
-          const uint32_t tm[4] = {see.x, see.y, see.z, see.w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int in = min(32, max(0, valid - 32 * c));
-            const uint32_t bits = tm[c] & (in == 32 ? ~0u : (1u << in) - 1u);
+          for (int c = 0; c < 2; ++c) {
+            const int in = min(32, max(0, valid - 64 * half - 32 * c));
+            const uint32_t bits = (c ? see.y : see.x) & (in == 32 ? ~0u : (1u << in) - 1u);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!((bits >> j) & 1u)) s[c][j] = 0xff800000u;  // -inf
           }
         }
-        float mx[4];
+        float mx[2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
           for (int j = 2; j < 32; j += 2)
             mx[c] = max3(mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
         }
-        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        float top = fmaxf(mx[0], mx[1]);
+        // (also: both halves of S are read, so P may be written over them; and
+        // the partner has read this before the next tile's scores can come)
+        S.red[q][half][row] = top;
+        pair_sync(pair);
+        top = fmaxf(top, S.red[q][half ^ 1][row]);
         if (!some) {
           m = fmaxf(top, -1e30f);  // (nothing seen yet: weights 0, no NaN)
           l = 0.f;
@@ -510,57 +578,45 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
           const float to = top > m + kLazy ? top : m, al = ex2(m - to);
           m = to;
           l *= al;
-          if (!warp_wait(S, a, &S.pv_done[q], (ns - 1) & 1)) return;
+          idle_wait(S, a, &S.pv_done[q], (ns - 1) & 1);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 16; ++c) {  // (rare: few registers beside S matter more than speed)
+          for (int c = 0; c < 8; ++c) {  // (rare: few registers beside S matter more than speed)
             uint32_t r[8];
-            tmem_ld8(o_tmem + 8 * c, r);
+            tmem_ld8(o_tmem + 64 * half + 8 * c, r);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al);
-            tmem_st8(o_tmem + 8 * c, r);
+            tmem_st8(o_tmem + 64 * half + 8 * c, r);
           }
         }
         const uint64_t neg = pack2(-m, -m);
         uint64_t sum[2] = {0, 0};
+        uint32_t p[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // P in two halves: PV starts on the first
-          uint32_t p[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float p0, p1;
-            unpack2(add2(pack2(__uint_as_float(s[2 * c + j / 16][2 * j % 32]),
-                               __uint_as_float(s[2 * c + j / 16][2 * j % 32 + 1])), neg), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
-            p[j] = pack_bf16(p0, p1);
-          }
-          tmem_st32(s_tmem + 32 * c, p);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(c == 0 ? &S.p_half[q] : &S.p_full[q]);
+        for (int j = 0; j < 32; ++j) {
+          float p0, p1;
+          unpack2(add2(pack2(__uint_as_float(s[j / 16][2 * j % 32]), __uint_as_float(s[j / 16][2 * j % 32 + 1])), neg), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
+          p[j] = pack_bf16(p0, p1);
         }
+        tmem_st32(s_tmem + 32 * half, p);
         float x[4];
         unpack2(sum[0], x[0], x[1]);
         unpack2(sum[1], x[2], x[3]);
         l += ((x[0] + x[1]) + (x[2] + x[3])) + (bad ? NAN : 0.f);
-      } else {
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S.p_half[q]);
-          mbar_arrive(&S.p_full[q]);
-        }
+        tmem_wait_st();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[q]);
       some = true;
       ++ns;
     }
   } while ((step = w.next()));
-  if (some && !warp_wait(S, a, &S.pv_done[q], (ns - 1) & 1)) return;
-  tc_fence_after();
-  store_record(a, o_tmem, rec, rec_cols, rec_col, m, l, some);
+  record();
 }
 
 // A programmatic dependent of the append launch, which itself starts its
@@ -571,8 +627,8 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv) {
-  extern __shared__ uint8_t smem_raw[];
-  TcSmem &S = *reinterpret_cast<TcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  TcSmem &S = *reinterpret_cast<TcSmem *>(smem_raw);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!tree_plan_ok(a)) {
@@ -593,20 +649,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&S.kv_full[s], 1);
-      mbar_init(&S.kv_empty[s], 1);
+      mbar_init(&S.kv_empty[s], 2);  // one arrival a stream
     }
     for (int q = 0; q < 2; ++q) {
-      mbar_init(&S.q_full[q], 4);
-      mbar_init(&S.p_half[q], 4);
+      mbar_init(&S.q_full[q], 8);
       mbar_init(&S.s_full[q], 1);
-      mbar_init(&S.p_full[q], 4);
+      mbar_init(&S.p_full[q], 8);
       mbar_init(&S.pv_done[q], 1);
-      mbar_init(&S.o_empty[q], 4);
-      mbar_init(&S.scanned[q][0], 4);
-      mbar_init(&S.scanned[q][1], 4);
+      mbar_init(&S.o_empty[q], 8);
+      mbar_init(&S.scanned[q][0], 8);
+      mbar_init(&S.scanned[q][1], 8);
     }
-    mbar_init(&S.q_free, 1);
-    mbar_init(&S.mma_done, 1);
+    mbar_init(&S.q_free, 2);
+    mbar_init(&S.order, 1);
+    mbar_init(&S.mma_done, 2);
     S.abort_flag = 0;
     fence_mbar_init();
   }
@@ -620,10 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
   if (warp == kWarpTma) {
     if ((tid & 31) == 0) producer(a, S, &tk, &tv, w);
-  } else if (warp == kWarpMma) {
-    mma_issuer(a, S, tmem, w);
-  } else if (warp < 8) {
-    softmax(a, S, tmem, w, warp >> 2);
+  } else if (warp >= kWarpMma) {
+    mma_issuer(a, S, tmem, w, warp - kWarpMma);
+  } else {
+    softmax(a, S, tmem, w, warp >> 3);
   }
   __syncwarp();
   tc_fence_before();
@@ -635,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
-  const size_t smem = sizeof(TcSmem) + 1024;
+  const size_t smem = sizeof(TcSmem);
   static bool configured = false;
   if (!configured) {
     const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
