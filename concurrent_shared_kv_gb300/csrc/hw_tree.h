@@ -17,7 +17,7 @@
 //              a tile weighs tile1 or tile2 (over 128 columns), the first tile
 //              of a span `span` more, that of a group `group` more still.  CTA
 //              c of C takes the units that start in [c W / C, (c + 1) W / C);
-//              C is small enough that every CTA inside a group owns a unit.
+//              shares without a unit get no CTA.
 //   record   = what a CTA leaves for (kv head, group): per column the running
 //              maximum m and sum l of the softmax (log2 domain) and the
 //              unnormalised output.  The records of one (kv head, group) lie
@@ -26,8 +26,11 @@
 //              side, then the next 8: a thread that owns a column and a warp
 //              that owns a row both move whole sectors.
 // The rotation of a (row, view entry, node) is the same for every layer and q
-// head: the plan holds its cos and sin, fp32, head_dim / 2 pairs each (in the
-// order of rot_at).
+// head: the plan holds its cos and sin, head_dim / 2 pairs each - in fp32 for
+// the keys that are stored and for the CUDA cores, in fp16 (in the order of
+// rot16_at) for the tensor-core kernel, which rounds the turned query to bf16:
+// 2^-12 beside bf16's 2^-8, and half the loads of a warp with a thousand
+// clocks of latency and few registers.
 // tree_merge_kernel joins the records of every (row, node, q head).
 #pragma once
 
@@ -63,7 +66,6 @@ struct TreeSpan {
   int32_t map;         // block: in the map, per row of the group its view entry, or -1
   int32_t tile0;       // tiles of the group before it
   int32_t partial;     // not every column sees every token of it
-  int64_t w0;          // weight of the group before it
 };
 struct TreeColumn {
   int32_t node, head;   // row * max_nodes + node; q head within its kv head's
@@ -76,7 +78,7 @@ struct TreeCta {
 
 // Byte offsets of the plan's arrays in the workspace (the error word is at 0).
 struct TreeLayout {
-  size_t hdr, groups, wbase, spans, map, columns, rot, piece_row, piece_cta, ctas;
+  size_t hdr, groups, wbase, spans, map, columns, rot, rot16, piece_row, piece_cta, ctas;
   size_t n_nodes, slot, pos, end, col, run, rot0, rank, depth, mask, heads, block_start, block_len;
   size_t ml, o, total;
   int64_t max_groups, max_spans, max_map, max_cols, max_rots, max_rows;
@@ -133,11 +135,11 @@ cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaS
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
-// Where a table row keeps element e's (cos, sin), e < half = head_dim / 2:
-// elements 8c + 2j and 8c + 2j + 1 side by side, c running before j, so that
+// Where an fp16 table row keeps element e's (cos, sin), e < half = head_dim / 2:
+// elements 8c + 4j .. 8c + 4j + 3 side by side, c running before j, so that
 // the lanes that each turn 8 neighbouring elements read neighbouring memory.
-__host__ __device__ __forceinline__ int rot_at(int e, int half) {
-  return ((((e & 7) >> 1) * (half >> 3) + (e >> 3)) << 1) | (e & 1);
+__host__ __device__ __forceinline__ int rot16_at(int e, int half) {
+  return ((((e & 7) >> 2) * (half >> 3) + (e >> 3)) << 2) | (e & 3);
 }
 // Element d of column col in a record of n_cols columns that starts at row rec.
 __device__ __forceinline__ int64_t record_at(int64_t rec, int n_cols, int col, int d, int D) {

@@ -1,6 +1,7 @@
 // tree_plan.cu - the draft-tree operators' plan (hw_tree.h), the write of the
 // drafted tokens into the cache, the merge of the partial results, and the
 // commit of an accepted path.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "hw_device.cuh"
@@ -15,15 +16,15 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
-// Weights of the unit line.  Tensor cores: a tile against up to 128 columns
-// is bound by its K/V bytes, one against 129..256 by both products and the
-// softmax of two query tiles; a span costs new rotated queries, a group its
-// records and an empty pipeline.
+// Weights of the unit line, measured on the tensor-core kernel in steps of
+// about 750 clocks: a tile, a span's new queries and empty pipeline, a group's
+// records.  Where every unit can have a CTA of its own, each does: the units
+// then weigh the same.
 struct TreeCost {
   int32_t tile1, tile2, span, group;
 };
-__host__ __device__ inline TreeCost tree_cost(int cols) {
-  return cols > 128 ? TreeCost{2, 3, 3, 3} : TreeCost{4, 4, 1, 1};
+__device__ inline TreeCost tree_cost(int cols, bool alone) {
+  return alone ? TreeCost{1, 1, 0, 0} : cols > 128 ? TreeCost{4, 4, 6, 6} : TreeCost{4, 4, 1, 1};
 }
 
 struct TreePlanSmem {
@@ -31,6 +32,7 @@ struct TreePlanSmem {
   int64_t scan[kPlanWarps + 1];
   int64_t carry;
   int64_t uidx[1025];
+  int16_t number[kPlanThreads];  // of every share with units
   int32_t ok, n_groups, n_spans, n_map, n_live;
   union {
     uint8_t parent[kPlanWarps][kMaxNodes];
@@ -204,9 +206,8 @@ __device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
   S.n_groups = n;
 }
 
-// A group's spans, by one warp; its weight and tiles go to wbase and ubase.
-__device__ void plan_spans(const TreeArgs &a, TreePlanSmem &S, const TreeCost &cost, int gi, int64_t *wbase,
-                           int64_t *ubase, int lane) {
+// A group's spans, by one warp; its number of tiles goes to ubase.
+__device__ void plan_spans(const TreeArgs &a, TreePlanSmem &S, int gi, int64_t *ubase, int lane) {
   const int V = a.n_view, TL = a.L.tile, warp = threadIdx.x >> 5;
   TreeGroup &g = tree_at<TreeGroup>(a, a.L.groups)[gi];
   uint8_t *count = S.count[warp];
@@ -250,7 +251,7 @@ __device__ void plan_spans(const TreeArgs &a, TreePlanSmem &S, const TreeCost &c
   for (int x = lane; x < nb * g.n_rows; x += 32) map[x] = -1;
   for (int b = lane; b < a.n_blocks; b += 32)
     for (int k = 0; k < count[b]; ++k)
-      spans[first[b] + k] = TreeSpan{S.start[b], S.len[b], -1, map0 + (first[b] + k) * g.n_rows, 0, 0, 0};
+      spans[first[b] + k] = TreeSpan{S.start[b], S.len[b], -1, map0 + (first[b] + k) * g.n_rows, 0, 0};
   __syncwarp();
   int j = 0;
   for (int r = g.row0; r <= g.row1; ++r) {
@@ -260,40 +261,33 @@ __device__ void plan_spans(const TreeArgs &a, TreePlanSmem &S, const TreeCost &c
       bool last;
       if (b >= 0) map[(first[b] + entry_rank(S, r * V, v, V, &last)) * g.n_rows + j] = static_cast<int16_t>(v);
     }
-    if (lane == 0) spans[nb + j] = TreeSpan{tree_at<int32_t>(a, a.L.slot)[r], S.nodes[r], r, 0, 0, 1, 0};
+    if (lane == 0) spans[nb + j] = TreeSpan{tree_at<int32_t>(a, a.L.slot)[r], S.nodes[r], r, 0, 0, 1};
     ++j;
   }
   __syncwarp();
-  int64_t w = 0;
   int tiles = 0;
   for (int s0 = 0; s0 < n; s0 += 32) {
     const int s = s0 + lane;
     const int t = s < n ? (spans[s].len + TL - 1) / TL : 0;
-    const int64_t ws = s < n ? tile_weight(cost, g.n_cols, s == 0, t) : 0;
     int ti = t;
-    int64_t wi = ws;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, ti, o);
-      const int64_t z = __shfl_up_sync(0xffffffffu, wi, o);
-      if (lane >= o) {
-        ti += y;
-        wi += z;
-      }
+      if (lane >= o) ti += y;
     }
     if (s < n) {
       spans[s].tile0 = tiles + ti - t;
-      spans[s].w0 = w + wi - ws;
       if (s < nb)
         for (int x = 0; x < g.n_rows; ++x) spans[s].partial |= map[s * g.n_rows + x] < 0;
     }
     tiles += __shfl_sync(0xffffffffu, ti, 31);
-    w += __shfl_sync(0xffffffffu, wi, 31);
   }
-  if (lane == 0) {
-    wbase[gi] = w;
-    ubase[gi] = tiles;
-  }
+  if (lane == 0) ubase[gi] = tiles;
+}
+
+// Weight of a group before its span s, which has tile0 tiles before it.
+__device__ __forceinline__ int64_t span_weight(const TreeCost &c, int n_cols, int s, int tile0) {
+  return s == 0 ? 0 : c.group + static_cast<int64_t>(s) * c.span + static_cast<int64_t>(tile0) * (n_cols > 128 ? c.tile2 : c.tile1);
 }
 
 // The plan but for its tables, by one CTA.
@@ -304,7 +298,6 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = a.n_rows, V = a.n_view, E = R * V, T = a.max_nodes;
   const int G = a.n_q_heads / a.n_kv_heads, TL = a.L.tile;
-  const TreeCost cost = tree_cost(a.L.cols);
   int32_t *err = reinterpret_cast<int32_t *>(a.ws);
   TreeHeader &hdr = *tree_at<TreeHeader>(a, a.L.hdr);
   if (tid == 0) {
@@ -369,35 +362,36 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   const int n_groups = S.n_groups;
   int64_t *wbase = tree_at<int64_t>(a, a.L.wbase), *ubase = wbase + a.L.max_groups;
-  for (int g = warp; g < n_groups; g += kPlanWarps) plan_spans(a, S, cost, g, wbase, ubase, lane);
+  for (int g = warp; g < n_groups; g += kPlanWarps) plan_spans(a, S, g, ubase, lane);
   __syncthreads();
   const TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
   const TreeSpan *spans = tree_at<TreeSpan>(a, a.L.spans);
-  // weights and units before each group
+  // units, then weights before each group
   for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
     const int g = g0 + tid;
-    const int64_t at = block_scan(S, g < n_groups ? wbase[g] : 0);
+    const int64_t at = block_scan(S, g < n_groups ? ubase[g] : 0);
+    if (g < n_groups) ubase[g] = at;
+  }
+  const int64_t UH = S.carry, U = UH * a.n_kv_heads;
+  __syncthreads();
+  if (tid == 0) S.carry = 0;
+  __syncthreads();
+  const TreeCost cost = tree_cost(a.L.cols, U <= a.L.ctas_max);
+  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    const int64_t tiles = g < n_groups ? (g + 1 < n_groups ? ubase[g + 1] : UH) - ubase[g] : 0;
+    const int64_t at = block_scan(S, g < n_groups ? span_weight(cost, groups[g].n_cols, groups[g].n_spans, static_cast<int>(tiles)) : 0);
     if (g < n_groups) wbase[g] = at;
   }
   const int64_t WH = S.carry, W = WH * a.n_kv_heads;
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
-  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
-    const int g = g0 + tid;
-    const int64_t at = block_scan(S, g < n_groups ? ubase[g] : 0);
-    if (g < n_groups) ubase[g] = at;
-  }
-  const int64_t UH = S.carry;
-  __syncthreads();
-  if (tid == 0) S.carry = 0;
-  __syncthreads();
-  // as many CTAs as leave each at least one unit of every group it is inside
-  const int64_t most = W / (cost.group + cost.span + cost.tile2);
-  const int C = W == 0 ? 0 : static_cast<int>(most < 1 ? 1 : most < a.L.ctas_max ? most : a.L.ctas_max);
+  const int C = static_cast<int>(U < a.L.ctas_max ? U : a.L.ctas_max);
   // every CTA's first unit
   TreeCta *ctas = tree_at<TreeCta>(a, a.L.ctas);
-  for (int c = tid; c <= C && C > 0; c += kPlanThreads) {
+  TreeCta first = {};
+  for (int c = tid; c <= C && C > 0; c += kPlanThreads) {  // (C < kPlanThreads: once each)
     const int64_t lo = c * W / C;
     int h = static_cast<int>(lo / WH);
     if (h >= a.n_kv_heads) {
@@ -417,9 +411,9 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     hi = gr.n_spans;
     while (hi - s > 1) {
       const int mid = (s + hi) >> 1;
-      if (sp[mid].w0 <= in) s = mid; else hi = mid;
+      if (span_weight(cost, gr.n_cols, mid, sp[mid].tile0) <= in) s = mid; else hi = mid;
     }
-    const int64_t x = in - sp[s].w0;
+    const int64_t x = in - span_weight(cost, gr.n_cols, s, sp[s].tile0);
     const int own = cost.span + (s == 0 ? cost.group : 0), tw = gr.n_cols > 128 ? cost.tile2 : cost.tile1;
     int t = x == 0 ? 0 : x <= own + tw ? 1 : static_cast<int>((x - own + tw - 1) / tw);
     if (t >= (sp[s].len + TL - 1) / TL) {
@@ -433,10 +427,21 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       }
     }
     S.uidx[c] = h < a.n_kv_heads ? h * UH + ubase[g] + spans[groups[g].span0 + s].tile0 + t : UH * a.n_kv_heads;
-    if (c < C) ctas[c] = TreeCta{h, g, s, t, 0};
+    first = TreeCta{h, g, s, t, 0};
   }
   __syncthreads();
-  for (int c = tid; c < C; c += kPlanThreads) ctas[c].n_units = static_cast<int>(S.uidx[c + 1] - S.uidx[c]);
+  // a share without a unit gets no CTA: those with units are numbered anew
+  const int n_units = tid < C ? static_cast<int>(S.uidx[tid + 1] - S.uidx[tid]) : 0;
+  const int number = static_cast<int>(block_scan(S, n_units > 0));
+  const int n_ctas = static_cast<int>(S.carry);
+  if (n_units > 0) {
+    first.n_units = n_units;
+    ctas[number] = first;
+    S.number[tid] = static_cast<int16_t>(number);
+  }
+  __syncthreads();
+  if (tid == 0) S.carry = 0;
+  __syncthreads();
   // the records of every (kv head, group)
   int32_t *piece_row = tree_at<int32_t>(a, a.L.piece_row);
   int2 *piece_cta = tree_at<int2>(a, a.L.piece_cta);
@@ -451,8 +456,9 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       const TreeSpan last = spans[gr.span0 + gr.n_spans - 1];
       const int64_t w = k / n_groups * WH + wbase[g];
       const int tiles = (last.len + TL - 1) / TL;
-      pc.x = cta_of_weight(w, W, C);
-      pc.y = cta_of_weight(w + last.w0 + tile_weight(cost, gr.n_cols, gr.n_spans == 1, tiles - 1), W, C) - pc.x + 1;
+      pc.x = S.number[cta_of_weight(w, W, C)];
+      pc.y = S.number[cta_of_weight(w + span_weight(cost, gr.n_cols, gr.n_spans - 1, last.tile0) +
+                                        tile_weight(cost, gr.n_cols, gr.n_spans == 1, tiles - 1), W, C)] - pc.x + 1;
       // tensor cores: up to 128 columns leave two records a CTA (tree_tc.cu)
       if (a.L.cols > 128 && gr.n_cols <= 128) pc.y *= 2;
       rows = static_cast<int64_t>(pc.y) * gr.n_cols;
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   }
   if (tid == 0)
     hdr = TreeHeader{kTreeMagic, R, T, a.n_q_heads, a.n_kv_heads, a.head_dim, a.n_blocks, V, a.dtype,
-                     n_groups, C, 0, a.capacity};
+                     n_groups, n_ctas, 0, a.capacity};
 }
 
 // cos and sin of a position's angle for one pair: the angle in turns is exact in 64-bit integers (rope_cos_sin); here
@@ -513,9 +519,12 @@ __global__ void __launch_bounds__(256) tree_tables_kernel(const __grid_constant_
     for (int i = warp; i < n; i += 8) {
       const int64_t rel = root + tree_at<int32_t>(a, a.L.depth)[static_cast<int64_t>(r) * T + i];
       float2 *to = tree_at<float2>(a, a.L.rot) + (rot0[r] + static_cast<int64_t>(v) * n + i) * half;
+      __half2 *to16 = tree_at<__half2>(a, a.L.rot16) + (rot0[r] + static_cast<int64_t>(v) * n + i) * half;
       for (int j = lane; j < half; j += 32) {
-        float2 &x = to[rot_at(j, half)];
+        float2 x;
         rope_cos_sin_exact(rel, a.phase[j], &x.x, &x.y);
+        to[j] = x;
+        to16[rot16_at(j, half)] = __floats2half2_rn(x.x, x.y);
       }
     }
   }
@@ -550,7 +559,7 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
   const int64_t to = (h * a.capacity + slot) * D;
   const float ks = kFp8 ? a.k_scale[h] : 1.f, vs = kFp8 ? a.v_scale[h] : 1.f;
   for (int j = lane; j < half; j += 32) {
-    const float2 cs = rot[rot_at(j, half)];
+    const float2 cs = rot[j];
     const float c = cs.x, s = cs.y;
     const float x0 = to_f32<T>(kn[j]), x1 = to_f32<T>(kn[j + half]);
     const float y0 = __fmaf_rn(x0, c, -__fmul_rn(x1, s)), y1 = __fmaf_rn(x1, c, __fmul_rn(x0, s));
@@ -775,7 +784,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.cols = tc ? 256 : 32;
   L.tile = tc ? 128 : 64;
   L.ctas_max = tc ? sms : 2 * sms;
-  if (L.ctas_max > 1024) L.ctas_max = 1024;
+  if (L.ctas_max > 1000) L.ctas_max = 1000;  // (one thread of the plan each)
   const int64_t R = d.n_rows, V = d.max_view_blocks, G = d.n_q_heads / d.n_kv_heads;
   const int64_t Q = R * max_nodes;  // nodes
   L.max_cols = Q * G;
@@ -800,6 +809,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.map = put(2 * L.max_map);
   L.columns = put(sizeof(TreeColumn) * L.max_cols);
   L.rot = put(4 * static_cast<size_t>(d.head_dim) * L.max_rots);
+  L.rot16 = put(2 * static_cast<size_t>(d.head_dim) * L.max_rots);
   L.piece_row = put(4 * L.max_groups * d.n_kv_heads);
   L.piece_cta = put(8 * L.max_groups * d.n_kv_heads);
   L.ctas = put(sizeof(TreeCta) * L.ctas_max);

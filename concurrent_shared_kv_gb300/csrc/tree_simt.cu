@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
         const int64_t row = static_cast<int64_t>(S.col[qi].node) * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[h * G + S.col[qi].head];
         const T *qp = reinterpret_cast<const T *>(a.q) + row * D;
         const float x0 = to_f32<T>(qp[i]), x1 = to_f32<T>(qp[i + D / 2]);
-        const float2 r = tree_at<float2>(a, a.L.rot)[static_cast<int64_t>(S.rot[qi]) * (D / 2) + rot_at(i, D / 2)];
+        const float2 r = tree_at<float2>(a, a.L.rot)[static_cast<int64_t>(S.rot[qi]) * (D / 2) + i];
         S.q[qi][i] = x0 * r.x - x1 * r.y;
         S.q[qi][i + D / 2] = x1 * r.x + x0 * r.y;
       }

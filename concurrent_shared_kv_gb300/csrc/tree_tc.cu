@@ -23,6 +23,7 @@
 // units; they are rounded to bf16 once, as P is: both leave an error of half a
 // bf16 step, that of the output itself.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "hw_device.cuh"
 #include "hw_sm100.cuh"
@@ -326,48 +327,42 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
 // rotation's table row of this lane's own query, rot < 0: it does not see the
 // span, and its row of the tile may hold anything.
 template <int N>
-__device__ __forceinline__ void write_queries(const __nv_bfloat16 *q, const float4 *table, int src, int rot, uint32_t to,
+__device__ __forceinline__ void write_queries(const __nv_bfloat16 *q, const uint4 *table, int src, int rot, uint32_t to,
                                               float scale, int first, int lane) {
   const int c = lane & 7;
   // (rows that see nothing read row 0: loads without branches are all under
   // way before the first is needed, and one trip to L2 costs a thousand
   // clocks or more)
-  uint4 u[N / 4], v[N / 4];
-  int turn[N / 4];
+  uint4 u[N / 4], v[N / 4], cs[N / 4][2];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     const int at = first + 4 * i + (lane >> 3);
-    const int row = __shfl_sync(0xffffffffu, src, at);
-    turn[i] = max(0, __shfl_sync(0xffffffffu, rot, at));
+    const int row = __shfl_sync(0xffffffffu, src, at), turn = max(0, __shfl_sync(0xffffffffu, rot, at));
     const uint4 *x = reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(row) * 128);
+    const uint4 *t = table + static_cast<int64_t>(turn) * 16;
     u[i] = __ldg(x + c);
     v[i] = __ldg(x + c + 8);
+    cs[i][0] = __ldg(t + c);  // (cos, sin) of elements 8c .. 8c + 3, then of the next four
+    cs[i][1] = __ldg(t + c + 8);
   }
 #pragma unroll
-  for (int i0 = 0; i0 < N / 4; i0 += 2) {
-    float4 cs[2][4];  // (cos, sin) of elements 8c + 2j and 8c + 2j + 1
+  for (int i = 0; i < N / 4; ++i) {
+    const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    const uint32_t w[8] = {cs[i][0].x, cs[i][0].y, cs[i][0].z, cs[i][0].w, cs[i][1].x, cs[i][1].y, cs[i][1].z, cs[i][1].w};
+    uint32_t p[4], r[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) cs[i][j] = __ldg(table + static_cast<int64_t>(turn[i0 + i]) * 32 + 8 * j + c);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 a = u[i0 + i], b = v[i0 + i];
-      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-      uint32_t p[4], r[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 w = cs[i][j];
-        const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
-        const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
-        p[j] = pack_bf16((x0 * w.x - y0 * w.y) * scale, (x1 * w.z - y1 * w.w) * scale);
-        r[j] = pack_bf16((y0 * w.x + x0 * w.y) * scale, (y1 * w.z + x1 * w.w) * scale);
-      }
-      const int at = first + 4 * (i0 + i) + (lane >> 3);
-      const uint32_t o = to + at * 128 + ((c ^ (at & 7)) << 4);
-      st_shared_v4(o, p[0], p[1], p[2], p[3]);
-      st_shared_v4(o + kBox, r[0], r[1], r[2], r[3]);
+    for (int j = 0; j < 4; ++j) {
+      const float2 w0 = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * j]));
+      const float2 w1 = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * j + 1]));
+      const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
+      const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
+      p[j] = pack_bf16((x0 * w0.x - y0 * w0.y) * scale, (x1 * w1.x - y1 * w1.y) * scale);
+      r[j] = pack_bf16((y0 * w0.x + x0 * w0.y) * scale, (y1 * w1.x + x1 * w1.y) * scale);
     }
+    const int at = first + 4 * i + (lane >> 3);
+    const uint32_t o = to + at * 128 + ((c ^ (at & 7)) << 4);
+    st_shared_v4(o, p[0], p[1], p[2], p[3]);
+    st_shared_v4(o + kBox, r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -389,11 +384,12 @@ __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem,
     tmem_wait_ld();
     if (on) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float4 v = make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
-                                     __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
-        *reinterpret_cast<float4 *>(dst + static_cast<int64_t>(4 * c + x / 2) * n_cols * 8 + (x & 1) * 4) = v;
-      }
+      for (int x = 0; x < 4; ++x)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                         dst + static_cast<int64_t>(4 * c + x) * n_cols * 8),
+                     "r"(r[8 * x]), "r"(r[8 * x + 1]), "r"(r[8 * x + 2]), "r"(r[8 * x + 3]), "r"(r[8 * x + 4]),
+                     "r"(r[8 * x + 5]), "r"(r[8 * x + 6]), "r"(r[8 * x + 7])
+                     : "memory");
     }
   }
 }
@@ -471,7 +467,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
     if (nspan > 0) idle_wait(S, a, &S.q_free, (nspan - 1) & 1);
     if (warp_on) {
       const __nv_bfloat16 *qs = static_cast<const __nv_bfloat16 *>(a.q);
-      const float4 *table = tree_at<float4>(a, a.L.rot);
+      const uint4 *table = tree_at<uint4>(a, a.L.rot16);
       const int rot = v < 0 ? -1 : tc.rot + v * tc.n_nodes;
       // two query tiles: a tile a stream, half of a warp's rows a half; one: a quarter each
       const uint32_t to = smem_u32(S.q[two ? q : 0]) + quarter * 32 * 128;
