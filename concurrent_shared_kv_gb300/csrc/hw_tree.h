@@ -123,7 +123,7 @@ struct TreeVerifyArgs {
 TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms);
 // Whether these caches run on the tensor cores.
 inline bool tree_on_tensor_cores(int dtype, int head_dim) {
-  return dtype == HW_BF16 && head_dim == 128;
+  return (dtype == HW_BF16 || dtype == HW_FP8_E4M3) && head_dim == 128;
 }
 
 cudaError_t launch_tree_plan(const TreeArgs &a, const TreeMeta &m, cudaStream_t s);

@@ -76,8 +76,9 @@ static int decode_tree(const hw_attn_desc *d, int32_t max_nodes, const void *q, 
   cudaError_t e = launch_tree_append(a, s);
   if (e == cudaSuccess && tree_on_tensor_cores(d->dtype, d->head_dim)) {
     CUtensorMap km, vm;
-    if (!make_pool_map(&km, k_cache, d->cache_capacity, d->n_kv_heads) ||
-        !make_pool_map(&vm, v_cache, d->cache_capacity, d->n_kv_heads))
+    const bool e4m3 = d->dtype == HW_FP8_E4M3;
+    if (!make_pool_map(&km, k_cache, d->cache_capacity, d->n_kv_heads, e4m3) ||
+        !make_pool_map(&vm, v_cache, d->cache_capacity, d->n_kv_heads, e4m3))
       return cuda_fail(cudaErrorInvalidValue);
     e = launch_tree_tc(a, km, vm, s);
   } else if (e == cudaSuccess) {

@@ -6,8 +6,6 @@
 // memory, rotated anew for every span, tiles of 64 tokens, an online softmax
 // in the log2 domain, and a record of (m, l, o) per column at the end.  A
 // tree's tile is masked with the ancestor bits of each column's node.
-#include <cuda_fp8.h>
-
 #include "hw_device.cuh"
 #include "hw_tree.h"
 
@@ -31,7 +29,7 @@ struct Smem {
   uint32_t bad[2];        // a partial tile's tokens with a value that is not finite
 };
 
-template <typename KV>
+template <typename T>
 __device__ __forceinline__ void unpack(const uint4 &u, float *x);
 template <>
 __device__ __forceinline__ void unpack<float>(const uint4 &u, float *x) {
@@ -49,22 +47,7 @@ __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4 &u, float *x) 
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-template <>
-__device__ __forceinline__ void unpack<uint8_t>(const uint4 &u, float *x) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i] >> (16 * p)), __NV_E4M3));
-      const float2 f = __half22float2(h);
-      x[4 * i + 2 * p] = f.x;
-      x[4 * i + 2 * p + 1] = f.y;
-    }
-}
-
-// T: queries and outputs; KV: the cache's element (uint8_t: E4M3 codes).
-template <typename T, typename KV, int D>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<D> &S = *reinterpret_cast<Smem<D> *>(smem_raw);
@@ -80,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
   const TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
   const TreeSpan *spans = tree_at<TreeSpan>(a, a.L.spans);
   const int G = a.n_q_heads / a.n_kv_heads;
-  constexpr int EPV = 16 / sizeof(KV), CPR = D / EPV;
+  constexpr int EPV = 16 / sizeof(T), CPR = D / EPV;
   constexpr int QSTEP = kThreads / D;   // columns side by side in P.V
   constexpr int QPT = kCols / QSTEP;    // columns of a thread
   const int dcol = tid % D, qfirst = tid / D;
@@ -88,7 +71,6 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
   while (at.n_units > 0) {
     const TreeGroup gr = groups[at.group];
     const int h = at.head, nq = gr.n_cols;
-    const float ks = a.k_scale ? a.k_scale[h] : 1.f, vs = a.v_scale ? a.v_scale[h] : 1.f;
     if (tid < nq) {
       S.col[tid] = tree_at<TreeColumn>(a, a.L.columns)[gr.col0 + tid];
       S.m[tid] = -INFINITY;
@@ -121,8 +103,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
       for (int t = at.tile; t < t1; ++t) {
         const int valid = min(kTile, sp.len - t * kTile);
         const int64_t row0 = static_cast<int64_t>(h) * a.capacity + sp.start + t * kTile;
-        const KV *kb = reinterpret_cast<const KV *>(a.k) + row0 * D;
-        const KV *vb = reinterpret_cast<const KV *>(a.v) + row0 * D;
+        const T *kb = reinterpret_cast<const T *>(a.k) + row0 * D;
+        const T *vb = reinterpret_cast<const T *>(a.v) + row0 * D;
         __syncthreads();
         if (tid < 2) S.bad[tid] = 0;
         __syncthreads();
@@ -130,8 +112,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
           const int row = x / CPR, col = (x % CPR) * EPV;
           float kf[EPV], vf[EPV];
           if (row < valid) {
-            unpack<KV>(*reinterpret_cast<const uint4 *>(kb + static_cast<int64_t>(row) * D + col), kf);
-            unpack<KV>(*reinterpret_cast<const uint4 *>(vb + static_cast<int64_t>(row) * D + col), vf);
+            unpack<T>(*reinterpret_cast<const uint4 *>(kb + static_cast<int64_t>(row) * D + col), kf);
+            unpack<T>(*reinterpret_cast<const uint4 *>(vb + static_cast<int64_t>(row) * D + col), vf);
           } else {  // rows past the span may hold anything
 #pragma unroll
             for (int i = 0; i < EPV; ++i) kf[i] = vf[i] = 0.f;
@@ -148,8 +130,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
           }
 #pragma unroll
           for (int i = 0; i < EPV; ++i) {
-            S.k[row][col + i] = kf[i] * ks;
-            S.v[row][col + i] = vf[i] * vs;
+            S.k[row][col + i] = kf[i];
+            S.v[row][col + i] = vf[i];
           }
         }
         __syncthreads();
@@ -233,29 +215,26 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
   }
 }
 
-template <typename T, typename KV, int D>
+template <typename T, int D>
 cudaError_t launch(const TreeArgs &a, cudaStream_t s) {
   const size_t smem = sizeof(Smem<D>);
   static bool configured = false;
   if (!configured) {
-    const cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<T, KV, D>,
+    const cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<T, D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     configured = true;
   }
-  tree_simt_kernel<T, KV, D><<<a.L.ctas_max, kThreads, smem, s>>>(a);
+  tree_simt_kernel<T, D><<<a.L.ctas_max, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t s) {
-  if (a.dtype == HW_FP8_E4M3) return launch<__nv_bfloat16, uint8_t, 128>(a, s);
-  if (a.dtype == HW_BF16)
-    return a.head_dim == 64 ? launch<__nv_bfloat16, __nv_bfloat16, 64>(a, s)
-                            : launch<__nv_bfloat16, __nv_bfloat16, 128>(a, s);
-  return a.head_dim == 64 ? launch<float, float, 64>(a, s) : launch<float, float, 128>(a, s);
+  if (a.dtype == HW_BF16) return launch<__nv_bfloat16, 64>(a, s);
+  return a.head_dim == 64 ? launch<float, 64>(a, s) : launch<float, 128>(a, s);
 }
 
 }  // namespace hw

@@ -1,5 +1,5 @@
 // tree_tc.cu - attention for trees of drafted tokens on the sm_100 tensor
-// cores (tcgen05 + TMEM): bf16 caches with head_dim 128.
+// cores (tcgen05 + TMEM): bf16 and E4M3 caches with head_dim 128.
 //
 // A group (hw_tree.h) puts up to 256 query columns (nodes x q heads of a kv
 // head x rows that share blocks) against its spans' tokens, as two query tiles
@@ -22,6 +22,16 @@
 // Rotated queries carry scale * log2(e), so scores leave the MMA in log2
 // units; they are rounded to bf16 once, as P is: both leave an error of half a
 // bf16 step, that of the output itself.
+//
+// E4M3 caches: both products run as kind::f8f6f4 on the codes, at twice the
+// rate, with Q~ and P each as two E4M3 parts x = hi + lo, lo the rounded
+// remainder (half a step 2^-4 twice: 2^-8, bf16's), summed into the same
+// accumulator.  A query is scaled by a power of two that brings its largest
+// element into [128, 256), and takes its kv head's k_scale along; its scores
+// are scaled back in the softmax.  P is kept 2^6 times larger than the running
+// maximum asks for (below 2^8 until O is rescaled, E4M3 ends at 448), so that
+// weights down to 2^-12 keep both parts' full precision; the factor is in the
+// record's m.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -39,31 +49,42 @@ constexpr int kThreads = 608;
 constexpr int kWarpTma = 16, kWarpMma = 17;  // and 18: an issuer a stream
 constexpr int kT = 128;                      // tokens per tile
 constexpr uint32_t kBox = 128 * 128;         // 128 rows of 128 bytes, 128-byte swizzled
-constexpr uint32_t kQTile = 2 * kBox;        // a query tile: d 0-63, d 64-127
-constexpr uint32_t kStage = 2 * kBox;        // a K or a V tile
-constexpr int kStages = 5;
-constexpr float kLazy = 8.f;                 // O is rescaled only when a maximum grows by over 2^8
+constexpr uint32_t kQTile = 2 * kBox;        // a query tile: d 0-63, d 64-127 (E4M3: hi, lo)
+// The ring of K and V tiles: bf16 two boxes each, E4M3 one.
+template <bool kFp8>
+struct Ring {
+  static constexpr uint32_t kStage = kFp8 ? kBox : 2 * kBox;
+  static constexpr int kStages = kFp8 ? 9 : 5;
+  static constexpr int kStep = kFp8 ? 32 : 16;  // tokens of one MMA
+};
+constexpr float kLazy = 8.f;                 // O is rescaled only when a weight would pass 2^8
+constexpr float kLift = 6.f;                 // E4M3: log2 of P's factor
 constexpr uint32_t kTmemCols = 512;          // S0/P0, S1/P1, O0, O1: 128 columns each
 
+template <bool kFp8>
 struct TcSmem {
+  static constexpr int kStages = Ring<kFp8>::kStages;
   alignas(1024) uint8_t q[2][kQTile];
-  alignas(1024) uint8_t kv[kStages][kStage];
+  alignas(1024) uint8_t kv[kStages][Ring<kFp8>::kStage];
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full[2], q_free, s_full[2], p_full[2], pv_done[2], o_empty[2], order, mma_done;
   // tidied V tiles, by the stream that does it, alternating; the tokens with a value that is not finite
   uint64_t scanned[2][2];
   uint32_t bad[2][2][2][4];
   float red[2][2][128];  // per stream: the maxima of a row's halves (at a record: sums)
+  float back[kFp8 ? 2 : 1][2][kFp8 ? 128 : 1];  // E4M3: per span parity and query tile, the rows' score factors
   uint32_t tmem;
   int32_t abort_flag;
 };
-static_assert(sizeof(TcSmem) <= 232448, "shared memory of one CTA per SM");
+static_assert(sizeof(TcSmem<false>) <= 232448 && sizeof(TcSmem<true>) <= 232448, "shared memory of one CTA per SM");
 
-__device__ __forceinline__ bool aborted(TcSmem &S) {
+template <typename Smem>
+__device__ __forceinline__ bool aborted(Smem &S) {
   return *reinterpret_cast<volatile int32_t *>(&S.abort_flag) != 0;
 }
 // Wait with a bound; false once the CTA winds down.
-__device__ __forceinline__ bool wait_or_abort(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
+template <typename Smem>
+__device__ __forceinline__ bool wait_or_abort(Smem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
   if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_test(bar, parity)) {
@@ -79,12 +100,14 @@ __device__ __forceinline__ bool wait_or_abort(TcSmem &S, const TreeArgs &a, uint
 
 // wait_or_abort by a whole warp, with one answer for all its lanes: what
 // follows are warp-wide TMEM accesses.
-__device__ __forceinline__ bool warp_wait(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
+template <typename Smem>
+__device__ __forceinline__ bool warp_wait(Smem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_or_abort(S, a, bar, parity));
 }
 // The same for the softmax warps: suspended while they wait.  (Sixteen warps
 // that poll take the issue slots of those that compute.)
-__device__ __forceinline__ void idle_wait(TcSmem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
+template <typename Smem>
+__device__ __forceinline__ void idle_wait(Smem &S, const TreeArgs &a, uint64_t *bar, uint32_t parity) {
   if (!mbar_try(bar, parity)) {
     const long long t0 = clock64();
     while (!mbar_try(bar, parity)) {
@@ -142,9 +165,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&p);
 }
+// The same for 8-bit inputs.
+__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Two numbers as E4M3 codes (first in the low byte), from fp16; and back.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+// (x, y) as two E4M3 parts each: hi and lo = x - hi, two codes in each.  fp16
+// in between keeps 11 bits, more than the parts do together.
+__device__ __forceinline__ void split_e4m3(float x, float y, uint32_t &hi, uint32_t &lo) {
+  const __half2 v = __floats2half2_rn(x, y);
+  hi = e4m3x2(*reinterpret_cast<const uint32_t *>(&v));
+  const uint32_t back = half2_of(hi);
+  const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2 *>(&back));
+  lo = e4m3x2(*reinterpret_cast<const uint32_t *>(&rest));
+}
+
 __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&x)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -183,7 +248,10 @@ struct Walk {
   }
 };
 
-__device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, const CUtensorMap *tv, Walk w) {
+template <bool kFp8>
+__device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *tk, const CUtensorMap *tv, Walk w) {
+  constexpr int kStages = Ring<kFp8>::kStages;
+  constexpr uint32_t kStage = Ring<kFp8>::kStage;
   const uint64_t pol = policy_evict_first();
   int n = 0;  // ring entries issued: K(0), V(0), K(1), V(1), ...
   bool waited = false, go = true;
@@ -203,7 +271,7 @@ __device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, co
         }
         mbar_arrive_expect_tx(&S.kv_full[s], kStage);
         tma_load_3d(S.kv[s], kv ? tv : tk, &S.kv_full[s], 0, row, w.head, pol);
-        tma_load_3d(S.kv[s] + kBox, kv ? tv : tk, &S.kv_full[s], 64, row, w.head, pol);
+        if constexpr (!kFp8) tma_load_3d(S.kv[s] + kBox, kv ? tv : tk, &S.kv_full[s], 64, row, w.head, pol);
       }
     }
   } while (go && w.next());
@@ -217,15 +285,19 @@ __device__ void producer(const TreeArgs &a, TcSmem &S, const CUtensorMap *tk, co
 // of one lane, 8 MMAs took 1200 clocks instead of the 512 the tensor cores
 // need for them.  Even so a tile's waits and 16 MMAs keep a warp busy for
 // 1700 clocks, which is why each stream has its own.)
-__device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int q) {
-  constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0), idesc_pv = idesc_bf16(128, 128, 0, 1);
+template <bool kFp8>
+__device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk w, int q) {
+  constexpr int kStages = Ring<kFp8>::kStages, kStep = Ring<kFp8>::kStep;
+  constexpr uint32_t kStage = Ring<kFp8>::kStage;
+  constexpr uint32_t idesc_qk = kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+  constexpr uint32_t idesc_pv = kFp8 ? idesc_e4m3(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);
   const uint32_t q0 = smem_u32(S.q[0]), kv0 = smem_u32(S.kv[0]);
   const uint64_t a_qk = smem_desc(q0, 16, 1024, kSw128), b_qk = smem_desc(kv0, 16, 1024, kSw128);
   const uint64_t b_pv = smem_desc(kv0, kBox, 1024, kSw128);
   const uint32_t s_tmem = tmem + q * 128, o_tmem = s_tmem + 256;
   int np = 0, no = 0, nspan = 0;  // PVs issued, groups whose PVs have begun, spans
   // the tile whose PV is to come: its V's ring entry (-1: none), its steps of
-  // 16 tokens, whether it is the stream's first of a group
+  // kStep tokens, whether it is the stream's first of a group
   int pend = -1, pend_steps = 0;
   bool pend_first = false, pend_two = false, first = true;
   // Everything but P is waited for first: P is what the products wait for.
@@ -239,9 +311,16 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
     const int s = pend % kStages;
     const uint64_t bs = b_pv + ((s * kStage) >> 4);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < pend_steps)
-        mma_bf16_ts(o_tmem, s_tmem + k * 8, bs + ((k * 2048) >> 4), idesc_pv, !(pend_first && k == 0));
+    for (int k = 0; k < 128 / kStep; ++k)
+      if (k < pend_steps) {
+        const uint64_t b = bs + ((k * kStep * 128) >> 4);
+        if constexpr (kFp8) {
+          mma_f8_ts(o_tmem, s_tmem + k * 8, b, idesc_pv, !(pend_first && k == 0));
+          mma_f8_ts(o_tmem, s_tmem + 32 + k * 8, b, idesc_pv, true);
+        } else {
+          mma_bf16_ts(o_tmem, s_tmem + k * 8, b, idesc_pv, !(pend_first && k == 0));
+        }
+      }
     mma_commit(&S.pv_done[q]);
     mma_commit(&S.kv_empty[s]);
     if (!pend_two) mma_commit(&S.kv_empty[s]);  // (for the other stream, which does not use it)
@@ -290,9 +369,12 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
       if (elect_one()) {
         if (pend >= 0) pv();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d
+        for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d (E4M3: 4 of 32, hi then lo)
           const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-          mma_bf16(s_tmem, as + o, bs + o, idesc_qk, k > 0);
+          if constexpr (kFp8)
+            mma_f8(s_tmem, as + o, bs + (((k & 3) * 32) >> 4), idesc_qk, k > 0);
+          else
+            mma_bf16(s_tmem, as + o, bs + o, idesc_qk, k > 0);
           if (k == 5) mbar_arrive(&S.order);  // (the next turn's first MMA is two MMAs away)
         }
         mma_commit(&S.s_full[q]);
@@ -302,7 +384,7 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
       __syncwarp();
       if (pend >= 0) ++np;
       pend = nk + 1;
-      pend_steps = (min(kT, w.sp.len - (w.tile + t) * kT) + 15) / 16;
+      pend_steps = (min(kT, w.sp.len - (w.tile + t) * kT) + kStep - 1) / kStep;
       pend_first = first;
       pend_two = two;
       first = false;
@@ -325,10 +407,11 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, 
 // rotation is then one line of memory.  (A thread a query touched 32 lines a
 // load and took 8000 clocks for 256 queries.)  src, rot: the query and the
 // rotation's table row of this lane's own query, rot < 0: it does not see the
-// span, and its row of the tile may hold anything.
-template <int N>
+// span, and its row of the tile may hold anything.  back (E4M3): the rows'
+// factors that undo their scaling.
+template <bool kFp8, int N>
 __device__ __forceinline__ void write_queries(const __nv_bfloat16 *q, const uint4 *table, int src, int rot, uint32_t to,
-                                              float scale, int first, int lane) {
+                                              float scale, int first, int lane, float *back) {
   const int c = lane & 7;
   // (rows that see nothing read row 0: loads without branches are all under
   // way before the first is needed, and one trip to L2 costs a thousand
@@ -349,20 +432,44 @@ __device__ __forceinline__ void write_queries(const __nv_bfloat16 *q, const uint
   for (int i = 0; i < N / 4; ++i) {
     const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     const uint32_t w[8] = {cs[i][0].x, cs[i][0].y, cs[i][0].z, cs[i][0].w, cs[i][1].x, cs[i][1].y, cs[i][1].z, cs[i][1].w};
-    uint32_t p[4], r[4];
+    float p[8], r[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 w0 = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * j]));
-      const float2 w1 = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * j + 1]));
-      const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xffff0000u);
-      const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xffff0000u);
-      p[j] = pack_bf16((x0 * w0.x - y0 * w0.y) * scale, (x1 * w1.x - y1 * w1.y) * scale);
-      r[j] = pack_bf16((y0 * w0.x + x0 * w0.y) * scale, (y1 * w1.x + x1 * w1.y) * scale);
+    for (int j = 0; j < 8; ++j) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+      const float x0 = __uint_as_float(j & 1 ? x[j / 2] & 0xffff0000u : x[j / 2] << 16);
+      const float y0 = __uint_as_float(j & 1 ? y[j / 2] & 0xffff0000u : y[j / 2] << 16);
+      p[j] = (x0 * t.x - y0 * t.y) * scale;
+      r[j] = (y0 * t.x + x0 * t.y) * scale;
     }
     const int at = first + 4 * i + (lane >> 3);
-    const uint32_t o = to + at * 128 + ((c ^ (at & 7)) << 4);
-    st_shared_v4(o, p[0], p[1], p[2], p[3]);
-    st_shared_v4(o + kBox, r[0], r[1], r[2], r[3]);
+    const uint32_t o = to + at * 128;
+    if constexpr (kFp8) {
+      // a power of two brings the largest element into [128, 256)
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max3(top, fabsf(p[j]), fabsf(r[j]));
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      // (exponent of top, at most 2^127; the two factors' product is 1)
+      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 20), 240);
+      const float up = __uint_as_float(static_cast<uint32_t>(254 + 7 - e) << 23);  // 2^(7 - exponent)
+      if (c == 0) back[at] = top < INFINITY ? __uint_as_float(static_cast<uint32_t>(e - 7) << 23) : NAN;
+      uint32_t hp[4], lp[4], hr[4], lr[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        split_e4m3(p[2 * j] * up, p[2 * j + 1] * up, hp[j], lp[j]);
+        split_e4m3(r[2 * j] * up, r[2 * j + 1] * up, hr[j], lr[j]);
+      }
+      const uint32_t o0 = o + (((c >> 1) ^ (at & 7)) << 4) + (c & 1) * 8, o1 = o + (((4 + (c >> 1)) ^ (at & 7)) << 4) + (c & 1) * 8;
+      st_shared_v2(o0, hp[0] | hp[1] << 16, hp[2] | hp[3] << 16);
+      st_shared_v2(o1, hr[0] | hr[1] << 16, hr[2] | hr[3] << 16);
+      st_shared_v2(o0 + kBox, lp[0] | lp[1] << 16, lp[2] | lp[3] << 16);
+      st_shared_v2(o1 + kBox, lr[0] | lr[1] << 16, lr[2] | lr[3] << 16);
+    } else {
+      const uint32_t oc = o + ((c ^ (at & 7)) << 4);
+      st_shared_v4(oc, pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+      st_shared_v4(oc + kBox, pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]), pack_bf16(r[4], r[5]), pack_bf16(r[6], r[7]));
+    }
   }
 }
 
@@ -374,7 +481,7 @@ __device__ __forceinline__ void pair_sync(int id) {
 // Half of one row's record: 64 of O's columns, 32 bytes of every 8 d side by
 // side for the group's columns, so that a warp's stores fill whole sectors.
 __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem, int64_t rec, int n_cols, int col,
-                                             int half) {
+                                             int half, float scale) {
   float *dst = tree_at<float>(a, a.L.o) + rec * 128 + col * 8 + static_cast<int64_t>(half) * 8 * n_cols * 8;
   const bool on = col < n_cols;
 #pragma unroll
@@ -382,6 +489,8 @@ __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem,
     uint32_t r[32];
     tmem_ld32(o_tmem + 64 * half + 32 * c, r);
     tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * scale);
     if (on) {
 #pragma unroll
       for (int x = 0; x < 4; ++x)
@@ -403,6 +512,11 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
 __device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -412,7 +526,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // The softmax of a stream.  Its waits give up together (abort_flag), and the
 // code then runs on to its end without waiting, on whatever the tiles hold:
 // the named barriers in it stay matched.
-__device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int q) {
+template <bool kFp8>
+__device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk w, int q) {
+  constexpr int kStages = Ring<kFp8>::kStages, kStep = Ring<kFp8>::kStep;
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = (threadIdx.x >> 7) & 1;
   const int row = quarter * 32 + lane, pair = 1 + q * 4 + quarter;
   const uint32_t s_tmem = tmem + q * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -425,6 +541,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
   // the record to come: that of the group before (0 columns: none)
   int64_t rec = 0;
   int rec_cols = 0, rec_col = 0;
+  float rec_scale = 1.f;   // E4M3: its kv head's v_scale
   bool some = false;       // the stream had a tile of it
   TreeColumn tc = {};
   int src = 0;             // the row's query (row 0 where there is none)
@@ -439,7 +556,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
             some ? make_float2(m, l + S.red[q][1][row]) : make_float2(-INFINITY, 0.f);
       pair_sync(pair);
       tc_fence_after();
-      if (some) store_record(a, o_tmem, rec, rec_cols, rec_col, half);
+      if (some) store_record(a, o_tmem, rec, rec_cols, rec_col, half, rec_scale);
     }
     tc_fence_before();
     __syncwarp();
@@ -471,10 +588,12 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
       const int rot = v < 0 ? -1 : tc.rot + v * tc.n_nodes;
       // two query tiles: a tile a stream, half of a warp's rows a half; one: a quarter each
       const uint32_t to = smem_u32(S.q[two ? q : 0]) + quarter * 32 * 128;
+      const float scale = kFp8 ? a.scale_log2 * a.k_scale[w.head] : a.scale_log2;
+      float *back = &S.back[kFp8 ? nspan & 1 : 0][two ? q : 0][kFp8 ? quarter * 32 : 0];
       if (two)
-        write_queries<16>(qs, table, src, rot, to, a.scale_log2, 16 * half, lane);
+        write_queries<kFp8, 16>(qs, table, src, rot, to, scale, 16 * half, lane, back);
       else
-        write_queries<8>(qs, table, src, rot, to, a.scale_log2, 8 * (2 * q + half), lane);
+        write_queries<kFp8, 8>(qs, table, src, rot, to, scale, 8 * (2 * q + half), lane, back);
       fence_proxy_async_smem();
     }
     __syncwarp();
@@ -484,6 +603,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
       const int64_t k = static_cast<int64_t>(w.head) * w.n_groups + w.group;
       rec_cols = w.g.n_cols;
       rec_col = col;
+      if (kFp8) rec_scale = a.v_scale[w.head];
       // one record a CTA, or one a stream
       const int nth = static_cast<int>(blockIdx.x) - tree_at<int2>(a, a.L.piece_cta)[k].x;
       rec = tree_at<int32_t>(a, a.L.piece_row)[k] + static_cast<int64_t>(two ? nth : 2 * nth + q) * rec_cols;
@@ -494,7 +614,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
     for (int t = 0; t < w.tiles; ++t, ++i, turn ^= 1) {
       const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
       const int owner = two ? 0 : turn;  // who tidies the V tile, where that is needed
-      const bool tidy = w.sp.partial || (valid & 15);
+      const bool tidy = w.sp.partial || (valid & (kStep - 1));
       if (!two && turn != q) {
         if (tidy) ++(owner ? np1 : np0);
         continue;
@@ -505,24 +625,26 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
         const int nv = 2 * i + 1, np = owner ? np1 : np0, par = np & 1;
         if (q == owner) {
           // 0 * NaN would poison a sum.  V rows past the span, up to the end
-          // of the last step of 16 tokens, may hold anything: cleared.  In a
+          // of the last step of tokens, may hold anything: cleared.  In a
           // tile that not every column sees, so are values that are not
           // finite: the columns that see their token get a NaN through l.
           idle_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1);
-          const uint32_t at = smem_u32(S.kv[nv % kStages]) + half * kBox + row * 128;
-          const bool clear = row >= valid && row < ((valid + 15) & ~15);
+          constexpr int kPieces = kFp8 ? 4 : 8;  // 16-byte pieces of a row's half
+          const uint32_t at = smem_u32(S.kv[nv % kStages]) + half * (kFp8 ? 64 : kBox) + row * 128;
+          const bool clear = row >= valid && row < ((valid + kStep - 1) & ~(kStep - 1));
           bool odd = false;
           if (w.sp.partial && row < valid)
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < kPieces; ++c) {
               uint32_t x[4];
-              ld_shared_v4(at + ((c + row) & 7) * 16, x);
+              ld_shared_v4(at + ((c + row) & (kPieces - 1)) * 16, x);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                odd |= (x[j] & 0x7f80u) == 0x7f80u || (x[j] & 0x7f800000u) == 0x7f800000u;
+                odd |= kFp8 ? __vcmpeq4(x[j] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0
+                            : (x[j] & 0x7f80u) == 0x7f80u || (x[j] & 0x7f800000u) == 0x7f800000u;
             }
           if (clear || odd) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) st_shared_v4(at + c * 16, 0, 0, 0, 0);
+            for (int c = 0; c < kPieces; ++c) st_shared_v4(at + c * 16, 0, 0, 0, 0);
             fence_proxy_async_smem();
           }
           const uint32_t bits = __ballot_sync(0xffffffffu, odd);
@@ -566,12 +688,15 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
         S.red[q][half][row] = top;
         pair_sync(pair);
         top = fmaxf(top, S.red[q][half ^ 1][row]);
+        const float f = kFp8 ? S.back[kFp8 ? (nspan - 1) & 1 : 0][two ? q : 0][kFp8 ? row : 0] : 1.f;
+        if constexpr (kFp8) top *= f;
+        constexpr float lift = kFp8 ? kLift : 0.f;
         if (!some) {
-          m = fmaxf(top, -1e30f);  // (nothing seen yet: weights 0, no NaN)
+          m = fmaxf(top - lift, -1e30f);  // (nothing seen yet: weights 0, no NaN)
           l = 0.f;
         } else if (__any_sync(0xffffffffu, mine && top > m + kLazy)) {
           // (rows without a query hold anything: they must not count)
-          const float to = top > m + kLazy ? top : m, al = ex2(m - to);
+          const float to = top > m + kLazy ? top - lift : m, al = ex2(m - to);
           m = to;
           l *= al;
           idle_wait(S, a, &S.pv_done[q], (ns - 1) & 1);
@@ -586,19 +711,32 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
             tmem_st8(o_tmem + 64 * half + 8 * c, r);
           }
         }
-        const uint64_t neg = pack2(-m, -m);
+        const uint64_t neg = pack2(-m, -m), mul = pack2(f, f);
         uint64_t sum[2] = {0, 0};
-        uint32_t p[32];
+        uint32_t p[kFp8 ? 1 : 32], hi[kFp8 ? 16 : 1], lo[kFp8 ? 16 : 1];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
+          const uint64_t s2 = pack2(__uint_as_float(s[j / 16][2 * j % 32]), __uint_as_float(s[j / 16][2 * j % 32 + 1]));
           float p0, p1;
-          unpack2(add2(pack2(__uint_as_float(s[j / 16][2 * j % 32]), __uint_as_float(s[j / 16][2 * j % 32 + 1])), neg), p0, p1);
+          unpack2(kFp8 ? fma2(s2, mul, neg) : add2(s2, neg), p0, p1);
           p0 = ex2(p0);
           p1 = ex2(p1);
           sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
-          p[j] = pack_bf16(p0, p1);
+          if constexpr (kFp8) {
+            uint32_t h2, l2;
+            split_e4m3(p0, p1, h2, l2);
+            hi[j / 2] = j & 1 ? hi[j / 2] | h2 << 16 : h2;
+            lo[j / 2] = j & 1 ? lo[j / 2] | l2 << 16 : l2;
+          } else {
+            p[j] = pack_bf16(p0, p1);
+          }
         }
-        tmem_st32(s_tmem + 32 * half, p);
+        if constexpr (kFp8) {  // four codes a column: hi in 0 .. 31, lo in 32 .. 63
+          tmem_st16(s_tmem + 16 * half, hi);
+          tmem_st16(s_tmem + 32 + 16 * half, lo);
+        } else {
+          tmem_st32(s_tmem + 32 * half, p);
+        }
         float x[4];
         unpack2(sum[0], x[0], x[1]);
         unpack2(sum[1], x[2], x[3]);
@@ -620,11 +758,12 @@ __device__ void softmax(const TreeArgs &a, TcSmem &S, uint32_t tmem, Walk w, int
 // records' memory may be used at once, and only the trees' tiles wait for the
 // launch before (the producer).  Every CTA waits for it before it ends, so
 // that whoever follows this grid follows the append too.
+template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  TcSmem &S = *reinterpret_cast<TcSmem *>(smem_raw);
+  TcSmem<kFp8> &S = *reinterpret_cast<TcSmem<kFp8> *>(smem_raw);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!tree_plan_ok(a)) {
@@ -643,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.g = w.groups[w.group];
   w.load_span();
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < Ring<kFp8>::kStages; ++s) {
       mbar_init(&S.kv_full[s], 1);
       mbar_init(&S.kv_empty[s], 2);  // one arrival a stream
     }
@@ -686,11 +825,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
-  const size_t smem = sizeof(TcSmem);
+namespace {
+template <bool kFp8>
+cudaError_t launch(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
+  const size_t smem = sizeof(TcSmem<kFp8>);
   static bool configured = false;
   if (!configured) {
-    const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     configured = true;
@@ -705,7 +846,12 @@ cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_tc_kernel, a, tk, tv);
+  return cudaLaunchKernelEx(&cfg, tree_tc_kernel<kFp8>, a, tk, tv);
+}
+}  // namespace
+
+cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
+  return a.dtype == HW_FP8_E4M3 ? launch<true>(a, tk, tv, s) : launch<false>(a, tk, tv, s);
 }
 
 }  // namespace hw
