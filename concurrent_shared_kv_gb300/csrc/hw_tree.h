@@ -74,6 +74,8 @@ struct TreeColumn {
 };
 struct TreeCta {
   int32_t head, group, span, tile, n_units;  // first unit and count
+  TreeGroup g;                               // copies: one load instead of three in a row
+  TreeSpan sp;
 };
 
 // Byte offsets of the plan's arrays in the workspace (the error word is at 0).
@@ -118,6 +120,7 @@ struct TreeVerifyArgs {
   const float *u_accept, *u_sample;
   int32_t *path, *n_path, *next_token;
   int32_t n_rows, max_nodes, vocab, dtype;
+  int32_t keep;  // slices fit shared memory (set by the launch)
 };
 
 TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms);

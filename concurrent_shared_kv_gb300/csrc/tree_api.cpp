@@ -184,7 +184,7 @@ int hw_tree_verify(int32_t dtype, int32_t n_rows, int32_t max_nodes, int32_t voc
   const uintptr_t esz = dtype == HW_F32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & (esz - 1)) return HW_ERR_INVALID;
   const TreeVerifyArgs a = {p, q, p_stride, q_stride, n_nodes, parent, token, u_accept, u_sample,
-                            path, n_path, next_token, n_rows, max_nodes, vocab, dtype};
+                            path, n_path, next_token, n_rows, max_nodes, vocab, dtype, 0};
   const cudaError_t e = launch_tree_verify(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HW_OK : cuda_fail(e);
 }

@@ -427,7 +427,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       }
     }
     S.uidx[c] = h < a.n_kv_heads ? h * UH + ubase[g] + spans[groups[g].span0 + s].tile0 + t : UH * a.n_kv_heads;
-    first = TreeCta{h, g, s, t, 0};
+    first.head = h;
+    first.group = g;
+    first.span = s;
+    first.tile = t;
   }
   __syncthreads();
   // a share without a unit gets no CTA: those with units are numbered anew
@@ -436,6 +439,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   const int n_ctas = static_cast<int>(S.carry);
   if (n_units > 0) {
     first.n_units = n_units;
+    first.g = groups[first.group];
+    first.sp = spans[first.g.span0 + first.span];
     ctas[number] = first;
     S.number[tid] = static_cast<int16_t>(number);
   }
@@ -542,18 +547,18 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
   // the attention kernel counts on it.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (!tree_plan_ok(a)) return;  // the attention launch records it
   const int lane = threadIdx.x & 31, half = a.head_dim / 2, D = a.head_dim;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int h = static_cast<int>(item % a.n_kv_heads);
   const int64_t node = item / a.n_kv_heads;
   const int r = static_cast<int>(node / a.max_nodes), i = static_cast<int>(node % a.max_nodes);
-  if (r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) return;
+  const int row = min(r, a.n_rows - 1);
+  const int nodes = tree_at<int32_t>(a, a.L.n_nodes)[row], rot0 = tree_at<int32_t>(a, a.L.rot0)[row];
+  const int64_t slot = static_cast<int64_t>(tree_at<int32_t>(a, a.L.slot)[row]) + i;
+  // (without a plan the attention launch says so)
+  if (!tree_plan_ok(a) || r >= a.n_rows || i >= nodes) return;
   // the keys turn as the queries do against their own tree
-  const int nodes = tree_at<int32_t>(a, a.L.n_nodes)[r];
-  const float2 *rot = tree_at<float2>(a, a.L.rot) +
-                      (tree_at<int32_t>(a, a.L.rot0)[r] + static_cast<int64_t>(a.n_view) * nodes + i) * half;
-  const int64_t slot = static_cast<int64_t>(tree_at<int32_t>(a, a.L.slot)[r]) + i;
+  const float2 *rot = tree_at<float2>(a, a.L.rot) + (rot0 + static_cast<int64_t>(a.n_view) * nodes + i) * half;
   const T *kn = reinterpret_cast<const T *>(a.k_new) + item * D;
   const T *vn = reinterpret_cast<const T *>(a.v_new) + item * D;
   const int64_t to = (h * a.capacity + slot) * D;
@@ -588,21 +593,26 @@ constexpr int kMergeWarps = 8;
 //   M = max m,  out = sum o 2^(m - M) / sum l 2^(m - M),  lse = (M + log2 l) ln 2.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int EPL = D / 32;
+  constexpr int EPL = D / 32, kBatch = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp;
   const int G = a.n_q_heads / a.n_kv_heads;
   const int x = static_cast<int>(item % a.n_q_heads);  // place in the head list: kv head, then its q heads
   const int64_t node = item / a.n_q_heads;
   const int r = static_cast<int>(node / a.max_nodes), i = static_cast<int>(node % a.max_nodes);
-  if (!tree_plan_ok(a) || r >= a.n_rows || i >= tree_at<int32_t>(a, a.L.n_nodes)[r]) {
+  const int row = min(r, a.n_rows - 1);
+  // (loads that do not hang on one another first: trips to L2 are what this
+  // kernel takes)
+  const int n_nodes = tree_at<int32_t>(a, a.L.n_nodes)[row], hq = tree_at<int32_t>(a, a.L.heads)[x];
+  const int2 run = tree_at<int2>(a, a.L.run)[row];
+  const int first = tree_at<int32_t>(a, a.L.col)[row];
+  const int n_groups = tree_at<const TreeHeader>(a, a.L.hdr)->n_groups;
+  if (!tree_plan_ok(a) || r >= a.n_rows || i >= n_nodes) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever follows this grid follows that one
     return;
   }
-  const int n_groups = tree_at<const TreeHeader>(a, a.L.hdr)->n_groups;
-  const int h = x / G, hq = tree_at<int32_t>(a, a.L.heads)[x];
-  const int2 run = tree_at<int2>(a, a.L.run)[r];
-  const int in_run = tree_at<int32_t>(a, a.L.col)[r] + i * G + x % G - run.y;
+  const int h = x / G;
+  const int in_run = first + i * G + x % G - run.y;
   const int g = run.x + in_run / a.L.cols, col = in_run % a.L.cols;
   const int n_cols = tree_at<TreeGroup>(a, a.L.groups)[g].n_cols;
   const int64_t k = static_cast<int64_t>(h) * n_groups + g;
@@ -610,31 +620,50 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   const int64_t row0 = tree_at<int32_t>(a, a.L.piece_row)[k];
   const float2 *ml = tree_at<float2>(a, a.L.ml) + row0 + col;
   const float *o = tree_at<float>(a, a.L.o) + record_at(row0, n_cols, col, lane * EPL, D);
+  const int64_t step = static_cast<int64_t>(n_cols) * D;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the records
-  float M = -INFINITY;
-  for (int j = lane; j < n; j += 32) M = fmaxf(M, ml[j * n_cols].x);
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float L = 0.f, acc[EPL];
+  float M = -INFINITY, L = 0.f, acc[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const float2 x2 = ml[j * n_cols];
-    const float *src = o + static_cast<int64_t>(j) * n_cols * D;
-    const bool none = x2.x == -INFINITY;  // a record without tiles: no output either
-    const float w = none ? 0.f : ex2(x2.x - M);
-    L += x2.y * w;
-    float val[EPL];
-    if constexpr (EPL == 4) {
-      const float4 y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(src);
-      val[0] = y.x; val[1] = y.y; val[2] = y.z; val[3] = y.w;
-    } else {
-      const float2 y = none ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(src);
-      val[0] = y.x; val[1] = y.y;
-    }
+  for (int j0 = 0; j0 < n; j0 += 32) {  // a lane a record's (m, l)
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (j0 + lane < n) mine = ml[static_cast<int64_t>(j0 + lane) * n_cols];
+    float top = fmaxf(M, mine.x);
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, val[e], acc[e]);
+    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float old = M == -INFINITY ? 0.f : ex2(M - top);
+    const float w = mine.x == -INFINITY ? 0.f : ex2(mine.x - top);  // a record without tiles: no output either
+    M = top;
+    float sum = mine.y * w;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    L = L * old + sum;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] *= old;
+    const int last = min(32, n - j0);
+    for (int j1 = 0; j1 < last; j1 += kBatch) {  // kBatch outputs under way
+      float val[kBatch][EPL], wj[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        wj[b] = __shfl_sync(0xffffffffu, w, j1 + b);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) val[b][e] = 0.f;
+        if (j1 + b < last && wj[b] > 0.f) {
+          const float *src = o + (j0 + j1 + b) * step;
+          if constexpr (EPL == 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(src);
+            val[b][0] = y.x; val[b][1] = y.y; val[b][2] = y.z; val[b][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2 *>(src);
+            val[b][0] = y.x; val[b][1] = y.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] = fmaf(wj[b], val[b][e], acc[e]);
+    }
   }
   const float inv = 1.f / L;  // (a node attends itself; NaN where its values are)
   T res[EPL];

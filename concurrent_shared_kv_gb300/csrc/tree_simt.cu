@@ -52,14 +52,14 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<D> &S = *reinterpret_cast<Smem<D> *>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!tree_plan_ok(a)) {
-    if (tid == 0) flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_BAD_PLAN);
-    return;
-  }
-  const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int c = blockIdx.x;
-  if (c >= hdr.n_ctas) return;
   TreeCta at = tree_at<TreeCta>(a, a.L.ctas)[c];
+  const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
+  const bool ok = tree_plan_ok(a), work = ok && c < hdr.n_ctas;
+  if (!ok && tid == 0) flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_BAD_PLAN);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the trees' tokens
+  if (!work) return;
   const TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
   const TreeSpan *spans = tree_at<TreeSpan>(a, a.L.spans);
   const int G = a.n_q_heads / a.n_kv_heads;
@@ -226,8 +226,18 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured = true;
   }
-  tree_simt_kernel<T, D><<<a.L.ctas_max, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  // a dependent of the append launch (tree_plan.cu), started while that ends
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.L.ctas_max);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_simt_kernel<T, D>, a);
 }
 
 }  // namespace

@@ -226,6 +226,9 @@ struct Walk {
   int tiles;  // of this span that are the CTA's
   __device__ __forceinline__ void load_span() {
     sp = spans[g.span0 + span];
+    begin();
+  }
+  __device__ __forceinline__ void begin() {
     asm volatile("prefetch.global.L1 [%0];" ::"l"(spans + g.span0 + span + 1));
     tiles = min((sp.len + kT - 1) / kT - tile, left);
   }
@@ -568,10 +571,15 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     const int col = two ? q * 128 + row : row;               // the thread's column of the group
     const bool mine = col < w.g.n_cols;                      // a query in this row
     const bool warp_on = col - lane < w.g.n_cols;
+    int heads = 0;  // the kv head's q heads, a lane each
+    if (step == 2) {
+      const int G = a.n_q_heads / a.n_kv_heads;
+      heads = tree_at<int32_t>(a, a.L.heads)[w.head * G + min(lane, G - 1)];
+    }
     if (mine && step == 2) {
       tc = tree_at<TreeColumn>(a, a.L.columns)[w.g.col0 + col];
-      src = tc.node * a.n_q_heads + tree_at<int32_t>(a, a.L.heads)[w.head * (a.n_q_heads / a.n_kv_heads) + tc.head];
     }
+    if (step == 2) src = tc.node * a.n_q_heads + __shfl_sync(0xffffffffu, heads, tc.head);
     // the tokens the column sees: all, a node's ancestors and itself, or none
     uint2 see = make_uint2(0, 0);
     int v = -1;
@@ -766,21 +774,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   TcSmem<kFp8> &S = *reinterpret_cast<TcSmem<kFp8> *>(smem_raw);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (!tree_plan_ok(a)) {
-    if (tid == 0) flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_BAD_PLAN);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
-  if (static_cast<int>(blockIdx.x) >= hdr.n_ctas) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  // (the grid is at most ctas_max: the record is there, whatever it holds)
   const TreeCta c = tree_at<TreeCta>(a, a.L.ctas)[blockIdx.x];
+  const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
+  const bool ok = tree_plan_ok(a);
+  if (!ok || static_cast<int>(blockIdx.x) >= hdr.n_ctas) {
+    if (!ok && tid == 0) flag_error(reinterpret_cast<int32_t *>(a.ws), HW_DEV_BAD_PLAN);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   Walk w = {tree_at<TreeGroup>(a, a.L.groups), tree_at<TreeSpan>(a, a.L.spans), hdr.n_groups,
-            c.head, c.group, c.span, c.tile, c.n_units, {}, {}, 0};
-  w.g = w.groups[w.group];
-  w.load_span();
+            c.head, c.group, c.span, c.tile, c.n_units, c.g, c.sp, 0};
+  w.begin();
   if (tid == 0) {
     for (int s = 0; s < Ring<kFp8>::kStages; ++s) {
       mbar_init(&S.kv_full[s], 1);

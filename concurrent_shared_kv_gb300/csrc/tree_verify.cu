@@ -10,13 +10,16 @@
 // u q(x) s_k < a_k(x); with none left, the next token is the first x whose
 // running sum of a_k passes u s.
 //
-// Arithmetic: unsigned fixed point, 56 bits behind the point.  A probability
-// from 2^-32 up is exact, smaller ones and the products lose less than 2^-56
-// each, and sums do not depend on their order, so the decisions are those of
-// a 64-bit evaluation and the same on every run.  (fp32 sums would misplace
-// the drawn token with a probability of about vocab x 2^-27.)
+// Arithmetic: what is decided is decided in integers, with 56 bits behind the
+// point.  The single values of a test are exact (a probability from 2^-32 up)
+// or lose less than 2^-56; an element of a sum is p - c q in fp32 with c as two
+// floats - an error of 2^-24 of the difference itself - rounded to 43 bits
+// behind the point and added as an integer.  Sums so do not depend on their
+// order, runs repeat, and a running sum over a vocabulary of 2^17 is off by
+// some 1e-10, where fp32 sums would misplace the drawn token once in a
+// thousand draws.
 //
-// One cluster of 8 CTAs a row: the vocabulary is cut into one slice a warp,
+// One cluster of 8 or 16 CTAs a row: the vocabulary is cut into one slice a warp,
 // a rejection costs one pass over the node's two rows of probabilities, and
 // the slices' sums are joined through distributed shared memory.  Everything
 // else needs single values: every drafted token's p and q are fetched at
@@ -24,6 +27,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include "hw_internal.h"
 #include "hw_tree.h"
 
 namespace hw {
@@ -33,8 +37,7 @@ namespace {
 namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kSlices = kCluster * kWarps;
+constexpr int kMaxCluster = 16;
 constexpr int kShift = 56;
 constexpr uint64_t kOne = 1ull << kShift;
 
@@ -49,6 +52,66 @@ __device__ __forceinline__ uint64_t mul_fix(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t left_of(uint64_t p, uint64_t c, uint64_t q) {
   const uint64_t t = mul_fix(c, q);
   return p > t ? p - t : 0;
+}
+// Packed fp32: two numbers an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// max(p - c q, 0) of two pairs held to [0, 1] (NaN counts as 0), c = c0 + c1.
+template <bool kFirst>
+__device__ __forceinline__ void left2(float &p0, float &p1, float c0, float c1, float q0, float q1) {
+  const uint64_t p = pack2(__saturatef(p0), __saturatef(p1)), q = pack2(__saturatef(q0), __saturatef(q1));
+  unpack2(kFirst ? fma2(pack2(-1.f, -1.f), q, p) : fma2(pack2(-c1, -c1), q, fma2(pack2(-c0, -c0), q, p)), p0, p1);
+  p0 = fmaxf(p0, 0.f);
+  p1 = fmaxf(p1, 0.f);
+}
+// Numbers in [0, 1] as k0 2^-20 + k1 2^-43, both rounded to nearest: adding a
+// constant leaves the integer in the last bits of the sum.
+struct Pieces {
+  uint32_t k0 = 0, k1 = 0;
+  __device__ __forceinline__ void add(float x0, float x1) {
+    const uint64_t x = pack2(x0, x1);
+    const uint64_t a = add2(x, pack2(12.f, 12.f));  // 2^3 .. 2^4: steps of 2^-20
+    const uint64_t d = fma2(add2(a, pack2(-12.f, -12.f)), pack2(-1.f, -1.f), x);  // at most 2^-21, exact
+    const uint64_t b = add2(d, pack2(0x1.8p-20f, 0x1.8p-20f));                    // steps of 2^-43
+    float a0, a1, b0, b1;
+    unpack2(a, a0, a1);
+    unpack2(b, b0, b1);
+    k0 += __float_as_uint(a0) + __float_as_uint(a1) - 2 * __float_as_uint(12.f);
+    k1 += __float_as_uint(b0) + __float_as_uint(b1) - 2 * __float_as_uint(0x1.8p-20f);
+  }
+  // 56 bits behind the point (up to 512 numbers: |k1| stays below 2^31)
+  __device__ __forceinline__ uint64_t sum() const {
+    return (static_cast<uint64_t>(k0) << (kShift - 20)) +
+           static_cast<uint64_t>(static_cast<int64_t>(static_cast<int32_t>(k1)) << (kShift - 43));
+  }
+};
+__device__ __forceinline__ uint64_t pieces(float x) {
+  Pieces k;
+  k.add(x, 0.f);
+  return k.sum();
+}
+
+// c as two floats: off by at most 2^-49 of it.
+__device__ __forceinline__ void split_c(uint64_t c, float &c0, float &c1) {
+  c0 = __ull2float_rn(c);
+  c1 = __ll2float_rn(static_cast<int64_t>(c - __float2ull_rn(c0))) * 0x1p-56f;
+  c0 *= 0x1p-56f;
 }
 
 // A row of probabilities.  Vector loads start at multiples of four elements
@@ -101,20 +164,128 @@ struct Smem {
   int32_t parent[kMaxNodes], token[kMaxNodes];
   uint64_t px[kMaxNodes], qx[kMaxNodes], u[kMaxNodes];
   uint64_t wsum[kWarps];
-  uint64_t total[2][kCluster];  // per pass parity: every CTA's sum
+  uint64_t total[2][kMaxCluster];  // per pass parity: every CTA's sum
   uint64_t scan[kWarps];
   int32_t path[kMaxNodes], gone[kMaxNodes];  // accepted nodes; tokens removed at the current node
   // the walk, written by thread 0
   int32_t cur, next, n_path, n_gone, again;
   uint64_t c, s;
+  float c0, c1;    // the next pass's c
   int32_t bad;
   int32_t slice;   // the drawn token's warp slice in this CTA, or -1
   uint64_t target;  // what is left of the draw there
 };
 
+// The CTA's slices of a node's two rows in shared memory, so that the passes
+// after a node's first, and the draw, need not go to memory again.
 template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    tree_verify_kernel(const __grid_constant__ TreeVerifyArgs a) {
+struct Kept {
+  T *p, *q;  // null: the slices are too long
+  int y0;    // the CTA's first position
+};
+__device__ __forceinline__ void put4(float *to, const float (&x)[4]) {
+  *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void put4(__nv_bfloat16 *to, const float (&x)[4]) {  // (bf16 values: exact)
+  *reinterpret_cast<uint2 *>(to) =
+      make_uint2(__float_as_uint(x[0]) >> 16 | (__float_as_uint(x[1]) & 0xffff0000u),
+                 __float_as_uint(x[2]) >> 16 | (__float_as_uint(x[3]) & 0xffff0000u));
+}
+
+// What is left of four tokens, in place of x; the same added to a sum.
+template <bool kFirst, bool kDraft>
+__device__ __forceinline__ void left4(float (&x)[4], const float (&z)[4], float c0, float c1) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    if (kDraft) {
+      left2<kFirst>(x[e], x[e + 1], c0, c1, z[e], z[e + 1]);
+    } else {
+      x[e] = __saturatef(x[e]);
+      x[e + 1] = __saturatef(x[e + 1]);
+    }
+  }
+}
+template <bool kFirst, bool kDraft>
+__device__ __forceinline__ void add4(Pieces &k, float (&x)[4], const float (&z)[4], float c0, float c1) {
+  left4<kFirst, kDraft>(x, z, c0, c1);
+  k.add(x[0], x[1]);
+  k.add(x[2], x[3]);
+}
+
+// N steps of 128 positions, all of their loads first.  kFrom: memory (0), the
+// same and kept (1), what was kept (2).
+template <typename T, bool kFirst, bool kDraft, int kFrom, int N>
+__device__ __forceinline__ void steps(const Row<T> &p, const Row<T> &q, const Kept<T> &kept, float c0, float c1, int y,
+                                      Pieces &k) {
+  float x[N][4], z[kDraft ? N : 1][4];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = y + 128 * i;
+    four(kFrom == 2 ? kept.p + (at - kept.y0) : p.at + at, x[i]);
+    if constexpr (kDraft) four(kFrom == 2 ? kept.q + (at - kept.y0) : q.at + at, z[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (kFrom == 1) {
+      put4(kept.p + (y + 128 * i - kept.y0), x[i]);
+      if constexpr (kDraft) put4(kept.q + (y + 128 * i - kept.y0), z[i]);
+    }
+    add4<kFirst, kDraft>(k, x[i], z[kDraft ? i : 0], c0, c1);
+  }
+}
+
+// One pass over a warp's slice [y0, y1): the sum of max(p - c q, 0), or of p.
+// (60 instructions an element with 64-bit integers throughout, and the
+// instructions were what a pass took; about 15 so.)
+template <typename T, bool kFirst, bool kDraft, int kFrom>
+__device__ __forceinline__ uint64_t slice_sum(const Row<T> &p, const Row<T> &q, const Kept<T> &kept, float c0, float c1,
+                                              int y0, int y1, int lane) {
+  uint64_t sum = 0;
+  for (int yb = y0; yb < y1; yb += 128 * 64) {  // (512 elements a lane at most)
+    Pieces k;
+    const int stop = min(y1, yb + 128 * 64);
+    int y = yb + 4 * lane;
+    // Inside the row and with both rows alike in memory, plain vector loads:
+    // up to eight steps' are under way together.
+    if (kFrom == 2 || (yb >= p.off && (!kDraft || p.off == q.off))) {
+      int left = kFrom == 2 ? (stop - yb + 127) / 128 : (min(stop, p.end) - yb) / 128;
+      for (; left >= 8; left -= 8, y += 1024) steps<T, kFirst, kDraft, kFrom, 8>(p, q, kept, c0, c1, y, k);
+      if (left & 4) steps<T, kFirst, kDraft, kFrom, 4>(p, q, kept, c0, c1, y, k), y += 512;
+      if (left & 2) steps<T, kFirst, kDraft, kFrom, 2>(p, q, kept, c0, c1, y, k), y += 256;
+      if (left & 1) steps<T, kFirst, kDraft, kFrom, 1>(p, q, kept, c0, c1, y, k), y += 128;
+    }
+    if (kFrom < 2)
+      for (; y - 4 * lane < stop; y += 128) {  // (whole steps: what is kept ends with zeros)
+        float x[4], z[4];
+        load_p(p, y, x);
+        if (kDraft) load_q(p, q, y, z);
+        if (kFrom == 1) {
+          put4(kept.p + (y - kept.y0), x);
+          if (kDraft) put4(kept.q + (y - kept.y0), z);
+        }
+        add4<kFirst, kDraft>(k, x, z, c0, c1);
+      }
+    sum += k.sum();
+  }
+  return sum;
+}
+template <typename T, bool kFirst, bool kDraft>
+__device__ __forceinline__ uint64_t slice_sum_from(int from, const Row<T> &p, const Row<T> &q, const Kept<T> &kept, float c0,
+                                                   float c1, int y0, int y1, int lane) {
+  return from == 0   ? slice_sum<T, kFirst, kDraft, 0>(p, q, kept, c0, c1, y0, y1, lane)
+         : from == 1 ? slice_sum<T, kFirst, kDraft, 1>(p, q, kept, c0, c1, y0, y1, lane)
+                     : slice_sum<T, kFirst, kDraft, 2>(p, q, kept, c0, c1, y0, y1, lane);
+}
+
+// Positions of a warp's slice: whole steps of 128 (a lane's 4 x 32 lanes).
+__host__ __device__ __forceinline__ int slice_length(int vocab, int slices) {
+  return ((vocab + 3 + slices - 1) / slices + 127) / 128 * 128;
+}
+
+template <typename T, int kCluster>
+__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_constant__ TreeVerifyArgs a) {
+  constexpr int kSlices = kCluster * kWarps;
+  extern __shared__ __align__(16) uint8_t kept_raw[];
   __shared__ Smem S;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
@@ -122,12 +293,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   const int TN = a.max_nodes, V = a.vocab, n = a.n_nodes[r];
   const T *p0 = static_cast<const T *>(a.p) + static_cast<int64_t>(r) * TN * a.p_stride;
   const T *q0 = a.q ? static_cast<const T *>(a.q) + static_cast<int64_t>(r) * TN * a.q_stride : nullptr;
+  int par = -2, tok = 0;
+  float ua = 0.f;
+  if (tid < TN) {  // (beside the load of n)
+    const int64_t at = static_cast<int64_t>(r) * TN + tid;
+    par = a.parent[at];
+    tok = a.token[at];
+    ua = a.u_accept[at];
+  }
+  const float us = a.u_sample[r];
   if (tid == 0) S.bad = n < 0 || n > TN;
   __syncthreads();
   if (!S.bad && tid < n) {
-    const int64_t at = static_cast<int64_t>(r) * TN + tid;
-    const int par = a.parent[at], tok = a.token[at];
-    S.parent[tid] = par;
     S.token[tid] = tok;
     const bool root = tid == 0;
     if (par < -1 || par >= tid || (!root && (tok < 0 || tok >= V))) {
@@ -135,9 +312,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     } else if (par >= 0) {
       S.px[tid] = to_fix(one(p0 + par * a.p_stride + tok));
       S.qx[tid] = q0 ? to_fix(one(q0 + par * a.q_stride + tok)) : kOne;
-      S.u[tid] = to_fix(a.u_accept[at]);
+      S.u[tid] = to_fix(ua);
     }
   }
+  if (tid < kMaxNodes) S.parent[tid] = tid < n ? par : -2;
   __syncthreads();
   if (S.bad || n == 0) {  // (the same in every CTA of the cluster)
     if (rank == 0) {
@@ -158,42 +336,72 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     S.c = 0;
     S.s = kOne;
   }
-  // positions of a warp's slice: whole groups of 128 (a lane's 4 x 32 lanes)
-  const int per = ((V + 3 + kSlices - 1) / kSlices + 127) / 128 * 128;
+  const int per = slice_length(V, kSlices);
+  Kept<T> kept = {nullptr, nullptr, rank * kWarps * per};
+  if (a.keep) {
+    kept.p = reinterpret_cast<T *>(kept_raw);
+    kept.q = kept.p + kWarps * per;
+  }
+  int kept_p = -1, kept_q = -1;  // the nodes whose rows are kept
   int parity = 0;
   uint64_t c_pass = 0, c_kept = 0;
   bool fresh = false;  // the slices' sums are those of (cur, c)
   for (;;) {
-    if (tid == 0) {
-      // on to the next rejection that needs a sum, or to the end
-      int cur = S.cur, i = S.next, again = 0;
+    if (warp == 0) {
+      // on to the next rejection that needs a sum, or to the end: the whole
+      // warp walks, its lanes looking for a node's next child
+      int cur = S.cur, i = S.next, n_path = S.n_path, n_gone = S.n_gone, again = 0;
+      uint64_t c = S.c, s = S.s;
       bool moved = false;
-      for (; i < n && !again; ++i) {
-        if (S.parent[i] != cur) continue;
-        uint64_t rest = left_of(S.px[i], S.c, S.qx[i]);
-        if (!q0) {
-          rest = S.px[i];
-          for (int j = 0; j < S.n_gone; ++j)
-            if (S.gone[j] == S.token[i]) rest = 0;
+      while (!again) {
+        int x = kMaxNodes;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const unsigned hit = __ballot_sync(0xffffffffu, S.parent[32 * k + lane] == cur && 32 * k + lane >= i);
+          if (hit) x = 32 * k + __ffs(hit) - 1;
         }
-        if (mul_fix(mul_fix(S.u[i], S.qx[i]), S.s) < rest) {
-          cur = i;
-          S.path[S.n_path++] = i;
-          S.n_gone = 0;
-          S.c = 0;
-          S.s = kOne;
+        if (x == kMaxNodes) {
+          i = n;
+          break;
+        }
+        i = x + 1;
+        uint64_t rest = left_of(S.px[x], c, S.qx[x]);
+        if (!q0) {
+          bool gone = false;
+          for (int j = lane; j < n_gone; j += 32) gone |= S.gone[j] == S.token[x];
+          rest = __any_sync(0xffffffffu, gone) ? 0 : S.px[x];
+        }
+        if (mul_fix(mul_fix(S.u[x], S.qx[x]), s) < rest) {
+          cur = x;
+          if (lane == 0) S.path[n_path] = x;
+          ++n_path;
+          n_gone = 0;
+          c = 0;
+          s = kOne;
           moved = true;
         } else if (!q0) {
-          if (rest > 0) S.gone[S.n_gone++] = S.token[i];
-          S.s = S.s > rest ? S.s - rest : 0;
+          if (rest > 0) {
+            if (lane == 0) S.gone[n_gone] = S.token[x];
+            ++n_gone;
+            __syncwarp();
+          }
+          s = s > rest ? s - rest : 0;
           moved = true;
         } else {
           again = 1;
         }
       }
-      S.cur = cur;
-      S.next = i;
-      S.again = again | (moved ? 2 : 0);
+      if (lane == 0) {
+        S.cur = cur;
+        S.next = i;
+        S.n_path = n_path;
+        S.n_gone = n_gone;
+        S.c = c;
+        S.s = s;
+        S.again = again | (moved ? 2 : 0);
+        // (64-bit conversions run at a sixteenth of the rate: one thread's)
+        split_c(again ? c + s : c, S.c0, S.c1);
+      }
     }
     __syncthreads();
     const int again = S.again;
@@ -206,40 +414,36 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     uint64_t sum = 0;
     const int y0 = (rank * kWarps + warp) * per, y1 = min(y0 + per, p.end);
     if (c_pass == 0) {
-#pragma unroll 4
-      for (int y = y0 + 4 * lane; y < y1; y += 128) {
-        float x[4];
-        load_p(p, y, x);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += to_fix(x[e]);
-      }
+      const int from = !a.keep ? 0 : kept_p == S.cur ? 2 : 1;
+      sum = slice_sum_from<T, false, false>(from, p, p, kept, 0.f, 0.f, y0, y1, lane);
+      if (from == 1) kept_p = S.cur, kept_q = -1;
     } else {
       const Row<T> q(q0 + S.cur * a.q_stride, V);
-#pragma unroll 4
-      for (int y = y0 + 4 * lane; y < y1; y += 128) {
-        float x[4], z[4];
-        load_p(p, y, x);
-        load_q(p, q, y, z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += left_of(to_fix(x[e]), c_pass, to_fix(z[e]));
-      }
+      const float c0 = S.c0, c1 = S.c1;
+      const int from = !a.keep ? 0 : kept_q == S.cur ? 2 : 1;
+      sum = c_pass == kOne ? slice_sum_from<T, true, true>(from, p, q, kept, c0, c1, y0, y1, lane)
+                           : slice_sum_from<T, false, true>(from, p, q, kept, c0, c1, y0, y1, lane);
+      if (from == 1) kept_p = kept_q = S.cur;
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) S.wsum[warp] = sum;
     __syncthreads();
-    if (tid == 0) {
-      for (int j = 0; j < S.n_gone; ++j) {  // tokens removed at this node
-        const int y = S.gone[j] + p.off, w = y / per - rank * kWarps;
-        if (w >= 0 && w < kWarps) S.wsum[w] -= to_fix(one(p.at + y));
+    if (warp == 0) {
+      if (S.n_gone > 0) {  // tokens removed at this node
+        if (lane == 0)
+          for (int j = 0; j < S.n_gone; ++j) {
+            const int y = S.gone[j] + p.off, w = y / per - rank * kWarps;
+            if (w >= 0 && w < kWarps) S.wsum[w] -= pieces(__saturatef(one(p.at + y)));
+          }
+        __syncwarp();
       }
-      uint64_t t = 0;
+      uint64_t t = lane < kWarps ? S.wsum[lane] : 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) t += S.wsum[w];
-      S.scan[0] = t;
+      for (int o = kWarps / 2; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      if (lane < kCluster) cluster.map_shared_rank(&S, lane)->total[parity][rank] = t;
     }
-    __syncthreads();
-    if (tid < kCluster) cluster.map_shared_rank(&S, tid)->total[parity][rank] = S.scan[0];
     cluster.sync();
     if (again & 1) {
       uint64_t t = 0;
@@ -267,7 +471,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
     S.slice = -1;
     if (all > 0) {
-      uint64_t t = mul_fix(to_fix(a.u_sample[r]), all);
+      uint64_t t = mul_fix(to_fix(us), all);
       if (t >= all) t = all - 1;
       if (t >= before && t - before < S.total[parity][rank]) {
         t -= before;
@@ -291,22 +495,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   const Row<T> p(p0 + S.cur * a.p_stride, V);
   const int y0 = (rank * kWarps + S.slice) * per, y1 = min(y0 + per, p.end);
   const uint64_t c = S.c;
+  const float c0 = S.c0, c1 = S.c1;  // (the last pass's c is the one that stays)
   uint64_t target = S.target;
   for (int yb = y0; yb < y1; yb += 4 * kThreads) {
     const int y = yb + 4 * tid;
     uint64_t v[4] = {0, 0, 0, 0}, mine = 0;
     if (y < y1) {
-      float x[4];
-      load_p(p, y, x);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = to_fix(x[e]);
+      float x[4], z[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kept_p == S.cur) four(kept.p + (y - kept.y0), x);
+      else load_p(p, y, x);
       if (c != 0) {
         const Row<T> q(q0 + S.cur * a.q_stride, V);
-        float z[4];
-        load_q(p, q, y, z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = left_of(v[e], c, to_fix(z[e]));
+        if (kept_q == S.cur) four(kept.q + (y - kept.y0), z);
+        else load_q(p, q, y, z);
       }
+      if (c == 0) left4<true, false>(x, z, c0, c1);
+      else if (c == kOne) left4<true, true>(x, z, c0, c1);
+      else left4<false, true>(x, z, c0, c1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = pieces(x[e]);
       for (int j = 0; j < S.n_gone; ++j) {
         const int e = S.gone[j] + p.off - y;
 #pragma unroll
@@ -343,13 +550,47 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 
 }  // namespace
 
+namespace {
+constexpr size_t kMostKept = 200 * 1024;  // of a CTA's shared memory
+
+template <typename T, int kCluster>
+cudaError_t launch(TreeVerifyArgs a, cudaStream_t s) {
+  static bool configured = false;
+  if (!configured) {
+    cudaError_t e = cudaFuncSetAttribute(tree_verify_kernel<T, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kMostKept));
+    if (e == cudaSuccess && kCluster > 8)
+      e = cudaFuncSetAttribute(tree_verify_kernel<T, kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    configured = true;
+  }
+  const size_t kept = static_cast<size_t>(slice_length(a.vocab, kCluster * kWarps)) * kWarps * sizeof(T) * (a.q ? 2 : 1);
+  a.keep = kept <= kMostKept;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_rows) * kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = a.keep ? kept : 0;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_verify_kernel<T, kCluster>, a);
+}
+template <typename T>
+cudaError_t launch(const TreeVerifyArgs &a, cudaStream_t s) {
+  // Sixteen CTAs a row while all rows' run at once, two on an SM (4 rows of
+  // 131072 fp32: 12.3 us, with eight 13.4), else eight (64 rows in bf16: 25.7
+  // us in two waves, with four 28.0 in one).
+  return a.n_rows * 16 <= 2 * device_sm_count() ? launch<T, 16>(a, s) : launch<T, 8>(a, s);
+}
+}  // namespace
+
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.n_rows) * kCluster;
-  if (a.dtype == HW_F32)
-    tree_verify_kernel<float><<<grid, kThreads, 0, s>>>(a);
-  else
-    tree_verify_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.dtype == HW_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
 }
 
 }  // namespace hw

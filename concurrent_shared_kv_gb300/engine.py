@@ -256,15 +256,16 @@ def tree_verify(n_nodes: torch.Tensor, parent: torch.Tensor, token: torch.Tensor
     """hw_tree_verify: (path, n_path, next_token) of drafted trees.  p and q:
     [rows][max_nodes][vocab], float32 or bfloat16, the last dimension dense and
     the first two one stride apart; q None: the tokens were chosen, not drawn."""
-    R, T, V = p.shape
+    R, T, V = shape = p.shape
 
     def step(x):
-        if x.shape != p.shape or x.dtype != p.dtype:
-            raise ValueError("p and q differ in shape or type")
-        if (x.stride(2) != 1 and V > 1) or (R > 1 and T > 1 and x.stride(0) != T * x.stride(1)):
+        s0, s1, s2 = x.stride()
+        if (s2 != 1 and V > 1) or (R > 1 and T > 1 and s0 != T * s1):
             raise ValueError("p and q need rows one stride apart with dense values")
-        return x.stride(1) if T > 1 else x.stride(0) if R > 1 else V
+        return s1 if T > 1 else s0 if R > 1 else V
 
+    if q is not None and (q.shape != shape or q.dtype != p.dtype):
+        raise ValueError("p and q differ in shape or type")
     if path is None:
         path = torch.empty((R, T), dtype=torch.int32, device=p.device)
     if n_path is None:
