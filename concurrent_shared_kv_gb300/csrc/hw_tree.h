@@ -50,7 +50,7 @@ struct TreeHeader {
   int32_t n_rows, max_nodes, n_q_heads, n_kv_heads, head_dim, n_blocks, n_view, dtype;
   int32_t n_groups;  // per kv head
   int32_t n_ctas;    // CTAs with units (0: nothing to attend)
-  int32_t pad;
+  int32_t streams;   // records that a CTA leaves of a group with up to 128 columns
   int64_t capacity;
 };
 

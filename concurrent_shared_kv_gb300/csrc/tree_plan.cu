@@ -447,7 +447,9 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
-  // the records of every (kv head, group)
+  // the records of every (kv head, group); on the tensor cores a CTA with two
+  // units or more may leave two of a group with up to 128 columns (tree_tc.cu)
+  const int streams = a.L.cols > 128 && U > a.L.ctas_max ? 2 : 1;
   int32_t *piece_row = tree_at<int32_t>(a, a.L.piece_row);
   int2 *piece_cta = tree_at<int2>(a, a.L.piece_cta);
   const int64_t K = C > 0 ? static_cast<int64_t>(n_groups) * a.n_kv_heads : 0;
@@ -464,8 +466,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       pc.x = S.number[cta_of_weight(w, W, C)];
       pc.y = S.number[cta_of_weight(w + span_weight(cost, gr.n_cols, gr.n_spans - 1, last.tile0) +
                                         tile_weight(cost, gr.n_cols, gr.n_spans == 1, tiles - 1), W, C)] - pc.x + 1;
-      // tensor cores: up to 128 columns leave two records a CTA (tree_tc.cu)
-      if (a.L.cols > 128 && gr.n_cols <= 128) pc.y *= 2;
+      if (streams == 2 && gr.n_cols <= 128) pc.y *= 2;
       rows = static_cast<int64_t>(pc.y) * gr.n_cols;
     }
     const int64_t at = block_scan(S, rows);
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   }
   if (tid == 0)
     hdr = TreeHeader{kTreeMagic, R, T, a.n_q_heads, a.n_kv_heads, a.head_dim, a.n_blocks, V, a.dtype,
-                     n_groups, n_ctas, 0, a.capacity};
+                     n_groups, n_ctas, streams, a.capacity};
 }
 
 // cos and sin of a position's angle for one pair: the angle in turns is exact in 64-bit integers (rope_cos_sin); here
@@ -588,12 +589,54 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
 
 constexpr int kMergeWarps = 8;
 
+// The next N of n records joined to (M, L, acc): their (m, l), a lane each, and
+// their outputs, all under way in one trip to memory.  Without branches: the
+// ones past the end read the last record again, and what a record without
+// tiles (m = -inf) holds is dropped.
+template <int D, int N>
+__device__ __forceinline__ void merge_batch(const float2 *ml, const float *o, int n_cols, int64_t step, int j, int n, int lane,
+                                            float &M, float &L, float (&acc)[D / 32]) {
+  constexpr int EPL = D / 32;
+  float2 mine = ml[static_cast<int64_t>(min(j + lane, n - 1)) * n_cols];
+  float val[N][EPL];
+#pragma unroll
+  for (int b = 0; b < N; ++b) {
+    const float *src = o + min(j + b, n - 1) * step;
+    if constexpr (EPL == 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(src);
+      val[b][0] = y.x; val[b][1] = y.y; val[b][2] = y.z; val[b][3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2 *>(src);
+      val[b][0] = y.x; val[b][1] = y.y;
+    }
+  }
+  if (lane >= N || j + lane >= n) mine = make_float2(-INFINITY, 0.f);
+  float top = fmaxf(M, mine.x);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float old = M == -INFINITY ? 0.f : ex2(M - top);
+  const float w = mine.x == -INFINITY ? 0.f : ex2(mine.x - top);
+  M = top;
+  float sum = mine.y * w;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  L = L * old + sum;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) acc[e] *= old;
+#pragma unroll
+  for (int b = 0; b < N; ++b) {
+    const float wj = __shfl_sync(0xffffffffu, w, b);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = wj != 0.f ? fmaf(wj, val[b][e], acc[e]) : acc[e];
+  }
+}
+
 // One (row, node, q head) a warp: its records - one for every CTA that
 // touched its group - joined as
 //   M = max m,  out = sum o 2^(m - M) / sum l 2^(m - M),  lse = (M + log2 l) ln 2.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int EPL = D / 32, kBatch = 8;
+  constexpr int EPL = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp;
   const int G = a.n_q_heads / a.n_kv_heads;
@@ -625,45 +668,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   float M = -INFINITY, L = 0.f, acc[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  for (int j0 = 0; j0 < n; j0 += 32) {  // a lane a record's (m, l)
-    float2 mine = make_float2(-INFINITY, 0.f);
-    if (j0 + lane < n) mine = ml[static_cast<int64_t>(j0 + lane) * n_cols];
-    float top = fmaxf(M, mine.x);
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float old = M == -INFINITY ? 0.f : ex2(M - top);
-    const float w = mine.x == -INFINITY ? 0.f : ex2(mine.x - top);  // a record without tiles: no output either
-    M = top;
-    float sum = mine.y * w;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    L = L * old + sum;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] *= old;
-    const int last = min(32, n - j0);
-    for (int j1 = 0; j1 < last; j1 += kBatch) {  // kBatch outputs under way
-      float val[kBatch][EPL], wj[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        wj[b] = __shfl_sync(0xffffffffu, w, j1 + b);
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) val[b][e] = 0.f;
-        if (j1 + b < last && wj[b] > 0.f) {
-          const float *src = o + (j0 + j1 + b) * step;
-          if constexpr (EPL == 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(src);
-            val[b][0] = y.x; val[b][1] = y.y; val[b][2] = y.z; val[b][3] = y.w;
-          } else {
-            const float2 y = *reinterpret_cast<const float2 *>(src);
-            val[b][0] = y.x; val[b][1] = y.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = fmaf(wj[b], val[b][e], acc[e]);
-    }
+  for (int j = 0; j < n;) {
+    const int left = n - j;
+    if (left > 8) merge_batch<D, 16>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 16;
+    else if (left > 4) merge_batch<D, 8>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 8;
+    else if (left > 2) merge_batch<D, 4>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 4;
+    else merge_batch<D, 2>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 2;
   }
   const float inv = 1.f / L;  // (a node attends itself; NaN where its values are)
   T res[EPL];

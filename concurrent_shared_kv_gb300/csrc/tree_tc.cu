@@ -219,7 +219,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 struct Walk {
   const TreeGroup *groups;
   const TreeSpan *spans;
-  int n_groups;
+  int n_groups, streams;
   int head, group, span, tile, left;  // kv head, group, span, its first tile, units still to come
   TreeGroup g;
   TreeSpan sp;
@@ -554,7 +554,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     if (on) {
       S.red[q][half][row] = l;
       pair_sync(pair);
-      if (half == 0 && rec_col < rec_cols)  // a stream without a tile leaves m = -inf and no O
+      if (half == 0 && rec_col < rec_cols && (some || w.streams == 2))  // a stream without a tile leaves m = -inf and no O
         tree_at<float2>(a, a.L.ml)[rec + rec_col] =
             some ? make_float2(m, l + S.red[q][1][row]) : make_float2(-INFINITY, 0.f);
       pair_sync(pair);
@@ -583,8 +583,13 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     // the tokens the column sees: all, a node's ancestors and itself, or none
     uint2 see = make_uint2(0, 0);
     int v = -1;
+    // (a lane loads a row's entry beside the columns' load, not behind it)
+    int entry = -1;
+    const bool few = w.g.n_rows <= 32;
+    if (w.sp.row < 0 && few && lane < w.g.n_rows) entry = tree_at<int16_t>(a, a.L.map)[w.sp.map + lane];
+    entry = __shfl_sync(0xffffffffu, entry, tc.row & 31);
     if (mine) {
-      v = w.sp.row < 0 ? tree_at<int16_t>(a, a.L.map)[w.sp.map + tc.row]
+      v = w.sp.row < 0 ? few ? entry : tree_at<int16_t>(a, a.L.map)[w.sp.map + tc.row]
           : static_cast<uint32_t>(tc.node - w.sp.row * a.max_nodes) < static_cast<uint32_t>(a.max_nodes) ? a.n_view : -1;
       if (v >= 0) see = w.sp.row < 0 ? make_uint2(~0u, ~0u) : tree_at<uint2>(a, a.L.mask)[2 * static_cast<int64_t>(tc.node) + half];
     }
@@ -614,7 +619,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
       if (kFp8) rec_scale = a.v_scale[w.head];
       // one record a CTA, or one a stream
       const int nth = static_cast<int>(blockIdx.x) - tree_at<int2>(a, a.L.piece_cta)[k].x;
-      rec = tree_at<int32_t>(a, a.L.piece_row)[k] + static_cast<int64_t>(two ? nth : 2 * nth + q) * rec_cols;
+      rec = tree_at<int32_t>(a, a.L.piece_row)[k] + static_cast<int64_t>(two ? nth : w.streams * nth + q) * rec_cols;
       some = false;
       turn = 0;
     }
@@ -783,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  Walk w = {tree_at<TreeGroup>(a, a.L.groups), tree_at<TreeSpan>(a, a.L.spans), hdr.n_groups,
+  Walk w = {tree_at<TreeGroup>(a, a.L.groups), tree_at<TreeSpan>(a, a.L.spans), hdr.n_groups, hdr.streams,
             c.head, c.group, c.span, c.tile, c.n_units, c.g, c.sp, 0};
   w.begin();
   if (tid == 0) {
