@@ -51,6 +51,7 @@ struct TreeHeader {
   int32_t n_groups;  // per kv head
   int32_t n_ctas;    // CTAs with units (0: nothing to attend)
   int32_t streams;   // records that a CTA leaves of a group with up to 128 columns
+  int32_t n_col_blocks, pad;  // entries of the merge's table: (group, first column) of 32 columns
   int64_t capacity;
 };
 
@@ -80,10 +81,10 @@ struct TreeCta {
 
 // Byte offsets of the plan's arrays in the workspace (the error word is at 0).
 struct TreeLayout {
-  size_t hdr, groups, wbase, spans, map, columns, rot, rot16, piece_row, piece_cta, ctas;
-  size_t n_nodes, slot, pos, end, col, run, rot0, rank, depth, mask, heads, block_start, block_len;
+  size_t hdr, groups, wbase, spans, map, columns, rot, rot16, blocks, piece_row, piece_cta, ctas;
+  size_t n_nodes, slot, pos, end, col, rot0, rank, depth, mask, heads, block_start, block_len;
   size_t ml, o, total;
-  int64_t max_groups, max_spans, max_map, max_cols, max_rots, max_rows;
+  int64_t max_groups, max_spans, max_map, max_cols, max_blocks, max_rots, max_rows;
   int32_t cols, tile, ctas_max;
 };
 

@@ -171,7 +171,6 @@ __device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
   const int R = a.n_rows, V = a.n_view, G = a.n_q_heads / a.n_kv_heads, CG = a.L.cols;
   TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
   int col = 0, rank = 0, rot = 0, n = 0;
-  int2 run = make_int2(0, 0);  // the run's first group and column
   TreeGroup g = {};
   g.n_cols = CG;
   for (int r = 0; r < R; ++r) {
@@ -183,9 +182,7 @@ __device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
     if (S.apart[r]) {
       if (n > 0) groups[n - 1] = g;
       g.n_cols = CG;
-      run = make_int2(n, col);
     }
-    tree_at<int2>(a, a.L.run)[r] = run;
     for (int left = nodes * G; left > 0;) {
       if (g.n_cols == CG) {
         if (n > 0 && !(S.apart[r] && left == nodes * G)) groups[n - 1] = g;
@@ -447,6 +444,17 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
+  // every group's columns by 32, for the merge
+  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    const int nb = g < n_groups ? (groups[g].n_cols + 31) / 32 : 0;
+    const int64_t at = block_scan(S, nb);
+    for (int x = 0; x < nb; ++x) tree_at<int2>(a, a.L.blocks)[at + x] = make_int2(g, 32 * x);
+  }
+  const int n_col_blocks = static_cast<int>(S.carry);
+  __syncthreads();
+  if (tid == 0) S.carry = 0;
+  __syncthreads();
   // the records of every (kv head, group); on the tensor cores a CTA with two
   // units or more may leave two of a group with up to 128 columns (tree_tc.cu)
   const int streams = a.L.cols > 128 && U > a.L.ctas_max ? 2 : 1;
@@ -477,7 +485,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   }
   if (tid == 0)
     hdr = TreeHeader{kTreeMagic, R, T, a.n_q_heads, a.n_kv_heads, a.head_dim, a.n_blocks, V, a.dtype,
-                     n_groups, n_ctas, streams, a.capacity};
+                     n_groups, n_ctas, streams, n_col_blocks, 0, a.capacity};
 }
 
 // cos and sin of a position's angle for one pair: the angle in turns is exact in 64-bit integers (rope_cos_sin); here
@@ -587,102 +595,118 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
 
 // ----------------------------------------------------------------- merge
 
-constexpr int kMergeWarps = 8;
+// Every query's records - one for every CTA (or stream) that touched its
+// group - joined as
+//   M = max m,  out = sum o 2^(m - M) / sum l 2^(m - M),  lse = (M + log2 l) ln 2.
+// A CTA takes 32 columns of a group, one a lane, and a quarter of the head
+// dimension: a warp has 8 elements of it, which lie side by side in a record
+// (a load is 32 sectors of 8 lines; with a query a warp it was 16 lines for
+// half as much).  Two warps share the records of every 8 elements and join at
+// the end, so that up to 16 records cost one trip to memory.
+template <int D>
+struct MergeShape {
+  static constexpr int kChunks = D / 32;               // of 8 elements, in a quarter
+  static constexpr int kThreads = kChunks * 2 * 32;
+};
 
-// The next N of n records joined to (M, L, acc): their (m, l), a lane each, and
-// their outputs, all under way in one trip to memory.  Without branches: the
-// ones past the end read the last record again, and what a record without
-// tiles (m = -inf) holds is dropped.
-template <int D, int N>
-__device__ __forceinline__ void merge_batch(const float2 *ml, const float *o, int n_cols, int64_t step, int j, int n, int lane,
-                                            float &M, float &L, float (&acc)[D / 32]) {
-  constexpr int EPL = D / 32;
-  float2 mine = ml[static_cast<int64_t>(min(j + lane, n - 1)) * n_cols];
-  float val[N][EPL];
+// Up to 8 records from j on in steps of 2, joined to (M, L, acc).
+__device__ __forceinline__ void merge_batch(const float2 *ml, const float *o, int n_cols, int64_t step, int j, int n,
+                                            float &M, float &L, float (&acc)[8]) {
+  constexpr int N = 8;
+  float2 x[N];
+  float4 v[N][2];
+  // without branches: the ones past the end read the last record again, and
+  // what a record without tiles (m = -inf) holds is dropped
 #pragma unroll
   for (int b = 0; b < N; ++b) {
-    const float *src = o + min(j + b, n - 1) * step;
-    if constexpr (EPL == 4) {
-      const float4 y = *reinterpret_cast<const float4 *>(src);
-      val[b][0] = y.x; val[b][1] = y.y; val[b][2] = y.z; val[b][3] = y.w;
-    } else {
-      const float2 y = *reinterpret_cast<const float2 *>(src);
-      val[b][0] = y.x; val[b][1] = y.y;
-    }
+    const int64_t at = min(j + 2 * b, n - 1);
+    x[b] = ml[at * n_cols];
+    const float4 *src = reinterpret_cast<const float4 *>(o + at * step);
+    v[b][0] = src[0];
+    v[b][1] = src[1];
   }
-  if (lane >= N || j + lane >= n) mine = make_float2(-INFINITY, 0.f);
-  float top = fmaxf(M, mine.x);
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float old = M == -INFINITY ? 0.f : ex2(M - top);
-  const float w = mine.x == -INFINITY ? 0.f : ex2(mine.x - top);
-  M = top;
-  float sum = mine.y * w;
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  L = L * old + sum;
-#pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[e] *= old;
+  float top = M;
 #pragma unroll
   for (int b = 0; b < N; ++b) {
-    const float wj = __shfl_sync(0xffffffffu, w, b);
+    if (j + 2 * b >= n) x[b].x = -INFINITY;
+    top = fmaxf(top, x[b].x);
+  }
+  const float old = M == -INFINITY ? 0.f : ex2(M - top);
+  M = top;
+  L *= old;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = wj != 0.f ? fmaf(wj, val[b][e], acc[e]) : acc[e];
+  for (int e = 0; e < 8; ++e) acc[e] *= old;
+#pragma unroll
+  for (int b = 0; b < N; ++b) {
+    const bool use = x[b].x != -INFINITY;
+    const float w = use ? ex2(x[b].x - top) : 0.f;
+    const float y[8] = {v[b][0].x, v[b][0].y, v[b][0].z, v[b][0].w, v[b][1].x, v[b][1].y, v[b][1].z, v[b][1].w};
+    L = use ? fmaf(w, x[b].y, L) : L;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = use ? fmaf(w, y[e], acc[e]) : acc[e];
   }
 }
 
-// One (row, node, q head) a warp: its records - one for every CTA that
-// touched its group - joined as
-//   M = max m,  out = sum o 2^(m - M) / sum l 2^(m - M),  lse = (M + log2 l) ln 2.
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int EPL = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp;
+__global__ void __launch_bounds__(MergeShape<D>::kThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kChunks = MergeShape<D>::kChunks, kRow = kChunks * 8;  // elements of a row here
+  constexpr int kPiece = 16 / sizeof(T);                               // elements of a 16-byte store
+  __shared__ float part[kChunks][8][32], part_m[kChunks][32], part_l[kChunks][32];
+  __shared__ __align__(16) T tile[32][kRow];
+  __shared__ int32_t out_row[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunk = warp >> 1, share = warp & 1;
+  const int quarter = blockIdx.x & 3, h = (blockIdx.x >> 2) % a.n_kv_heads, b = (blockIdx.x >> 2) / a.n_kv_heads;
   const int G = a.n_q_heads / a.n_kv_heads;
-  const int x = static_cast<int>(item % a.n_q_heads);  // place in the head list: kv head, then its q heads
-  const int64_t node = item / a.n_q_heads;
-  const int r = static_cast<int>(node / a.max_nodes), i = static_cast<int>(node % a.max_nodes);
-  const int row = min(r, a.n_rows - 1);
   // (loads that do not hang on one another first: trips to L2 are what this
   // kernel takes)
-  const int n_nodes = tree_at<int32_t>(a, a.L.n_nodes)[row], hq = tree_at<int32_t>(a, a.L.heads)[x];
-  const int2 run = tree_at<int2>(a, a.L.run)[row];
-  const int first = tree_at<int32_t>(a, a.L.col)[row];
-  const int n_groups = tree_at<const TreeHeader>(a, a.L.hdr)->n_groups;
-  if (!tree_plan_ok(a) || r >= a.n_rows || i >= n_nodes) {
+  const TreeHeader &hdr = *tree_at<const TreeHeader>(a, a.L.hdr);
+  const int2 at = tree_at<int2>(a, a.L.blocks)[b];
+  const int hq_of = tree_at<int32_t>(a, a.L.heads)[h * G + min(lane, G - 1)];
+  if (!tree_plan_ok(a) || b >= hdr.n_col_blocks) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever follows this grid follows that one
     return;
   }
-  const int h = x / G;
-  const int in_run = first + i * G + x % G - run.y;
-  const int g = run.x + in_run / a.L.cols, col = in_run % a.L.cols;
-  const int n_cols = tree_at<TreeGroup>(a, a.L.groups)[g].n_cols;
-  const int64_t k = static_cast<int64_t>(h) * n_groups + g;
+  const TreeGroup g = tree_at<TreeGroup>(a, a.L.groups)[at.x];
+  const int64_t k = static_cast<int64_t>(h) * hdr.n_groups + at.x;
   const int n = tree_at<int2>(a, a.L.piece_cta)[k].y;
   const int64_t row0 = tree_at<int32_t>(a, a.L.piece_row)[k];
+  const bool on = at.y + lane < g.n_cols;
+  const int col = min(at.y + lane, g.n_cols - 1);
+  const TreeColumn tc = tree_at<TreeColumn>(a, a.L.columns)[g.col0 + col];
+  const int hq = __shfl_sync(0xffffffffu, hq_of, tc.head);
   const float2 *ml = tree_at<float2>(a, a.L.ml) + row0 + col;
-  const float *o = tree_at<float>(a, a.L.o) + record_at(row0, n_cols, col, lane * EPL, D);
-  const int64_t step = static_cast<int64_t>(n_cols) * D;
+  const float *o = tree_at<float>(a, a.L.o) + record_at(row0, g.n_cols, col, (quarter * kChunks + chunk) * 8, D);
+  const int64_t step = static_cast<int64_t>(g.n_cols) * D;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the records
-  float M = -INFINITY, L = 0.f, acc[EPL];
+  float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j = share; j < n; j += 16) merge_batch(ml, o, g.n_cols, step, j, n, M, L, acc);
+  if (share == 1) {
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  for (int j = 0; j < n;) {
-    const int left = n - j;
-    if (left > 8) merge_batch<D, 16>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 16;
-    else if (left > 4) merge_batch<D, 8>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 8;
-    else if (left > 2) merge_batch<D, 4>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 4;
-    else merge_batch<D, 2>(ml, o, n_cols, step, j, n, lane, M, L, acc), j += 2;
+    for (int e = 0; e < 8; ++e) part[chunk][e][lane] = acc[e];
+    part_m[chunk][lane] = M;
+    part_l[chunk][lane] = L;
   }
-  const float inv = 1.f / L;  // (a node attends itself; NaN where its values are)
-  T res[EPL];
+  if (tid < 32) out_row[lane] = on ? tc.node * a.n_q_heads + hq : -1;
+  __syncthreads();
+  if (share == 0) {
+    const float M1 = part_m[chunk][lane], top = fmaxf(M, M1);
+    const float w0 = M == -INFINITY ? 0.f : ex2(M - top), w1 = M1 == -INFINITY ? 0.f : ex2(M1 - top);
+    L = L * w0 + part_l[chunk][lane] * w1;
+    const float inv = 1.f / L;  // (a node attends itself; NaN where its values are)
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) res[e] = from_f32<T>(acc[e] * inv);
-  const int64_t out_row = node * a.n_q_heads + hq;
-  store_row_part<T, EPL>(static_cast<T *>(a.out) + out_row * D + lane * EPL, res);
-  if (a.lse && lane == 0)
-    a.lse[out_row] = (M + log2f(L)) * 0.693147180559945309f;
+    for (int e = 0; e < 8; ++e) tile[lane][chunk * 8 + e] = from_f32<T>((acc[e] * w0 + part[chunk][e][lane] * w1) * inv);
+    if (a.lse && warp == 0 && quarter == 0 && on)
+      a.lse[tc.node * a.n_q_heads + hq] = (top + log2f(L)) * 0.693147180559945309f;
+  }
+  __syncthreads();
+  for (int x = tid; x < 32 * kRow / kPiece; x += MergeShape<D>::kThreads) {
+    const int r = x / (kRow / kPiece), e = x % (kRow / kPiece) * kPiece;
+    if (out_row[r] < 0) continue;
+    T res[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) res[i] = tile[r][e + i];
+    store_row_part<T, kPiece>(static_cast<T *>(a.out) + static_cast<int64_t>(out_row[r]) * D + quarter * kRow + e, res);
+  }
 }
 
 // ---------------------------------------------------------------- commit
@@ -797,13 +821,13 @@ cudaError_t launch_tree_append(const TreeArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_merge(const TreeArgs &a, cudaStream_t s) {
-  const int64_t items = static_cast<int64_t>(a.n_rows) * a.max_nodes * a.n_q_heads;
-  const unsigned grid = static_cast<unsigned>((items + kMergeWarps - 1) / kMergeWarps);
+  const unsigned grid = static_cast<unsigned>(4 * a.n_kv_heads * a.L.max_blocks);
   const bool d64 = a.head_dim == 64;
+  const int threads = d64 ? MergeShape<64>::kThreads : MergeShape<128>::kThreads;
   if (a.dtype == HW_F32)
-    return launch_dependent(d64 ? tree_merge_kernel<float, 64> : tree_merge_kernel<float, 128>, grid, kMergeWarps * 32, s, a);
+    return launch_dependent(d64 ? tree_merge_kernel<float, 64> : tree_merge_kernel<float, 128>, grid, threads, s, a);
   return launch_dependent(d64 ? tree_merge_kernel<__nv_bfloat16, 64> : tree_merge_kernel<__nv_bfloat16, 128>, grid,
-                          kMergeWarps * 32, s, a);
+                          threads, s, a);
 }
 
 cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaStream_t s) {
@@ -849,6 +873,8 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.columns = put(sizeof(TreeColumn) * L.max_cols);
   L.rot = put(4 * static_cast<size_t>(d.head_dim) * L.max_rots);
   L.rot16 = put(2 * static_cast<size_t>(d.head_dim) * L.max_rots);
+  L.max_blocks = L.max_cols / 32 + L.max_groups;
+  L.blocks = put(8 * L.max_blocks);
   L.piece_row = put(4 * L.max_groups * d.n_kv_heads);
   L.piece_cta = put(8 * L.max_groups * d.n_kv_heads);
   L.ctas = put(sizeof(TreeCta) * L.ctas_max);
@@ -857,7 +883,6 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.pos = put(4 * R);
   L.end = put(4 * R);
   L.col = put(4 * R);
-  L.run = put(8 * R);
   L.rot0 = put(4 * R);
   L.rank = put(4 * R);
   L.depth = put(4 * Q);
