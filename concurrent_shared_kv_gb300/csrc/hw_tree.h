@@ -15,7 +15,8 @@
 //   unit     = one tile of `tile` tokens of a span for one kv head; units are
 //              ordered by kv head, group, span and tile, on a weighted line:
 //              a tile weighs tile1 or tile2 (over 128 columns), the first tile
-//              of a span `span` more, that of a group `group` more still.  CTA
+//              of a span `span` more (a tree's `tree` more still), that of a
+//              group `group` more.  CTA
 //              c of C takes the units that start in [c W / C, (c + 1) W / C);
 //              shares without a unit get no CTA.
 //   record   = what a CTA leaves for (kv head, group): per column the running

@@ -16,15 +16,16 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
-// Weights of the unit line, measured on the tensor-core kernel in steps of
-// about 750 clocks: a tile, a span's new queries and empty pipeline, a group's
-// records.  Where every unit can have a CTA of its own, each does: the units
-// then weigh the same.
+// Weights of the unit line, measured on the tensor-core kernel (a fit of its
+// CTAs' times) in steps of 750 clocks: a tile against up to 128 columns and
+// against more, what a span's new queries and empty pipeline cost beside its
+// tiles, a tree's more of that, a group's records.  Where every unit can have
+// a CTA of its own, each does: the units then weigh the same.
 struct TreeCost {
-  int32_t tile1, tile2, span, group;
+  int32_t tile1, tile2, span, tree, group;
 };
-__device__ inline TreeCost tree_cost(int cols, bool alone) {
-  return alone ? TreeCost{1, 1, 0, 0} : cols > 128 ? TreeCost{4, 4, 6, 6} : TreeCost{4, 4, 1, 1};
+__device__ inline TreeCost tree_cost(int cols, bool e4m3, bool alone) {
+  return alone ? TreeCost{1, 1, 0, 0, 0} : cols <= 128 ? TreeCost{4, 4, 1, 0, 1} : e4m3 ? TreeCost{4, 6, 12, 4, 8} : TreeCost{4, 4, 8, 4, 8};
 }
 
 struct TreePlanSmem {
@@ -144,10 +145,6 @@ __device__ int plan_row(const TreeArgs &a, const TreeMeta &m, TreePlanSmem &S, i
   return n;
 }
 
-// Weight of a span before its tile t (t > 0 includes the span's own).
-__device__ __forceinline__ int64_t tile_weight(const TreeCost &c, int n_cols, bool first, int t) {
-  return t == 0 ? 0 : c.span + (first ? c.group : 0) + static_cast<int64_t>(t) * (n_cols > 128 ? c.tile2 : c.tile1);
-}
 // The CTA that owns a unit starting at weight w.
 __device__ __forceinline__ int cta_of_weight(int64_t w, int64_t W, int C) {
   return static_cast<int>(((w + 1) * C - 1) / W);
@@ -282,9 +279,15 @@ __device__ void plan_spans(const TreeArgs &a, TreePlanSmem &S, int gi, int64_t *
   if (lane == 0) ubase[gi] = tiles;
 }
 
-// Weight of a group before its span s, which has tile0 tiles before it.
-__device__ __forceinline__ int64_t span_weight(const TreeCost &c, int n_cols, int s, int tile0) {
-  return s == 0 ? 0 : c.group + static_cast<int64_t>(s) * c.span + static_cast<int64_t>(tile0) * (n_cols > 128 ? c.tile2 : c.tile1);
+// Weight of a group before its span s, which has tile0 tiles before it (its
+// last n_rows spans are trees), and of what a span costs beside its tiles.
+__device__ __forceinline__ int64_t span_weight(const TreeCost &c, const TreeGroup &g, int s, int tile0) {
+  return s == 0 ? 0
+                : c.group + static_cast<int64_t>(s) * c.span + static_cast<int64_t>(max(0, s - g.n_spans + g.n_rows)) * c.tree +
+                      static_cast<int64_t>(tile0) * (g.n_cols > 128 ? c.tile2 : c.tile1);
+}
+__device__ __forceinline__ int span_cost(const TreeCost &c, const TreeGroup &g, int s) {
+  return c.span + (s == 0 ? c.group : 0) + (s >= g.n_spans - g.n_rows ? c.tree : 0);
 }
 
 // The plan but for its tables, by one CTA.
@@ -373,11 +376,11 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
-  const TreeCost cost = tree_cost(a.L.cols, U <= a.L.ctas_max);
+  const TreeCost cost = tree_cost(a.L.cols, a.dtype == HW_FP8_E4M3, U <= a.L.ctas_max);
   for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
     const int g = g0 + tid;
     const int64_t tiles = g < n_groups ? (g + 1 < n_groups ? ubase[g + 1] : UH) - ubase[g] : 0;
-    const int64_t at = block_scan(S, g < n_groups ? span_weight(cost, groups[g].n_cols, groups[g].n_spans, static_cast<int>(tiles)) : 0);
+    const int64_t at = block_scan(S, g < n_groups ? span_weight(cost, groups[g], groups[g].n_spans, static_cast<int>(tiles)) : 0);
     if (g < n_groups) wbase[g] = at;
   }
   const int64_t WH = S.carry, W = WH * a.n_kv_heads;
@@ -408,10 +411,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     hi = gr.n_spans;
     while (hi - s > 1) {
       const int mid = (s + hi) >> 1;
-      if (span_weight(cost, gr.n_cols, mid, sp[mid].tile0) <= in) s = mid; else hi = mid;
+      if (span_weight(cost, gr, mid, sp[mid].tile0) <= in) s = mid; else hi = mid;
     }
-    const int64_t x = in - span_weight(cost, gr.n_cols, s, sp[s].tile0);
-    const int own = cost.span + (s == 0 ? cost.group : 0), tw = gr.n_cols > 128 ? cost.tile2 : cost.tile1;
+    const int64_t x = in - span_weight(cost, gr, s, sp[s].tile0);
+    const int own = span_cost(cost, gr, s), tw = gr.n_cols > 128 ? cost.tile2 : cost.tile1;
     int t = x == 0 ? 0 : x <= own + tw ? 1 : static_cast<int>((x - own + tw - 1) / tw);
     if (t >= (sp[s].len + TL - 1) / TL) {
       t = 0;
@@ -472,8 +475,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       const int64_t w = k / n_groups * WH + wbase[g];
       const int tiles = (last.len + TL - 1) / TL;
       pc.x = S.number[cta_of_weight(w, W, C)];
-      pc.y = S.number[cta_of_weight(w + span_weight(cost, gr.n_cols, gr.n_spans - 1, last.tile0) +
-                                        tile_weight(cost, gr.n_cols, gr.n_spans == 1, tiles - 1), W, C)] - pc.x + 1;
+      const int ls = gr.n_spans - 1;
+      int64_t end = w + span_weight(cost, gr, ls, last.tile0);  // where the group's last unit starts
+      if (tiles > 1) end += span_cost(cost, gr, ls) + static_cast<int64_t>(tiles - 1) * (gr.n_cols > 128 ? cost.tile2 : cost.tile1);
+      pc.y = S.number[cta_of_weight(end, W, C)] - pc.x + 1;
       if (streams == 2 && gr.n_cols <= 128) pc.y *= 2;
       rows = static_cast<int64_t>(pc.y) * gr.n_cols;
     }
