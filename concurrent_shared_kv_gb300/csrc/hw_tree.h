@@ -76,6 +76,7 @@ struct TreeColumn {
 };
 struct TreeCta {
   int32_t head, group, span, tile, n_units;  // first unit and count
+  int32_t wide;                              // one of its groups has over 128 columns
   TreeGroup g;                               // copies: one load instead of three in a row
   TreeSpan sp;
 };

@@ -50,12 +50,32 @@ constexpr int kWarpTma = 16, kWarpMma = 17;  // and 18: an issuer a stream
 constexpr int kT = 128;                      // tokens per tile
 constexpr uint32_t kBox = 128 * 128;         // 128 rows of 128 bytes, 128-byte swizzled
 constexpr uint32_t kQTile = 2 * kBox;        // a query tile: d 0-63, d 64-127 (E4M3: hi, lo)
-// The ring of K and V tiles: bf16 two boxes each, E4M3 one.
+// The ring of K and V tiles: bf16 two boxes each, E4M3 one.  A CTA without a
+// group of over 128 columns has no second query tile, and that much more ring
+// (kMore stages): what one query tile can do is bound by the bytes under way.
 template <bool kFp8>
 struct Ring {
   static constexpr uint32_t kStage = kFp8 ? kBox : 2 * kBox;
   static constexpr int kStages = kFp8 ? 9 : 5;
+  static constexpr int kMore = kQTile / kStage;
   static constexpr int kStep = kFp8 ? 32 : 16;  // tokens of one MMA
+};
+// A place in a ring of n stages.
+struct RingPos {
+  int s;
+  uint32_t phase;
+  __device__ __forceinline__ void on(int by, int n) {
+    s += by;
+    if (s >= n) {
+      s -= n;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ RingPos next(int n) const {
+    RingPos p = *this;
+    p.on(1, n);
+    return p;
+  }
 };
 constexpr float kLazy = 8.f;                 // O is rescaled only when a weight would pass 2^8
 constexpr float kLift = 6.f;                 // E4M3: log2 of P's factor
@@ -64,9 +84,10 @@ constexpr uint32_t kTmemCols = 512;          // S0/P0, S1/P1, O0, O1: 128 column
 template <bool kFp8>
 struct TcSmem {
   static constexpr int kStages = Ring<kFp8>::kStages;
-  alignas(1024) uint8_t q[2][kQTile];
+  static constexpr int kAll = kStages + Ring<kFp8>::kMore;
+  alignas(1024) uint8_t q[2][kQTile];                     // (the second tile's place: part of the ring without one)
   alignas(1024) uint8_t kv[kStages][Ring<kFp8>::kStage];
-  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t kv_full[kAll], kv_empty[kAll];
   uint64_t q_full[2], q_free, s_full[2], p_full[2], pv_done[2], o_empty[2], order, mma_done;
   // tidied V tiles, by the stream that does it, alternating; the tokens with a value that is not finite
   uint64_t scanned[2][2];
@@ -222,6 +243,8 @@ struct Walk {
   TreeGroup g;
   TreeSpan sp;
   int tiles;  // of this span that are the CTA's
+  int stages;     // of the ring
+  uint32_t ring;  // its shared-memory address
   __device__ __forceinline__ void load_span() {
     sp = spans[g.span0 + span];
     begin();
@@ -251,10 +274,11 @@ struct Walk {
 
 template <bool kFp8>
 __device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *tk, const CUtensorMap *tv, Walk w) {
-  constexpr int kStages = Ring<kFp8>::kStages;
   constexpr uint32_t kStage = Ring<kFp8>::kStage;
   const uint64_t pol = policy_evict_first();
+  uint8_t *ring = w.stages > Ring<kFp8>::kStages ? S.q[1] : S.kv[0];
   int n = 0;  // ring entries issued: K(0), V(0), K(1), V(1), ...
+  RingPos at = {0, 0};
   bool waited = false, go = true;
   do {
     if (w.sp.row >= 0 && !waited) {  // a tree: its tokens come from the launch before
@@ -264,21 +288,23 @@ __device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *
     }
     for (int t = w.tile; go && t < w.tile + w.tiles; ++t) {
       const int row = w.sp.start + t * kT;
-      for (int kv = 0; kv < 2; ++kv, ++n) {
-        const int s = n % kStages;
-        if (n >= kStages && !wait_or_abort(S, a, &S.kv_empty[s], ((n / kStages) & 1) ^ 1)) {
+      for (int kv = 0; kv < 2; ++kv, ++n, at.on(1, w.stages)) {
+        if (n >= w.stages && !wait_or_abort(S, a, &S.kv_empty[at.s], at.phase ^ 1)) {
           go = false;
           break;
         }
-        mbar_arrive_expect_tx(&S.kv_full[s], kStage);
-        tma_load_3d(S.kv[s], kv ? tv : tk, &S.kv_full[s], 0, row, w.head, pol);
-        if constexpr (!kFp8) tma_load_3d(S.kv[s] + kBox, kv ? tv : tk, &S.kv_full[s], 64, row, w.head, pol);
+        uint8_t *to = ring + at.s * kStage;
+        mbar_arrive_expect_tx(&S.kv_full[at.s], kStage);
+        tma_load_3d(to, kv ? tv : tk, &S.kv_full[at.s], 0, row, w.head, pol);
+        if constexpr (!kFp8) tma_load_3d(to + kBox, kv ? tv : tk, &S.kv_full[at.s], 64, row, w.head, pol);
       }
     }
   } while (go && w.next());
   if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
   // no copy may still be landing when the CTA retires
-  for (int j = n > kStages ? n - kStages : 0; j < n; ++j) mbar_wait(&S.kv_full[j % kStages], (j / kStages) & 1);
+  RingPos back = {0, 0};
+  if (n >= w.stages) back = {at.s, at.phase ^ 1};
+  for (int j = min(n, w.stages); j > 0; --j, back.on(1, w.stages)) mbar_wait(&S.kv_full[back.s], back.phase);
 }
 
 // One stream's products.  The whole warp walks and waits; one elected lane
@@ -288,28 +314,28 @@ __device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *
 // 1700 clocks, which is why each stream has its own.)
 template <bool kFp8>
 __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk w, int q) {
-  constexpr int kStages = Ring<kFp8>::kStages, kStep = Ring<kFp8>::kStep;
+  constexpr int kStep = Ring<kFp8>::kStep;
   constexpr uint32_t kStage = Ring<kFp8>::kStage;
   constexpr uint32_t idesc_qk = kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
   constexpr uint32_t idesc_pv = kFp8 ? idesc_e4m3(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);
-  const uint32_t q0 = smem_u32(S.q[0]), kv0 = smem_u32(S.kv[0]);
+  const uint32_t q0 = smem_u32(S.q[0]), kv0 = w.ring;
   const uint64_t a_qk = smem_desc(q0, 16, 1024, kSw128), b_qk = smem_desc(kv0, 16, 1024, kSw128);
   const uint64_t b_pv = smem_desc(kv0, kBox, 1024, kSw128);
   const uint32_t s_tmem = tmem + q * 128, o_tmem = s_tmem + 256;
   int np = 0, no = 0, nspan = 0;  // PVs issued, groups whose PVs have begun, spans
-  // the tile whose PV is to come: its V's ring entry (-1: none), its steps of
-  // kStep tokens, whether it is the stream's first of a group
-  int pend = -1, pend_steps = 0;
-  bool pend_first = false, pend_two = false, first = true;
+  // the tile whose PV is to come, if any: its V's place, its steps of kStep
+  // tokens, whether it is the stream's first of a group
+  RingPos pend_v = {0, 0};
+  int pend_steps = 0;
+  bool pend = false, pend_first = false, pend_two = false, first = true;
   // Everything but P is waited for first: P is what the products wait for.
   auto pv_ready = [&]() -> bool {
-    const int s = pend % kStages;
-    return warp_wait(S, a, &S.kv_full[s], (pend / kStages) & 1) &&
+    return warp_wait(S, a, &S.kv_full[pend_v.s], pend_v.phase) &&
            (!pend_first || warp_wait(S, a, &S.o_empty[q], (no++ & 1) ^ 1)) &&
            warp_wait(S, a, &S.p_full[q], np & 1);
   };
   auto pv = [&]() {  // by the elected lane
-    const int s = pend % kStages;
+    const int s = pend_v.s;
     const uint64_t bs = b_pv + ((s * kStage) >> 4);
 #pragma unroll
     for (int k = 0; k < 128 / kStep; ++k)
@@ -333,7 +359,7 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
     if (elect_one()) pv();
     __syncwarp();
     ++np;
-    pend = -1;
+    pend = false;
     return true;
   };
   // The span's queries; one query tile is written by all softmax warps.
@@ -341,50 +367,52 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
     return ((two && q == 1) || warp_wait(S, a, &S.q_full[0], nspan & 1)) &&
            ((two && q == 0) || warp_wait(S, a, &S.q_full[1], nspan & 1));
   };
-  int i = 0, step = 2;  // tiles so far; 2: a group starts
+  RingPos k = {0, 0};   // the next tile's K
+  int step = 2;         // 2: a group starts
   int turn = 0;         // the next tile's stream, where streams take turns
   int turns = 0;        // turns at the tensor cores so far, of both streams
   bool go = true;
   do {
     const bool two = w.g.n_cols > 128;
     if (step == 2) {  // the softmax warps wait for a group's last products
-      if (pend >= 0 && !(go = flush())) break;
+      if (pend && !(go = flush())) break;
       turn = 0;
       first = true;
     }
     bool turned = false;  // this span's queries are there
-    for (int t = 0; t < w.tiles; ++t, ++i, turn ^= 1, turns += two ? 2 : 1) {
+    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turn ^= 1, turns += two ? 2 : 1) {
       if (!two && turn != q) continue;
-      const int nk = 2 * i, s = nk % kStages, mine = turns + (two ? q : 0);
-      if (!(go = warp_wait(S, a, &S.kv_full[s], (nk / kStages) & 1))) break;
+      const int s = k.s, mine = turns + (two ? q : 0);
+      if (!(go = warp_wait(S, a, &S.kv_full[s], k.phase))) break;
       // (a new span's queries come after the last P, so their wait is last)
       // One stream's PV and QK go out together, the streams in turn: mixed,
       // both would wait for both, and their softmaxes would run at the same
       // time, the tensor cores idle.
       if (mine > 0 && !(go = warp_wait(S, a, &S.order, (mine - 1) & 1))) break;
-      if (pend >= 0 && !(go = pv_ready())) break;
+      if (pend && !(go = pv_ready())) break;
       if (!turned && !(go = queries(two))) break;
       turned = true;
       tc_fence_after();
       const uint64_t as = a_qk + ((two ? q * kQTile : 0) >> 4), bs = b_qk + ((s * kStage) >> 4);
       if (elect_one()) {
-        if (pend >= 0) pv();
+        if (pend) pv();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {  // 8 steps of 16 over d (E4M3: 4 of 32, hi then lo)
-          const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+        for (int j = 0; j < 8; ++j) {  // 8 steps of 16 over d (E4M3: 4 of 32, hi then lo)
+          const uint32_t o = ((j >> 2) * kBox + (j & 3) * 32) >> 4;
           if constexpr (kFp8)
-            mma_f8(s_tmem, as + o, bs + (((k & 3) * 32) >> 4), idesc_qk, k > 0);
+            mma_f8(s_tmem, as + o, bs + (((j & 3) * 32) >> 4), idesc_qk, j > 0);
           else
-            mma_bf16(s_tmem, as + o, bs + o, idesc_qk, k > 0);
-          if (k == 5) mbar_arrive(&S.order);  // (the next turn's first MMA is two MMAs away)
+            mma_bf16(s_tmem, as + o, bs + o, idesc_qk, j > 0);
+          if (j == 5) mbar_arrive(&S.order);  // (the next turn's first MMA is two MMAs away)
         }
         mma_commit(&S.s_full[q]);
         mma_commit(&S.kv_empty[s]);
         if (!two) mma_commit(&S.kv_empty[s]);
       }
       __syncwarp();
-      if (pend >= 0) ++np;
-      pend = nk + 1;
+      if (pend) ++np;
+      pend = true;
+      pend_v = k.next(w.stages);
       pend_steps = (min(kT, w.sp.len - (w.tile + t) * kT) + kStep - 1) / kStep;
       pend_first = first;
       pend_two = two;
@@ -396,7 +424,7 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
     __syncwarp();
     ++nspan;
   } while ((step = w.next()));
-  if (go && pend >= 0) flush();
+  if (go && pend) flush();
   if (elect_one()) mma_commit(&S.mma_done);
   __syncwarp();
   mbar_wait(&S.mma_done, 0);
@@ -529,13 +557,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // the named barriers in it stay matched.
 template <bool kFp8>
 __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk w, int q) {
-  constexpr int kStages = Ring<kFp8>::kStages, kStep = Ring<kFp8>::kStep;
+  constexpr int kStep = Ring<kFp8>::kStep;
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = (threadIdx.x >> 7) & 1;
   const int row = quarter * 32 + lane, pair = 1 + q * 4 + quarter;
   const uint32_t s_tmem = tmem + q * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t o_tmem = s_tmem + 256;
   int ns = 0;              // tiles of this stream so far
-  int i = 0;               // tiles of the CTA so far
+  RingPos k = {0, 0};      // the next tile's K
   int nspan = 0;           // spans of the CTA so far
   int np0 = 0, np1 = 0;    // tiles tidied by each stream so far
   float m = 0.f, l = 0.f;  // the row's maximum; this half's sum
@@ -611,18 +639,18 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     if (lane == 0) mbar_arrive(&S.q_full[q]);
     if (step == 2) {
       if (rec_cols > 0) record();
-      const int64_t k = static_cast<int64_t>(w.head) * w.n_groups + w.group;
+      const int64_t p = static_cast<int64_t>(w.head) * w.n_groups + w.group;
       rec_cols = w.g.n_cols;
       rec_col = col;
       if (kFp8) rec_scale = a.v_scale[w.head];
       // one record a CTA, or one a stream
-      const int nth = static_cast<int>(blockIdx.x) - tree_at<int2>(a, a.L.piece_cta)[k].x;
-      rec = tree_at<int32_t>(a, a.L.piece_row)[k] + static_cast<int64_t>(two ? nth : w.streams * nth + q) * rec_cols;
+      const int nth = static_cast<int>(blockIdx.x) - tree_at<int2>(a, a.L.piece_cta)[p].x;
+      rec = tree_at<int32_t>(a, a.L.piece_row)[p] + static_cast<int64_t>(two ? nth : w.streams * nth + q) * rec_cols;
       some = false;
       turn = 0;
     }
     ++nspan;
-    for (int t = 0; t < w.tiles; ++t, ++i, turn ^= 1) {
+    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turn ^= 1) {
       const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
       const int owner = two ? 0 : turn;  // who tidies the V tile, where that is needed
       const bool tidy = w.sp.partial || (valid & (kStep - 1));
@@ -633,15 +661,16 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
       idle_wait(S, a, &S.s_full[q], ns & 1);
       bool bad = false;
       if (tidy) {
-        const int nv = 2 * i + 1, np = owner ? np1 : np0, par = np & 1;
+        const int np = owner ? np1 : np0, par = np & 1;
+        const RingPos v = k.next(w.stages);
         if (q == owner) {
           // 0 * NaN would poison a sum.  V rows past the span, up to the end
           // of the last step of tokens, may hold anything: cleared.  In a
           // tile that not every column sees, so are values that are not
           // finite: the columns that see their token get a NaN through l.
-          idle_wait(S, a, &S.kv_full[nv % kStages], (nv / kStages) & 1);
+          idle_wait(S, a, &S.kv_full[v.s], v.phase);
           constexpr int kPieces = kFp8 ? 4 : 8;  // 16-byte pieces of a row's half
-          const uint32_t at = smem_u32(S.kv[nv % kStages]) + half * (kFp8 ? 64 : kBox) + row * 128;
+          const uint32_t at = w.ring + v.s * Ring<kFp8>::kStage + half * (kFp8 ? 64 : kBox) + row * 128;
           const bool clear = row >= valid && row < ((valid + kStep - 1) & ~(kStep - 1));
           bool odd = false;
           if (w.sp.partial && row < valid)
@@ -787,10 +816,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   Walk w = {tree_at<TreeGroup>(a, a.L.groups), tree_at<TreeSpan>(a, a.L.spans), hdr.n_groups, hdr.streams,
-            c.head, c.group, c.span, c.tile, c.n_units, c.g, c.sp, 0};
+            c.head, c.group, c.span, c.tile, c.n_units, c.g, c.sp, 0,
+            Ring<kFp8>::kStages + (c.wide ? 0 : Ring<kFp8>::kMore), smem_u32(c.wide ? S.kv[0] : S.q[1])};
   w.begin();
   if (tid == 0) {
-    for (int s = 0; s < Ring<kFp8>::kStages; ++s) {
+    for (int s = 0; s < TcSmem<kFp8>::kAll; ++s) {
       mbar_init(&S.kv_full[s], 1);
       mbar_init(&S.kv_empty[s], 2);  // one arrival a stream
     }
