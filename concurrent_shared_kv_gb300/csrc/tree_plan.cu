@@ -17,7 +17,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Weights of the unit line, measured on the tensor-core kernel (a fit of its
-// CTAs' times) in steps of 375 clocks: a tile against up to 128 columns and
+// CTAs' times) in steps of about 420 clocks: a tile against up to 128 columns and
 // against more, what a span's new queries and empty pipeline cost beside its
 // tiles, a tree's more of that, a group's records.  Where every unit can have
 // a CTA of its own, each does: the units then weigh the same.
@@ -25,7 +25,7 @@ struct TreeCost {
   int32_t tile1, tile2, span, tree, group;
 };
 __device__ inline TreeCost tree_cost(int cols, bool e4m3, bool alone) {
-  return alone ? TreeCost{1, 1, 0, 0, 0} : cols <= 128 ? TreeCost{4, 4, 1, 0, 1} : e4m3 ? TreeCost{7, 13, 27, 4, 8} : TreeCost{5, 8, 17, 6, 18};
+  return alone ? TreeCost{1, 1, 0, 0, 0} : cols <= 128 ? TreeCost{4, 4, 1, 0, 1} : e4m3 ? TreeCost{6, 13, 27, 4, 8} : TreeCost{4, 7, 17, 8, 22};
 }
 
 struct TreePlanSmem {
