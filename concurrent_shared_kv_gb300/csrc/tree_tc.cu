@@ -343,11 +343,13 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
     for (int k = 0; k < 128 / kStep; ++k)
       if (k < pend_steps) {
         const uint64_t b = bs + ((k * kStep * 128) >> 4);
+        // (each half of the tokens has its weights in the first columns of its scores')
+        const uint32_t p = s_tmem + (k * kStep >= 64 ? 64 + (k * kStep - 64) / (kFp8 ? 4 : 2) : k * kStep / (kFp8 ? 4 : 2));
         if constexpr (kFp8) {
-          mma_f8_ts(o_tmem, s_tmem + k * 8, b, idesc_pv, !(pend_first && k == 0));
-          mma_f8_ts(o_tmem, s_tmem + 32 + k * 8, b, idesc_pv, true);
+          mma_f8_ts(o_tmem, p, b, idesc_pv, !(pend_first && k == 0));
+          mma_f8_ts(o_tmem, p + 16, b, idesc_pv, true);
         } else {
-          mma_bf16_ts(o_tmem, s_tmem + k * 8, b, idesc_pv, !(pend_first && k == 0));
+          mma_bf16_ts(o_tmem, p, b, idesc_pv, !(pend_first && k == 0));
         }
       }
     mma_commit(&S.pv_done[q]);
@@ -702,31 +704,34 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
       }
       if (warp_on) {
         tc_fence_after();
-        uint32_t s[2][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(s_tmem + 64 * half + 32 * c, s[c]);
-        tmem_wait_ld();
-        if (valid < kT || w.sp.partial) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
+        // Half of the row's scores are in registers at a time, those of tokens
+        // 32-63 twice: what does not fit there is kept in local memory, for
+        // which the shared memory in use leaves next to no L1.
+        uint32_t s[32];
+        auto load = [&](int c) {
+          tmem_ld32(s_tmem + 64 * half + 32 * c, s);
+          tmem_wait_ld();
+          if (valid < kT || w.sp.partial) {
             const int in = min(32, max(0, valid - 64 * half - 32 * c));
             const uint32_t bits = (c ? see.y : see.x) & (in == 32 ? ~0u : (1u << in) - 1u);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!((bits >> j) & 1u)) s[c][j] = 0xff800000u;  // -inf
+              if (!((bits >> j) & 1u)) s[j] = 0xff800000u;  // -inf
           }
-        }
-        float mx[2];
+        };
+        float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+        for (int c = 1; c >= 0; --c) {
+          load(c);
+          float mx[2] = {-INFINITY, top};
 #pragma unroll
-          for (int j = 2; j < 32; j += 2)
-            mx[c] = max3(mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+          for (int j = 0; j < 32; j += 4) {
+            mx[0] = max3(mx[0], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            mx[1] = max3(mx[1], __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+          }
+          top = fmaxf(mx[0], mx[1]);
         }
-        float top = fmaxf(mx[0], mx[1]);
-        // (also: both halves of S are read, so P may be written over them; and
-        // the partner has read this before the next tile's scores can come)
+        // (the partner has read this before the next tile's scores can come)
         S.red[q][half][row] = top;
         pair_sync(pair);
         top = fmaxf(top, S.red[q][half ^ 1][row]);
@@ -755,29 +760,35 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
         }
         const uint64_t neg = pack2(-m, -m), mul = pack2(f, f);
         uint64_t sum[2] = {0, 0};
-        uint32_t p[kFp8 ? 1 : 32], hi[kFp8 ? 16 : 1], lo[kFp8 ? 16 : 1];
+        // P goes over this half's own scores, the first 32 tokens': the partner
+        // and the second load are not disturbed
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint64_t s2 = pack2(__uint_as_float(s[j / 16][2 * j % 32]), __uint_as_float(s[j / 16][2 * j % 32 + 1]));
-          float p0, p1;
-          unpack2(kFp8 ? fma2(s2, mul, neg) : add2(s2, neg), p0, p1);
-          p0 = ex2(p0);
-          p1 = ex2(p1);
-          sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
-          if constexpr (kFp8) {
-            uint32_t h2, l2;
-            split_e4m3(p0, p1, h2, l2);
-            hi[j / 2] = j & 1 ? hi[j / 2] | h2 << 16 : h2;
-            lo[j / 2] = j & 1 ? lo[j / 2] | l2 << 16 : l2;
-          } else {
-            p[j] = pack_bf16(p0, p1);
+        for (int c = 0; c < 2; ++c) {
+          if (c == 1) load(1);
+          uint32_t p[kFp8 ? 1 : 16], hi[kFp8 ? 8 : 1], lo[kFp8 ? 8 : 1];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t s2 = pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+            float p0, p1;
+            unpack2(kFp8 ? fma2(s2, mul, neg) : add2(s2, neg), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
+            if constexpr (kFp8) {
+              uint32_t h2, l2;
+              split_e4m3(p0, p1, h2, l2);
+              hi[j / 2] = j & 1 ? hi[j / 2] | h2 << 16 : h2;
+              lo[j / 2] = j & 1 ? lo[j / 2] | l2 << 16 : l2;
+            } else {
+              p[j] = pack_bf16(p0, p1);
+            }
           }
-        }
-        if constexpr (kFp8) {  // four codes a column: hi in 0 .. 31, lo in 32 .. 63
-          tmem_st16(s_tmem + 16 * half, hi);
-          tmem_st16(s_tmem + 32 + 16 * half, lo);
-        } else {
-          tmem_st32(s_tmem + 32 * half, p);
+          if constexpr (kFp8) {  // four codes a column: hi, and 16 columns further lo
+            tmem_st8(s_tmem + 64 * half + 8 * c, hi);
+            tmem_st8(s_tmem + 64 * half + 16 + 8 * c, lo);
+          } else {
+            tmem_st16(s_tmem + 64 * half + 16 * c, p);
+          }
         }
         float x[4];
         unpack2(sum[0], x[0], x[1]);
