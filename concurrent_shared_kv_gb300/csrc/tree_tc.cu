@@ -238,9 +238,8 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 
 // The CTA's units, span by span.
 struct Walk {
-  const TreeGroup *groups;
-  const TreeSpan *spans;
-  int n_groups, streams;
+  const TreeArgs &a;
+  int streams;
   int head, group, span, tile, left;  // kv head, group, span, its first tile, units still to come
   TreeGroup g;
   TreeSpan sp;
@@ -248,11 +247,11 @@ struct Walk {
   int stages;     // of the ring
   uint32_t ring;  // its shared-memory address
   __device__ __forceinline__ void load_span() {
-    sp = spans[g.span0 + span];
+    sp = tree_at<TreeSpan>(a, a.L.spans)[g.span0 + span];
     begin();
   }
   __device__ __forceinline__ void begin() {
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(spans + g.span0 + span + 1));
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(tree_at<TreeSpan>(a, a.L.spans) + g.span0 + span + 1));
     tiles = min((sp.len + kT - 1) / kT - tile, left);
   }
   // On to the next span: 0 at the end, 1 in the same group, 2 in another one.
@@ -263,11 +262,11 @@ struct Walk {
     const bool other = ++span == g.n_spans;
     if (other) {
       span = 0;
-      if (++group == n_groups) {
+      if (++group == tree_at<TreeHeader>(a, a.L.hdr)->n_groups) {
         group = 0;
         ++head;
       }
-      g = groups[group];
+      g = tree_at<TreeGroup>(a, a.L.groups)[group];
     }
     load_span();
     return other ? 2 : 1;
@@ -517,22 +516,17 @@ __device__ __forceinline__ void store_record(const TreeArgs &a, uint32_t o_tmem,
                                              int half, float scale) {
   float *dst = tree_at<float>(a, a.L.o) + rec * 128 + col * 8 + static_cast<int64_t>(half) * 8 * n_cols * 8;
   const bool on = col < n_cols;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t r[32];
-    tmem_ld32(o_tmem + 64 * half + 32 * c, r);
+#pragma unroll 4
+  for (int c = 0; c < 8; ++c) {
+    uint32_t r[8];
+    tmem_ld8(o_tmem + 64 * half + 8 * c, r);
     tmem_wait_ld();
 #pragma unroll
-    for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * scale);
-    if (on) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                         dst + static_cast<int64_t>(4 * c + x) * n_cols * 8),
-                     "r"(r[8 * x]), "r"(r[8 * x + 1]), "r"(r[8 * x + 2]), "r"(r[8 * x + 3]), "r"(r[8 * x + 4]),
-                     "r"(r[8 * x + 5]), "r"(r[8 * x + 6]), "r"(r[8 * x + 7])
-                     : "memory");
-    }
+    for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * scale);
+    if (on)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + static_cast<int64_t>(c) * n_cols * 8),
+                   "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                   : "memory");
   }
 }
 
@@ -576,8 +570,6 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
   int rec_cols = 0, rec_col = 0;
   float rec_scale = 1.f;   // E4M3: its kv head's v_scale
   bool some = false;       // the stream had a tile of it
-  TreeColumn tc = {};
-  int src = 0;             // the row's query (row 0 where there is none)
   auto record = [&]() {
     const bool on = rec_col - lane < rec_cols;  // (the same for the pair's warps)
     if (some) idle_wait(S, a, &S.pv_done[q], (ns - 1) & 1);
@@ -601,15 +593,12 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     const int col = two ? q * 128 + row : row;               // the thread's column of the group
     const bool mine = col < w.g.n_cols;                      // a query in this row
     const bool warp_on = col - lane < w.g.n_cols;
-    int heads = 0;  // the kv head's q heads, a lane each
-    if (step == 2) {
-      const int G = a.n_q_heads / a.n_kv_heads;
-      heads = tree_at<int32_t>(a, a.L.heads)[w.head * G + min(lane, G - 1)];
-    }
-    if (mine && step == 2) {
-      tc = tree_at<TreeColumn>(a, a.L.columns)[w.g.col0 + col];
-    }
-    if (step == 2) src = tc.node * a.n_q_heads + __shfl_sync(0xffffffffu, heads, tc.head);
+    // (loaded again for every span of a group: registers are what is short)
+    const int G = a.n_q_heads / a.n_kv_heads;
+    const int heads = tree_at<int32_t>(a, a.L.heads)[w.head * G + min(lane, G - 1)];  // the kv head's q heads, a lane each
+    TreeColumn tc = {};
+    if (mine) tc = tree_at<TreeColumn>(a, a.L.columns)[w.g.col0 + col];
+    const int src = tc.node * a.n_q_heads + __shfl_sync(0xffffffffu, heads, tc.head);  // the row's query (row 0 where there is none)
     // the tokens the column sees: all, a node's ancestors and itself, or none
     uint2 see = make_uint2(0, 0);
     int v = -1;
@@ -643,7 +632,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     if (lane == 0) mbar_arrive(&S.q_full[q]);
     if (step == 2) {
       if (rec_cols > 0) record();
-      const int64_t p = static_cast<int64_t>(w.head) * w.n_groups + w.group;
+      const int64_t p = static_cast<int64_t>(w.head) * tree_at<TreeHeader>(a, a.L.hdr)->n_groups + w.group;
       rec_cols = w.g.n_cols;
       rec_col = col;
       if (kFp8) rec_scale = a.v_scale[w.head];
@@ -828,8 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  Walk w = {tree_at<TreeGroup>(a, a.L.groups), tree_at<TreeSpan>(a, a.L.spans), hdr.n_groups, hdr.streams,
-            c.head, c.group, c.span, c.tile, c.n_units, c.g, c.sp, 0,
+  Walk w = {a, hdr.streams, c.head, c.group, c.span, c.tile, c.n_units, c.g, c.sp, 0,
             Ring<kFp8>::kStages + (c.wide ? 0 : Ring<kFp8>::kMore), smem_u32(c.wide ? S.kv[0] : S.q[1])};
   w.begin();
   if (tid == 0) {
