@@ -90,7 +90,7 @@ struct TcSmem {
   alignas(1024) uint8_t q[2][kQTile];                     // (the second tile's place: part of the ring without one)
   alignas(1024) uint8_t kv[kStages][Ring<kFp8>::kStage];
   uint64_t kv_full[kAll], kv_empty[kAll];
-  uint64_t q_full[2], q_free, s_full[2], p_full[2], pv_done[2], o_empty[2], order, mma_done;
+  uint64_t q_full[2], q_free, s_full[2], p_half[2], p_full[2], pv_done[2], o_empty[2], order, mma_done;
   // tidied V tiles, by the stream that does it, alternating; the tokens with a value that is not finite
   uint64_t scanned[2][2];
   uint32_t bad[2][2][2][4];
@@ -329,18 +329,19 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
   RingPos pend_v = {0, 0};
   int pend_steps = 0;
   bool pend = false, pend_first = false, pend_two = false, first = true;
-  // Everything but P is waited for first: P is what the products wait for.
+  // Everything but P is waited for first: P is what the products wait for.  It
+  // comes in two parts, the first 32 tokens of each half of the tile before
+  // the others; the first part's products run while the second is computed.
   auto pv_ready = [&]() -> bool {
     return warp_wait(S, a, &S.kv_full[pend_v.s], pend_v.phase) &&
            (!pend_first || warp_wait(S, a, &S.o_empty[q], (no++ & 1) ^ 1)) &&
-           warp_wait(S, a, &S.p_full[q], np & 1);
+           warp_wait(S, a, &S.p_half[q], np & 1);
   };
-  auto pv = [&]() {  // by the elected lane
-    const int s = pend_v.s;
-    const uint64_t bs = b_pv + ((s * kStage) >> 4);
+  auto pv_part = [&](int part) {  // by the elected lane
+    const uint64_t bs = b_pv + ((pend_v.s * kStage) >> 4);
 #pragma unroll
     for (int k = 0; k < 128 / kStep; ++k)
-      if (k < pend_steps) {
+      if (((k * kStep >> 5) & 1) == part && k < pend_steps) {
         const uint64_t b = bs + ((k * kStep * 128) >> 4);
         // (each half of the tokens has its weights in the first columns of its scores')
         const uint32_t p = s_tmem + (k * kStep >= 64 ? 64 + (k * kStep - 64) / (kFp8 ? 4 : 2) : k * kStep / (kFp8 ? 4 : 2));
@@ -351,13 +352,24 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
           mma_bf16_ts(o_tmem, p, b, idesc_pv, !(pend_first && k == 0));
         }
       }
+  };
+  auto pv_first = [&]() -> bool {
+    if (!pv_ready()) return false;
+    tc_fence_after();
+    if (elect_one()) pv_part(0);
+    __syncwarp();
+    return warp_wait(S, a, &S.p_full[q], np & 1);
+  };
+  auto pv = [&]() {  // what is left of them, by the elected lane
+    const int s = pend_v.s;
+    pv_part(1);
     mma_commit(&S.pv_done[q]);
     mma_commit(&S.kv_empty[s]);
     if (!pend_two) mma_commit(&S.kv_empty[s]);  // (for the other stream, which does not use it)
   };
   // The products that end a group, outside the order of the others.
   auto flush = [&]() -> bool {
-    if (!pv_ready()) return false;
+    if (!pv_first()) return false;
     tc_fence_after();
     if (elect_one()) pv();
     __syncwarp();
@@ -392,7 +404,7 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
       // both would wait for both, and their softmaxes would run at the same
       // time, the tensor cores idle.
       if (mine > 0 && !(go = warp_wait(S, a, &S.order, (mine - 1) & 1))) break;
-      if (pend && !(go = pv_ready())) break;
+      if (pend && !(go = pv_first())) break;
       if (!turned && !(go = queries(two))) break;
       turned = true;
       tc_fence_after();
@@ -778,12 +790,20 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
           } else {
             tmem_st16(s_tmem + 64 * half + 16 * c, p);
           }
+          if (c == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_half[q]);
+          }
         }
         float x[4];
         unpack2(sum[0], x[0], x[1]);
         unpack2(sum[1], x[2], x[3]);
         l += ((x[0] + x[1]) + (x[2] + x[3])) + (bad ? NAN : 0.f);
         tmem_wait_st();
+      } else if (lane == 0) {
+        mbar_arrive(&S.p_half[q]);
       }
       tc_fence_before();
       __syncwarp();
@@ -828,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = 0; q < 2; ++q) {
       mbar_init(&S.q_full[q], 8);
       mbar_init(&S.s_full[q], 1);
+      mbar_init(&S.p_half[q], 8);
       mbar_init(&S.p_full[q], 8);
       mbar_init(&S.pv_done[q], 1);
       mbar_init(&S.o_empty[q], 8);
