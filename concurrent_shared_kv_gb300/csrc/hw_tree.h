@@ -45,6 +45,9 @@ namespace hw {
 
 constexpr uint32_t kTreeMagic = 0x48577472u;
 constexpr int kMaxNodes = HW_MAX_TREE_NODES;
+// The running maximum before any score: finite, so that what sees nothing gets
+// weights of 0, and what sees only NaN a sum of NaN, not none.
+constexpr float kNoScore = -3.402823466e38f;
 
 struct TreeHeader {
   uint32_t magic;

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     const int h = at.head, nq = gr.n_cols;
     if (tid < nq) {
       S.col[tid] = tree_at<TreeColumn>(a, a.L.columns)[gr.col0 + tid];
-      S.m[tid] = -INFINITY;
+      S.m[tid] = kNoScore;
       S.l[tid] = 0.f;
     }
     float acc[QPT];
@@ -159,8 +159,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
           for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           const float m_old = S.m[qq];
           const float m_new = fmaxf(m_old, mx);
-          const float base = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: weights 0, no NaN
-          const float p0 = ex2(s0 - base), p1 = ex2(s1 - base);
+          const float p0 = ex2(s0 - m_new), p1 = ex2(s1 - m_new);
           float sum = p0 + p1;
           if ((in0 && (S.bad[0] >> lane) & 1u) || (in1 && (S.bad[1] >> lane) & 1u)) sum = NAN;
 #pragma unroll
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
           S.p[qq][lane] = p0;
           S.p[qq][lane + 32] = p1;
           if (lane == 0) {
-            const float alpha = ex2(m_old - base);
+            const float alpha = ex2(m_old - m_new);
             S.alpha[qq] = alpha;
             S.m[qq] = m_new;
             S.l[qq] = S.l[qq] * alpha + sum;

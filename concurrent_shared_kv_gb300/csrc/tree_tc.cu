@@ -740,7 +740,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
         if constexpr (kFp8) top *= f;
         constexpr float lift = kFp8 ? kLift : 0.f;
         if (!some) {
-          m = fmaxf(top - lift, -1e30f);  // (nothing seen yet: weights 0, no NaN)
+          m = fmaxf(top - lift, kNoScore);
           l = 0.f;
         } else if (__any_sync(0xffffffffu, mine && top > m + kLazy)) {
           // (rows without a query hold anything: they must not count)

@@ -355,8 +355,8 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
  *  lse         dev  float [n_rows][max_nodes][Hq] or NULL
  * (q, k_new, v_new, out bf16 for HW_FP8_E4M3 caches).  Entries of q, k_new and
  * v_new at or behind n_nodes[r] are not read, those of out and lse keep what
- * they hold.  v_new must be finite: as in any masked product, an infinite or
- * NaN value reaches the nodes that do not attend it too.
+ * they hold.  Keys and values that are not finite touch only the
+ * nodes that attend them.
  *
  * The trees' tokens lie outside every block and one another.  A row whose
  * tree does not (or leaves the pool) sets HW_DEV_BAD_RANGE, one whose counts
@@ -419,8 +419,9 @@ int hw_attn_decode_tree_fp8(const hw_attn_desc *d, int32_t max_nodes, const void
  *  path        dev int32 [n_rows][max_nodes]: 0, then the accepted nodes, then -1
  *  n_path      dev int32 [n_rows]: their number with the root
  *  next_token  dev int32 [n_rows]
- * Sums are kept in 64-bit fixed point, so the result does not depend on the
- * order of anything.  A row with n_nodes 0, or whose counts, parents or tokens
+ * Sums and tests are kept in 64-bit fixed point with 56 bits behind the point
+ * (smaller values count as 0), so the result does not depend on the order of
+ * anything.  A row with n_nodes 0, or whose counts, parents or tokens
  * (of nodes 1 ..) are out of range, gets n_path 0 and next_token -1.
  */
 int hw_tree_verify(int32_t dtype, int32_t n_rows, int32_t max_nodes, int32_t vocab,

@@ -703,3 +703,162 @@ def test_outputs_at_any_element_address():
         o2 = buf[1:].view(o1.shape)
         t.run(s, o2, l1)
         assert torch.equal(o1, o2) and float(buf[0]) == 0
+
+
+# ------------------------------------------------------- values, views, sizes
+
+def bits(x):
+    return x.contiguous().view(torch.uint8)
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("where", ["v_new", "k_new", "v", "k", "q"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_stay_with_their_readers(dtype, d, where, value):
+    """Queries that do not attend such a token give the same bits as without
+    it; those that do are not finite."""
+    def make():
+        return Tree(dtype, hq=6, hkv=2, d=d, lens=(200, 40, 130), views=([[0, 1], [0, 2]], [[0, 200], [0, 200]], [240, 330]),
+                    T=7, kind="forest", seed=60)
+    clean, t = make(), make()
+    o0, l0 = clean.run(clean.session())
+    touched = torch.zeros(t.R, t.T, t.hq, dtype=torch.bool, device="cuda")
+    G = t.hq // t.hkv
+    if where in ("v_new", "k_new"):   # row 0's node 2, kv head 1
+        getattr(t, where)[0, 2, 1, 5] = value
+        anc = ref.ancestors(t.parent[0], t.T)
+        for i in range(t.T):
+            touched[0, i, G:] = bool(anc[i, 2])
+    elif where == "q":
+        t.q[1, 3, 4, 9] = value
+        touched[1, 3, 4] = True
+    else:                             # block 2, which row 0 does not see
+        getattr(t, where)[0, int(t.block_start[2]) + 5, 7] = value if dtype != "fp8" else float("nan")
+        touched[1, :, :G] = True
+    o1, l1 = t.run(t.session())
+    assert torch.equal(bits(o1[~touched]), bits(o0[~touched])) and torch.equal(l1[~touched], l0[~touched])
+    stored_as_448 = dtype == "fp8" and where in ("v_new", "k_new") and value == value
+    # (an infinite score of -inf is a token without weight)
+    if not stored_as_448 and not (value != value) and where in ("k_new", "k"):
+        return
+    if not stored_as_448:
+        assert not torch.isfinite(o1[touched].float()).all(-1).any()
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("power", [-30, 20])
+def test_scaled_queries(dtype, d, power):
+    """Powers of two that move from the queries to the softmax scale."""
+    t = Tree(dtype, hq=6, hkv=2, d=d, lens=(150, 40), T=5, seed=61)
+    o1, l1 = t.run(t.session())
+    o1, l1 = o1.clone(), l1.clone()
+    t.q = t.q * 2.0 ** power
+    t.scale = t.scale * 2.0 ** -power
+    o2, l2 = t.run(t.session())
+    assert torch.equal(bits(o1), bits(o2)) and torch.equal(l1, l2)
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_queries_of_zero(dtype, d):
+    t = Tree(dtype, hq=6, hkv=2, d=d, lens=(150, 40), T=5, seed=62)
+    t.q.zero_()
+    t.check()
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_wide_and_narrow_groups_in_turn(dtype, d):
+    # 700, 42 and 350 columns a kv head: full groups of queries and rests, for one CTA or more each
+    Tree(dtype, hq=14, hkv=2, d=d, lens=(700, 60, 33, 129), T=100, n_nodes=[100, 6, 50], seed=63).check()
+    Tree(dtype, hq=14, hkv=2, d=d, lens=(9000, 60, 33, 129), T=50, n_nodes=[50, 6, 21], seed=64).check(what="long")
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("seed", [65, 66, 67])
+def test_rows_with_views_of_their_own(dtype, d, seed):
+    rng = np.random.Generator(np.random.PCG64(seed))
+    B, R, V = 9, 12, 5
+    lens = [int(x) for x in rng.integers(0, 300, B)]
+    vb = rng.integers(-1, B, (R, V))
+    vo = rng.integers(0, 2000, (R, V))
+    Tree(dtype, hq=4, hkv=2, d=d, lens=lens, views=(vb, vo, rng.integers(500, 3000, R)),
+         tree_block=rng.integers(0, B, R), n_nodes=rng.integers(0, 12, R), T=11, seed=seed).check()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp8", 128), ("f32", 64)])
+def test_hundreds_of_rows(dtype, d):
+    # (two rows a block: HW_MAX_BLOCKS is 256)
+    lens = [30] + [int(x) for x in np.random.default_rng(2).integers(0, 9, 250)]
+    own = 1 + np.arange(500) % 250
+    Tree(dtype, hq=2, hkv=1, d=d, lens=lens, views=([[0, b] for b in own], [[0, 30]] * 500, [31] * 500), tree_block=own, T=2,
+         seed=68).check()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp8", 128), ("f32", 128)])
+def test_offsets_past_32_bits(dtype, d):
+    """The same tokens in a small pool and at the end of one whose elements
+    pass 2^32: the same bits."""
+    t = Tree(dtype, hq=4, hkv=2, d=d, lens=(300, 40, 129), T=6, seed=69, poison=False)
+    o1, l1 = t.run(t.session())
+    o1, l1 = o1.clone(), l1.clone()
+    small = t.k.clone(), t.v.clone()
+    end = 2 ** 32 // (2 * d) + 1000    # tokens of a head; two heads
+    move = end - t.cap
+    big = torch.zeros(2, 2, end, d, dtype=t.k.dtype, device="cuda")
+    big[0, :, move:], big[1, :, move:] = t.k, t.v
+    for r in range(t.R):               # without the trees' tokens
+        big[:, :, move + int(t.tree_start[r]):move + int(t.tree_start[r]) + t.T] = 0
+    t.k, t.v, t.cap = big[0], big[1], end
+    t.block_start, t.tree_start = t.block_start + move, t.tree_start + move
+    s = t.session()
+    o2, l2 = t.run(s)
+    assert torch.equal(bits(o1), bits(o2)) and torch.equal(l1, l2)
+    assert torch.equal(bits(t.k[:, move:]), bits(small[0])) and torch.equal(bits(t.v[:, move:]), bits(small[1]))
+    assert int(bits(t.k[:, :move]).max()) == 0
+    # an accepted path moves there too
+    path = np.full((t.R, t.T), -1, np.int32)
+    path[:, :2] = [0, 3]
+    s.commit(t.k, t.v, ref.dev(path), ref.dev([2] * t.R))
+    assert s.device_flags() == 0
+    for r in range(t.R):
+        at, src = int(t.block_start[r + 1] + t.block_len[r + 1]), int(t.tree_start[r])
+        for j, i in enumerate((0, 3)):
+            assert torch.equal(bits(t.k[:, at + j]), bits(t.k[:, src + i]))
+            assert torch.equal(bits(t.v[:, at + j]), bits(t.v[:, src + i]))
+
+
+@pytest.mark.parametrize("R", [3, 25])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_long_vocabularies(R, dtype, drawn):
+    # few rows: sixteen CTAs each; many: eight; the longer vocabulary is read again at every step
+    for V in (150_001, 1_500_000 if R == 3 else 700_000):
+        rng = np.random.Generator(np.random.PCG64(V))
+        T = 3
+        w = rng.random((R, T, V), dtype=np.float32) ** 8
+        p = torch.tensor(w / w.sum(-1, keepdims=True))
+        w *= rng.random((R, T, V), dtype=np.float32) + 0.5
+        q = torch.tensor(w / w.sum(-1, keepdims=True))
+        dt = torch.float32 if dtype == "f32" else torch.bfloat16
+        # (the likeliest of 64 tokens: what is below 2^-56 counts as 0, and was not drawn either)
+        some = rng.integers(0, V, (R, T, 64))
+        token = np.take_along_axis(some, np.take_along_axis(w[:, :1].repeat(T, 1), some, 2).argmax(2)[..., None], 2)[..., 0].astype(np.int32)
+        x = dict(n_nodes=np.full(R, T), parent=np.tile([-1, 0, 0], (R, 1)), token=token, p=p.to(dt), q=q.to(dt) if drawn else None, u_accept=rng.random((R, T), dtype=np.float32),
+                 u_sample=rng.random(R, dtype=np.float32))
+        check_verify(x)
+
+
+def test_sessions_that_share_a_pool_and_a_stream():
+    """Two plans in turn on one pool, as two groups of workers would have:
+    neither disturbs the other's blocks."""
+    a = Tree("bf16", hq=4, hkv=2, lens=(300, 40, 129), T=6, seed=70)
+    b = Tree("bf16", hq=4, hkv=2, lens=(90, 200), T=4, seed=71)
+    pool_k = torch.cat([a.k, b.k], 1).contiguous()
+    pool_v = torch.cat([a.v, b.v], 1).contiguous()
+    b.block_start, b.tree_start = b.block_start + a.cap, b.tree_start + a.cap
+    a.cap = b.cap = a.cap + b.cap
+    for t in (a, b):
+        t.k, t.v = pool_k, pool_v
+    sa, sb = a.session(), b.session()
+    b.check(s=sb)
+    a.check(s=sa)
+    b.check(s=sb)
