@@ -139,9 +139,10 @@ def _ptr(x) -> Optional[int]:
     """Device/host pointer of a tensor, numpy array or int (None stays NULL)."""
     if x is None:
         return None
-    data_ptr = getattr(x, "data_ptr", None)
-    if data_ptr is not None:
-        return data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
     if isinstance(x, np.ndarray):
@@ -149,13 +150,21 @@ def _ptr(x) -> Optional[int]:
     raise TypeError(type(x))
 
 
+_torch_c = None
+
+
 def _raw_stream() -> int:
     """The current CUDA stream's handle.  (torch.cuda.current_stream() builds an
     object around it: 3 us of a call that may run for 5.)"""
-    import torch
+    global _torch_c
+    if _torch_c is None:
+        import torch
+        torch.cuda.current_device()
+        _torch_c = torch._C
     try:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
     except AttributeError:
+        import torch
         return torch.cuda.current_stream().cuda_stream
 
 

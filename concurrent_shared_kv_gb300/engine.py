@@ -172,6 +172,17 @@ def _int32(x, device):
     return t.to(device, dtype=torch.int32).contiguous()
 
 
+def _fits(what: str, x, n: int, dtype) -> None:
+    """A dense tensor of n elements: what a kernel would read past otherwise."""
+    if x.numel() != n or x.dtype != dtype or not x.is_contiguous():
+        raise ValueError(f"{what} needs {n} dense elements of {dtype}, got {tuple(x.shape)} of {x.dtype}")
+
+
+def _pool_fits(what: str, x, n: int, dtype) -> None:
+    if x.numel() != n or x.element_size() != dtype.itemsize or not x.is_contiguous():  # (E4M3 may be held as bytes)
+        raise ValueError(f"{what} needs {n} dense elements of {dtype}, got {tuple(x.shape)} of {x.dtype}")
+
+
 class TreeSession:
     """Steps whose rows each query a tree of drafted tokens: plan(), one
     decode() a layer, tree_verify(), commit()."""
@@ -193,16 +204,30 @@ class TreeSession:
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         api.workspace_init(self.workspace, self.ws_bytes)
         self.meta = None
+        nodes = n_rows * self.max_nodes
+        self.sizes = (nodes * n_q_heads * head_dim, nodes * n_kv_heads * head_dim, n_kv_heads * capacity * head_dim)
+        self.cache_dtype = torch.float8_e4m3fn if kv_fp8 else dtype
 
     def set_metadata(self, block_start, block_len, view_block, view_offset, q_pos, q_to_kv=None):
         """Upload the step's views: those of the rows' tokens before their trees."""
         self.meta = [_int32(x, self.device) for x in (block_start, block_len, view_block, view_offset, q_pos)]
         self.q_to_kv = None if q_to_kv is None else _int32(q_to_kv, self.device)
+        d = self.desc
+        for what, x, n in zip(("block_start", "block_len", "view_block", "view_offset", "q_pos"), self.meta,
+                              (d.n_blocks, d.n_blocks, d.n_rows * d.max_view_blocks, d.n_rows * d.max_view_blocks, d.n_rows)):
+            _fits(what, x, n, torch.int32)
+        if self.q_to_kv is not None:
+            _fits("q_to_kv", self.q_to_kv, d.n_q_heads, torch.int32)
 
     def plan(self, tree_block, n_nodes, parent, tree_start=None, stream=None):
         """hw_attn_plan_tree: the step's trees (tree_start None: behind each row's block)."""
         self.trees = [_int32(x, self.device) for x in (tree_block, n_nodes, parent)]
         self.tree_start = None if tree_start is None else _int32(tree_start, self.device)
+        R = self.desc.n_rows
+        for what, x, n in zip(("tree_block", "n_nodes", "parent"), self.trees, (R, R, R * self.max_nodes)):
+            _fits(what, x, n, torch.int32)
+        if self.tree_start is not None:
+            _fits("tree_start", self.tree_start, R, torch.int32)
         api.attn_plan_tree(self.desc, self.max_nodes, *self.meta, *self.trees, self.workspace,
                            self.ws_bytes, tree_start=self.tree_start, q_to_kv=self.q_to_kv,
                            stream=stream)
@@ -216,12 +241,25 @@ class TreeSession:
             lse = torch.empty(shape, dtype=torch.float32, device=self.device)
         return out, lse
 
+    def _check_layer(self, q, k_new, v_new, k_cache, v_cache, out, lse):
+        n_q, n_new, n_pool = self.sizes
+        dtype, cache = self.dtype, self.cache_dtype
+        _fits("q", q, n_q, dtype)
+        _fits("k_new", k_new, n_new, dtype)
+        _fits("v_new", v_new, n_new, dtype)
+        _fits("out", out, n_q, dtype)
+        _pool_fits("k_cache", k_cache, n_pool, cache)
+        _pool_fits("v_cache", v_cache, n_pool, cache)
+        if lse is not None:
+            _fits("lse", lse, n_q // self.desc.head_dim, torch.float32)
+
     def decode(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                k_cache: torch.Tensor, v_cache: torch.Tensor, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
         """One layer: the trees' tokens written into the cache, then attended.
         Rows of out and lse behind a tree's nodes keep what they hold."""
         out, lse = self._outputs(out, lse, want_lse)
+        self._check_layer(q, k_new, v_new, k_cache, v_cache, out, lse)
         api.attn_decode_tree(self.desc, self.max_nodes, q, k_new, v_new, k_cache, v_cache, out, lse,
                              self.workspace, self.ws_bytes, stream=stream)
         return out, lse
@@ -232,6 +270,9 @@ class TreeSession:
                    lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
         """decode() over E4M3 pools with float32 scales [Hkv]; q and the new tokens bf16."""
         out, lse = self._outputs(out, lse, want_lse)
+        self._check_layer(q, k_new, v_new, k_cache, v_cache, out, lse)
+        _fits("k_scale", k_scale, self.desc.n_kv_heads, torch.float32)
+        _fits("v_scale", v_scale, self.desc.n_kv_heads, torch.float32)
         api.attn_decode_tree_fp8(self.desc, self.max_nodes, q, k_new, v_new, k_cache, v_cache,
                                  k_scale, v_scale, out, lse, self.workspace, self.ws_bytes,
                                  stream=stream)
@@ -242,6 +283,11 @@ class TreeSession:
         """The accepted nodes (tree_verify's path and n_path) appended to the
         rows' blocks in every layer; pools [layers][Hkv][cap][D] or [Hkv][cap][D]."""
         layers = 1 if k_cache.dim() == 3 else k_cache.shape[0]
+        n, R, cache = layers * self.sizes[2], self.desc.n_rows, self.cache_dtype
+        _pool_fits("k_cache", k_cache, n, cache)
+        _pool_fits("v_cache", v_cache, n, cache)
+        _fits("path", path, R * self.max_nodes, torch.int32)
+        _fits("n_path", n_path, R, torch.int32)
         api.tree_commit(self.desc, self.max_nodes, layers, k_cache, v_cache, path, n_path,
                         self.workspace, self.ws_bytes, stream=stream)
 
@@ -272,6 +318,15 @@ def tree_verify(n_nodes: torch.Tensor, parent: torch.Tensor, token: torch.Tensor
         n_path = torch.empty(R, dtype=torch.int32, device=p.device)
     if next_token is None:
         next_token = torch.empty(R, dtype=torch.int32, device=p.device)
+    i32 = torch.int32
+    _fits("n_nodes", n_nodes, R, i32)
+    _fits("parent", parent, R * T, i32)
+    _fits("token", token, R * T, i32)
+    _fits("path", path, R * T, i32)
+    _fits("n_path", n_path, R, i32)
+    _fits("next_token", next_token, R, i32)
+    _fits("u_accept", u_accept, R * T, torch.float32)
+    _fits("u_sample", u_sample, R, torch.float32)
     api.tree_verify(DTYPES[p.dtype], R, T, V, n_nodes, parent, token, p, step(p), q,
                     0 if q is None else step(q), u_accept, u_sample, path, n_path, next_token,
                     stream=stream)

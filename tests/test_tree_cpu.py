@@ -135,3 +135,43 @@ def test_verify_tensor_layouts():
         engine.tree_verify(i[:, 0], i, i, p[..., ::2], None, u, u[:, 0])
     with pytest.raises(ValueError):
         engine.tree_verify(i[:, 0], i, i, torch.zeros(4, 3, 8)[::2], None, u, u[:, 0])
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    """What a kernel would read past: refused before the library is called."""
+    torch = pytest.importorskip("torch")
+    from concurrent_shared_kv_gb300 import engine
+    i, f, p = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3), torch.zeros(2, 3, 8)
+    good = dict(n_nodes=i[:, 0].contiguous(), parent=i, token=i, p=p, q=None, u_accept=f, u_sample=f[:, 0].contiguous())
+    for name, bad in (("n_nodes", i[0]), ("n_nodes", i[:, 0]), ("parent", i[:, :2]), ("parent", i.long()), ("token", i[:1]),
+                      ("u_accept", f.double()), ("u_accept", f[:, :2]), ("u_sample", f[0])):
+        with pytest.raises(ValueError, match=name):
+            engine.tree_verify(**{**good, name: bad})
+    s = object.__new__(engine.TreeSession)   # (a session needs a device)
+    s.desc, s.max_nodes, s.device = desc(n_rows=2, max_view_blocks=2), 3, torch.device("cpu")
+    s.dtype = s.cache_dtype = torch.bfloat16
+    s.sizes, s.workspace, s.ws_bytes = (2 * 3 * 8 * 128, 2 * 3 * 2 * 128, 2 * 1000 * 128), None, 0
+    meta = dict(block_start=[0] * 3, block_len=[0] * 3, view_block=[[0, 1]] * 2, view_offset=[[0, 1]] * 2, q_pos=[0, 0])
+    for name, bad in (("block_start", [0, 1]), ("view_block", [[0]] * 2), ("view_offset", [0] * 3), ("q_pos", [0])):
+        with pytest.raises(ValueError, match=name):
+            s.set_metadata(**{**meta, name: bad})
+    with pytest.raises(ValueError, match="q_to_kv"):
+        s.set_metadata(**meta, q_to_kv=[0])
+    s.set_metadata(**meta)
+    trees = dict(tree_block=[0, 1], n_nodes=[1, 1], parent=[[-1] * 3] * 2, tree_start=[0, 5])
+    for name, bad in (("tree_block", [0]), ("n_nodes", [1]), ("parent", [[-1] * 2] * 2), ("tree_start", [0])):
+        with pytest.raises(ValueError, match=name):
+            s.plan(**{**trees, name: bad})
+    bf = dict(dtype=torch.bfloat16)
+    layer = dict(q=torch.zeros(2, 3, 8, 128, **bf), k_new=torch.zeros(2, 3, 2, 128, **bf), v_new=torch.zeros(2, 3, 2, 128, **bf),
+                 k_cache=torch.zeros(2, 1000, 128, **bf), v_cache=torch.zeros(2, 1000, 128, **bf),
+                 out=torch.zeros(2, 3, 8, 128, **bf), lse=torch.zeros(2, 3, 8))
+    for name, bad in (("q", layer["q"][:, :2]), ("q", layer["q"].float()), ("q", layer["q"].transpose(1, 2)),
+                      ("k_new", layer["k_new"][:1]), ("v_new", layer["q"]), ("k_cache", layer["k_cache"][:, :999]),
+                      ("v_cache", layer["v_cache"].float()), ("out", layer["q"][:1]), ("lse", torch.zeros(2, 3, 7))):
+        with pytest.raises(ValueError, match=name):
+            s.decode(**{**layer, name: bad})
+    step = dict(k_cache=layer["k_cache"], v_cache=layer["v_cache"], path=i, n_path=i[:, 0].contiguous())
+    for name, bad in (("k_cache", layer["k_cache"][:1]), ("v_cache", layer["v_cache"][:, 1:]), ("path", i[:, :2]), ("n_path", i)):
+        with pytest.raises(ValueError, match=name):
+            s.commit(**{**step, name: bad})
