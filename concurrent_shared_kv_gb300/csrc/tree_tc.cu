@@ -236,6 +236,8 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // The CTA's units, span by span.
 struct Walk {
   const TreeArgs &a;
@@ -251,7 +253,7 @@ struct Walk {
     begin();
   }
   __device__ __forceinline__ void begin() {
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(tree_at<TreeSpan>(a, a.L.spans) + g.span0 + span + 1));
+    prefetch_l1(tree_at<TreeSpan>(a, a.L.spans) + g.span0 + span + 1);
     tiles = min((sp.len + kT - 1) / kT - tile, left);
   }
   // On to the next span: 0 at the end, 1 in the same group, 2 in another one.
@@ -286,6 +288,14 @@ __device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *
       asm volatile("griddepcontrol.wait;" ::: "memory");
       asm volatile("fence.proxy.async;" ::: "memory");
       waited = true;
+    }
+    // what the softmax warps look up first when they get to this span (a trip
+    // to L2 there holds up everything)
+    if (w.sp.row < 0) {
+      prefetch_l1(tree_at<int16_t>(a, a.L.map) + w.sp.map);
+    } else {
+      const uint2 *mask = tree_at<uint2>(a, a.L.mask) + 2 * static_cast<int64_t>(w.sp.row) * a.max_nodes;
+      for (int i = 0; i < w.sp.len; i += 8) prefetch_l1(mask + 2 * i);
     }
     for (int t = w.tile; go && t < w.tile + w.tiles; ++t) {
       const int row = w.sp.start + t * kT;
