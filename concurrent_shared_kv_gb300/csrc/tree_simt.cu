@@ -16,6 +16,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 64;
 constexpr int kCols = 32;
+constexpr int kPerWarp = kCols / (kThreads / 32);  // queries of a warp
 
 template <int D>
 struct Smem {
@@ -28,6 +29,25 @@ struct Smem {
   int32_t rot[kCols];     // row of the rotation table for this span, or -1: unseen
   uint32_t bad[2];        // a partial tile's tokens with a value that is not finite
 };
+
+// The scores of N queries (warp, warp + 8, ..) against tokens lane and
+// lane + 32, before scaling.  A key's four elements are loaded once for all N.
+template <int D, int N>
+__device__ __forceinline__ void scores(const Smem<D> &S, int warp, int lane, float (&s)[kPerWarp][2]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i][0] = s[i][1] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    const float4 k0 = *reinterpret_cast<const float4 *>(&S.k[lane][d]);
+    const float4 k1 = *reinterpret_cast<const float4 *>(&S.k[lane + 32][d]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 q = *reinterpret_cast<const float4 *>(&S.q[warp + i * (kThreads / 32)][d]);
+      s[i][0] += q.x * k0.x + q.y * k0.y + q.z * k0.z + q.w * k0.w;
+      s[i][1] += q.x * k1.x + q.y * k1.y + q.z * k1.z + q.w * k1.w;
+    }
+  }
+}
 
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4 &u, float *x);
@@ -129,22 +149,24 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
               }
           }
 #pragma unroll
-          for (int i = 0; i < EPV; ++i) {
-            S.k[row][col + i] = kf[i];
-            S.v[row][col + i] = vf[i];
+          for (int i = 0; i < EPV; i += 4) {
+            *reinterpret_cast<float4 *>(&S.k[row][col + i]) = make_float4(kf[i], kf[i + 1], kf[i + 2], kf[i + 3]);
+            *reinterpret_cast<float4 *>(&S.v[row][col + i]) = make_float4(vf[i], vf[i + 1], vf[i + 2], vf[i + 3]);
           }
         }
         __syncthreads();
-        for (int qq = warp; qq < nq; qq += kThreads / 32) {
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll 8
-          for (int d = 0; d < D; d += 4) {
-            const float4 qv = *reinterpret_cast<const float4 *>(&S.q[qq][d]);
-            const float4 k0 = *reinterpret_cast<const float4 *>(&S.k[lane][d]);
-            const float4 k1 = *reinterpret_cast<const float4 *>(&S.k[lane + 32][d]);
-            s0 += qv.x * k0.x + qv.y * k0.y + qv.z * k0.z + qv.w * k0.w;
-            s1 += qv.x * k1.x + qv.y * k1.y + qv.z * k1.z + qv.w * k1.w;
-          }
+        float score[kPerWarp][2];
+        switch ((nq - warp + kThreads / 32 - 1) / (kThreads / 32)) {  // this warp's queries
+          case 4: scores<D, 4>(S, warp, lane, score); break;
+          case 3: scores<D, 3>(S, warp, lane, score); break;
+          case 2: scores<D, 2>(S, warp, lane, score); break;
+          default: scores<D, 1>(S, warp, lane, score); break;
+        }
+#pragma unroll
+        for (int i = 0; i < kPerWarp; ++i) {
+          const int qq = warp + i * (kThreads / 32);
+          if (qq >= nq) break;
+          float s0 = score[i][0], s1 = score[i][1];
           const bool seen = S.rot[qq] >= 0;
           bool in0 = seen && lane < valid, in1 = seen && lane + 32 < valid;
           if (sp.row >= 0) {  // a tree: the node's ancestors and itself
