@@ -858,7 +858,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   const bool tc = tree_on_tensor_cores(d.dtype, d.head_dim);
   L.cols = tc ? 256 : 32;
   L.tile = tc ? 128 : 64;
-  L.ctas_max = tc ? sms : 2 * sms;
+  L.ctas_max = tc ? sms : (d.head_dim == 64 ? 3 : 2) * sms;  // what fits an SM at once
   if (L.ctas_max > 1000) L.ctas_max = 1000;  // (one thread of the plan each)
   const int64_t R = d.n_rows, V = d.max_view_blocks, G = d.n_q_heads / d.n_kv_heads;
   const int64_t Q = R * max_nodes;  // nodes
