@@ -6,6 +6,12 @@
 // memory, rotated anew for every span, tiles of 64 tokens, an online softmax
 // in the log2 domain, and a record of (m, l, o) per column at the end.  A
 // tree's tile is masked with the ancestor bits of each column's node.
+// Bound by shared memory: 12 wavefronts of loads for 8 clocks of FMAs in the
+// scores (a warp's 4 queries share a key's load; a query at a time it was 36),
+// 20 for 16 in P.V, and by tiles loaded without anything under way beside them
+// but the SM's other CTAs.  4 trees of 16 nodes over 16K tokens (40/8 heads):
+// bf16 with head_dim 64 0.51 ms, fp32 with 128 1.26 ms, 18 TFLOP/s; 2 trees of
+// 6 nodes over 256 fp32 tokens (4/2 heads) 13.5 us, all latency.
 #include "hw_device.cuh"
 #include "hw_tree.h"
 

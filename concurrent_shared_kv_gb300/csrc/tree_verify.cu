@@ -24,6 +24,10 @@
 // the slices' sums are joined through distributed shared memory.  Everything
 // else needs single values: every drafted token's p and q are fetched at
 // once, so a path of any depth waits for memory once.
+// Bound by latency: a launch, a cluster barrier a rejection, two trips to
+// memory.  4 rows of 16 nodes over 131072 fp32 values 11 us (0.6 us of bytes),
+// 64 rows of 8 nodes in bf16 22 us (5 us: two waves of clusters), 64 chosen
+// nodes over 50021 values 9 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
