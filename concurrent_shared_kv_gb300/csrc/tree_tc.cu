@@ -29,11 +29,12 @@
 // stream 1, 16 the TMA producer, 17 and 18 the issuers.
 // Rotated queries carry scale * log2(e), so scores leave the MMA in log2
 // units; they are rounded to bf16 once, as models round theirs, and P is too.
-// Relative to the exact result (2-norm) outputs are 0.0032 off, of which the
-// output's own rounding is 0.0015.  (Queries as two bf16 parts give 0.0019, but
-// QK twice over and three ring stages instead of five: 4 trees of 16 nodes over
-// 16K tokens took 47 us instead of 39.5, of 64 nodes 114 instead of 93, a
-// ragged batch of 8 x 4 trees of 8 nodes 174 instead of 157.)
+// For keys and queries of unit variance each of the three roundings (queries,
+// P, output) leaves 0.0016 of the exact result in the 2-norm; outputs are
+// measured 0.003 to 0.004 off.  (Queries as two bf16 parts remove one of the
+// three, at QK twice over and three ring stages instead of five: 4 trees of 16
+// nodes over 16K tokens took 47 us instead of 39.5, of 64 nodes 114 instead of
+// 93, a ragged batch of 8 x 4 trees of 8 nodes 174 instead of 157.)
 //
 // E4M3 caches: both products run as kind::f8f6f4 on the codes, at twice the
 // rate, with Q~ and P each as two E4M3 parts x = hi + lo, lo the rounded
