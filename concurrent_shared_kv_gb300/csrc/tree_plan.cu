@@ -620,15 +620,17 @@ __global__ void __launch_bounds__(256) tree_append_kernel(const __grid_constant_
 // dimension: a warp has 8 elements of it, which lie side by side in a record
 // (a load is 32 sectors of 8 lines; with a query a warp it was 16 lines for
 // half as much: 17 us instead of 14.5 for two chains of 4 nodes, 57 instead of
-// 51 for 4 trees of 16).  Two warps share the records of every 8 elements and join at
-// the end, so that up to 16 records cost one trip to memory.
-template <int D>
+// 51 for 4 trees of 16).  Two to eight warps share the records of every 8
+// elements and join at the end, so that up to 16 (64) records cost one trip to
+// memory.
+template <int D, int kShares>
 struct MergeShape {
   static constexpr int kChunks = D / 32;               // of 8 elements, in a quarter
-  static constexpr int kThreads = kChunks * 2 * 32;
+  static constexpr int kThreads = kChunks * kShares * 32;
 };
 
-// Up to 8 records from j on in steps of 2, joined to (M, L, acc).
+// Up to 8 records from j on in steps of kShares, joined to (M, L, acc).
+template <int kShares>
 __device__ __forceinline__ void merge_batch(const float2 *ml, const float *o, int n_cols, int64_t step, int j, int n,
                                             float &M, float &L, float (&acc)[8]) {
   constexpr int N = 8;
@@ -638,7 +640,7 @@ __device__ __forceinline__ void merge_batch(const float2 *ml, const float *o, in
   // what a record without tiles (m = -inf) holds is dropped
 #pragma unroll
   for (int b = 0; b < N; ++b) {
-    const int64_t at = min(j + 2 * b, n - 1);
+    const int64_t at = min(j + kShares * b, n - 1);
     x[b] = ml[at * n_cols];
     const float4 *src = reinterpret_cast<const float4 *>(o + at * step);
     v[b][0] = src[0];
@@ -647,7 +649,7 @@ __device__ __forceinline__ void merge_batch(const float2 *ml, const float *o, in
   float top = M;
 #pragma unroll
   for (int b = 0; b < N; ++b) {
-    if (j + 2 * b >= n) x[b].x = -INFINITY;
+    if (j + kShares * b >= n) x[b].x = -INFINITY;
     top = fmaxf(top, x[b].x);
   }
   const float old = M == -INFINITY ? 0.f : ex2(M - top);
@@ -666,14 +668,14 @@ __device__ __forceinline__ void merge_batch(const float2 *ml, const float *o, in
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(MergeShape<D>::kThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int kChunks = MergeShape<D>::kChunks, kRow = kChunks * 8;  // elements of a row here
+template <typename T, int D, int kShares>
+__global__ void __launch_bounds__(MergeShape<D, kShares>::kThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kChunks = MergeShape<D, kShares>::kChunks, kRow = kChunks * 8;  // elements of a row here
   constexpr int kPiece = 16 / sizeof(T);                               // elements of a 16-byte store
-  __shared__ float part[kChunks][8][32], part_m[kChunks][32], part_l[kChunks][32];
+  __shared__ float part[kShares][kChunks][8][32], part_m[kShares][kChunks][32], part_l[kShares][kChunks][32];
   __shared__ __align__(16) T tile[32][kRow];
   __shared__ int32_t out_row[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunk = warp >> 1, share = warp & 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunk = warp / kShares, share = warp % kShares;
   const int quarter = blockIdx.x & 3, h = (blockIdx.x >> 2) % a.n_kv_heads, b = (blockIdx.x >> 2) / a.n_kv_heads;
   const int G = a.n_q_heads / a.n_kv_heads;
   // (loads that do not hang on one another first: trips to L2 are what this
@@ -698,27 +700,38 @@ __global__ void __launch_bounds__(MergeShape<D>::kThreads) tree_merge_kernel(con
   const int64_t step = static_cast<int64_t>(g.n_cols) * D;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the records
   float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int j = share; j < n; j += 16) merge_batch(ml, o, g.n_cols, step, j, n, M, L, acc);
-  if (share == 1) {
+  for (int j = share; j < n; j += 8 * kShares) merge_batch<kShares>(ml, o, g.n_cols, step, j, n, M, L, acc);
+  if (share > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[chunk][e][lane] = acc[e];
-    part_m[chunk][lane] = M;
-    part_l[chunk][lane] = L;
+    for (int e = 0; e < 8; ++e) part[share][chunk][e][lane] = acc[e];
+    part_m[share][chunk][lane] = M;
+    part_l[share][chunk][lane] = L;
   }
   if (tid < 32) out_row[lane] = on ? tc.node * a.n_q_heads + hq : -1;
   __syncthreads();
   if (share == 0) {
-    const float M1 = part_m[chunk][lane], top = fmaxf(M, M1);
-    const float w0 = M == -INFINITY ? 0.f : ex2(M - top), w1 = M1 == -INFINITY ? 0.f : ex2(M1 - top);
-    L = L * w0 + part_l[chunk][lane] * w1;
+    float top = M;
+#pragma unroll
+    for (int x = 1; x < kShares; ++x) top = fmaxf(top, part_m[x][chunk][lane]);
+    const float w0 = M == -INFINITY ? 0.f : ex2(M - top);
+    L *= w0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= w0;
+#pragma unroll
+    for (int x = 1; x < kShares; ++x) {
+      const float m = part_m[x][chunk][lane], w = m == -INFINITY ? 0.f : ex2(m - top);
+      L = fmaf(part_l[x][chunk][lane], w, L);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(part[x][chunk][e][lane], w, acc[e]);
+    }
     const float inv = 1.f / L;  // (a node attends itself; NaN where its values are)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile[lane][chunk * 8 + e] = from_f32<T>((acc[e] * w0 + part[chunk][e][lane] * w1) * inv);
+    for (int e = 0; e < 8; ++e) tile[lane][chunk * 8 + e] = from_f32<T>(acc[e] * inv);
     if (a.lse && warp == 0 && quarter == 0 && on)
       a.lse[tc.node * a.n_q_heads + hq] = (top + log2f(L)) * 0.693147180559945309f;
   }
   __syncthreads();
-  for (int x = tid; x < 32 * kRow / kPiece; x += MergeShape<D>::kThreads) {
+  for (int x = tid; x < 32 * kRow / kPiece; x += MergeShape<D, kShares>::kThreads) {
     const int r = x / (kRow / kPiece), e = x % (kRow / kPiece) * kPiece;
     if (out_row[r] < 0) continue;
     T res[kPiece];
@@ -841,14 +854,23 @@ cudaError_t launch_tree_append(const TreeArgs &a, cudaStream_t s) {
   return launch_dependent(tree_append_kernel<__nv_bfloat16, false>, grid, 256, s, a);
 }
 
-cudaError_t launch_tree_merge(const TreeArgs &a, cudaStream_t s) {
+template <typename T, int D>
+static cudaError_t launch_merge(const TreeArgs &a, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(4 * a.n_kv_heads * a.L.max_blocks);
+  // Few columns have many records each and leave most of the GPU idle: CTAs of
+  // 512 threads then, whose warps share them (a layer of one tree of 2 nodes
+  // over 38466 tokens, 4/2 heads: 31.2 -> 24.6 us, with head_dim 64 45 -> 32;
+  // a chain of 4 over 16384, 40/8 heads: 24.8 -> 22.3).  Where the columns fill
+  // the GPU two warps are enough (4 trees of 16 nodes: 38.4 us, with four 44.4).
+  constexpr int kMost = 512 / D;  // a CTA of 512 threads
+  return grid <= 2u * device_sm_count()
+             ? launch_dependent(tree_merge_kernel<T, D, kMost>, grid, MergeShape<D, kMost>::kThreads, s, a)
+             : launch_dependent(tree_merge_kernel<T, D, 2>, grid, MergeShape<D, 2>::kThreads, s, a);
+}
+cudaError_t launch_tree_merge(const TreeArgs &a, cudaStream_t s) {
   const bool d64 = a.head_dim == 64;
-  const int threads = d64 ? MergeShape<64>::kThreads : MergeShape<128>::kThreads;
-  if (a.dtype == HW_F32)
-    return launch_dependent(d64 ? tree_merge_kernel<float, 64> : tree_merge_kernel<float, 128>, grid, threads, s, a);
-  return launch_dependent(d64 ? tree_merge_kernel<__nv_bfloat16, 64> : tree_merge_kernel<__nv_bfloat16, 128>, grid,
-                          threads, s, a);
+  if (a.dtype == HW_F32) return d64 ? launch_merge<float, 64>(a, s) : launch_merge<float, 128>(a, s);
+  return d64 ? launch_merge<__nv_bfloat16, 64>(a, s) : launch_merge<__nv_bfloat16, 128>(a, s);
 }
 
 cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaStream_t s) {
