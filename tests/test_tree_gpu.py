@@ -862,3 +862,25 @@ def test_sessions_that_share_a_pool_and_a_stream():
     b.check(s=sb)
     a.check(s=sa)
     b.check(s=sb)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp8", 128), ("f32", 64)])
+def test_the_largest_description(dtype, d):
+    """HW_MAX_VIEW_ENTRIES rows and HW_MAX_TREE_QUERIES nodes, HW_MAX_BLOCKS blocks."""
+    R, B = 4096, 256
+    rng = np.random.Generator(np.random.PCG64(72))
+    own = np.arange(R) % B
+    Tree(dtype, hq=1, hkv=1, d=d, lens=[int(x) for x in rng.integers(0, 40, B)], views=(own[:, None], np.zeros((R, 1)), rng.integers(0, 99, R)),
+         tree_block=own, n_nodes=rng.integers(0, 17, R), T=16, seed=72).check()
+
+
+def test_the_longest_verification():
+    # HW_MAX_VOCAB values, bf16: a row's slices fit no shared memory
+    V = 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(3)
+    p = torch.rand(1, 2, V, generator=g, device="cuda").pow(40).bfloat16()
+    p = (p.float() / p.float().sum(-1, keepdim=True)).bfloat16()
+    token = p[0, 0].float().topk(2).indices.int()
+    x = dict(n_nodes=np.array([2]), parent=np.array([[-1, 0]]), token=token.cpu().numpy()[None].astype(np.int32), p=p.cpu(), q=None,
+             u_accept=np.full((1, 2), 0.999, np.float32), u_sample=np.array([0.37], np.float32))
+    check_verify(x)
