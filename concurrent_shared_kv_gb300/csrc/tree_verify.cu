@@ -587,8 +587,9 @@ cudaError_t launch(TreeVerifyArgs a, cudaStream_t s) {
 template <typename T>
 cudaError_t launch(const TreeVerifyArgs &a, cudaStream_t s) {
   // Sixteen CTAs a row while all rows' run at once, two on an SM (4 rows of
-  // 131072 fp32: 12.3 us, with eight 13.4), else eight (64 rows in bf16: 25.7
-  // us in two waves, with four 28.0 in one).
+  // 131072 fp32: 11.0 us, with eight a tenth more), else eight (64 rows in
+  // bf16: 22.8 us in two waves; with four 28.0 in one, and with CTAs of 256
+  // threads, sixteen a row and all rows at once, 24.3).
   return a.n_rows * 16 <= 2 * device_sm_count() ? launch<T, 16>(a, s) : launch<T, 8>(a, s);
 }
 }  // namespace
