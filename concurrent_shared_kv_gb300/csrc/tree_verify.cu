@@ -293,6 +293,9 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
   __shared__ Smem S;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
+  // Shared memory of another CTA may be touched only once that CTA is known to
+  // run: arrive here, wait behind the loads of the single values, which hide it.
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const int r = blockIdx.x / kCluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int TN = a.max_nodes, V = a.vocab, n = a.n_nodes[r];
   const T *p0 = static_cast<const T *>(a.p) + static_cast<int64_t>(r) * TN * a.p_stride;
@@ -321,6 +324,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
   }
   if (tid < kMaxNodes) S.parent[tid] = tid < n ? par : -2;
   __syncthreads();
+  asm volatile("barrier.cluster.wait;" ::: "memory");
   if (S.bad || n == 0) {  // (the same in every CTA of the cluster)
     if (rank == 0) {
       for (int j = tid; j < TN; j += kThreads) a.path[static_cast<int64_t>(r) * TN + j] = -1;

@@ -884,3 +884,25 @@ def test_the_longest_verification():
     x = dict(n_nodes=np.array([2]), parent=np.array([[-1, 0]]), token=token.cpu().numpy()[None].astype(np.int32), p=p.cpu(), q=None,
              u_accept=np.full((1, 2), 0.999, np.float32), u_sample=np.array([0.37], np.float32))
     check_verify(x)
+
+
+# ------------------------------------------------------- many clusters at once
+
+@pytest.mark.parametrize("dtype,V", [("f32", 2003), ("bf16", 40_001), ("f32", 300_000)])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_more_rows_than_run_at_once(dtype, V, drawn):
+    """Clusters that start as others end, rows that leave at once between those
+    that exchange sums, slices that leave room for one CTA an SM (the longest
+    vocabulary, nine rows: sixteen CTAs each): every row as by itself."""
+    R = 9 if V == 300_000 else 250
+    rng = np.random.Generator(np.random.PCG64(V))
+    n = rng.integers(-1, 6, R) if R > 9 else np.array([4, 0, 3, 5, 4, 2, 1, 4, 3])  # (-1 and 5 are refused)
+    x = draw_verify(rng, R, 4, V if R == 9 else 64, dtype, drawn, n_nodes=n)
+    if R > 9:  # the values spread over the vocabulary: p and q of 64 tokens, 0 elsewhere
+        at = np.sort(rng.choice(V, 64, replace=False))
+        wide = {k: torch.zeros(R, 4, V, dtype=x[k].dtype) for k in ("p", "q") if x[k] is not None}
+        for k, t in wide.items():
+            t[..., torch.as_tensor(at)] = x[k]
+        x.update(wide, token=at[x["token"]].astype(np.int32))
+    for _ in range(3):
+        check_verify(x)
