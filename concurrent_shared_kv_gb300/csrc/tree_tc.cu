@@ -11,8 +11,8 @@
 //
 // The CTA runs two streams, each with its own S/P, O, issuing warp and eight
 // softmax warps: with over 128 columns stream q is query tile q and both take
-// every K/V tile; with up to 128 there is one query tile and stream q takes
-// every other K/V tile (two records, like two CTAs).  One stream's products
+// every K/V tile; with up to 128 there is one query tile and the streams take
+// the K/V tiles by turns (two records, like two CTAs).  One stream's products
 // run under the other's softmax; within a stream QK, softmax and PV follow one
 // another (S and P share their columns: TMEM holds no third score tile), so
 // what counts is the length of that chain.  Two threads share a row, 64 tokens
@@ -405,26 +405,29 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
     return true;
   };
   // The span's queries; one query tile is written by all softmax warps.
+  // (This stream's first: once they are there the other issuer has seen the
+  // other stream's of the span before.)
   auto queries = [&](bool two) -> bool {
-    return ((two && q == 1) || warp_wait(S, a, &S.q_full[0], nspan & 1)) &&
-           ((two && q == 0) || warp_wait(S, a, &S.q_full[1], nspan & 1));
+    return warp_wait(S, a, &S.q_full[q], nspan & 1) && (two || warp_wait(S, a, &S.q_full[q ^ 1], nspan & 1));
   };
   RingPos k = {0, 0};   // the next tile's K
   int step = 2;         // 2: a group starts
-  int turn = 0;         // the next tile's stream, where streams take turns
-  int turns = 0;        // turns at the tensor cores so far, of both streams
+  // Turns at the tensor cores so far, of both streams.  They alternate over the
+  // whole of the CTA's work, stream 0 the even ones: whoever waits for the turn
+  // before its own has made the one before that, so a bit tells them apart.
+  int turns = 0;
   bool go = true;
   do {
     const bool two = w.g.n_cols > 128;
     if (step == 2) {  // the softmax warps wait for a group's last products
       if (pend && !(go = flush())) break;
-      turn = 0;
       first = true;
     }
     bool turned = false;  // this span's queries are there
-    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turn ^= 1, turns += two ? 2 : 1) {
-      if (!two && turn != q) continue;
-      const int s = k.s, mine = turns + (two ? q : 0);
+    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turns += two ? 2 : 1) {
+      const bool later = (turns ^ q) & 1;  // the other stream's turn is before this one's
+      if (!two && later) continue;
+      const int s = k.s, mine = turns + later;
       if (!(go = warp_wait(S, a, &S.kv_full[s], k.phase))) break;
       // (a new span's queries come after the last P, so their wait is last)
       // One stream's PV and QK go out together, the streams in turn: mixed,
@@ -626,7 +629,8 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     __syncwarp();
     if (some && lane == 0) mbar_arrive(&S.o_empty[q]);
   };
-  int step = 2, turn = 0;
+  int step = 2;
+  int turn = 0;  // the stream of the next tile that is one stream's (the issuers' turns)
   do {
     const bool two = w.g.n_cols > 128;
     const int col = two ? q * 128 + row : row;               // the thread's column of the group
@@ -679,10 +683,9 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
       const int nth = static_cast<int>(blockIdx.x) - tree_at<int2>(a, a.L.piece_cta)[p].x;
       rec = tree_at<int32_t>(a, a.L.piece_row)[p] + static_cast<int64_t>(two ? nth : w.streams * nth + q) * rec_cols;
       some = false;
-      turn = 0;
     }
     ++nspan;
-    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turn ^= 1) {
+    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turn ^= !two) {
       const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
       const int owner = two ? 0 : turn;  // who tidies the V tile, where that is needed
       const bool tidy = w.sp.partial || (valid & (kStep - 1));

@@ -906,3 +906,27 @@ def test_verify_more_rows_than_run_at_once(dtype, V, drawn):
         x.update(wide, token=at[x["token"]].astype(np.int32))
     for _ in range(3):
         check_verify(x)
+
+
+# ------------------------------------------- turns of the two streams of a CTA
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("T", [4, 50])
+@pytest.mark.parametrize("seed", [80, 81, 82])
+def test_groups_of_odd_numbers_of_tiles(dtype, T, seed):
+    """Many groups behind one another in a CTA, of one to some tiles each, so
+    that groups end with either stream; of up to 128 queries and of more in
+    turn.  Repeated runs give the same bits."""
+    rng = np.random.Generator(np.random.PCG64(seed))
+    R = 48
+    # every row's own block alone: a group a row; 8 queries a node, so 50 nodes fill more than one query tile
+    lens = [int(x) for x in rng.choice([1, 100, 128, 129, 300, 384, 500, 640, 1100], R)]
+    n = rng.integers(1, T + 1, R)
+    t = Tree(dtype, hq=32, hkv=4, lens=lens, views=([[b] for b in range(R)], [[0]] * R, lens), tree_block=np.arange(R), T=T,
+             n_nodes=n, seed=seed)
+    s, out, lse = t.check(what="odd")
+    live = torch.as_tensor(np.arange(T)[None] < n[:, None]).cuda()
+    for _ in range(20):
+        o2, l2 = t.run(s)
+        assert torch.equal(bits(o2[live]), bits(out[live])) and torch.equal(l2[live], lse[live])
+    assert s.device_flags() == 0
