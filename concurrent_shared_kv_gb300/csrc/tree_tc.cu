@@ -75,8 +75,11 @@ struct Ring {
   static constexpr int kMore = kQTile / kStage;
   static constexpr int kStep = kFp8 ? 32 : 16;  // tokens of one MMA
   // A wait for a stage's next tile can be told from its last one only if that
-  // has landed.  Five stages back is a V whose products this stream issued, or
-  // the other one in a turn before; three back it may still be under way.
+  // has landed.  Five stages before the K of tile t is the V of tile t - 3: its
+  // turn at least three before tile t's.  A stream that has waited for turn
+  // m - 1 of the other one knows that the V tiles of that one's turns up to
+  // m - 3 have landed, and those of its own up to m - 4.  Three stages back a V
+  // may still be under way.
   static_assert(kStages >= 5, "the barriers' phases");
 };
 // A place in a ring of n stages.
@@ -428,12 +431,13 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
       const bool later = (turns ^ q) & 1;  // the other stream's turn is before this one's
       if (!two && later) continue;
       const int s = k.s, mine = turns + later;
-      if (!(go = warp_wait(S, a, &S.kv_full[s], k.phase))) break;
       // (a new span's queries come after the last P, so their wait is last)
       // One stream's PV and QK go out together, the streams in turn: mixed,
       // both would wait for both, and their softmaxes would run at the same
       // time, the tensor cores idle.
       if (mine > 0 && !(go = warp_wait(S, a, &S.order, (mine - 1) & 1))) break;
+      // Not before the turn: it says that the stage's last tile has landed (Ring).
+      if (!(go = warp_wait(S, a, &S.kv_full[s], k.phase))) break;
       if (pend && !(go = pv_first())) break;
       if (!turned && !(go = queries(two))) break;
       turned = true;

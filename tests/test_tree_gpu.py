@@ -930,3 +930,23 @@ def test_groups_of_odd_numbers_of_tiles(dtype, T, seed):
         o2, l2 = t.run(s)
         assert torch.equal(bits(o2[live]), bits(out[live])) and torch.equal(l2[live], lse[live])
     assert s.device_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("seed", [83, 84])
+def test_narrow_groups_in_ctas_with_a_wide_one(dtype, seed):
+    """The short ring of a CTA that has a group of over 128 queries, run
+    through by groups of few queries with many tiles: every stage is used
+    again and again by either stream."""
+    rng = np.random.Generator(np.random.PCG64(seed))
+    R = 12
+    lens = [int(x) for x in rng.choice([20, 2100, 5000, 9001], R)]
+    n = np.where(np.arange(R) % 3 == 0, 40, rng.integers(1, 5, R))
+    t = Tree(dtype, hq=64, hkv=16, lens=lens, views=([[b] for b in range(R)], [[0]] * R, lens), tree_block=np.arange(R), T=40,
+             n_nodes=n, seed=seed)
+    s, out, lse = t.check(what="wide and narrow")
+    live = torch.as_tensor(np.arange(40)[None] < n[:, None]).cuda()
+    for _ in range(20):
+        o2, l2 = t.run(s)
+        assert torch.equal(bits(o2[live]), bits(out[live])) and torch.equal(l2[live], lse[live])
+    assert s.device_flags() == 0
