@@ -942,7 +942,7 @@ def test_narrow_groups_in_ctas_with_a_wide_one(dtype, seed):
     R = 12
     lens = [int(x) for x in rng.choice([20, 2100, 5000, 9001], R)]
     n = np.where(np.arange(R) % 3 == 0, 40, rng.integers(1, 5, R))
-    t = Tree(dtype, hq=64, hkv=16, lens=lens, views=([[b] for b in range(R)], [[0]] * R, lens), tree_block=np.arange(R), T=40,
+    t = Tree(dtype, hq=16, hkv=4, lens=lens, views=([[b] for b in range(R)], [[0]] * R, lens), tree_block=np.arange(R), T=40,
              n_nodes=n, seed=seed)
     s, out, lse = t.check(what="wide and narrow")
     live = torch.as_tensor(np.arange(40)[None] < n[:, None]).cuda()
