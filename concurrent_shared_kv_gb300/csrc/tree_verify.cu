@@ -53,9 +53,12 @@ __device__ __forceinline__ uint64_t to_fix(float x) {
 __device__ __forceinline__ uint64_t mul_fix(uint64_t a, uint64_t b) {
   return (__umul64hi(a, b) << (64 - kShift)) | ((a * b) >> kShift);
 }
-__device__ __forceinline__ uint64_t left_of(uint64_t p, uint64_t c, uint64_t q) {
-  const uint64_t t = mul_fix(c, q);
-  return p > t ? p - t : 0;
+// c, with the same 56 bits behind the point: it grows by a row's sum, up to 128,
+// with each of up to 127 rejections, to 2^14.
+using Wide = unsigned __int128;
+__device__ __forceinline__ uint64_t left_of(uint64_t p, Wide c, uint64_t q) {
+  const Wide t = (c * q) >> kShift;  // (below 2^126)
+  return p > t ? p - static_cast<uint64_t>(t) : 0;
 }
 // Packed fp32: two numbers an instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -111,11 +114,15 @@ __device__ __forceinline__ uint64_t pieces(float x) {
   return k.sum();
 }
 
-// c as two floats: off by at most 2^-49 of it.
-__device__ __forceinline__ void split_c(uint64_t c, float &c0, float &c1) {
-  c0 = __ull2float_rn(c);
-  c1 = __ll2float_rn(static_cast<int64_t>(c - __float2ull_rn(c0))) * 0x1p-56f;
-  c0 *= 0x1p-56f;
+// c as two floats: off by at most 2^-49 of it (from 2^8 on its last 8 bits are
+// dropped first, 2^-56 of it).
+__device__ __forceinline__ void split_c(Wide c, float &c0, float &c1) {
+  const bool large = (c >> 64) != 0;
+  const uint64_t x = static_cast<uint64_t>(large ? c >> 8 : c);
+  const float unit = large ? 0x1p-48f : 0x1p-56f;
+  c0 = __ull2float_rn(x);
+  c1 = __ll2float_rn(static_cast<int64_t>(x - __float2ull_rn(c0))) * unit;
+  c0 *= unit;
 }
 
 // A row of probabilities.  Vector loads start at multiples of four elements
@@ -173,8 +180,10 @@ struct Smem {
   int32_t path[kMaxNodes], gone[kMaxNodes];  // accepted nodes; tokens removed at the current node
   // the walk, written by thread 0
   int32_t cur, next, n_path, n_gone, again;
-  uint64_t c, s;
-  float c0, c1;    // the next pass's c
+  uint64_t s;
+  Wide c, c_pass;  // that of the distribution now, that of the next pass
+  int32_t kind;    // the next pass's c: 0, 1, or another (2)
+  float c0, c1;    // the same as two floats
   int32_t bad;
   int32_t slice;   // the drawn token's warp slice in this CTA, or -1
   uint64_t target;  // what is left of the draw there
@@ -352,14 +361,14 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
   }
   int kept_p = -1, kept_q = -1;  // the nodes whose rows are kept
   int parity = 0;
-  uint64_t c_pass = 0, c_kept = 0;
   bool fresh = false;  // the slices' sums are those of (cur, c)
   for (;;) {
     if (warp == 0) {
       // on to the next rejection that needs a sum, or to the end: the whole
       // warp walks, its lanes looking for a node's next child
       int cur = S.cur, i = S.next, n_path = S.n_path, n_gone = S.n_gone, again = 0;
-      uint64_t c = S.c, s = S.s;
+      Wide c = S.c;
+      uint64_t s = S.s;
       bool moved = false;
       while (!again) {
         int x = kMaxNodes;
@@ -407,21 +416,23 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
         S.c = c;
         S.s = s;
         S.again = again | (moved ? 2 : 0);
+        const Wide pass = again ? c + s : c;
+        S.c_pass = pass;
+        S.kind = pass == 0 ? 0 : pass == kOne ? 1 : 2;
         // (64-bit conversions run at a sixteenth of the rate: one thread's)
-        split_c(again ? c + s : c, S.c0, S.c1);
+        split_c(pass, S.c0, S.c1);
       }
     }
     __syncthreads();
     const int again = S.again;
     if (again & 2) fresh = false;
-    c_kept = S.c;
     if (!(again & 1) && fresh) break;
     // one pass: the slices' sums of max(p - c q, 0)
-    c_pass = again & 1 ? c_kept + S.s : c_kept;
+    const int kind = S.kind;
     const Row<T> p(p0 + S.cur * a.p_stride, V);
     uint64_t sum = 0;
     const int y0 = (rank * kWarps + warp) * per, y1 = min(y0 + per, p.end);
-    if (c_pass == 0) {
+    if (kind == 0) {
       const int from = !a.keep ? 0 : kept_p == S.cur ? 2 : 1;
       sum = slice_sum_from<T, false, false>(from, p, p, kept, 0.f, 0.f, y0, y1, lane);
       if (from == 1) kept_p = S.cur, kept_q = -1;
@@ -429,8 +440,8 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
       const Row<T> q(q0 + S.cur * a.q_stride, V);
       const float c0 = S.c0, c1 = S.c1;
       const int from = !a.keep ? 0 : kept_q == S.cur ? 2 : 1;
-      sum = c_pass == kOne ? slice_sum_from<T, true, true>(from, p, q, kept, c0, c1, y0, y1, lane)
-                           : slice_sum_from<T, false, true>(from, p, q, kept, c0, c1, y0, y1, lane);
+      sum = kind == 1 ? slice_sum_from<T, true, true>(from, p, q, kept, c0, c1, y0, y1, lane)
+                      : slice_sum_from<T, false, true>(from, p, q, kept, c0, c1, y0, y1, lane);
       if (from == 1) kept_p = kept_q = S.cur;
     }
 #pragma unroll
@@ -460,7 +471,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
       fresh = t > 0;  // nothing left: the distribution before the rejection stays
       __syncthreads();
       if (tid == 0 && t > 0) {
-        S.c = c_pass;
+        S.c = S.c_pass;
         S.s = t;
       }
     } else {
@@ -502,8 +513,8 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
   // the owner goes over the slice once more, four positions a thread
   const Row<T> p(p0 + S.cur * a.p_stride, V);
   const int y0 = (rank * kWarps + S.slice) * per, y1 = min(y0 + per, p.end);
-  const uint64_t c = S.c;
-  const float c0 = S.c0, c1 = S.c1;  // (the last pass's c is the one that stays)
+  const int kind = S.kind;  // (the last pass's c is the one that stays)
+  const float c0 = S.c0, c1 = S.c1;
   uint64_t target = S.target;
   for (int yb = y0; yb < y1; yb += 4 * kThreads) {
     const int y = yb + 4 * tid;
@@ -512,13 +523,13 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
       float x[4], z[4] = {0.f, 0.f, 0.f, 0.f};
       if (kept_p == S.cur) four(kept.p + (y - kept.y0), x);
       else load_p(p, y, x);
-      if (c != 0) {
+      if (kind != 0) {
         const Row<T> q(q0 + S.cur * a.q_stride, V);
         if (kept_q == S.cur) four(kept.q + (y - kept.y0), z);
         else load_q(p, q, y, z);
       }
-      if (c == 0) left4<true, false>(x, z, c0, c1);
-      else if (c == kOne) left4<true, true>(x, z, c0, c1);
+      if (kind == 0) left4<true, false>(x, z, c0, c1);
+      else if (kind == 1) left4<true, true>(x, z, c0, c1);
       else left4<false, true>(x, z, c0, c1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = pieces(x[e]);

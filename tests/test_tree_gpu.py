@@ -950,3 +950,27 @@ def test_narrow_groups_in_ctas_with_a_wide_one(dtype, seed):
         o2, l2 = t.run(s)
         assert torch.equal(bits(o2[live]), bits(out[live])) and torch.equal(l2[live], lse[live])
     assert s.device_flags() == 0
+
+
+@pytest.mark.parametrize("mass", [3.0, 64.0, 120.0, 127.5, 128.0])
+def test_verify_rows_whose_sum_is_not_one(mass):
+    """A row of p may sum to 128: c grows by up to that much a rejection."""
+    rng = np.random.Generator(np.random.PCG64(int(2 * mass)))
+    R, T, V = 64, 128, 300
+    p = np.zeros((R, T, V), np.float32)
+    q = np.zeros((R, T, V), np.float32)
+    p[:, 0, :128] = np.float32(mass / 128)
+    # tokens 200 .. 249 cannot stand; a few others can while c q is below p
+    q[:, 0, 200:250] = np.float32(0.01)
+    some = rng.integers(0, 128, (R, 8))
+    for r in range(R):
+        q[r, 0, some[r]] = np.float32(2.0) ** -rng.integers(7, 16, 8) * rng.random(8, dtype=np.float32)
+    p[:, 1:, 5] = 1
+    q[:, 1:, 6] = 1
+    token = rng.integers(200, 250, (R, T)).astype(np.int32)
+    late = rng.integers(2, 10, R)          # rejections before the first that could stand
+    for r in range(R):
+        token[r, late[r]::3] = rng.choice(some[r], len(token[r, late[r]::3]))
+    x = dict(n_nodes=rng.integers(2, T + 1, R), parent=np.tile(np.r_[-1, np.zeros(T - 1)], (R, 1)).astype(np.int32), token=token,
+             p=torch.tensor(p), q=torch.tensor(q), u_accept=rng.random((R, T), dtype=np.float32), u_sample=rng.random(R, dtype=np.float32))
+    check_verify(x)
