@@ -13,11 +13,11 @@
 // Arithmetic: what is decided is decided in integers, with 56 bits behind the
 // point.  The single values of a test are exact (a probability from 2^-32 up)
 // or lose less than 2^-56; an element of a sum is p - c q in fp32 with c as two
-// floats - an error of 2^-24 of the difference itself - rounded to 43 bits
+// floats - an error of 2^-24 of the difference itself - rounded to 56 bits
 // behind the point and added as an integer.  Sums so do not depend on their
-// order, runs repeat, and a running sum over a vocabulary of 2^17 is off by
-// some 1e-10, where fp32 sums would misplace the drawn token once in a
-// thousand draws.
+// order, runs repeat, and a running sum is off by some 2^-24 of its largest
+// elements, where fp32 sums would misplace the drawn token once in a thousand
+// draws.
 //
 // One cluster of 8 or 16 CTAs a row: the vocabulary is cut into one slice a warp,
 // a rejection costs one pass over the node's two rows of probabilities, and
@@ -87,25 +87,32 @@ __device__ __forceinline__ void left2(float &p0, float &p1, float c0, float c1, 
   p0 = fmaxf(p0, 0.f);
   p1 = fmaxf(p1, 0.f);
 }
-// Numbers in [0, 1] as k0 2^-20 + k1 2^-43, both rounded to nearest: adding a
-// constant leaves the integer in the last bits of the sum.
+// Numbers in [0, 1] as k0 2^-20 + k1 2^-43 + k2 2^-56, each rounded to nearest:
+// adding a constant leaves the integer in the last bits of the sum.  (Two pieces
+// would count what is below 2^-44 as nothing: a long vocabulary beside one token
+// that was all but certain.)
 struct Pieces {
-  uint32_t k0 = 0, k1 = 0;
+  uint32_t k0 = 0, k1 = 0, k2 = 0;
   __device__ __forceinline__ void add(float x0, float x1) {
     const uint64_t x = pack2(x0, x1);
     const uint64_t a = add2(x, pack2(12.f, 12.f));  // 2^3 .. 2^4: steps of 2^-20
     const uint64_t d = fma2(add2(a, pack2(-12.f, -12.f)), pack2(-1.f, -1.f), x);  // at most 2^-21, exact
     const uint64_t b = add2(d, pack2(0x1.8p-20f, 0x1.8p-20f));                    // steps of 2^-43
-    float a0, a1, b0, b1;
+    const uint64_t r = fma2(add2(b, pack2(-0x1.8p-20f, -0x1.8p-20f)), pack2(-1.f, -1.f), d);  // at most 2^-44, exact
+    const uint64_t f = add2(r, pack2(0x1.8p-33f, 0x1.8p-33f));                    // steps of 2^-56
+    float a0, a1, b0, b1, f0, f1;
     unpack2(a, a0, a1);
     unpack2(b, b0, b1);
+    unpack2(f, f0, f1);
     k0 += __float_as_uint(a0) + __float_as_uint(a1) - 2 * __float_as_uint(12.f);
     k1 += __float_as_uint(b0) + __float_as_uint(b1) - 2 * __float_as_uint(0x1.8p-20f);
+    k2 += __float_as_uint(f0) + __float_as_uint(f1) - 2 * __float_as_uint(0x1.8p-33f);
   }
-  // 56 bits behind the point (up to 512 numbers: |k1| stays below 2^31)
+  // 56 bits behind the point (up to 512 numbers: |k1| and |k2| stay below 2^31)
   __device__ __forceinline__ uint64_t sum() const {
     return (static_cast<uint64_t>(k0) << (kShift - 20)) +
-           static_cast<uint64_t>(static_cast<int64_t>(static_cast<int32_t>(k1)) << (kShift - 43));
+           static_cast<uint64_t>(static_cast<int64_t>(static_cast<int32_t>(k1)) << (kShift - 43)) +
+           static_cast<uint64_t>(static_cast<int64_t>(static_cast<int32_t>(k2)));
   }
 };
 __device__ __forceinline__ uint64_t pieces(float x) {

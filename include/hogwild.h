@@ -422,9 +422,9 @@ int hw_attn_decode_tree_fp8(const hw_attn_desc *d, int32_t max_nodes, const void
  *  path        dev int32 [n_rows][max_nodes]: 0, then the accepted nodes, then -1
  *  n_path      dev int32 [n_rows]: their number with the root
  *  next_token  dev int32 [n_rows]
- * Sums and tests are kept in 64-bit fixed point with 56 bits behind the point
- * (smaller values count as 0), so the result does not depend on the order of
- * anything.  A row with n_nodes 0, or whose counts, parents or tokens
+ * Sums and tests are kept in fixed point with 56 bits behind the point (smaller
+ * values count as 0), so the result does not depend on the order of anything;
+ * what is left of a token is rounded to fp32 before it is added to a sum.  A row with n_nodes 0, or whose counts, parents or tokens
  * (of nodes 1 ..) are out of range, gets n_path 0 and next_token -1.
  */
 int hw_tree_verify(int32_t dtype, int32_t n_rows, int32_t max_nodes, int32_t vocab,

@@ -974,3 +974,21 @@ def test_verify_rows_whose_sum_is_not_one(mass):
     x = dict(n_nodes=rng.integers(2, T + 1, R), parent=np.tile(np.r_[-1, np.zeros(T - 1)], (R, 1)).astype(np.int32), token=token,
              p=torch.tensor(p), q=torch.tensor(q), u_accept=rng.random((R, T), dtype=np.float32), u_sample=rng.random(R, dtype=np.float32))
     check_verify(x)
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("V", [1000, 70_000, 1 << 20])
+def test_verify_thin_remainders(drawn, V):
+    """What is left beside one token that was all but certain: multiples of
+    2^-56 up to 2^-46 each, exact in 32 bits, and drawn from."""
+    rng = np.random.Generator(np.random.PCG64(V))
+    R = 3
+    p = np.ldexp(rng.integers(1, 1 << 10, (R, 2, V)).astype(np.float32), -56)
+    q = np.ldexp(rng.integers(0, 1 << 8, (R, 2, V)).astype(np.float32), -56)
+    sure = rng.integers(0, V, R)
+    p[np.arange(R), 0, sure] = np.float32(1 - 2.0 ** -24)
+    q[np.arange(R), 0, sure] = 1
+    token = np.stack([np.zeros(R), sure], 1).astype(np.int32)
+    x = dict(n_nodes=np.full(R, 2), parent=np.tile([-1, 0], (R, 1)).astype(np.int32), token=token, p=torch.tensor(p),
+             q=torch.tensor(q) if drawn else None, u_accept=np.ones((R, 2), np.float32), u_sample=rng.random(R, dtype=np.float32))
+    check_verify(x)
