@@ -57,6 +57,7 @@ struct TreeHeader {
   int32_t streams;   // records that a CTA leaves of a group with up to 128 columns
   int32_t n_col_blocks, pad;  // entries of the merge's table: (group, first column) of 32 columns
   int64_t capacity;
+  double rope_theta;  // of the rotations that the plan holds
 };
 
 struct TreeGroup {
@@ -103,6 +104,7 @@ struct TreeArgs {
   TreeLayout L;
   int32_t n_rows, max_nodes, n_q_heads, n_kv_heads, head_dim, n_blocks, n_view, dtype;
   int64_t capacity;
+  double rope_theta;
   float scale_log2;
   uint64_t phase[64];  // RoPE phase table (hw_internal.h)
 };
@@ -164,7 +166,7 @@ __device__ __forceinline__ bool tree_plan_ok(const TreeArgs &a) {
   return h.magic == kTreeMagic && h.n_rows == a.n_rows && h.max_nodes == a.max_nodes &&
          h.n_q_heads == a.n_q_heads && h.n_kv_heads == a.n_kv_heads && h.head_dim == a.head_dim &&
          h.n_blocks == a.n_blocks && h.n_view == a.n_view && h.dtype == a.dtype &&
-         h.capacity == a.capacity;
+         h.capacity == a.capacity && h.rope_theta == a.rope_theta;
 }
 #endif
 

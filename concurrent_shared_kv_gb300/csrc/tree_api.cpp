@@ -42,6 +42,7 @@ static int tree_args(TreeArgs &a, const hw_attn_desc *d, int32_t max_nodes, void
   a.n_view = d->max_view_blocks;
   a.dtype = d->dtype;
   a.capacity = d->cache_capacity;
+  a.rope_theta = d->rope_theta;
   a.scale_log2 = static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634074);
   rope_phase_table(d->head_dim, d->rope_theta, a.phase);
   return HW_OK;

@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   }
   if (tid == 0)
     hdr = TreeHeader{kTreeMagic, R, T, a.n_q_heads, a.n_kv_heads, a.head_dim, a.n_blocks, V, a.dtype,
-                     n_groups, n_ctas, streams, n_col_blocks, 0, a.capacity};
+                     n_groups, n_ctas, streams, n_col_blocks, 0, a.capacity, a.rope_theta};
 }
 
 // cos and sin of a position's angle for one pair: the angle in turns is exact in 64-bit integers (rope_cos_sin); here

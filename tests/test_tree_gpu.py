@@ -992,3 +992,16 @@ def test_verify_thin_remainders(drawn, V):
     x = dict(n_nodes=np.full(R, 2), parent=np.tile([-1, 0], (R, 1)).astype(np.int32), token=token, p=torch.tensor(p),
              q=torch.tensor(q) if drawn else None, u_accept=np.ones((R, 2), np.float32), u_sample=rng.random(R, dtype=np.float32))
     check_verify(x)
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_a_plan_of_another_rope_theta_is_reported(dtype, d):
+    t = Tree(dtype, d=d, lens=(50, 10), T=3, seed=24)
+    s = t.session()
+    s.desc.rope_theta = 2 * t.theta
+    t.check(rows=[], s=s)
+    assert s.device_flags() == 32
+    s.commit(t.k, t.v, torch.zeros(1, 3, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"))
+    assert s.device_flags() == 32
+    s.desc.rope_theta = t.theta
+    t.check(s=s)
