@@ -93,12 +93,12 @@ __device__ __forceinline__ bool ranges_meet(int64_t a, int64_t na, int64_t b, in
   return na > 0 && nb > 0 && a < b + nb && b < a + na;
 }
 
-// One row, by one warp: its checks, depths and ancestor masks.  Returns its
-// node count (0 if the row is refused).
+// One row, by one warp: its checks but for the other rows' trees (tree_meets),
+// depths and ancestor masks.  Returns its node count (0 if the row is refused).
 __device__ int plan_row(const TreeArgs &a, const TreeMeta &m, TreePlanSmem &S, int32_t *err, int r,
                         int lane) {
-  const int T = a.max_nodes, R = a.n_rows;
-  int n = m.n_nodes[r];
+  const int T = a.max_nodes;
+  const int n = m.n_nodes[r];
   if (n == 0) return 0;
   if (n < 0 || n > T) {
     if (lane == 0) flag_error(err, HW_DEV_BAD_TREE);
@@ -109,13 +109,11 @@ __device__ int plan_row(const TreeArgs &a, const TreeMeta &m, TreePlanSmem &S, i
     if (lane == 0) flag_error(err, HW_DEV_BAD_BLOCK);
     return 0;
   }
-  // the nodes' tokens: inside the pool, outside every block and other tree
+  // the nodes' tokens: inside the pool, outside every block
   const int64_t slot = tree_slot(m, a.n_blocks, r);
   bool bad_range = S.len[b] < 0 || slot < 0 || slot + n > a.capacity;
   for (int x = lane; x < a.n_blocks; x += 32)
     bad_range |= ranges_meet(slot, n, S.start[x], S.len[x]);
-  for (int x = lane; x < R; x += 32)
-    if (x != r) bad_range |= ranges_meet(slot, n, tree_slot(m, a.n_blocks, x), m.n_nodes[x]);
   // parents before their children
   uint8_t *par = S.parent[threadIdx.x >> 5];
   bool bad_tree = false;
@@ -148,6 +146,17 @@ __device__ int plan_row(const TreeArgs &a, const TreeMeta &m, TreePlanSmem &S, i
   }
   __syncwarp();
   return n;
+}
+
+// Whether the row's tree meets that of another row which takes part, as far as
+// plan_row can tell.  By one warp.
+__device__ bool tree_meets(const TreeArgs &a, const TreePlanSmem &S, int r, int lane) {
+  const int32_t *slot = tree_at<int32_t>(a, a.L.slot);
+  bool meets = false;
+  if (S.nodes[r] > 0)
+    for (int x = lane; x < a.n_rows; x += 32)
+      if (x != r && S.nodes[x] > 0) meets |= ranges_meet(slot[r], S.nodes[r], slot[x], S.nodes[x]);
+  return __any_sync(0xffffffffu, meets);
 }
 
 // The CTA that owns a unit starting at weight w.
@@ -342,16 +351,25 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   for (int r = warp; r < R; r += kPlanWarps) {
     int n = plan_row(a, m, S, err, r, lane);
     if (!S.ok) n = 0;  // no usable head map: the plan attends and writes nothing
-    if (lane == 0) {
-      tree_at<int32_t>(a, a.L.n_nodes)[r] = n;
-      S.nodes[r] = static_cast<uint8_t>(n);
-    }
+    if (lane == 0) S.nodes[r] = static_cast<uint8_t>(n);
   }
   for (int e = tid; e < E; e += kPlanThreads) {
     const int b = m.view_block[e];
     const bool bad = b < -1 || b >= a.n_blocks;
     if (bad) flag_error(err, HW_DEV_BAD_BLOCK);
     S.vb[e] = static_cast<int16_t>(bad || b < 0 || S.len[b] <= 0 ? -1 : b);
+  }
+  __syncthreads();
+  // rows whose trees meet are refused together (apart[] holds which, for now)
+  for (int r = warp; r < R; r += kPlanWarps) {
+    const bool meets = tree_meets(a, S, r, lane);
+    if (lane == 0) S.apart[r] = meets;
+    if (meets && lane == 0) flag_error(err, HW_DEV_BAD_RANGE);
+  }
+  __syncthreads();
+  for (int r = tid; r < R; r += kPlanThreads) {
+    if (S.apart[r]) S.nodes[r] = 0;
+    tree_at<int32_t>(a, a.L.n_nodes)[r] = S.nodes[r];
   }
   __syncthreads();
   for (int r = warp; r < R; r += kPlanWarps) {

@@ -1005,3 +1005,34 @@ def test_a_plan_of_another_rope_theta_is_reported(dtype, d):
     assert s.device_flags() == 32
     s.desc.rope_theta = t.theta
     t.check(s=s)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+def test_refused_rows_do_not_take_others_along(dtype, d):
+    base = dict(dtype=dtype, d=d, lens=(100, 20, 30, 40), T=4, seed=25)
+    for what, change, bit in (
+            ("nodes beyond the table", dict(n_nodes=[4, 1000, 4]), 64), ("the most nodes", dict(n_nodes=[4, 2 ** 31 - 1, 4]), 64),
+            ("a bad parent, on another's tokens", dict(parent=[[-1, 0, 1, 2], [-1, 2, 0, 1], [-1, 0, 0, 0]]), 64),
+            ("no block, on another's tokens", dict(tree_block=[1, -1, 3]), 1)):
+        t = Tree(**base)
+        ts = t.tree_start.copy()
+        if "another" in what:
+            ts[1] = ts[2] + 1
+        s, f = flags_of(t, tree_start=ts, **change)
+        assert f == bit, what
+        t.tree_block = np.asarray([1, 2, 3], np.int32)
+        t.n_nodes = np.clip(t.n_nodes, 0, 4)
+        t.parent[1] = [-1, 0, 0, 0]
+        t.check(rows=[0, 2], s=s, what=what)
+    # trees behind their blocks: the first one at token 0, another row without a block
+    t = Tree(in_place=True, **base)
+    t.block_len[1] = 0
+    t.block_start = np.asarray([200, 0, 20, 60], np.int32)
+    t.cap = max(t.cap, 320)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    t.k, t.v = [torch.randn(t.hkv, t.cap, d, generator=g, device="cuda").to(t.k.dtype) for _ in range(2)]
+    t.tree_start = t.block_start[1:] + t.block_len[1:]
+    s, f = flags_of(t, tree_block=[1, -1, 3])
+    assert f == 1
+    t.tree_block = np.asarray([1, 2, 3], np.int32)
+    t.check(rows=[0, 2], s=s)
