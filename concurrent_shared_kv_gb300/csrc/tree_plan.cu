@@ -761,6 +761,13 @@ __global__ void __launch_bounds__(MergeShape<D, kShares>::kThreads) tree_merge_k
 
 // ---------------------------------------------------------------- commit
 
+// The n nodes that a row of `nodes` nodes may keep: ascending node numbers.
+__device__ bool path_ok(const int32_t *path, int n, int nodes) {
+  bool ok = n <= nodes;
+  for (int j = 0, before = -1; ok && j < n; before = path[j++]) ok = path[j] > before && path[j] < nodes;
+  return ok;
+}
+
 // The accepted path of each row moved behind its block, bit for bit:
 //   K[l][h][end + j] = K[l][h][slot + path[j]],  V alike,  j < n_path.
 // (64 layers of 4 rows: 6.6 us, the call's own time on the host; 36 layers of
@@ -805,11 +812,13 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
   for (int x = tid; x < a.n_rows; x += blockDim.x)
     if (x != r && n_nodes[x] > 0 &&
         (ranges_meet(end, n, slot_of[x], n_nodes[x]) ||
-         ranges_meet(end, n, end_of[x], min(max(c.n_path[x], 0), n_nodes[x]))))
+         // (a row whose path is refused has no destination)
+         (ranges_meet(end, n, end_of[x], c.n_path[x]) &&
+          path_ok(c.path + static_cast<int64_t>(x) * a.max_nodes, c.n_path[x], n_nodes[x]))))
       atomicOr(&bad, 2);
   __syncthreads();
   if (bad) {
-    if (tid == 0) flag_error(err, (bad & 1 ? HW_DEV_BAD_TREE : 0) | (bad & 2 ? HW_DEV_BAD_RANGE : 0));
+    if (tid == 0) flag_error(err, bad & 1 ? HW_DEV_BAD_TREE : HW_DEV_BAD_RANGE);
     return;
   }
   const int row_bytes = a.head_dim * c.elem_bytes, per = row_bytes / 16;  // 16-byte pieces a token: 4 .. 32

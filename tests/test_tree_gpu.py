@@ -1036,3 +1036,24 @@ def test_refused_rows_do_not_take_others_along(dtype, d):
     assert f == 1
     t.tree_block = np.asarray([1, 2, 3], np.int32)
     t.check(rows=[0, 2], s=s)
+
+
+def test_commit_of_one_block_by_the_row_that_may():
+    """Two rows of one block: a row whose path is refused has no destination."""
+    for bad, n_bad in (([0, 0, -1, -1], 2), ([1, 4, -1, -1], 2), ([0, 1, 2, 3], 5), ([0, 1, 2, 3], -1), ([-1, -1, -1, -1], 1)):
+        t = Tree("f32", hq=4, hkv=2, lens=(50, 7, 30), T=4, tree_block=[1, 1], seed=32)
+        s = t.session()
+        k, v = t.k.clone(), t.v.clone()
+        s.commit(k, v, ref.dev([[0, 2, 3, -1], bad]), ref.dev([3, n_bad]))
+        assert s.device_flags() == 64, bad
+        end, at = int(t.block_start[1] + t.block_len[1]), int(t.tree_start[0])
+        for got, x in ((k, t.k), (v, t.v)):
+            want = x.clone()
+            want[:, end:end + 3] = want[:, [at, at + 2, at + 3]]
+            assert torch.equal(bits(got), bits(want)), bad
+    # two paths that may both move meet
+    t = Tree("f32", hq=4, hkv=2, lens=(50, 7, 30), T=4, tree_block=[1, 1], seed=32)
+    s = t.session()
+    k = t.k.clone()
+    s.commit(k, t.v.clone(), ref.dev([[0, 2, 3, -1], [0, 1, -1, -1]]), ref.dev([3, 2]))
+    assert s.device_flags() == 2 and torch.equal(bits(k), bits(t.k))
