@@ -210,24 +210,28 @@ class TreeSession:
 
     def set_metadata(self, block_start, block_len, view_block, view_offset, q_pos, q_to_kv=None):
         """Upload the step's views: those of the rows' tokens before their trees."""
-        self.meta = [_int32(x, self.device) for x in (block_start, block_len, view_block, view_offset, q_pos)]
-        self.q_to_kv = None if q_to_kv is None else _int32(q_to_kv, self.device)
+        meta = [_int32(x, self.device) for x in (block_start, block_len, view_block, view_offset, q_pos)]
+        q_to_kv = None if q_to_kv is None else _int32(q_to_kv, self.device)
         d = self.desc
-        for what, x, n in zip(("block_start", "block_len", "view_block", "view_offset", "q_pos"), self.meta,
+        for what, x, n in zip(("block_start", "block_len", "view_block", "view_offset", "q_pos"), meta,
                               (d.n_blocks, d.n_blocks, d.n_rows * d.max_view_blocks, d.n_rows * d.max_view_blocks, d.n_rows)):
             _fits(what, x, n, torch.int32)
-        if self.q_to_kv is not None:
-            _fits("q_to_kv", self.q_to_kv, d.n_q_heads, torch.int32)
+        if q_to_kv is not None:
+            _fits("q_to_kv", q_to_kv, d.n_q_heads, torch.int32)
+        self.meta, self.q_to_kv = meta, q_to_kv
 
     def plan(self, tree_block, n_nodes, parent, tree_start=None, stream=None):
         """hw_attn_plan_tree: the step's trees (tree_start None: behind each row's block)."""
-        self.trees = [_int32(x, self.device) for x in (tree_block, n_nodes, parent)]
-        self.tree_start = None if tree_start is None else _int32(tree_start, self.device)
+        if self.meta is None:
+            raise ValueError("plan() needs the step's views: set_metadata() first")
+        trees = [_int32(x, self.device) for x in (tree_block, n_nodes, parent)]
+        tree_start = None if tree_start is None else _int32(tree_start, self.device)
         R = self.desc.n_rows
-        for what, x, n in zip(("tree_block", "n_nodes", "parent"), self.trees, (R, R, R * self.max_nodes)):
+        for what, x, n in zip(("tree_block", "n_nodes", "parent"), trees, (R, R, R * self.max_nodes)):
             _fits(what, x, n, torch.int32)
-        if self.tree_start is not None:
-            _fits("tree_start", self.tree_start, R, torch.int32)
+        if tree_start is not None:
+            _fits("tree_start", tree_start, R, torch.int32)
+        self.trees, self.tree_start = trees, tree_start
         api.attn_plan_tree(self.desc, self.max_nodes, *self.meta, *self.trees, self.workspace,
                            self.ws_bytes, tree_start=self.tree_start, q_to_kv=self.q_to_kv,
                            stream=stream)

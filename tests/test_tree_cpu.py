@@ -175,3 +175,39 @@ def test_tensors_that_do_not_fit_are_refused():
     for name, bad in (("k_cache", layer["k_cache"][:1]), ("v_cache", layer["v_cache"][:, 1:]), ("path", i[:, :2]), ("n_path", i)):
         with pytest.raises(ValueError, match=name):
             s.commit(**{**step, name: bad})
+
+
+def cpu_session(engine, torch):
+    """A session without a device: what it checks before the library is called."""
+    s = object.__new__(engine.TreeSession)
+    s.desc, s.max_nodes, s.device = desc(n_rows=2, max_view_blocks=2), 3, torch.device("cpu")
+    s.dtype = s.cache_dtype = torch.bfloat16
+    s.sizes, s.workspace, s.ws_bytes, s.meta = (2 * 3 * 8 * 128, 2 * 3 * 2 * 128, 2 * 1000 * 128), None, 0, None
+    return s
+
+
+def test_refused_tensors_do_not_stay(monkeypatch):
+    """After a refusal the session holds what it held before."""
+    torch = pytest.importorskip("torch")
+    from concurrent_shared_kv_gb300 import engine
+    s = cpu_session(engine, torch)
+    calls = []
+    monkeypatch.setattr(engine.api, "attn_plan_tree", lambda *a, **kw: calls.append((a, kw)))
+    meta = dict(block_start=[0] * 3, block_len=[1] * 3, view_block=[[0, 1]] * 2, view_offset=[[0, 1]] * 2, q_pos=[0, 0])
+    trees = dict(tree_block=[0, 1], n_nodes=[1, 1], parent=[[-1] * 3] * 2)
+    with pytest.raises(ValueError):
+        s.plan(**trees)                      # no views yet
+    with pytest.raises(ValueError, match="q_pos"):
+        s.set_metadata(**{**meta, "q_pos": [0]})
+    with pytest.raises(ValueError):
+        s.plan(**trees)                      # still none
+    s.set_metadata(**meta)
+    for bad in (dict(meta, block_len=[7]), dict(meta, view_block=[[7]] * 2), dict(meta, q_to_kv=[0])):
+        with pytest.raises(ValueError):
+            s.set_metadata(**bad)
+    s.plan(**trees)
+    with pytest.raises(ValueError):
+        s.plan(**{**trees, "parent": [[-1] * 2] * 2})
+    assert len(calls) == 1 and s.trees[2].numel() == 6
+    a, kw = calls[0]
+    assert [x.numel() for x in a[2:7]] == [3, 3, 4, 4, 2] and a[3].tolist() == [1] * 3 and kw["q_to_kv"] is None
