@@ -153,16 +153,26 @@ def _ptr(x) -> Optional[int]:
 _torch_c = None
 
 
-def _raw_stream() -> int:
-    """The current CUDA stream's handle.  (torch.cuda.current_stream() builds an
-    object around it: 3 us of a call that may run for 5.)"""
+def current_device() -> int:
+    """The current CUDA device's index."""
     global _torch_c
     if _torch_c is None:
         import torch
         torch.cuda.current_device()
         _torch_c = torch._C
     try:
-        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+        return _torch_c._cuda_getDevice()
+    except AttributeError:
+        import torch
+        return torch.cuda.current_device()
+
+
+def _raw_stream() -> int:
+    """The current CUDA stream's handle.  (torch.cuda.current_stream() builds an
+    object around it: 3 us of a call that may run for 5.)"""
+    device = current_device()
+    try:
+        return _torch_c._cuda_getCurrentRawStream(device)
     except AttributeError:
         import torch
         return torch.cuda.current_stream().cuda_stream

@@ -172,15 +172,34 @@ def _int32(x, device):
     return t.to(device, dtype=torch.int32).contiguous()
 
 
-def _fits(what: str, x, n: int, dtype) -> None:
+def _current(device) -> None:
+    """Kernels are launched on the current device."""
+    index = device.index  # (of a GPU)
+    if index is not None and index != api.current_device():
+        raise ValueError(f"{device} is not the current device")
+
+
+def _on_gpu(device) -> None:
+    if device.type != "cuda":
+        raise ValueError(f"the tree calls need tensors on a GPU, not on {device}")
+    _current(device)
+
+
+def _misfit(what: str, x, n: int, dtype, device):
+    if x.device != device:
+        raise ValueError(f"{what} is on the device {x.device}, not on {device}")
+    raise ValueError(f"{what} needs {n} dense elements of {dtype}, got {tuple(x.shape)} of {x.dtype}")
+
+
+def _fits(what: str, x, n: int, dtype, device) -> None:
     """A dense tensor of n elements: what a kernel would read past otherwise."""
-    if x.numel() != n or x.dtype != dtype or not x.is_contiguous():
-        raise ValueError(f"{what} needs {n} dense elements of {dtype}, got {tuple(x.shape)} of {x.dtype}")
+    if x.numel() != n or x.dtype != dtype or x.device != device or not x.is_contiguous():
+        _misfit(what, x, n, dtype, device)
 
 
-def _pool_fits(what: str, x, n: int, dtype) -> None:
-    if x.numel() != n or x.element_size() != dtype.itemsize or not x.is_contiguous():  # (E4M3 may be held as bytes)
-        raise ValueError(f"{what} needs {n} dense elements of {dtype}, got {tuple(x.shape)} of {x.dtype}")
+def _pool_fits(what: str, x, n: int, dtype, device) -> None:
+    if x.numel() != n or x.element_size() != dtype.itemsize or x.device != device or not x.is_contiguous():
+        _misfit(what, x, n, dtype, device)  # (E4M3 may be held as bytes)
 
 
 class TreeSession:
@@ -194,6 +213,9 @@ class TreeSession:
         """max_nodes: nodes of the largest tree (q, out and the new tokens are
         [rows][max_nodes][heads][D]).  dtype, kv_fp8: as in DecodeSession."""
         self.device = torch.device(device)
+        if self.device == torch.device("cuda"):
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        _on_gpu(self.device)
         self.dtype = dtype
         self.max_nodes = int(max_nodes)
         self.desc = api.make_desc(n_rows, n_q_heads, n_kv_heads, head_dim, n_blocks,
@@ -215,9 +237,9 @@ class TreeSession:
         d = self.desc
         for what, x, n in zip(("block_start", "block_len", "view_block", "view_offset", "q_pos"), meta,
                               (d.n_blocks, d.n_blocks, d.n_rows * d.max_view_blocks, d.n_rows * d.max_view_blocks, d.n_rows)):
-            _fits(what, x, n, torch.int32)
+            _fits(what, x, n, torch.int32, self.device)
         if q_to_kv is not None:
-            _fits("q_to_kv", q_to_kv, d.n_q_heads, torch.int32)
+            _fits("q_to_kv", q_to_kv, d.n_q_heads, torch.int32, self.device)
         self.meta, self.q_to_kv = meta, q_to_kv
 
     def plan(self, tree_block, n_nodes, parent, tree_start=None, stream=None):
@@ -228,9 +250,10 @@ class TreeSession:
         tree_start = None if tree_start is None else _int32(tree_start, self.device)
         R = self.desc.n_rows
         for what, x, n in zip(("tree_block", "n_nodes", "parent"), trees, (R, R, R * self.max_nodes)):
-            _fits(what, x, n, torch.int32)
+            _fits(what, x, n, torch.int32, self.device)
         if tree_start is not None:
-            _fits("tree_start", tree_start, R, torch.int32)
+            _fits("tree_start", tree_start, R, torch.int32, self.device)
+        _current(self.device)
         self.trees, self.tree_start = trees, tree_start
         api.attn_plan_tree(self.desc, self.max_nodes, *self.meta, *self.trees, self.workspace,
                            self.ws_bytes, tree_start=self.tree_start, q_to_kv=self.q_to_kv,
@@ -247,15 +270,16 @@ class TreeSession:
 
     def _check_layer(self, q, k_new, v_new, k_cache, v_cache, out, lse):
         n_q, n_new, n_pool = self.sizes
-        dtype, cache = self.dtype, self.cache_dtype
-        _fits("q", q, n_q, dtype)
-        _fits("k_new", k_new, n_new, dtype)
-        _fits("v_new", v_new, n_new, dtype)
-        _fits("out", out, n_q, dtype)
-        _pool_fits("k_cache", k_cache, n_pool, cache)
-        _pool_fits("v_cache", v_cache, n_pool, cache)
+        dtype, cache, dev = self.dtype, self.cache_dtype, self.device
+        _fits("q", q, n_q, dtype, dev)
+        _fits("k_new", k_new, n_new, dtype, dev)
+        _fits("v_new", v_new, n_new, dtype, dev)
+        _fits("out", out, n_q, dtype, dev)
+        _pool_fits("k_cache", k_cache, n_pool, cache, dev)
+        _pool_fits("v_cache", v_cache, n_pool, cache, dev)
         if lse is not None:
-            _fits("lse", lse, n_q // self.desc.head_dim, torch.float32)
+            _fits("lse", lse, n_q // self.desc.head_dim, torch.float32, dev)
+        _current(dev)
 
     def decode(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                k_cache: torch.Tensor, v_cache: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -275,8 +299,8 @@ class TreeSession:
         """decode() over E4M3 pools with float32 scales [Hkv]; q and the new tokens bf16."""
         out, lse = self._outputs(out, lse, want_lse)
         self._check_layer(q, k_new, v_new, k_cache, v_cache, out, lse)
-        _fits("k_scale", k_scale, self.desc.n_kv_heads, torch.float32)
-        _fits("v_scale", v_scale, self.desc.n_kv_heads, torch.float32)
+        _fits("k_scale", k_scale, self.desc.n_kv_heads, torch.float32, self.device)
+        _fits("v_scale", v_scale, self.desc.n_kv_heads, torch.float32, self.device)
         api.attn_decode_tree_fp8(self.desc, self.max_nodes, q, k_new, v_new, k_cache, v_cache,
                                  k_scale, v_scale, out, lse, self.workspace, self.ws_bytes,
                                  stream=stream)
@@ -287,11 +311,12 @@ class TreeSession:
         """The accepted nodes (tree_verify's path and n_path) appended to the
         rows' blocks in every layer; pools [layers][Hkv][cap][D] or [Hkv][cap][D]."""
         layers = 1 if k_cache.dim() == 3 else k_cache.shape[0]
-        n, R, cache = layers * self.sizes[2], self.desc.n_rows, self.cache_dtype
-        _pool_fits("k_cache", k_cache, n, cache)
-        _pool_fits("v_cache", v_cache, n, cache)
-        _fits("path", path, R * self.max_nodes, torch.int32)
-        _fits("n_path", n_path, R, torch.int32)
+        n, R, cache, dev = layers * self.sizes[2], self.desc.n_rows, self.cache_dtype, self.device
+        _pool_fits("k_cache", k_cache, n, cache, dev)
+        _pool_fits("v_cache", v_cache, n, cache, dev)
+        _fits("path", path, R * self.max_nodes, torch.int32, dev)
+        _fits("n_path", n_path, R, torch.int32, dev)
+        _current(dev)
         api.tree_commit(self.desc, self.max_nodes, layers, k_cache, v_cache, path, n_path,
                         self.workspace, self.ws_bytes, stream=stream)
 
@@ -314,8 +339,12 @@ def tree_verify(n_nodes: torch.Tensor, parent: torch.Tensor, token: torch.Tensor
             raise ValueError("p and q need rows one stride apart with dense values")
         return s1 if T > 1 else s0 if R > 1 else V
 
-    if q is not None and (q.shape != shape or q.dtype != p.dtype):
-        raise ValueError("p and q differ in shape or type")
+    dev = p.device
+    if q is not None:
+        if q.shape != shape or q.dtype != p.dtype:
+            raise ValueError("p and q differ in shape or type")
+        if q.device != dev:
+            _misfit("q", q, q.numel(), q.dtype, dev)
     if path is None:
         path = torch.empty((R, T), dtype=torch.int32, device=p.device)
     if n_path is None:
@@ -323,14 +352,18 @@ def tree_verify(n_nodes: torch.Tensor, parent: torch.Tensor, token: torch.Tensor
     if next_token is None:
         next_token = torch.empty(R, dtype=torch.int32, device=p.device)
     i32 = torch.int32
-    _fits("n_nodes", n_nodes, R, i32)
-    _fits("parent", parent, R * T, i32)
-    _fits("token", token, R * T, i32)
-    _fits("path", path, R * T, i32)
-    _fits("n_path", n_path, R, i32)
-    _fits("next_token", next_token, R, i32)
-    _fits("u_accept", u_accept, R * T, torch.float32)
-    _fits("u_sample", u_sample, R, torch.float32)
+    _fits("n_nodes", n_nodes, R, i32, dev)
+    _fits("parent", parent, R * T, i32, dev)
+    _fits("token", token, R * T, i32, dev)
+    _fits("path", path, R * T, i32, dev)
+    _fits("n_path", n_path, R, i32, dev)
+    _fits("next_token", next_token, R, i32, dev)
+    _fits("u_accept", u_accept, R * T, torch.float32, dev)
+    _fits("u_sample", u_sample, R, torch.float32, dev)
+    if p.is_cuda:
+        _current(dev)
+    else:
+        _on_gpu(dev)
     api.tree_verify(DTYPES[p.dtype], R, T, V, n_nodes, parent, token, p, step(p), q,
                     0 if q is None else step(q), u_accept, u_sample, path, n_path, next_token,
                     stream=stream)

@@ -211,3 +211,53 @@ def test_refused_tensors_do_not_stay(monkeypatch):
     assert len(calls) == 1 and s.trees[2].numel() == 6
     a, kw = calls[0]
     assert [x.numel() for x in a[2:7]] == [3, 3, 4, 4, 2] and a[3].tolist() == [1] * 3 and kw["q_to_kv"] is None
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """A kernel would be handed an address that is not its own: refused, as are
+    tensors that are on no GPU at all."""
+    torch = pytest.importorskip("torch")
+    from concurrent_shared_kv_gb300 import engine
+
+    def called(*a, **kw):
+        raise AssertionError("the library was called")
+    for name in ("attn_plan_tree", "attn_decode_tree", "attn_decode_tree_fp8", "tree_commit", "tree_verify"):
+        monkeypatch.setattr(engine.api, name, called)
+    i, f, p = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3), torch.zeros(2, 3, 8)
+    good = dict(n_nodes=i[:, 0].contiguous(), parent=i, token=i, p=p, q=p, u_accept=f, u_sample=f[:, 0].contiguous(), path=i.clone(),
+                n_path=i[:, 0].contiguous(), next_token=i[:, 0].contiguous())
+    for name in good:
+        if name != "p":
+            with pytest.raises(ValueError, match=f"{name} is on the device meta"):
+                engine.tree_verify(**{**good, name: good[name].to("meta")})
+    with pytest.raises(ValueError, match="on a GPU"):
+        engine.tree_verify(**good)
+    s = cpu_session(engine, torch)
+    bf = dict(dtype=torch.bfloat16)
+    layer = dict(q=torch.zeros(2, 3, 8, 128, **bf), k_new=torch.zeros(2, 3, 2, 128, **bf), v_new=torch.zeros(2, 3, 2, 128, **bf),
+                 k_cache=torch.zeros(2, 1000, 128, **bf), v_cache=torch.zeros(2, 1000, 128, **bf),
+                 out=torch.zeros(2, 3, 8, 128, **bf), lse=torch.zeros(2, 3, 8))
+    scales = dict(k_scale=torch.ones(2), v_scale=torch.ones(2))
+    for name in layer:
+        with pytest.raises(ValueError, match=f"{name} is on the device meta"):
+            s.decode(**{**layer, name: layer[name].to("meta")})
+    step = dict(k_cache=layer["k_cache"], v_cache=layer["v_cache"], path=i, n_path=i[:, 0].contiguous())
+    for name in step:
+        with pytest.raises(ValueError, match=f"{name} is on the device meta"):
+            s.commit(**{**step, name: step[name].to("meta")})
+    for name in scales:
+        with pytest.raises(ValueError, match=f"{name} is on the device meta"):
+            s.decode_fp8(**layer, **{**scales, name: scales[name].to("meta")})
+    # a GPU that is not the current one
+    monkeypatch.setattr(engine.api, "current_device", lambda: 1)
+    s.device = torch.device("cuda", 0)
+    monkeypatch.setattr(engine, "_fits", lambda *a: None)
+    monkeypatch.setattr(engine, "_pool_fits", lambda *a: None)
+    monkeypatch.setattr(engine, "_int32", lambda x, *a: x)
+    s.set_metadata([], [], [], [], [])
+    for call in (lambda: s.decode(**layer), lambda: s.commit(**step), lambda: s.plan([], [], [])):
+        with pytest.raises(ValueError, match="not the current device"):
+            call()
+    with pytest.raises(ValueError, match="on a GPU"):
+        engine.TreeSession(n_rows=1, max_nodes=1, n_q_heads=1, n_kv_heads=1, head_dim=64, n_blocks=1, max_view_blocks=1, capacity=8,
+                           dtype=torch.float32, rope_theta=1e4, device="cpu")
