@@ -198,8 +198,9 @@ def _fits(what: str, x, n: int, dtype, device) -> None:
 
 
 def _pool_fits(what: str, x, n: int, dtype, device) -> None:
-    if x.numel() != n or x.element_size() != dtype.itemsize or x.device != device or not x.is_contiguous():
-        _misfit(what, x, n, dtype, device)  # (E4M3 may be held as bytes)
+    if x.numel() != n or x.device != device or not x.is_contiguous() or (
+            x.dtype != dtype and (dtype != torch.float8_e4m3fn or x.dtype != torch.uint8)):  # (codes may be bytes)
+        _misfit(what, x, n, dtype, device)
 
 
 class TreeSession:

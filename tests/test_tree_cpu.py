@@ -261,3 +261,36 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     with pytest.raises(ValueError, match="on a GPU"):
         engine.TreeSession(n_rows=1, max_nodes=1, n_q_heads=1, n_kv_heads=1, head_dim=64, n_blocks=1, max_view_blocks=1, capacity=8,
                            dtype=torch.float32, rope_theta=1e4, device="cpu")
+
+
+@pytest.mark.parametrize("cache,good,bad", [
+    ("bfloat16", ["bfloat16"], ["float16", "int16", "float32", "uint8"]), ("float32", ["float32"], ["int32", "bfloat16", "float64"]),
+    ("float8_e4m3fn", ["float8_e4m3fn", "uint8"], ["float8_e5m2", "int8", "bfloat16"])])
+def test_pools_of_another_type_are_refused(monkeypatch, cache, good, bad):
+    """A type of the same size is read as something else."""
+    torch = pytest.importorskip("torch")
+    from concurrent_shared_kv_gb300 import engine
+    s = cpu_session(engine, torch)
+    s.cache_dtype = getattr(torch, cache)
+    s.dtype = torch.float32 if cache == "float32" else torch.bfloat16
+    calls = []
+    for name in ("attn_decode_tree", "attn_decode_tree_fp8", "tree_commit"):
+        monkeypatch.setattr(engine.api, name, lambda *a, **kw: calls.append(a))
+
+    def new(dtype, *shape):
+        return torch.zeros(*shape).to(dtype)
+    q, kn = new(s.dtype, 2, 3, 8, 128), new(s.dtype, 2, 3, 2, 128)
+    path, n_path = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    ok = new(s.cache_dtype, 2, 1000, 128)
+    for names, refused in ((good, False), (bad, True)):
+        for name in names:
+            x = new(getattr(torch, name), 2, 1000, 128)
+            for k, v, what in ((x, ok, "k_cache"), (ok, x, "v_cache")):
+                for call in (lambda: s.decode(q, kn, kn, k, v, out=q, want_lse=False), lambda: s.commit(k, v, path, n_path),
+                             lambda: s.decode_fp8(q, kn, kn, k, v, torch.ones(2), torch.ones(2), out=q, want_lse=False)):
+                    if refused:
+                        with pytest.raises(ValueError, match=what):
+                            call()
+                    else:
+                        call()
+    assert len(calls) == 6 * len(good)
