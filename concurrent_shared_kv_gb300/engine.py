@@ -3,6 +3,7 @@ device copies of the per-step metadata.  PyTorch only allocates memory and
 provides streams here; every step of the computation runs in libhogwild."""
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import numpy as np
@@ -167,9 +168,47 @@ class DecodeSession:
         return api.workspace_status(self.workspace)
 
 
-def _int32(x, device):
+def _int32(x, device, stream=None):
+    """x as dense int32 on the device, under _on(stream)."""
     t = torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32)) if not torch.is_tensor(x) else x
-    return t.to(device, dtype=torch.int32).contiguous()
+    r = t.to(device, dtype=torch.int32).contiguous()
+    if r is not t and t.is_cuda:
+        _kept_for(stream, t)
+    return r
+
+
+def _on(stream, device):
+    """The stream of a call as torch's current one: tensors made under it are
+    made by it and go back to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):  # a handle
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _kept_for(stream, *tensors) -> None:
+    """Memory that goes back to the stream it came from only once `stream` (None:
+    the current one) is done with it.  (Not for handles: the allocator would
+    have to use one that may be gone by then.)"""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    if isinstance(stream, torch.cuda.Stream):
+        for x in tensors:
+            if x is not None and x.is_cuda:
+                x.record_stream(stream)
+
+
+def _new(shape, dtype, device, stream):
+    """An output of a call on `stream`, for the caller's current one as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    if x.is_cuda:
+        x.record_stream(torch.cuda.current_stream())
+    return x
 
 
 def _current(device) -> None:
@@ -205,7 +244,12 @@ def _pool_fits(what: str, x, n: int, dtype, device) -> None:
 
 class TreeSession:
     """Steps whose rows each query a tree of drafted tokens: plan(), one
-    decode() a layer, tree_verify(), commit()."""
+    decode() a layer, tree_verify(), commit().
+
+    A call with stream= runs on that stream (a torch stream, or a handle), and
+    what it makes - converted or uploaded arrays, outputs - is made there.  The
+    caller's own tensors have to be there for that stream and stay until it has
+    used them; a session whose calls have a handle is kept until they are done."""
 
     def __init__(self, *, n_rows: int, max_nodes: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
                  n_blocks: int, max_view_blocks: int, capacity: int, dtype: torch.dtype,
@@ -227,14 +271,17 @@ class TreeSession:
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         api.workspace_init(self.workspace, self.ws_bytes)
         self.meta = None
+        self.workspace_on = api._stream(None)  # the stream that its memory came from
         nodes = n_rows * self.max_nodes
         self.sizes = (nodes * n_q_heads * head_dim, nodes * n_kv_heads * head_dim, n_kv_heads * capacity * head_dim)
         self.cache_dtype = torch.float8_e4m3fn if kv_fp8 else dtype
 
-    def set_metadata(self, block_start, block_len, view_block, view_offset, q_pos, q_to_kv=None):
-        """Upload the step's views: those of the rows' tokens before their trees."""
-        meta = [_int32(x, self.device) for x in (block_start, block_len, view_block, view_offset, q_pos)]
-        q_to_kv = None if q_to_kv is None else _int32(q_to_kv, self.device)
+    def set_metadata(self, block_start, block_len, view_block, view_offset, q_pos, q_to_kv=None, stream=None):
+        """Upload the step's views: those of the rows' tokens before their trees.
+        stream: the one that plan() will have."""
+        with _on(stream, self.device):
+            meta = [_int32(x, self.device, stream) for x in (block_start, block_len, view_block, view_offset, q_pos)]
+            q_to_kv = None if q_to_kv is None else _int32(q_to_kv, self.device, stream)
         d = self.desc
         for what, x, n in zip(("block_start", "block_len", "view_block", "view_offset", "q_pos"), meta,
                               (d.n_blocks, d.n_blocks, d.n_rows * d.max_view_blocks, d.n_rows * d.max_view_blocks, d.n_rows)):
@@ -242,13 +289,15 @@ class TreeSession:
         if q_to_kv is not None:
             _fits("q_to_kv", q_to_kv, d.n_q_heads, torch.int32, self.device)
         self.meta, self.q_to_kv = meta, q_to_kv
+        self.meta_on = api._stream(stream)
 
     def plan(self, tree_block, n_nodes, parent, tree_start=None, stream=None):
         """hw_attn_plan_tree: the step's trees (tree_start None: behind each row's block)."""
         if self.meta is None:
             raise ValueError("plan() needs the step's views: set_metadata() first")
-        trees = [_int32(x, self.device) for x in (tree_block, n_nodes, parent)]
-        tree_start = None if tree_start is None else _int32(tree_start, self.device)
+        with _on(stream, self.device):
+            trees = [_int32(x, self.device, stream) for x in (tree_block, n_nodes, parent)]
+            tree_start = None if tree_start is None else _int32(tree_start, self.device, stream)
         R = self.desc.n_rows
         for what, x, n in zip(("tree_block", "n_nodes", "parent"), trees, (R, R, R * self.max_nodes)):
             _fits(what, x, n, torch.int32, self.device)
@@ -256,17 +305,19 @@ class TreeSession:
             _fits("tree_start", tree_start, R, torch.int32, self.device)
         _current(self.device)
         self.trees, self.tree_start = trees, tree_start
+        if self.device.type == "cuda" and not self.workspace_on == self.meta_on == api._stream(stream):
+            _kept_for(stream, self.workspace, *self.meta, self.q_to_kv)
         api.attn_plan_tree(self.desc, self.max_nodes, *self.meta, *self.trees, self.workspace,
                            self.ws_bytes, tree_start=self.tree_start, q_to_kv=self.q_to_kv,
                            stream=stream)
 
-    def _outputs(self, out, lse, want_lse):
+    def _outputs(self, out, lse, want_lse, stream):
         d = self.desc
         shape = (d.n_rows, self.max_nodes, d.n_q_heads)
         if out is None:
-            out = torch.empty(shape + (d.head_dim,), dtype=self.dtype, device=self.device)
+            out = _new(shape + (d.head_dim,), self.dtype, self.device, stream)
         if lse is None and want_lse:
-            lse = torch.empty(shape, dtype=torch.float32, device=self.device)
+            lse = _new(shape, torch.float32, self.device, stream)
         return out, lse
 
     def _check_layer(self, q, k_new, v_new, k_cache, v_cache, out, lse):
@@ -287,7 +338,7 @@ class TreeSession:
                lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
         """One layer: the trees' tokens written into the cache, then attended.
         Rows of out and lse behind a tree's nodes keep what they hold."""
-        out, lse = self._outputs(out, lse, want_lse)
+        out, lse = self._outputs(out, lse, want_lse, stream)
         self._check_layer(q, k_new, v_new, k_cache, v_cache, out, lse)
         api.attn_decode_tree(self.desc, self.max_nodes, q, k_new, v_new, k_cache, v_cache, out, lse,
                              self.workspace, self.ws_bytes, stream=stream)
@@ -298,7 +349,7 @@ class TreeSession:
                    v_scale: torch.Tensor, out: Optional[torch.Tensor] = None,
                    lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
         """decode() over E4M3 pools with float32 scales [Hkv]; q and the new tokens bf16."""
-        out, lse = self._outputs(out, lse, want_lse)
+        out, lse = self._outputs(out, lse, want_lse, stream)
         self._check_layer(q, k_new, v_new, k_cache, v_cache, out, lse)
         _fits("k_scale", k_scale, self.desc.n_kv_heads, torch.float32, self.device)
         _fits("v_scale", v_scale, self.desc.n_kv_heads, torch.float32, self.device)
@@ -346,13 +397,13 @@ def tree_verify(n_nodes: torch.Tensor, parent: torch.Tensor, token: torch.Tensor
             raise ValueError("p and q differ in shape or type")
         if q.device != dev:
             _misfit("q", q, q.numel(), q.dtype, dev)
-    if path is None:
-        path = torch.empty((R, T), dtype=torch.int32, device=p.device)
-    if n_path is None:
-        n_path = torch.empty(R, dtype=torch.int32, device=p.device)
-    if next_token is None:
-        next_token = torch.empty(R, dtype=torch.int32, device=p.device)
     i32 = torch.int32
+    if path is None:
+        path = _new((R, T), i32, dev, stream)
+    if n_path is None:
+        n_path = _new(R, i32, dev, stream)
+    if next_token is None:
+        next_token = _new(R, i32, dev, stream)
     _fits("n_nodes", n_nodes, R, i32, dev)
     _fits("parent", parent, R * T, i32, dev)
     _fits("token", token, R * T, i32, dev)

@@ -294,3 +294,46 @@ def test_pools_of_another_type_are_refused(monkeypatch, cache, good, bad):
                     else:
                         call()
     assert len(calls) == 6 * len(good)
+
+
+def test_a_call_makes_its_tensors_on_its_stream(monkeypatch):
+    """Conversions, uploads and outputs of a call with stream= belong to that
+    stream, those of a call without one to the current stream."""
+    torch = pytest.importorskip("torch")
+    import contextlib
+    from concurrent_shared_kv_gb300 import engine
+    now, made = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, now[0] = now[0], stream
+        yield
+        now[0] = before
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle, raising=False)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    for module, name in ((engine, "_int32"), (torch, "empty")):
+        real = getattr(module, name)
+        monkeypatch.setattr(module, name, lambda *a, real=real, **kw: (made.append(now[0]), real(*a, **kw))[1])
+    for name in ("attn_plan_tree", "attn_decode_tree", "attn_decode_tree_fp8", "tree_verify"):
+        monkeypatch.setattr(engine.api, name, lambda *a, **kw: None)
+    monkeypatch.setattr(engine, "_on_gpu", lambda device: None)
+
+    class Handle:  # another library's stream
+        cuda_stream = 99
+
+    s = cpu_session(engine, torch)
+    bf = dict(dtype=torch.bfloat16)
+    q, kn, k = torch.zeros(2, 3, 8, 128, **bf), torch.zeros(2, 3, 2, 128, **bf), torch.zeros(2, 1000, 128, **bf)
+    i, f, p = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3), torch.zeros(2, 3, 8)
+    for stream, want in ((None, None), (77, 77), (0, "default"), (Handle(), 99)):
+        made.clear()
+        s.set_metadata([0] * 3, [1] * 3, [[0, 1]] * 2, [[0, 1]] * 2, [0, 0], q_to_kv=[0] * 8, stream=stream)
+        s.plan([0, 1], torch.tensor([1, 1]), [[-1] * 3] * 2, tree_start=[0, 5], stream=stream)
+        assert len(made) == 10
+        s.decode(q, kn, kn, k, k, stream=stream)
+        s.decode_fp8(q, kn, kn, k, k, torch.ones(2), torch.ones(2), stream=stream)
+        engine.tree_verify(i[:, 0].contiguous(), i, i, p, None, f, f[:, 0].contiguous(), stream=stream)
+        assert made == [want] * 17
+        s.decode(q, kn, kn, k, k, out=q, want_lse=False, stream=stream)
+        assert len(made) == 17 and now[0] is None

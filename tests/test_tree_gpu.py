@@ -1057,3 +1057,92 @@ def test_commit_of_one_block_by_the_row_that_may():
     k = t.k.clone()
     s.commit(k, t.v.clone(), ref.dev([[0, 2, 3, -1], [0, 1, -1, -1]]), ref.dev([3, 2]))
     assert s.device_flags() == 2 and torch.equal(bits(k), bits(t.k))
+
+
+# ------------------------------------------------- calls with a stream of their own
+
+def busy(stream=None, ms=60):
+    """Work that keeps a stream busy for about so long."""
+    with torch.cuda.stream(stream or torch.cuda.current_stream()):
+        torch.cuda._sleep(int(ms * 1.5e6))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_plan_converts_on_its_own_stream(handle):
+    """The current stream is busy while a plan on another one converts its
+    arrays; the plans before it are still to come when their arrays go."""
+    st = torch.cuda.Stream()
+    stream = st.cuda_stream if handle else st
+    good = [Tree("bf16", lens=(300, 40, 129), T=6, in_place=True, seed=90 + i) for i in range(3)]
+    want = []
+    for t in good:
+        o, l = t.run(t.session())
+        want.append(o.clone())
+    s = good[0].session()
+    arrays = [[ref.dev(x, torch.int64) for x in (t.tree_block, t.n_nodes, t.parent)] for t in good]
+    outs = [torch.empty_like(t.q) for t in good]
+    torch.cuda.synchronize()
+    busy()        # the current stream: what is made there comes late
+    busy(st, 30)  # the plans' stream: the host is ahead by all three
+    for i, (t, o) in enumerate(zip(good, outs)):
+        s.plan(*arrays[i], stream=stream)
+        s.decode(t.q, t.k_new, t.v_new, t.k, t.v, out=o, want_lse=False, stream=stream)
+        junk = [torch.full((n,), 2 ** 30, dtype=torch.int32, device="cuda") for n in (2, 2, 12, 2) for _ in range(8)]
+        del junk
+    torch.cuda.synchronize()
+    assert s.device_flags() == 0
+    for o, w in zip(outs, want):
+        assert torch.equal(bits(o), bits(w))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_do_not_take_memory_that_is_still_in_use(handle):
+    """Memory that a caller has given back may still be written by its stream."""
+    st = torch.cuda.Stream()
+    stream = st.cuda_stream if handle else st
+    t = Tree("bf16", lens=(300, 40, 129), T=6, seed=93)
+    s = t.session()
+    o, l = t.run(s)
+    rng = np.random.Generator(np.random.PCG64(93))
+    x = draw_verify(rng, 4, 5, 100, "f32", True)
+    args = [ref.dev(x["n_nodes"]), ref.dev(x["parent"]), ref.dev(x["token"]), x["p"].cuda(), x["q"].cuda(),
+            ref.dev(x["u_accept"], torch.float32), ref.dev(x["u_sample"], torch.float32)]
+    verified = [g.clone() for g in engine.tree_verify(*args)]
+    torch.cuda.synchronize()
+    old = [torch.empty_like(y) for y in (o, l, *verified)]
+    busy()
+    for y in old:
+        y.fill_(7)
+    del old, y
+    o2, l2 = s.decode(t.q, t.k_new, t.v_new, t.k, t.v, stream=stream)
+    got = engine.tree_verify(*args, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(o2), bits(o)) and torch.equal(l2, l)
+    for a, b in zip(got, verified):
+        assert torch.equal(a, b)
+
+
+def test_a_session_captured_with_its_plan():
+    """plan() and decode() of the session itself in a graph, on arrays of the
+    caller's; the session and other sessions go on beside it."""
+    t, t2 = (Tree("bf16", lens=(300, 40, 129), T=6, in_place=True, seed=94 + i) for i in range(2))
+    want = [x.run(x.session())[0].clone() for x in (t, t2)]
+    s = t.session()
+    arrays = [ref.dev(x) for x in (t.tree_block, t.n_nodes, t.parent)]
+    g, out = torch.cuda.CUDAGraph(), torch.empty_like(t.q)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        s.plan(*arrays)
+        s.decode(t.q, t.k_new, t.v_new, t.k, t.v, out=out, want_lse=False)
+    mine = (t.q, t.k_new, t.v_new, t.k, t.v, arrays[2])
+    first, second = [y.clone() for y in mine], (t2.q, t2.k_new, t2.v_new, t2.k, t2.v, ref.dev(t2.parent))
+    for values, w in ((first, want[0]), (second, want[1]), (first, want[0])):
+        for a, b in zip(mine, values):
+            a.copy_(b)
+        out.fill_(1)
+        g.replay()
+        assert torch.equal(bits(out), bits(w))
+    assert s.device_flags() == 0
+    del g
+    s.plan(*arrays)
+    assert torch.equal(bits(s.decode(t.q, t.k_new, t.v_new, t.k, t.v)[0]), bits(want[0]))
