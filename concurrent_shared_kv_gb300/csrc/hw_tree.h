@@ -28,10 +28,9 @@
 //              that owns a row both move whole sectors.
 // The rotation of a (row, view entry, node) is the same for every layer and q
 // head: the plan holds its cos and sin, head_dim / 2 pairs each - in fp32 for
-// the keys that are stored and for the CUDA cores, in fp16 (in the order of
-// rot16_at) for the tensor-core kernel, which rounds the turned query to bf16:
-// 2^-12 beside bf16's 2^-8, and half the loads of a warp with a thousand
-// clocks of latency and few registers.
+// the keys that are stored and for the CUDA cores, and again in the order
+// in which the tensor-core kernel reads them (turn_at): in fp32 for bf16 caches,
+// whose turned queries keep 16 bits, in fp16 for E4M3 caches, whose keep 8.
 // tree_merge_kernel joins the records of every (row, node, q head).
 #pragma once
 
@@ -87,7 +86,7 @@ struct TreeCta {
 
 // Byte offsets of the plan's arrays in the workspace (the error word is at 0).
 struct TreeLayout {
-  size_t hdr, groups, wbase, spans, map, columns, rot, rot16, blocks, piece_row, piece_cta, ctas;
+  size_t hdr, groups, wbase, spans, map, columns, rot, turns, blocks, piece_row, piece_cta, ctas;
   size_t n_nodes, slot, pos, end, col, rot0, rank, depth, mask, heads, block_start, block_len;
   size_t ml, o, total;
   int64_t max_groups, max_spans, max_map, max_cols, max_blocks, max_rots, max_rows;
@@ -146,11 +145,12 @@ cudaError_t launch_tree_commit(const TreeArgs &a, const TreeCommitArgs &c, cudaS
 cudaError_t launch_tree_verify(const TreeVerifyArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
-// Where an fp16 table row keeps element e's (cos, sin), e < half = head_dim / 2:
-// elements 8c + 4j .. 8c + 4j + 3 side by side, c running before j, so that
-// the lanes that each turn 8 neighbouring elements read neighbouring memory.
-__host__ __device__ __forceinline__ int rot16_at(int e, int half) {
-  return ((((e & 7) >> 2) * (half >> 3) + (e >> 3)) << 2) | (e & 3);
+// Where a table row keeps element e's (cos, sin), e < half = head_dim / 2:
+// the n that 16 bytes hold (4 in fp16, 2 in fp32) side by side, 8c + n j ..
+// 8c + n j + n - 1, c running before j, so that the lanes that each turn 8
+// neighbouring elements read neighbouring memory.
+__host__ __device__ __forceinline__ int turn_at(int e, int half, int n) {
+  return ((e & 7) / n * (half >> 3) + (e >> 3)) * n + e % n;
 }
 // Element d of column col in a record of n_cols columns that starts at row rec.
 __device__ __forceinline__ int64_t record_at(int64_t rec, int n_cols, int col, int d, int D) {

@@ -568,13 +568,13 @@ __global__ void __launch_bounds__(256) tree_tables_kernel(const __grid_constant_
                                : tree_at<int32_t>(a, a.L.pos)[r];
     for (int i = warp; i < n; i += 8) {
       const int64_t rel = root + tree_at<int32_t>(a, a.L.depth)[static_cast<int64_t>(r) * T + i];
-      float2 *to = tree_at<float2>(a, a.L.rot) + (rot0[r] + static_cast<int64_t>(v) * n + i) * half;
-      __half2 *to16 = tree_at<__half2>(a, a.L.rot16) + (rot0[r] + static_cast<int64_t>(v) * n + i) * half;
+      const int64_t row = (rot0[r] + static_cast<int64_t>(v) * n + i) * half;
       for (int j = lane; j < half; j += 32) {
         float2 x;
         rope_cos_sin_exact(rel, a.phase[j], &x.x, &x.y);
-        to[j] = x;
-        to16[rot16_at(j, half)] = __floats2half2_rn(x.x, x.y);
+        tree_at<float2>(a, a.L.rot)[row + j] = x;
+        if (a.L.cols > 32 && a.dtype == HW_BF16) tree_at<float2>(a, a.L.turns)[row + turn_at(j, half, 2)] = x;
+        else if (a.L.cols > 32) tree_at<__half2>(a, a.L.turns)[row + turn_at(j, half, 4)] = __floats2half2_rn(x.x, x.y);
       }
     }
   }
@@ -942,7 +942,7 @@ TreeLayout tree_layout(const hw_attn_desc &d, int max_nodes, int sms) {
   L.map = put(2 * L.max_map);
   L.columns = put(sizeof(TreeColumn) * L.max_cols);
   L.rot = put(4 * static_cast<size_t>(d.head_dim) * L.max_rots);
-  L.rot16 = put(2 * static_cast<size_t>(d.head_dim) * L.max_rots);
+  L.turns = put((!tc ? 0 : d.dtype == HW_BF16 ? 4 : 2) * static_cast<size_t>(d.head_dim) * L.max_rots);
   L.max_blocks = L.max_cols / 32 + L.max_groups;
   L.blocks = put(8 * L.max_blocks);
   L.piece_row = put(4 * L.max_groups * d.n_kv_heads);

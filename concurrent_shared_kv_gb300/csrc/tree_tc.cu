@@ -4,7 +4,7 @@
 // A group (hw_tree.h) puts up to 256 query columns (nodes x q heads of a kv
 // head x rows that share blocks) against its spans' tokens, as two query tiles
 // of 128 rows that share every K/V tile:
-//   S [128 queries x 128 tokens] = Q~ . K^T     (A, B in shared memory)
+//   S [128 queries x 128 tokens] = Q~ . K^T     (A, B in shared memory; Q~ in two parts)
 //   O [128 queries x 128 d]     += P . V        (A = P in TMEM)
 // With a query per TMEM lane, a softmax thread owns its row: no exchange for
 // maxima and sums, and P goes back to the columns that S came from.
@@ -28,13 +28,12 @@
 // Warps: 0-7 softmax of stream 0 (0-3 tokens 0-63, 4-7 the others), 8-15 of
 // stream 1, 16 the TMA producer, 17 and 18 the issuers.
 // Rotated queries carry scale * log2(e), so scores leave the MMA in log2
-// units; they are rounded to bf16 once, as models round theirs, and P is too.
-// For keys and queries of unit variance each of the three roundings (queries,
-// P, output) leaves 0.0016 of the exact result in the 2-norm; outputs are
-// measured 0.003 to 0.004 off.  (Queries as two bf16 parts remove one of the
-// three, at QK twice over and three ring stages instead of five: 4 trees of 16
-// nodes over 16K tokens took 47 us instead of 39.5, of 64 nodes 114 instead of
-// 93, a ragged batch of 8 x 4 trees of 8 nodes 174 instead of 157.)
+// units.  They are held as two bf16 parts, hi and what that leaves, as the
+// decode holds them: a score keeps 16 bits, and QK runs over both.  P is rounded
+// to bf16 once, against sums of weights in fp32.  Outputs are measured 0.0015 to
+// 0.0016 off the exact result in the 2-norm, which is the output's own rounding.
+// (With queries rounded to bf16 once it was 0.0033, and more for larger scores:
+// the error of a score grows with it, that of a weight does not.)
 //
 // E4M3 caches: both products run as kind::f8f6f4 on the codes, at twice the
 // rate, with Q~ and P each as two E4M3 parts x = hi + lo, lo the rounded
@@ -64,23 +63,26 @@ constexpr int kThreads = 608;
 constexpr int kWarpTma = 16, kWarpMma = 17;  // and 18: an issuer a stream
 constexpr int kT = 128;                      // tokens per tile
 constexpr uint32_t kBox = 128 * 128;         // 128 rows of 128 bytes, 128-byte swizzled
-constexpr uint32_t kQTile = 2 * kBox;        // a query tile: d 0-63, d 64-127 (E4M3: hi, lo)
 // The ring of K and V tiles: bf16 two boxes each, E4M3 one.  A CTA without a
 // group of over 128 columns has no second query tile, and that much more ring
 // (kMore stages): what one query tile can do is bound by the bytes under way.
 template <bool kFp8>
 struct Ring {
+  static constexpr uint32_t kQTile = kFp8 ? 2 * kBox : 4 * kBox;  // a query tile: hi, then lo; bf16 d 0-63 and d 64-127 of each
   static constexpr uint32_t kStage = kFp8 ? kBox : 2 * kBox;
-  static constexpr int kStages = kFp8 ? 9 : 5;
+  static constexpr int kStages = kFp8 ? 9 : 3;
   static constexpr int kMore = kQTile / kStage;
   static constexpr int kStep = kFp8 ? 32 : 16;  // tokens of one MMA
   // A wait for a stage's next tile can be told from its last one only if that
-  // has landed.  Five stages before the K of tile t is the V of tile t - 3: its
-  // turn at least three before tile t's.  A stream that has waited for turn
-  // m - 1 of the other one knows that the V tiles of that one's turns up to
-  // m - 3 have landed, and those of its own up to m - 4.  Three stages back a V
-  // may still be under way.
-  static_assert(kStages >= 5, "the barriers' phases");
+  // has landed.  A stream that has waited for turn m - 1 of the other one knows
+  // that the V tiles of that one's turns up to m - 3 have landed, and those of
+  // its own up to m - 4.  Five stages before the K of tile t is the V of tile
+  // t - 3, its turn at least three before tile t's.  Three stages before it is
+  // the V of tile t - 2: known where both streams take every tile, but where
+  // they take turns that is the one whose products this stream has still to
+  // issue; they go first then (kShort), as the K can only come after them.
+  static constexpr int kShort = 5;  // rings of fewer stages
+  static_assert(kStages == 3 || kStages >= kShort, "the barriers' phases");
 };
 // A place in a ring of n stages.
 struct RingPos {
@@ -107,7 +109,7 @@ template <bool kFp8>
 struct TcSmem {
   static constexpr int kStages = Ring<kFp8>::kStages;
   static constexpr int kAll = kStages + Ring<kFp8>::kMore;
-  alignas(1024) uint8_t q[2][kQTile];                     // (the second tile's place: part of the ring without one)
+  alignas(1024) uint8_t q[2][Ring<kFp8>::kQTile];                     // (the second tile's place: part of the ring without one)
   alignas(1024) uint8_t kv[kStages][Ring<kFp8>::kStage];
   uint64_t kv_full[kAll], kv_empty[kAll];
   uint64_t q_full[2], q_free, s_full[2], p_half[2], p_full[2], pv_done[2], o_empty[2], order, mma_done;
@@ -207,6 +209,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&p);
+}
+// (x, y) in bf16, and what that leaves of them, in bf16 too.  (An infinity
+// leaves NaN, as its products with values of both signs do.)
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
+  hi = pack_bf16(x, y);
+  lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
 }
 // The same for 8-bit inputs.
 __device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -346,6 +354,7 @@ __device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *
 template <bool kFp8>
 __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk w, int q) {
   constexpr int kStep = Ring<kFp8>::kStep;
+  constexpr int kSteps = kFp8 ? 8 : 16;  // of QK: 128 d, 32 or 16 a step, hi and lo
   constexpr uint32_t kStage = Ring<kFp8>::kStage;
   constexpr uint32_t idesc_qk = kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
   constexpr uint32_t idesc_pv = kFp8 ? idesc_e4m3(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);
@@ -437,22 +446,23 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
       // time, the tensor cores idle.
       if (mine > 0 && !(go = warp_wait(S, a, &S.order, (mine - 1) & 1))) break;
       // Not before the turn: it says that the stage's last tile has landed (Ring).
+      if (w.stages < Ring<kFp8>::kShort && !two && pend && !(go = flush())) break;
       if (!(go = warp_wait(S, a, &S.kv_full[s], k.phase))) break;
       if (pend && !(go = pv_first())) break;
       if (!turned && !(go = queries(two))) break;
       turned = true;
       tc_fence_after();
-      const uint64_t as = a_qk + ((two ? q * kQTile : 0) >> 4), bs = b_qk + ((s * kStage) >> 4);
+      const uint64_t as = a_qk + ((two ? q * Ring<kFp8>::kQTile : 0) >> 4), bs = b_qk + ((s * kStage) >> 4);
       if (elect_one()) {
         if (pend) pv();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {  // 8 steps of 16 over d (E4M3: 4 of 32, hi then lo)
+        for (int j = 0; j < kSteps; ++j) {  // over d with hi, then with lo
           const uint32_t o = ((j >> 2) * kBox + (j & 3) * 32) >> 4;
           if constexpr (kFp8)
             mma_f8(s_tmem, as + o, bs + (((j & 3) * 32) >> 4), idesc_qk, j > 0);
           else
-            mma_bf16(s_tmem, as + o, bs + o, idesc_qk, j > 0);
-          if (j == 5) mbar_arrive(&S.order);  // (the next turn's first MMA is two MMAs away)
+            mma_bf16(s_tmem, as + o, bs + ((((j >> 2) & 1) * kBox + (j & 3) * 32) >> 4), idesc_qk, j > 0);
+          if (j == kSteps - 3) mbar_arrive(&S.order);  // (the next turn's first MMA is two MMAs away)
         }
         mma_commit(&S.s_full[q]);
         mma_commit(&S.kv_empty[s]);
@@ -494,26 +504,30 @@ __device__ __forceinline__ void write_queries(const __nv_bfloat16 *q, const uint
   // (rows that see nothing read row 0: loads without branches are all under
   // way before the first is needed, and one trip to L2 costs a thousand
   // clocks or more)
-  uint4 u[N / 4], v[N / 4], cs[N / 4][2];
+  constexpr int kTurn = kFp8 ? 2 : 4;  // 16-byte pieces of (cos, sin) for 8 elements: fp16, fp32
+  uint4 u[N / 4], v[N / 4], cs[N / 4][kTurn];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     const int at = first + 4 * i + (lane >> 3);
     const int row = __shfl_sync(0xffffffffu, src, at), turn = max(0, __shfl_sync(0xffffffffu, rot, at));
     const uint4 *x = reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(row) * 128);
-    const uint4 *t = table + static_cast<int64_t>(turn) * 16;
+    const uint4 *t = table + static_cast<int64_t>(turn) * 8 * kTurn;
     u[i] = __ldg(x + c);
     v[i] = __ldg(x + c + 8);
-    cs[i][0] = __ldg(t + c);  // (cos, sin) of elements 8c .. 8c + 3, then of the next four
-    cs[i][1] = __ldg(t + c + 8);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) cs[i][j] = __ldg(t + c + 8 * j);  // (turn_at)
   }
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    const uint32_t w[8] = {cs[i][0].x, cs[i][0].y, cs[i][0].z, cs[i][0].w, cs[i][1].x, cs[i][1].y, cs[i][1].z, cs[i][1].w};
+    uint32_t w[4 * kTurn];
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) w[4 * j] = cs[i][j].x, w[4 * j + 1] = cs[i][j].y, w[4 * j + 2] = cs[i][j].z, w[4 * j + 3] = cs[i][j].w;
     float p[8], r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+      const float2 t = kFp8 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[j]))
+                            : make_float2(__uint_as_float(w[(2 * j) % (4 * kTurn)]), __uint_as_float(w[(2 * j + 1) % (4 * kTurn)]));
       const float x0 = __uint_as_float(j & 1 ? x[j / 2] & 0xffff0000u : x[j / 2] << 16);
       const float y0 = __uint_as_float(j & 1 ? y[j / 2] & 0xffff0000u : y[j / 2] << 16);
       p[j] = (x0 * t.x - y0 * t.y) * scale;
@@ -545,8 +559,15 @@ __device__ __forceinline__ void write_queries(const __nv_bfloat16 *q, const uint
       st_shared_v2(o1 + kBox, lr[0] | lr[1] << 16, lr[2] | lr[3] << 16);
     } else {
       const uint32_t oc = o + ((c ^ (at & 7)) << 4);
-      st_shared_v4(oc, pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
-      st_shared_v4(oc + kBox, pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]), pack_bf16(r[4], r[5]), pack_bf16(r[6], r[7]));
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split_bf16(p[2 * j], p[2 * j + 1], hi[j], lo[j]);
+      st_shared_v4(oc, hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(oc + 2 * kBox, lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split_bf16(r[2 * j], r[2 * j + 1], hi[j], lo[j]);
+      st_shared_v4(oc + kBox, hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(oc + 3 * kBox, lo[0], lo[1], lo[2], lo[3]);
     }
   }
 }
@@ -663,15 +684,17 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
     if (nspan > 0) idle_wait(S, a, &S.q_free, (nspan - 1) & 1);
     if (warp_on) {
       const __nv_bfloat16 *qs = static_cast<const __nv_bfloat16 *>(a.q);
-      const uint4 *table = tree_at<uint4>(a, a.L.rot16);
+      const uint4 *table = tree_at<uint4>(a, a.L.turns);
       const int rot = v < 0 ? -1 : tc.rot + v * tc.n_nodes;
       // two query tiles: a tile a stream, half of a warp's rows a half; one: a quarter each
       const uint32_t to = smem_u32(S.q[two ? q : 0]) + quarter * 32 * 128;
       const float scale = kFp8 ? a.scale_log2 * a.k_scale[w.head] : a.scale_log2;
       float *back = &S.back[kFp8 ? nspan & 1 : 0][two ? q : 0][kFp8 ? quarter * 32 : 0];
-      if (two)
-        write_queries<kFp8, 16>(qs, table, src, rot, to, scale, 16 * half, lane, back);
-      else
+      if (two) {
+        constexpr int N = kFp8 ? 16 : 8;  // (as many as registers hold)
+#pragma unroll 1
+        for (int i = 0; i < 16; i += N) write_queries<kFp8, N>(qs, table, src, rot, to, scale, 16 * half + i, lane, back);
+      } else
         write_queries<kFp8, 8>(qs, table, src, rot, to, scale, 8 * (2 * q + half), lane, back);
       fence_proxy_async_smem();
     }

@@ -369,9 +369,10 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
  * Types: those of hw_attn_decode, and HW_FP8_E4M3 (hw_attn_decode_tree_fp8,
  * scales as in hw_attn_decode_planned_fp8, new tokens stored as
  * hw_attn_append_decode_planned_fp8 stores them); no HW_DESC_VIEW_LIMITS.
- * On the tensor cores (head_dim 128, bf16 or E4M3 caches) a rotated query and
- * a token's weight are rounded to bf16 (E4M3: to two E4M3 parts) once; sums,
- * maxima and lse are fp32.
+ * On the tensor cores (head_dim 128) a rotated query is held as two bf16
+ * parts, about 16 bits, and a token's weight is rounded to bf16 once (E4M3
+ * caches: both are held as two E4M3 parts, about 8 bits); sums, maxima and lse
+ * are fp32.
  * HW_DESC_EARLY_LOADS is accepted and changes nothing.  The workspace is that
  * of hw_attn_tree_workspace_size, zeroed once with hw_workspace_init, used by
  * one stream at a time and by the tree calls of this description and

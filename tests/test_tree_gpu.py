@@ -1146,3 +1146,28 @@ def test_a_session_captured_with_its_plan():
     del g
     s.plan(*arrays)
     assert torch.equal(bits(s.decode(t.q, t.k_new, t.v_new, t.k, t.v)[0]), bits(want[0]))
+
+
+# ----------------------------------------------------------- what scores keep
+
+@pytest.mark.parametrize("spread", [1.0, 6.0])
+@pytest.mark.parametrize("T,n", [(4, 600), (40, 3000)])
+def test_bf16_scores_keep_two_parts_of_a_query(spread, T, n):
+    """A turned query is held as two bf16 parts, as the decode holds it: half a
+    step twice, 2^-16 of it, and as much again for sums in fp32.  So lse is that
+    near, and a weight is off by its own rounding and twice that (a quotient)."""
+    t = Tree("bf16", hq=10, hkv=2, lens=(n, 40, 300), T=T, seed=100 + T, scale=spread * 128 ** -0.5)
+    t.q_pos = t.q_pos + 100_000
+    s = t.session()
+    out, lse = t.run(s)
+    o, l, absv, reach = ref.attend(
+        q=ref.to_np(t.q), k=np.nan_to_num(t.stored(t.k, None)), v=np.nan_to_num(t.stored(t.v, None)), block_start=t.block_start,
+        block_len=t.block_len, views=t.view_block, offsets=t.view_offset, q_pos=t.q_pos, tree_block=t.tree_block,
+        tree_start=t.tree_start, n_nodes=t.n_nodes, parent=t.parent, heads=t.heads, scale=t.scale, theta=t.theta)
+    score = 2.0 ** -15 * reach
+    worst = (np.abs(ref.to_np(lse) - l) / (score + 1e-5)).max()
+    assert worst <= 1
+    step = STEP["bf16"]
+    most = step * np.abs(o) + 1.05 * (step + 2 * score[..., None]) * absv + 1e-6
+    worst = (np.abs(ref.to_np(out) - o) / most).max()
+    assert worst <= 1
