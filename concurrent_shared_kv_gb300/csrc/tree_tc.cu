@@ -95,10 +95,23 @@ struct RingPos {
       phase ^= 1;
     }
   }
-  __device__ __forceinline__ RingPos next(int n) const {
-    RingPos p = *this;
-    p.on(1, n);
-    return p;
+};
+// Where the CTA's tiles are in the ring.  Where streams take turns the V of
+// tile t is used with the K of tile t + 2, and where that makes a difference
+// (`ahead`) the ring is filled in that order, K(0) K(1) V(0) K(2) V(1) .. V(n-1):
+// a place then is not held up by one that is used later.  Else K(0) V(0) K(1) ..
+struct KvPos {
+  RingPos k, v;
+  int left, stages;  // tiles from this one on
+  bool ahead, first;
+  __device__ __forceinline__ KvPos(int n, int ring, bool a) : k{0, 0}, v{0, 0}, left(n), stages(ring), ahead(a), first(true) {
+    v.on(ahead && n > 1 ? 2 : 1, stages);
+  }
+  __device__ __forceinline__ void next() {
+    k.on(ahead && first ? 1 : 2, stages);
+    v.on(ahead && left == 2 ? 1 : 2, stages);
+    first = false;
+    --left;
   }
 };
 constexpr float kLazy = 8.f;                 // O is rescaled only when a weight would pass 2^8
@@ -275,6 +288,7 @@ struct Walk {
   TreeSpan sp;
   int tiles;  // of this span that are the CTA's
   int stages;     // of the ring
+  bool ahead;     // how it is filled (KvPos)
   uint32_t ring;  // its shared-memory address
   __device__ __forceinline__ void load_span() {
     sp = tree_at<TreeSpan>(a, a.L.spans)[g.span0 + span];
@@ -311,6 +325,17 @@ __device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *
   int n = 0;  // ring entries issued: K(0), V(0), K(1), V(1), ...
   RingPos at = {0, 0};
   bool waited = false, go = true;
+  auto load = [&](bool v, int row, int head) {
+    if (n >= w.stages && !wait_or_abort(S, a, &S.kv_empty[at.s], at.phase ^ 1)) return false;
+    uint8_t *to = ring + at.s * kStage;
+    mbar_arrive_expect_tx(&S.kv_full[at.s], kStage);
+    tma_load_3d(to, v ? tv : tk, &S.kv_full[at.s], 0, row, head, pol);
+    if constexpr (!kFp8) tma_load_3d(to + kBox, v ? tv : tk, &S.kv_full[at.s], 64, row, head, pol);
+    ++n;
+    at.on(1, w.stages);
+    return true;
+  };
+  int v_row = -1, v_head = 0;  // the V behind the next K, if any
   do {
     if (w.sp.row >= 0 && !waited) {  // a tree: its tokens come from the launch before
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -327,18 +352,17 @@ __device__ void producer(const TreeArgs &a, TcSmem<kFp8> &S, const CUtensorMap *
     }
     for (int t = w.tile; go && t < w.tile + w.tiles; ++t) {
       const int row = w.sp.start + t * kT;
-      for (int kv = 0; kv < 2; ++kv, ++n, at.on(1, w.stages)) {
-        if (n >= w.stages && !wait_or_abort(S, a, &S.kv_empty[at.s], at.phase ^ 1)) {
-          go = false;
-          break;
-        }
-        uint8_t *to = ring + at.s * kStage;
-        mbar_arrive_expect_tx(&S.kv_full[at.s], kStage);
-        tma_load_3d(to, kv ? tv : tk, &S.kv_full[at.s], 0, row, w.head, pol);
-        if constexpr (!kFp8) tma_load_3d(to + kBox, kv ? tv : tk, &S.kv_full[at.s], 64, row, w.head, pol);
+      go = load(false, row, w.head);
+      if (w.ahead) {
+        if (go && v_row >= 0) go = load(true, v_row, v_head);
+        v_row = row;
+        v_head = w.head;
+      } else if (go) {
+        go = load(true, row, w.head);
       }
     }
   } while (go && w.next());
+  if (go && v_row >= 0) load(true, v_row, v_head);
   if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
   // no copy may still be landing when the CTA retires
   RingPos back = {0, 0};
@@ -422,7 +446,7 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
   auto queries = [&](bool two) -> bool {
     return warp_wait(S, a, &S.q_full[q], nspan & 1) && (two || warp_wait(S, a, &S.q_full[q ^ 1], nspan & 1));
   };
-  RingPos k = {0, 0};   // the next tile's K
+  KvPos at(w.left, w.stages, w.ahead);
   int step = 2;         // 2: a group starts
   // Turns at the tensor cores so far, of both streams.  They alternate over the
   // whole of the CTA's work, stream 0 the even ones: whoever waits for the turn
@@ -436,18 +460,18 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
       first = true;
     }
     bool turned = false;  // this span's queries are there
-    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turns += two ? 2 : 1) {
+    for (int t = 0; t < w.tiles; ++t, at.next(), turns += two ? 2 : 1) {
       const bool later = (turns ^ q) & 1;  // the other stream's turn is before this one's
       if (!two && later) continue;
-      const int s = k.s, mine = turns + later;
+      const int s = at.k.s, mine = turns + later;
       // (a new span's queries come after the last P, so their wait is last)
       // One stream's PV and QK go out together, the streams in turn: mixed,
       // both would wait for both, and their softmaxes would run at the same
       // time, the tensor cores idle.
       if (mine > 0 && !(go = warp_wait(S, a, &S.order, (mine - 1) & 1))) break;
       // Not before the turn: it says that the stage's last tile has landed (Ring).
-      if (w.stages < Ring<kFp8>::kShort && !two && pend && !(go = flush())) break;
-      if (!(go = warp_wait(S, a, &S.kv_full[s], k.phase))) break;
+      if (w.stages < Ring<kFp8>::kShort && pend && !(go = flush())) break;
+      if (!(go = warp_wait(S, a, &S.kv_full[s], at.k.phase))) break;
       if (pend && !(go = pv_first())) break;
       if (!turned && !(go = queries(two))) break;
       turned = true;
@@ -471,7 +495,7 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
       __syncwarp();
       if (pend) ++np;
       pend = true;
-      pend_v = k.next(w.stages);
+      pend_v = at.v;
       pend_steps = (min(kT, w.sp.len - (w.tile + t) * kT) + kStep - 1) / kStep;
       pend_first = first;
       pend_two = two;
@@ -628,7 +652,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
   const uint32_t s_tmem = tmem + q * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t o_tmem = s_tmem + 256;
   int ns = 0;              // tiles of this stream so far
-  RingPos k = {0, 0};      // the next tile's K
+  KvPos at(w.left, w.stages, w.ahead);
   int nspan = 0;           // spans of the CTA so far
   int np0 = 0, np1 = 0;    // tiles tidied by each stream so far
   float m = 0.f, l = 0.f;  // the row's maximum; this half's sum
@@ -712,7 +736,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
       some = false;
     }
     ++nspan;
-    for (int t = 0; t < w.tiles; ++t, k.on(2, w.stages), turn ^= !two) {
+    for (int t = 0; t < w.tiles; ++t, at.next(), turn ^= !two) {
       const int valid = min(kT, w.sp.len - (w.tile + t) * kT);
       const int owner = two ? 0 : turn;  // who tidies the V tile, where that is needed
       const bool tidy = w.sp.partial || (valid & (kStep - 1));
@@ -724,7 +748,7 @@ __device__ void softmax(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Walk 
       bool bad = false;
       if (tidy) {
         const int np = owner ? np1 : np0, par = np & 1;
-        const RingPos v = k.next(w.stages);
+        const RingPos v = at.v;
         if (q == owner) {
           // 0 * NaN would poison a sum.  V rows past the span, up to the end
           // of the last step of tokens, may hold anything: cleared.  In a
@@ -895,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   Walk w = {a, hdr.streams, c.head, c.group, c.span, c.tile, c.n_units, c.g, c.sp, 0,
-            Ring<kFp8>::kStages + (c.wide ? 0 : Ring<kFp8>::kMore), smem_u32(c.wide ? S.kv[0] : S.q[1])};
+            Ring<kFp8>::kStages + (c.wide ? 0 : Ring<kFp8>::kMore), !kFp8 && !c.wide, smem_u32(c.wide ? S.kv[0] : S.q[1])};
   w.begin();
   if (tid == 0) {
     for (int s = 0; s < TcSmem<kFp8>::kAll; ++s) {
