@@ -13,12 +13,15 @@
 //              row names twice, twice), then its rows' trees.  From span to
 //              span only the queries' rotation changes; the softmax goes on.
 //   unit     = one tile of `tile` tokens of a span for one kv head; units are
-//              ordered by kv head, group, span and tile, on a weighted line:
+//              ordered by kv head, group, span and tile, on a weighted line,
+//              first those of the groups with over 128 columns, which need a
+//              CTA's shared memory laid out otherwise (n_wide groups; they come
+//              first by number as well), then the others'; no CTA has both:
 //              a tile weighs tile1 or tile2 (over 128 columns), the first tile
 //              of a span `span` more (a tree's `tree` more still), that of a
 //              group `group` more.  CTA
-//              c of C takes the units that start in [c W / C, (c + 1) W / C);
-//              shares without a unit get no CTA.
+//              c of C takes the units that start in [c W / C, (c + 1) W / C) of
+//              its kind's part; shares without a unit get no CTA.
 //   record   = what a CTA leaves for (kv head, group): per column the running
 //              maximum m and sum l of the softmax (log2 domain) and the
 //              unnormalised output.  The records of one (kv head, group) lie
@@ -54,7 +57,8 @@ struct TreeHeader {
   int32_t n_groups;  // per kv head
   int32_t n_ctas;    // CTAs with units (0: nothing to attend)
   int32_t streams;   // records that a CTA leaves of a group with up to 128 columns
-  int32_t n_col_blocks, pad;  // entries of the merge's table: (group, first column) of 32 columns
+  int32_t n_col_blocks;  // entries of the merge's table: (group, first column) of 32 columns
+  int32_t n_wide;        // groups with over 128 columns (per kv head; the first ones)
   int64_t capacity;
   double rope_theta;  // of the rotations that the plan holds
 };
@@ -79,7 +83,7 @@ struct TreeColumn {
 };
 struct TreeCta {
   int32_t head, group, span, tile, n_units;  // first unit and count
-  int32_t wide;                              // one of its groups has over 128 columns
+  int32_t wide;                              // its groups have over 128 columns (all or none)
   TreeGroup g;                               // copies: one load instead of three in a row
   TreeSpan sp;
 };
@@ -159,6 +163,16 @@ __device__ __forceinline__ int64_t record_at(int64_t rec, int n_cols, int col, i
 template <typename T>
 __device__ __forceinline__ T *tree_at(const TreeArgs &a, size_t off) {
   return reinterpret_cast<T *>(a.ws + off);
+}
+// The group behind one on the unit line; head may come to n_kv_heads behind the last.
+__device__ __forceinline__ void next_group(const TreeHeader &h, int &head, int &group) {
+  if (++group == h.n_wide) {
+    group = 0;
+    if (++head == h.n_kv_heads && h.n_wide < h.n_groups) head = 0, group = h.n_wide;
+  } else if (group == h.n_groups) {
+    group = h.n_wide;
+    ++head;
+  }
 }
 // The plan in the workspace is one of this description.
 __device__ __forceinline__ bool tree_plan_ok(const TreeArgs &a) {

@@ -19,18 +19,18 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 // Weights of the unit line, measured on the tensor-core kernel (a fit of its
 // CTAs' times, then tried out) in steps of about 420 clocks: a tile against up
 // to 128 columns and against more, what a span's new queries and empty pipeline
-// cost beside its tiles, a tree's more of that, a group's records.  (Against
-// one weight for both kinds of tiles, with 1.5 to 2 tiles a span and a group:
-// 4 trees of 16 nodes 41.5 us instead of 48, a ragged batch 159 instead of
-// 173.)  On the CUDA cores tiles outweigh the rest.  Where every unit can have
-// a CTA of its own, each does: the units then weigh the same.
+// cost beside its tiles, a tree's more of that, a group's records.  (For bf16
+// tile2 7, 8, 9: 4 trees of 16 nodes over 16K 47.1, 45.6, 43.2 us; group 22 and
+// 16: a ragged batch, over five seeds, 160 and 156 us.)  On the CUDA cores tiles
+// outweigh the rest.  Where every unit can have a CTA of its own, each does:
+// the units then weigh the same.
 struct TreeCost {
   int32_t tile1, tile2, span, tree, group;
 };
 __device__ inline TreeCost tree_cost(int cols, bool e4m3, bool alone) {
   if (alone) return TreeCost{1, 1, 0, 0, 0};
   if (cols <= 128) return TreeCost{4, 4, 1, 0, 1};
-  return e4m3 ? TreeCost{6, 13, 27, 4, 8} : TreeCost{4, 7, 17, 8, 22};
+  return e4m3 ? TreeCost{6, 12, 27, 0, 8} : TreeCost{4, 9, 17, 8, 16};
 }
 
 struct TreePlanSmem {
@@ -214,6 +214,30 @@ __device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
   S.n_groups = n;
 }
 
+// The groups with over 128 columns ahead of the others, each in order; returns
+// their number.  By all threads (S.carry is 0 before and after).
+__device__ int wide_first(const TreeArgs &a, TreePlanSmem &S, int n) {
+  TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
+  TreeGroup *sorted = tree_at<TreeGroup>(a, a.L.o);  // (room for records, which this step has none of yet)
+  int n_wide = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int g0 = 0; g0 < n; g0 += kPlanThreads) {
+      const int g = g0 + threadIdx.x;
+      const bool wide = g < n && groups[g].n_cols > 128;
+      const int at = static_cast<int>(block_scan(S, wide));
+      if (pass == 1 && g < n) sorted[wide ? at : n_wide + g - at] = groups[g];
+    }
+    n_wide = static_cast<int>(S.carry);
+    __syncthreads();
+    if (threadIdx.x == 0) S.carry = 0;
+    __syncthreads();
+    if (n_wide == 0 || n_wide == n) return n_wide;
+  }
+  for (int g = threadIdx.x; g < n; g += kPlanThreads) groups[g] = sorted[g];
+  __syncthreads();
+  return n_wide;
+}
+
 // A group's spans, by one warp; its number of tiles goes to ubase.
 __device__ void plan_spans(const TreeArgs &a, TreePlanSmem &S, int gi, int64_t *ubase, int lane) {
   const int V = a.n_view, TL = a.L.tile, warp = threadIdx.x >> 5;
@@ -384,7 +408,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   if (tid == 0) plan_groups(a, S);
   __syncthreads();
-  const int n_groups = S.n_groups;
+  const int n_groups = S.n_groups, n_wide = a.L.cols > 128 ? wide_first(a, S, n_groups) : 0;
   int64_t *wbase = tree_at<int64_t>(a, a.L.wbase), *ubase = wbase + a.L.max_groups;
   for (int g = warp; g < n_groups; g += kPlanWarps) plan_spans(a, S, g, ubase, lane);
   __syncthreads();
@@ -411,19 +435,46 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   if (tid == 0) S.carry = 0;
   __syncthreads();
+  // a kv head's wide groups: their weight and units
+  const int64_t WW = n_wide < n_groups ? wbase[n_wide] : WH, UW = n_wide < n_groups ? ubase[n_wide] : UH;
+  const auto weight_before = [&](int h, int g) {  // on the line
+    return g < n_wide ? h * WW + wbase[g] : (a.n_kv_heads - 1 - h) * WW + h * WH + wbase[g];
+  };
+  const auto units_before = [&](int h, int g) {
+    return g < n_wide ? h * UW + ubase[g] : (a.n_kv_heads - 1 - h) * UW + h * UH + ubase[g];
+  };
   const int C = static_cast<int>(U < a.L.ctas_max ? U : a.L.ctas_max);
+  TreeHeader line = {};  // what next_group() needs of the header to come
+  line.n_groups = n_groups;
+  line.n_wide = n_wide;
+  line.n_kv_heads = a.n_kv_heads;
+  // No CTA has both wide and other groups: each kind gets its share of the CTAs,
+  // rounded to the side that leaves the less work to the busiest one.
+  const int64_t WT = WW * a.n_kv_heads;  // the wide groups' part of the line
+  int CW = n_wide == n_groups ? C : 0;
+  if (n_wide > 0 && n_wide < n_groups) {
+    const auto most = [&](int cw) { return max(static_cast<double>(WT) / cw, static_cast<double>(W - WT) / (C - cw)); };
+    CW = static_cast<int>(min(max(C * WT / W, int64_t{1}), static_cast<int64_t>(C - 1)));
+    if (CW + 1 < C && most(CW + 1) < most(CW)) ++CW;
+  }
+  const auto cta_from = [&](int c) { return c >= C ? W : c < CW ? c * WT / CW : WT + (c - CW) * (W - WT) / (C - CW); };
+  const auto cta_of = [&](int64_t w) {
+    return w < WT ? cta_of_weight(w, WT, CW) : CW + cta_of_weight(w - WT, W - WT, C - CW);
+  };
   // every CTA's first unit
   TreeCta *ctas = tree_at<TreeCta>(a, a.L.ctas);
   TreeCta first = {};
   for (int c = tid; c <= C && C > 0; c += kPlanThreads) {  // (C < kPlanThreads: once each)
-    const int64_t lo = c * W / C;
-    int h = static_cast<int>(lo / WH);
-    if (h >= a.n_kv_heads) {
-      S.uidx[c] = UH * a.n_kv_heads;
+    const int64_t lo = cta_from(c);
+    if (lo >= W) {
+      S.uidx[c] = U;
       continue;
     }
-    const int64_t rem = lo - h * WH;
-    int g = 0, hi = n_groups;
+    const bool in_wide = lo < WT;
+    const int64_t from = in_wide ? lo : lo - WT, per = in_wide ? WW : WH - WW;
+    int h = static_cast<int>(from / per);
+    const int64_t rem = from - h * per + (in_wide ? 0 : WW);
+    int g = in_wide ? 0 : n_wide, hi = in_wide ? n_wide : n_groups;
     while (hi - g > 1) {  // the last group that starts at or before rem
       const int mid = (g + hi) >> 1;
       if (wbase[mid] <= rem) g = mid; else hi = mid;
@@ -444,13 +495,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       t = 0;
       if (++s == gr.n_spans) {
         s = 0;
-        if (++g == n_groups) {
-          g = 0;
-          ++h;
-        }
+        next_group(line, h, g);
       }
     }
-    S.uidx[c] = h < a.n_kv_heads ? h * UH + ubase[g] + spans[groups[g].span0 + s].tile0 + t : UH * a.n_kv_heads;
+    S.uidx[c] = h < a.n_kv_heads ? units_before(h, g) + spans[groups[g].span0 + s].tile0 + t : U;
     first.head = h;
     first.group = g;
     first.span = s;
@@ -463,13 +511,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   const int n_ctas = static_cast<int>(S.carry);
   if (n_units > 0) {
     first.n_units = n_units;
-    first.wide = 0;
-    int h = first.head, g = first.group;
-    for (int64_t u = S.uidx[tid]; u < S.uidx[tid + 1];) {  // its groups
-      first.wide |= groups[g].n_cols > 128;
-      u = h * UH + (g + 1 < n_groups ? ubase[g + 1] : UH);
-      if (++g == n_groups) g = 0, ++h;
-    }
+    first.wide = first.group < n_wide;
     first.g = groups[first.group];
     first.sp = spans[first.g.span0 + first.span];
     ctas[number] = first;
@@ -503,13 +545,13 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       const int g = static_cast<int>(k % n_groups);
       const TreeGroup gr = groups[g];
       const TreeSpan last = spans[gr.span0 + gr.n_spans - 1];
-      const int64_t w = k / n_groups * WH + wbase[g];
+      const int64_t w = weight_before(static_cast<int>(k / n_groups), g);
       const int tiles = (last.len + TL - 1) / TL;
-      pc.x = S.number[cta_of_weight(w, W, C)];
+      pc.x = S.number[cta_of(w)];
       const int ls = gr.n_spans - 1;
       int64_t end = w + span_weight(cost, gr, ls, last.tile0);  // where the group's last unit starts
       if (tiles > 1) end += span_cost(cost, gr, ls) + static_cast<int64_t>(tiles - 1) * (gr.n_cols > 128 ? cost.tile2 : cost.tile1);
-      pc.y = S.number[cta_of_weight(end, W, C)] - pc.x + 1;
+      pc.y = S.number[cta_of(end)] - pc.x + 1;
       if (streams == 2 && gr.n_cols <= 128) pc.y *= 2;
       rows = static_cast<int64_t>(pc.y) * gr.n_cols;
     }
@@ -521,7 +563,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   }
   if (tid == 0)
     hdr = TreeHeader{kTreeMagic, R, T, a.n_q_heads, a.n_kv_heads, a.head_dim, a.n_blocks, V, a.dtype,
-                     n_groups, n_ctas, streams, n_col_blocks, 0, a.capacity, a.rope_theta};
+                     n_groups, n_ctas, streams, n_col_blocks, n_wide, a.capacity, a.rope_theta};
 }
 
 // cos and sin of a position's angle for one pair: the angle in turns is exact in 64-bit integers (rope_cos_sin); here

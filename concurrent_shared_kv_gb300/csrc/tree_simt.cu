@@ -235,10 +235,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     }
     __syncthreads();
     at.span = at.tile = 0;
-    if (++at.group == hdr.n_groups) {
-      at.group = 0;
-      ++at.head;
-    }
+    next_group(hdr, at.head, at.group);
   }
 }
 

@@ -76,13 +76,11 @@ struct Ring {
   // A wait for a stage's next tile can be told from its last one only if that
   // has landed.  A stream that has waited for turn m - 1 of the other one knows
   // that the V tiles of that one's turns up to m - 3 have landed, and those of
-  // its own up to m - 4.  Five stages before the K of tile t is the V of tile
-  // t - 3, its turn at least three before tile t's.  Three stages before it is
-  // the V of tile t - 2: known where both streams take every tile, but where
-  // they take turns that is the one whose products this stream has still to
-  // issue; they go first then (kShort), as the K can only come after them.
-  static constexpr int kShort = 5;  // rings of fewer stages
-  static_assert(kStages == 3 || kStages >= kShort, "the barriers' phases");
+  // its own up to m - 4.  Three stages before the K of tile t is the V of tile
+  // t - 2, its turns at least three and four before tile t's where both streams
+  // take every tile, as they do wherever the ring has fewer stages than five;
+  // five before it, in the order of KvPos, that of tile t - 4, four turns back.
+  static_assert(kStages >= 3 && kStages + kMore >= 5, "the barriers' phases");
 };
 // A place in a ring of n stages.
 struct RingPos {
@@ -306,10 +304,7 @@ struct Walk {
     const bool other = ++span == g.n_spans;
     if (other) {
       span = 0;
-      if (++group == tree_at<TreeHeader>(a, a.L.hdr)->n_groups) {
-        group = 0;
-        ++head;
-      }
+      next_group(*tree_at<const TreeHeader>(a, a.L.hdr), head, group);
       g = tree_at<TreeGroup>(a, a.L.groups)[group];
     }
     load_span();
@@ -470,7 +465,9 @@ __device__ void mma_issuer(const TreeArgs &a, TcSmem<kFp8> &S, uint32_t tmem, Wa
       // time, the tensor cores idle.
       if (mine > 0 && !(go = warp_wait(S, a, &S.order, (mine - 1) & 1))) break;
       // Not before the turn: it says that the stage's last tile has landed (Ring).
-      if (w.stages < Ring<kFp8>::kShort && pend && !(go = flush())) break;
+      // (With three stages the next K comes into the place of the V before the
+      // pending one: the pending products do not wait for it.)
+      if (w.stages < 5 && pend && !(go = flush())) break;
       if (!(go = warp_wait(S, a, &S.kv_full[s], at.k.phase))) break;
       if (pend && !(go = pv_first())) break;
       if (!turned && !(go = queries(two))) break;
