@@ -39,7 +39,7 @@ struct TreePlanSmem {
   int64_t carry;
   int64_t uidx[1025];
   int16_t number[kPlanThreads];  // of every share with units
-  int32_t ok, n_groups, n_spans, n_map, n_live;
+  int32_t ok, n_groups, n_wide, n_spans, n_map;
   union {
     uint8_t parent[kPlanWarps][kMaxNodes];
     uint8_t count[kPlanWarps][HW_MAX_BLOCKS];  // of a group: the most often a row names the block
@@ -181,9 +181,14 @@ __device__ __forceinline__ int entry_rank(const TreePlanSmem &S, int e0, int v, 
 __device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
   const int R = a.n_rows, V = a.n_view, G = a.n_q_heads / a.n_kv_heads, CG = a.L.cols;
   TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
-  int col = 0, rank = 0, rot = 0, n = 0;
+  int col = 0, rank = 0, rot = 0, n = 0, n_wide = 0;
   TreeGroup g = {};
   g.n_cols = CG;
+  const auto done = [&] {
+    if (n == 0) return;
+    groups[n - 1] = g;
+    n_wide += g.n_cols > 128;
+  };
   for (int r = 0; r < R; ++r) {
     const int nodes = S.nodes[r];
     tree_at<int32_t>(a, a.L.col)[r] = col;
@@ -191,12 +196,12 @@ __device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
     tree_at<int32_t>(a, a.L.rot0)[r] = rot;
     if (nodes == 0) continue;
     if (S.apart[r]) {
-      if (n > 0) groups[n - 1] = g;
+      done();
       g.n_cols = CG;
     }
     for (int left = nodes * G; left > 0;) {
       if (g.n_cols == CG) {
-        if (n > 0 && !(S.apart[r] && left == nodes * G)) groups[n - 1] = g;
+        if (!(S.apart[r] && left == nodes * G)) done();
         g = TreeGroup{r, r, rank, 0, col, 0, 0, 0};
         ++n;
       }
@@ -210,32 +215,27 @@ __device__ void plan_groups(const TreeArgs &a, TreePlanSmem &S) {
     ++rank;
     rot += nodes * (V + 1);
   }
-  if (n > 0) groups[n - 1] = g;
+  done();
   S.n_groups = n;
+  S.n_wide = n_wide;
 }
 
-// The groups with over 128 columns ahead of the others, each in order; returns
-// their number.  By all threads (S.carry is 0 before and after).
-__device__ int wide_first(const TreeArgs &a, TreePlanSmem &S, int n) {
+// The n_wide groups with over 128 columns ahead of the others, each in order.
+// By all threads (S.carry is 0 before and after).
+__device__ void wide_first(const TreeArgs &a, TreePlanSmem &S, int n, int n_wide) {
+  if (n_wide == 0 || n_wide == n) return;
   TreeGroup *groups = tree_at<TreeGroup>(a, a.L.groups);
   TreeGroup *sorted = tree_at<TreeGroup>(a, a.L.o);  // (room for records, which this step has none of yet)
-  int n_wide = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int g0 = 0; g0 < n; g0 += kPlanThreads) {
-      const int g = g0 + threadIdx.x;
-      const bool wide = g < n && groups[g].n_cols > 128;
-      const int at = static_cast<int>(block_scan(S, wide));
-      if (pass == 1 && g < n) sorted[wide ? at : n_wide + g - at] = groups[g];
-    }
-    n_wide = static_cast<int>(S.carry);
-    __syncthreads();
-    if (threadIdx.x == 0) S.carry = 0;
-    __syncthreads();
-    if (n_wide == 0 || n_wide == n) return n_wide;
+  for (int g0 = 0; g0 < n; g0 += kPlanThreads) {
+    const int g = g0 + threadIdx.x;
+    const TreeGroup own = g < n ? groups[g] : TreeGroup{};
+    const int at = static_cast<int>(block_scan(S, own.n_cols > 128));
+    if (g < n) sorted[own.n_cols > 128 ? at : n_wide + g - at] = own;
   }
+  if (threadIdx.x == 0) S.carry = 0;
+  __syncthreads();
   for (int g = threadIdx.x; g < n; g += kPlanThreads) groups[g] = sorted[g];
   __syncthreads();
-  return n_wide;
 }
 
 // A group's spans, by one warp; its number of tiles goes to ubase.
@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   __syncthreads();
   if (tid == 0) plan_groups(a, S);
   __syncthreads();
-  const int n_groups = S.n_groups, n_wide = a.L.cols > 128 ? wide_first(a, S, n_groups) : 0;
+  const int n_groups = S.n_groups, n_wide = S.n_wide;
+  wide_first(a, S, n_groups, n_wide);
   int64_t *wbase = tree_at<int64_t>(a, a.L.wbase), *ubase = wbase + a.L.max_groups;
   for (int g = warp; g < n_groups; g += kPlanWarps) plan_spans(a, S, g, ubase, lane);
   __syncthreads();
@@ -453,9 +454,9 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   const int64_t WT = WW * a.n_kv_heads;  // the wide groups' part of the line
   int CW = n_wide == n_groups ? C : 0;
   if (n_wide > 0 && n_wide < n_groups) {
-    const auto most = [&](int cw) { return max(static_cast<double>(WT) / cw, static_cast<double>(W - WT) / (C - cw)); };
     CW = static_cast<int>(min(max(C * WT / W, int64_t{1}), static_cast<int64_t>(C - 1)));
-    if (CW + 1 < C && most(CW + 1) < most(CW)) ++CW;
+    // (rounded down a wide one has the most, WT / CW; rounded up another, (W - WT) / (C - CW - 1))
+    if ((W - WT) * CW < WT * (C - CW - 1)) ++CW;
   }
   const auto cta_from = [&](int c) { return c >= C ? W : c < CW ? c * WT / CW : WT + (c - CW) * (W - WT) / (C - CW); };
   const auto cta_of = [&](int64_t w) {

@@ -235,7 +235,10 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     }
     __syncthreads();
     at.span = at.tile = 0;
-    next_group(hdr, at.head, at.group);
+    if (++at.group == hdr.n_groups) {  // (no group is wide here)
+      at.group = 0;
+      ++at.head;
+    }
   }
 }
 
