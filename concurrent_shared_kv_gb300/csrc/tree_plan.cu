@@ -328,7 +328,7 @@ __device__ __forceinline__ int span_cost(const TreeCost &c, const TreeGroup &g, 
   return c.span + (s == 0 ? c.group : 0) + (s >= g.n_spans - g.n_rows ? c.tree : 0);
 }
 
-// The plan but for its tables, by one CTA.  (With the tables 23 to 33 us, once
+// The plan but for its tables, by one CTA.  (With the tables 23 to 35 us, once
 // a step: trips to L2 and barriers, not work.)
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_constant__ TreeArgs a,
                                                                  const __grid_constant__ TreeMeta m) {
@@ -813,7 +813,7 @@ __device__ bool path_ok(const int32_t *path, int n, int nodes) {
 
 // The accepted path of each row moved behind its block, bit for bit:
 //   K[l][h][end + j] = K[l][h][slot + path[j]],  V alike,  j < n_path.
-// (64 layers of 4 rows: 6.6 us, the call's own time on the host; 36 layers of
+// (64 layers of 4 rows: 6.5 to 7.5 us, the call's own time on the host; 36 layers of
 // 64 rows of E4M3 codes: 16 us, 4.1 TB/s of 128-byte pieces.)
 // A warp moves one (layer, head, pool) line of one row in steps of ascending
 // j: a destination never lies behind its own source (path[j] >= j, and the

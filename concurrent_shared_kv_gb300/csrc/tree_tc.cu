@@ -17,14 +17,17 @@
 // another (S and P share their columns: TMEM holds no third score tile), so
 // what counts is the length of that chain.  Two threads share a row, 64 tokens
 // each, and exchange their maxima.
-// What bounds it: a tile of 128 tokens against 256 columns needs 2048 clocks of
-// the tensor cores and takes 2900; against 128 columns 1024 and 1700 (the
-// chain), of which the DRAM needs 2400 where every tile is new.  A new span
-// costs 6000: its queries are loaded, turned and written while the tensor
-// cores wait.  Measured, a layer with its writes and merge: 4 trees of 64
-// nodes over 16K tokens (40/8 heads) 93 us, 995 TFLOP/s; of 16 nodes 39.5 us;
-// 8 x 4 ragged trees of 8 nodes over up to 32K tokens 157 us, 4.6 TB/s;
-// E4M3, 4 trees of 24 nodes over 32K tokens (32/8 heads) 65 us, 860 TFLOP/s.
+// What bounds it: a tile of 128 tokens against 256 columns needs 3072 clocks of
+// the tensor cores (QK over both parts of Q~; E4M3 2048) and takes about 3800:
+// the chain, and a ring of three stages beside two query tiles of two parts.
+// Against 128 columns it is 1536 and about 1700, of which the DRAM needs 2400
+// where every tile is new.  A new span costs 6000 or more: its queries are
+// loaded, turned and written while the tensor cores wait.  Measured, a layer
+// with its writes and merge: 4 trees of 64 nodes over 16K tokens (40/8 heads)
+// 117 us, the tensor cores busy for 68 %; of 16 nodes 43 us; 8 x 4 ragged trees
+// of 8 nodes over up to 32K tokens 141 to 157 us, 4.6 to 5.2 TB/s; E4M3, 4 trees
+// of 24 nodes over 32K tokens (32/8 heads) 65 us.  (With Q~ in one part, half
+// the QK products and five stages: 93, 39.6 and 139 to 163 us.)
 // Warps: 0-7 softmax of stream 0 (0-3 tokens 0-63, 4-7 the others), 8-15 of
 // stream 1, 16 the TMA producer, 17 and 18 the issuers.
 // Rotated queries carry scale * log2(e), so scores leave the MMA in log2

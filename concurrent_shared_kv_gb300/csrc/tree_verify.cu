@@ -25,9 +25,9 @@
 // else needs single values: every drafted token's p and q are fetched at
 // once, so a path of any depth waits for memory once.
 // Bound by latency: a launch, a cluster barrier a rejection, two trips to
-// memory.  4 rows of 16 nodes over 131072 fp32 values 11 us (0.6 us of bytes),
-// 64 rows of 8 nodes in bf16 22 us (5 us: two waves of clusters), 64 chosen
-// nodes over 50021 values 9 us.
+// memory.  4 rows of 16 nodes over 131072 fp32 values 11.6 to 13.8 us, by the
+// rejections there are (0.6 us of bytes), 64 rows of 8 nodes in bf16 24.6 to
+// 26.3 us (5 us: two waves of clusters), 64 chosen nodes over 50021 values 9.5 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -611,7 +611,8 @@ cudaError_t launch(const TreeVerifyArgs &a, cudaStream_t s) {
   // Sixteen CTAs a row while all rows' run at once, two on an SM (4 rows of
   // 131072 fp32: 11.0 us, with eight a tenth more), else eight (64 rows in
   // bf16: 22.8 us in two waves; with four 28.0 in one, and with CTAs of 256
-  // threads, sixteen a row and all rows at once, 24.3).
+  // threads, sixteen a row and all rows at once, 24.3; all measured with sums of
+  // 43 bits, which took 0.4 to 2 us less).
   return a.n_rows * 16 <= 2 * device_sm_count() ? launch<T, 16>(a, s) : launch<T, 8>(a, s);
 }
 }  // namespace

@@ -358,6 +358,10 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
  * they hold.  Keys and values that are not finite touch only the
  * nodes that attend them.
  *
+ * Rows that share blocks and stand next to one another (a problem's workers)
+ * are attended together and read those blocks once; other orders of the rows
+ * give the same results, but read a shared block once for every run of such rows.
+ *
  * The trees' tokens lie outside every block and one another.  A row whose
  * tree does not (or leaves the pool) sets HW_DEV_BAD_RANGE, one whose counts
  * or parents are not a tree's HW_DEV_BAD_TREE, one without a block

@@ -935,9 +935,8 @@ def test_groups_of_odd_numbers_of_tiles(dtype, T, seed):
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 @pytest.mark.parametrize("seed", [83, 84])
 def test_narrow_groups_in_ctas_with_a_wide_one(dtype, seed):
-    """The short ring of a CTA that has a group of over 128 queries, run
-    through by groups of few queries with many tiles: every stage is used
-    again and again by either stream."""
+    """Groups of over 128 queries and groups of few with many tiles, row by
+    row: every stage of either ring is used again and again."""
     rng = np.random.Generator(np.random.PCG64(seed))
     R = 12
     lens = [int(x) for x in rng.choice([20, 2100, 5000, 9001], R)]
