@@ -33,10 +33,12 @@
 // Rotated queries carry scale * log2(e), so scores leave the MMA in log2
 // units.  They are held as two bf16 parts, hi and what that leaves, as the
 // decode holds them: a score keeps 16 bits, and QK runs over both.  P is rounded
-// to bf16 once, against sums of weights in fp32.  Outputs are measured 0.0015 to
-// 0.0016 off the exact result in the 2-norm, which is the output's own rounding.
-// (With queries rounded to bf16 once it was 0.0033, and more for larger scores:
-// the error of a score grows with it, that of a weight does not.)
+// to bf16 once, as the decode's is, against sums of weights in fp32.  Outputs
+// are measured 0.0015 to 0.0016 off the exact result in the 2-norm, which is the
+// output's own rounding; 0.0024 where 60000 tokens of unlike values share the
+// weight, P's rounding beside it.  (With queries rounded to bf16 once it was
+// 0.0033, and more for larger scores: the error of a score grows with it, that of
+// a weight does not.)
 //
 // E4M3 caches: both products run as kind::f8f6f4 on the codes, at twice the
 // rate, with Q~ and P each as two E4M3 parts x = hi + lo, lo the rounded
