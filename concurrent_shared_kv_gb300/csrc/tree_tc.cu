@@ -17,8 +17,8 @@
 // another (S and P share their columns: TMEM holds no third score tile), so
 // what counts is the length of that chain.  Two threads share a row, 64 tokens
 // each, and exchange their maxima.
-// What bounds it: a tile of 128 tokens against 256 columns needs 3072 clocks of
-// the tensor cores (QK over both parts of Q~; E4M3 2048) and takes about 3800:
+// What bounds it: a tile of 128 tokens against 256 columns needs 3100 clocks of
+// the tensor cores (QK over both parts of Q~; E4M3 2100) and takes about 3800:
 // the chain, and a ring of three stages beside two query tiles of two parts.
 // Against 128 columns it is 1536 and about 1700, of which the DRAM needs 2400
 // where every tile is new.  A new span costs 6000 or more: its queries are
