@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libhogwild.so")
 
 HW_OK = 0
-HW_F32, HW_BF16, HW_FP8_E4M3 = 0, 1, 2
+HW_F32, HW_BF16, HW_FP8_E4M3, HW_FP4_E2M1 = 0, 1, 2, 3
 HW_DESC_VIEW_LIMITS = 1
 HW_DESC_EARLY_LOADS = 2
 STATUS = {0: "HW_OK", -1: "HW_ERR_INVALID", -2: "HW_ERR_UNSUPPORTED", -3: "HW_ERR_WORKSPACE",
@@ -35,12 +35,15 @@ EXPORTS = ["hw_attn_decode_workspace_size", "hw_workspace_init", "hw_attn_decode
            "hw_views", "hw_views_chunked", "hw_last_cuda_error", "hw_status_string",
            "hw_test_set_merge_wait_limit", "hw_noalloc_status", "hw_trace_read", "hw_trace_clear",
            "hw_attn_tree_workspace_size", "hw_attn_plan_tree", "hw_attn_decode_tree",
-           "hw_attn_decode_tree_fp8", "hw_tree_verify", "hw_tree_commit"]
+           "hw_attn_decode_tree_fp8", "hw_tree_verify", "hw_tree_commit",
+           "hw_cache_write", "hw_cache_read",
+           "hw_block_commit_many_fp4", "hw_block_move", "hw_compact_moves"]
 HW_LAYOUT_COMBINED, HW_LAYOUT_INTERLEAVED, HW_LAYOUT_CONTIGUOUS = 0, 1, 2
 LAYOUTS = {"combined": HW_LAYOUT_COMBINED, "interleaved": HW_LAYOUT_INTERLEAVED,
            "contiguous": HW_LAYOUT_CONTIGUOUS}
 HW_MAX_COMMITS = 64
 HW_MAX_TREE_NODES = 128
+HW_MAX_MOVES = 256
 
 
 class HwError(RuntimeError):
@@ -114,6 +117,12 @@ def lib(path: Optional[str] = None):
     L.hw_tree_commit.argtypes = tree + [ctypes.c_int32] + [_P] * 5 + [ctypes.c_size_t, _P]
     L.hw_tree_verify.argtypes = [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_int64, _P, ctypes.c_int64] + [
         _P] * 6
+    L.hw_cache_write.argtypes = [ctypes.c_int32] * 5 + [ctypes.c_double] + [_P] * 9 + [ctypes.c_int64, _P, _P]
+    L.hw_cache_read.argtypes = [ctypes.c_int32] * 5 + [_P] * 5 + [ctypes.c_int64] + [_P] * 5
+    L.hw_block_commit_many_fp4.argtypes = [ctypes.c_int32] * 3 + [ctypes.c_double] + [_P] * 3 + [
+        ctypes.c_int64] + [_P] * 3 + [ctypes.c_int64, ctypes.c_int32] + [_P] * 5
+    L.hw_block_move.argtypes = [ctypes.c_int32] * 4 + [_P] * 3 + [ctypes.c_int64, ctypes.c_int32] + [_P] * 4
+    L.hw_compact_moves.argtypes = [ctypes.c_int32] + [_P] * 3 + [ctypes.c_int64] + [_P] * 5
     L.hw_last_cuda_error.argtypes = []
     L.hw_test_set_merge_wait_limit.argtypes = [ctypes.c_int64]
     L.hw_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int32), _P]
@@ -467,6 +476,104 @@ def tree_commit(desc: AttnDesc, max_nodes: int, n_layers: int, k_cache, v_cache,
                               int(workspace_bytes), _stream(stream))
     _check("hw_tree_commit", st)
     return st
+
+
+def attn_decode_planned_fp4(desc: AttnDesc, q, k_cache, v_cache, kv_scale, out, lse, workspace,
+                            workspace_bytes: int, stream=None) -> int:
+    """hw_attn_decode_planned_fp4: one layer over E2M1 caches with a scale a
+    token, against the plan in the workspace."""
+    st = lib().hw_attn_decode_planned_fp4(ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                          _ptr(kv_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                                          int(workspace_bytes), _stream(stream))
+    _check("hw_attn_decode_planned_fp4", st)
+    return st
+
+
+def attn_append_decode_planned_fp4(desc: AttnDesc, q, k_new, v_new, k_cache, v_cache, kv_scale, out,
+                                   lse, workspace, workspace_bytes: int, stream=None) -> int:
+    """hw_attn_append_decode_planned_fp4: the layer's new tokens encoded into
+    E2M1 caches, then the layer decoded."""
+    st = lib().hw_attn_append_decode_planned_fp4(
+        ctypes.byref(desc), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+        _ptr(kv_scale), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes),
+        _stream(stream))
+    _check("hw_attn_append_decode_planned_fp4", st)
+    return st
+
+
+def cache_write(dtype: int, n_layers: int, n_tokens: int, n_kv_heads: int, head_dim: int,
+                rope_theta: float, k_new, v_new, slot, pos, k_cache, v_cache, k_scale, v_scale,
+                kv_scale, capacity: int, flags=None, stream=None) -> int:
+    """hw_cache_write: tokens into a cache, in every layer."""
+    st = lib().hw_cache_write(int(dtype), int(n_layers), int(n_tokens), int(n_kv_heads), int(head_dim),
+                              float(rope_theta), _ptr(k_new), _ptr(v_new), _ptr(slot), _ptr(pos),
+                              _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                              _ptr(kv_scale), int(capacity), _ptr(flags), _stream(stream))
+    _check("hw_cache_write", st)
+    return st
+
+
+def cache_read(dtype: int, n_layers: int, n_tokens: int, n_kv_heads: int, head_dim: int, k_cache,
+               v_cache, k_scale, v_scale, kv_scale, capacity: int, slot, k_out, v_out, flags=None,
+               stream=None) -> int:
+    """hw_cache_read: stored tokens as values."""
+    st = lib().hw_cache_read(int(dtype), int(n_layers), int(n_tokens), int(n_kv_heads), int(head_dim),
+                             _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                             _ptr(kv_scale), int(capacity), _ptr(slot), _ptr(k_out), _ptr(v_out),
+                             _ptr(flags), _stream(stream))
+    _check("hw_cache_read", st)
+    return st
+
+
+def _host_int32(what: str, *xs):
+    arrs = [np.ascontiguousarray(x, dtype=np.int32) for x in xs]
+    if any(a.shape != arrs[0].shape or a.ndim != 1 for a in arrs):
+        raise ValueError(f"{what}: sequences of different lengths")
+    return arrs
+
+
+def block_commit_many_fp4(n_layers: int, n_kv_heads: int, head_dim: int, rope_theta: float, k_src,
+                          v_src, scale_src, src_capacity: int, k_dst, v_dst, scale_dst,
+                          dst_capacity: int, src_begin, n_tokens, dst_offset, pos_delta,
+                          stream=None) -> int:
+    """hw_block_commit_many_fp4; the four per-commit sequences are host ints."""
+    arrs = _host_int32("commits", src_begin, n_tokens, dst_offset, pos_delta)
+    st = lib().hw_block_commit_many_fp4(int(n_layers), int(n_kv_heads), int(head_dim),
+                                        float(rope_theta), _ptr(k_src), _ptr(v_src),
+                                        _ptr(scale_src), int(src_capacity), _ptr(k_dst),
+                                        _ptr(v_dst), _ptr(scale_dst), int(dst_capacity),
+                                        len(arrs[0]), *[x.ctypes.data for x in arrs],
+                                        _stream(stream))
+    _check("hw_block_commit_many_fp4", st)
+    return st
+
+
+def block_move(dtype: int, n_layers: int, n_kv_heads: int, head_dim: int, k_cache, v_cache, kv_scale,
+               capacity: int, src_begin, n_tokens, dst_begin, stream=None) -> int:
+    """hw_block_move; the three per-move sequences are host ints."""
+    arrs = _host_int32("moves", src_begin, n_tokens, dst_begin)
+    st = lib().hw_block_move(int(dtype), int(n_layers), int(n_kv_heads), int(head_dim),
+                             _ptr(k_cache), _ptr(v_cache), _ptr(kv_scale), int(capacity),
+                             len(arrs[0]), *[x.ctypes.data for x in arrs], _stream(stream))
+    _check("hw_block_move", st)
+    return st
+
+
+def compact_moves(block_start, block_len, capacity: int, room=None):
+    """Host helper: (new_start, src_begin, n_tokens, dst_begin), where the blocks
+    stand once slid together and the moves that bring them there."""
+    start, length = _host_int32("blocks", block_start, block_len)
+    room = None if room is None else np.ascontiguousarray(room, dtype=np.int32)
+    if room is not None and room.shape != start.shape:
+        raise ValueError("room needs an entry a block")
+    new, src, n, dst = (np.zeros(len(start), np.int32) for _ in range(4))
+    count = ctypes.c_int32(0)
+    _check("hw_compact_moves",
+           lib().hw_compact_moves(len(start), start.ctypes.data, length.ctypes.data, _ptr(room),
+                                  int(capacity), new.ctypes.data, ctypes.addressof(count),
+                                  src.ctypes.data, n.ctypes.data, dst.ctypes.data))
+    k = count.value
+    return new, src[:k], n[:k], dst[:k]
 
 
 def status_string(st: int) -> str:

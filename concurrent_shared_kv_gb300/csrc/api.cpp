@@ -565,22 +565,30 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
 
 static_assert(kMaxCommits == HW_MAX_COMMITS, "commit table size");
 
-// Checks and launch of n commits (hw_block_commit: n = 1).
-static int commit_impl(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
-                       double rope_theta, const void *k_src, const void *v_src,
-                       int64_t src_capacity, void *k_dst, void *v_dst, int64_t dst_capacity,
-                       int32_t n, const int32_t *src_begin, const int32_t *n_tokens,
-                       const int32_t *dst_offset, const int32_t *pos_delta, void *stream) {
-  if (dtype != HW_F32 && dtype != HW_BF16 && dtype != HW_FP8_E4M3) return HW_ERR_INVALID;
+}  // extern "C"
+
+namespace hw {
+
+// The checks of n commits (hw_block_commit: n = 1) and the kernel's arguments;
+// HW_OK with n_commits 0: nothing to move.
+int commit_check(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                 double rope_theta, const void *k_src, const void *v_src, int64_t src_capacity,
+                 void *k_dst, void *v_dst, int64_t dst_capacity, int32_t n, const int32_t *src_begin,
+                 const int32_t *n_tokens, const int32_t *dst_offset, const int32_t *pos_delta,
+                 CommitArgs *args) {
+  CommitArgs &a = *args;
+  std::memset(&a, 0, sizeof a);
   if (n < 0 || n > HW_MAX_COMMITS) return HW_ERR_INVALID;
   if (n > 0 && (!src_begin || !n_tokens || !dst_offset || !pos_delta)) return HW_ERR_INVALID;
   if (n_layers < 0 || n_kv_heads <= 0 || src_capacity < 0 || dst_capacity < 0) return HW_ERR_INVALID;
   for (int c = 0; c < n; ++c)
     if (n_tokens[c] < 0 || src_begin[c] < 0 || dst_offset[c] < 0) return HW_ERR_INVALID;
   if (!(rope_theta > 1.0) || !std::isfinite(rope_theta)) return HW_ERR_INVALID;
+  // 4-bit rows: 64 bytes of codes
   const int esz = dtype == HW_F32 ? 4 : dtype == HW_FP8_E4M3 ? 1 : 2;
   const int epv = 16 / esz;
-  if (head_dim <= 0 || head_dim > 128 || head_dim % (2 * epv) != 0) return HW_ERR_UNSUPPORTED;
+  if (dtype == HW_FP4_E2M1 ? head_dim != 128 : head_dim <= 0 || head_dim > 128 || head_dim % (2 * epv) != 0)
+    return HW_ERR_UNSUPPORTED;
   int64_t tokens = 0;
   for (int c = 0; c < n; ++c) tokens += n_tokens[c];
   if (n_layers == 0 || tokens == 0) return HW_OK;
@@ -606,7 +614,7 @@ static int commit_impl(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int3
   for (int c = 0; c < n; ++c)
     for (int e = 0; e < n; ++e)
       if (!disjoint(dst_offset[c], n_tokens[c], src_begin[e], n_tokens[e])) tokens_disjoint = false;
-  const int64_t row = static_cast<int64_t>(head_dim) * esz;
+  const int64_t row = dtype == HW_FP4_E2M1 ? head_dim / 2 : static_cast<int64_t>(head_dim) * esz;
   const int64_t src_span = static_cast<int64_t>(n_layers) * n_kv_heads * src_capacity * row;
   const int64_t dst_span = static_cast<int64_t>(n_layers) * n_kv_heads * dst_capacity * row;
   auto meets = [](const void *a, int64_t na, const void *b, int64_t nb) {
@@ -622,8 +630,6 @@ static int commit_impl(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int3
   }
   if (meets(k_dst, dst_span, v_dst, dst_span)) return HW_ERR_OVERLAP;
 
-  CommitArgs a;
-  std::memset(&a, 0, sizeof a);
   a.k_src = k_src;
   a.v_src = v_src;
   a.k_dst = k_dst;
@@ -641,9 +647,26 @@ static int commit_impl(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int3
     a.delta[c] = pos_delta[c];
   }
   rope_phase_table(head_dim, rope_theta, a.phase);
+  return HW_OK;
+}
+
+static int commit_impl(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                       double rope_theta, const void *k_src, const void *v_src,
+                       int64_t src_capacity, void *k_dst, void *v_dst, int64_t dst_capacity,
+                       int32_t n, const int32_t *src_begin, const int32_t *n_tokens,
+                       const int32_t *dst_offset, const int32_t *pos_delta, void *stream) {
+  if (dtype != HW_F32 && dtype != HW_BF16 && dtype != HW_FP8_E4M3) return HW_ERR_INVALID;
+  CommitArgs a;
+  const int st = commit_check(dtype, n_layers, n_kv_heads, head_dim, rope_theta, k_src, v_src, src_capacity, k_dst,
+                              v_dst, dst_capacity, n, src_begin, n_tokens, dst_offset, pos_delta, &a);
+  if (st != HW_OK || a.n_commits == 0) return st;
   const cudaError_t e = launch_commit(a, dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HW_OK : cuda_fail(e);
 }
+
+}  // namespace hw
+
+extern "C" {
 
 int hw_block_commit(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
                     double rope_theta, const void *k_src, const void *v_src, int64_t src_capacity,

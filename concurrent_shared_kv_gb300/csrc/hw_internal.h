@@ -149,6 +149,11 @@ struct CommitArgs {
   int32_t delta[kMaxCommits];  // pos_delta
 };
 cudaError_t launch_commit(const CommitArgs &a, int dtype, cudaStream_t s);
+// The host checks of n commits, and their arguments for the kernel (api.cpp).
+int commit_check(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim, double rope_theta,
+                 const void *k_src, const void *v_src, int64_t src_capacity, void *k_dst, void *v_dst,
+                 int64_t dst_capacity, int32_t n, const int32_t *src_begin, const int32_t *n_tokens,
+                 const int32_t *dst_offset, const int32_t *pos_delta, CommitArgs *args);
 
 // Fixed-point phase table for RoPE (host): frac(theta^(-2i/D) / 2pi) * 2^64.
 void rope_phase_table(int head_dim, double theta, uint64_t *phase);

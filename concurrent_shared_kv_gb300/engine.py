@@ -21,22 +21,26 @@ class DecodeSession:
     def __init__(self, *, n_rows: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
                  n_blocks: int, max_view_blocks: int, capacity: int, dtype: torch.dtype,
                  rope_theta: float, scale: Optional[float] = None, device="cuda",
-                 view_limits: bool = False, kv_fp8: bool = False):
+                 view_limits: bool = False, kv_fp8: bool = False, kv_fp4: bool = False):
         """view_limits: the steps are planned with per-view-entry token limits
         (plan_limited; decode_planned then applies them).  kv_fp8: the K and V
         pools hold E4M3 codes with per-kv-head scales (decode_planned_fp8);
-        dtype is then that of q and out (bf16)."""
+        kv_fp4: E2M1 codes with a scale a token (decode_planned_fp4); dtype is
+        then that of q and out (bf16)."""
+        if kv_fp4 and (kv_fp8 or dtype != torch.bfloat16):
+            raise ValueError("4-bit caches: dtype bfloat16, and not kv_fp8")
         self.device = torch.device(device)
         self.dtype = dtype
+        storage = api.HW_FP4_E2M1 if kv_fp4 else api.HW_FP8_E4M3 if kv_fp8 else DTYPES[dtype]
         self.desc = api.make_desc(n_rows, n_q_heads, n_kv_heads, head_dim, n_blocks,
                                   max_view_blocks, capacity,
-                                  api.HW_FP8_E4M3 if kv_fp8 else DTYPES[dtype], rope_theta,
+                                  storage, rope_theta,
                                   head_dim ** -0.5 if scale is None else scale,
                                   flags=api.HW_DESC_VIEW_LIMITS if view_limits else 0)
         # the same description with the early-loads promise (see early= below)
         self.desc_early = api.make_desc(n_rows, n_q_heads, n_kv_heads, head_dim, n_blocks,
                                         max_view_blocks, capacity,
-                                        api.HW_FP8_E4M3 if kv_fp8 else DTYPES[dtype], rope_theta,
+                                        storage, rope_theta,
                                         head_dim ** -0.5 if scale is None else scale,
                                         flags=self.desc.flags | api.HW_DESC_EARLY_LOADS)
         self.ws_bytes = api.attn_decode_workspace_size(self.desc)
@@ -164,6 +168,53 @@ class DecodeSession:
                                            out, lse, self.workspace, self.ws_bytes, stream=stream)
         return out, lse
 
+    def _fp4_layer(self, q, k_cache, v_cache, kv_scale, out, lse, want_lse, stream, new=()):
+        """The outputs of a layer over 4-bit caches, and what a kernel would
+        read past checked."""
+        d, dev = self.desc, q.device
+        if d.dtype != api.HW_FP4_E2M1:
+            raise ValueError("the session has no 4-bit caches (kv_fp4)")
+        n, rows = d.n_rows * d.n_q_heads, d.n_kv_heads * d.cache_capacity
+        if out is None:
+            out = _new((d.n_rows, d.n_q_heads, d.head_dim), self.dtype, dev, stream)
+        if lse is None and want_lse:
+            lse = _new((d.n_rows, d.n_q_heads), torch.float32, dev, stream)
+        _fits("q", q, n * d.head_dim, self.dtype, self.workspace.device)
+        _fits("out", out, n * d.head_dim, self.dtype, dev)
+        if lse is not None:
+            _fits("lse", lse, n, torch.float32, dev)
+        _fits("k_cache", k_cache, rows * d.head_dim // 2, torch.uint8, dev)
+        _fits("v_cache", v_cache, rows * d.head_dim // 2, torch.uint8, dev)
+        _fits("kv_scale", kv_scale, rows * 2, torch.bfloat16, dev)
+        for what, x in zip(("k_new", "v_new"), new):
+            _fits(what, x, d.n_rows * d.n_kv_heads * d.head_dim, self.dtype, dev)
+        _current(dev)
+        return out, lse
+
+    def decode_planned_fp4(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           kv_scale: torch.Tensor, out: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None,
+                           early: bool = False):
+        """One layer over E2M1 pools (packed codes, uint8 [Hkv][cap][D / 2]) with
+        the tokens' scales (bfloat16 [Hkv][cap][2]: key, value)."""
+        out, lse = self._fp4_layer(q, k_cache, v_cache, kv_scale, out, lse, want_lse, stream)
+        api.attn_decode_planned_fp4(self.desc_early if early else self.desc, q, k_cache, v_cache, kv_scale,
+                                    out, lse, self.workspace, self.ws_bytes, stream=stream)
+        return out, lse
+
+    def append_decode_planned_fp4(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                                  k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  kv_scale: torch.Tensor, out: Optional[torch.Tensor] = None,
+                                  lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                                  stream=None, early: bool = False):
+        """One layer over E2M1 pools: its new tokens (bf16, [rows][Hkv][D])
+        encoded into them, then decoded."""
+        out, lse = self._fp4_layer(q, k_cache, v_cache, kv_scale, out, lse, want_lse, stream, (k_new, v_new))
+        api.attn_append_decode_planned_fp4(self.desc_early if early else self.desc, q, k_new, v_new,
+                                           k_cache, v_cache, kv_scale, out, lse, self.workspace,
+                                           self.ws_bytes, stream=stream)
+        return out, lse
+
     def device_flags(self) -> int:
         return api.workspace_status(self.workspace)
 
@@ -220,7 +271,7 @@ def _current(device) -> None:
 
 def _on_gpu(device) -> None:
     if device.type != "cuda":
-        raise ValueError(f"the tree calls need tensors on a GPU, not on {device}")
+        raise ValueError(f"the calls need tensors on a GPU, not on {device}")
     _current(device)
 
 
@@ -445,3 +496,116 @@ def block_commit_many(k_src: torch.Tensor, v_src: torch.Tensor, commits, k_dst: 
     cols = list(zip(*commits)) if commits else [(), (), (), ()]
     return api.block_commit_many(DTYPES[k_src.dtype], L, H, D, rope_theta, k_src, v_src, cs, k_dst,
                                  v_dst, cd, *cols, stream=stream)
+
+
+def _pools(k_cache, v_cache, kv_scale, what=""):
+    """(dtype, layers, Hkv, capacity, D) of a cache's pools, [layers][Hkv][cap][D]
+    or [Hkv][cap][D] (with kv_scale: packed codes, D / 2 bytes a token)."""
+    if k_cache.dim() not in (3, 4):
+        raise ValueError(f"pools are [layers][Hkv][cap][D] or [Hkv][cap][D], not {tuple(k_cache.shape)}")
+    layers = k_cache.shape[0] if k_cache.dim() == 4 else 1
+    heads, cap, width = k_cache.shape[-3:]
+    if kv_scale is not None:
+        if k_cache.dtype != torch.uint8:
+            raise ValueError("4-bit pools are bytes (torch.uint8)")
+        _fits(f"kv_scale{what}", kv_scale, layers * heads * cap * 2, torch.bfloat16, k_cache.device)
+    elif k_cache.dtype not in DTYPES:
+        raise ValueError(f"no cache of {k_cache.dtype}")
+    _fits(f"k{what or '_cache'}", k_cache, k_cache.numel(), k_cache.dtype, k_cache.device)
+    _fits(f"v{what or '_cache'}", v_cache, k_cache.numel(), k_cache.dtype, k_cache.device)
+    if k_cache.is_cuda:
+        _current(k_cache.device)
+    else:
+        _on_gpu(k_cache.device)
+    return (DTYPES[k_cache.dtype] if kv_scale is None else api.HW_FP4_E2M1, layers, heads, cap,
+            width if kv_scale is None else 2 * width)
+
+
+def _head_scales(dtype, k_scale, v_scale, n, device):
+    if dtype == api.HW_FP8_E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("8-bit caches need k_scale and v_scale (4-bit ones: kv_scale)")
+        _fits("k_scale", k_scale, n, torch.float32, device)
+        _fits("v_scale", v_scale, n, torch.float32, device)
+
+
+def cache_write(k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.Tensor, pos: torch.Tensor,
+                k_cache: torch.Tensor, v_cache: torch.Tensor, *, rope_theta: float,
+                k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                kv_scale: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None,
+                stream=None) -> None:
+    """hw_cache_write: tokens k_new, v_new ([layers][n][Hkv][D], or without the
+    layers) into the pools' tokens slot[n] (int32, -1: left out), keys rotated at
+    pos[n] (int32).  E4M3 pools with k_scale, v_scale (float32 [layers][Hkv]), E2M1
+    pools (uint8, D / 2 bytes a token) with kv_scale (bfloat16 [layers][Hkv][cap][2]).
+    flags: int32 [1], HW_DEV_BAD_RANGE is ORed in for slots outside the pool."""
+    dtype, layers, heads, cap, dim = _pools(k_cache, v_cache, kv_scale)
+    dev, n = k_cache.device, slot.numel()
+    act = torch.float32 if dtype == api.HW_F32 else torch.bfloat16
+    _fits("slot", slot, n, torch.int32, dev)
+    _fits("pos", pos, n, torch.int32, dev)
+    _fits("k_new", k_new, layers * n * heads * dim, act, dev)
+    _fits("v_new", v_new, layers * n * heads * dim, act, dev)
+    _head_scales(dtype, k_scale, v_scale, layers * heads, dev)
+    if flags is not None:
+        _fits("flags", flags, 1, torch.int32, dev)
+    api.cache_write(dtype, layers, n, heads, dim, rope_theta, k_new, v_new, slot, pos, k_cache, v_cache, k_scale,
+                    v_scale, kv_scale, cap, flags, stream=stream)
+
+
+def cache_read(slot: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *,
+               k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+               kv_scale: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+               v_out: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None, stream=None):
+    """hw_cache_read: (k_out, v_out), the values of the pools' tokens slot[n],
+    [layers][n][Hkv][D] (without the layers where the pools have none); the rows of
+    tokens left out (-1) keep what they hold.  Pools and scales as in cache_write."""
+    dtype, layers, heads, cap, dim = _pools(k_cache, v_cache, kv_scale)
+    dev, n = k_cache.device, slot.numel()
+    act = torch.float32 if dtype == api.HW_F32 else torch.bfloat16
+    shape = ((layers,) if k_cache.dim() == 4 else ()) + (n, heads, dim)
+    if k_out is None:
+        k_out = _new(shape, act, dev, stream)
+    if v_out is None:
+        v_out = _new(shape, act, dev, stream)
+    _fits("slot", slot, n, torch.int32, dev)
+    _fits("k_out", k_out, layers * n * heads * dim, act, dev)
+    _fits("v_out", v_out, layers * n * heads * dim, act, dev)
+    _head_scales(dtype, k_scale, v_scale, layers * heads, dev)
+    if flags is not None:
+        _fits("flags", flags, 1, torch.int32, dev)
+    api.cache_read(dtype, layers, n, heads, dim, k_cache, v_cache, k_scale, v_scale, kv_scale, cap, slot, k_out,
+                   v_out, flags, stream=stream)
+    return k_out, v_out
+
+
+def block_commit_fp4(k_src: torch.Tensor, v_src: torch.Tensor, scale_src: torch.Tensor,
+                     k_dst: torch.Tensor, v_dst: torch.Tensor, scale_dst: torch.Tensor, src_begin,
+                     n_tokens, dst_offset, pos_delta, *, rope_theta: float, stream=None) -> None:
+    """hw_block_commit_many_fp4: finished steps of 4-bit caches, one for each entry
+    of the four host sequences; pools [layers][Hkv][cap][D / 2] (or without the
+    layers), scales bfloat16 [layers][Hkv][cap][2]."""
+    _, layers, heads, cs, dim = _pools(k_src, v_src, scale_src, "_src")
+    _, ld, hd, cd, dd = _pools(k_dst, v_dst, scale_dst, "_dst")
+    if (layers, heads, dim) != (ld, hd, dd) or k_src.device != k_dst.device:
+        raise ValueError("the two caches differ in layers, heads, head_dim or device")
+    api.block_commit_many_fp4(layers, heads, dim, rope_theta, k_src, v_src, scale_src, cs, k_dst, v_dst, scale_dst,
+                              cd, src_begin, n_tokens, dst_offset, pos_delta, stream=stream)
+
+
+def block_move(k_cache: torch.Tensor, v_cache: torch.Tensor, src_begin, n_tokens, dst_begin, *,
+               kv_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """hw_block_move: token ranges of the pools moved one after the other (host
+    sequences), in every layer; pools as in cache_write."""
+    dtype, layers, heads, cap, dim = _pools(k_cache, v_cache, kv_scale)
+    api.block_move(dtype, layers, heads, dim, k_cache, v_cache, kv_scale, cap, src_begin, n_tokens, dst_begin,
+                   stream=stream)
+
+
+def compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_start, block_len, *, room=None,
+            kv_scale: Optional[torch.Tensor] = None, stream=None) -> np.ndarray:
+    """The pools' blocks slid together over the tokens no block holds (room[b] tokens
+    kept free behind block b): where each now starts."""
+    new, src, n, dst = api.compact_moves(block_start, block_len, k_cache.shape[-2], room)
+    block_move(k_cache, v_cache, src, n, dst, kv_scale=kv_scale, stream=stream)
+    return new

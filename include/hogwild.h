@@ -70,7 +70,23 @@ typedef enum {
  * hw_attn_plan + hw_attn_decode_planned_fp8 and committed by hw_block_commit
  * (the other decode calls return HW_ERR_UNSUPPORTED for it).
  */
-typedef enum { HW_F32 = 0, HW_BF16 = 1, HW_FP8_E4M3 = 2 } hw_dtype;
+/*
+ * HW_FP4_E2M1: the K and V pools hold E2M1 codes, [Hkv][capacity][D / 2] bytes, two
+ * to a byte with the even element in the low bits; a third array kv_scale, bf16
+ * [Hkv][capacity][2], holds a token's scale of its key and of its value: an element
+ * is level(code) * scale with the levels 0, 1/2, 1, 3/2, 2, 3, 4, 6 and a sign
+ * (code + 8).  A stored vector x has the scale bf16(max|x| / 6) and the codes of
+ * the levels nearest to x / scale (ties to the even code).  A scale below 2^-100
+ * counts as zero; a vector with an element of 2^100 or more, or not finite,
+ * gets the scale NaN: its elements are NaN.  Scales outside these bounds are not
+ * to be stored by other means.  q, k_new, v_new and out are bf16; head_dim 128;
+ * pools 16-byte, kv_scale 4-byte aligned.  Filled by hw_cache_write, decoded by
+ * hw_attn_plan (_append, _limited) + hw_attn_decode_planned_fp4 and
+ * hw_attn_append_decode_planned_fp4, committed by hw_block_commit_many_fp4,
+ * moved by hw_block_move, read by hw_cache_read (the other calls return
+ * HW_ERR_UNSUPPORTED or HW_ERR_INVALID for it).
+ */
+typedef enum { HW_F32 = 0, HW_BF16 = 1, HW_FP8_E4M3 = 2, HW_FP4_E2M1 = 3 } hw_dtype;
 
 /* Device-side error bits reported by hw_workspace_status. */
 enum {
@@ -99,6 +115,7 @@ enum {
 #define HW_MAX_TREE_NODES 128      /* nodes of a row's draft tree (max_nodes) */
 #define HW_MAX_TREE_QUERIES 65536  /* n_rows * max_nodes of the draft-tree calls */
 #define HW_MAX_VOCAB (1 << 24)     /* hw_tree_verify's vocabulary */
+#define HW_MAX_MOVES 256           /* moves of one hw_block_move */
 
 /* Host-side description of one decode call (all scalars, host memory). */
 typedef struct {
@@ -554,6 +571,100 @@ int hw_block_commit_many(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, in
                          int64_t src_capacity, void *k_dst, void *v_dst, int64_t dst_capacity,
                          int32_t n_commits, const int32_t *src_begin, const int32_t *n_tokens,
                          const int32_t *dst_offset, const int32_t *pos_delta, void *stream);
+
+/*
+ * hw_block_commit_many for HW_FP4_E2M1 caches: each key is decoded (code times
+ * scale), rotated in fp32 and encoded anew, with a scale of its own; values keep
+ * their codes and scales.  pos_delta = 0 is a bit copy.  scale_src and scale_dst:
+ * kv_scale of the pools, [n_layers][Hkv][capacity][2] (dev), the same array
+ * exactly where the pools are the same.
+ */
+int hw_block_commit_many_fp4(int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                             double rope_theta, const void *k_src, const void *v_src,
+                             const void *scale_src, int64_t src_capacity, void *k_dst, void *v_dst,
+                             void *scale_dst, int64_t dst_capacity, int32_t n_commits,
+                             const int32_t *src_begin, const int32_t *n_tokens,
+                             const int32_t *dst_offset, const int32_t *pos_delta, void *stream);
+
+/*
+ * Tokens written into a cache of any type, in n_layers layers: a prompt's into
+ * its block, or a step's.  For every token i with slot[i] >= 0, layer l and kv
+ * head h
+ *   K[l][h][slot[i]] = rho(k_new[l][i][h], pos[i])
+ *   V[l][h][slot[i]] = v_new[l][i][h]
+ * as the cache holds them: rotated in fp32 and rounded once (fp32, bf16),
+ * divided by the head's scale first (HW_FP8_E4M3, saturating at 448), or encoded with
+ * scales of their own (HW_FP4_E2M1, stored in kv_scale).  The bits are those
+ * that the append calls store for the same token.
+ *  k_new, v_new  dev [n_layers][n_tokens][Hkv][D]: fp32 for HW_F32, else bf16;
+ *                16-byte aligned
+ *  slot          dev int32 [n_tokens], the pool token; -1: left out (padding).
+ *                No two tokens may name one slot: what it then holds is made of
+ *                both
+ *  pos           dev int32 [n_tokens], its block-local position (not read for
+ *                its place: any int32)
+ *  k_cache, v_cache  dev pools [n_layers][Hkv][capacity][D] (HW_FP4_E2M1: D / 2
+ *                bytes a token), 16-byte aligned
+ *  k_scale, v_scale  dev float [n_layers][Hkv] (HW_FP8_E4M3, else ignored)
+ *  kv_scale      dev bf16 [n_layers][Hkv][capacity][2] (HW_FP4_E2M1, else ignored)
+ *  flags         dev int32 or NULL: HW_DEV_BAD_RANGE is ORed in for a slot
+ *                outside [-1, capacity); such a token is left out
+ * head_dim 64 or 128 (8 and 4 bits: 128), at most HW_MAX_Q_HEADS kv heads.
+ * Nothing but the named slots is written.
+ */
+int hw_cache_write(int32_t dtype, int32_t n_layers, int32_t n_tokens, int32_t n_kv_heads,
+                   int32_t head_dim, double rope_theta, const void *k_new, const void *v_new,
+                   const int32_t *slot, const int32_t *pos, void *k_cache, void *v_cache,
+                   const float *k_scale, const float *v_scale, void *kv_scale, int64_t capacity,
+                   int32_t *flags, void *stream);
+
+/*
+ * Stored tokens as values, e.g. to move them to a cache of another type:
+ *   k_out[l][i][h] = K[l][h][slot[i]],  v_out alike
+ * with codes times their scales (in fp32, rounded once to bf16); keys stay
+ * rotated as they stand.  Arguments as in hw_cache_write; k_out, v_out dev
+ * [n_layers][n_tokens][Hkv][D], fp32 for HW_F32, else bf16, 16-byte aligned.  The
+ * rows of a token whose slot is -1 (or, with HW_DEV_BAD_RANGE in flags, out of
+ * range) are left as they were.  One slot may be read by several tokens.
+ */
+int hw_cache_read(int32_t dtype, int32_t n_layers, int32_t n_tokens, int32_t n_kv_heads,
+                  int32_t head_dim, const void *k_cache, const void *v_cache, const float *k_scale,
+                  const float *v_scale, const void *kv_scale, int64_t capacity,
+                  const int32_t *slot, void *k_out, void *v_out, int32_t *flags, void *stream);
+
+/*
+ * Token ranges moved within a pool, bit for bit, in all layers and heads of K, V
+ * and (HW_FP4_E2M1) kv_scale:
+ *   pool[l][h][dst_begin[m] + j] = pool[l][h][src_begin[m] + j],  j < n_tokens[m]
+ * for the moves m in order, each as memmove does: ranges may overlap, and a move
+ * sees what those before it wrote.  So one call copies a block, forks it to several
+ * places (a worker split into several that go on from its step: keys stand at
+ * block-local positions, a copy needs no rotation), or slides the blocks of a pool
+ * together over the freed ones between them (hw_compact_moves).  Block starts are
+ * the caller's to update; a block is freed by no longer being named.
+ *  pools, kv_scale, head_dim as in hw_cache_write (kv_scale NULL for the other types)
+ *  src_begin, n_tokens, dst_begin  host int32 [n_moves], n_moves <= HW_MAX_MOVES
+ * HW_ERR_CAPACITY if a range leaves the pool, HW_ERR_OVERLAP if the K, V and
+ * kv_scale arrays meet.
+ */
+int hw_block_move(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                  void *k_cache, void *v_cache, void *kv_scale, int64_t capacity, int32_t n_moves,
+                  const int32_t *src_begin, const int32_t *n_tokens, const int32_t *dst_begin,
+                  void *stream);
+
+/*
+ * Host helper: the moves that slide a pool's blocks together, in the order of
+ * their starts, from token 0 on, with room[b] tokens left free behind block b (room
+ * NULL: none), for hw_block_move.  A block of length 0 holds nothing and only gets a
+ * place.  All arrays host: block_start, block_len, room [n_blocks], new_start
+ * [n_blocks] (where each block stands afterwards), src_begin, n_tokens, dst_begin
+ * [n_blocks] (the first *n_moves are written).  HW_ERR_OVERLAP if two blocks share
+ * tokens, HW_ERR_CAPACITY if a block leaves the pool or they do not fit;
+ * n_blocks <= HW_MAX_MOVES.
+ */
+int hw_compact_moves(int32_t n_blocks, const int32_t *block_start, const int32_t *block_len,
+                     const int32_t *room, int64_t capacity, int32_t *new_start, int32_t *n_moves,
+                     int32_t *src_begin, int32_t *n_tokens, int32_t *dst_begin);
 
 /*
  * Synchronises `stream`, reads and clears the device error bits of a
