@@ -36,7 +36,7 @@ EXPORTS = ["hw_attn_decode_workspace_size", "hw_workspace_init", "hw_attn_decode
            "hw_test_set_merge_wait_limit", "hw_noalloc_status", "hw_trace_read", "hw_trace_clear",
            "hw_attn_tree_workspace_size", "hw_attn_plan_tree", "hw_attn_decode_tree",
            "hw_attn_decode_tree_fp8", "hw_tree_verify", "hw_tree_commit",
-           "hw_cache_write", "hw_cache_read",
+           "hw_attn_decode_planned_fp4", "hw_attn_append_decode_planned_fp4", "hw_cache_write", "hw_cache_read",
            "hw_block_commit_many_fp4", "hw_block_move", "hw_compact_moves"]
 HW_LAYOUT_COMBINED, HW_LAYOUT_INTERLEAVED, HW_LAYOUT_CONTIGUOUS = 0, 1, 2
 LAYOUTS = {"combined": HW_LAYOUT_COMBINED, "interleaved": HW_LAYOUT_INTERLEAVED,
@@ -117,6 +117,8 @@ def lib(path: Optional[str] = None):
     L.hw_tree_commit.argtypes = tree + [ctypes.c_int32] + [_P] * 5 + [ctypes.c_size_t, _P]
     L.hw_tree_verify.argtypes = [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_int64, _P, ctypes.c_int64] + [
         _P] * 6
+    L.hw_attn_decode_planned_fp4.argtypes = [ctypes.POINTER(AttnDesc)] + [_P] * 7 + [ctypes.c_size_t, _P]
+    L.hw_attn_append_decode_planned_fp4.argtypes = [ctypes.POINTER(AttnDesc)] + [_P] * 9 + [ctypes.c_size_t, _P]
     L.hw_cache_write.argtypes = [ctypes.c_int32] * 5 + [ctypes.c_double] + [_P] * 9 + [ctypes.c_int64, _P, _P]
     L.hw_cache_read.argtypes = [ctypes.c_int32] * 5 + [_P] * 5 + [ctypes.c_int64] + [_P] * 5
     L.hw_block_commit_many_fp4.argtypes = [ctypes.c_int32] * 3 + [ctypes.c_double] + [_P] * 3 + [

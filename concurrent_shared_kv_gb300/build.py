@@ -22,7 +22,7 @@ LIB = os.path.join(BUILD, "libhogwild.so")
 BUILD_TRACE = os.path.join(PKG, "_build_trace")
 LIB_TRACE = os.path.join(BUILD_TRACE, "libhogwild_trace.so")
 
-SOURCES = ["api.cpp", "attn_decode_simt.cu", "attn_decode_tc.cu", "block_commit.cu",
+SOURCES = ["api.cpp", "attn_decode_simt.cu", "attn_decode_tc.cu", "attn_decode_fp4.cu", "block_commit.cu",
            "attn_decode_noalloc.cu", "tree_api.cpp", "tree_plan.cu", "tree_simt.cu", "tree_tc.cu", "tree_verify.cu",
            "cache_api.cpp", "cache_ops.cu", "block_move.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

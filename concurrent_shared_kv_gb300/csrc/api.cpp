@@ -104,6 +104,22 @@ bool make_pool_map(CUtensorMap *m, const void *pool, int64_t capacity, int n_kv_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// E2M1: [Hkv][capacity][64] bytes; 16 codes (8 bytes) go to 16 bytes of shared
+// memory, so a tile has the layout of E4M3's there.  The map wants the pool on a
+// 32-byte boundary.
+bool make_pool_map_fp4(CUtensorMap *m, const void *pool, int64_t capacity, int n_kv_heads) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t cap = capacity > 0 ? static_cast<cuuint64_t>(capacity) : 1;
+  cuuint64_t dims[3] = {128, cap, static_cast<cuuint64_t>(n_kv_heads)};
+  cuuint64_t strides[2] = {64, cap * 64};
+  cuuint32_t box[3] = {128u, static_cast<cuuint32_t>(kTcTile), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void *>(pool), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Upper bound on the CTAs of any decode launch: slots are sized for it.
 static int max_decode_ctas() {
   const int sms = device_sm_count();
@@ -181,11 +197,12 @@ int check_desc(const hw_attn_desc *d) {
     return HW_ERR_INVALID;
   if (d->n_q_heads <= 0 || d->n_kv_heads <= 0 || d->n_q_heads % d->n_kv_heads != 0)
     return HW_ERR_INVALID;
-  if (d->dtype != HW_F32 && d->dtype != HW_BF16 && d->dtype != HW_FP8_E4M3) return HW_ERR_INVALID;
+  if (d->dtype != HW_F32 && d->dtype != HW_BF16 && d->dtype != HW_FP8_E4M3 && d->dtype != HW_FP4_E2M1)
+    return HW_ERR_INVALID;
   if (!(d->rope_theta > 1.0) || !std::isfinite(d->rope_theta)) return HW_ERR_INVALID;
   if (!std::isfinite(d->scale)) return HW_ERR_INVALID;
   if (d->head_dim != 64 && d->head_dim != 128) return HW_ERR_UNSUPPORTED;
-  if (d->dtype == HW_FP8_E4M3 && d->head_dim != 128) return HW_ERR_UNSUPPORTED;
+  if ((d->dtype == HW_FP8_E4M3 || d->dtype == HW_FP4_E2M1) && d->head_dim != 128) return HW_ERR_UNSUPPORTED;
   if (d->n_blocks > HW_MAX_BLOCKS) return HW_ERR_UNSUPPORTED;
   if (d->n_q_heads > HW_MAX_Q_HEADS) return HW_ERR_UNSUPPORTED;
   if (d->max_view_blocks > HW_MAX_VIEW_BLOCKS) return HW_ERR_UNSUPPORTED;
@@ -194,9 +211,7 @@ int check_desc(const hw_attn_desc *d) {
   if (d->n_q_heads / d->n_kv_heads > kMaxQ) return HW_ERR_UNSUPPORTED;
   if (d->cache_capacity > INT32_MAX) return HW_ERR_UNSUPPORTED;
   if (d->flags & ~(HW_DESC_VIEW_LIMITS | HW_DESC_EARLY_LOADS)) return HW_ERR_INVALID;
-  if ((d->flags & HW_DESC_VIEW_LIMITS) &&
-      !((d->dtype == HW_BF16 || d->dtype == HW_FP8_E4M3) && d->head_dim == 128))
-    return HW_ERR_UNSUPPORTED;
+  if ((d->flags & HW_DESC_VIEW_LIMITS) && (d->dtype == HW_F32 || d->head_dim != 128)) return HW_ERR_UNSUPPORTED;
   return HW_OK;
 }
 
@@ -278,9 +293,12 @@ static void use_plan_cache(DecodeArgs &a, const WorkspaceLayout &L, void *worksp
 }
 
 static bool tensor_core_path(const hw_attn_desc *d) {
-  return (d->dtype == HW_BF16 || d->dtype == HW_FP8_E4M3) && d->head_dim == 128;
+  return d->dtype != HW_F32 && d->head_dim == 128;
 }
 static bool e4m3(const hw_attn_desc *d) { return d->dtype == HW_FP8_E4M3; }
+static bool e2m1(const hw_attn_desc *d) { return d->dtype == HW_FP4_E2M1; }
+// Caches of codes are decoded by calls of their own, which take the scales.
+static bool coded(const hw_attn_desc *d) { return e4m3(d) || e2m1(d); }
 
 // One decode launch: metadata from the caller (plan null) or from the
 // workspace copies with the step's plan.
@@ -293,13 +311,14 @@ static int decode_common(const hw_attn_desc *d, const void *q, const void *k_cac
                          const int32_t *append_pos = nullptr, const void *k_new = nullptr,
                          const void *v_new = nullptr, const int32_t *view_limit = nullptr,
                          const float *k_scale = nullptr, const float *v_scale = nullptr,
-                         bool from_cache = false) {
+                         bool from_cache = false, const void *kv_scale = nullptr) {
   DecodeArgs a;
   fill_args(a, d, L, workspace);
   if (from_cache) use_plan_cache(a, L, workspace);  // hw_attn_decode: the plan cache
   a.view_limit = view_limit;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  a.kv_scale = static_cast<const uint32_t *>(kv_scale);
   a.append_block = append_block;
   a.append_pos = append_pos;
   a.k_new = k_new;
@@ -324,17 +343,21 @@ static int decode_common(const hw_attn_desc *d, const void *q, const void *k_cac
     a.plan = plan;
     const bool have_pool = d->n_blocks > 0 && d->cache_capacity > 0;
     if (reinterpret_cast<uintptr_t>(q) & 15u) return HW_ERR_INVALID;  // 16-byte query loads
-    if (have_pool && ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u))
+    if (have_pool && ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & (e2m1(d) ? 31u : 15u)))
       return HW_ERR_INVALID;
     CUtensorMap km, vm;
     std::memset(&km, 0, sizeof km);
     std::memset(&vm, 0, sizeof vm);
-    if (have_pool) {
+    if (have_pool && e2m1(d)) {
+      if (!make_pool_map_fp4(&km, k_cache, d->cache_capacity, d->n_kv_heads) ||
+          !make_pool_map_fp4(&vm, v_cache, d->cache_capacity, d->n_kv_heads))
+        return cuda_fail(cudaErrorInvalidValue);
+    } else if (have_pool) {
       if (!make_pool_map(&km, k_cache, d->cache_capacity, d->n_kv_heads, e4m3(d)) ||
           !make_pool_map(&vm, v_cache, d->cache_capacity, d->n_kv_heads, e4m3(d)))
         return cuda_fail(cudaErrorInvalidValue);
     }
-    e = launch_decode_tc(a, km, vm, sms, s);
+    e = e2m1(d) ? launch_decode_fp4(a, km, vm, sms, s) : launch_decode_tc(a, km, vm, sms, s);
   } else {
     const int per_sm = decode_simt_ctas_per_sm(d->dtype, d->head_dim);
     int ctas = sms * (per_sm > 4 ? 4 : per_sm);
@@ -344,10 +367,11 @@ static int decode_common(const hw_attn_desc *d, const void *q, const void *k_cac
   return e == cudaSuccess ? HW_OK : cuda_fail(e);
 }
 
-// hw_attn_decode_planned and its E4M3 form, after their own checks.
+// hw_attn_decode_planned and its forms for codes, after their own checks.
 static int planned_impl(const hw_attn_desc *d, const void *q, const void *k_cache,
                         const void *v_cache, const float *k_scale, const float *v_scale, void *out,
-                        float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+                        float *lse, void *workspace, size_t workspace_bytes, void *stream,
+                        const void *kv_scale = nullptr) {
   if (d->n_rows == 0) return HW_OK;
   if (!q || !out) return HW_ERR_INVALID;
   if (d->n_blocks > 0 && d->cache_capacity > 0 && (!k_cache || !v_cache)) return HW_ERR_INVALID;
@@ -360,7 +384,7 @@ static int planned_impl(const hw_attn_desc *d, const void *q, const void *k_cach
   return decode_common(d, q, k_cache, v_cache, m.block_start, m.block_len, m.view_block,
                        m.view_offset, m.q_pos, m.q_to_kv, plan, out, lse, workspace, L, max_ctas,
                        stream, nullptr, nullptr, nullptr, nullptr,
-                       limited(d) ? m.view_limit : nullptr, k_scale, v_scale);
+                       limited(d) ? m.view_limit : nullptr, k_scale, v_scale, false, kv_scale);
 }
 
 }  // namespace hw
@@ -375,7 +399,7 @@ int hw_attn_decode(const hw_attn_desc *d, const void *q, const void *k_cache, co
   int st = check_desc(d);
   if (st != HW_OK) return st;
   if (limited(d)) return HW_ERR_UNSUPPORTED;  // limits come with a plan
-  if (e4m3(d)) return HW_ERR_UNSUPPORTED;     // E4M3 caches: planned, with their scales
+  if (coded(d)) return HW_ERR_UNSUPPORTED;    // caches of codes: planned, with their scales
   if (d->n_rows == 0) return HW_OK;
   if (!q || !out || !q_pos) return HW_ERR_INVALID;
   if (d->max_view_blocks > 0 && (!view_block || !view_offset)) return HW_ERR_INVALID;
@@ -473,7 +497,7 @@ int hw_attn_decode_planned(const hw_attn_desc *d, const void *q, const void *k_c
                            size_t workspace_bytes, void *stream) {
   int st = check_desc(d);
   if (st != HW_OK) return st;
-  if (e4m3(d)) return HW_ERR_UNSUPPORTED;  // hw_attn_decode_planned_fp8 takes the scales
+  if (coded(d)) return HW_ERR_UNSUPPORTED;  // the _fp8 and _fp4 forms take the scales
   return planned_impl(d, q, k_cache, v_cache, nullptr, nullptr, out, lse, workspace,
                       workspace_bytes, stream);
 }
@@ -488,6 +512,23 @@ int hw_attn_decode_planned_fp8(const hw_attn_desc *d, const void *q, const void 
   if (d->n_rows > 0 && (!k_scale || !v_scale)) return HW_ERR_INVALID;
   return planned_impl(d, q, k_cache, v_cache, k_scale, v_scale, out, lse, workspace,
                       workspace_bytes, stream);
+}
+
+// The scales of a 4-bit cache that is read.
+static int check_kv_scale(const hw_attn_desc *d, const void *kv_scale) {
+  if (!e2m1(d)) return HW_ERR_INVALID;
+  if (d->n_rows > 0 && d->n_blocks > 0 && d->cache_capacity > 0 && !kv_scale) return HW_ERR_INVALID;
+  return reinterpret_cast<uintptr_t>(kv_scale) & 3u ? HW_ERR_INVALID : HW_OK;
+}
+
+int hw_attn_decode_planned_fp4(const hw_attn_desc *d, const void *q, const void *k_cache,
+                               const void *v_cache, const void *kv_scale, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+  int st = check_desc(d);
+  if (st == HW_OK) st = check_kv_scale(d, kv_scale);
+  if (st != HW_OK) return st;
+  return planned_impl(d, q, k_cache, v_cache, nullptr, nullptr, out, lse, workspace, workspace_bytes, stream,
+                      kv_scale);
 }
 
 int hw_plan_export(const hw_attn_desc *d, const void *workspace, size_t workspace_bytes,
@@ -515,11 +556,11 @@ int hw_plan_export(const hw_attn_desc *d, const void *workspace, size_t workspac
   return HW_OK;
 }
 
-// hw_attn_append_decode_planned and its E4M3 form, after their own checks.
+// hw_attn_append_decode_planned and its forms for codes, after their own checks.
 static int append_impl(const hw_attn_desc *d, const void *q, const void *k_new, const void *v_new,
                        void *k_cache, void *v_cache, const float *k_scale, const float *v_scale,
                        void *out, float *lse, void *workspace, size_t workspace_bytes,
-                       void *stream) {
+                       void *stream, void *kv_scale = nullptr) {
   if (d->n_rows == 0) return HW_OK;
   if (!tensor_core_path(d)) return HW_ERR_UNSUPPORTED;
   if (!q || !out || !k_new || !v_new) return HW_ERR_INVALID;
@@ -535,7 +576,7 @@ static int append_impl(const hw_attn_desc *d, const void *q, const void *k_new, 
   return decode_common(d, q, k_cache, v_cache, m.block_start, m.block_len, m.view_block,
                        m.view_offset, m.q_pos, m.q_to_kv, plan, out, lse, workspace, L, max_ctas,
                        stream, m.append_block, m.append_pos, k_new, v_new, nullptr, k_scale,
-                       v_scale);
+                       v_scale, false, kv_scale);
 }
 
 int hw_attn_append_decode_planned(const hw_attn_desc *d, const void *q, const void *k_new,
@@ -544,7 +585,7 @@ int hw_attn_append_decode_planned(const hw_attn_desc *d, const void *q, const vo
                                   void *stream) {
   int st = check_desc(d);
   if (st != HW_OK) return st;
-  if (limited(d) || e4m3(d)) return HW_ERR_UNSUPPORTED;  // E4M3: the _fp8 form takes the scales
+  if (limited(d) || coded(d)) return HW_ERR_UNSUPPORTED;  // the _fp8 and _fp4 forms take the scales
   return append_impl(d, q, k_new, v_new, k_cache, v_cache, nullptr, nullptr, out, lse, workspace,
                      workspace_bytes, stream);
 }
@@ -561,6 +602,19 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
   if (d->n_rows > 0 && (!k_scale || !v_scale)) return HW_ERR_INVALID;
   return append_impl(d, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, out, lse, workspace,
                      workspace_bytes, stream);
+}
+
+int hw_attn_append_decode_planned_fp4(const hw_attn_desc *d, const void *q, const void *k_new,
+                                      const void *v_new, void *k_cache, void *v_cache,
+                                      void *kv_scale, void *out, float *lse, void *workspace,
+                                      size_t workspace_bytes, void *stream) {
+  int st = check_desc(d);
+  if (st != HW_OK) return st;
+  if (limited(d)) return HW_ERR_UNSUPPORTED;
+  st = check_kv_scale(d, kv_scale);
+  if (st != HW_OK) return st;
+  return append_impl(d, q, k_new, v_new, k_cache, v_cache, nullptr, nullptr, out, lse, workspace, workspace_bytes,
+                     stream, kv_scale);
 }
 
 static_assert(kMaxCommits == HW_MAX_COMMITS, "commit table size");

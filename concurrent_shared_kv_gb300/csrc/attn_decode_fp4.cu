@@ -1,0 +1,999 @@
+// attn_decode_fp4.cu - concurrent decode attention for 4-bit caches (E2M1 codes, a
+// scale a token and kv head; head_dim 128) on the sm_100 tensor cores.
+//
+// The plan, the split over the CTAs, the records and the merge are those of the other
+// caches (hw_device.cuh, hw_decode_plan.cuh), and so are the two products of a tile:
+//   S^T [128 tokens x 32 columns] = K codes . Q~^T
+//   O^T [128 d x 32 columns]     += V codes^T . P^T
+// A tile is 16.5 KB here, a quarter of bf16's: DRAM brings one to an SM every 0.38 us,
+// so what the other kernels hide behind their loads (1.2 us a tile with E4M3
+// caches, the softmax of four warps) is what bounds this one.  It is built for it:
+//
+//  - Codes go from memory into the products.  The copy engine spreads 16 codes over 16
+//    bytes (8 bytes of codes, 8 left), which is how kind::f8f6f4 reads 4-bit operands;
+//    nothing is widened by a thread.  Both products are E2M1 x E4M3.
+//  - Scales stay out of the products.  A token is a row of S^T, so its thread has the
+//    one factor of its scores, and takes the value's scale into the weight:
+//    w = 2^(s ks + log2 vs - m), O = sum w c, l = sum w / vs.  Two fused
+//    multiply-adds an element, the ones that the sum and the shift cost anyway.
+//  - Sixteen softmax warps in two streams, one for even tiles, one for odd ones, with
+//    scores, weights, maxima and outputs of their own: one stream's latencies (TMEM,
+//    votes, fences) run under the other's arithmetic.  In a stream two threads share a
+//    token, each with half the columns; columns go to the halves by turns, and
+//    groups of four that hold none are skipped, so 20 columns cost 24, not 32.
+//  - Q~ is held as kQParts E4M3 parts x = a + b + ..., each the rounded remainder of those
+//    before it, and summed by the tensor cores into one S (12 bits of every element;
+//    2^-19 of the largest one where E4M3 runs out of exponents).  P is two E4M3 parts side
+//    by side (N = 64), the second 16 times larger, added where records are written.
+//  - Four tiles' scores are ahead of the weights, so that a stream finds its next
+//    tile's waiting; K and V share one ring, filled in the order of their use.
+//
+// Warps: 0-7 softmax of stream 0 (0-3 the first half of the columns, 4-7 the other),
+// 8-15 of stream 1, 16 TMA producer, 17 MMA issuer (the warp walks as a whole, one
+// elected lane issues: descriptors then stay in uniform registers), 18-19 rotated
+// queries of the segments to come, arrivals, appended tokens.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cfloat>
+
+#include "hw_decode_plan.cuh"
+#include "hw_fp4.cuh"
+#include "hw_rope_exact.cuh"
+
+namespace hw {
+
+namespace {
+
+constexpr int kThreads = 640;
+constexpr int kWarpTma = 16, kWarpMma = 17, kWarpQ = 18;
+constexpr int kSoftWarps = 16;
+constexpr uint32_t kTile = 128 * 128;      // a K or V tile in shared memory, 128-byte swizzled
+constexpr uint32_t kTileTx = 128 * 64;     // the bytes of it that come from memory
+constexpr int kSlots = 9;                  // of the ring
+constexpr int kLead = 4;                   // tiles whose scores are asked for before the first one's weights
+constexpr int kQParts = 3;
+constexpr uint32_t kQPart = kN * 128;      // a part of Q~: [32 columns][128], 128-byte swizzled
+constexpr uint32_t kQBytes = kQParts * kQPart;
+constexpr uint32_t kPBytes = 128 * 64;     // P: [128 tokens][32 first parts, 32 second ones], 64-byte swizzled
+constexpr int kHalf = kN / 2;              // columns of a softmax thread
+// Weights are kept 2^kLift times larger than the running maximum asks for, and O is
+// rescaled once one would pass 2^(kLift + kLazy) = 256 (E4M3 ends at 448): weights down to
+// 2^-10 of the maximum keep both parts' precision.  The factor is in the record's m.
+constexpr float kLift = 4.f, kLazy = 4.f;
+// TMEM columns: S of (stream, buffer), then O of (segment parity, stream): 32 + 32 columns
+constexpr uint32_t kTmemO = 4 * kN, kTmemCols = 512;
+
+struct Fp4Smem {
+  alignas(1024) uint8_t ring[kSlots][kTile];
+  alignas(1024) uint8_t q[2][kQBytes];  // by segment parity
+  alignas(1024) uint8_t p[2][2][kPBytes];  // by stream and buffer
+  PlanShared ps;
+  CtaPlan cp;
+  PlanHeader hdr;
+  alignas(16) float red[2][2][kHalf][4];  // stream, half: a tile's column maxima of the four warps
+  float hm[2][2][kN];          // segment parity, stream: reference maxima of the columns
+  float hl[2][2][4][kN];       // and the warps' sums of weights
+  int32_t nref[2];             // segment parity: references,
+  float q_mul[2];              // the power of two that scores are to be multiplied with
+  float qmax[8], qmax_next[2];  // the prologue's warps', the query warps'
+  int32_t abort_flag, plan_ok;
+  uint32_t tmem_base;
+  alignas(8) uint64_t kv_full[kSlots];
+  uint64_t kv_empty[kSlots];
+  uint64_t s_full[2][2], s_empty[2][2], p_full[2][2], p_empty[2][2];  // by stream and buffer
+  uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2], hand[2];     // by segment parity
+  uint64_t rec_ready[4];                                              // by segment mod 4
+  uint64_t plan_bar, app_bar, mma_done;
+};
+static_assert(sizeof(Fp4Smem) + 1024 <= 232448, "shared memory of one CTA per SM");
+static_assert(sizeof(PlanHeader) % 16 == 0 && offsetof(Fp4Smem, hdr) % 16 == 0, "bulk copies");
+static_assert(sizeof(MergeSmem<8>) <= kSlots * kTile, "merge scratch fits the ring");
+
+// kind::f8f6f4, A E2M1 (format 5), B E4M3, fp32 accumulator.
+constexpr uint32_t idesc_fp4(int M, int N, int a_mn, int b_mn) { return idesc_e4m3(M, N, a_mn, b_mn) | (5u << 7); }
+
+__device__ __forceinline__ void set_abort(Fp4Smem &S, const DecodeArgs &a) {
+  if (atomicExch(&S.abort_flag, 1) == 0) flag_error(a.err, HW_DEV_TIMEOUT);
+}
+__device__ __forceinline__ bool aborted(Fp4Smem &S) { return *reinterpret_cast<volatile int32_t *>(&S.abort_flag) != 0; }
+// Bounded wait, suspended; on a timeout the CTA winds down (no wait blocks any more
+// and every role runs to its end).
+__device__ __forceinline__ void idle_wait(Fp4Smem &S, const DecodeArgs &a, uint64_t *bar, uint32_t parity) {
+  if (!mbar_try(bar, parity)) {
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+      if (aborted(S)) break;
+      if (clock64() - t0 > kWaitLimit) {
+        set_abort(S, a);
+        break;
+      }
+    }
+  }
+  __syncwarp();
+}
+// The same spinning, with one answer for the warp.
+__device__ __forceinline__ bool warp_spin(Fp4Smem &S, const DecodeArgs &a, uint64_t *bar, uint32_t parity) {
+  bool ok = mbar_test(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!(ok = mbar_test(bar, parity))) {
+      if (aborted(S)) break;
+      if (clock64() - t0 > kWaitLimit) {
+        set_abort(S, a);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// A place in the ring.
+struct RingPos {
+  int s;
+  uint32_t phase;
+  __device__ __forceinline__ void next() {
+    if (++s == kSlots) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Column qi's place among S's columns: by turns in the two halves.
+__device__ __forceinline__ int column_place(int qi) { return (qi & 1) * kHalf + (qi >> 1); }
+
+// ------------------------------------------------------------------ producer
+
+// The order in which tiles are used, K(0) .. K(kLead-1), V(0), K(kLead), V(1), ...:
+// step j takes V(j - kLead), then K(j).  Steps [j0, j1) of the CTA's n units; `count`:
+// copies issued so far.
+struct Producer {
+  RingPos at;
+  int count;
+  UnitPos k, v;  // the next K's and V's unit
+};
+
+__device__ void produce(const DecodeArgs &a, Fp4Smem &S, const CUtensorMap *tk, const CUtensorMap *tv, Producer &p,
+                        int n, int j0, int j1, int app_tile, int lane) {
+  const uint64_t pol = policy_evict_first();
+  const PlanCore &P = S.ps.plan;
+  auto load = [&](const CUtensorMap *m, const UnitPos &x) {
+    if (p.count >= kSlots && !warp_spin(S, a, &S.kv_empty[p.at.s], p.at.phase ^ 1)) return false;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&S.kv_full[p.at.s], kTileTx);
+      tma_load_3d(S.ring[p.at.s], m, &S.kv_full[p.at.s], 0, P.start[x.b] + x.t * kT, x.h, pol);
+    }
+    ++p.count;
+    p.at.next();
+    return true;
+  };
+  for (int j = j0; j < j1; ++j) {
+    if (j >= kLead) {
+      if (!load(tv, p.v)) return;
+      unit_pos_next(P, a.n_blocks, p.v);
+    }
+    if (j < n) {
+      // the first tile with a new token is loaded once the tokens are written (and
+      // fenced for the copy engine)
+      if (j == app_tile && !warp_spin(S, a, &S.app_bar, 0)) return;
+      // the tile's scales into L2 (its threads load them shortly before they need them)
+      const int left = P.len[p.k.b] - p.k.t * kT;
+      if (lane < 4 && lane * 32 < left)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            a.kv_scale + static_cast<int64_t>(p.k.h) * a.capacity + P.start[p.k.b] + p.k.t * kT + lane * 32));
+      if (!load(tk, p.k)) return;
+      unit_pos_next(P, a.n_blocks, p.k);
+    }
+  }
+}
+
+// No copy may still be landing when the CTA retires.
+__device__ void drain(Fp4Smem &S, const Producer &p) {
+  RingPos back = p.count >= kSlots ? RingPos{p.at.s, p.at.phase ^ 1} : RingPos{0, 0};
+  for (int j = min(p.count, kSlots); j > 0; --j, back.next()) mbar_wait(&S.kv_full[back.s], back.phase);
+}
+
+// ---------------------------------------------------------------- MMA issuer
+
+__device__ void mma_issuer(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int64_t u0, int n) {
+  constexpr uint32_t idesc_qk = idesc_fp4(128, kN, 0, 0), idesc_pv = idesc_fp4(128, 2 * kN, 1, 1);
+  const uint64_t k_desc = smem_desc(smem_u32(S.ring[0]), 16, 1024, kSw128);
+  const uint64_t v_desc = smem_desc(smem_u32(S.ring[0]), kTile, 1024, kSw128);
+  const uint64_t q_desc = smem_desc(smem_u32(S.q[0]), 16, 1024, kSw128);
+  const uint64_t p_desc = smem_desc(smem_u32(S.p[0][0]), 512, 512, kSw64);
+  const PlanCore &P = S.ps.plan;
+  RingPos at = {0, 0};
+  // segments of the tiles that QK and PV are at: index, tiles left of it
+  const UnitPos x0 = unit_pos(P, a.n_blocks, u0);
+  UnitPos xk = x0, xv = x0;
+  int seg_k = -1, left_k = 0, seg_v = -1, left_v = 0, in_v = 0;
+  for (int j = 0; j < n + kLead; ++j) {
+    if (j >= kLead) {  // PV(i)
+      const int i = j - kLead, st = i & 1, buf = (i >> 1) & 1;
+      if (left_v == 0) {
+        if (seg_v >= 0) {
+          xv.t = xv.tiles - 1;
+          unit_pos_next(P, a.n_blocks, xv);
+        }
+        ++seg_v;
+        left_v = min(n - i, xv.tiles - xv.t);
+        in_v = 0;
+        if (!warp_spin(S, a, &S.o_empty[seg_v & 1], ((seg_v >> 1) & 1) ^ 1)) return;
+      }
+      if (!warp_spin(S, a, &S.p_full[st][buf], (i >> 2) & 1)) return;
+      if (!warp_spin(S, a, &S.kv_full[at.s], at.phase)) return;
+      tc_fence_after();
+      --left_v;
+      const bool first = in_v < 2;  // of its stream in this segment
+      ++in_v;
+      if (elect_one()) {
+        const uint32_t o = tmem + kTmemO + ((seg_v & 1) * 2 + st) * 2 * kN;
+        const uint64_t v = v_desc + ((at.s * kTile) >> 4), p = p_desc + (((st * 2 + buf) * kPBytes) >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 4 steps of 32 tokens
+          mma_f8(o, v + ((k * 4096) >> 4), p + ((k * 2048) >> 4), idesc_pv, !(first && k == 0));
+        mma_commit(&S.kv_empty[at.s]);
+        mma_commit(&S.p_empty[st][buf]);
+        if (left_v == 0) mma_commit(&S.o_full[seg_v & 1]);
+      }
+      __syncwarp();
+      at.next();
+    }
+    if (j < n) {  // QK(j)
+      const int st = j & 1, buf = (j >> 1) & 1;
+      if (left_k == 0) {
+        if (seg_k >= 0) {
+          xk.t = xk.tiles - 1;
+          unit_pos_next(P, a.n_blocks, xk);
+        }
+        ++seg_k;
+        left_k = min(n - j, xk.tiles - xk.t);
+        if (!warp_spin(S, a, &S.q_full[seg_k & 1], (seg_k >> 1) & 1)) return;
+      }
+      if (!warp_spin(S, a, &S.s_empty[st][buf], ((j >> 2) & 1) ^ 1)) return;
+      if (!warp_spin(S, a, &S.kv_full[at.s], at.phase)) return;
+      tc_fence_after();
+      --left_k;
+      if (elect_one()) {
+        const uint32_t s = tmem + (st * 2 + buf) * kN;
+        const uint64_t k0 = k_desc + ((at.s * kTile) >> 4), q = q_desc + (((seg_k & 1) * kQBytes) >> 4);
+#pragma unroll
+        for (int part = 0; part < kQParts; ++part)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 4 steps of 32 elements
+            mma_f8(s, k0 + ((k * 32) >> 4), q + ((part * kQPart + k * 32) >> 4), idesc_qk, part > 0 || k > 0);
+        mma_commit(&S.kv_empty[at.s]);
+        mma_commit(&S.s_full[st][buf]);
+        if (left_k == 0) mma_commit(&S.q_empty[seg_k & 1]);
+      }
+      __syncwarp();
+      at.next();
+    }
+  }
+}
+
+// ------------------------------------------------------------------- queries
+
+// A column's largest pair length over the item's elements, squared: turned
+// elements are no longer than that.
+__device__ __forceinline__ float item_reach(const QItem &it) {
+  const uint32_t lo[4] = {it.lo.x, it.lo.y, it.lo.z, it.lo.w}, hi[4] = {it.hi.x, it.hi.y, it.hi.z, it.hi.w};
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a0 = __uint_as_float(lo[e] << 16), a1 = __uint_as_float(hi[e] << 16);
+    const float b0 = __uint_as_float(lo[e] & 0xffff0000u), b1 = __uint_as_float(hi[e] & 0xffff0000u);
+    m = fmaxf(m, fmaxf(__fmaf_rn(a0, a0, a1 * a1), __fmaf_rn(b0, b0, b1 * b1)));
+  }
+  return m;
+}
+// The exponent e of the power of two with |y| / 2^e < 448, E4M3's largest value, for a
+// segment whose pairs reach the square root of `reach` before scale * log2(e).
+__device__ __forceinline__ int part_exponent(const DecodeArgs &a, float reach) {
+  const float mx = sqrtf(reach) * fabsf(a.scale_log2) * 1.0001f;
+  int e = 0;
+  if (mx > 0.f && mx < INFINITY) frexpf(mx * (1.f / 448.f), &e);
+  return max(-120, min(e, 120));
+}
+
+// Two E4M3 codes (low byte first) as two fp32, exactly.
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
+  const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3));
+  return __half22float2(h);
+}
+
+// The item turned, scaled by scale * log2(e) / 2^e and split into parts, into Q~'s
+// row `place`: 8 codes at byte 8c, 8 at 64 + 8c, 16-byte chunks swizzled.
+__device__ __forceinline__ void store_item(const DecodeArgs &a, const Fp4Smem &S, const QItem &it, uint32_t qbase,
+                                           int place, int c, float inv) {
+  const uint32_t lo32[4] = {it.lo.x, it.lo.y, it.lo.z, it.lo.w}, hi32[4] = {it.hi.x, it.hi.y, it.hi.z, it.hi.w};
+  uint32_t w[kQParts][4];
+#pragma unroll
+  for (int j = 0; j < kQParts; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[j][k] = 0;
+  const float mul = a.scale_log2 * inv;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 y0, y1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x0 = __uint_as_float(h ? (lo32[e] & 0xffff0000u) : (lo32[e] << 16));
+      const float x1 = __uint_as_float(h ? (hi32[e] & 0xffff0000u) : (hi32[e] << 16));
+      float cs, sn;
+      rope_cos_sin_fast(it.rel, S.ps.cache.phase[8 * c + 2 * e + h], &cs, &sn);
+      (h ? y0.y : y0.x) = (x0 * cs - x1 * sn) * mul;
+      (h ? y1.y : y1.x) = (x1 * cs + x0 * sn) * mul;
+    }
+#pragma unroll
+    for (int j = 0; j < kQParts; ++j) {
+      const uint32_t q0 = __nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3);
+      const uint32_t q1 = __nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3);
+      w[j][e >> 1] |= q0 << (16 * (e & 1));
+      w[j][2 + (e >> 1)] |= q1 << (16 * (e & 1));
+      if (j + 1 < kQParts) {
+        const float2 v0 = e4m3x2_values(q0), v1 = e4m3x2_values(q1);
+        y0 = make_float2(y0.x - v0.x, y0.y - v0.y);
+        y1 = make_float2(y1.x - v1.x, y1.y - v1.y);
+      }
+    }
+  }
+  const uint32_t row = qbase + place * 128, sub = 8u * (c & 1);
+  const uint32_t c0 = ((static_cast<uint32_t>(c >> 1) ^ (place & 7)) << 4) + sub;
+  const uint32_t c1 = ((static_cast<uint32_t>(4 + (c >> 1)) ^ (place & 7)) << 4) + sub;
+#pragma unroll
+  for (int j = 0; j < kQParts; ++j) {
+    st_shared_v2(row + j * kQPart + c0, w[j][0], w[j][1]);
+    st_shared_v2(row + j * kQPart + c1, w[j][2], w[j][3]);
+  }
+}
+
+// Segment 0's queries, by warps 0-7 (256 threads, an item each).
+__device__ void query_prologue(const DecodeArgs &a, Fp4Smem &S) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  NamedSync<5, 256> sync;
+  const SegQ &X = S.cp.pre[0];
+  const int items = min(X.m.n_ref * (a.n_q_heads / a.n_kv_heads), kN) * 8;
+  QItem it;
+  float reach = 0.f;
+  if (t < items) {
+    load_item(a, X, t >> 3, t & 7, it);
+    reach = item_reach(it);
+  }
+  reach = warp_max_nonneg(reach);
+  if (lane == 0) S.qmax[warp] = reach;
+  sync();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) reach = fmaxf(reach, S.qmax[w]);
+  const int e = part_exponent(a, reach);
+  if (t < items) store_item(a, S, it, smem_u32(S.q[0]), column_place(t >> 3), t & 7, ldexpf(1.f, -e));
+  if (t == 0) {
+    S.nref[0] = X.m.n_ref;
+    S.q_mul[0] = ldexpf(1.f, e);
+  }
+  fence_proxy_async_smem();
+  sync();
+  if (t == 0) mbar_arrive(&S.q_full[0]);
+}
+
+// Queries of segments 1, 2, ..., and the arrivals of finished ones two segments
+// late, by warps 18 and 19 (as in the other tensor-core kernel).
+template <bool kLimit>
+__device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
+  const int tq = threadIdx.x - kWarpQ * 32;
+  const int lane = threadIdx.x & 31, wq = tq >> 5;
+  const int G = a.n_q_heads / a.n_kv_heads;
+  NamedSync<6, 64> sync;
+  auto arrivals = [&](int done) {
+    idle_wait(S, a, &S.rec_ready[done & 3], (done >> 2) & 1);
+    if (wq == 0) arrive_segment(a, S.cp.pre[done % kPre].m, lane);
+  };
+  int64_t u = S.cp.us[1];
+  int64_t u_prep = S.cp.us[kPre - 1] < u1 ? next_segment(S.ps.plan, a.n_blocks, S.cp.us[kPre - 1]) : u1;
+  for (int seg = 1;; ++seg) {
+    if (u >= u1) {
+      if (seg >= 2) arrivals(seg - 2);
+      arrivals(seg - 1);
+      break;
+    }
+    const SegQ &X = S.cp.pre[seg % kPre];
+    const int nq = min(X.m.n_ref * G, kN), par = seg & 1;
+    QItem raw[4];
+    float reach = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((tq >> 3) + 8 * k < nq) {
+        load_item(a, X, (tq >> 3) + 8 * k, tq & 7, raw[k]);
+        reach = fmaxf(reach, item_reach(raw[k]));
+      }
+    reach = warp_max_nonneg(reach);
+    if (lane == 0) S.qmax_next[wq] = reach;
+    sync();
+    reach = fmaxf(S.qmax_next[0], S.qmax_next[1]);
+    const int e = part_exponent(a, reach);
+    if (seg >= 2) idle_wait(S, a, &S.q_empty[par], ((seg >> 1) - 1) & 1);
+    if (tq == 0) {
+      S.nref[par] = X.m.n_ref;
+      S.q_mul[par] = ldexpf(1.f, e);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((tq >> 3) + 8 * k < nq)
+        store_item(a, S, raw[k], smem_u32(S.q[par]), column_place((tq >> 3) + 8 * k), tq & 7, ldexpf(1.f, -e));
+    fence_proxy_async_smem();
+    sync();
+    if (tq == 0) mbar_arrive(&S.q_full[par]);
+    if (seg >= 2) {
+      arrivals(seg - 2);
+      sync();  // the slot of segment seg - 2 is read; it now takes segment seg + 2
+      if (u_prep < u1) {
+        const UnitPos x = unit_pos(S.ps.plan, a.n_blocks, u_prep);
+        if (wq == 0) seg_pre<kLimit>(a, S.ps.plan, S.ps.cache, S.cp.pre[(seg + 2) % kPre], x.b, x.g, x.h, lane);
+        u_prep = x.seg_first + x.tiles;
+      }
+      sync();
+    }
+    u = next_segment(S.ps.plan, a.n_blocks, u);
+  }
+}
+
+// The CTA's new tokens (hw_attn_append_decode_planned_fp4), by warps 18 and 19, four
+// (row, kv head) pairs a warp, 8 threads each: the bits that hw_cache_write stores.
+__device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64_t u1) {
+  const int tq = threadIdx.x - kWarpQ * 32;
+  const int lane = tq & 31, wq = tq >> 5, c = lane & 7;
+  const PlanCore &P = S.ps.plan;
+  const int Hkv = a.n_kv_heads, npairs = a.n_rows * Hkv;
+  uint32_t *kc = static_cast<uint32_t *>(const_cast<void *>(a.k)), *vc = static_cast<uint32_t *>(const_cast<void *>(a.v));
+  uint32_t *sc = const_cast<uint32_t *>(a.kv_scale);
+  auto write = [&](bool on, int pr, int pos, int row) {
+    const int h = pr % Hkv;
+    float k0[8], k1[8], v0[8], v1[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k0[j] = k1[j] = v0[j] = v1[j] = 0.f;
+    if (on) {
+      const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(a.k_new) + static_cast<int64_t>(pr) * 128 + 8 * c;
+      const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(a.v_new) + static_cast<int64_t>(pr) * 128 + 8 * c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float cs, sn;
+        rope_cos_sin_exact(pos, a.phase[8 * c + j], &cs, &sn);
+        fp4_turn(__bfloat162float(kn[j]), __bfloat162float(kn[64 + j]), cs, sn, k0[j], k1[j]);
+        v0[j] = __bfloat162float(vn[j]);
+        v1[j] = __bfloat162float(vn[64 + j]);
+      }
+    }
+    uint32_t kl, kh, vl, vh;
+    const float ks = fp4_row(k0, k1, kl, kh), vs = fp4_row(v0, v1, vl, vh);
+    if (on) {
+      const int64_t at = static_cast<int64_t>(h) * a.capacity + row;
+      kc[at * 16 + c] = kl;
+      kc[at * 16 + 8 + c] = kh;
+      vc[at * 16 + c] = vl;
+      vc[at * 16 + 8 + c] = vh;
+      if (c == 0) sc[at] = fp4_scale_word(ks, vs);
+    }
+  };
+  if (S.cp.app_n <= kAppList) {
+    for (int e0 = wq * 4; e0 < S.cp.app_n; e0 += 8) {
+      const int e = e0 + (lane >> 3);
+      const bool on = e < S.cp.app_n;
+      write(on, on ? S.cp.app_pair[e] : 0, on ? S.cp.app_pos[e] : 0, on ? S.cp.app_row[e] : 0);
+    }
+  } else {
+    // more than the plan lists: every pair is checked (each CTA that reads a token's
+    // tile writes it, the same bytes, before its own copy of the tile)
+    for (int base = wq * 4; base < npairs; base += 8) {
+      const int pr = base + (lane >> 3);
+      int pos = 0, row = 0;
+      bool mine = false;
+      if (pr < npairs) {
+        const int r = pr / Hkv, h = pr - r * Hkv;
+        const int b = __ldg(a.append_block + r);
+        if (b >= 0 && b < a.n_blocks && P.tiles[b] > 0) {
+          pos = __ldg(a.append_pos + r);
+          if (pos >= 0 && pos < P.len[b]) {
+            mine = tile_unit_in(P, b, h, pos / kT, u0, u1) >= 0;
+            row = P.start[b] + pos;
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, mine)) write(mine, mine ? pr : 0, pos, row);
+    }
+  }
+  __threadfence_block();
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  NamedSync<6, 64>()();
+  if (tq == 0) mbar_arrive(&S.app_bar);
+}
+
+// ------------------------------------------------------------------- softmax
+
+// Whether any of the 128 threads of barrier `id` says so.
+__device__ __forceinline__ bool vote_128(int id, bool pred) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\t"
+      "setp.ne.u32 pi, %2, 0;\n\t"
+      "bar.red.or.pred po, %1, 128, pi;\n\t"
+      "selp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(out)
+      : "r"(id), "r"(pred ? 1u : 0u)
+      : "memory");
+  return out != 0;
+}
+
+// Butterfly over the warp: on entry v[j] is this lane's value of column j, on exit
+// v[0] is the whole warp's of column lane & 15.
+template <bool kMax>
+__device__ __forceinline__ void reduce_columns(float (&v)[kHalf], int lane) {
+#pragma unroll
+  for (int off = kHalf / 2; off >= 1; off >>= 1) {
+#pragma unroll
+    for (int k = 0; k < off; ++k) {
+      const bool up = (lane & off) != 0;
+      const float mine = up ? v[k + off] : v[k];
+      const float other = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + off], off);
+      v[k] = kMax ? fmaxf(mine, other) : mine + other;
+    }
+  }
+  const float other = __shfl_xor_sync(0xffffffffu, v[0], 16);
+  v[0] = kMax ? fmaxf(v[0], other) : v[0] + other;
+}
+
+// x, y (at most 448) as two E4M3 parts each, x = hi + lo / 16: the codes of hi in the
+// low half of the word, those of lo in the high one.  fp16 in between keeps 11 bits,
+// more than the parts do together; hi is cut to E4M3's 3 bits behind the leading one
+// there (ties away), so no code has to be turned back.
+__device__ __forceinline__ void split_weights(float x, float y, uint16_t &hi, uint16_t &lo) {
+  const __half2 v = __floats2half2_rn(x, y);
+  const uint32_t top = (*reinterpret_cast<const uint32_t *>(&v) + 0x00400040u) & 0xff80ff80u;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(top));
+  const __half2 rest = __hmul2(__hsub2(v, *reinterpret_cast<const __half2 *>(&top)), __float2half2_rn(16.f));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t *>(&rest)));
+}
+
+// Records of a finished segment: every warp joins the two streams' outputs of 8 of its
+// half's columns (stream 0's warps the first 8 places, stream 1's the others).
+__device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int seg, int64_t sid,
+                                             int nq, int cnt, int first_stream) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int st = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3, par = seg & 1;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(qd * 32) << 16) + kTmemO + par * 4 * kN;
+  const int place = half * kHalf + st * 8;  // of the first column
+  idle_wait(S, a, &S.hand[par], (seg >> 1) & 1);
+  idle_wait(S, a, &S.o_full[par], (seg >> 1) & 1);
+  tc_fence_after();
+  float o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = 0.f;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (cnt < 2 && s != first_stream) continue;  // the stream had no tile of this segment
+    uint32_t hi[8], lo[8];
+    tmem_ld8(tl + s * 2 * kN + place, hi);
+    tmem_ld8(tl + s * 2 * kN + kN + place, lo);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float m0 = S.hm[par][0][place + j], m1 = S.hm[par][1][place + j];
+      const float f = ex2((s ? m1 : m0) - fmaxf(m0, m1));
+      o[j] = __fmaf_rn(__fmaf_rn(__uint_as_float(lo[j]), 0.0625f, __uint_as_float(hi[j])), f, o[j]);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&S.o_empty[par]);
+  const int64_t slot = sid + S.cp.c_log;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int qi = 2 * (st * 8 + j) + half;
+    if (qi < nq) record_ptr(a, slot, qi)[qd * 32 + lane] = o[j];
+  }
+  if (qd == 0 && lane < 8) {
+    const int qi = 2 * (st * 8 + lane) + half, k = place + lane;
+    if (qi < nq) {
+      const float m0 = S.hm[par][0][k], m1 = S.hm[par][1][k], m = fmaxf(m0, m1);
+      float l = 0.f;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const float *hl = &S.hl[par][s][0][k];
+        l += (hl[0] + hl[kN] + hl[2 * kN] + hl[3 * kN]) * ex2((s ? m1 : m0) - m);
+      }
+      *reinterpret_cast<float2 *>(record_ptr(a, slot, qi) + 128) = make_float2(m, l);
+    }
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&S.rec_ready[seg & 3]);
+}
+
+template <bool kAppend, bool kLimit>
+__device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int64_t u0, int n) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int st = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3;
+  const int row = qd * 32 + lane;  // token of the tile
+  const int bar = 1 + st * 2 + half;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const PlanCore &P = S.ps.plan;
+  const uint32_t pbase = smem_u32(S.p[st][0]) + row * 64, swz = (row >> 1) & 3;
+  const uint32_t p_hi = pbase + ((half ^ swz) << 4), p_lo = pbase + (((2 + half) ^ swz) << 4);
+  const int app_tile = kAppend && S.cp.app_n > 0 ? S.cp.app_tile : INT32_MAX;
+
+  // A wait that gives up (HW_DEV_TIMEOUT) does not leave the loops: all threads keep
+  // the same control flow, so the votes are always reached by all 128.
+  // ref[j]: the exponent that column j's weights are taken against (its maximum less
+  // kLift), the same in every lane of the four warps; ref_mine: that of column lane & 15.
+  // They start at -FLT_MAX, not -inf: a column whose tokens are all masked
+  // then has weights 2^-inf = 0.
+  float ref[kHalf], l[kHalf], ref_mine = -FLT_MAX;
+  int pend = -1, pend_nq = 0, pend_cnt = 0, pend_first = 0;
+  int64_t pend_sid = 0;
+  UnitPos x = unit_pos(P, a.n_blocks, u0);
+  // the scales of the stream's next tile (of this segment), loaded a tile ahead
+  auto scales_of = [&](int i, int t) -> uint32_t {
+    const int at = t * kT + row;
+    if (at >= P.len[x.b]) return 0x3f803f80u;  // (past the block: 1, and masked)
+    if (kAppend && i >= app_tile) idle_wait(S, a, &S.app_bar, 0);
+    return __ldcg(a.kv_scale + static_cast<int64_t>(x.h) * a.capacity + P.start[x.b] + at);
+  };
+  for (int i0 = 0, seg = 0; i0 < n; ++seg) {
+    const int par = seg & 1;
+    const int cnt = min(n - i0, x.tiles - x.t), len = P.len[x.b];
+    int i = i0 + ((i0 ^ st) & 1);
+    uint32_t sw_next = i < i0 + cnt ? scales_of(i, x.t + i - i0) : 0;
+    idle_wait(S, a, &S.q_full[par], (seg >> 1) & 1);
+    const int nq = min(S.nref[par] * G, kN);
+    const int nh = (nq + 1 - half) >> 1;  // the half's columns
+    const float q_mul = S.q_mul[par];
+    int minlim = INT32_MAX, lim_mine = INT32_MAX;
+    if constexpr (kLimit) {
+      const SegQ &X = S.cp.pre[seg % kPre];
+      minlim = X.minlim;
+      lim_mine = len;
+      const int qi = 2 * (lane & (kHalf - 1)) + half;
+      if (minlim < len && qi < nq) lim_mine = entry_limit(a.view_limit, X.m.ref_entry[qi / G], len);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.q_empty[par]);  // this warp has read the hand-off
+#pragma unroll
+    for (int j = 0; j < kHalf; ++j) {
+      ref[j] = -FLT_MAX;
+      l[j] = 0.f;
+    }
+    ref_mine = -FLT_MAX;
+    bool started = false;  // O holds a tile of this segment
+    for (; i < i0 + cnt; i += 2) {
+      const int buf = (i >> 1) & 1, t = x.t + i - i0;
+      const uint32_t sw = sw_next;
+      if (i + 2 < i0 + cnt) sw_next = scales_of(i + 2, t + 2);
+      const bool tok_ok = t * kT + row < len;
+      const float vs = fp4_v_scale(sw);
+      // (a value of zeros has weight like any other)
+      const float ks = fp4_k_scale(sw) * q_mul, lv = vs == 0.f ? 0.f : __log2f(vs);
+      const float rv = vs == 0.f ? 1.f : __fdividef(1.f, vs);
+      idle_wait(S, a, &S.s_full[st][buf], (i >> 2) & 1);
+      tc_fence_after();
+      uint32_t r[kHalf];
+      tmem_ld16(tl + (st * 2 + buf) * kN + half * kHalf, r);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.s_empty[st][buf]);
+      // scores in log2 units with the value's scale in them, against the reference
+      float d[kHalf];
+#pragma unroll
+      for (int j = 0; j < kHalf; j += 2) {
+        const float2 v = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), make_float2(ks, ks),
+                                    make_float2(lv, lv));
+        d[j] = v.x;
+        d[j + 1] = v.y;
+      }
+      if (kLimit && (t + 1) * kT > minlim) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          const int lim = __shfl_sync(0xffffffffu, lim_mine, j);
+          if (t * kT + row >= lim) d[j] = -INFINITY;
+        }
+      }
+      if (!tok_ok) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) d[j] = -INFINITY;
+      }
+      bool exceed = false;
+#pragma unroll
+      for (int j = 0; j < kHalf; ++j) exceed |= j < nh && d[j] - ref[j] > kLift + kLazy;
+      if (vote_128(bar, exceed)) {
+        float v[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) v[j] = d[j];
+        reduce_columns<true>(v, lane);
+        if (lane < kHalf) S.red[st][half][lane][qd] = v[0];
+        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+        const float4 t4 = *reinterpret_cast<const float4 *>(S.red[st][half][lane & (kHalf - 1)]);
+        const float tmax = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
+        const float old = ref_mine;
+        if ((lane & (kHalf - 1)) < nh && tmax - old > kLift + kLazy) ref_mine = tmax - kLift;
+        const float a_mine = ref_mine == old ? 1.f : ex2(old - ref_mine);
+        float alpha[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          ref[j] = __shfl_sync(0xffffffffu, ref_mine, j);
+          alpha[j] = __shfl_sync(0xffffffffu, a_mine, j);
+          l[j] *= alpha[j];
+        }
+        if (started) {
+          // O must hold the stream's earlier tiles before it is rescaled
+          idle_wait(S, a, &S.p_empty[st][buf ^ 1], ((i - 2) >> 2) & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t col = tl + kTmemO + (par * 2 + st) * 2 * kN + h * kN + half * kHalf;
+            uint32_t o[kHalf];
+            tmem_ld16(col, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
+            tmem_st16(col, o);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // (red is read before the next tile writes it)
+      }
+      started = true;
+      // weights: their sum, and their parts to the tensor cores
+      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (4 * c < nh) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int j = 4 * c + 2 * k;
+            const float w0 = ex2(d[j] - ref[j]), w1 = ex2(d[j + 1] - ref[j + 1]);
+            const float2 s = __ffma2_rn(make_float2(w0, w1), make_float2(rv, rv), make_float2(l[j], l[j + 1]));
+            l[j] = s.x;
+            l[j + 1] = s.y;
+            uint16_t wh, wl;
+            split_weights(w0, w1, wh, wl);
+            hi[c] |= static_cast<uint32_t>(wh) << (16 * k);
+            lo[c] |= static_cast<uint32_t>(wl) << (16 * k);
+          }
+        }
+      }
+      if (i >= 4) idle_wait(S, a, &S.p_empty[st][buf], ((i - 4) >> 2) & 1);  // PV of the buffer's last tile
+      st_shared_v4(p_hi + buf * kPBytes, hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(p_lo + buf * kPBytes, lo[0], lo[1], lo[2], lo[3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[st][buf]);
+      if (pend >= 0) {  // records of the segment before, a tile late
+        segment_records(a, S, tmem, pend, pend_sid, pend_nq, pend_cnt, pend_first);
+        pend = -1;
+      }
+    }
+    // (before this segment's hand-over: the other stream writes to the same places only
+    // once both are done with the segment before)
+    if (pend >= 0) segment_records(a, S, tmem, pend, pend_sid, pend_nq, pend_cnt, pend_first);
+    reduce_columns<false>(l, lane);
+    if (lane < kHalf) {
+      S.hl[par][st][qd][half * kHalf + lane] = l[0];
+      if (qd == 0) S.hm[par][st][half * kHalf + lane] = ref_mine;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.hand[par]);
+    pend = seg;
+    pend_sid = seg_id(P, x.b, x.g, x.h);
+    pend_nq = nq;
+    pend_cnt = cnt;
+    pend_first = i0 & 1;
+    i0 += cnt;
+    x.t = x.tiles - 1;
+    unit_pos_next(P, a.n_blocks, x);
+  }
+  if (pend >= 0) segment_records(a, S, tmem, pend, pend_sid, pend_nq, pend_cnt, pend_first);
+}
+
+// The plan into shared memory (around the RoPE table, which is the launch's own).
+__device__ __forceinline__ void issue_plan_copies(const DecodeArgs &a, Fp4Smem &S) {
+  constexpr uint32_t kTail = sizeof(PlanShared) - kPhaseOff - kPhaseBytes;
+  const uint8_t *src = a.plan + kPlanHeaderBytes;
+  uint8_t *dst = reinterpret_cast<uint8_t *>(&S.ps);
+  mbar_arrive_expect_tx(&S.plan_bar, sizeof(PlanHeader) + kPhaseOff + kTail + sizeof(CtaPlan));
+  bulk_g2s(&S.hdr, a.plan, sizeof(PlanHeader), &S.plan_bar);
+  if (kPhaseOff) bulk_g2s(dst, src, kPhaseOff, &S.plan_bar);
+  bulk_g2s(dst + kPhaseOff + kPhaseBytes, src + kPhaseOff + kPhaseBytes, kTail, &S.plan_bar);
+  bulk_g2s(&S.cp, plan_cta_record(a.plan, blockIdx.x), sizeof(CtaPlan), &S.plan_bar);
+}
+
+// Each CTA's share of an array read early by all, into L2.
+__device__ __forceinline__ void warm_l2(const void *p, uint64_t total) {
+  const uint64_t per = ((total + gridDim.x - 1) / gridDim.x + 255) & ~static_cast<uint64_t>(255);
+  const uint64_t off = per * blockIdx.x;
+  if (off < total) {
+    const uint32_t n = static_cast<uint32_t>(total - off < per ? total - off : per);
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const uint8_t *>(p) + off), "r"(n)
+                 : "memory");
+  }
+}
+
+template <bool kAppend, bool kLimit>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_fp4_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ uint8_t smem_raw[];
+  Fp4Smem &S = *reinterpret_cast<Fp4Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // As the other tensor-core kernel (a programmatic dependent of the launch before, see
+  // there): before griddepcontrol.wait nothing is written, and nothing read but an L2
+  // prefetch and, under the early-loads promise, the plan and the first tiles.
+  if (tid == 0) {
+    mbar_init(&S.plan_bar, 1);
+    fence_mbar_init();
+    if (a.early) issue_plan_copies(a, S);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&S.kv_full[s], 1);
+      mbar_init(&S.kv_empty[s], 1);
+    }
+    for (int k = 0; k < 4; ++k) {
+      mbar_init(&S.s_full[k >> 1][k & 1], 1);
+      mbar_init(&S.s_empty[k >> 1][k & 1], 8);  // the stream's warps
+      mbar_init(&S.p_full[k >> 1][k & 1], 8);
+      mbar_init(&S.p_empty[k >> 1][k & 1], 1);
+      mbar_init(&S.rec_ready[k], kSoftWarps);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&S.q_full[k], 1);
+      mbar_init(&S.q_empty[k], 1 + kSoftWarps);  // the segment's last QK, the softmax warps' reads
+      mbar_init(&S.o_full[k], 1);
+      mbar_init(&S.o_empty[k], kSoftWarps);
+      mbar_init(&S.hand[k], kSoftWarps);
+    }
+    mbar_init(&S.app_bar, 1);
+    mbar_init(&S.mma_done, 1);
+    S.abort_flag = 0;
+    S.plan_ok = 1;
+    fence_mbar_init();
+  }
+  if (tid >= 64 && tid < 128) S.ps.cache.phase[tid - 64] = a.phase[tid - 64];
+  if (warp == kWarpMma) {
+    tmem_alloc(&S.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == 32) warm_l2(a.q, static_cast<uint64_t>(a.n_rows) * a.n_q_heads * 256);
+  if (kAppend && tid == 96) {
+    warm_l2(a.k_new, static_cast<uint64_t>(a.n_rows) * a.n_kv_heads * 256);
+    warm_l2(a.v_new, static_cast<uint64_t>(a.n_rows) * a.n_kv_heads * 256);
+  }
+  bool plan_timeout = false;
+  auto get_plan = [&]() {
+    if (tid == 0 && !a.early) issue_plan_copies(a, S);
+    __syncthreads();  // the barriers are initialised
+    if (!mbar_wait(&S.plan_bar, 0)) {
+      plan_timeout = true;
+      S.plan_ok = 0;
+    }
+    if (tid == 0 && !header_matches(a, S.hdr, static_cast<int>(gridDim.x))) S.plan_ok = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
+  Producer prod = {{0, 0}, 0, {}, {}};
+  int step = 0;  // of the producer, before griddepcontrol.wait
+  auto start_producer = [&]() {
+    prod.k = prod.v = unit_pos(S.ps.plan, a.n_blocks, S.cp.u0);
+  };
+  if (a.early) {
+    get_plan();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == kWarpTma && S.plan_ok && S.cp.u0 < S.cp.u1) {
+      // the first tiles into the empty ring (not past the first one with a new token)
+      const int n = static_cast<int>(S.cp.u1 - S.cp.u0);
+      start_producer();
+      while (step < n + kLead && prod.count + 2 <= kSlots && !(kAppend && S.cp.app_n > 0 && step >= S.cp.app_tile)) {
+        produce(a, S, &tm_k, &tm_v, prod, n, step, step + 1, -1, lane);
+        ++step;
+      }
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!a.early) {
+    get_plan();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == kWarpTma && S.plan_ok && S.cp.u0 < S.cp.u1) start_producer();
+  }
+  if (plan_timeout) flag_error(a.err, HW_DEV_TIMEOUT);
+  const uint32_t tmem = S.tmem_base;
+  const bool ok = S.plan_ok != 0;
+  if (!ok && tid == 0 && blockIdx.x == 0) flag_error(a.err, HW_DEV_BAD_PLAN);
+  const int64_t u0 = ok ? S.cp.u0 : 0, u1 = ok ? S.cp.u1 : 0;
+  if (u0 < u1) {
+    const int n = static_cast<int>(u1 - u0);
+    const bool appending = kAppend && S.cp.app_n > 0;
+    if (warp == kWarpTma) {
+      produce(a, S, &tm_k, &tm_v, prod, n, step, n + kLead, appending ? S.cp.app_tile : -1, lane);
+      drain(S, prod);
+    } else if (warp == kWarpMma) {
+      mma_issuer(a, S, tmem, u0, n);
+      if (elect_one()) mma_commit(&S.mma_done);
+      __syncwarp();
+      mbar_wait(&S.mma_done, 0);
+    } else if (warp >= kWarpQ) {
+      if (appending) append_tokens(a, S, u0, u1);
+      qprep<kLimit>(a, S, u1);
+    } else {
+      if (warp < 8) query_prologue(a, S);
+      softmax_role<kAppend, kLimit>(a, S, tmem, u0, n);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  // the merge's 256 threads; its scratch lies in the ring, which nothing uses any more
+  if (ok && warp < 8)
+    merge_phase<__nv_bfloat16, 128, 8, true>(a, S.ps.plan, S.ps.cache, *reinterpret_cast<MergeSmem<8> *>(S.ring[0]),
+                                             &S.cp.mpre[0][0], S.cp.mpre_n, kPreItems, kPreList, tid, 256,
+                                             NamedSync<5, 256>(), a.wait_limit, S.cp.mrank,
+                                             merge_ctas(a, static_cast<int>(gridDim.x)));
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                              cudaStream_t s) {
+  if (ctas > 256 || !a.plan || !a.kv_scale || (a.k_new && a.view_limit)) return cudaErrorInvalidValue;
+  void (*const kernel)(DecodeArgs, CUtensorMap, CUtensorMap) =
+      a.k_new ? decode_fp4_kernel<true, false> : a.view_limit ? decode_fp4_kernel<false, true> : decode_fp4_kernel<false, false>;
+  constexpr int kSmem = static_cast<int>(sizeof(Fp4Smem) + 1024);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, tk, tv);
+}
+
+}  // namespace hw

@@ -91,29 +91,6 @@ __device__ __forceinline__ void e4m3x4_values(uint32_t w, float *x) {
   }
 }
 
-// The larger of `top` over the 8 neighbouring threads that hold a row.
-__device__ __forceinline__ float max_of_8(float top) {
-#pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  return top;
-}
-
-// A row of 128 elements among 8 threads, each with the 8 of `lo` (from 8c) and the 8
-// of `hi` (from 64 + 8c): its scale, and the thread's codes.
-__device__ __forceinline__ float fp4_row(const float (&lo)[8], const float (&hi)[8], uint32_t &wlo, uint32_t &whi) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_nan(top, max_nan(fabsf(lo[i]), fabsf(hi[i])));
-  const float s = fp4_scale(max_of_8(top));
-  wlo = whi = 0;
-  if (s > 0.f) {
-    const float inv = 1.f / s;
-    wlo = fp4_encode8(lo, s, inv);
-    whi = fp4_encode8(hi, s, inv);
-  }
-  return s;
-}
-
 // Rows of a CTA's tokens: (layer, token, kv head), 8 or so threads each.  blockIdx.x: the
 // tokens, blockIdx.y: a share of the layers.
 template <typename Store, int D>
@@ -175,9 +152,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float2 cs = turn[t][c * N + j];
-        if constexpr (kFp4) {  // every product rounded: the codes do not hang on how they are fused
-          k0[j] = __fsub_rn(__fmul_rn(x0[j], cs.x), __fmul_rn(x1[j], cs.y));
-          k1[j] = __fadd_rn(__fmul_rn(x1[j], cs.x), __fmul_rn(x0[j], cs.y));
+        if constexpr (kFp4) {
+          fp4_turn(x0[j], x1[j], cs.x, cs.y, k0[j], k1[j]);
         } else {  // as the appends of the decode calls
           k0[j] = __fmaf_rn(x0[j], cs.x, -__fmul_rn(x1[j], cs.y));
           k1[j] = __fmaf_rn(x1[j], cs.x, __fmul_rn(x0[j], cs.y));
@@ -327,11 +303,7 @@ __global__ void __launch_bounds__(kThreads) commit_fp4_kernel(const __grid_const
       fp4_levels8(kl, x0);
       fp4_levels8(kh, x1);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float p = x0[e] * s, q = x1[e] * s, cc = cs[ch * 8 + e], ss = sn[ch * 8 + e];
-        y0[e] = __fsub_rn(__fmul_rn(p, cc), __fmul_rn(q, ss));
-        y1[e] = __fadd_rn(__fmul_rn(q, cc), __fmul_rn(p, ss));
-      }
+      for (int e = 0; e < 8; ++e) fp4_turn(x0[e] * s, x1[e] * s, cs[ch * 8 + e], sn[ch * 8 + e], y0[e], y1[e]);
       const float t = fp4_row(y0, y1, kl, kh);
       sw = fp4_scale_word(t, fp4_v_scale(sw));
     }

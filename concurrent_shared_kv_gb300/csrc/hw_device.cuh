@@ -751,7 +751,8 @@ constexpr int kMergeBatch = 4;
 
 // rank / grid: this CTA's position among the nm CTAs that merge (items rank,
 // rank + nm, ...); a rank at or past nm merges nothing.
-template <typename T, int D, int NL, typename Sync>
+// kNan: a NaN among the weights makes the row NaN (else such a row is empty).
+template <typename T, int D, int NL, bool kNan = false, typename Sync>
 __device__ void merge_phase(const DecodeArgs &a, const PlanCore &P, const MetaCache &MC,
                             MergeSmem<NL> &Z, const int32_t *pre_list, const int32_t *pre_n,
                             int n_pre, int pre_stride, int tid, int nt, Sync sync,
@@ -894,7 +895,7 @@ __device__ void merge_phase(const DecodeArgs &a, const PlanCore &P, const MetaCa
           for (int e = 0; e < EPL; ++e) sum[e] += Z.acc[(w0 + w2) & (kW - 1)][lane * EPL + e] * f;
         }
         // L = 0: view limits left the row no token (its partials are empty)
-        const bool any = L > 0.f;
+        const bool any = kNan ? !(L <= 0.f) : L > 0.f;
         T ov[EPL];
 #pragma unroll
         for (int e = 0; e < EPL; ++e) ov[e] = from_f32<T>(any ? sum[e] / L : 0.f);

@@ -93,6 +93,36 @@ __device__ __forceinline__ void fp4_levels8(uint32_t w, float (&v)[8]) {
   }
 }
 
+// The larger of `top` over the 8 neighbouring threads that hold a row.
+__device__ __forceinline__ float max_of_8(float top) {
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top;
+}
+
+// A row of 128 elements among 8 threads, each with the 8 of `lo` (from 8c) and the 8
+// of `hi` (from 64 + 8c): its scale, and the thread's codes.  Whole warps call it.
+__device__ __forceinline__ float fp4_row(const float (&lo)[8], const float (&hi)[8], uint32_t &wlo, uint32_t &whi) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_nan(top, max_nan(fabsf(lo[i]), fabsf(hi[i])));
+  const float s = fp4_scale(max_of_8(top));
+  wlo = whi = 0;
+  if (s > 0.f) {
+    const float inv = 1.f / s;
+    wlo = fp4_encode8(lo, s, inv);
+    whi = fp4_encode8(hi, s, inv);
+  }
+  return s;
+}
+
+// The pair (x0, x1) turned by the angle of (cos, sin).  Every product is rounded:
+// what the codes become does not hang on how they are fused.
+__device__ __forceinline__ void fp4_turn(float x0, float x1, float c, float s, float &y0, float &y1) {
+  y0 = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
+  y1 = __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
+}
+
 // The two scales of a token as its word of kv_scale: the key's in the low half.
 __device__ __forceinline__ uint32_t fp4_scale_word(float ks, float vs) {
   return __float_as_uint(ks) >> 16 | (__float_as_uint(vs) & 0xffff0000u);

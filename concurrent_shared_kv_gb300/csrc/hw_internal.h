@@ -67,6 +67,8 @@ struct DecodeArgs {
   const int32_t *view_limit;
   // E4M3 caches: per kv head, the scale of its K and V codes (null: bf16 caches)
   const float *k_scale, *v_scale;
+  // E2M1 caches: the tokens' scales, [Hkv][capacity] words (hw_fp4.cuh)
+  const uint32_t *kv_scale;
   float scale_log2;   // softmax scale * log2(e): scores live in the log2 domain
   // RoPE phase increments: for pair i, the fraction of a turn per position,
   // frac(w_i / 2pi), as an unsigned 0.64 fixed-point number.  The angle of
@@ -118,11 +120,15 @@ int cuda_fail(cudaError_t e);           // records the error; HW_ERR_CUDA
 // TMA map of a head_dim-128 pool in 128-token tiles.
 bool make_pool_map(CUtensorMap *m, const void *pool, int64_t capacity, int n_kv_heads,
                    bool e4m3 = false);
+// The same of a pool of E2M1 codes.
+bool make_pool_map_fp4(CUtensorMap *m, const void *pool, int64_t capacity, int n_kv_heads);
 
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_decode_simt(const DecodeArgs &a, int dtype, int ctas, cudaStream_t s);
 cudaError_t launch_decode_tc(const DecodeArgs &a, const CUtensorMap &k_map,
                              const CUtensorMap &v_map, int ctas, cudaStream_t s);
+cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &k_map,
+                              const CUtensorMap &v_map, int ctas, cudaStream_t s);
 size_t decode_tc_smem_bytes();
 
 // Destinations of hw_attn_plan: metadata copies (int32) and, for the

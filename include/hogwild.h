@@ -344,6 +344,28 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
                                       void *stream);
 
 /*
+ * hw_attn_decode_planned and hw_attn_append_decode_planned for HW_FP4_E2M1 caches:
+ * attention over the decoded, scaled cache, q, k_new, v_new and out in bf16.  Planned
+ * by hw_attn_plan (hw_attn_plan_limited with HW_DESC_VIEW_LIMITS), the second one
+ * by hw_attn_plan_append with the same descriptor; its new tokens are stored as
+ * hw_cache_write stores them.
+ *  k_cache, v_cache  dev [Hkv][capacity][64] bytes, 32-byte aligned
+ *  kv_scale          dev bf16 [Hkv][capacity][2]: a token's key and value scale
+ * On the tensor cores a rotated query is held in about 12 bits of every element and a
+ * token's weight in 8 (three and two E4M3 parts); sums, maxima and lse are fp32.  A
+ * query that attends a token whose scale is NaN gets NaN in out and lse, others do
+ * not.  HW_ERR_INVALID for another dtype or a null kv_scale.
+ */
+int hw_attn_decode_planned_fp4(const hw_attn_desc *d, const void *q, const void *k_cache,
+                               const void *v_cache, const void *kv_scale, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+int hw_attn_append_decode_planned_fp4(const hw_attn_desc *d, const void *q, const void *k_new,
+                                      const void *v_new, void *k_cache, void *v_cache,
+                                      void *kv_scale, void *out, float *lse, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
  * Trees of drafted tokens.  A step may propose several continuations of each
  * row (worker) at once, as a tree: its nodes are tokens, parent[i] < i is the
  * node before node i (-1: none; node 0 is usually the row's pending token),
