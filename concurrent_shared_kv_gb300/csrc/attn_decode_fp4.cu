@@ -47,12 +47,12 @@ namespace hw {
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kWarpTma = 16, kWarpMma = 17, kWarpQ = 18;
+constexpr int kWarpTma = 16, kWarpQk = 17, kWarpPv = 18, kWarpQ = 19;
 constexpr int kSoftWarps = 16;
 constexpr uint32_t kTile = 128 * 128;      // a K or V tile in shared memory, 128-byte swizzled
 constexpr uint32_t kTileTx = 128 * 64;     // the bytes of it that come from memory
 constexpr int kSlots = 9;                  // of the ring
-constexpr int kLead = 4;                   // tiles whose scores are asked for before the first one's weights
+constexpr int kLead = 2;                   // tiles whose scores are asked for before the first one's weights
 constexpr int kQParts = 3;
 constexpr uint32_t kQPart = kN * 128;      // a part of Q~: [32 columns][128], 128-byte swizzled
 constexpr uint32_t kQBytes = kQParts * kQPart;
@@ -62,8 +62,10 @@ constexpr int kHalf = kN / 2;              // columns of a softmax thread
 // rescaled once one would pass 2^(kLift + kLazy) = 256 (E4M3 ends at 448): weights down to
 // 2^-10 of the maximum keep both parts' precision.  The factor is in the record's m.
 constexpr float kLift = 4.f, kLazy = 4.f;
-// TMEM columns: S of (stream, buffer), then O of (segment parity, stream): 32 + 32 columns
-constexpr uint32_t kTmemO = 4 * kN, kTmemCols = 512;
+// TMEM columns: S of either stream, its parts side by side, then O of (segment parity,
+// stream): 32 columns for each part of P
+constexpr uint32_t kSCols = kQParts * kN, kTmemO = 2 * kSCols, kTmemCols = 512;
+static_assert(kTmemO + 4 * 2 * kN <= kTmemCols, "TMEM columns");
 
 struct Fp4Smem {
   alignas(1024) uint8_t ring[kSlots][kTile];
@@ -73,19 +75,27 @@ struct Fp4Smem {
   CtaPlan cp;
   PlanHeader hdr;
   alignas(16) float red[2][2][kHalf][4];  // stream, half: a tile's column maxima of the four warps
+  alignas(16) float neg_ref[kSoftWarps][kHalf];  // a warp's own copy: minus its columns' references
   float hm[2][2][kN];          // segment parity, stream: reference maxima of the columns
   float hl[2][2][4][kN];       // and the warps' sums of weights
   int32_t nref[2];             // segment parity: references,
   float q_mul[2];              // the power of two that scores are to be multiplied with
-  float qmax[8], qmax_next[2];  // the prologue's warps', the query warps'
+  float qmax[8];
   int32_t abort_flag, plan_ok;
   uint32_t tmem_base;
+  // what a softmax warp needs only between segments: its place in the units, the
+  // segment whose records are due (registers are few in its loop over tiles)
+  UnitPos walk[kSoftWarps];
+  struct Due {
+    int64_t sid;
+    int32_t nq, cnt, first;
+  } due[kSoftWarps];
   alignas(8) uint64_t kv_full[kSlots];
   uint64_t kv_empty[kSlots];
-  uint64_t s_full[2][2], s_empty[2][2], p_full[2][2], p_empty[2][2];  // by stream and buffer
+  uint64_t s_full[2], s_empty[2], p_full[2][2], p_empty[2][2];        // by stream (and buffer)
   uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2], hand[2];     // by segment parity
   uint64_t rec_ready[4];                                              // by segment mod 4
-  uint64_t plan_bar, app_bar, mma_done;
+  uint64_t plan_bar, app_bar, mma_done[2];
 };
 static_assert(sizeof(Fp4Smem) + 1024 <= 232448, "shared memory of one CTA per SM");
 static_assert(sizeof(PlanHeader) % 16 == 0 && offsetof(Fp4Smem, hdr) % 16 == 0, "bulk copies");
@@ -112,6 +122,17 @@ __device__ __forceinline__ void idle_wait(Fp4Smem &S, const DecodeArgs &a, uint6
     }
   }
   __syncwarp();
+}
+// idle_wait by some lanes of a warp.
+__device__ __forceinline__ void idle_wait_lane(Fp4Smem &S, const DecodeArgs &a, uint64_t *bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (aborted(S)) break;
+    if (clock64() - t0 > kWaitLimit) {
+      set_abort(S, a);
+      break;
+    }
+  }
 }
 // The same spinning, with one answer for the warp.
 __device__ __forceinline__ bool warp_spin(Fp4Smem &S, const DecodeArgs &a, uint64_t *bar, uint32_t parity) {
@@ -149,13 +170,10 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // A place in the ring.
@@ -224,82 +242,97 @@ __device__ void drain(Fp4Smem &S, const Producer &p) {
   for (int j = min(p.count, kSlots); j > 0; --j, back.next()) mbar_wait(&S.kv_full[back.s], back.phase);
 }
 
-// ---------------------------------------------------------------- MMA issuer
+// --------------------------------------------------------------- MMA issuers
+//
+// A warp for either product: neither then waits for what the other one waits for, and the
+// tensor cores have the one's instructions while the other looks at its barriers
+// (about 60 clocks each).  An instruction of 32 bytes along K takes 32 + N / 4 clocks
+// (measured, N from 32 to 128), so parts stand side by side on N, not one after the other
+// on K: 4 x 56 clocks for S, 4 x 48 for O.
 
-__device__ void mma_issuer(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int64_t u0, int n) {
-  constexpr uint32_t idesc_qk = idesc_fp4(128, kN, 0, 0), idesc_pv = idesc_fp4(128, 2 * kN, 1, 1);
+// Walks a CTA's tiles segment by segment.
+struct SegWalk {
+  UnitPos x;
+  int seg, left;  // segment, tiles left of it
+  __device__ __forceinline__ SegWalk(const DecodeArgs &a, const PlanCore &P, int64_t u0)
+      : x(unit_pos(P, a.n_blocks, u0)), seg(-1), left(0) {}
+  // On to tile i of n: whether it starts a segment.
+  __device__ __forceinline__ bool next(const DecodeArgs &a, const PlanCore &P, int i, int n) {
+    const bool first = left == 0;
+    if (first) {
+      if (seg >= 0) {
+        x.t = x.tiles - 1;
+        unit_pos_next(P, a.n_blocks, x);
+      }
+      ++seg;
+      left = min(n - i, x.tiles - x.t);
+    }
+    --left;
+    return first;
+  }
+};
+
+__device__ void qk_issuer(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int64_t u0, int n) {
+  constexpr uint32_t idesc = idesc_fp4(128, kSCols, 0, 0);
   const uint64_t k_desc = smem_desc(smem_u32(S.ring[0]), 16, 1024, kSw128);
-  const uint64_t v_desc = smem_desc(smem_u32(S.ring[0]), kTile, 1024, kSw128);
   const uint64_t q_desc = smem_desc(smem_u32(S.q[0]), 16, 1024, kSw128);
-  const uint64_t p_desc = smem_desc(smem_u32(S.p[0][0]), 512, 512, kSw64);
-  const PlanCore &P = S.ps.plan;
+  SegWalk w(a, S.ps.plan, u0);
   RingPos at = {0, 0};
-  // segments of the tiles that QK and PV are at: index, tiles left of it
-  const UnitPos x0 = unit_pos(P, a.n_blocks, u0);
-  UnitPos xk = x0, xv = x0;
-  int seg_k = -1, left_k = 0, seg_v = -1, left_v = 0, in_v = 0;
-  for (int j = 0; j < n + kLead; ++j) {
-    if (j >= kLead) {  // PV(i)
-      const int i = j - kLead, st = i & 1, buf = (i >> 1) & 1;
-      if (left_v == 0) {
-        if (seg_v >= 0) {
-          xv.t = xv.tiles - 1;
-          unit_pos_next(P, a.n_blocks, xv);
-        }
-        ++seg_v;
-        left_v = min(n - i, xv.tiles - xv.t);
-        in_v = 0;
-        if (!warp_spin(S, a, &S.o_empty[seg_v & 1], ((seg_v >> 1) & 1) ^ 1)) return;
-      }
-      if (!warp_spin(S, a, &S.p_full[st][buf], (i >> 2) & 1)) return;
-      if (!warp_spin(S, a, &S.kv_full[at.s], at.phase)) return;
-      tc_fence_after();
-      --left_v;
-      const bool first = in_v < 2;  // of its stream in this segment
-      ++in_v;
-      if (elect_one()) {
-        const uint32_t o = tmem + kTmemO + ((seg_v & 1) * 2 + st) * 2 * kN;
-        const uint64_t v = v_desc + ((at.s * kTile) >> 4), p = p_desc + (((st * 2 + buf) * kPBytes) >> 4);
+  for (int i = 0; i < n; ++i) {
+    const int st = i & 1;
+    const bool first = w.next(a, S.ps.plan, i, n);
+    if (first && !warp_spin(S, a, &S.q_full[w.seg & 1], (w.seg >> 1) & 1)) return;
+    if (!warp_spin(S, a, &S.s_empty[st], ((i >> 1) & 1) ^ 1)) return;
+    if (!warp_spin(S, a, &S.kv_full[at.s], at.phase)) return;
+    tc_fence_after();
+    if (elect_one()) {
+      const uint64_t k0 = k_desc + ((at.s * kTile) >> 4), q = q_desc + (((w.seg & 1) * kQBytes) >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // 4 steps of 32 tokens
-          mma_f8(o, v + ((k * 4096) >> 4), p + ((k * 2048) >> 4), idesc_pv, !(first && k == 0));
-        mma_commit(&S.kv_empty[at.s]);
-        mma_commit(&S.p_empty[st][buf]);
-        if (left_v == 0) mma_commit(&S.o_full[seg_v & 1]);
-      }
-      __syncwarp();
-      at.next();
+      for (int k = 0; k < 4; ++k)  // 4 steps of 32 elements
+        mma_f8(tmem + st * kSCols, k0 + ((k * 32) >> 4), q + ((k * 32) >> 4), idesc, k > 0);
+      mma_commit(&S.s_full[st]);
+      mma_commit(&S.kv_empty[at.s]);
+      if (w.left == 0) mma_commit(&S.q_empty[w.seg & 1]);
     }
-    if (j < n) {  // QK(j)
-      const int st = j & 1, buf = (j >> 1) & 1;
-      if (left_k == 0) {
-        if (seg_k >= 0) {
-          xk.t = xk.tiles - 1;
-          unit_pos_next(P, a.n_blocks, xk);
-        }
-        ++seg_k;
-        left_k = min(n - j, xk.tiles - xk.t);
-        if (!warp_spin(S, a, &S.q_full[seg_k & 1], (seg_k >> 1) & 1)) return;
-      }
-      if (!warp_spin(S, a, &S.s_empty[st][buf], ((j >> 2) & 1) ^ 1)) return;
-      if (!warp_spin(S, a, &S.kv_full[at.s], at.phase)) return;
-      tc_fence_after();
-      --left_k;
-      if (elect_one()) {
-        const uint32_t s = tmem + (st * 2 + buf) * kN;
-        const uint64_t k0 = k_desc + ((at.s * kTile) >> 4), q = q_desc + (((seg_k & 1) * kQBytes) >> 4);
-#pragma unroll
-        for (int part = 0; part < kQParts; ++part)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // 4 steps of 32 elements
-            mma_f8(s, k0 + ((k * 32) >> 4), q + ((part * kQPart + k * 32) >> 4), idesc_qk, part > 0 || k > 0);
-        mma_commit(&S.kv_empty[at.s]);
-        mma_commit(&S.s_full[st][buf]);
-        if (left_k == 0) mma_commit(&S.q_empty[seg_k & 1]);
-      }
-      __syncwarp();
-      at.next();
+    __syncwarp();
+    // (the next K: behind the next V from the kLead-th on)
+    at.next();
+    if (i + 1 >= kLead) at.next();
+  }
+}
+
+__device__ void pv_issuer(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int64_t u0, int n) {
+  constexpr uint32_t idesc = idesc_fp4(128, 2 * kN, 1, 1);
+  const uint64_t v_desc = smem_desc(smem_u32(S.ring[0]), kTile, 1024, kSw128);
+  const uint64_t p_desc = smem_desc(smem_u32(S.p[0][0]), 512, 512, kSw64);
+  SegWalk w(a, S.ps.plan, u0);
+  RingPos at = {0, 0};
+  for (int k = min(kLead, n); k > 0; --k) at.next();  // V(0) is behind the first K's
+  int in = 0;  // the tile's index in its segment
+  for (int i = 0; i < n; ++i) {
+    const int st = i & 1, buf = (i >> 1) & 1;
+    if (w.next(a, S.ps.plan, i, n)) {
+      in = 0;
+      if (!warp_spin(S, a, &S.o_empty[w.seg & 1], ((w.seg >> 1) & 1) ^ 1)) return;
     }
+    if (!warp_spin(S, a, &S.kv_full[at.s], at.phase)) return;
+    if (!warp_spin(S, a, &S.p_full[st][buf], (i >> 2) & 1)) return;
+    tc_fence_after();
+    const bool first = in < 2;  // of its stream in this segment
+    ++in;
+    if (elect_one()) {
+      const uint32_t o = tmem + kTmemO + ((w.seg & 1) * 2 + st) * 2 * kN;
+      const uint64_t v = v_desc + ((at.s * kTile) >> 4), p = p_desc + (((st * 2 + buf) * kPBytes) >> 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // 4 steps of 32 tokens
+        mma_f8(o, v + ((k * 4096) >> 4), p + ((k * 2048) >> 4), idesc, !(first && k == 0));
+      mma_commit(&S.p_empty[st][buf]);
+      mma_commit(&S.kv_empty[at.s]);
+      if (w.left == 0) mma_commit(&S.o_full[w.seg & 1]);
+    }
+    __syncwarp();
+    at.next();
+    if (i + kLead < n) at.next();  // (the K between this V and the next)
   }
 }
 
@@ -333,17 +366,23 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
   return __half22float2(h);
 }
 
-// The item turned, scaled by scale * log2(e) / 2^e and split into parts, into Q~'s
-// row `place`: 8 codes at byte 8c, 8 at 64 + 8c, 16-byte chunks swizzled.
-__device__ __forceinline__ void store_item(const DecodeArgs &a, const Fp4Smem &S, const QItem &it, uint32_t qbase,
-                                           int place, int c, float inv) {
+// cos and sin of an item's 8 elements.
+__device__ __forceinline__ void item_turns(const Fp4Smem &S, int64_t rel, int c, float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) rope_cos_sin_fast(rel, S.ps.cache.phase[8 * c + e], &cs[e], &sn[e]);
+}
+
+// The item turned, scaled by mul and split into parts, each the remainder of those before
+// it times 16, into row `place` of Q~'s parts: 8 codes at byte 8c, 8 at 64 + 8c, 16-byte
+// chunks swizzled.
+__device__ __forceinline__ void store_item(const QItem &it, const float (&cs)[8], const float (&sn)[8], uint32_t qbase,
+                                           int place, int c, float mul) {
   const uint32_t lo32[4] = {it.lo.x, it.lo.y, it.lo.z, it.lo.w}, hi32[4] = {it.hi.x, it.hi.y, it.hi.z, it.hi.w};
   uint32_t w[kQParts][4];
 #pragma unroll
   for (int j = 0; j < kQParts; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[j][k] = 0;
-  const float mul = a.scale_log2 * inv;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float2 y0, y1;
@@ -351,10 +390,8 @@ __device__ __forceinline__ void store_item(const DecodeArgs &a, const Fp4Smem &S
     for (int h = 0; h < 2; ++h) {
       const float x0 = __uint_as_float(h ? (lo32[e] & 0xffff0000u) : (lo32[e] << 16));
       const float x1 = __uint_as_float(h ? (hi32[e] & 0xffff0000u) : (hi32[e] << 16));
-      float cs, sn;
-      rope_cos_sin_fast(it.rel, S.ps.cache.phase[8 * c + 2 * e + h], &cs, &sn);
-      (h ? y0.y : y0.x) = (x0 * cs - x1 * sn) * mul;
-      (h ? y1.y : y1.x) = (x1 * cs + x0 * sn) * mul;
+      (h ? y0.y : y0.x) = (x0 * cs[2 * e + h] - x1 * sn[2 * e + h]) * mul;
+      (h ? y1.y : y1.x) = (x1 * cs[2 * e + h] + x0 * sn[2 * e + h]) * mul;
     }
 #pragma unroll
     for (int j = 0; j < kQParts; ++j) {
@@ -364,8 +401,8 @@ __device__ __forceinline__ void store_item(const DecodeArgs &a, const Fp4Smem &S
       w[j][2 + (e >> 1)] |= q1 << (16 * (e & 1));
       if (j + 1 < kQParts) {
         const float2 v0 = e4m3x2_values(q0), v1 = e4m3x2_values(q1);
-        y0 = make_float2(y0.x - v0.x, y0.y - v0.y);
-        y1 = make_float2(y1.x - v1.x, y1.y - v1.y);
+        y0 = make_float2((y0.x - v0.x) * 16.f, (y0.y - v0.y) * 16.f);
+        y1 = make_float2((y1.x - v1.x) * 16.f, (y1.y - v1.y) * 16.f);
       }
     }
   }
@@ -397,7 +434,11 @@ __device__ void query_prologue(const DecodeArgs &a, Fp4Smem &S) {
 #pragma unroll
   for (int w = 0; w < 8; ++w) reach = fmaxf(reach, S.qmax[w]);
   const int e = part_exponent(a, reach);
-  if (t < items) store_item(a, S, it, smem_u32(S.q[0]), column_place(t >> 3), t & 7, ldexpf(1.f, -e));
+  if (t < items) {
+    float cs[8], sn[8];
+    item_turns(S, it.rel, t & 7, cs, sn);
+    store_item(it, cs, sn, smem_u32(S.q[0]), column_place(t >> 3), t & 7, a.scale_log2 * ldexpf(1.f, -e));
+  }
   if (t == 0) {
     S.nref[0] = X.m.n_ref;
     S.q_mul[0] = ldexpf(1.f, e);
@@ -408,16 +449,14 @@ __device__ void query_prologue(const DecodeArgs &a, Fp4Smem &S) {
 }
 
 // Queries of segments 1, 2, ..., and the arrivals of finished ones two segments
-// late, by warps 18 and 19 (as in the other tensor-core kernel).
+// late, by warp 19 (as in the other tensor-core kernel).
 template <bool kLimit>
 __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
-  const int tq = threadIdx.x - kWarpQ * 32;
-  const int lane = threadIdx.x & 31, wq = tq >> 5;
+  const int lane = threadIdx.x & 31;
   const int G = a.n_q_heads / a.n_kv_heads;
-  NamedSync<6, 64> sync;
   auto arrivals = [&](int done) {
     idle_wait(S, a, &S.rec_ready[done & 3], (done >> 2) & 1);
-    if (wq == 0) arrive_segment(a, S.cp.pre[done % kPre].m, lane);
+    arrive_segment(a, S.cp.pre[done % kPre].m, lane);
   };
   int64_t u = S.cp.us[1];
   int64_t u_prep = S.cp.us[kPre - 1] < u1 ? next_segment(S.ps.plan, a.n_blocks, S.cp.us[kPre - 1]) : u1;
@@ -428,51 +467,53 @@ __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
       break;
     }
     const SegQ &X = S.cp.pre[seg % kPre];
-    const int nq = min(X.m.n_ref * G, kN), par = seg & 1;
-    QItem raw[4];
+    const int n_ref = X.m.n_ref, par = seg & 1;
+    // a lane's items: (reference, chunk), for each its q heads, which share a turn
     float reach = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if ((tq >> 3) + 8 * k < nq) {
-        load_item(a, X, (tq >> 3) + 8 * k, tq & 7, raw[k]);
-        reach = fmaxf(reach, item_reach(raw[k]));
+    for (int it = lane; it < n_ref * 8; it += 32)
+      for (int g = 0; g < G; ++g) {
+        QItem raw;
+        load_item(a, X, (it >> 3) * G + g, it & 7, raw);
+        reach = fmaxf(reach, item_reach(raw));
       }
-    reach = warp_max_nonneg(reach);
-    if (lane == 0) S.qmax_next[wq] = reach;
-    sync();
-    reach = fmaxf(S.qmax_next[0], S.qmax_next[1]);
-    const int e = part_exponent(a, reach);
+    const int e = part_exponent(a, warp_max_nonneg(reach));
+    const float mul = a.scale_log2 * ldexpf(1.f, -e);
     if (seg >= 2) idle_wait(S, a, &S.q_empty[par], ((seg >> 1) - 1) & 1);
-    if (tq == 0) {
-      S.nref[par] = X.m.n_ref;
+    if (lane == 0) {
+      S.nref[par] = n_ref;
       S.q_mul[par] = ldexpf(1.f, e);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if ((tq >> 3) + 8 * k < nq)
-        store_item(a, S, raw[k], smem_u32(S.q[par]), column_place((tq >> 3) + 8 * k), tq & 7, ldexpf(1.f, -e));
+    for (int it = lane; it < n_ref * 8; it += 32) {
+      float cs[8], sn[8];
+      item_turns(S, X.rel[(it >> 3) * G], it & 7, cs, sn);
+      for (int g = 0; g < G; ++g) {
+        const int qi = (it >> 3) * G + g;
+        QItem raw;
+        load_item(a, X, qi, it & 7, raw);
+        store_item(raw, cs, sn, smem_u32(S.q[par]), column_place(qi), it & 7, mul);
+      }
+    }
     fence_proxy_async_smem();
-    sync();
-    if (tq == 0) mbar_arrive(&S.q_full[par]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.q_full[par]);
     if (seg >= 2) {
       arrivals(seg - 2);
-      sync();  // the slot of segment seg - 2 is read; it now takes segment seg + 2
+      __syncwarp();  // the slot of segment seg - 2 is read; it now takes segment seg + 2
       if (u_prep < u1) {
         const UnitPos x = unit_pos(S.ps.plan, a.n_blocks, u_prep);
-        if (wq == 0) seg_pre<kLimit>(a, S.ps.plan, S.ps.cache, S.cp.pre[(seg + 2) % kPre], x.b, x.g, x.h, lane);
+        seg_pre<kLimit>(a, S.ps.plan, S.ps.cache, S.cp.pre[(seg + 2) % kPre], x.b, x.g, x.h, lane);
         u_prep = x.seg_first + x.tiles;
       }
-      sync();
+      __syncwarp();
     }
     u = next_segment(S.ps.plan, a.n_blocks, u);
   }
 }
 
-// The CTA's new tokens (hw_attn_append_decode_planned_fp4), by warps 18 and 19, four
-// (row, kv head) pairs a warp, 8 threads each: the bits that hw_cache_write stores.
+// The CTA's new tokens (hw_attn_append_decode_planned_fp4), by warp 19, four
+// (row, kv head) pairs at a time, 8 threads each: the bits that hw_cache_write stores.
 __device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64_t u1) {
-  const int tq = threadIdx.x - kWarpQ * 32;
-  const int lane = tq & 31, wq = tq >> 5, c = lane & 7;
+  const int lane = threadIdx.x & 31, c = lane & 7;
   const PlanCore &P = S.ps.plan;
   const int Hkv = a.n_kv_heads, npairs = a.n_rows * Hkv;
   uint32_t *kc = static_cast<uint32_t *>(const_cast<void *>(a.k)), *vc = static_cast<uint32_t *>(const_cast<void *>(a.v));
@@ -506,7 +547,7 @@ __device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64
     }
   };
   if (S.cp.app_n <= kAppList) {
-    for (int e0 = wq * 4; e0 < S.cp.app_n; e0 += 8) {
+    for (int e0 = 0; e0 < S.cp.app_n; e0 += 4) {
       const int e = e0 + (lane >> 3);
       const bool on = e < S.cp.app_n;
       write(on, on ? S.cp.app_pair[e] : 0, on ? S.cp.app_pos[e] : 0, on ? S.cp.app_row[e] : 0);
@@ -514,7 +555,7 @@ __device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64
   } else {
     // more than the plan lists: every pair is checked (each CTA that reads a token's
     // tile writes it, the same bytes, before its own copy of the tile)
-    for (int base = wq * 4; base < npairs; base += 8) {
+    for (int base = 0; base < npairs; base += 4) {
       const int pr = base + (lane >> 3);
       int pos = 0, row = 0;
       bool mine = false;
@@ -534,8 +575,8 @@ __device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64
   }
   __threadfence_block();
   asm volatile("fence.proxy.async.global;" ::: "memory");
-  NamedSync<6, 64>()();
-  if (tq == 0) mbar_arrive(&S.app_bar);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&S.app_bar);
 }
 
 // ------------------------------------------------------------------- softmax
@@ -554,10 +595,32 @@ __device__ __forceinline__ bool vote_128(int id, bool pred) {
   return out != 0;
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// r + r1 * f, elementwise.
+__device__ __forceinline__ void join_parts(uint32_t (&r)[kHalf], const uint32_t (&r1)[kHalf], float f) {
+#pragma unroll
+  for (int j = 0; j < kHalf; j += 2) {
+    const float2 v = __ffma2_rn(make_float2(__uint_as_float(r1[j]), __uint_as_float(r1[j + 1])), make_float2(f, f),
+                                make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+    r[j] = __float_as_uint(v.x);
+    r[j + 1] = __float_as_uint(v.y);
+  }
+}
+
 // Butterfly over the warp: on entry v[j] is this lane's value of column j, on exit
-// v[0] is the whole warp's of column lane & 15.
-template <bool kMax>
-__device__ __forceinline__ void reduce_columns(float (&v)[kHalf], int lane) {
+// v[0] is the whole warp's sum of column lane & 15.
+__device__ __forceinline__ void sum_columns(float (&v)[kHalf], int lane) {
 #pragma unroll
   for (int off = kHalf / 2; off >= 1; off >>= 1) {
 #pragma unroll
@@ -565,11 +628,10 @@ __device__ __forceinline__ void reduce_columns(float (&v)[kHalf], int lane) {
       const bool up = (lane & off) != 0;
       const float mine = up ? v[k + off] : v[k];
       const float other = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + off], off);
-      v[k] = kMax ? fmaxf(mine, other) : mine + other;
+      v[k] = mine + other;
     }
   }
-  const float other = __shfl_xor_sync(0xffffffffu, v[0], 16);
-  v[0] = kMax ? fmaxf(v[0], other) : v[0] + other;
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 // x, y (at most 448) as two E4M3 parts each, x = hi + lo / 16: the codes of hi in the
@@ -586,12 +648,13 @@ __device__ __forceinline__ void split_weights(float x, float y, uint16_t &hi, ui
 
 // Records of a finished segment: every warp joins the two streams' outputs of 8 of its
 // half's columns (stream 0's warps the first 8 places, stream 1's the others).
-__device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int seg, int64_t sid,
-                                             int nq, int cnt, int first_stream) {
+__device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int seg) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int st = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3, par = seg & 1;
   const uint32_t tl = tmem + (static_cast<uint32_t>(qd * 32) << 16) + kTmemO + par * 4 * kN;
   const int place = half * kHalf + st * 8;  // of the first column
+  const Fp4Smem::Due due = S.due[warp];
+  const int nq = due.nq;
   idle_wait(S, a, &S.hand[par], (seg >> 1) & 1);
   idle_wait(S, a, &S.o_full[par], (seg >> 1) & 1);
   tc_fence_after();
@@ -600,7 +663,7 @@ __device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, ui
   for (int j = 0; j < 8; ++j) o[j] = 0.f;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    if (cnt < 2 && s != first_stream) continue;  // the stream had no tile of this segment
+    if (due.cnt < 2 && s != due.first) continue;  // the stream had no tile of this segment
     uint32_t hi[8], lo[8];
     tmem_ld8(tl + s * 2 * kN + place, hi);
     tmem_ld8(tl + s * 2 * kN + kN + place, lo);
@@ -615,7 +678,7 @@ __device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, ui
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&S.o_empty[par]);
-  const int64_t slot = sid + S.cp.c_log;
+  const int64_t slot = due.sid + S.cp.c_log;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int qi = 2 * (st * 8 + j) + half;
@@ -653,26 +716,35 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
 
   // A wait that gives up (HW_DEV_TIMEOUT) does not leave the loops: all threads keep
   // the same control flow, so the votes are always reached by all 128.
-  // ref[j]: the exponent that column j's weights are taken against (its maximum less
-  // kLift), the same in every lane of the four warps; ref_mine: that of column lane & 15.
-  // They start at -FLT_MAX, not -inf: a column whose tokens are all masked
-  // then has weights 2^-inf = 0.
-  float ref[kHalf], l[kHalf], ref_mine = -FLT_MAX;
-  int pend = -1, pend_nq = 0, pend_cnt = 0, pend_first = 0;
-  int64_t pend_sid = 0;
-  UnitPos x = unit_pos(P, a.n_blocks, u0);
-  // the scales of the stream's next tile (of this segment), loaded a tile ahead
-  auto scales_of = [&](int i, int t) -> uint32_t {
-    const int at = t * kT + row;
-    if (at >= P.len[x.b]) return 0x3f803f80u;  // (past the block: 1, and masked)
-    if (kAppend && i >= app_tile) idle_wait(S, a, &S.app_bar, 0);
-    return __ldcg(a.kv_scale + static_cast<int64_t>(x.h) * a.capacity + P.start[x.b] + at);
-  };
+  // ref: the exponent that a column's weights are taken against (its maximum less
+  // kLift), the same in the four warps; ref_mine is column (lane & 15)'s, neg_ref in shared
+  // memory has all of the half's (16 registers that would spill otherwise).  They
+  // start at -FLT_MAX, not -inf: a column whose tokens are all masked then has weights
+  // 2^-inf = 0.
+  float l[kHalf], ref_mine = -FLT_MAX;
+  const float4 *neg_ref = reinterpret_cast<const float4 *>(S.neg_ref[warp]);
+  int pend = -1;
+  if (lane == 0) S.walk[warp] = unit_pos(P, a.n_blocks, u0);
+  __syncwarp();
   for (int i0 = 0, seg = 0; i0 < n; ++seg) {
     const int par = seg & 1;
-    const int cnt = min(n - i0, x.tiles - x.t), len = P.len[x.b];
+    int len, t0, i_end;  // the block's tokens; the first tile less i0; where the segment ends
+    const uint32_t *scales;  // of this thread's token in tile 0
+    {
+      const UnitPos x = S.walk[warp];
+      len = P.len[x.b];
+      t0 = x.t - i0;
+      i_end = i0 + min(n - i0, x.tiles - x.t);
+      scales = a.kv_scale + static_cast<int64_t>(x.h) * a.capacity + P.start[x.b] + row;
+    }
+    // the scales of the stream's next tile, loaded a tile ahead (past the block: 1, and masked)
+    auto scales_of = [&](int i) -> uint32_t {
+      if (i >= i_end || (i + t0) * kT + row >= len) return 0x3f803f80u;
+      if (kAppend && i >= app_tile) idle_wait_lane(S, a, &S.app_bar, 0);
+      return __ldcg(scales + static_cast<int64_t>(i + t0) * kT);
+    };
     int i = i0 + ((i0 ^ st) & 1);
-    uint32_t sw_next = i < i0 + cnt ? scales_of(i, x.t + i - i0) : 0;
+    uint32_t sw_next = scales_of(i);
     idle_wait(S, a, &S.q_full[par], (seg >> 1) & 1);
     const int nq = min(S.nref[par] * G, kN);
     const int nh = (nq + 1 - half) >> 1;  // the half's columns
@@ -688,91 +760,110 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.q_empty[par]);  // this warp has read the hand-off
 #pragma unroll
-    for (int j = 0; j < kHalf; ++j) {
-      ref[j] = -FLT_MAX;
-      l[j] = 0.f;
-    }
+    for (int j = 0; j < kHalf; ++j) l[j] = 0.f;
     ref_mine = -FLT_MAX;
+    // (columns that the half does not have get scores of -inf, and weights of 0)
+    if (lane < kHalf) S.neg_ref[warp][lane] = lane < nh ? FLT_MAX : -INFINITY;
+    __syncwarp();
     bool started = false;  // O holds a tile of this segment
-    for (; i < i0 + cnt; i += 2) {
-      const int buf = (i >> 1) & 1, t = x.t + i - i0;
+    for (; i < i_end; i += 2) {
+      const int buf = (i >> 1) & 1, t = i + t0;
       const uint32_t sw = sw_next;
-      if (i + 2 < i0 + cnt) sw_next = scales_of(i + 2, t + 2);
-      const bool tok_ok = t * kT + row < len;
+      sw_next = scales_of(i + 2);
       const float vs = fp4_v_scale(sw);
       // (a value of zeros has weight like any other)
       const float ks = fp4_k_scale(sw) * q_mul, lv = vs == 0.f ? 0.f : __log2f(vs);
       const float rv = vs == 0.f ? 1.f : __fdividef(1.f, vs);
-      idle_wait(S, a, &S.s_full[st][buf], (i >> 2) & 1);
+      idle_wait(S, a, &S.s_full[st], (i >> 1) & 1);
       tc_fence_after();
-      uint32_t r[kHalf];
-      tmem_ld16(tl + (st * 2 + buf) * kN + half * kHalf, r);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_empty[st][buf]);
-      // scores in log2 units with the value's scale in them, against the reference
-      float d[kHalf];
+      // scores in log2 units with the value's scale in them, less the references
+      float e[kHalf];
+      auto scores = [&]() {
+        const uint32_t col = tl + st * kSCols + half * kHalf;
+        uint32_t r[kHalf], r1[kHalf];
+        tmem_ld16(col, r);
+        tmem_ld16(col + kN, r1);
+        tmem_wait_ld();
+        join_parts(r, r1, 0.0625f);
+        if constexpr (kQParts == 3) {
+          tmem_ld16(col + 2 * kN, r1);
+          tmem_wait_ld();
+          join_parts(r, r1, 0.00390625f);
+        }
 #pragma unroll
-      for (int j = 0; j < kHalf; j += 2) {
-        const float2 v = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), make_float2(ks, ks),
-                                    make_float2(lv, lv));
-        d[j] = v.x;
-        d[j + 1] = v.y;
-      }
-      if (kLimit && (t + 1) * kT > minlim) {
+        for (int c = 0; c < 4; ++c) {
+          const float4 f = neg_ref[c];
+          const float2 v0 = __ffma2_rn(make_float2(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])),
+                                       make_float2(ks, ks), __fadd2_rn(make_float2(lv, lv), make_float2(f.x, f.y)));
+          const float2 v1 = __ffma2_rn(make_float2(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])),
+                                       make_float2(ks, ks), __fadd2_rn(make_float2(lv, lv), make_float2(f.z, f.w)));
+          e[4 * c] = v0.x;
+          e[4 * c + 1] = v0.y;
+          e[4 * c + 2] = v1.x;
+          e[4 * c + 3] = v1.y;
+        }
+        if (kLimit && (t + 1) * kT > minlim) {
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) {
+            const int lim = __shfl_sync(0xffffffffu, lim_mine, j);
+            if (t * kT + row >= lim) e[j] = -INFINITY;
+          }
+        }
+        if ((t + 1) * kT > len) {  // the block ends in this tile
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) e[j] = t * kT + row < len ? e[j] : -INFINITY;
+        }
+      };
+      scores();
+      float most = fmaxf(e[0], e[1]);
+#pragma unroll
+      for (int j = 2; j < kHalf; j += 2) most = max3(most, e[j], e[j + 1]);
+      if (vote_128(bar, most > kLift + kLazy)) {
+        if (lane < nh) S.neg_ref[warp][lane] = 0.f;  // the scores as they are
+        __syncwarp();
+        scores();
+        float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
-          const int lim = __shfl_sync(0xffffffffu, lim_mine, j);
-          if (t * kT + row >= lim) d[j] = -INFINITY;
+          const float m = warp_max(e[j]);
+          if (lane == j) top = m;
         }
-      }
-      if (!tok_ok) {
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) d[j] = -INFINITY;
-      }
-      bool exceed = false;
-#pragma unroll
-      for (int j = 0; j < kHalf; ++j) exceed |= j < nh && d[j] - ref[j] > kLift + kLazy;
-      if (vote_128(bar, exceed)) {
-        float v[kHalf];
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) v[j] = d[j];
-        reduce_columns<true>(v, lane);
-        if (lane < kHalf) S.red[st][half][lane][qd] = v[0];
+        if (lane < kHalf) S.red[st][half][lane][qd] = top;
         asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
         const float4 t4 = *reinterpret_cast<const float4 *>(S.red[st][half][lane & (kHalf - 1)]);
         const float tmax = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
         const float old = ref_mine;
         if ((lane & (kHalf - 1)) < nh && tmax - old > kLift + kLazy) ref_mine = tmax - kLift;
         const float a_mine = ref_mine == old ? 1.f : ex2(old - ref_mine);
-        float alpha[kHalf];
+        if (lane < nh) S.neg_ref[warp][lane] = -ref_mine;
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          ref[j] = __shfl_sync(0xffffffffu, ref_mine, j);
-          alpha[j] = __shfl_sync(0xffffffffu, a_mine, j);
-          l[j] *= alpha[j];
-        }
+        for (int j = 0; j < kHalf; ++j) l[j] *= __shfl_sync(0xffffffffu, a_mine, j);
+        __syncwarp();
+        scores();
         if (started) {
           // O must hold the stream's earlier tiles before it is rescaled
           idle_wait(S, a, &S.p_empty[st][buf ^ 1], ((i - 2) >> 2) & 1);
           tc_fence_after();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t col = tl + kTmemO + (par * 2 + st) * 2 * kN + h * kN + half * kHalf;
-            uint32_t o[kHalf];
-            tmem_ld16(col, o);
+          for (int h = 0; h < 4; ++h) {  // 8 columns of the first parts, 8 more, then of the second ones
+            const uint32_t col = tl + kTmemO + (par * 2 + st) * 2 * kN + (h >> 1) * kN + half * kHalf + (h & 1) * 8;
+            uint32_t o[8];
+            tmem_ld8(col, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
-            tmem_st16(col, o);
-            tmem_wait_st();
+            for (int j = 0; j < 8; ++j)
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * __shfl_sync(0xffffffffu, a_mine, (h & 1) * 8 + j));
+            tmem_st8(col, o);
           }
+          tmem_wait_st();
           tc_fence_before();
         }
         asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // (red is read before the next tile writes it)
       }
       started = true;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.s_empty[st]);
       // weights: their sum, and their parts to the tensor cores
       uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -781,7 +872,7 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int j = 4 * c + 2 * k;
-            const float w0 = ex2(d[j] - ref[j]), w1 = ex2(d[j + 1] - ref[j + 1]);
+            const float w0 = ex2(e[j]), w1 = ex2(e[j + 1]);
             const float2 s = __ffma2_rn(make_float2(w0, w1), make_float2(rv, rv), make_float2(l[j], l[j + 1]));
             l[j] = s.x;
             l[j + 1] = s.y;
@@ -799,14 +890,14 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[st][buf]);
       if (pend >= 0) {  // records of the segment before, a tile late
-        segment_records(a, S, tmem, pend, pend_sid, pend_nq, pend_cnt, pend_first);
+        segment_records(a, S, tmem, pend);
         pend = -1;
       }
     }
     // (before this segment's hand-over: the other stream writes to the same places only
     // once both are done with the segment before)
-    if (pend >= 0) segment_records(a, S, tmem, pend, pend_sid, pend_nq, pend_cnt, pend_first);
-    reduce_columns<false>(l, lane);
+    if (pend >= 0) segment_records(a, S, tmem, pend);
+    sum_columns(l, lane);
     if (lane < kHalf) {
       S.hl[par][st][qd][half * kHalf + lane] = l[0];
       if (qd == 0) S.hm[par][st][half * kHalf + lane] = ref_mine;
@@ -814,15 +905,17 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.hand[par]);
     pend = seg;
-    pend_sid = seg_id(P, x.b, x.g, x.h);
-    pend_nq = nq;
-    pend_cnt = cnt;
-    pend_first = i0 & 1;
-    i0 += cnt;
-    x.t = x.tiles - 1;
-    unit_pos_next(P, a.n_blocks, x);
+    if (lane == 0) {
+      UnitPos x = S.walk[warp];
+      S.due[warp] = {seg_id(P, x.b, x.g, x.h), nq, i_end - i0, i0 & 1};
+      x.t = x.tiles - 1;
+      unit_pos_next(P, a.n_blocks, x);
+      S.walk[warp] = x;
+    }
+    __syncwarp();
+    i0 = i_end;
   }
-  if (pend >= 0) segment_records(a, S, tmem, pend, pend_sid, pend_nq, pend_cnt, pend_first);
+  if (pend >= 0) segment_records(a, S, tmem, pend);
 }
 
 // The plan into shared memory (around the RoPE table, which is the launch's own).
@@ -869,13 +962,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.kv_empty[s], 1);
     }
     for (int k = 0; k < 4; ++k) {
-      mbar_init(&S.s_full[k >> 1][k & 1], 1);
-      mbar_init(&S.s_empty[k >> 1][k & 1], 8);  // the stream's warps
-      mbar_init(&S.p_full[k >> 1][k & 1], 8);
+      mbar_init(&S.p_full[k >> 1][k & 1], 8);  // the stream's warps
       mbar_init(&S.p_empty[k >> 1][k & 1], 1);
       mbar_init(&S.rec_ready[k], kSoftWarps);
     }
     for (int k = 0; k < 2; ++k) {
+      mbar_init(&S.s_full[k], 1);
+      mbar_init(&S.s_empty[k], 8);
+      mbar_init(&S.mma_done[k], 1);
       mbar_init(&S.q_full[k], 1);
       mbar_init(&S.q_empty[k], 1 + kSoftWarps);  // the segment's last QK, the softmax warps' reads
       mbar_init(&S.o_full[k], 1);
@@ -883,13 +977,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.hand[k], kSoftWarps);
     }
     mbar_init(&S.app_bar, 1);
-    mbar_init(&S.mma_done, 1);
     S.abort_flag = 0;
     S.plan_ok = 1;
     fence_mbar_init();
   }
   if (tid >= 64 && tid < 128) S.ps.cache.phase[tid - 64] = a.phase[tid - 64];
-  if (warp == kWarpMma) {
+  if (warp == kWarpQk) {
     tmem_alloc(&S.tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -946,12 +1039,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpTma) {
       produce(a, S, &tm_k, &tm_v, prod, n, step, n + kLead, appending ? S.cp.app_tile : -1, lane);
       drain(S, prod);
-    } else if (warp == kWarpMma) {
-      mma_issuer(a, S, tmem, u0, n);
-      if (elect_one()) mma_commit(&S.mma_done);
+    } else if (warp == kWarpQk || warp == kWarpPv) {
+      if (warp == kWarpQk)
+        qk_issuer(a, S, tmem, u0, n);
+      else
+        pv_issuer(a, S, tmem, u0, n);
+      // (no product may be under way when the CTA retires)
+      if (elect_one()) mma_commit(&S.mma_done[warp - kWarpQk]);
       __syncwarp();
-      mbar_wait(&S.mma_done, 0);
-    } else if (warp >= kWarpQ) {
+      mbar_wait(&S.mma_done[warp - kWarpQk], 0);
+    } else if (warp == kWarpQ) {
       if (appending) append_tokens(a, S, u0, u1);
       qprep<kLimit>(a, S, u1);
     } else {
@@ -961,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == kWarpQk) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
