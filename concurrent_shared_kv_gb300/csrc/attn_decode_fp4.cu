@@ -74,13 +74,14 @@ struct Fp4Smem {
   PlanShared ps;
   CtaPlan cp;
   PlanHeader hdr;
-  alignas(16) float red[2][2][kHalf][4];  // stream, half: a tile's column maxima of the four warps
+  // stream, half, parity of the stream's tile: the column maxima of the four warps
+  alignas(16) float red[2][2][2][kHalf][4];
   alignas(16) float neg_ref[kSoftWarps][kHalf];  // a warp's own copy: minus its columns' references
   float hm[2][2][kN];          // segment parity, stream: reference maxima of the columns
   float hl[2][2][4][kN];       // and the warps' sums of weights
   int32_t nref[2];             // segment parity: references,
   float q_mul[2];              // the power of two that scores are to be multiplied with
-  float qmax[8];
+  float qmax[kSoftWarps];
   int32_t abort_flag, plan_ok;
   uint32_t tmem_base;
   // what a softmax warp needs only between segments: its place in the units, the
@@ -193,45 +194,83 @@ __device__ __forceinline__ int column_place(int qi) { return (qi & 1) * kHalf + 
 
 // ------------------------------------------------------------------ producer
 
-// The order in which tiles are used, K(0) .. K(kLead-1), V(0), K(kLead), V(1), ...:
-// step j takes V(j - kLead), then K(j).  Steps [j0, j1) of the CTA's n units; `count`:
-// copies issued so far.
+// One thread, which has under 800 clocks for a tile's two copies: within a segment a
+// tile's place is the one before it plus 128 tokens, and a V's is that of the K kLead
+// tiles before.  Tiles are loaded in the order of their use, K(0) .. K(kLead-1), V(0),
+// K(kLead), V(1), ...: step j takes V(j - kLead), then K(j).
 struct Producer {
   RingPos at;
-  int count;
-  UnitPos k, v;  // the next K's and V's unit
+  int count;  // copies issued so far
+  int step;
+  int row[kLead + 1], h[kLead + 1];  // the K's of this step and those before it
+  UnitPos x;  // the segment's first unit of the CTA's
+  int left;   // tiles of the segment from this one on
 };
 
-__device__ void produce(const DecodeArgs &a, Fp4Smem &S, const CUtensorMap *tk, const CUtensorMap *tv, Producer &p,
-                        int n, int j0, int j1, int app_tile, int lane) {
+__device__ __forceinline__ void start(const DecodeArgs &a, const Fp4Smem &S, Producer &p) {
+  p.at = {0, 0};
+  p.count = p.step = 0;
+  p.x = unit_pos(S.ps.plan, a.n_blocks, S.cp.u0);
+  p.left = p.x.tiles - p.x.t;
+#pragma unroll
+  for (int k = 0; k <= kLead; ++k) p.row[k] = p.h[k] = 0;
+  p.row[0] = S.ps.plan.start[p.x.b] + p.x.t * kT;
+  p.h[0] = p.x.h;
+}
+
+// Steps up to j1 of n tiles, while `room` copies are left; app_tile: the first tile with
+// a new token (or -1), loaded once the tokens are written (and fenced for the copy engine).
+__device__ __forceinline__ void produce(const DecodeArgs &a, Fp4Smem &S, const CUtensorMap *tk, const CUtensorMap *tv,
+                                        Producer &p, int n, int j1, int room, int app_tile) {
   const uint64_t pol = policy_evict_first();
   const PlanCore &P = S.ps.plan;
-  auto load = [&](const CUtensorMap *m, const UnitPos &x) {
-    if (p.count >= kSlots && !warp_spin(S, a, &S.kv_empty[p.at.s], p.at.phase ^ 1)) return false;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&S.kv_full[p.at.s], kTileTx);
-      tma_load_3d(S.ring[p.at.s], m, &S.kv_full[p.at.s], 0, P.start[x.b] + x.t * kT, x.h, pol);
+  auto spin = [&](uint64_t *bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_test(bar, parity)) {
+      if (aborted(S)) return false;
+      if (clock64() - t0 > kWaitLimit) {
+        set_abort(S, a);
+        return false;
+      }
     }
+    return true;
+  };
+  auto load = [&](const CUtensorMap *m, int row, int h) {
+    if (p.count >= kSlots && !spin(&S.kv_empty[p.at.s], p.at.phase ^ 1)) return false;
+    mbar_arrive_expect_tx(&S.kv_full[p.at.s], kTileTx);
+    tma_load_3d(S.ring[p.at.s], m, &S.kv_full[p.at.s], 0, row, h, pol);
     ++p.count;
     p.at.next();
     return true;
   };
-  for (int j = j0; j < j1; ++j) {
-    if (j >= kLead) {
-      if (!load(tv, p.v)) return;
-      unit_pos_next(P, a.n_blocks, p.v);
-    }
+  for (; p.step < j1 && p.count + 2 <= room; ++p.step) {
+    const int j = p.step;
+    if (j >= kLead && !load(tv, p.row[kLead], p.h[kLead])) return;
     if (j < n) {
-      // the first tile with a new token is loaded once the tokens are written (and
-      // fenced for the copy engine)
-      if (j == app_tile && !warp_spin(S, a, &S.app_bar, 0)) return;
-      // the tile's scales into L2 (its threads load them shortly before they need them)
-      const int left = P.len[p.k.b] - p.k.t * kT;
-      if (lane < 4 && lane * 32 < left)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            a.kv_scale + static_cast<int64_t>(p.k.h) * a.capacity + P.start[p.k.b] + p.k.t * kT + lane * 32));
-      if (!load(tk, p.k)) return;
-      unit_pos_next(P, a.n_blocks, p.k);
+      if (j == app_tile && !spin(&S.app_bar, 0)) return;
+      // the tile's scales into L2 (its threads load them shortly before they need them);
+      // of a tile that the block fills, whole 16-byte pieces
+      if (p.left > 1)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         (reinterpret_cast<uint64_t>(a.kv_scale + static_cast<int64_t>(p.h[0]) * a.capacity + p.row[0]) + 15) &
+                         ~15ull),
+                     "n"(kT * 4 - 16)
+                     : "memory");
+      if (!load(tk, p.row[0], p.h[0])) return;
+    }
+#pragma unroll
+    for (int k = kLead; k > 0; --k) {
+      p.row[k] = p.row[k - 1];
+      p.h[k] = p.h[k - 1];
+    }
+    p.row[0] += kT;
+    if (--p.left == 0) {
+      p.x.t = p.x.tiles - 1;
+      unit_pos_next(P, a.n_blocks, p.x);
+      p.left = p.x.tiles - p.x.t;
+      p.row[0] = P.start[p.x.b] + p.x.t * kT;
+      p.h[0] = p.x.h;
     }
   }
 }
@@ -338,6 +377,12 @@ __device__ void pv_issuer(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int64_
 
 // ------------------------------------------------------------------- queries
 
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
 // A column's largest pair length over the item's elements, squared: turned
 // elements are no longer than that.
 __device__ __forceinline__ float item_reach(const QItem &it) {
@@ -351,14 +396,13 @@ __device__ __forceinline__ float item_reach(const QItem &it) {
   }
   return m;
 }
-// The exponent e of the power of two with |y| / 2^e < 448, E4M3's largest value, for a
-// segment whose pairs reach the square root of `reach` before scale * log2(e).
+// The exponent e with |y| < 2^(e + 8) (E4M3 ends at 448) for a segment whose squared pair
+// lengths reach `reach` before scale * log2(e); and 2^e.
 __device__ __forceinline__ int part_exponent(const DecodeArgs &a, float reach) {
-  const float mx = sqrtf(reach) * fabsf(a.scale_log2) * 1.0001f;
-  int e = 0;
-  if (mx > 0.f && mx < INFINITY) frexpf(mx * (1.f / 448.f), &e);
-  return max(-120, min(e, 120));
+  const float r = reach * a.scale_log2 * a.scale_log2;
+  return max(-120, min(((static_cast<int>(__float_as_uint(r) >> 23) - 127) >> 1) - 7, 120));
 }
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
 
 // Two E4M3 codes (low byte first) as two fp32, exactly.
 __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
@@ -366,10 +410,28 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
   return __half22float2(h);
 }
 
+// cos and sin of the angle rel * phase, from its upper 32 bits (2^-32 turns are far
+// below what the parts keep) by the fast hardware functions.
+__device__ __forceinline__ void turn_of(int64_t rel, uint64_t phase, float *c, float *s) {
+  const int32_t turns = static_cast<int32_t>((static_cast<uint64_t>(rel) * phase) >> 32);
+  __sincosf(static_cast<float>(turns) * (3.14159265358979323846f * 0x1p-31f), s, c);
+}
 // cos and sin of an item's 8 elements.
 __device__ __forceinline__ void item_turns(const Fp4Smem &S, int64_t rel, int c, float (&cs)[8], float (&sn)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) rope_cos_sin_fast(rel, S.ps.cache.phase[8 * c + e], &cs[e], &sn[e]);
+  for (int e = 0; e < 8; ++e) turn_of(rel, S.ps.cache.phase[8 * c + e], &cs[e], &sn[e]);
+}
+
+// (x, y) as kQParts E4M3 parts, each the remainder of those before it times 16.
+__device__ __forceinline__ void split_query(float2 y, uint32_t (&q)[kQParts]) {
+#pragma unroll
+  for (int j = 0; j < kQParts; ++j) {
+    q[j] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    if (j + 1 < kQParts) {
+      const float2 v = e4m3x2_values(q[j]);
+      y = make_float2((y.x - v.x) * 16.f, (y.y - v.y) * 16.f);
+    }
+  }
 }
 
 // The item turned, scaled by mul and split into parts, each the remainder of those before
@@ -393,17 +455,13 @@ __device__ __forceinline__ void store_item(const QItem &it, const float (&cs)[8]
       (h ? y0.y : y0.x) = (x0 * cs[2 * e + h] - x1 * sn[2 * e + h]) * mul;
       (h ? y1.y : y1.x) = (x1 * cs[2 * e + h] + x0 * sn[2 * e + h]) * mul;
     }
+    uint32_t q0[kQParts], q1[kQParts];
+    split_query(y0, q0);
+    split_query(y1, q1);
 #pragma unroll
     for (int j = 0; j < kQParts; ++j) {
-      const uint32_t q0 = __nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3);
-      const uint32_t q1 = __nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3);
-      w[j][e >> 1] |= q0 << (16 * (e & 1));
-      w[j][2 + (e >> 1)] |= q1 << (16 * (e & 1));
-      if (j + 1 < kQParts) {
-        const float2 v0 = e4m3x2_values(q0), v1 = e4m3x2_values(q1);
-        y0 = make_float2((y0.x - v0.x) * 16.f, (y0.y - v0.y) * 16.f);
-        y1 = make_float2((y1.x - v1.x) * 16.f, (y1.y - v1.y) * 16.f);
-      }
+      w[j][e >> 1] |= q0[j] << (16 * (e & 1));
+      w[j][2 + (e >> 1)] |= q1[j] << (16 * (e & 1));
     }
   }
   const uint32_t row = qbase + place * 128, sub = 8u * (c & 1);
@@ -416,32 +474,65 @@ __device__ __forceinline__ void store_item(const QItem &it, const float (&cs)[8]
   }
 }
 
-// Segment 0's queries, by warps 0-7 (256 threads, an item each).
+// Segment 0's queries, by the softmax warps (nothing else can start before them): a
+// thread has 4 elements of the first half of a column's, and the 4 that they turn with.
 __device__ void query_prologue(const DecodeArgs &a, Fp4Smem &S) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  NamedSync<5, 256> sync;
+  static_assert(kSoftWarps == kN / 2, "16 threads a column");
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, qi = t >> 4, c = t & 15;
+  NamedSync<5, 32 * kSoftWarps> sync;
   const SegQ &X = S.cp.pre[0];
-  const int items = min(X.m.n_ref * (a.n_q_heads / a.n_kv_heads), kN) * 8;
-  QItem it;
-  float reach = 0.f;
-  if (t < items) {
-    load_item(a, X, t >> 3, t & 7, it);
-    reach = item_reach(it);
+  const bool on = qi < min(X.m.n_ref * (a.n_q_heads / a.n_kv_heads), kN);
+  uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
+  int64_t rel = 0;
+  if (on) {
+    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + static_cast<int64_t>(X.qrow[qi]) * 128 + 4 * c;
+    lo = __ldg(reinterpret_cast<const uint2 *>(qp));
+    hi = __ldg(reinterpret_cast<const uint2 *>(qp + 64));
+    rel = X.rel[qi];
   }
-  reach = warp_max_nonneg(reach);
+  float cs[4], sn[4];  // (while the loads are under way)
+#pragma unroll
+  for (int e = 0; e < 4; ++e) turn_of(rel, S.ps.cache.phase[4 * c + e], &cs[e], &sn[e]);
+  float x0[4], x1[4], reach = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t l = e < 2 ? lo.x : lo.y, h = e < 2 ? hi.x : hi.y;
+    x0[e] = __uint_as_float(e & 1 ? l & 0xffff0000u : l << 16);
+    x1[e] = __uint_as_float(e & 1 ? h & 0xffff0000u : h << 16);
+    reach = fmaxf(reach, __fmaf_rn(x0[e], x0[e], x1[e] * x1[e]));
+  }
+  reach = warp_max(reach);
   if (lane == 0) S.qmax[warp] = reach;
   sync();
+  reach = warp_max(S.qmax[lane & (kSoftWarps - 1)]);
+  const int ex = part_exponent(a, reach);
+  if (on) {
+    const float mul = a.scale_log2 * two_to(-ex);
+    uint32_t w0[kQParts], w1[kQParts];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) reach = fmaxf(reach, S.qmax[w]);
-  const int e = part_exponent(a, reach);
-  if (t < items) {
-    float cs[8], sn[8];
-    item_turns(S, it.rel, t & 7, cs, sn);
-    store_item(it, cs, sn, smem_u32(S.q[0]), column_place(t >> 3), t & 7, a.scale_log2 * ldexpf(1.f, -e));
+    for (int e = 0; e < 4; e += 2) {
+      uint32_t q0[kQParts], q1[kQParts];
+      split_query(make_float2((x0[e] * cs[e] - x1[e] * sn[e]) * mul, (x0[e + 1] * cs[e + 1] - x1[e + 1] * sn[e + 1]) * mul), q0);
+      split_query(make_float2((x1[e] * cs[e] + x0[e] * sn[e]) * mul, (x1[e + 1] * cs[e + 1] + x0[e + 1] * sn[e + 1]) * mul), q1);
+#pragma unroll
+      for (int j = 0; j < kQParts; ++j) {
+        w0[j] = e ? w0[j] | q0[j] << 16 : q0[j];
+        w1[j] = e ? w1[j] | q1[j] << 16 : q1[j];
+      }
+    }
+    // (codes at byte 4c and 64 + 4c of the row, 16-byte chunks swizzled)
+    const int place = column_place(qi);
+    const uint32_t row = smem_u32(S.q[0]) + place * 128 + 4 * (c & 3);
+    const uint32_t c0 = (c >> 2 ^ (place & 7)) << 4, c1 = ((4 + (c >> 2)) ^ (place & 7)) << 4;
+#pragma unroll
+    for (int j = 0; j < kQParts; ++j) {
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + j * kQPart + c0), "r"(w0[j]) : "memory");
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + j * kQPart + c1), "r"(w1[j]) : "memory");
+    }
   }
   if (t == 0) {
     S.nref[0] = X.m.n_ref;
-    S.q_mul[0] = ldexpf(1.f, e);
+    S.q_mul[0] = two_to(ex);
   }
   fence_proxy_async_smem();
   sync();
@@ -477,11 +568,11 @@ __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
         reach = fmaxf(reach, item_reach(raw));
       }
     const int e = part_exponent(a, warp_max_nonneg(reach));
-    const float mul = a.scale_log2 * ldexpf(1.f, -e);
+    const float mul = a.scale_log2 * two_to(-e);
     if (seg >= 2) idle_wait(S, a, &S.q_empty[par], ((seg >> 1) - 1) & 1);
     if (lane == 0) {
       S.nref[par] = n_ref;
-      S.q_mul[par] = ldexpf(1.f, e);
+      S.q_mul[par] = two_to(e);
     }
     for (int it = lane; it < n_ref * 8; it += 32) {
       float cs[8], sn[8];
@@ -595,32 +686,20 @@ __device__ __forceinline__ bool vote_128(int id, bool pred) {
   return out != 0;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-// r + r1 * f, elementwise.
-__device__ __forceinline__ void join_parts(uint32_t (&r)[kHalf], const uint32_t (&r1)[kHalf], float f) {
-#pragma unroll
-  for (int j = 0; j < kHalf; j += 2) {
-    const float2 v = __ffma2_rn(make_float2(__uint_as_float(r1[j]), __uint_as_float(r1[j + 1])), make_float2(f, f),
-                                make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
-    r[j] = __float_as_uint(v.x);
-    r[j + 1] = __float_as_uint(v.y);
-  }
+__device__ __forceinline__ float2 as_pair(uint32_t x, uint32_t y) {
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
 }
 
-// Butterfly over the warp: on entry v[j] is this lane's value of column j, on exit
-// v[0] is the whole warp's sum of column lane & 15.
-__device__ __forceinline__ void sum_columns(float (&v)[kHalf], int lane) {
+// Butterflies over the warp: on entry v[j] is this lane's value of column j, on exit
+// v[0] is the whole warp's sum (largest one) of column lane & 15.
+template <bool kMax>
+__device__ __forceinline__ void join_columns(float (&v)[kHalf], int lane) {
 #pragma unroll
   for (int off = kHalf / 2; off >= 1; off >>= 1) {
 #pragma unroll
@@ -628,11 +707,14 @@ __device__ __forceinline__ void sum_columns(float (&v)[kHalf], int lane) {
       const bool up = (lane & off) != 0;
       const float mine = up ? v[k + off] : v[k];
       const float other = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + off], off);
-      v[k] = mine + other;
+      v[k] = kMax ? fmaxf(mine, other) : mine + other;
     }
   }
-  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+  const float other = __shfl_xor_sync(0xffffffffu, v[0], 16);
+  v[0] = kMax ? fmaxf(v[0], other) : v[0] + other;
 }
+__device__ __forceinline__ void sum_columns(float (&v)[kHalf], int lane) { join_columns<false>(v, lane); }
+__device__ __forceinline__ void max_columns(float (&v)[kHalf], int lane) { join_columns<true>(v, lane); }
 
 // x, y (at most 448) as two E4M3 parts each, x = hi + lo / 16: the codes of hi in the
 // low half of the word, those of lo in the high one.  fp16 in between keeps 11 bits,
@@ -716,12 +798,12 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
 
   // A wait that gives up (HW_DEV_TIMEOUT) does not leave the loops: all threads keep
   // the same control flow, so the votes are always reached by all 128.
-  // ref: the exponent that a column's weights are taken against (its maximum less
-  // kLift), the same in the four warps; ref_mine is column (lane & 15)'s, neg_ref in shared
-  // memory has all of the half's (16 registers that would spill otherwise).  They
-  // start at -FLT_MAX, not -inf: a column whose tokens are all masked then has weights
-  // 2^-inf = 0.
-  float l[kHalf], ref_mine = -FLT_MAX;
+  // A column's reference is the exponent that its weights are taken against (its maximum
+  // less kLift), the same in the four warps; ref_mine: column (lane & 15)'s, in shared memory
+  // (negative) all of the half's, which would spill from registers.  Columns past the
+  // segment's have inf there, and weights of 0.  One whose tokens are all masked keeps
+  // -FLT_MAX (not -inf: its weights are then 2^-inf = 0).
+  float l[kHalf], ref_mine;
   const float4 *neg_ref = reinterpret_cast<const float4 *>(S.neg_ref[warp]);
   int pend = -1;
   if (lane == 0) S.walk[warp] = unit_pos(P, a.n_blocks, u0);
@@ -761,10 +843,7 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
     if (lane == 0) mbar_arrive(&S.q_empty[par]);  // this warp has read the hand-off
 #pragma unroll
     for (int j = 0; j < kHalf; ++j) l[j] = 0.f;
-    ref_mine = -FLT_MAX;
-    // (columns that the half does not have get scores of -inf, and weights of 0)
-    if (lane < kHalf) S.neg_ref[warp][lane] = lane < nh ? FLT_MAX : -INFINITY;
-    __syncwarp();
+    ref_mine = (lane & (kHalf - 1)) < nh ? -FLT_MAX : INFINITY;
     bool started = false;  // O holds a tile of this segment
     for (; i < i_end; i += 2) {
       const int buf = (i >> 1) & 1, t = i + t0;
@@ -776,75 +855,80 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
       const float rv = vs == 0.f ? 1.f : __fdividef(1.f, vs);
       idle_wait(S, a, &S.s_full[st], (i >> 1) & 1);
       tc_fence_after();
-      // scores in log2 units with the value's scale in them, less the references
+      // scores in log2 units with the value's scale in them
       float e[kHalf];
-      auto scores = [&]() {
-        const uint32_t col = tl + st * kSCols + half * kHalf;
-        uint32_t r[kHalf], r1[kHalf];
-        tmem_ld16(col, r);
-        tmem_ld16(col + kN, r1);
+      {
+        uint32_t r[kQParts][kHalf];
+#pragma unroll
+        for (int k = 0; k < kQParts; ++k) tmem_ld16(tl + st * kSCols + k * kN + half * kHalf, r[k]);
         tmem_wait_ld();
-        join_parts(r, r1, 0.0625f);
-        if constexpr (kQParts == 3) {
-          tmem_ld16(col + 2 * kN, r1);
-          tmem_wait_ld();
-          join_parts(r, r1, 0.00390625f);
-        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 f = neg_ref[c];
-          const float2 v0 = __ffma2_rn(make_float2(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])),
-                                       make_float2(ks, ks), __fadd2_rn(make_float2(lv, lv), make_float2(f.x, f.y)));
-          const float2 v1 = __ffma2_rn(make_float2(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])),
-                                       make_float2(ks, ks), __fadd2_rn(make_float2(lv, lv), make_float2(f.z, f.w)));
-          e[4 * c] = v0.x;
-          e[4 * c + 1] = v0.y;
-          e[4 * c + 2] = v1.x;
-          e[4 * c + 3] = v1.y;
-        }
-        if (kLimit && (t + 1) * kT > minlim) {
+        for (int j = 0; j < kHalf; j += 2) {
+          float2 v = as_pair(r[kQParts - 1][j], r[kQParts - 1][j + 1]);
 #pragma unroll
-          for (int j = 0; j < kHalf; ++j) {
-            const int lim = __shfl_sync(0xffffffffu, lim_mine, j);
-            if (t * kT + row >= lim) e[j] = -INFINITY;
-          }
+          for (int k = kQParts - 2; k >= 0; --k)
+            v = __ffma2_rn(v, make_float2(0.0625f, 0.0625f), as_pair(r[k][j], r[k][j + 1]));
+          v = __ffma2_rn(v, make_float2(ks, ks), make_float2(lv, lv));
+          e[j] = v.x;
+          e[j + 1] = v.y;
         }
-        if ((t + 1) * kT > len) {  // the block ends in this tile
-#pragma unroll
-          for (int j = 0; j < kHalf; ++j) e[j] = t * kT + row < len ? e[j] : -INFINITY;
-        }
-      };
-      scores();
-      float most = fmaxf(e[0], e[1]);
-#pragma unroll
-      for (int j = 2; j < kHalf; j += 2) most = max3(most, e[j], e[j + 1]);
-      if (vote_128(bar, most > kLift + kLazy)) {
-        if (lane < nh) S.neg_ref[warp][lane] = 0.f;  // the scores as they are
-        __syncwarp();
-        scores();
-        float top = -INFINITY;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.s_empty[st]);
+      if (kLimit && (t + 1) * kT > minlim) {
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
-          const float m = warp_max(e[j]);
-          if (lane == j) top = m;
+          const int lim = __shfl_sync(0xffffffffu, lim_mine, j);
+          if (t * kT + row >= lim) e[j] = -INFINITY;
         }
-        if (lane < kHalf) S.red[st][half][lane][qd] = top;
+      }
+      if ((t + 1) * kT > len) {  // the block ends in this tile
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) e[j] = t * kT + row < len ? e[j] : -INFINITY;
+      }
+      auto add_refs = [&](float sign) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 4) {
+          const float4 f = neg_ref[j / 4];
+          const float2 v0 = __ffma2_rn(make_float2(f.x, f.y), make_float2(sign, sign), make_float2(e[j], e[j + 1]));
+          const float2 v1 = __ffma2_rn(make_float2(f.z, f.w), make_float2(sign, sign), make_float2(e[j + 2], e[j + 3]));
+          e[j] = v0.x;
+          e[j + 1] = v0.y;
+          e[j + 2] = v1.x;
+          e[j + 3] = v1.y;
+          most = max3(max3(most, v0.x, v0.y), v1.x, v1.y);
+        }
+        return most;
+      };
+      // The references move only when some weight would pass 2^(kLift + kLazy), so O
+      // is rarely touched; the 128 threads of a half decide together (at a segment's first
+      // tile there is nothing to decide).
+      bool move = true;
+      if (started) move = vote_128(bar, add_refs(1.f) > kLift + kLazy);
+      if (move) {
+        if (started) add_refs(-1.f);
+        float v[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) v[j] = e[j];
+        max_columns(v, lane);
+        float(*red)[4] = S.red[st][half][(i >> 1) & 1];
+        if (lane < kHalf) red[lane][qd] = v[0];
         asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
-        const float4 t4 = *reinterpret_cast<const float4 *>(S.red[st][half][lane & (kHalf - 1)]);
+        const float4 t4 = *reinterpret_cast<const float4 *>(red[lane & (kHalf - 1)]);
         const float tmax = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
         const float old = ref_mine;
-        if ((lane & (kHalf - 1)) < nh && tmax - old > kLift + kLazy) ref_mine = tmax - kLift;
+        if (tmax - old > kLift + kLazy) ref_mine = tmax - kLift;
         const float a_mine = ref_mine == old ? 1.f : ex2(old - ref_mine);
-        if (lane < nh) S.neg_ref[warp][lane] = -ref_mine;
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) l[j] *= __shfl_sync(0xffffffffu, a_mine, j);
-        __syncwarp();
-        scores();
+        if (lane < kHalf) S.neg_ref[warp][lane] = -ref_mine;
         if (started) {
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) l[j] *= __shfl_sync(0xffffffffu, a_mine, j);
           // O must hold the stream's earlier tiles before it is rescaled
           idle_wait(S, a, &S.p_empty[st][buf ^ 1], ((i - 2) >> 2) & 1);
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 4; ++h) {  // 8 columns of the first parts, 8 more, then of the second ones
             const uint32_t col = tl + kTmemO + (par * 2 + st) * 2 * kN + (h >> 1) * kN + half * kHalf + (h & 1) * 8;
             uint32_t o[8];
@@ -858,12 +942,10 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
           tmem_wait_st();
           tc_fence_before();
         }
-        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // (red is read before the next tile writes it)
+        __syncwarp();
+        add_refs(1.f);
       }
       started = true;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_empty[st]);
       // weights: their sum, and their parts to the tensor cores
       uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -1004,29 +1086,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
   };
-  Producer prod = {{0, 0}, 0, {}, {}};
-  int step = 0;  // of the producer, before griddepcontrol.wait
-  auto start_producer = [&]() {
-    prod.k = prod.v = unit_pos(S.ps.plan, a.n_blocks, S.cp.u0);
-  };
+  Producer prod;
+  prod.count = 0;
+  const bool producer = warp == kWarpTma && lane == 0;
   if (a.early) {
     get_plan();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == kWarpTma && S.plan_ok && S.cp.u0 < S.cp.u1) {
-      // the first tiles into the empty ring (not past the first one with a new token)
+    if (producer && S.plan_ok && S.cp.u0 < S.cp.u1) {
+      // the first tiles into the empty ring (not from the first one with a new token on)
       const int n = static_cast<int>(S.cp.u1 - S.cp.u0);
-      start_producer();
-      while (step < n + kLead && prod.count + 2 <= kSlots && !(kAppend && S.cp.app_n > 0 && step >= S.cp.app_tile)) {
-        produce(a, S, &tm_k, &tm_v, prod, n, step, step + 1, -1, lane);
-        ++step;
-      }
+      start(a, S, prod);
+      produce(a, S, &tm_k, &tm_v, prod, n, kAppend && S.cp.app_n > 0 ? S.cp.app_tile : n + kLead, kSlots, -1);
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!a.early) {
     get_plan();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == kWarpTma && S.plan_ok && S.cp.u0 < S.cp.u1) start_producer();
+    if (producer && S.plan_ok && S.cp.u0 < S.cp.u1) start(a, S, prod);
   }
   if (plan_timeout) flag_error(a.err, HW_DEV_TIMEOUT);
   const uint32_t tmem = S.tmem_base;
@@ -1037,8 +1114,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = static_cast<int>(u1 - u0);
     const bool appending = kAppend && S.cp.app_n > 0;
     if (warp == kWarpTma) {
-      produce(a, S, &tm_k, &tm_v, prod, n, step, n + kLead, appending ? S.cp.app_tile : -1, lane);
-      drain(S, prod);
+      if (producer) {
+        produce(a, S, &tm_k, &tm_v, prod, n, n + kLead, INT32_MAX, appending ? S.cp.app_tile : -1);
+        drain(S, prod);
+      }
     } else if (warp == kWarpQk || warp == kWarpPv) {
       if (warp == kWarpQk)
         qk_issuer(a, S, tmem, u0, n);
@@ -1052,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (appending) append_tokens(a, S, u0, u1);
       qprep<kLimit>(a, S, u1);
     } else {
-      if (warp < 8) query_prologue(a, S);
+      query_prologue(a, S);
       softmax_role<kAppend, kLimit>(a, S, tmem, u0, n);
     }
   }
