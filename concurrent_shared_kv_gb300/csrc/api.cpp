@@ -281,6 +281,7 @@ static void fill_args(DecodeArgs &a, const hw_attn_desc *d, const WorkspaceLayou
   a.head_dim = d->head_dim;
   a.n_blocks = d->n_blocks;
   a.n_view = d->max_view_blocks;
+  a.fp4 = d->dtype == HW_FP4_E2M1;
   a.capacity = d->cache_capacity;
   a.scale_log2 = static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634074);
   rope_phase_table(d->head_dim, d->rope_theta, a.phase);

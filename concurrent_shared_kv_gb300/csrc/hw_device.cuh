@@ -219,6 +219,16 @@ __device__ __forceinline__ int entry_rank_scan(const DecodeArgs &a, int e, int l
 // ratio can be made finer through kTileW.
 constexpr int kTileW = 1;
 constexpr int kSegW = 2;
+// 4-bit caches: a tile takes a third of the time and a segment start as long, so it
+// weighs more; but where a CTA has hardly more than a tile, the weight would leave CTAs
+// without work.  Measured with weights 0, 1, 2, 3, 4, 5, 6, 8: 1001 + 375 tokens (0.6 tiles
+// a CTA) 13.3, 13.5, 15.4, 14.2, 15.5, 16.2, 15.7, 16.2 us; 16384 + 1280 (7) 28.5, 22.4, 21.6,
+// 19.6, 20.7, 20.6, 20.2, 20.9; 32768 + 2560 (18) 37.6, 30.0, 29.5, 28.3, 27.5, 26.2, 26.4,
+// 27.1; 8 ragged problems (150) 120, 116, 115, 113, 111, 109.1, 108.8, 111.
+__device__ __forceinline__ int segment_weight_fp4(int64_t units, int grid) {
+  const int64_t w = 1 + 2 * units / (3 * grid);
+  return static_cast<int>(w < 6 ? w : 6);
+}
 
 struct PlanCore {
   int32_t tiles[HW_MAX_BLOCKS];      // tiles of one group for one kv head (0: block skipped)
@@ -228,6 +238,7 @@ struct PlanCore {
   uint16_t sord[HW_MAX_BLOCKS + 1];  // segments of a head before block b; [n] = NS
   int64_t UH, U, WH, W;              // units per head and in all; weights likewise
   int32_t NS, C;                     // segments per head; working CTAs
+  int32_t seg_w;                     // weight of a segment start (kSegW, segment_weight_fp4)
 };
 
 // Column groups of block b (0 when it takes no part).
@@ -271,13 +282,13 @@ __device__ __forceinline__ int64_t cta_unit_begin(const PlanCore &P, int n_block
   int lo = 0, hi = n_blocks - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (kTileW * P.ubase[mid] + static_cast<int64_t>(kSegW) * P.sord[mid] <= l) lo = mid; else hi = mid - 1;
+    if (kTileW * P.ubase[mid] + static_cast<int64_t>(P.seg_w) * P.sord[mid] <= l) lo = mid; else hi = mid - 1;
   }
   const int64_t T = P.tiles[lo];
-  const int64_t off = l - (kTileW * P.ubase[lo] + static_cast<int64_t>(kSegW) * P.sord[lo]);
-  const int64_t span = kSegW + kTileW * T;
+  const int64_t off = l - (kTileW * P.ubase[lo] + static_cast<int64_t>(P.seg_w) * P.sord[lo]);
+  const int64_t span = P.seg_w + kTileW * T;
   const int64_t g = div_nn(off, span);
-  const int64_t rem = off - g * span - kSegW;
+  const int64_t rem = off - g * span - P.seg_w;
   return static_cast<int64_t>(h) * P.UH + P.ubase[lo] + g * T +
          (rem > 0 ? (rem + kTileW - 1) / kTileW : 0);
 }
@@ -404,9 +415,10 @@ __device__ void build_plan(const DecodeArgs &a, PlanCore &P, MetaCache &M, PlanS
       P.UH = carry;
       P.U = carry * a.n_kv_heads;
       P.NS = ncarry;
-      P.WH = kTileW * carry + static_cast<int64_t>(kSegW) * ncarry;
+      P.seg_w = a.fp4 ? segment_weight_fp4(P.U, grid) : kSegW;
+      P.WH = kTileW * carry + static_cast<int64_t>(P.seg_w) * ncarry;
       P.W = P.WH * a.n_kv_heads;
-      const int64_t cmax = P.W / (kSegW + kTileW);
+      const int64_t cmax = P.W / (P.seg_w + kTileW);
       P.C = static_cast<int>(cmax < static_cast<int64_t>(grid) ? cmax : grid);
     }
     __syncwarp();
@@ -526,7 +538,7 @@ __device__ __forceinline__ int64_t unit_weight(const PlanCore &P, int n_blocks, 
   const int64_t local = u - static_cast<int64_t>(h) * P.UH;
   const int b = block_of_unit(P, n_blocks, local);
   const int64_t g = P.tiles[b] > 0 ? div_nn(local - P.ubase[b], P.tiles[b]) : 0;
-  return static_cast<int64_t>(h) * P.WH + kTileW * local + static_cast<int64_t>(kSegW) * (P.sord[b] + g + 1);
+  return static_cast<int64_t>(h) * P.WH + kTileW * local + static_cast<int64_t>(P.seg_w) * (P.sord[b] + g + 1);
 }
 
 // The CTA that owns unit u: the largest c with floor(c W / C) <= weight(u).

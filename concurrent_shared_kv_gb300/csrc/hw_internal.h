@@ -51,6 +51,7 @@ struct DecodeArgs {
   int32_t trace_call;  // the call's index in the process (layer-timeline build)
 #endif
   int32_t n_rows, n_q_heads, n_kv_heads, head_dim, n_blocks, n_view;
+  int32_t fp4;  // a plan for 4-bit caches
   int64_t capacity;
   const uint8_t *plan;  // precomputed plan of the tensor-core kernel (hw_attn_plan), or null
   // hw_attn_decode's plan cache in the workspace (see PlanCache), or null
