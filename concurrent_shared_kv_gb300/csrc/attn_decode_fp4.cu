@@ -601,53 +601,57 @@ __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
   }
 }
 
-// The CTA's new tokens (hw_attn_append_decode_planned_fp4), by warp 19, four
-// (row, kv head) pairs at a time, 8 threads each: the bits that hw_cache_write stores.
+// The CTA's new tokens (hw_attn_append_decode_planned_fp4), by warp 19, a (row, kv head) pair
+// at a time, lane l the elements 2l, 2l + 1 and those that they turn with: the bits that
+// hw_cache_write stores.  (With 8 lanes a pair it took 7 us, one warp's chain of
+// 1500 instructions, and everything behind the first new token waits for it.)
 __device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64_t u1) {
-  const int lane = threadIdx.x & 31, c = lane & 7;
+  const int lane = threadIdx.x & 31;
   const PlanCore &P = S.ps.plan;
   const int Hkv = a.n_kv_heads, npairs = a.n_rows * Hkv;
-  uint32_t *kc = static_cast<uint32_t *>(const_cast<void *>(a.k)), *vc = static_cast<uint32_t *>(const_cast<void *>(a.v));
-  uint32_t *sc = const_cast<uint32_t *>(a.kv_scale);
-  auto write = [&](bool on, int pr, int pos, int row) {
-    const int h = pr % Hkv;
-    float k0[8], k1[8], v0[8], v1[8];
+  auto scale_of = [](float x0, float x1, float x2, float x3) {
+    float top = max_nan(max_nan(fabsf(x0), fabsf(x1)), max_nan(fabsf(x2), fabsf(x3)));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) k0[j] = k1[j] = v0[j] = v1[j] = 0.f;
-    if (on) {
-      const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(a.k_new) + static_cast<int64_t>(pr) * 128 + 8 * c;
-      const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(a.v_new) + static_cast<int64_t>(pr) * 128 + 8 * c;
+    for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return fp4_scale(top);
+  };
+  auto write = [&](int pr, int pos, int row) {
+    const uint32_t *kn = static_cast<const uint32_t *>(a.k_new) + static_cast<int64_t>(pr) * 64 + lane;
+    const uint32_t *vn = static_cast<const uint32_t *>(a.v_new) + static_cast<int64_t>(pr) * 64 + lane;
+    const uint32_t k0 = __ldg(kn), k1 = __ldg(kn + 32), v0 = __ldg(vn), v1 = __ldg(vn + 32);
+    float cs[2], sn[2];  // (while the loads are under way)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float cs, sn;
-        rope_cos_sin_exact(pos, a.phase[8 * c + j], &cs, &sn);
-        fp4_turn(__bfloat162float(kn[j]), __bfloat162float(kn[64 + j]), cs, sn, k0[j], k1[j]);
-        v0[j] = __bfloat162float(vn[j]);
-        v1[j] = __bfloat162float(vn[64 + j]);
-      }
+    for (int j = 0; j < 2; ++j) rope_cos_sin_exact(pos, S.ps.cache.phase[2 * lane + j], &cs[j], &sn[j]);
+    float y[4];
+    fp4_turn(__uint_as_float(k0 << 16), __uint_as_float(k1 << 16), cs[0], sn[0], y[0], y[2]);
+    fp4_turn(__uint_as_float(k0 & 0xffff0000u), __uint_as_float(k1 & 0xffff0000u), cs[1], sn[1], y[1], y[3]);
+    const float x[4] = {__uint_as_float(v0 << 16), __uint_as_float(v0 & 0xffff0000u), __uint_as_float(v1 << 16),
+                        __uint_as_float(v1 & 0xffff0000u)};
+    const float ks = scale_of(y[0], y[1], y[2], y[3]), vs = scale_of(x[0], x[1], x[2], x[3]);
+    uint32_t c[4] = {0, 0, 0, 0};
+    if (ks > 0.f) {
+      c[0] = fp4_encode2(y[0], y[1], ks, 1.f / ks);
+      c[1] = fp4_encode2(y[2], y[3], ks, 1.f / ks);
     }
-    uint32_t kl, kh, vl, vh;
-    const float ks = fp4_row(k0, k1, kl, kh), vs = fp4_row(v0, v1, vl, vh);
-    if (on) {
-      const int64_t at = static_cast<int64_t>(h) * a.capacity + row;
-      kc[at * 16 + c] = kl;
-      kc[at * 16 + 8 + c] = kh;
-      vc[at * 16 + c] = vl;
-      vc[at * 16 + 8 + c] = vh;
-      if (c == 0) sc[at] = fp4_scale_word(ks, vs);
+    if (vs > 0.f) {
+      c[2] = fp4_encode2(x[0], x[1], vs, 1.f / vs);
+      c[3] = fp4_encode2(x[2], x[3], vs, 1.f / vs);
     }
+    const int64_t at = static_cast<int64_t>(pr % Hkv) * a.capacity + row;
+    uint8_t *kc = static_cast<uint8_t *>(const_cast<void *>(a.k)) + at * 64, *vc = static_cast<uint8_t *>(const_cast<void *>(a.v)) + at * 64;
+    kc[lane] = static_cast<uint8_t>(c[0]);
+    kc[32 + lane] = static_cast<uint8_t>(c[1]);
+    vc[lane] = static_cast<uint8_t>(c[2]);
+    vc[32 + lane] = static_cast<uint8_t>(c[3]);
+    if (lane == 0) const_cast<uint32_t *>(a.kv_scale)[at] = fp4_scale_word(ks, vs);
   };
   if (S.cp.app_n <= kAppList) {
-    for (int e0 = 0; e0 < S.cp.app_n; e0 += 4) {
-      const int e = e0 + (lane >> 3);
-      const bool on = e < S.cp.app_n;
-      write(on, on ? S.cp.app_pair[e] : 0, on ? S.cp.app_pos[e] : 0, on ? S.cp.app_row[e] : 0);
-    }
+    for (int e = 0; e < S.cp.app_n; ++e) write(S.cp.app_pair[e], S.cp.app_pos[e], S.cp.app_row[e]);
   } else {
     // more than the plan lists: every pair is checked (each CTA that reads a token's
     // tile writes it, the same bytes, before its own copy of the tile)
-    for (int base = 0; base < npairs; base += 4) {
-      const int pr = base + (lane >> 3);
+    for (int base = 0; base < npairs; base += 32) {
+      const int pr = base + lane;
       int pos = 0, row = 0;
       bool mine = false;
       if (pr < npairs) {
@@ -661,7 +665,10 @@ __device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64
           }
         }
       }
-      if (__any_sync(0xffffffffu, mine)) write(mine, mine ? pr : 0, pos, row);
+      for (unsigned m = __ballot_sync(0xffffffffu, mine); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        write(__shfl_sync(0xffffffffu, pr, src), __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, row, src));
+      }
     }
   }
   __threadfence_block();

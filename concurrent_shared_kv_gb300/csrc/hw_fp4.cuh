@@ -82,6 +82,18 @@ __device__ __forceinline__ uint32_t fp4_encode8(const float (&x)[8], float s, fl
   return w;
 }
 
+// The same of 2 numbers.
+__device__ __forceinline__ uint32_t fp4_encode2(float x, float y, float s, float inv) {
+  const float tx = x * inv, ty = y * inv;
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b8 a, b;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %3, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %5, %4;\n\t"
+      "mov.b32 %0, {a, a, a, a};\n\tmov.b32 %1, {b, b, b, b};\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "f"(tx * (1.f - 0x1p-20f)), "f"(ty * (1.f - 0x1p-20f)), "f"(tx * (1.f + 0x1p-20f)), "f"(ty * (1.f + 0x1p-20f)));
+  if (lo != hi) return fp4_code_exact(x, s) | fp4_code_exact(y, s) << 4;
+  return lo & 0xffu;
+}
+
 // The levels (with signs) of 8 codes.
 __device__ __forceinline__ void fp4_levels8(uint32_t w, float (&v)[8]) {
 #pragma unroll

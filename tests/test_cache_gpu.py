@@ -140,7 +140,7 @@ def test_write_and_read(dtype, layers, n, heads, d):
         assert torch.equal(out[:, on].cpu(), value)
 
 
-@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("dtype", [BF16, FP8, FP4])
 def test_written_as_appended(dtype):
     """A token has the same bits whether hw_cache_write stores it or a decode call
     appends it."""
