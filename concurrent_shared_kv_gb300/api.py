@@ -528,10 +528,15 @@ def cache_read(dtype: int, n_layers: int, n_tokens: int, n_kv_heads: int, head_d
 
 
 def _host_int32(what: str, *xs):
-    arrs = [np.ascontiguousarray(x, dtype=np.int32) for x in xs]
-    if any(a.shape != arrs[0].shape or a.ndim != 1 for a in arrs):
+    """Host int sequences of one length as int32: (length, array kept alive, their pointers)."""
+    try:
+        a = np.array(xs, dtype=np.int32)
+    except ValueError:
+        a = None
+    if a is None or a.ndim != 2:
         raise ValueError(f"{what}: sequences of different lengths")
-    return arrs
+    at, step = a.ctypes.data, a.shape[1] * 4
+    return a.shape[1], a, [at + i * step for i in range(len(xs))]
 
 
 def block_commit_many_fp4(n_layers: int, n_kv_heads: int, head_dim: int, rope_theta: float, k_src,
@@ -539,13 +544,12 @@ def block_commit_many_fp4(n_layers: int, n_kv_heads: int, head_dim: int, rope_th
                           dst_capacity: int, src_begin, n_tokens, dst_offset, pos_delta,
                           stream=None) -> int:
     """hw_block_commit_many_fp4; the four per-commit sequences are host ints."""
-    arrs = _host_int32("commits", src_begin, n_tokens, dst_offset, pos_delta)
+    n, _keep, at = _host_int32("commits", src_begin, n_tokens, dst_offset, pos_delta)
     st = lib().hw_block_commit_many_fp4(int(n_layers), int(n_kv_heads), int(head_dim),
                                         float(rope_theta), _ptr(k_src), _ptr(v_src),
                                         _ptr(scale_src), int(src_capacity), _ptr(k_dst),
                                         _ptr(v_dst), _ptr(scale_dst), int(dst_capacity),
-                                        len(arrs[0]), *[x.ctypes.data for x in arrs],
-                                        _stream(stream))
+                                        n, *at, _stream(stream))
     _check("hw_block_commit_many_fp4", st)
     return st
 
@@ -553,10 +557,10 @@ def block_commit_many_fp4(n_layers: int, n_kv_heads: int, head_dim: int, rope_th
 def block_move(dtype: int, n_layers: int, n_kv_heads: int, head_dim: int, k_cache, v_cache, kv_scale,
                capacity: int, src_begin, n_tokens, dst_begin, stream=None) -> int:
     """hw_block_move; the three per-move sequences are host ints."""
-    arrs = _host_int32("moves", src_begin, n_tokens, dst_begin)
+    n, _keep, at = _host_int32("moves", src_begin, n_tokens, dst_begin)
     st = lib().hw_block_move(int(dtype), int(n_layers), int(n_kv_heads), int(head_dim),
                              _ptr(k_cache), _ptr(v_cache), _ptr(kv_scale), int(capacity),
-                             len(arrs[0]), *[x.ctypes.data for x in arrs], _stream(stream))
+                             n, *at, _stream(stream))
     _check("hw_block_move", st)
     return st
 
@@ -564,14 +568,11 @@ def block_move(dtype: int, n_layers: int, n_kv_heads: int, head_dim: int, k_cach
 def compact_moves(block_start, block_len, capacity: int, room=None):
     """Host helper: (new_start, src_begin, n_tokens, dst_begin), where the blocks
     stand once slid together and the moves that bring them there."""
-    start, length = _host_int32("blocks", block_start, block_len)
-    room = None if room is None else np.ascontiguousarray(room, dtype=np.int32)
-    if room is not None and room.shape != start.shape:
-        raise ValueError("room needs an entry a block")
-    new, src, n, dst = (np.zeros(len(start), np.int32) for _ in range(4))
+    nb, _keep, at = _host_int32("blocks", block_start, block_len, *(() if room is None else (room,)))
+    new, src, n, dst = (np.zeros(nb, np.int32) for _ in range(4))
     count = ctypes.c_int32(0)
     _check("hw_compact_moves",
-           lib().hw_compact_moves(len(start), start.ctypes.data, length.ctypes.data, _ptr(room),
+           lib().hw_compact_moves(nb, at[0], at[1], None if room is None else at[2],
                                   int(capacity), new.ctypes.data, ctypes.addressof(count),
                                   src.ctypes.data, n.ctypes.data, dst.ctypes.data))
     k = count.value

@@ -630,12 +630,12 @@ __device__ void append_tokens(const DecodeArgs &a, Fp4Smem &S, int64_t u0, int64
     const float ks = scale_of(y[0], y[1], y[2], y[3]), vs = scale_of(x[0], x[1], x[2], x[3]);
     uint32_t c[4] = {0, 0, 0, 0};
     if (ks > 0.f) {
-      c[0] = fp4_encode2(y[0], y[1], ks, 1.f / ks);
-      c[1] = fp4_encode2(y[2], y[3], ks, 1.f / ks);
+      c[0] = fp4_encode2(y[0], y[1], ks);
+      c[1] = fp4_encode2(y[2], y[3], ks);
     }
     if (vs > 0.f) {
-      c[2] = fp4_encode2(x[0], x[1], vs, 1.f / vs);
-      c[3] = fp4_encode2(x[2], x[3], vs, 1.f / vs);
+      c[2] = fp4_encode2_bf16(x[0], x[1], vs);
+      c[3] = fp4_encode2_bf16(x[2], x[3], vs);
     }
     const int64_t at = static_cast<int64_t>(pr % Hkv) * a.capacity + row;
     uint8_t *kc = static_cast<uint8_t *>(const_cast<void *>(a.k)) + at * 64, *vc = static_cast<uint8_t *>(const_cast<void *>(a.v)) + at * 64;

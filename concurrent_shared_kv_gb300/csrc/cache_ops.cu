@@ -91,15 +91,31 @@ __device__ __forceinline__ void e4m3x4_values(uint32_t w, float *x) {
   }
 }
 
+// 8 elements of a row's first half and the 8 that they turn with.
+__device__ __forceinline__ void turn8(const float (&x0)[8], const float (&x1)[8], const float (&cs)[8],
+                                      const float (&sn)[8], float (&y0)[8], float (&y1)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float2 a, b;
+    fp4_turn2(make_float2(x0[e], x0[e + 1]), make_float2(x1[e], x1[e + 1]), make_float2(cs[e], cs[e + 1]),
+              make_float2(sn[e], sn[e + 1]), a, b);
+    y0[e] = a.x;
+    y0[e + 1] = a.y;
+    y1[e] = b.x;
+    y1[e + 1] = b.y;
+  }
+}
+
 // Rows of a CTA's tokens: (layer, token, kv head), 8 or so threads each.  blockIdx.x: the
 // tokens, blockIdx.y: a share of the layers.
 template <typename Store, int D>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const __grid_constant__ CacheArgs a) {
   using Act = typename Format<Store>::Act;
   constexpr bool kFp4 = std::is_same_v<Store, E2M1x2>;
   constexpr int N = Vec<Act>::N, kPer = D / 2 / N;  // threads a row
   __shared__ float2 turn[kTokens][D / 2];
   __shared__ int32_t slots[kTokens];
+  __shared__ float2 table[kFp4 ? 65 : 1];
   const int tid = threadIdx.x;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
   const int nt = static_cast<int>(min(static_cast<int64_t>(kTokens), a.n_tokens - t0));
@@ -111,93 +127,106 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     }
     slots[tid] = s;
   }
+  if constexpr (kFp4) {
+    if (tid >= 64 && tid < 129) table[tid - 64] = kSin256[tid - 64];
+    __syncthreads();
+  }
   for (int i = tid; i < nt * (D / 2); i += kThreads) {
     const int t = i / (D / 2), j = i % (D / 2);
     const int64_t p = __ldg(a.pos + t0 + t);
     float c, s;
     if constexpr (kFp4)
-      rope_cos_sin_exact(p, a.phase[j], &c, &s);
+      rope_cos_sin_exact(p, a.phase[j], &c, &s, table);
     else
       rope_cos_sin(p, a.phase[j], &c, &s);
     turn[t][j] = make_float2(c, s);
   }
   __syncthreads();
   const int H = a.n_kv_heads;
-  const int per_layer = nt * H * kPer;
   const int l0 = static_cast<int>(static_cast<int64_t>(a.n_layers) * blockIdx.y / gridDim.y);
   const int l1 = static_cast<int>(static_cast<int64_t>(a.n_layers) * (blockIdx.y + 1) / gridDim.y);
-  const int64_t end = static_cast<int64_t>(l1 - l0) * per_layer;
-  const Act *kn = static_cast<const Act *>(a.k_new), *vn = static_cast<const Act *>(a.v_new);
-  // (whole warps: the rows' threads shuffle)
-  for (int64_t base = 0; base < end; base += kThreads) {
-    const int64_t i = base + tid;
-    const bool in = i < end;
-    const int l_in = in ? static_cast<int>(div_nn(i, per_layer)) : 0;
-    const int l = l0 + l_in, r = in ? static_cast<int>(i - static_cast<int64_t>(l_in) * per_layer) : 0;
-    const int c = r % kPer, th = r / kPer, t = th / H, h = th - t * H;
+  const int parts = nt * H * kPer;
+  const int64_t from_step = static_cast<int64_t>(a.n_tokens) * H * D, row_step = static_cast<int64_t>(H) * a.capacity;
+  // A thread's part of a row in one layer after the other: its place and its angles are
+  // the same in all of them.  The next layer's loads run under this one's arithmetic (without
+  // that, 32 warps of 64 bytes a thread, it reached 4.4 TB/s).  (Whole warps: the rows'
+  // threads shuffle.)
+  for (int base = 0; base < parts; base += kThreads) {
+    const bool in = base + tid < parts;
+    const int r = in ? base + tid : 0;
+    const int c = r % kPer, th = r / kPer, h = th / nt, t = th - h * nt;  // (neighbours in the cache side by side)
     const int32_t slot = slots[t];
     const bool on = in && slot >= 0;
-    float k0[N], k1[N], v0[N], v1[N];
-    if (on) {
-      const int64_t from = ((static_cast<int64_t>(l) * a.n_tokens + t0 + t) * H + h) * D + c * N;
-      const uint4 a0 = __ldcs(reinterpret_cast<const uint4 *>(kn + from));
-      const uint4 a1 = __ldcs(reinterpret_cast<const uint4 *>(kn + from + D / 2));
-      const uint4 b0 = __ldcs(reinterpret_cast<const uint4 *>(vn + from));
-      const uint4 b1 = __ldcs(reinterpret_cast<const uint4 *>(vn + from + D / 2));
-      float x0[N], x1[N];
-      Vec<Act>::unpack(a0, x0);
-      Vec<Act>::unpack(a1, x1);
-      Vec<Act>::unpack(b0, v0);
-      Vec<Act>::unpack(b1, v1);
+    int64_t from = ((static_cast<int64_t>(l0) * a.n_tokens + t0 + t) * H + h) * D + c * N;
+    int64_t row = (static_cast<int64_t>(l0) * H + h) * a.capacity + (on ? slot : 0);
+    float cs[N], sn[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float2 cs = turn[t][c * N + j];
-        if constexpr (kFp4) {
-          fp4_turn(x0[j], x1[j], cs.x, cs.y, k0[j], k1[j]);
-        } else {  // as the appends of the decode calls
-          k0[j] = __fmaf_rn(x0[j], cs.x, -__fmul_rn(x1[j], cs.y));
-          k1[j] = __fmaf_rn(x1[j], cs.x, __fmul_rn(x0[j], cs.y));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) k0[j] = k1[j] = v0[j] = v1[j] = 0.f;
+    for (int j = 0; j < N; ++j) {
+      cs[j] = turn[t][c * N + j].x;
+      sn[j] = turn[t][c * N + j].y;
     }
-    const int64_t row = (static_cast<int64_t>(l) * H + h) * a.capacity + (on ? slot : 0);
-    if constexpr (kFp4) {
-      uint32_t kl, kh, vl, vh;
-      const float ks = fp4_row(k0, k1, kl, kh);
-      const float vs = fp4_row(v0, v1, vl, vh);
-      if (on) {
-        uint32_t *kd = reinterpret_cast<uint32_t *>(a.k_cache) + row * (D / 8);
-        uint32_t *vd = reinterpret_cast<uint32_t *>(a.v_cache) + row * (D / 8);
-        kd[c] = kl;
-        kd[D / 16 + c] = kh;
-        vd[c] = vl;
-        vd[D / 16 + c] = vh;
-        if (c == 0) static_cast<uint32_t *>(a.kv_scale)[row] = fp4_scale_word(ks, vs);
-      }
-    } else if (on) {
-      Store *kd = static_cast<Store *>(a.k_cache) + row * D + c * N;
-      Store *vd = static_cast<Store *>(a.v_cache) + row * D + c * N;
-      if constexpr (sizeof(Store) == 1) {  // E4M3
-        const float ki = 1.f / __ldg(a.k_scale + l * H + h), vi = 1.f / __ldg(a.v_scale + l * H + h);
+    uint4 next[4] = {};
+    auto load = [&]() {
+      const Act *kn = static_cast<const Act *>(a.k_new) + from, *vn = static_cast<const Act *>(a.v_new) + from;
+      next[0] = __ldg(reinterpret_cast<const uint4 *>(kn));
+      next[1] = __ldg(reinterpret_cast<const uint4 *>(kn + D / 2));
+      next[2] = __ldg(reinterpret_cast<const uint4 *>(vn));
+      next[3] = __ldg(reinterpret_cast<const uint4 *>(vn + D / 2));
+      from += from_step;
+    };
+    if (on && l0 < l1) load();
+    for (int l = l0; l < l1; ++l, row += row_step) {
+      const uint4 raw[4] = {next[0], next[1], next[2], next[3]};
+      if (on && l + 1 < l1) load();
+      float x0[N], x1[N], k0[N], k1[N], v0[N], v1[N];
+      Vec<Act>::unpack(raw[0], x0);
+      Vec<Act>::unpack(raw[1], x1);
+      Vec<Act>::unpack(raw[2], v0);
+      Vec<Act>::unpack(raw[3], v1);
+      if constexpr (kFp4) {
+        turn8(x0, x1, cs, sn, k0, k1);
+      } else {  // as the appends of the decode calls
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          k0[j] *= ki;
-          k1[j] *= ki;
-          v0[j] *= vi;
-          v1[j] *= vi;
+          k0[j] = __fmaf_rn(x0[j], cs[j], -__fmul_rn(x1[j], sn[j]));
+          k1[j] = __fmaf_rn(x1[j], cs[j], __fmul_rn(x0[j], sn[j]));
         }
-        *reinterpret_cast<uint2 *>(kd) = make_uint2(e4m3x4(k0), e4m3x4(k0 + 4));
-        *reinterpret_cast<uint2 *>(kd + D / 2) = make_uint2(e4m3x4(k1), e4m3x4(k1 + 4));
-        *reinterpret_cast<uint2 *>(vd) = make_uint2(e4m3x4(v0), e4m3x4(v0 + 4));
-        *reinterpret_cast<uint2 *>(vd + D / 2) = make_uint2(e4m3x4(v1), e4m3x4(v1 + 4));
-      } else {
-        *reinterpret_cast<uint4 *>(kd) = Vec<Act>::pack(k0);
-        *reinterpret_cast<uint4 *>(kd + D / 2) = Vec<Act>::pack(k1);
-        *reinterpret_cast<uint4 *>(vd) = Vec<Act>::pack(v0);
-        *reinterpret_cast<uint4 *>(vd + D / 2) = Vec<Act>::pack(v1);
+      }
+      if constexpr (kFp4) {
+        uint32_t kl, kh, vl, vh;
+        const float ks = fp4_row<false>(k0, k1, kl, kh);
+        const float vs = fp4_row<true>(v0, v1, vl, vh);
+        if (on) {
+          uint32_t *kd = static_cast<uint32_t *>(a.k_cache) + row * (D / 8) + c;
+          uint32_t *vd = static_cast<uint32_t *>(a.v_cache) + row * (D / 8) + c;
+          kd[0] = kl;
+          kd[D / 16] = kh;
+          vd[0] = vl;
+          vd[D / 16] = vh;
+          if (c == 0) static_cast<uint32_t *>(a.kv_scale)[row] = fp4_scale_word(ks, vs);
+        }
+      } else if (on) {
+        Store *kd = static_cast<Store *>(a.k_cache) + row * D + c * N;
+        Store *vd = static_cast<Store *>(a.v_cache) + row * D + c * N;
+        if constexpr (sizeof(Store) == 1) {  // E4M3
+          const float ki = 1.f / __ldg(a.k_scale + l * H + h), vi = 1.f / __ldg(a.v_scale + l * H + h);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            k0[j] *= ki;
+            k1[j] *= ki;
+            v0[j] *= vi;
+            v1[j] *= vi;
+          }
+          *reinterpret_cast<uint2 *>(kd) = make_uint2(e4m3x4(k0), e4m3x4(k0 + 4));
+          *reinterpret_cast<uint2 *>(kd + D / 2) = make_uint2(e4m3x4(k1), e4m3x4(k1 + 4));
+          *reinterpret_cast<uint2 *>(vd) = make_uint2(e4m3x4(v0), e4m3x4(v0 + 4));
+          *reinterpret_cast<uint2 *>(vd + D / 2) = make_uint2(e4m3x4(v1), e4m3x4(v1 + 4));
+        } else {
+          *reinterpret_cast<uint4 *>(kd) = Vec<Act>::pack(k0);
+          *reinterpret_cast<uint4 *>(kd + D / 2) = Vec<Act>::pack(k1);
+          *reinterpret_cast<uint4 *>(vd) = Vec<Act>::pack(v0);
+          *reinterpret_cast<uint4 *>(vd + D / 2) = Vec<Act>::pack(v1);
+        }
       }
     }
   }
@@ -264,54 +293,74 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   }
 }
 
-// Grid row c (blockIdx.y) commits range c; its CTAs stride over the range's
-// (layer, kv head, token) rows, 8 threads each.
-__global__ void __launch_bounds__(kThreads) commit_fp4_kernel(const __grid_constant__ CommitArgs a,
+constexpr int kCommitRows = 64;  // tokens that a CTA of commit_fp4_kernel takes at a time
+
+// A CTA takes 64 tokens at a time, 8 threads each, two to a thread, of range blockIdx.z and one (layer, kv
+// head), from its share blockIdx.x on; a thread's angles stay in registers.
+__global__ void __launch_bounds__(kThreads, 4) commit_fp4_kernel(const __grid_constant__ CommitArgs a,
                                                               const CommitScales scales) {
-  __shared__ float cs[64], sn[64];
-  const int c = blockIdx.y;
-  const int n_tokens = a.n_tokens[c];
+  constexpr int kAtOnce = kCommitRows / (kThreads / 8), kRows = kCommitRows;
+  const int c = blockIdx.z, n_tokens = a.n_tokens[c], ch = threadIdx.x & 7;
   const int64_t delta = a.delta[c];
-  if (threadIdx.x < 64) rope_cos_sin_exact(delta, a.phase[threadIdx.x], &cs[threadIdx.x], &sn[threadIdx.x]);
+  __shared__ float2 turn[64];
+  if (static_cast<int64_t>(blockIdx.x) * kRows >= n_tokens) return;  // (other ranges are longer)
+  if (threadIdx.x < 64) rope_cos_sin_exact(delta, a.phase[threadIdx.x], &turn[threadIdx.x].x, &turn[threadIdx.x].y);
   __syncthreads();
-  const int64_t end = static_cast<int64_t>(a.n_layers) * a.n_kv_heads * n_tokens * 8;
-  const uint32_t *ksrc = static_cast<const uint32_t *>(a.k_src);
-  const uint2 *vsrc = static_cast<const uint2 *>(a.v_src);
-  uint32_t *kdst = static_cast<uint32_t *>(a.k_dst);
-  uint2 *vdst = static_cast<uint2 *>(a.v_dst);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  // (whole warps: the rows' threads shuffle)
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads; base < end; base += step) {
-    const int64_t i = base + threadIdx.x;
-    const bool on = i < end;
-    const int ch = static_cast<int>(i & 7);
-    const int64_t row = on ? i >> 3 : 0;
-    const int64_t lh = div_nn(row, n_tokens), j = row - lh * n_tokens;
-    const int64_t so = lh * a.src_capacity + a.src_begin[c] + j;
-    const int64_t to = lh * a.dst_capacity + a.dst_offset[c] + j;
-    uint32_t kl = 0, kh = 0, sw = 0;
-    uint2 v = make_uint2(0, 0);
-    if (on) {
-      kl = __ldcs(ksrc + so * 16 + ch);
-      kh = __ldcs(ksrc + so * 16 + 8 + ch);
-      v = __ldcs(vsrc + so * 8 + ch);
-      sw = __ldg(scales.src + so);
-    }
-    if (delta != 0) {  // (the same for the whole CTA)
-      const float s = fp4_k_scale(sw);
-      float x0[8], x1[8], y0[8], y1[8];
-      fp4_levels8(kl, x0);
-      fp4_levels8(kh, x1);
+  float cs[8], sn[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) fp4_turn(x0[e] * s, x1[e] * s, cs[ch * 8 + e], sn[ch * 8 + e], y0[e], y1[e]);
-      const float t = fp4_row(y0, y1, kl, kh);
-      sw = fp4_scale_word(t, fp4_v_scale(sw));
-    }
-    if (on) {
-      kdst[to * 16 + ch] = kl;
-      kdst[to * 16 + 8 + ch] = kh;
-      vdst[to * 8 + ch] = v;
-      if (ch == 0) scales.dst[to] = sw;
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = turn[ch * 8 + e].x;
+    sn[e] = turn[ch * 8 + e].y;
+  }
+  for (int64_t lh = blockIdx.y; lh < static_cast<int64_t>(a.n_layers) * a.n_kv_heads; lh += gridDim.y) {
+    const int64_t s0 = lh * a.src_capacity + a.src_begin[c], d0 = lh * a.dst_capacity + a.dst_offset[c];
+    // (whole warps: the rows' threads shuffle)
+    for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * kRows; j0 < n_tokens; j0 += static_cast<int64_t>(gridDim.x) * kRows) {
+      // kAtOnce tokens a thread: their loads first, then one after the other
+      uint32_t kl[kAtOnce], kh[kAtOnce], sw[kAtOnce];
+      uint2 v[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t j = j0 + u * (kThreads / 8) + (threadIdx.x >> 3), so = s0 + j;
+        kl[u] = kh[u] = sw[u] = 0;
+        v[u] = make_uint2(0, 0);
+        if (j < n_tokens) {
+          const uint32_t *ks = static_cast<const uint32_t *>(a.k_src) + so * 16 + ch;
+          kl[u] = __ldcs(ks);
+          kh[u] = __ldcs(ks + 8);
+          v[u] = __ldcs(static_cast<const uint2 *>(a.v_src) + so * 8 + ch);
+          sw[u] = __ldg(scales.src + so);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t j = j0 + u * (kThreads / 8) + (threadIdx.x >> 3), to = d0 + j;
+        if (delta != 0) {  // (the same for the whole CTA)
+          const float s = fp4_k_scale(sw[u]);
+          float x0[8], x1[8], y0[8], y1[8];
+          fp4_levels8(kl[u], x0);
+          fp4_levels8(kh[u], x1);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float2 p = __fmul2_rn(make_float2(x0[e], x0[e + 1]), make_float2(s, s));
+            const float2 q = __fmul2_rn(make_float2(x1[e], x1[e + 1]), make_float2(s, s));
+            x0[e] = p.x;
+            x0[e + 1] = p.y;
+            x1[e] = q.x;
+            x1[e + 1] = q.y;
+          }
+          turn8(x0, x1, cs, sn, y0, y1);
+          const float t = fp4_row<false>(y0, y1, kl[u], kh[u]);
+          sw[u] = fp4_scale_word(t, fp4_v_scale(sw[u]));
+        }
+        if (j < n_tokens) {
+          uint32_t *kd = static_cast<uint32_t *>(a.k_dst) + to * 16 + ch;
+          kd[0] = kl[u];
+          kd[8] = kh[u];
+          static_cast<uint2 *>(a.v_dst)[to * 8 + ch] = v[u];
+          if (ch == 0) scales.dst[to] = sw[u];
+        }
+      }
     }
   }
 }
@@ -366,16 +415,16 @@ cudaError_t launch_cache_read(const CacheArgs &a, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_commit_fp4(const CommitArgs &a, const CommitScales &scales, cudaStream_t s) {
-  int64_t work = 0;
-  for (int c = 0; c < a.n_commits; ++c)
-    work += static_cast<int64_t>(a.n_layers) * a.n_kv_heads * a.n_tokens[c] * 8;
-  if (work == 0) return cudaSuccess;
-  // about eight CTAs per SM in all, shared evenly by the commits
-  int64_t ctas = (work + kThreads - 1) / kThreads;
-  const int64_t cap = 8ll * sm_count();
-  if (ctas > cap) ctas = cap;
-  const int64_t per = (ctas + a.n_commits - 1) / a.n_commits;
-  commit_fp4_kernel<<<dim3(static_cast<unsigned>(per), static_cast<unsigned>(a.n_commits)), kThreads, 0, s>>>(a, scales);
+  int longest = 0;
+  for (int c = 0; c < a.n_commits; ++c) longest = longest > a.n_tokens[c] ? longest : a.n_tokens[c];
+  if (longest == 0) return cudaSuccess;
+  // about sixteen CTAs per SM: (layer, kv head) pairs first, then tokens
+  const int64_t rows = static_cast<int64_t>(a.n_layers) * a.n_kv_heads, most = 16ll * sm_count();
+  const unsigned y = static_cast<unsigned>(rows < 65535 ? rows : 65535);
+  int64_t x = (longest + kCommitRows - 1) / kCommitRows;
+  const int64_t share = most / (static_cast<int64_t>(y) * a.n_commits);
+  if (x > share) x = share > 1 ? share : 1;
+  commit_fp4_kernel<<<dim3(static_cast<unsigned>(x), y, static_cast<unsigned>(a.n_commits)), kThreads, 0, s>>>(a, scales);
   return cudaGetLastError();
 }
 

@@ -33,6 +33,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+__device__ __forceinline__ float2 fpair2(float x) { return make_float2(x, x); }
+
 // The nearest codes of 8 numbers already in units of the scale, the first one lowest.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&t)[8]) {
   uint32_t w;
@@ -62,36 +69,61 @@ __device__ __forceinline__ uint32_t fp4_code_exact(float x, float s) {
   return c | (__float_as_uint(x) >> 28 & 8u);
 }
 
-// The codes of 8 numbers under the scale s > 0, with inv = 1 / s.  The product with inv
-// is off by less than 2^-22, so where 2^-20 to either side gives the same codes
-// they are the quotient's; elsewhere (one word in ten thousand) borders decide.
-__device__ __forceinline__ uint32_t fp4_encode8(const float (&x)[8], float s, float inv) {
+// The codes of 8 numbers under the scale s > 0.  A product with 1 / s is off by less than
+// 2^-22, so where 2^-20 to either side give the same code it is the quotient's; at the few
+// elements where they do not, the border between the two decides.
+__device__ __forceinline__ uint32_t fp4_encode8(const float (&x)[8], float s) {
+  const float inv = 1.f / s, inv_lo = inv * (1.f - 0x1p-20f), inv_hi = inv * (1.f + 0x1p-20f);
   float lo[8], hi[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = x[i] * inv;
-    lo[i] = t * (1.f - 0x1p-20f);
-    hi[i] = t * (1.f + 0x1p-20f);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 a = __fmul2_rn(make_float2(x[i], x[i + 1]), fpair2(inv_lo));
+    const float2 b = __fmul2_rn(make_float2(x[i], x[i + 1]), fpair2(inv_hi));
+    lo[i] = a.x;
+    lo[i + 1] = a.y;
+    hi[i] = b.x;
+    hi[i + 1] = b.y;
   }
   uint32_t w = e2m1x8(lo);
-  if (w != e2m1x8(hi)) {
-    w = 0;
+  const uint32_t diff = w ^ e2m1x8(hi);
+  if (diff) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= fp4_code_exact(x[i], s) << (4 * i);
+    for (int i = 0; i < 8; ++i)
+      if (diff >> (4 * i) & 0xfu) w = (w & ~(0xfu << (4 * i))) | fp4_code_exact(x[i], s) << (4 * i);
   }
   return w;
 }
 
-// The same of 2 numbers.
-__device__ __forceinline__ uint32_t fp4_encode2(float x, float y, float s, float inv) {
-  const float tx = x * inv, ty = y * inv;
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b8 a, b;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %3, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %5, %4;\n\t"
-      "mov.b32 %0, {a, a, a, a};\n\tmov.b32 %1, {b, b, b, b};\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "f"(tx * (1.f - 0x1p-20f)), "f"(ty * (1.f - 0x1p-20f)), "f"(tx * (1.f + 0x1p-20f)), "f"(ty * (1.f + 0x1p-20f)));
-  if (lo != hi) return fp4_code_exact(x, s) | fp4_code_exact(y, s) << 4;
-  return lo & 0xffu;
+// The same for numbers of bf16: a quotient then is a border or 2^-11 of one away (8 bits
+// against 8 times 3), so that rounded to 14 bits it stands on the right side of it, or
+// on it.  (Ties are common among such numbers.)
+__device__ __forceinline__ float fp4_snap(float t) { return __uint_as_float((__float_as_uint(t) + 0x200u) & ~0x3ffu); }
+__device__ __forceinline__ uint32_t fp4_encode8_bf16(const float (&x)[8], float s) {
+  const float inv = 1.f / s;
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 a = __fmul2_rn(make_float2(x[i], x[i + 1]), fpair2(inv));
+    t[i] = fp4_snap(a.x);
+    t[i + 1] = fp4_snap(a.y);
+  }
+  return e2m1x8(t);
+}
+
+// Of 2 numbers.
+__device__ __forceinline__ uint32_t e2m1x2(float x, float y) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tmov.b32 %0, {a, a, a, a};\n\t}" : "=r"(w) : "f"(x), "f"(y));
+  return w & 0xffu;
+}
+__device__ __forceinline__ uint32_t fp4_encode2(float x, float y, float s) {
+  const float inv = 1.f / s, lo = inv * (1.f - 0x1p-20f), hi = inv * (1.f + 0x1p-20f);
+  const uint32_t w = e2m1x2(x * lo, y * lo);
+  return w == e2m1x2(x * hi, y * hi) ? w : fp4_code_exact(x, s) | fp4_code_exact(y, s) << 4;
+}
+__device__ __forceinline__ uint32_t fp4_encode2_bf16(float x, float y, float s) {
+  const float inv = 1.f / s;
+  return e2m1x2(fp4_snap(x * inv), fp4_snap(y * inv));
 }
 
 // The levels (with signs) of 8 codes.
@@ -114,16 +146,17 @@ __device__ __forceinline__ float max_of_8(float top) {
 
 // A row of 128 elements among 8 threads, each with the 8 of `lo` (from 8c) and the 8
 // of `hi` (from 64 + 8c): its scale, and the thread's codes.  Whole warps call it.
+// kBf16: the elements are numbers of bf16.
+template <bool kBf16>
 __device__ __forceinline__ float fp4_row(const float (&lo)[8], const float (&hi)[8], uint32_t &wlo, uint32_t &whi) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_nan(top, max_nan(fabsf(lo[i]), fabsf(hi[i])));
+  for (int i = 0; i < 8; ++i) top = max3_abs_nan(top, lo[i], hi[i]);
   const float s = fp4_scale(max_of_8(top));
   wlo = whi = 0;
   if (s > 0.f) {
-    const float inv = 1.f / s;
-    wlo = fp4_encode8(lo, s, inv);
-    whi = fp4_encode8(hi, s, inv);
+    wlo = kBf16 ? fp4_encode8_bf16(lo, s) : fp4_encode8(lo, s);
+    whi = kBf16 ? fp4_encode8_bf16(hi, s) : fp4_encode8(hi, s);
   }
   return s;
 }
@@ -133,6 +166,13 @@ __device__ __forceinline__ float fp4_row(const float (&lo)[8], const float (&hi)
 __device__ __forceinline__ void fp4_turn(float x0, float x1, float c, float s, float &y0, float &y1) {
   y0 = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
   y1 = __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
+}
+
+// Two neighbouring pairs at once.
+__device__ __forceinline__ void fp4_turn2(float2 x0, float2 x1, float2 c, float2 s, float2 &y0, float2 &y1) {
+  const float2 d = __fmul2_rn(x1, s);
+  y0 = __fadd2_rn(__fmul2_rn(x0, c), make_float2(-d.x, -d.y));
+  y1 = __fadd2_rn(__fmul2_rn(x1, c), __fmul2_rn(x0, s));
 }
 
 // The two scales of a token as its word of kv_scale: the key's in the low half.

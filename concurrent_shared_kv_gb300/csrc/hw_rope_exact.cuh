@@ -74,14 +74,17 @@ __device__ __forceinline__ float turn_by(float2 x, float2 y, float rh, float rl,
   return __fadd_rn(s, __fadd_rn(lo, e));
 }
 
-__device__ __forceinline__ void rope_cos_sin_exact(int64_t rel, uint64_t phase, float *c, float *s) {
+// table: kSin256, or a copy of it in shared memory (where many angles are taken: lanes
+// read different entries).
+__device__ __forceinline__ void rope_cos_sin_exact(int64_t rel, uint64_t phase, float *c, float *s,
+                                                   const float2 *table = kSin256) {
   const uint64_t turns = static_cast<uint64_t>(rel) * phase;  // mod 2^64
   const uint64_t near = turns + (1ull << 55);
   const int k = static_cast<int>(near >> 56);  // the nearest 256th, 0 .. 255
   const int64_t rest = static_cast<int64_t>(near & ((1ull << 56) - 1)) - (1ll << 55);
   // sin and cos of k 256ths from the first quarter
   const int q = k >> 6, j = k & 63;
-  float2 a = kSin256[j], b = kSin256[64 - j];  // sin, cos of j
+  float2 a = table[j], b = table[64 - j];  // sin, cos of j
   float2 sn = (q & 1) ? b : a, cs = (q & 1) ? a : b;
   if (q & 2) sn = make_float2(-sn.x, -sn.y);
   if (q == 1 || q == 2) cs = make_float2(-cs.x, -cs.y);

@@ -501,23 +501,25 @@ def block_commit_many(k_src: torch.Tensor, v_src: torch.Tensor, commits, k_dst: 
 def _pools(k_cache, v_cache, kv_scale, what=""):
     """(dtype, layers, Hkv, capacity, D) of a cache's pools, [layers][Hkv][cap][D]
     or [Hkv][cap][D] (with kv_scale: packed codes, D / 2 bytes a token)."""
-    if k_cache.dim() not in (3, 4):
-        raise ValueError(f"pools are [layers][Hkv][cap][D] or [Hkv][cap][D], not {tuple(k_cache.shape)}")
-    layers = k_cache.shape[0] if k_cache.dim() == 4 else 1
-    heads, cap, width = k_cache.shape[-3:]
+    shape, dtype, dev = k_cache.shape, k_cache.dtype, k_cache.device
+    if len(shape) not in (3, 4):
+        raise ValueError(f"pools are [layers][Hkv][cap][D] or [Hkv][cap][D], not {tuple(shape)}")
+    heads, cap, width = shape[-3:]
+    layers = shape[0] if len(shape) == 4 else 1
     if kv_scale is not None:
-        if k_cache.dtype != torch.uint8:
+        if dtype != torch.uint8:
             raise ValueError("4-bit pools are bytes (torch.uint8)")
-        _fits(f"kv_scale{what}", kv_scale, layers * heads * cap * 2, torch.bfloat16, k_cache.device)
-    elif k_cache.dtype not in DTYPES:
-        raise ValueError(f"no cache of {k_cache.dtype}")
-    _fits(f"k{what or '_cache'}", k_cache, k_cache.numel(), k_cache.dtype, k_cache.device)
-    _fits(f"v{what or '_cache'}", v_cache, k_cache.numel(), k_cache.dtype, k_cache.device)
-    if k_cache.is_cuda:
-        _current(k_cache.device)
+        _fits(f"kv_scale{what}", kv_scale, layers * heads * cap * 2, torch.bfloat16, dev)
+    elif dtype not in DTYPES:
+        raise ValueError(f"no cache of {dtype}")
+    if not k_cache.is_contiguous():
+        raise ValueError(f"k{what or '_cache'} is not dense")
+    _fits(f"v{what or '_cache'}", v_cache, layers * heads * cap * width, dtype, dev)
+    if dev.type == "cuda":
+        _current(dev)
     else:
-        _on_gpu(k_cache.device)
-    return (DTYPES[k_cache.dtype] if kv_scale is None else api.HW_FP4_E2M1, layers, heads, cap,
+        _on_gpu(dev)
+    return (DTYPES[dtype] if kv_scale is None else api.HW_FP4_E2M1, layers, heads, cap,
             width if kv_scale is None else 2 * width)
 
 
