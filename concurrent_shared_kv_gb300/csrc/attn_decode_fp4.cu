@@ -21,17 +21,18 @@
 //    votes, fences) run under the other's arithmetic.  In a stream two threads share a
 //    token, each with half the columns; columns go to the halves by turns, and
 //    groups of four that hold none are skipped, so 20 columns cost 24, not 32.
-//  - Q~ is held as kQParts E4M3 parts x = a + b + ..., each the rounded remainder of those
-//    before it, and summed by the tensor cores into one S (12 bits of every element;
-//    2^-19 of the largest one where E4M3 runs out of exponents).  P is two E4M3 parts side
-//    by side (N = 64), the second 16 times larger, added where records are written.
-//  - Four tiles' scores are ahead of the weights, so that a stream finds its next
-//    tile's waiting; K and V share one ring, filled in the order of their use.
+//  - Q~ is held as kQParts E4M3 parts x = a + b/16 + ..., each the rounded remainder of those
+//    before it (12 bits of every element; 2^-19 of the largest one where E4M3 runs out
+//    of exponents), side by side on N (96 columns), and summed where S is read.  P is two
+//    E4M3 parts side by side (N = 64), summed where records are written.  On N because an
+//    instruction takes 32 + N / 4 clocks: a second part costs a quarter of a second one on K.
+//  - A warp issues either product, and the scores of kLead tiles are ahead of the weights; K
+//    and V share one ring, filled in the order of their use by one thread.
 //
 // Warps: 0-7 softmax of stream 0 (0-3 the first half of the columns, 4-7 the other),
-// 8-15 of stream 1, 16 TMA producer, 17 MMA issuer (the warp walks as a whole, one
-// elected lane issues: descriptors then stay in uniform registers), 18-19 rotated
-// queries of the segments to come, arrivals, appended tokens.
+// 8-15 of stream 1, 16 TMA producer, 17 issues Q~ K, 18 P V, 19 rotated queries of
+// segments behind the first, arrivals, appended tokens (the softmax warps do the first
+// segment's queries: nothing can start before them).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -384,7 +385,8 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // A column's largest pair length over the item's elements, squared: turned
-// elements are no longer than that.
+// elements are no longer than that.  One that is not finite makes its own column NaN, and
+// no other: it does not count for the exponent that the segment's columns share.
 __device__ __forceinline__ float item_reach(const QItem &it) {
   const uint32_t lo[4] = {it.lo.x, it.lo.y, it.lo.z, it.lo.w}, hi[4] = {it.hi.x, it.hi.y, it.hi.z, it.hi.w};
   float m = 0.f;
@@ -392,7 +394,7 @@ __device__ __forceinline__ float item_reach(const QItem &it) {
   for (int e = 0; e < 4; ++e) {
     const float a0 = __uint_as_float(lo[e] << 16), a1 = __uint_as_float(hi[e] << 16);
     const float b0 = __uint_as_float(lo[e] & 0xffff0000u), b1 = __uint_as_float(hi[e] & 0xffff0000u);
-    m = fmaxf(m, fmaxf(__fmaf_rn(a0, a0, a1 * a1), __fmaf_rn(b0, b0, b1 * b1)));
+    m = max_nan(m, max_nan(__fmaf_rn(a0, a0, a1 * a1), __fmaf_rn(b0, b0, b1 * b1)));
   }
   return m;
 }
@@ -499,15 +501,16 @@ __device__ void query_prologue(const DecodeArgs &a, Fp4Smem &S) {
     const uint32_t l = e < 2 ? lo.x : lo.y, h = e < 2 ? hi.x : hi.y;
     x0[e] = __uint_as_float(e & 1 ? l & 0xffff0000u : l << 16);
     x1[e] = __uint_as_float(e & 1 ? h & 0xffff0000u : h << 16);
-    reach = fmaxf(reach, __fmaf_rn(x0[e], x0[e], x1[e] * x1[e]));
+    reach = max_nan(reach, __fmaf_rn(x0[e], x0[e], x1[e] * x1[e]));
   }
-  reach = warp_max(reach);
+  const bool finite = reach < INFINITY;
+  reach = warp_max(finite ? reach : 0.f);
   if (lane == 0) S.qmax[warp] = reach;
   sync();
   reach = warp_max(S.qmax[lane & (kSoftWarps - 1)]);
   const int ex = part_exponent(a, reach);
   if (on) {
-    const float mul = a.scale_log2 * two_to(-ex);
+    const float mul = finite ? a.scale_log2 * two_to(-ex) : NAN;
     uint32_t w0[kQParts], w1[kQParts];
 #pragma unroll
     for (int e = 0; e < 4; e += 2) {
@@ -565,7 +568,8 @@ __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
       for (int g = 0; g < G; ++g) {
         QItem raw;
         load_item(a, X, (it >> 3) * G + g, it & 7, raw);
-        reach = fmaxf(reach, item_reach(raw));
+        const float r = item_reach(raw);
+        reach = fmaxf(reach, r < INFINITY ? r : 0.f);
       }
     const int e = part_exponent(a, warp_max_nonneg(reach));
     const float mul = a.scale_log2 * two_to(-e);
@@ -581,7 +585,7 @@ __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
         const int qi = (it >> 3) * G + g;
         QItem raw;
         load_item(a, X, qi, it & 7, raw);
-        store_item(raw, cs, sn, smem_u32(S.q[par]), column_place(qi), it & 7, mul);
+        store_item(raw, cs, sn, smem_u32(S.q[par]), column_place(qi), it & 7, item_reach(raw) < INFINITY ? mul : NAN);
       }
     }
     fence_proxy_async_smem();
@@ -856,10 +860,12 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
       const int buf = (i >> 1) & 1, t = i + t0;
       const uint32_t sw = sw_next;
       sw_next = scales_of(i + 2);
+      // A value of zeros (scales are 0 or at least 2^-100) weighs like any other in l, and
+      // is far below the others' in O and the references, whose precision it would take.  With a
+      // NaN scale the scores are NaN, and rv is not: a column that masks the token adds 0 rv.
       const float vs = fp4_v_scale(sw);
-      // (a value of zeros has weight like any other)
-      const float ks = fp4_k_scale(sw) * q_mul, lv = vs == 0.f ? 0.f : __log2f(vs);
-      const float rv = vs == 0.f ? 1.f : __fdividef(1.f, vs);
+      const float ks = fp4_k_scale(sw) * q_mul, lv = vs < 0x1p-100f ? -64.f : __log2f(vs);
+      const float rv = vs >= 0x1p-100f ? __fdividef(1.f, vs) : 0x1p64f;
       idle_wait(S, a, &S.s_full[st], (i >> 1) & 1);
       tc_fence_after();
       // scores in log2 units with the value's scale in them

@@ -16,8 +16,8 @@ namespace hw {
 static int check_tree(const hw_attn_desc *d, int32_t max_nodes) {
   const int st = check_desc(d);
   if (st != HW_OK) return st;
-  if (max_nodes <= 0) return HW_ERR_INVALID;
-  if ((d->flags & HW_DESC_VIEW_LIMITS) || d->dtype == HW_FP4_E2M1) return HW_ERR_UNSUPPORTED;
+  if (max_nodes <= 0 || d->dtype == HW_FP4_E2M1) return HW_ERR_INVALID;  // no trees over 4-bit caches
+  if (d->flags & HW_DESC_VIEW_LIMITS) return HW_ERR_UNSUPPORTED;
   if (max_nodes > HW_MAX_TREE_NODES || d->n_rows > HW_MAX_VIEW_ENTRIES) return HW_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(d->n_rows) * max_nodes > HW_MAX_TREE_QUERIES) return HW_ERR_UNSUPPORTED;
   return HW_OK;

@@ -75,12 +75,13 @@ typedef enum {
  * to a byte with the even element in the low bits; a third array kv_scale, bf16
  * [Hkv][capacity][2], holds a token's scale of its key and of its value: an element
  * is level(code) * scale with the levels 0, 1/2, 1, 3/2, 2, 3, 4, 6 and a sign
- * (code + 8).  A stored vector x has the scale bf16(max|x| / 6) and the codes of
- * the levels nearest to x / scale (ties to the even code).  A scale below 2^-100
+ * (code + 8).  A stored vector x has the scale bf16(max|x| * (1 / 6), the product and
+ * the sixth in fp32) and the codes of the levels nearest to x / scale (ties to the
+ * even code).  A scale below 2^-100
  * counts as zero; a vector with an element of 2^100 or more, or not finite,
  * gets the scale NaN: its elements are NaN.  Scales outside these bounds are not
  * to be stored by other means.  q, k_new, v_new and out are bf16; head_dim 128;
- * pools 16-byte, kv_scale 4-byte aligned.  Filled by hw_cache_write, decoded by
+ * pools 16-byte (32-byte for the decode calls), kv_scale 4-byte aligned.  Filled by hw_cache_write, decoded by
  * hw_attn_plan (_append, _limited) + hw_attn_decode_planned_fp4 and
  * hw_attn_append_decode_planned_fp4, committed by hw_block_commit_many_fp4,
  * moved by hw_block_move, read by hw_cache_read (the other calls return
@@ -354,7 +355,8 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
  * On the tensor cores a rotated query is held in about 12 bits of every element and a
  * token's weight in 8 (three and two E4M3 parts); sums, maxima and lse are fp32.  A
  * query that attends a token whose scale is NaN gets NaN in out and lse, others do
- * not.  HW_ERR_INVALID for another dtype or a null kv_scale.
+ * not; so does a query with an element that is not finite (or past 2^63: the squares
+ * are taken) in its row and head.  HW_ERR_INVALID for another dtype or a null kv_scale.
  */
 int hw_attn_decode_planned_fp4(const hw_attn_desc *d, const void *q, const void *k_cache,
                                const void *v_cache, const void *kv_scale, void *out, float *lse,
