@@ -47,9 +47,10 @@ def parse():
     p.add_argument("--chunk", type=int, default=0,
                    help="T > 0: T query tokens per worker, each seeing its own block up to its own "
                         "token (hw_views_chunked + hw_attn_plan_limited)")
-    p.add_argument("--kv", default="bf16", choices=["bf16", "fp8"],
+    p.add_argument("--kv", default="bf16", choices=["bf16", "fp8", "fp4"],
                    help="fp8: the K/V pools as E4M3 codes with per-kv-head scales "
-                        "(hw_attn_decode_planned_fp8)")
+                        "(hw_attn_decode_planned_fp8); fp4: as E2M1 codes with a scale a token "
+                        "(hw_attn_decode_planned_fp4)")
     p.add_argument("--commit-all", action="store_true",
                    help="C4: every worker's finished block joins the history each step, all in "
                         "one hw_block_commit_many launch (the common block gets room for them)")
@@ -277,10 +278,13 @@ def main():
         L = min(L, args.layers)
     lens, starts = w.block_lengths(), w.block_starts()
     chunk = args.chunk
-    fp8 = args.kv == "fp8"
-    if fp8:
-        assert not args.unplanned, "--kv fp8 runs planned decodes"
-        assert w.dtype == "bf16" and w.head_dim == 128, "E4M3 caches: the bf16 head_dim-128 shapes"
+    fp8, fp4 = args.kv == "fp8", args.kv == "fp4"
+    form = "" if args.kv == "bf16" else "_" + args.kv  # of the calls' names
+    if form:
+        assert not args.unplanned, "--kv fp8 and fp4 run planned decodes"
+        assert w.dtype == "bf16" and w.head_dim == 128, "caches of codes: the bf16 head_dim-128 shapes"
+    if fp4:
+        assert not commit_all, "4-bit caches commit one block a call here"
     if chunk > 0:
         assert not (args.append or args.unplanned), "--chunk runs planned decodes without appends"
         vb, vo, vl, qp = api.views_chunked(args.layout, lens, w.n_problems, w.n_workers, chunk)
@@ -292,17 +296,20 @@ def main():
                                 head_dim=w.head_dim, n_blocks=w.n_blocks,
                                 max_view_blocks=w.n_workers + 1, capacity=w.capacity, dtype=tdt,
                                 rope_theta=w.rope_theta, scale=w.scale, device=dev,
-                                view_limits=chunk > 0, kv_fp8=fp8)
+                                view_limits=chunk > 0, kv_fp8=fp8, kv_fp4=fp4)
     sess.set_metadata(starts, lens, vb, vo, qp)
     qs, ks, vs = [], [], []
     kscale, vscale = [], []  # E4M3: per layer, the per-kv-head scales
+    kvscale = []             # E2M1: per layer, the tokens' scales
     commit = w.commit_tokens > 0 and args.config == "C4"
     if commit:
         # one [layers][Hkv][cap][D] pool per K and V, so that one commit launch
         # covers every layer
-        k_all = torch.empty((L, w.n_kv_heads, w.capacity, w.head_dim),
-                            dtype=torch.uint8 if fp8 else tdt, device=dev)
+        k_all = torch.empty((L, w.n_kv_heads, w.capacity, w.head_dim // 2 if fp4 else w.head_dim),
+                            dtype=torch.uint8 if form else tdt, device=dev)
         v_all = torch.empty_like(k_all)
+        if fp4:
+            s_all = torch.zeros((L, w.n_kv_heads, w.capacity, 2), dtype=torch.bfloat16, device=dev)
     for l in range(L):
         q, k, v = wl.draw_device_layer(w, l, dev)
         if fp8:  # the layer's pools packed as E4M3 codes, one scale per kv head
@@ -310,6 +317,20 @@ def main():
             v, vsc = wl.e4m3_pack(v, lens, starts)
             kscale.append(ksc)
             vscale.append(vsc)
+        if fp4:  # as E2M1 codes (the drawn keys are turned already: position 0)
+            slot = torch.full((w.capacity,), -1, dtype=torch.int32, device=dev)
+            for st, n in zip(starts, lens):
+                slot[st:st + n] = torch.arange(st, st + n, dtype=torch.int32, device=dev)
+            packed = [torch.zeros((w.n_kv_heads, w.capacity, w.head_dim // 2), dtype=torch.uint8, device=dev)
+                      for _ in range(2)]
+            sc = torch.zeros((w.n_kv_heads, w.capacity, 2), dtype=torch.bfloat16, device=dev)
+            engine.cache_write(k.transpose(0, 1).contiguous(), v.transpose(0, 1).contiguous(), slot,
+                               torch.zeros_like(slot), *packed, rope_theta=w.rope_theta, kv_scale=sc)
+            k, v = packed
+            if commit:
+                s_all[l].copy_(sc)
+                sc = s_all[l]
+            kvscale.append(sc)
         if chunk > 0:  # one query per chunk token
             gq = torch.Generator(device=dev)
             gq.manual_seed(7000 + l)
@@ -324,7 +345,8 @@ def main():
     outs = [torch.empty_like(qs[0]) for _ in range(L)]
     lses = [torch.empty((n_rows, w.n_q_heads), dtype=torch.float32, device=dev) for _ in range(L)]
     calls_per_step = L if args.config != "C5" else 64  # C5: one layer timed x64
-    kernel = "decode_tc_kernel" if (w.dtype == "bf16" and w.head_dim == 128) else "decode_simt_kernel"
+    kernel = ("decode_fp4_kernel" if fp4 else
+              "decode_tc_kernel" if (w.dtype == "bf16" and w.head_dim == 128) else "decode_simt_kernel")
     stream = torch.cuda.Stream(device=dev)
 
     planned = not args.unplanned
@@ -341,7 +363,7 @@ def main():
         alt["q_pos"] = sess.meta["q_pos"] + 1
         metas.append(alt)
 
-    append = args.append and planned and kernel == "decode_tc_kernel"
+    append = args.append and planned and kernel != "decode_simt_kernel"
     if append:
         # every worker's new token at the last position of its own block (the
         # block lengths count it); the same rows are rewritten every step
@@ -380,12 +402,18 @@ def main():
                 sess.append_decode_planned_fp8(qsrc[l], new_k[l], new_v[l], ks[l], vs[l], kscale[l],
                                                vscale[l], out=osrc[l], lse=lsrc[l], stream=stream,
                                                early=early)
+            elif append and fp4:
+                sess.append_decode_planned_fp4(qsrc[l], new_k[l], new_v[l], ks[l], vs[l], kvscale[l],
+                                               out=osrc[l], lse=lsrc[l], stream=stream, early=early)
             elif append:
                 sess.append_decode_planned(qsrc[l], new_k[l], new_v[l], ks[l], vs[l], out=osrc[l],
                                            lse=lsrc[l], stream=stream, early=early)
             elif planned and fp8:
                 sess.decode_planned_fp8(qsrc[l], ks[l], vs[l], kscale[l], vscale[l], out=osrc[l],
                                         lse=lsrc[l], stream=stream, early=early)
+            elif planned and fp4:
+                sess.decode_planned_fp4(qsrc[l], ks[l], vs[l], kvscale[l], out=osrc[l], lse=lsrc[l],
+                                        stream=stream, early=early)
             elif planned:
                 sess.decode_planned(qsrc[l], ks[l], vs[l], out=osrc[l], lse=lsrc[l], stream=stream,
                                     early=early)
@@ -409,6 +437,11 @@ def main():
         wk = step_no[0] % w.n_workers
         step_no[0] += 1
         src = int(starts[1 + wk])
+        if fp4:
+            c0 = int(w.common_len[0])
+            engine.block_commit_fp4(k_all, v_all, s_all, k_all, v_all, s_all, [src], [w.commit_tokens],
+                                    [int(starts[0]) + c0], [c0], rope_theta=w.rope_theta, stream=stream)
+            return
         engine.block_commit(k_all, v_all, src, w.commit_tokens, k_all, v_all,
                             int(starts[0]) + int(w.common_len[0]), int(w.common_len[0]),
                             w.rope_theta, stream=stream)
@@ -462,10 +495,11 @@ def main():
         t = run_timed(args.steps)
     t = max_over_ranks(t, dev)
 
-    # algorithmic bytes: E4M3 codes are one byte where bf16 takes two
-    div = 2 if fp8 else 1
-    kv_layer = w.kv_bytes_per_layer() // div
-    commit_bytes = (w.commit_bytes_per_layer() // div * L * (w.n_workers if commit_all else 1)
+    # algorithmic bytes: an E4M3 code is one byte where bf16 takes two, 128 E2M1 codes
+    # and their scale are 66 bytes where they take 256
+    num, div = (33, 128) if fp4 else (1, 2) if fp8 else (1, 1)
+    kv_layer = w.kv_bytes_per_layer() * num // div
+    commit_bytes = (w.commit_bytes_per_layer() * num // div * L * (w.n_workers if commit_all else 1)
                     if commit else 0)
     step_bytes = kv_layer * calls_per_step + commit_bytes
     per_step = t / args.steps
@@ -556,7 +590,7 @@ def main():
     line = {
         "metric": METRIC, "value": value, "unit": "GB/s", "n_gpus": world, "steps": args.steps,
         "warmup": args.warmup, "ms_per_step": per_step * 1e3, "higher_is_better": True,
-        "scaling": "weak", "vs_baseline": None, "dtype": "e4m3 kv, bf16 q" if fp8 else w.dtype,
+        "scaling": "weak", "vs_baseline": None, "dtype": "e4m3 kv, bf16 q" if fp8 else "e2m1 kv, bf16 q" if fp4 else w.dtype,
         "data": "synthetic",
         "config": {
             **workload_config(w, args.config, args.layout, calls_per_step),
@@ -565,13 +599,15 @@ def main():
             "query_rows": n_rows, "chunk": chunk if chunk > 0 else None,
             "mode": "eager" if graphs is None else "cuda-graph",
             "calls": (f"hw_attn_plan_append once per step + hw_attn_append_decode_planned"
-                      f"{'_fp8' if fp8 else ''} per layer (each worker's new token written, then "
+                      f"{form} per layer (each worker's new token written, then "
                       "decoded)" if append else
-                      f"hw_attn_plan_limited once per step + hw_attn_decode_planned{'_fp8' if fp8 else ''} "
+                      f"hw_attn_plan_limited once per step + hw_attn_decode_planned{form} "
                       f"per layer ({chunk}-token chunks, causal within each worker's own block)"
                       if chunk > 0 else
                       "hw_attn_plan once per step + hw_attn_decode_planned_fp8 per layer (E4M3 "
                       "K/V codes, per-kv-head scales)" if fp8 else
+                      "hw_attn_plan once per step + hw_attn_decode_planned_fp4 per layer (E2M1 "
+                      "K/V codes, a scale a token)" if fp4 else
                       "hw_attn_plan once per step + hw_attn_decode_planned per layer" if planned
                       else "hw_attn_decode per layer"),
             "l2": "inputs larger than L2: each step reads every layer's own KV pools "
@@ -581,7 +617,7 @@ def main():
         "worker_tokens_per_s_per_layer": n_rows / per_launch,
         "roofline": {"bound": "hbm", "achieved": achieved, "peak": peak, "unit": "GB/s",
                      "frac": achieved / peak,
-                     "traffic": (measured_traffic(kernel, "qwq32b_w4_fp8" if fp8 else "qwq32b_w4")
+                     "traffic": (measured_traffic(kernel, "qwq32b_w4" + form)
                                  if args.config == "C3" and planned and not (append or chunk)
                                  and args.layout == "combined" else None),
                      "peak_kind": peak_kind,
@@ -592,7 +628,7 @@ def main():
         "clocks": clk.summary(),
         "e2e": e2e,
     }
-    if rank == 0 and world == 1 and not args.no_cpu_baseline and chunk == 0 and not fp8:
+    if rank == 0 and world == 1 and not args.no_cpu_baseline and chunk == 0 and not form:
         line["cpu_baseline"] = timed_oracle(w, qs, ks, vs, starts, lens, args.layout)
     if rank == 0:
         print(json.dumps(line), flush=True)
