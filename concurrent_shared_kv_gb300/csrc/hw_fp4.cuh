@@ -1,7 +1,7 @@
 // hw_fp4.cuh - the 4-bit cache format (HW_FP4_E2M1), written and read.
 //
 // A token's key (or value) of one kv head is 128 E2M1 codes, two to a byte with the
-// even element in the low bits, and one bf16 scale s = bf16(max|x| / 6); an element
+// even element in the low bits, and one bf16 scale s = bf16(max|x| (1 / 6)); an element
 // stands for level(code) * s with the levels 0, 1/2, 1, 3/2, 2, 3, 4, 6 and a sign.
 // E2M1 is what the tensor cores take as an operand, so a tile goes from memory into
 // the product without being widened, and a scale a token is one factor of a
