@@ -562,15 +562,21 @@ __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
     }
     const SegQ &X = S.cp.pre[seg % kPre];
     const int n_ref = X.m.n_ref, par = seg & 1;
-    // a lane's items: (reference, chunk), for each its q heads, which share a turn
+    // a lane's items: (reference, chunk), for each its q heads, which share a turn (32 in all
+    // at most: 32 of one reference's)
     float reach = 0.f;
+    uint32_t bad = 0;  // those that are not finite
+    int k = 0;
     for (int it = lane; it < n_ref * 8; it += 32)
       for (int g = 0; g < G; ++g) {
         QItem raw;
         load_item(a, X, (it >> 3) * G + g, it & 7, raw);
         const float r = item_reach(raw);
-        reach = fmaxf(reach, r < INFINITY ? r : 0.f);
+        const bool finite = r < INFINITY;
+        reach = fmaxf(reach, finite ? r : 0.f);
+        bad |= (finite ? 0u : 1u) << k++;
       }
+    k = 0;
     const int e = part_exponent(a, warp_max_nonneg(reach));
     const float mul = a.scale_log2 * two_to(-e);
     if (seg >= 2) idle_wait(S, a, &S.q_empty[par], ((seg >> 1) - 1) & 1);
@@ -585,7 +591,7 @@ __device__ void qprep(const DecodeArgs &a, Fp4Smem &S, int64_t u1) {
         const int qi = (it >> 3) * G + g;
         QItem raw;
         load_item(a, X, qi, it & 7, raw);
-        store_item(raw, cs, sn, smem_u32(S.q[par]), column_place(qi), it & 7, item_reach(raw) < INFINITY ? mul : NAN);
+        store_item(raw, cs, sn, smem_u32(S.q[par]), column_place(qi), it & 7, bad >> k++ & 1 ? NAN : mul);
       }
     }
     fence_proxy_async_smem();
@@ -864,8 +870,8 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
       // is far below the others' in O and the references, whose precision it would take.  With a
       // NaN scale the scores are NaN, and rv is not: a column that masks the token adds 0 rv.
       const float vs = fp4_v_scale(sw);
-      const float ks = fp4_k_scale(sw) * q_mul, lv = vs < 0x1p-100f ? -64.f : __log2f(vs);
-      const float rv = vs >= 0x1p-100f ? __fdividef(1.f, vs) : 0x1p64f;
+      const float vz = vs < 0x1p-100f ? 0x1p-64f : vs;
+      const float ks = fp4_k_scale(sw) * q_mul, lv = __log2f(vz), rv = vz >= 0x1p-100f ? __fdividef(1.f, vz) : 1.f;
       idle_wait(S, a, &S.s_full[st], (i >> 1) & 1);
       tc_fence_after();
       // scores in log2 units with the value's scale in them
