@@ -535,6 +535,8 @@ def _host_int32(what: str, *xs):
         a = None
     if a is None or a.ndim != 2:
         raise ValueError(f"{what}: sequences of different lengths")
+    if any(type(x) is not list and type(x) is not tuple for x in xs) and not np.array_equal(np.array(xs), a):
+        raise ValueError(f"{what}: not numbers of 32 bits")  # (lists raise OverflowError above)
     at, step = a.ctypes.data, a.shape[1] * 4
     return a.shape[1], a, [at + i * step for i in range(len(xs))]
 

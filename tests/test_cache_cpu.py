@@ -124,6 +124,14 @@ def test_sequences_of_unlike_lengths():
         commit(delta=(1, 2))
 
 
+def test_numbers_past_32_bits():
+    with pytest.raises(OverflowError):
+        move(src=[1 << 32])
+    for big in (np.array([1 << 32]), torch.tensor([(1 << 32) + 1]), np.array([0.5])):
+        with pytest.raises(ValueError):
+            move(src=big)
+
+
 def apply(pool, src, n, dst):
     for s, m, d in zip(src, n, dst):
         pool[d:d + m] = pool[s:s + m].copy()

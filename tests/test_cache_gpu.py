@@ -225,7 +225,8 @@ def test_slots_out_of_range():
 
 @pytest.mark.parametrize("layers,heads,commits", [
     (1, 1, [(0, 1, 3, 3)]), (2, 3, [(5, 37, 11, 1001)]), (3, 2, [(0, 20, 40, -7), (30, 1, 0, 65000), (31, 9, 60, 0)]),
-    (4, 8, [(0, 300, 100, 16384)])])
+    (4, 8, [(0, 300, 100, 16384)]),
+    (8, 8, [(0, 200, 0, 7), (200, 0, 200, 5), (200, 65, 200, -9), (265, 55, 340, 0)])])  # CTAs that cross ranges
 def test_commit(layers, heads, commits):
     g = gen(heads)
     cs, cd = 320, 400

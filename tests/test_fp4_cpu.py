@@ -72,6 +72,12 @@ def test_draft_trees_refuse_the_description(call, n):
     assert f(d, 4, *([A] * n if n else [1] + [A] * 5), 1 << 40, None) == INVALID
 
 
+def test_no_rows_is_no_work():
+    d = desc(n_rows=0)
+    api.attn_decode_planned_fp4(d, None, None, None, None, None, None, None, 0)
+    api.attn_append_decode_planned_fp4(d, None, None, None, None, None, None, None, None, None, 0)
+
+
 def test_sessions():
     with pytest.raises(ValueError):  # one format
         engine.DecodeSession(n_rows=1, n_q_heads=4, n_kv_heads=2, head_dim=128, n_blocks=1, max_view_blocks=1, capacity=100,
