@@ -48,7 +48,7 @@ def pack(codes):
 
 
 def unpack(b):
-    return np.stack([b & 15, b >> 4], -1).reshape(*b.shape[:-1], -1)
+    return np.stack([b & 15, b >> 4], -1).reshape(*b.shape[:-1], 2 * b.shape[-1])
 
 
 def rotate(x, pos, theta):
