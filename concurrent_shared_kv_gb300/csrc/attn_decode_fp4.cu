@@ -15,7 +15,9 @@
 //  - Scales stay out of the products.  A token is a row of S^T, so its thread has the
 //    one factor of its scores, and takes the value's scale into the weight:
 //    w = 2^(s ks + log2 vs - m), O = sum w c, l = sum w / vs.  Two fused
-//    multiply-adds an element, the ones that the sum and the shift cost anyway.
+//    multiply-adds an element, the ones that the sum and the shift cost anyway.  Scales
+//    span 2^200, more than w's exponents: where a warp has a scale below 2^-8, l takes
+//    2^(s ks - m) by itself, and a record's m is that of the scores alone.
 //  - Sixteen softmax warps in two streams, one for even tiles, one for odd ones, with
 //    scores, weights, maxima and outputs of their own: one stream's latencies (TMEM,
 //    votes, fences) run under the other's arithmetic.  In a stream two threads share a
@@ -762,8 +764,14 @@ __device__ __forceinline__ __half2 weight_dither(int token) {
   return __float2half2_rn(static_cast<float>(static_cast<int32_t>(token * 0x9e3779b9u)) * 0x1p-41f);
 }
 
+// l * 2^d, from half = 2^(d / 2): l is up to 2^100 times what O is (values of 2^-100), and 2^d
+// alone may be below fp32's range.
+__device__ __forceinline__ float l_shrink(float l, float half) { return l * half * half; }
+
 // Records of a finished segment: every warp joins the two streams' outputs of 8 of its
-// half's columns (stream 0's warps the first 8 places, stream 1's the others).
+// half's columns (stream 0's warps the first 8 places, stream 1's the others).  m has the
+// values' scales in it and l has not, so a power of two is taken from O and l into m that leaves
+// l between 1 and 2: then m is that of the scores, and the merge needs to know of no scales.
 __device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int seg) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int st = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3, par = seg & 1;
@@ -772,6 +780,20 @@ __device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, ui
   const Fp4Smem::Due due = S.due[warp];
   const int nq = due.nq;
   idle_wait(S, a, &S.hand[par], (seg >> 1) & 1);
+  // lane (s, j): column j's sum and reference in stream s, joined, and the factor of that stream's O
+  float m, l, f;
+  {
+    const int s = (lane >> 3) & 1, k = place + (lane & 7);
+    const float mine = S.hm[par][s][k], other = S.hm[par][s ^ 1][k];
+    const float *hl = &S.hl[par][s][0][k];
+    m = fmaxf(mine, other);
+    l = l_shrink(hl[0] + hl[kN] + hl[2 * kN] + hl[3 * kN], ex2(0.5f * (mine - m)));
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    const int e = l > 0.f && l < INFINITY ? (__float_as_int(l) >> 23) - 127 : 0;
+    l = __int_as_float(__float_as_int(l) - (e << 23));
+    f = ex2((mine - m) - static_cast<float>(e));
+    m += static_cast<float>(e);
+  }
   idle_wait(S, a, &S.o_full[par], (seg >> 1) & 1);
   tc_fence_after();
   float o[8];
@@ -785,11 +807,9 @@ __device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, ui
     tmem_ld8(tl + s * 2 * kN + kN + place, lo);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float m0 = S.hm[par][0][place + j], m1 = S.hm[par][1][place + j];
-      const float f = ex2((s ? m1 : m0) - fmaxf(m0, m1));
-      o[j] = __fmaf_rn(__fmaf_rn(__uint_as_float(lo[j]), 0.0625f, __uint_as_float(hi[j])), f, o[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+      o[j] = __fmaf_rn(__fmaf_rn(__uint_as_float(lo[j]), 0.0625f, __uint_as_float(hi[j])),
+                       __shfl_sync(0xffffffffu, f, s * 8 + j), o[j]);
   }
   tc_fence_before();
   __syncwarp();
@@ -801,17 +821,8 @@ __device__ __noinline__ void segment_records(const DecodeArgs &a, Fp4Smem &S, ui
     if (qi < nq) record_ptr(a, slot, qi)[qd * 32 + lane] = o[j];
   }
   if (qd == 0 && lane < 8) {
-    const int qi = 2 * (st * 8 + lane) + half, k = place + lane;
-    if (qi < nq) {
-      const float m0 = S.hm[par][0][k], m1 = S.hm[par][1][k], m = fmaxf(m0, m1);
-      float l = 0.f;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const float *hl = &S.hl[par][s][0][k];
-        l += (hl[0] + hl[kN] + hl[2 * kN] + hl[3 * kN]) * ex2((s ? m1 : m0) - m);
-      }
-      *reinterpret_cast<float2 *>(record_ptr(a, slot, qi) + 128) = make_float2(m, l);
-    }
+    const int qi = 2 * (st * 8 + lane) + half;
+    if (qi < nq) *reinterpret_cast<float2 *>(record_ptr(a, slot, qi) + 128) = make_float2(m, l);
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(&S.rec_ready[seg & 3]);
@@ -884,11 +895,17 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
       const uint32_t sw = sw_next;
       sw_next = scales_of(i + 2);
       // A value of zeros (scales are 0 or at least 2^-100) weighs like any other in l, and
-      // is far below the others' in O and the references, whose precision it would take.  With a
-      // NaN scale the scores are NaN, and rv is not: a column that masks the token adds 0 rv.
+      // is taken at 2^-101 in O and the references: below every other, whose precision it would
+      // take.  A scale below 2^-8 is "far": another one's up to 2^98 may have put w below fp32's range
+      // while the token's share of l counts (2^-24 and up), so l takes it without the scale.
+      // With a NaN scale the scores are NaN, and rv is not: a column that masks the token adds 0 rv.
       const float vs = fp4_v_scale(sw);
-      const float vz = vs < 0x1p-100f ? 0x1p-64f : vs;
-      const float ks = fp4_k_scale(sw) * q_mul, lv = __log2f(vz), rv = vz >= 0x1p-100f ? __fdividef(1.f, vz) : 1.f;
+      const float ks = fp4_k_scale(sw) * q_mul, lv = vs < 0x1p-100f ? -101.f : __log2f(vs);
+      const bool far = lv < -8.f;
+      const float rv = far ? 0.f : vs >= 0x1p-8f ? __fdividef(1.f, vs) : 1.f;
+      // (voted here: a vote beside its use cost 16K tokens 1.042 ms a step where this is 1.014, a
+      // ragged batch 12.41 where this is 12.58; an offset in the exponents of all, 1.060 and 12.81)
+      const bool any_far = __any_sync(0xffffffffu, far);
       idle_wait(S, a, &S.s_full[st], (i >> 1) & 1);
       tc_fence_after();
       // scores in log2 units with the value's scale in them
@@ -956,11 +973,12 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
         const float tmax = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
         const float old = ref_mine;
         if (tmax - old > kLift + kLazy) ref_mine = tmax - kLift;
-        const float a_mine = ref_mine == old ? 1.f : ex2(old - ref_mine);
+        const float half_mine = ref_mine == old ? 1.f : ex2(0.5f * (old - ref_mine));
         if (lane < kHalf) S.neg_ref[warp][lane] = -ref_mine;
         if (started) {
 #pragma unroll
-          for (int j = 0; j < kHalf; ++j) l[j] *= __shfl_sync(0xffffffffu, a_mine, j);
+          for (int j = 0; j < kHalf; ++j) l[j] = l_shrink(l[j], __shfl_sync(0xffffffffu, half_mine, j));
+          const float a_mine = half_mine * half_mine;
           // O must hold the stream's earlier tiles before it is rescaled
           idle_wait(S, a, &S.p_empty[st][buf ^ 1], ((i - 2) >> 2) & 1);
           tc_fence_after();
@@ -984,6 +1002,11 @@ __device__ void softmax_role(const DecodeArgs &a, Fp4Smem &S, uint32_t tmem, int
       started = true;
       // weights: their sum, and their parts to the tensor cores
       const __half2 dither = weight_dither(t * kT + row);
+      if (any_far) {
+        const float back = far ? -lv : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) l[j] += ex2(e[j] + back);
+      }
       uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {

@@ -8,8 +8,8 @@
 // row of scores (keys) or of a weight (values).
 // Codes are the nearest level to x / s, ties to the even code, of the exact quotient.
 // A scale below 2^-100 counts as zero (and the codes with it); a token with an element of
-// 2^100 or more, or not finite, gets the scale NaN: it reads as NaN.  (The attention kernel
-// takes scales into exponents and back: this keeps both in range.)
+// 2^100 or more, or not finite, gets the scale NaN: it reads as NaN.  (Products of scales, codes and
+// weights then stay inside fp32's range.)
 #pragma once
 
 #include <cuda_bf16.h>

@@ -355,7 +355,9 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
  * On the tensor cores a rotated query is held in about 12 bits of every element and a
  * token's weight in 8 (three and two E4M3 parts); sums, maxima and lse are fp32.  A weight
  * below 2^-10 of a row's largest keeps fewer bits, down to a step of 2^-17 of it, and is rounded up
- * or down so that the sum of many such weights is not off by more than chance.  A
+ * or down so that the sum of many such weights is not off by more than chance.  (A weight
+ * here is what a token adds to out, its value's scale included; lse and the weights' sum
+ * know no value scales, whatever they span, and a value of zeros stands for one of 2^-101.)  A
  * query that attends a token whose scale is NaN gets NaN in out and lse, others do
  * not; so does a query with an element that is not finite (or past 2^63: the squares
  * are taken) in its row and head.  HW_ERR_INVALID for another dtype or a null kv_scale.
