@@ -739,10 +739,12 @@ __device__ void append_tokens(const DecodeArgs &a, TcSmem &S, int64_t u0, int64_
     const int r = pr / Hkv, h = pr - r * Hkv;
     const int64_t s_off = (static_cast<int64_t>(r) * Hkv + h) * 128;
     const int64_t d_off = (static_cast<int64_t>(h) * a.capacity + row) * 128;
-    float kinv = 1.f, vinv = 1.f;
+    float ks = 1.f, vs = 1.f, ki = 1.f, vi = 1.f;
     if constexpr (kFp8) {
-      kinv = 1.f / __ldg(a.k_scale + h);
-      vinv = 1.f / __ldg(a.v_scale + h);
+      ks = __ldg(a.k_scale + h);
+      vs = __ldg(a.v_scale + h);
+      ki = reciprocal(ks);
+      vi = reciprocal(vs);
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -753,10 +755,10 @@ __device__ void append_tokens(const DecodeArgs &a, TcSmem &S, int64_t u0, int64_
       const float y0 = __fmaf_rn(x0, cs, -__fmul_rn(x1, sn));
       const float y1 = __fmaf_rn(x1, cs, __fmul_rn(x0, sn));
       if constexpr (kFp8) {
-        kc8[d_off + i] = code(y0 * kinv);
-        kc8[d_off + i + 64] = code(y1 * kinv);
-        vc8[d_off + i] = code(__bfloat162float(vn[s_off + i]) * vinv);
-        vc8[d_off + i + 64] = code(__bfloat162float(vn[s_off + i + 64]) * vinv);
+        kc8[d_off + i] = code(quotient(y0, ks, ki));
+        kc8[d_off + i + 64] = code(quotient(y1, ks, ki));
+        vc8[d_off + i] = code(quotient(__bfloat162float(vn[s_off + i]), vs, vi));
+        vc8[d_off + i + 64] = code(quotient(__bfloat162float(vn[s_off + i + 64]), vs, vi));
       } else {
         kc[d_off + i] = __float2bfloat16_rn(y0);
         kc[d_off + i + 64] = __float2bfloat16_rn(y1);

@@ -107,6 +107,20 @@ __device__ __forceinline__ void turn8(const float (&x0)[8], const float (&x1)[8]
   }
 }
 
+// The codes of x[] / s as quotient() has them, 8 bytes.
+__device__ __forceinline__ uint2 e4m3_quotients(const float (&x)[8], float s, float inv) {
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 q = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(inv, inv));
+    const float2 r = __ffma2_rn(q, make_float2(-s, -s), make_float2(x[j], x[j + 1]));
+    const float2 z = __ffma2_rn(r, make_float2(inv, inv), q);
+    y[j] = fabsf(q.x) < INFINITY ? z.x : q.x;
+    y[j + 1] = fabsf(q.y) < INFINITY ? z.y : q.y;
+  }
+  return make_uint2(e4m3x4(y), e4m3x4(y + 4));
+}
+
 // Rows of a CTA's tokens: (layer, token, kv head), 8 or so threads each.  blockIdx.x: the
 // tokens, blockIdx.y: a share of the layers.
 template <typename Store, int D>
@@ -188,9 +202,15 @@ __global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const __grid_c
         turn8(x0, x1, cs, sn, k0, k1);
       } else {  // as the appends of the decode calls
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          k0[j] = __fmaf_rn(x0[j], cs[j], -__fmul_rn(x1[j], sn[j]));
-          k1[j] = __fmaf_rn(x1[j], cs[j], __fmul_rn(x0[j], sn[j]));
+        for (int j = 0; j < N; j += 2) {
+          const float2 p = make_float2(x0[j], x0[j + 1]), q = make_float2(x1[j], x1[j + 1]);
+          const float2 c = make_float2(cs[j], cs[j + 1]), s = make_float2(sn[j], sn[j + 1]);
+          const float2 m = __fmul2_rn(q, s);
+          const float2 y0 = __ffma2_rn(p, c, make_float2(-m.x, -m.y)), y1 = __ffma2_rn(q, c, __fmul2_rn(p, s));
+          k0[j] = y0.x;
+          k0[j + 1] = y0.y;
+          k1[j] = y1.x;
+          k1[j + 1] = y1.y;
         }
       }
       if constexpr (kFp4) {
@@ -210,18 +230,13 @@ __global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const __grid_c
         Store *kd = static_cast<Store *>(a.k_cache) + row * D + c * N;
         Store *vd = static_cast<Store *>(a.v_cache) + row * D + c * N;
         if constexpr (sizeof(Store) == 1) {  // E4M3
-          const float ki = 1.f / __ldg(a.k_scale + l * H + h), vi = 1.f / __ldg(a.v_scale + l * H + h);
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            k0[j] *= ki;
-            k1[j] *= ki;
-            v0[j] *= vi;
-            v1[j] *= vi;
-          }
-          *reinterpret_cast<uint2 *>(kd) = make_uint2(e4m3x4(k0), e4m3x4(k0 + 4));
-          *reinterpret_cast<uint2 *>(kd + D / 2) = make_uint2(e4m3x4(k1), e4m3x4(k1 + 4));
-          *reinterpret_cast<uint2 *>(vd) = make_uint2(e4m3x4(v0), e4m3x4(v0 + 4));
-          *reinterpret_cast<uint2 *>(vd + D / 2) = make_uint2(e4m3x4(v1), e4m3x4(v1 + 4));
+          const float ks = __ldg(a.k_scale + l * H + h), vs = __ldg(a.v_scale + l * H + h);
+          const float ki = reciprocal(ks), vi = reciprocal(vs);
+          // (5003 tokens: 14.3 us, with the division of the language 18.6, with products by 1 / s 12.9)
+          *reinterpret_cast<uint2 *>(kd) = e4m3_quotients(k0, ks, ki);
+          *reinterpret_cast<uint2 *>(kd + D / 2) = e4m3_quotients(k1, ks, ki);
+          *reinterpret_cast<uint2 *>(vd) = e4m3_quotients(v0, vs, vi);
+          *reinterpret_cast<uint2 *>(vd + D / 2) = e4m3_quotients(v1, vs, vi);
         } else {
           *reinterpret_cast<uint4 *>(kd) = Vec<Act>::pack(k0);
           *reinterpret_cast<uint4 *>(kd + D / 2) = Vec<Act>::pack(k1);

@@ -103,6 +103,20 @@ __device__ __forceinline__ void flag_error(int32_t *err, int bits) {
   atomicOr(reinterpret_cast<int *>(err), bits);
 }
 
+// 1 / s to a unit or two in the last place, without a branch, for all normal s > 0.
+__device__ __forceinline__ float reciprocal(float s) {
+  const float m = s >= 1.f ? 0x1p-60f : 0x1p60f;  // (__fdividef has no quotient by more than 2^126)
+  return __fdividef(1.f, s * m) * m;
+}
+// x / s from inv = reciprocal(s): the product, and one step of refinement by its remainder,
+// which an fma gives exactly.  (The product alone is off by up to two units in the last place: on the wrong
+// side of one in ten of the quotients that lie at a border between E4M3 codes.)  What is
+// infinite or not a number stays what the product is.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = x * inv;
+  return fabsf(q) < INFINITY ? __fmaf_rn(__fmaf_rn(-q, s, x), inv, q) : q;
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T x);
 template <>

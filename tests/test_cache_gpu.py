@@ -432,3 +432,58 @@ def test_offsets_past_32_bits():
     for a, b in zip((k, v, s), small):
         for at in (7, 100):
             assert torch.equal(a[:, :, at:at + 33].view(torch.uint8), b.view(torch.uint8))
+
+
+def near_ties(n, seed):
+    """Numbers of bf16 and an fp32 scale each, whose quotient lies as near to a border between
+    two E4M3 codes as fp32 allows."""
+    r = np.random.default_rng(seed)
+    x = torch.tensor(r.standard_normal(n), dtype=torch.float32).bfloat16().float()
+    border = (17 + 2 * torch.tensor(r.integers(0, 8, n))) / 16.0 * 2.0 ** torch.tensor(r.integers(-5, 8, n))
+    return x, (x.abs().double() / border.double()).float()
+
+
+def test_e4m3_tokens_are_divided():
+    """Codes are those of the quotient by the head's scale (fp32, as the decode reads
+    them), whether written or appended: not of a product with the reciprocal."""
+    heads = 128
+    x, s = near_ties(40 * heads, 3)
+    want = (x / s).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    other = (x * (1 / s)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert (want != other).sum() > 100  # (the inputs tell the two apart)
+    x, s, want = x.view(40, heads, 1).cuda(), s.view(40, heads).cuda(), want.view(40, heads, 1).cuda()
+    new = x.expand(40, heads, 128).bfloat16().contiguous()[:, None]  # [layers][1][heads][128]
+    k, v, _ = pools(40, heads, 2, 128, FP8)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    engine.cache_write(new, new, zero, zero, k, v, rope_theta=1e4, k_scale=s, v_scale=s)
+    for pool in (k, v):  # (position 0: keys are not turned)
+        assert torch.equal(pool[:, :, 0].view(torch.uint8), want.expand(40, heads, 128))
+    t = engine.DecodeSession(n_rows=1, n_q_heads=heads, n_kv_heads=heads, head_dim=128, n_blocks=1, max_view_blocks=1,
+                             capacity=2, dtype=torch.bfloat16, rope_theta=1e4, kv_fp8=True)
+    t.set_metadata([0], [1], [[0]], [[0]], [0])
+    t.plan_append([0], [0])
+    for l in range(40):
+        k, v, _ = pools(1, heads, 2, 128, FP8)
+        t.append_decode_planned_fp8(new[l], new[l], new[l], k, v, s[l], s[l])
+        for pool in (k, v):
+            assert torch.equal(pool[0, :, 0].view(torch.uint8), want[l].expand(heads, 128))
+    assert t.device_flags() == 0
+
+
+def test_e4m3_saturates_at_any_scale():
+    """Quotients past 448 are 448, infinities among them, at scales from 2^-126 to 2^126; NaN stays NaN."""
+    scales = torch.tensor([2.0 ** -126, 2.0 ** -90, 1.7, 2.0 ** 90, 1.3 * 2.0 ** 126], device="cuda")
+    rows = []
+    for s in scales.double().tolist():
+        a = torch.linspace(-500, 500, 128, dtype=torch.float64) * s
+        a[:8] = torch.tensor([np.inf, -np.inf, np.nan, 3e38, -3e38, 0.0, 2.0 ** -126, s])
+        rows.append(a.clamp(-3.3e38, 3.3e38).where(a.abs() < np.inf, a).to(torch.bfloat16))
+    v_new = torch.stack(rows)[None].cuda().contiguous()  # [1 token][5 heads][128]
+    k, v, _ = pools(1, 5, 3, 128, FP8, fill=0)
+    at = torch.ones(1, dtype=torch.int32, device="cuda")
+    engine.cache_write(v_new, v_new, at, at - 1, k[0], v[0], rope_theta=1e4, k_scale=scales, v_scale=scales)
+    q = (v_new[0].float() / scales[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    got = v[0, :, 1]
+    assert torch.equal(torch.isnan(got.float()), torch.isnan(q.float())) and torch.isnan(got.float()).sum() == 5
+    same = ~torch.isnan(q.float())
+    assert torch.equal(got.view(torch.uint8)[same], q.view(torch.uint8)[same])
