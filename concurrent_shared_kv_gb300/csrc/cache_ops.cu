@@ -408,8 +408,13 @@ __device__ __forceinline__ void codes_of(const float (&y)[16], float r, uint32_t
 // A token's key, 32 elements from 32 (tid & 3) on in each of 4 neighbouring threads, turned and
 // encoded again; its new scale is the result.  The threads two apart hold what turns
 // together: they exchange 16 elements, so that either has 16 pairs, and exchange them back.
-// Levels are turned as they are (the scale is a factor of all), and their quotients by the
-// new scale, which the turn has rounded to 2^-23 already, taken with one product more.
+// Levels are turned as they are (the scale is a factor of all), in fp32 with fused products, and
+// encoded by one product with s / next: the code is the nearest one but where the quotient lies
+// within 2^-21 of a border, as near as the turn's own roundings are.  Numbers that the turn
+// leaves alone (slow pairs, with nothing to turn in) can stand on a border.  s / next is rounded
+// to nearest for them: n / m rounded, times m, is n for every m = 2^i + 2^j (W. Kahan), which levels
+// are, so a border is met exactly and goes to the even code.  (With every code decided exactly from
+// scaled, unfused products a model's commit takes 71 us, not 56.)
 __device__ __forceinline__ float commit_key(uint4 &k, const float (&cs)[16], const float (&sn)[16], float s) {
   const bool up = threadIdx.x & 2;
   auto other = [](uint32_t x) { return __shfl_xor_sync(0xffffffffu, x, 2); };
@@ -427,7 +432,7 @@ __device__ __forceinline__ float commit_key(uint4 &k, const float (&cs)[16], con
   top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const float next = fp4_scale(top * s);
   if (next > 0.f) {
-    const float r = __fdividef(s, next);
+    const float r = __fdiv_rn(s, next);
     codes_of(y0, r, e0);
     codes_of(y1, r, e1);
   } else {

@@ -6,7 +6,8 @@
 // E2M1 is what the tensor cores take as an operand, so a tile goes from memory into
 // the product without being widened, and a scale a token is one factor of a
 // row of scores (keys) or of a weight (values).
-// Codes are the nearest level to x / s, ties to the even code, of the exact quotient.
+// Codes are the nearest level to x / s, ties to the even code, of the exact quotient.  (Keys
+// that a commit turns: of a quotient that is off by up to 2^-21, see commit_key.)
 // A scale below 2^-100 counts as zero (and the codes with it); a token with an element of
 // 2^100 or more, or not finite, gets the scale NaN: it reads as NaN.  (Products of scales, codes and
 // weights then stay inside fp32's range.)

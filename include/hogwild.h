@@ -603,7 +603,9 @@ int hw_block_commit_many(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, in
 /*
  * hw_block_commit_many for HW_FP4_E2M1 caches: each key is decoded (code times
  * scale), rotated in fp32 and encoded anew, with a scale of its own; values keep
- * their codes and scales.  pos_delta = 0 is a bit copy.  scale_src and scale_dst:
+ * their codes and scales.  An element whose quotient by the new scale is within 2^-21 of a
+ * border between two levels may get either one's code (the rotation's roundings; one that
+ * the rotation leaves on a border gets the even code).  pos_delta = 0 is a bit copy.  scale_src and scale_dst:
  * kv_scale of the pools, [n_layers][Hkv][capacity][2] (dev), the same array
  * exactly where the pools are the same.
  */

@@ -487,3 +487,73 @@ def test_e4m3_saturates_at_any_scale():
     assert torch.equal(torch.isnan(got.float()), torch.isnan(q.float())) and torch.isnan(got.float()).sum() == 5
     same = ~torch.isnan(q.float())
     assert torch.equal(got.view(torch.uint8)[same], q.view(torch.uint8)[same])
+
+
+def turned_in_32_bits(x, delta, theta):
+    """x [..., 128] fp32 turned as the format defines it: cosines and sines rounded to fp32, every
+    product and sum rounded."""
+    a = np.float64(delta) * np.float64(theta) ** (-np.arange(64) / 64)
+    c, s = np.cos(a).astype(np.float32), np.sin(a).astype(np.float32)
+    lo, hi = x[..., :64], x[..., 64:]
+    return np.concatenate([lo * c - hi * s, hi * c + lo * s], -1)
+
+
+def encoded(y):
+    """(codes, scales) of fp32 rows: the nearest levels of the exact quotients, ties to the even code."""
+    top = np.abs(y).max(-1)
+    scale = F.bf16(top * np.float32(1 / 6))
+    r = np.abs(y).astype(np.float64)[..., None]
+    border = (F.LEVELS[1:] + F.LEVELS[:-1]) / 2 * scale[..., None, None]  # (exact: 3 bits times 8)
+    even_below = np.arange(7) % 2 == 0
+    code = np.where(even_below, r > border, r >= border).sum(-1)
+    return (code + 8 * np.signbit(y)).astype(np.uint8), scale
+
+
+def tie_rows(delta, theta):
+    """Keys whose last pair is not turned in 32 bits and stands, under the new scale that the first
+    pair makes, at a border between two levels."""
+    rows, scales = [], []
+    for m in range(128, 256):
+        s = np.float32(m / 128)
+        for a in range(16):
+            for b in range(8):
+                codes = np.zeros(128, np.uint8)
+                codes[0], codes[64] = a, b
+                _, nxt = encoded(turned_in_32_bits(F.decode(codes, s).astype(np.float32), delta, theta))
+                for level in range(1, 8):
+                    tie = F.LEVELS[level] * np.float64(s) / max(nxt, 1e-9)
+                    if tie in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0):
+                        codes[63] = level
+                        if encoded(turned_in_32_bits(F.decode(codes, s).astype(np.float32), delta, theta))[1] == nxt:
+                            rows.append(codes.copy())
+                            scales.append(s)
+    return np.array(rows), np.array(scales)
+
+
+@pytest.mark.parametrize("delta,theta", [(1, 1e6), (7, 1e6), (-100, 1e7), (40, 1e7)])
+def test_commits_decide_borders(delta, theta):
+    """A committed key is the stored one decoded, turned in 32 bits, and encoded: exactly at borders
+    between levels (ties to the even code), and but for 2^-21 beside them (the turn's
+    roundings, in whatever order they are made)."""
+    codes, scales = tie_rows(delta, theta)
+    assert len(codes) > 50
+    g = gen(17)
+    more, ms = F.draw(g, 3000, 128)
+    n = len(codes) + 3000
+    packed = torch.cat([torch.tensor(F.pack(codes)).cuda(), more])[None, None].contiguous()
+    ks = torch.cat([torch.tensor(scales).cuda().bfloat16(), ms])
+    scale = torch.stack([ks, torch.ones_like(ks)], -1)[None, None].contiguous()
+    kd, vd, sd = pools(1, 1, n, 128, FP4)
+    engine.block_commit_fp4(packed, packed, scale, kd, vd, sd, [0], [n], [0], [delta], rope_theta=theta)
+    y = turned_in_32_bits(F.values(packed[0, 0], ks).astype(np.float32), delta, theta)
+    want, want_scale = encoded(y)
+    got, got_scale = F.unpack(kd[0, 0].cpu().numpy()), sd[0, 0, :, 0].double().cpu().numpy()
+    same = got_scale == want_scale
+    assert same[:len(codes)].all() and same.mean() > 0.999
+    border = (F.LEVELS[1:] + F.LEVELS[:-1]) / 2 * want_scale[:, None, None]
+    size = (np.abs(y[:, :64]) + np.abs(y[:, 64:])).max(-1)[:, None]
+    beside = (np.abs(np.abs(y)[..., None] - border) <= 2.0 ** -21 * size[..., None]).any(-1)
+    beside[:len(codes), 63] = False  # (ties)
+    assert beside.mean() < 1e-3
+    wrong = F.decode(got, want_scale) != F.decode(want, want_scale)
+    assert not (wrong & ~beside)[same].any()
