@@ -161,9 +161,12 @@ int hw_block_commit_many_fp4(int32_t n_layers, int32_t n_kv_heads, int32_t head_
     if (spans_meet(t.p, t.bytes, scale_src, ns) || spans_meet(t.p, t.bytes, scale_dst, nd)) return HW_ERR_OVERLAP;
   for (const auto &f : from)
     if (spans_meet(f.p, f.bytes, scale_dst, nd)) return HW_ERR_OVERLAP;
-  // (the ranges are disjoint: commit_check compares every destination with every source where the pools are one)
-  if (spans_meet(scale_src, ns, scale_dst, nd) &&
-      !(scale_src == scale_dst && src_capacity == dst_capacity && k_src == k_dst))
+  // One array exactly where the pools are one: codes and scales of a token would part otherwise.  (The
+  // ranges are disjoint then: commit_check compares every destination with every source.)
+  if (k_src == v_dst || v_src == k_dst) return HW_ERR_OVERLAP;  // (keys among values: their scales' places differ)
+  const bool one_pool = k_src == k_dst || v_src == v_dst;
+  if (one_pool ? k_src != k_dst || v_src != v_dst || scale_src != scale_dst || src_capacity != dst_capacity
+               : spans_meet(scale_src, ns, scale_dst, nd))
     return HW_ERR_OVERLAP;
   const CommitScales scales = {static_cast<const uint32_t *>(scale_src), static_cast<uint32_t *>(scale_dst)};
   const cudaError_t e = launch_commit_fp4(a, scales, static_cast<cudaStream_t>(stream));

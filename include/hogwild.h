@@ -607,7 +607,8 @@ int hw_block_commit_many(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, in
  * border between two levels may get either one's code (the rotation's roundings; one that
  * the rotation leaves on a border gets the even code).  pos_delta = 0 is a bit copy.  scale_src and scale_dst:
  * kv_scale of the pools, [n_layers][Hkv][capacity][2] (dev), the same array
- * exactly where the pools are the same.
+ * exactly where the pools are the same (HW_ERR_OVERLAP else, and for keys committed to
+ * where values stand).
  */
 int hw_block_commit_many_fp4(int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
                              double rope_theta, const void *k_src, const void *v_src,

@@ -88,6 +88,17 @@ def test_commit_refusals(kw, st):
     assert status(commit, **kw) == st
 
 
+@pytest.mark.parametrize("kw", [
+    dict(k_dst=A, v_dst=2 * A),                     # one pool, scales of its tokens in two arrays
+    dict(k_dst=A, scale_dst=3 * A),                 # keys in one pool, values in two
+    dict(v_dst=2 * A, scale_dst=3 * A), dict(v_dst=2 * A), dict(k_dst=A),
+    dict(k_dst=2 * A, v_dst=A), dict(k_dst=2 * A), dict(v_dst=A),  # keys among values
+    dict(k_dst=2 * A, v_dst=A, scale_dst=3 * A)])
+def test_commit_scales_belong_to_their_pool(kw):
+    """The source's and the destination's scales are one array exactly where the pools are one."""
+    assert status(commit, dst_capacity=16, **kw) == OVERLAP
+
+
 def test_commit_of_nothing():
     assert commit(n=(0,), scale_src=None) == 0
 
