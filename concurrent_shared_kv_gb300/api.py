@@ -527,6 +527,9 @@ def cache_read(dtype: int, n_layers: int, n_tokens: int, n_kv_heads: int, head_d
     return st
 
 
+_INTS = frozenset((int, bool))
+
+
 def _host_int32(what: str, *xs):
     """Host int sequences of one length as int32: (length, array kept alive, their pointers)."""
     try:
@@ -535,8 +538,10 @@ def _host_int32(what: str, *xs):
         a = None
     if a is None or a.ndim != 2:
         raise ValueError(f"{what}: sequences of different lengths")
-    if any(type(x) is not list and type(x) is not tuple for x in xs) and not np.array_equal(np.array(xs), a):
-        raise ValueError(f"{what}: not numbers of 32 bits")  # (lists raise OverflowError above)
+    # (whole numbers in lists raise OverflowError above)
+    if not all((type(x) is list or type(x) is tuple) and _INTS.issuperset(map(type, x)) for x in xs) and not (
+            np.array_equal(np.array(xs), a)):
+        raise ValueError(f"{what}: not whole numbers of 32 bits")
     at, step = a.ctypes.data, a.shape[1] * 4
     return a.shape[1], a, [at + i * step for i in range(len(xs))]
 

@@ -143,6 +143,21 @@ def test_numbers_past_32_bits():
             move(src=big)
 
 
+@pytest.mark.parametrize("bad", [[1.5], (0.5,), [np.float32(-0.5)], [torch.tensor(1.5)], [0, 2.000001], ["1"]])
+def test_fractions_in_lists(bad):
+    """Host sequences hold whole numbers, in lists as in arrays: nothing is cut."""
+    some = [0] * len(bad)
+    for args in ((bad, some, some), (some, bad, some), (some, some, bad)):
+        with pytest.raises(ValueError):
+            move(*args)
+    with pytest.raises(ValueError):
+        commit(src=some, n=some, dst=some, delta=bad)
+    with pytest.raises(ValueError):
+        api.compact_moves(bad, some, 10)
+    whole = [float(x) for x in some]
+    assert move(whole, some, some) == 0  # (a whole number may be a float)
+
+
 def apply(pool, src, n, dst):
     for s, m, d in zip(src, n, dst):
         pool[d:d + m] = pool[s:s + m].copy()
