@@ -1213,7 +1213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                               cudaStream_t s) {
-  if (ctas > 256 || !a.plan || !a.kv_scale || (a.k_new && a.view_limit)) return cudaErrorInvalidValue;
+  // (kv_scale may be null where there is no token: check_kv_scale)
+  if (ctas > 256 || !a.plan || (a.k_new && a.view_limit)) return cudaErrorInvalidValue;
   void (*const kernel)(DecodeArgs, CUtensorMap, CUtensorMap) =
       a.k_new ? decode_fp4_kernel<true, false> : a.view_limit ? decode_fp4_kernel<false, true> : decode_fp4_kernel<false, false>;
   constexpr int kSmem = static_cast<int>(sizeof(Fp4Smem) + 1024);

@@ -487,6 +487,29 @@ def test_the_same_call_gives_the_same_bits():
         assert torch.equal(o[0], first[0]) and torch.equal(o[1], first[1])
 
 
+@pytest.mark.parametrize("n_blocks", [0, 2])
+def test_a_cache_of_nothing(n_blocks):
+    """No blocks, or empty ones, in pools of no tokens, whose addresses are null."""
+    none = torch.zeros(2, 0, 64, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(2, 0, 2, dtype=torch.bfloat16, device="cuda")
+    assert scales.data_ptr() == 0
+    for appends in (False, True):
+        t = engine.DecodeSession(n_rows=2, n_q_heads=4, n_kv_heads=2, head_dim=128, n_blocks=n_blocks, max_view_blocks=1,
+                                 capacity=0, dtype=torch.bfloat16, rope_theta=1e4, kv_fp4=True)
+        view = [[0 if n_blocks else -1]] * 2
+        t.set_metadata([0] * n_blocks, [0] * n_blocks, view, [[0]] * 2, [0, 0])
+        q = torch.ones(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+        if appends:
+            t.plan_append([-1, -1], [0, 0])
+            new = torch.ones(2, 2, 128, dtype=torch.bfloat16, device="cuda")
+            out, lse = t.append_decode_planned_fp4(q, new, new, none, none, scales)
+        else:
+            t.plan()
+            out, lse = t.decode_planned_fp4(q, none, none, scales)
+        assert t.device_flags() == 0
+        assert (out == 0).all() and (lse == -np.inf).all()
+
+
 # ------------------------------------------------------------ all together
 
 def test_a_serving_loop():
