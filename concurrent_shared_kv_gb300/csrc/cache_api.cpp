@@ -64,9 +64,10 @@ int check_cache(int32_t dtype, int32_t n_layers, int32_t n_tokens, int32_t n_kv_
     return HW_OK;
   }
   if (!k || !v || !slot || (capacity > 0 && (!k_cache || !v_cache))) return HW_ERR_INVALID;
-  if (dtype == HW_FP8_E4M3 && (!k_scale || !v_scale)) return HW_ERR_INVALID;
+  if (dtype == HW_FP8_E4M3 && (!k_scale || !v_scale || any_misaligned({k_scale, v_scale}, 4))) return HW_ERR_INVALID;
   if (dtype == HW_FP4_E2M1 && capacity > 0 && !kv_scale) return HW_ERR_INVALID;
-  if (any_misaligned({k_cache, v_cache, k, v}, 16) || any_misaligned({kv_scale, slot}, 4)) return HW_ERR_INVALID;
+  if (any_misaligned({k_cache, v_cache, k, v}, 16) || any_misaligned({slot}, 4)) return HW_ERR_INVALID;
+  if (dtype == HW_FP4_E2M1 && any_misaligned({kv_scale}, 4)) return HW_ERR_INVALID;
   return HW_OK;
 }
 

@@ -49,6 +49,13 @@ def test_cache_refusals(call, kw, st):
     assert status(call, **kw) == st
 
 
+@pytest.mark.parametrize("call", [write, read])
+@pytest.mark.parametrize("kw", [dict(k_scale=8 * A + 2), dict(v_scale=9 * A + 1)])
+def test_head_scales_off_their_boundary(call, kw):
+    """The heads' scales are read as floats: an address that is none is refused."""
+    assert status(call, **dict(dict(dtype=api.HW_FP8_E4M3, k_scale=8 * A, v_scale=9 * A, kv_scale=0), **kw)) == INVALID
+
+
 @pytest.mark.parametrize("kw", [dict(rope_theta=1.0), dict(rope_theta=float("nan")), dict(k_new=0), dict(v_new=0),
                                 dict(pos=0), dict(k_new=A + 8), dict(pos=4 * A + 1)])
 def test_write_refusals(kw):
