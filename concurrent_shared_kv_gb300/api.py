@@ -37,7 +37,7 @@ EXPORTS = ["hw_attn_decode_workspace_size", "hw_workspace_init", "hw_attn_decode
            "hw_attn_tree_workspace_size", "hw_attn_plan_tree", "hw_attn_decode_tree",
            "hw_attn_decode_tree_fp8", "hw_tree_verify", "hw_tree_commit",
            "hw_attn_decode_planned_fp4", "hw_attn_append_decode_planned_fp4", "hw_cache_write", "hw_cache_read",
-           "hw_block_commit_many_fp4", "hw_block_move", "hw_compact_moves"]
+           "hw_block_commit_many_fp4", "hw_block_move", "hw_block_move_status", "hw_compact_moves"]
 HW_LAYOUT_COMBINED, HW_LAYOUT_INTERLEAVED, HW_LAYOUT_CONTIGUOUS = 0, 1, 2
 LAYOUTS = {"combined": HW_LAYOUT_COMBINED, "interleaved": HW_LAYOUT_INTERLEAVED,
            "contiguous": HW_LAYOUT_CONTIGUOUS}
@@ -124,6 +124,7 @@ def lib(path: Optional[str] = None):
     L.hw_block_commit_many_fp4.argtypes = [ctypes.c_int32] * 3 + [ctypes.c_double] + [_P] * 3 + [
         ctypes.c_int64] + [_P] * 3 + [ctypes.c_int64, ctypes.c_int32] + [_P] * 5
     L.hw_block_move.argtypes = [ctypes.c_int32] * 4 + [_P] * 3 + [ctypes.c_int64, ctypes.c_int32] + [_P] * 4
+    L.hw_block_move_status.argtypes = [ctypes.POINTER(ctypes.c_int32), _P]
     L.hw_compact_moves.argtypes = [ctypes.c_int32] + [_P] * 3 + [ctypes.c_int64] + [_P] * 5
     L.hw_last_cuda_error.argtypes = []
     L.hw_test_set_merge_wait_limit.argtypes = [ctypes.c_int64]
@@ -570,6 +571,13 @@ def block_move(dtype: int, n_layers: int, n_kv_heads: int, head_dim: int, k_cach
                              n, *at, _stream(stream))
     _check("hw_block_move", st)
     return st
+
+
+def block_move_status(stream=None) -> int:
+    """hw_block_move_status: the device error bits of moves (read and cleared)."""
+    f = ctypes.c_int32(0)
+    _check("hw_block_move_status", lib().hw_block_move_status(ctypes.byref(f), _stream(stream)))
+    return f.value
 
 
 def compact_moves(block_start, block_len, capacity: int, room=None):

@@ -30,6 +30,8 @@ using namespace sm100;
 
 namespace {
 
+__device__ int32_t g_move_flags;  // HW_DEV_* bits of the device's moves (hw_block_move_status)
+
 constexpr int kThreads = 128;
 constexpr int kStages = 6;
 constexpr int kAhead = kStages - 2;  // chunks loaded ahead: a stage's store has two chunks' time to be read
@@ -169,8 +171,12 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ 
     uint32_t bytes;
     st.place(src, dst, bytes);
     const int s = static_cast<int>(done % kStages);
-    // (a load that does not land is a lost GPU: nothing is stored from it, and nothing waits on)
-    if (!mbar_wait(&full[s], static_cast<uint32_t>(done / kStages & 1))) break;
+    // (a load that does not land: nothing is stored from it, nothing waits on, and the caller can
+    // ask for it)
+    if (!mbar_wait(&full[s], static_cast<uint32_t>(done / kStages & 1))) {
+      flag_error(&g_move_flags, HW_DEV_TIMEOUT);
+      break;
+    }
     bulk_s2g(dst, ring + s * kChunk, bytes);
     ++done;
     st.next();
@@ -197,6 +203,14 @@ cudaError_t launch_move(const MoveArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   move_kernel<<<bulk + scale_ctas, kThreads, kSmem, s>>>(a, bulk);
   return cudaGetLastError();
+}
+
+cudaError_t read_move_flags(int32_t *flags, cudaStream_t s) {
+  const int32_t none = 0;
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(flags, g_move_flags, sizeof *flags);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_move_flags, &none, sizeof none);
+  return e;
 }
 
 }  // namespace hw

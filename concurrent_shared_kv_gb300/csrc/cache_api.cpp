@@ -224,6 +224,13 @@ int hw_block_move(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t h
   return e == cudaSuccess ? HW_OK : cuda_fail(e);
 }
 
+int hw_block_move_status(int32_t *flags, void *stream) {
+  if (!flags) return HW_ERR_INVALID;
+  *flags = 0;
+  const cudaError_t e = read_move_flags(flags, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HW_OK : cuda_fail(e);
+}
+
 int hw_compact_moves(int32_t n_blocks, const int32_t *block_start, const int32_t *block_len, const int32_t *room,
                      int64_t capacity, int32_t *new_start, int32_t *n_moves, int32_t *src_begin,
                      int32_t *n_tokens, int32_t *dst_begin) {

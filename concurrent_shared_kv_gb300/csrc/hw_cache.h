@@ -43,5 +43,7 @@ struct MoveArgs {
   uint32_t drain[kMaxMoves / 32];  // bit m: move m starts once the ones before it are written
 };
 cudaError_t launch_move(const MoveArgs &a, cudaStream_t s);
+// The current device's HW_DEV_* bits of moves, read and cleared once `s` is done.
+cudaError_t read_move_flags(int32_t *flags, cudaStream_t s);
 
 }  // namespace hw

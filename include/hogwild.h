@@ -684,6 +684,13 @@ int hw_block_move(int32_t dtype, int32_t n_layers, int32_t n_kv_heads, int32_t h
                   void *stream);
 
 /*
+ * The moves' device error bits, one word a device for all streams: synchronises
+ * `stream`, then reads and clears them.  HW_DEV_TIMEOUT: a copy into shared memory did not
+ * land within about a second, and some of a call's tokens were not moved.
+ */
+int hw_block_move_status(int32_t *flags, void *stream);
+
+/*
  * Host helper: the moves that slide a pool's blocks together, in the order of
  * their starts, from token 0 on, with room[b] tokens left free behind block b (room
  * NULL: none), for hw_block_move.  A block of length 0 holds nothing and only gets a

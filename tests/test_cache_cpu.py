@@ -135,6 +135,10 @@ def test_moves_of_nothing(kw):
     assert move(**dict(dict(k_cache=None), **kw)) == 0
 
 
+def test_move_status_needs_a_place():
+    assert api.lib().hw_block_move_status(None, None) == INVALID
+
+
 def test_sequences_of_unlike_lengths():
     with pytest.raises(ValueError):
         move(src=(0, 1))

@@ -557,3 +557,13 @@ def test_commits_decide_borders(delta, theta):
     assert beside.mean() < 1e-3
     wrong = F.decode(got, want_scale) != F.decode(want, want_scale)
     assert not (wrong & ~beside)[same].any()
+
+
+def test_moves_have_a_status():
+    """A move whose copies all land leaves no error bit, ordered or not, on any stream."""
+    k, v, s = pools(2, 3, 700, 128, FP4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for src, n, dst in MOVES.values():
+        engine.block_move(k, v, src, n, dst, kv_scale=s, stream=side)
+    assert api.block_move_status(stream=side) == 0 and api.block_move_status() == 0
