@@ -510,6 +510,54 @@ def test_a_cache_of_nothing(n_blocks):
         assert (out == 0).all() and (lse == -np.inf).all()
 
 
+@pytest.mark.parametrize("limits", [None, [[250, 100, -1], [0, 300, 7], [300, 0, 0]]])
+def test_a_block_twice_in_a_view(limits):
+    """A block may stand in a view more than once, at other offsets and under other limits."""
+    c = Case([300, 40], [[0, 0, 1], [1, 0, 0], [0, 1, 1]], 8, 2, seed=90, limits=limits,
+             offsets=[[0, 300, 600], [0, 40, 1000], [7, 2000, 2100]], q_pos=[640, 1300, 2140])
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("hq,hkv,rows", [(256, 8, 3), (256, 256, 2), (64, 64, 5), (6, 3, 70)])
+def test_many_heads_and_rows(hq, hkv, rows):
+    c = Case([400] + [5 + i % 7 for i in range(rows)], [[0, 1 + i] for i in range(rows)], hq, hkv, seed=91)
+    c.check(*c.run(), rows=range(0, rows, max(1, rows // 5)))
+
+
+def test_far_positions():
+    """Queries and offsets at both ends of what 32 bits hold."""
+    c = Case([300, 40], [[0, 1], [1, 0], [0]], 8, 2, seed=92, theta=1e4,
+             offsets=[[2 ** 31 - 400, -2 ** 31], [-5, 2 ** 31 - 1], [-2 ** 31, 0]], q_pos=[2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1])
+    # (this reference's angles have 53 bits of up to 2^32 radians; scores are off by 2^-20 of |q| |k| for that)
+    c.check(*c.run())
+
+
+def test_limited_layers_early_and_in_a_graph():
+    """Layers of one limited plan with early loads, on a stream and replayed: the same bits."""
+    limits = [[2000, 20], [1500, -1], [0, 3], [-1, 0]]
+    cases = [Case([3000, 40], [[0, 1]] * 4, 40, 8, seed=93 + i, limits=limits) for i in range(3)]
+    t = cases[0].session()
+    t.plan_limited(limits)
+    want = [t.decode_planned_fp4(c.q, c.k, c.v, c.s) for c in cases]
+    for c, w in zip(cases, want):
+        c.check(*w)
+    got = [(torch.full_like(o, float("nan")), torch.full_like(l, float("nan"))) for o, l in want]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for i, (c, (o, l)) in enumerate(zip(cases, got)):
+            t.decode_planned_fp4(c.q, c.k, c.v, c.s, o, l, early=i > 0, stream=side)
+    for _ in range(3):
+        for o, l in got:
+            o.fill_(float("nan")), l.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert t.device_flags() == 0
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 # ------------------------------------------------------------ all together
 
 def test_a_serving_loop():
