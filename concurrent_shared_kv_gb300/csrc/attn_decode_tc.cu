@@ -751,7 +751,10 @@ __device__ void append_tokens(const DecodeArgs &a, TcSmem &S, int64_t u0, int64_
       const int i = lane + 32 * half;
       const float x0 = __bfloat162float(kn[s_off + i]), x1 = __bfloat162float(kn[s_off + i + 64]);
       float cs, sn;
-      rope_cos_sin(pos, a.phase[i], &cs, &sn);
+      if constexpr (kFp8)
+        rope_cos_sin_near(pos, a.phase[i], &cs, &sn);
+      else
+        rope_cos_sin(pos, a.phase[i], &cs, &sn);
       const float y0 = __fmaf_rn(x0, cs, -__fmul_rn(x1, sn));
       const float y1 = __fmaf_rn(x1, cs, __fmul_rn(x0, sn));
       if constexpr (kFp8) {

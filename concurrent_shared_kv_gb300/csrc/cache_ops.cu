@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(kThreads, 3) cache_write_kernel(const __grid_c
     float c, s;
     if constexpr (kFp4)
       rope_cos_sin_exact(p, a.phase[j], &c, &s, table);
+    else if constexpr (sizeof(Store) == 1)
+      rope_cos_sin_near(p, a.phase[j], &c, &s);
     else
       rope_cos_sin(p, a.phase[j], &c, &s);
     turn[t][j] = make_float2(c, s);

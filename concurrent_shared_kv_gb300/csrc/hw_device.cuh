@@ -145,6 +145,20 @@ __device__ __forceinline__ void rope_cos_sin(int64_t rel, uint64_t phase, float 
   sincospif(t, s, c);
 }
 
+// The same from the nearest quarter turn, so that fp32 keeps 2^-26 of a half turn where it
+// keeps 2^-24 above: for keys that are stored as E4M3 codes, of which an error in the angle
+// puts some on the wrong side of a border.
+__device__ __forceinline__ void rope_cos_sin_near(int64_t rel, uint64_t phase, float *c, float *s) {
+  const uint64_t turns = static_cast<uint64_t>(rel) * phase;
+  const uint64_t quarter = (turns + (1ull << 61)) >> 62;
+  const float t = static_cast<float>(static_cast<int64_t>(turns - (quarter << 62))) * 0x1p-63f;
+  float sn, cs;
+  sincospif(t, &sn, &cs);
+  const float a = quarter & 1 ? sn : cs, b = quarter & 1 ? cs : sn;
+  *c = quarter == 1 || quarter == 2 ? -a : a;
+  *s = quarter & 2 ? -b : b;
+}
+
 // The same from the exactly reduced angle through the fast hardware sine and
 // cosine: pi * t lies in [-pi, pi), where their absolute error is at most
 // 2^-21.41 (CUDA math documentation) - far below the 16 bits that the

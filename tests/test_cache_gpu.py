@@ -567,3 +567,31 @@ def test_moves_have_a_status():
     for src, n, dst in MOVES.values():
         engine.block_move(k, v, src, n, dst, kv_scale=s, stream=side)
     assert api.block_move_status(stream=side) == 0 and api.block_move_status() == 0
+
+
+def test_e4m3_keys_turn_as_precisely_as_32_bits_can():
+    """Of 10^8 keys no more have another code than the 64-bit rotation gives than where
+    cosines, sines, products and sums are rounded to fp32 and nothing else is: both counts are of
+    independent, rare events, so three deviations of their difference are allowed."""
+    heads, n, theta = 8, 12500, 1e6
+    freq = theta ** (-torch.arange(64, dtype=torch.float64, device="cuda") / 64)
+    ours = plain = 0
+    for seed in range(8):
+        g = gen(seed)
+        x = torch.randn(1, n, heads, 128, generator=g, device="cuda").bfloat16()
+        pos = torch.randint(0, 70000, (n,), generator=g, device="cuda").int()
+        s = head_scales(x)
+        k, v, _ = pools(1, heads, n, 128, FP8)
+        slot = torch.arange(n, dtype=torch.int32, device="cuda")
+        engine.cache_write(x, x, slot, pos, k, v, rope_theta=theta, k_scale=s, v_scale=s)
+
+        def codes(dtype):
+            a = pos.double()[:, None, None] * freq
+            c, sn = a.cos().to(dtype), a.sin().to(dtype)
+            lo, hi = x[0, ..., :64].to(dtype), x[0, ..., 64:].to(dtype)
+            y = torch.cat([lo * c - hi * sn, hi * c + lo * sn], -1) / s[0].to(dtype)[:, None]
+            return y.float().clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        want = codes(torch.float64)
+        ours += (k[0].view(torch.uint8).transpose(0, 1) != want).sum().item()
+        plain += (codes(torch.float32) != want).sum().item()
+    assert plain > 50 and ours <= plain + 3 * (2 * plain) ** 0.5, (ours, plain)
