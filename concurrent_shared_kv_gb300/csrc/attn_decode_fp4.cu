@@ -31,9 +31,9 @@
 //  - A warp issues either product, and the scores of kLead tiles are ahead of the weights; K
 //    and V share one ring, filled in the order of their use by one thread.
 //
-// Measured (40/8 heads, 4 rows): 262,144 tokens 78 us, 3.6 TB/s, 0.53 us a tile and SM, of which the chain
+// Measured (40/8 heads, 4 rows): 262,144 tokens 79 us, 3.5 TB/s, 0.53 us a tile and SM, of which the chain
 // product - TMEM - vote - exponentials - product is what two streams leave; 16,384 tokens
-// 16.2 us a layer in a chain of layers (bf16 19.1, E4M3 21.4), of which 12 are trips to L2 at both
+// 15.8 us a layer in a chain of layers (bf16 19.1, E4M3 21.4), of which 12 are trips to L2 at both
 // ends.  (All columns a thread in eight warps: 92 us where two threads a token were 86; three
 // streams 100; two tiles at a time in a stream 98 and more.)
 //

@@ -352,7 +352,8 @@ int hw_attn_append_decode_planned_fp8(const hw_attn_desc *d, const void *q, cons
  * hw_cache_write stores them.
  *  k_cache, v_cache  dev [Hkv][capacity][64] bytes, 32-byte aligned
  *  kv_scale          dev bf16 [Hkv][capacity][2]: a token's key and value scale
- * On the tensor cores a rotated query is held in about 12 bits of every element and a
+ * On the tensor cores a rotated query is held in about 12 bits of every element (no finer
+ * than 2^-19 of the largest one among the queries that a tile's columns share: rows, heads) and a
  * token's weight in 8 (three and two E4M3 parts); sums, maxima and lse are fp32.  A weight
  * below 2^-10 of a row's largest keeps fewer bits, down to a step of 2^-17 of it, and is rounded up
  * or down so that the sum of many such weights is not off by more than chance.  (A weight
